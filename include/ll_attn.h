@@ -31,6 +31,12 @@
  *                        delta-rule pseudo-values), study note §3-5.
  *   ll_gdn_decode_step   one token of Log-Linear Gated DeltaNet decoding over the
  *                        Fenwick level states (reading A), study note §3-5/§3-6.
+ *   ll_gdr_fwd, ll_gdr_bwd, ll_gdr_decode_step
+ *                        the gated delta rule itself, the single-state base model
+ *                        of ll_gdn_* (study note §3-5 builds on it; the pages print
+ *                        no delta-rule equations, the standard ones are stated at
+ *                        the declarations): chunk-wise forward from and to states,
+ *                        its gradient, one token of decoding.
  *   ll_attn_fwd_level_decay, ll_attn_decode_step_level_decay
  *                        the forward and the decode step with one decay per level
  *                        (study note §7 "Follow-up design" names a learned memory
@@ -375,6 +381,99 @@ LL_API size_t ll_gdn_fwd_b_workspace_size(const ll_shape* shape);
 LL_API ll_status ll_gdn_fwd_b(const ll_shape* shape, const void* q, const void* k, const void* v,
                               const float* log_alpha, const float* beta, const float* lam, void* o,
                               void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- the gated delta rule (one state per head) ----
+ *   S_t = alpha_t S_{t-1} (I - beta_t k_t k_t^T) + beta_t v_t k_t^T     S_t [dv,dk]
+ *   o_t = scale S_t q_t
+ * the base model of the log-linear Gated DeltaNet above, whose level states
+ * follow the same transition: states have the layout of ll_gdn_decode_step's.
+ * Sequences run from given states to returned ones, can be packed end to end,
+ * and several value heads can share a key head. */
+
+/* Problem shape of ll_gdr_fwd and ll_gdr_bwd.
+ *   B, T      batch rows and tokens per row (>= 1)
+ *   H, Hk     value heads and query/key heads, H a multiple of Hk: value head
+ *             h reads query/key head h / (H / Hk)
+ *   dk, dv    key / value head dims, each in {16, 32, 64, 128}
+ *   n_seqs    0: every batch row is one sequence of T tokens.
+ *             n >= 1 (B == 1): n sequences packed along the row, sequence i
+ *             the tokens seq_starts[i] .. seq_starts[i+1] - 1 (may be empty)
+ *   scale     factor of the output
+ *   io        dtype of q, k, v, o and their gradients; log_alpha, beta and the
+ *             states are always float32                                       */
+typedef struct {
+  int B, H, Hk, T, dk, dv, n_seqs;
+  float scale;
+  ll_dtype io;
+} ll_gdr_shape;
+
+/* Bytes of workspace ll_gdr_fwd needs (0 when it needs none, or on an invalid shape). */
+LL_API size_t ll_gdr_fwd_workspace_size(const ll_gdr_shape* shape);
+
+/* Kernel launches of one ll_gdr_fwd call (0 on an invalid shape). */
+LL_API int ll_gdr_fwd_launches(const ll_gdr_shape* shape);
+
+/* Forward of the gated delta rule over whole sequences.
+ *   seq_starts [n_seqs+1]  int32, required iff n_seqs > 0: non-decreasing, within
+ *              0 .. T.  Tokens outside every sequence are neither read nor
+ *              written.  A sequence with bounds that break this sets the device
+ *              error word (LL_ERR_DEVICE) and is skipped.
+ *   q, k       [B,Hk,T,dk]  io dtype;   v, o [B,H,T,dv] io dtype
+ *   log_alpha, beta [B,H,T] float32 (log_alpha = -inf forgets the state; keys
+ *              are expected to be L2-normalised, not checked)
+ *   state_in   [N,H,dv,dk]  float32 or NULL (zero states), N = n_seqs or B
+ *   state_out  [N,H,dv,dk]  float32 or NULL: the states after the last token
+ *              (state_in's for an empty sequence).  May be state_in itself.
+ *   workspace  >= ll_gdr_fwd_workspace_size(shape) bytes, 256-byte aligned
+ *              (NULL when that is 0)
+ * o and state_out may not overlap the inputs (but state_out = state_in) or
+ * one another (LL_ERR_INVALID_ARG). */
+LL_API ll_status ll_gdr_fwd(const ll_gdr_shape* shape, const int32_t* seq_starts, const void* q, const void* k,
+                            const void* v, const float* log_alpha, const float* beta, const float* state_in,
+                            void* o, float* state_out, void* workspace, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace ll_gdr_bwd needs (0 on an invalid shape). */
+LL_API size_t ll_gdr_bwd_workspace_size(const ll_gdr_shape* shape);
+
+/* Kernel launches of one ll_gdr_bwd call (0 on an invalid shape). */
+LL_API int ll_gdr_bwd_launches(const ll_gdr_shape* shape);
+
+/* Backward of ll_gdr_fwd: for f = sum(o . dout) + sum(state_out . dstate_out)
+ * writes the exact gradients of q, k, v, log_alpha, beta and state_in.
+ *   seq_starts, q, k, v, log_alpha, beta, state_in   the forward's inputs
+ *   dout       [B,H,T,dv]  io dtype
+ *   dstate_out [N,H,dv,dk] float32 or NULL (zero)
+ *   dq, dk     [B,Hk,T,dk] io dtype, written: summed over the value heads that
+ *              share the key head, rounded once
+ *   dv         [B,H,T,dv]  io dtype, written
+ *   dlog_alpha, dbeta [B,H,T] float32, written
+ *   dstate_in  [N,H,dv,dk] float32 or NULL, written
+ *   workspace  >= ll_gdr_bwd_workspace_size(shape) bytes, 256-byte aligned
+ * With w_t = A_t k_t, A_t the gradient of S_t: dv = beta w, dbeta = e . w,
+ * dlog_alpha_t = <alpha_t S_{t-1}, A_t - beta_t w_t k_t^T>.
+ * Rows outside every sequence are not written.  No output may overlap an input
+ * or another output, but dstate_in may be dstate_out itself. */
+LL_API ll_status ll_gdr_bwd(const ll_gdr_shape* shape, const int32_t* seq_starts, const void* q, const void* k,
+                            const void* v, const float* log_alpha, const float* beta, const float* state_in,
+                            const void* dout, const float* dstate_out, void* dq, void* dk, void* dv,
+                            float* dlog_alpha, float* dbeta, float* dstate_in, void* workspace, size_t ws_bytes,
+                            void* stream);
+
+/* One decode step of the gated delta rule for every batch row.
+ *   B, H, Hk, dk, dv, io, scale: as ll_gdr_shape
+ *   slots   [B]  int64 or NULL: row b's state is states[slots[b]] (NULL: states[b]).
+ *           -1 marks a row of padding: its state and output are left as they
+ *           are.  Any other slot outside 0 .. n_slots-1, and a slot that two
+ *           rows name, sets the device error word (LL_ERR_DEVICE); the former's
+ *           row is left as it is, the latter's rows and state are unspecified.
+ *   n_slots states in the pool (>= B when slots is NULL)
+ *   q, k    [B,Hk,dk] io dtype;   v, o [B,H,dv] io dtype
+ *   log_alpha, beta [B,H] float32
+ *   states  [n_slots,H,dv,dk] float32, in/out, each named state read and written once */
+LL_API ll_status ll_gdr_decode_step(int B, int H, int Hk, int dk, int dv, ll_dtype io, float scale,
+                                    const int64_t* slots, int n_slots, const void* q, const void* k,
+                                    const void* v, const float* log_alpha, const float* beta, float* states,
+                                    void* o, void* stream);
 
 #ifdef __cplusplus
 }

@@ -28,7 +28,8 @@ SYMBOLS = ("ll_version", "ll_status_str", "ll_last_device_error", "ll_attn_fwd_w
            "ll_gdn_decode_step", "ll_gdn_fwd_b_workspace_size", "ll_gdn_fwd_b", "ll_attn_fwd_cont_workspace_size",
            "ll_attn_fwd_cont", "ll_attn_bwd_workspace_size", "ll_attn_bwd_launches", "ll_attn_bwd",
            "ll_attn_fwd_level_decay_workspace_size", "ll_attn_fwd_level_decay_launches", "ll_attn_fwd_level_decay",
-           "ll_attn_decode_step_level_decay",
+           "ll_attn_decode_step_level_decay", "ll_gdr_fwd_workspace_size", "ll_gdr_fwd_launches", "ll_gdr_fwd",
+           "ll_gdr_bwd_workspace_size", "ll_gdr_bwd_launches", "ll_gdr_bwd", "ll_gdr_decode_step",
            # test hooks (include/ll_attn_test.h)
            "ll_test_fwd_withhold_node")
 
@@ -42,6 +43,12 @@ class LLError(RuntimeError):
 class ll_shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("T", ctypes.c_int), ("dk", ctypes.c_int),
                 ("dv", ctypes.c_int), ("L", ctypes.c_int), ("chunk", ctypes.c_int), ("Ls", ctypes.c_int),
+                ("io", ctypes.c_int)]
+
+
+class ll_gdr_shape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("Hk", ctypes.c_int), ("T", ctypes.c_int),
+                ("dk", ctypes.c_int), ("dv", ctypes.c_int), ("n_seqs", ctypes.c_int), ("scale", ctypes.c_float),
                 ("io", ctypes.c_int)]
 
 
@@ -103,6 +110,20 @@ def lib() -> ctypes.CDLL:
     L.ll_attn_bwd_launches.argtypes = [shp]
     L.ll_attn_bwd.restype = i32
     L.ll_attn_bwd.argtypes = [shp, vp, vp, vp, fp, fp, vp, vp, vp, vp, fp, fp, vp, sz, vp]
+    gshp = ctypes.POINTER(ll_gdr_shape)
+    for n in ("ll_gdr_fwd_workspace_size", "ll_gdr_bwd_workspace_size"):
+        getattr(L, n).restype = sz
+        getattr(L, n).argtypes = [gshp]
+    for n in ("ll_gdr_fwd_launches", "ll_gdr_bwd_launches"):
+        getattr(L, n).restype = i32
+        getattr(L, n).argtypes = [gshp]
+    L.ll_gdr_fwd.restype = i32
+    L.ll_gdr_fwd.argtypes = [gshp] + [vp] * 10 + [sz, vp]
+    L.ll_gdr_bwd.restype = i32
+    L.ll_gdr_bwd.argtypes = [gshp] + [vp] * 16 + [sz, vp]
+    L.ll_gdr_decode_step.restype = i32
+    L.ll_gdr_decode_step.argtypes = [i32, i32, i32, i32, i32, i32, ctypes.c_float, vp, i32, vp, vp, vp, fp, fp, fp,
+                                     vp, vp]
     L.ll_test_fwd_withhold_node.restype = i32
     L.ll_test_fwd_withhold_node.argtypes = [shp, vp, vp, vp, fp, fp, vp, vp, sz, ctypes.c_longlong,
                                             ctypes.c_ulonglong, vp]
@@ -432,6 +453,138 @@ def ll_gdn_fwd_b(q, k, v, log_alpha, beta, lam, chunk: int, *, o=None, workspace
     delta-rule pseudo-values).  Arguments as ll_gdn_fwd."""
     return _gdn_forward("ll_gdn_fwd_b", ll_gdn_fwd_b_workspace_size, q, k, v, log_alpha, beta, lam, chunk, o,
                         workspace)
+
+
+def make_gdr_shape(B, H, Hk, T, dk, dv, n_seqs=0, scale=1.0, io=LL_BF16) -> ll_gdr_shape:
+    return ll_gdr_shape(B, H, Hk, T, dk, dv, n_seqs, scale, io)
+
+
+def ll_gdr_fwd_workspace_size(shape: ll_gdr_shape) -> int:
+    return int(lib().ll_gdr_fwd_workspace_size(ctypes.byref(shape)))
+
+
+def ll_gdr_fwd_launches(shape: ll_gdr_shape) -> int:
+    return int(lib().ll_gdr_fwd_launches(ctypes.byref(shape)))
+
+
+def ll_gdr_bwd_workspace_size(shape: ll_gdr_shape) -> int:
+    return int(lib().ll_gdr_bwd_workspace_size(ctypes.byref(shape)))
+
+
+def ll_gdr_bwd_launches(shape: ll_gdr_shape) -> int:
+    return int(lib().ll_gdr_bwd_launches(ctypes.byref(shape)))
+
+
+def _need_like(x, name, shape, dtype, device):
+    _need(x, name, dtype)
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(x.shape)}")
+    if x.device != device:
+        raise ValueError(f"{name} must be on {device}, got {x.device}")
+
+
+def _gdr_shape(q, k, v, log_alpha, beta, scale, seq_starts):
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q and v must be [B,Hk,T,dk] and [B,H,T,dv]")
+    B, Hk, T, dk = q.shape
+    H, dv = v.shape[1], v.shape[3]
+    _need(q, "q")
+    io = _io(q.dtype)
+    _need_like(k, "k", q.shape, q.dtype, q.device)
+    _need_like(v, "v", (B, H, T, dv), q.dtype, q.device)
+    _need_like(log_alpha, "log_alpha", (B, H, T), torch.float32, q.device)
+    _need_like(beta, "beta", (B, H, T), torch.float32, q.device)
+    n = 0
+    if seq_starts is not None:
+        n = seq_starts.numel() - 1
+        if n < 1:
+            raise ValueError("seq_starts must have at least two entries")
+        _need_like(seq_starts, "seq_starts", (n + 1,), torch.int32, q.device)
+    return make_gdr_shape(B, H, Hk, T, dk, dv, n, float(scale), io), (n or B, H, dv, dk)
+
+
+def ll_gdr_fwd(q, k, v, log_alpha, beta, *, scale=1.0, state_in=None, state_out=None, seq_starts=None, o=None,
+               workspace=None):
+    """Gated delta rule forward over whole sequences.  q, k [B,Hk,T,dk]; v
+    [B,H,T,dv] (f32 or bf16; H a multiple of Hk); log_alpha, beta [B,H,T]
+    float32.  state_in / state_out [N,H,dv,dk] float32 (N = sequences): the
+    states before and after, optional; state_out may be state_in.  seq_starts
+    [n+1] int32 packs n sequences along the tokens (B = 1).  Returns o
+    [B,H,T,dv]; rows outside every packed sequence are left as they are."""
+    shape, states = _gdr_shape(q, k, v, log_alpha, beta, scale, seq_starts)
+    for x, n in ((state_in, "state_in"), (state_out, "state_out")):
+        if x is not None:
+            _need_like(x, n, states, torch.float32, q.device)
+    if o is None:
+        o = torch.empty_like(v)
+    _need_like(o, "o", v.shape, q.dtype, q.device)
+    if workspace is None:
+        workspace = alloc_workspace(ll_gdr_fwd_workspace_size(shape), q.device)
+    _need_like(workspace, "workspace", workspace.shape, torch.uint8, q.device)
+    with torch.cuda.device(q.device):
+        st = lib().ll_gdr_fwd(ctypes.byref(shape), _ptr(seq_starts), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha),
+                              _ptr(beta), _ptr(state_in), _ptr(o), _ptr(state_out), _ptr(workspace),
+                              ctypes.c_size_t(workspace.numel()), _stream(q.device))
+    _check(st, "ll_gdr_fwd")
+    return o
+
+
+def ll_gdr_bwd(q, k, v, log_alpha, beta, dout, *, scale=1.0, state_in=None, dstate_out=None, seq_starts=None,
+               grads=None, dstate_in=None, workspace=None):
+    """Backward of ll_gdr_fwd for the gradients dout [B,H,T,dv] of o and
+    (optional) dstate_out of state_out.  Returns (dq, dk, dv, dlog_alpha,
+    dbeta), with dq and dk summed over the value heads of a key head; ``grads``
+    may pass those five to be written in place, dstate_in [N,H,dv,dk] receives
+    state_in's gradient (it may be dstate_out)."""
+    shape, states = _gdr_shape(q, k, v, log_alpha, beta, scale, seq_starts)
+    _need_like(dout, "dout", v.shape, q.dtype, q.device)
+    for x, n in ((state_in, "state_in"), (dstate_out, "dstate_out"), (dstate_in, "dstate_in")):
+        if x is not None:
+            _need_like(x, n, states, torch.float32, q.device)
+    if grads is None:
+        grads = tuple(torch.empty_like(x) for x in (q, k, v, log_alpha, beta))
+    for x, ref, n in zip(grads, (q, k, v, log_alpha, beta), ("dq", "dk", "dv", "dlog_alpha", "dbeta"), strict=True):
+        _need_like(x, n, ref.shape, ref.dtype, q.device)
+    if workspace is None:
+        workspace = alloc_workspace(ll_gdr_bwd_workspace_size(shape), q.device)
+    _need_like(workspace, "workspace", workspace.shape, torch.uint8, q.device)
+    with torch.cuda.device(q.device):
+        st = lib().ll_gdr_bwd(ctypes.byref(shape), _ptr(seq_starts), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha),
+                              _ptr(beta), _ptr(state_in), _ptr(dout), _ptr(dstate_out), *[_ptr(x) for x in grads],
+                              _ptr(dstate_in), _ptr(workspace), ctypes.c_size_t(workspace.numel()),
+                              _stream(q.device))
+    _check(st, "ll_gdr_bwd")
+    return tuple(grads)
+
+
+def ll_gdr_decode_step(q, k, v, log_alpha, beta, states, *, scale=1.0, slots=None, o=None):
+    """One gated delta rule decode step.  q, k [B,Hk,dk]; v [B,H,dv]; log_alpha,
+    beta [B,H] float32; states [n_slots,H,dv,dk] float32, updated in place.  Row b
+    uses states[slots[b]] (slots [B] int64, distinct; -1 = a row of padding, left
+    as it is) or states[b].  Returns o [B,H,dv]."""
+    if q.dim() != 3 or v.dim() != 3 or states.dim() != 4:
+        raise ValueError("q, v and states must be [B,Hk,dk], [B,H,dv] and [n_slots,H,dv,dk]")
+    B, Hk, dk = q.shape
+    H, dv = v.shape[1], v.shape[2]
+    _need(q, "q")
+    io = _io(q.dtype)
+    _need_like(k, "k", q.shape, q.dtype, q.device)
+    _need_like(v, "v", (B, H, dv), q.dtype, q.device)
+    _need_like(log_alpha, "log_alpha", (B, H), torch.float32, q.device)
+    _need_like(beta, "beta", (B, H), torch.float32, q.device)
+    _need_like(states, "states", (states.shape[0], H, dv, dk), torch.float32, q.device)
+    if slots is not None:
+        _need_like(slots, "slots", (B,), torch.int64, q.device)
+    if o is None:
+        o = torch.empty_like(v)
+    _need_like(o, "o", v.shape, q.dtype, q.device)
+    with torch.cuda.device(q.device):
+        st = lib().ll_gdr_decode_step(B, H, Hk, dk, dv, io, float(scale), _ptr(slots), states.shape[0], _ptr(q),
+                                      _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(states), _ptr(o),
+                                      _stream(q.device))
+    _check(st, "ll_gdr_decode_step")
+    return o
+
 
 def ll_test_fwd_withhold_node(q, k, v, log_alpha, lam, chunk: int, node: int, timeout_ns: int, *, o=None,
                               workspace=None) -> int:

@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "bwd.cuh"
+#include "gdr.cuh"
 #include "level_decay.cuh"
 
 namespace llattn {
@@ -583,6 +584,183 @@ ll_status ll_gdn_fwd(const ll_shape* s, const void* q, const void* k, const void
             static_cast<cudaStream_t>(stream), err_word()};
   if (!a.err) return LL_ERR_CUDA;
   return gdn_launch(a);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- the gated delta rule
+static ll_status check_gdr_shape(const ll_gdr_shape* s) {
+  if (!s) return LL_ERR_INVALID_ARG;
+  if (s->B < 1 || s->H < 1 || s->Hk < 1 || s->T < 1 || s->n_seqs < 0) return LL_ERR_INVALID_ARG;
+  if (s->H % s->Hk != 0 || (s->n_seqs > 0 && s->B != 1)) return LL_ERR_INVALID_ARG;
+  if (s->io != LL_F32 && s->io != LL_BF16) return LL_ERR_INVALID_ARG;
+  if (!(s->scale - s->scale == 0.f)) return LL_ERR_INVALID_ARG;  // finite
+  if (!head_dim_ok(s->dk) || !head_dim_ok(s->dv)) return LL_ERR_UNSUPPORTED;
+  // CTAs are counted in 31 bits: at most (sequences or 16-token pieces) x heads x 8 of them
+  const long long units = s->n_seqs ? (long long)s->T / 16 + s->n_seqs : (long long)s->B * ((s->T + 15ll) / 16);
+  if (units >= (1ll << 31) || units * s->H >= (1ll << 28)) return LL_ERR_UNSUPPORTED;
+  return LL_OK;
+}
+
+static GdrArgs gdr_args(const ll_gdr_shape* s) {
+  GdrArgs a{};
+  a.B = s->B;
+  a.H = s->H;
+  a.Hk = s->Hk;
+  a.T = s->T;
+  a.dk = s->dk;
+  a.dv = s->dv;
+  a.n_seqs = s->n_seqs;
+  a.io = s->io;
+  a.scale = s->scale;
+  return a;
+}
+
+namespace {
+struct Range {
+  const void* p;
+  size_t n;
+};
+bool ranges_overlap(const Range& a, const Range& b) {
+  if (!a.p || !b.p) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x < y + b.n && y < x + a.n;
+}
+}  // namespace
+
+extern "C" {
+
+size_t ll_gdr_fwd_workspace_size(const ll_gdr_shape* s) {
+  return check_gdr_shape(s) == LL_OK ? gdr_fwd_workspace(gdr_args(s)) : 0;
+}
+
+int ll_gdr_fwd_launches(const ll_gdr_shape* s) {
+  return check_gdr_shape(s) == LL_OK ? gdr_fwd_launches(gdr_args(s)) : 0;
+}
+
+ll_status ll_gdr_fwd(const ll_gdr_shape* s, const int32_t* seq_starts, const void* q, const void* k, const void* v,
+                     const float* log_alpha, const float* beta, const float* state_in, void* o, float* state_out,
+                     void* workspace, size_t ws_bytes, void* stream) {
+  const ll_status st = check_gdr_shape(s);
+  if (st != LL_OK) return st;
+  if ((seq_starts != nullptr) != (s->n_seqs > 0)) return LL_ERR_INVALID_ARG;
+  const size_t es = s->io == LL_F32 ? 4 : 2, rows = (size_t)s->B * s->H * s->T, krows = (size_t)s->B * s->Hk * s->T;
+  const size_t states = (size_t)(s->n_seqs ? s->n_seqs : s->B) * s->H * s->dv * s->dk * 4;
+  const Range in[7] = {{q, krows * s->dk * es}, {k, krows * s->dk * es}, {v, rows * s->dv * es},
+                       {log_alpha, rows * 4},   {beta, rows * 4},        {state_in, states},
+                       {seq_starts, (size_t)(s->n_seqs + 1) * 4}};
+  const Range out[2] = {{o, rows * s->dv * es}, {state_out, states}};
+  for (int i = 0; i < 7; ++i)
+    if ((i < 5 && !in[i].p) || !aligned16(in[i].p)) return LL_ERR_INVALID_ARG;
+  if (!o || !aligned16(o) || !aligned16(state_out)) return LL_ERR_INVALID_ARG;
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 7; ++j)
+      if (ranges_overlap(out[i], in[j]) && !(i == 1 && j == 5 && state_in == state_out)) return LL_ERR_INVALID_ARG;
+  if (ranges_overlap(out[0], out[1])) return LL_ERR_INVALID_ARG;
+  GdrArgs a = gdr_args(s);
+  const size_t need = gdr_fwd_workspace(a);
+  if (need && (!workspace || ws_bytes < need)) return LL_ERR_WORKSPACE;
+  if (need && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return LL_ERR_WORKSPACE;
+  a.seq_starts = seq_starts;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.log_alpha = log_alpha;
+  a.beta = beta;
+  a.state_in = state_in;
+  a.o = o;
+  a.state_out = state_out;
+  a.ws = workspace;
+  a.ws_bytes = ws_bytes;
+  a.stream = static_cast<cudaStream_t>(stream);
+  a.err = err_word();
+  if (!a.err) return LL_ERR_CUDA;
+  return gdr_fwd_launch(a);
+}
+
+size_t ll_gdr_bwd_workspace_size(const ll_gdr_shape* s) {
+  return check_gdr_shape(s) == LL_OK ? gdr_bwd_workspace(gdr_args(s)) : 0;
+}
+
+int ll_gdr_bwd_launches(const ll_gdr_shape* s) {
+  return check_gdr_shape(s) == LL_OK ? gdr_bwd_launches(gdr_args(s)) : 0;
+}
+
+ll_status ll_gdr_bwd(const ll_gdr_shape* s, const int32_t* seq_starts, const void* q, const void* k, const void* v,
+                     const float* log_alpha, const float* beta, const float* state_in, const void* dout,
+                     const float* dstate_out, void* dq, void* dk, void* dv, float* dlog_alpha, float* dbeta,
+                     float* dstate_in, void* workspace, size_t ws_bytes, void* stream) {
+  const ll_status st = check_gdr_shape(s);
+  if (st != LL_OK) return st;
+  if ((seq_starts != nullptr) != (s->n_seqs > 0)) return LL_ERR_INVALID_ARG;
+  const size_t es = s->io == LL_F32 ? 4 : 2, rows = (size_t)s->B * s->H * s->T, krows = (size_t)s->B * s->Hk * s->T;
+  const size_t states = (size_t)(s->n_seqs ? s->n_seqs : s->B) * s->H * s->dv * s->dk * 4;
+  const Range in[9] = {{q, krows * s->dk * es}, {k, krows * s->dk * es},    {v, rows * s->dv * es},
+                       {log_alpha, rows * 4},   {beta, rows * 4},           {dout, rows * s->dv * es},
+                       {state_in, states},      {dstate_out, states},       {seq_starts, (size_t)(s->n_seqs + 1) * 4}};
+  const Range out[6] = {{dq, krows * s->dk * es}, {dk, krows * s->dk * es}, {dv, rows * s->dv * es},
+                        {dlog_alpha, rows * 4},   {dbeta, rows * 4},        {dstate_in, states}};
+  for (int i = 0; i < 9; ++i)
+    if ((i < 6 && !in[i].p) || !aligned16(in[i].p)) return LL_ERR_INVALID_ARG;
+  for (int i = 0; i < 6; ++i) {
+    if ((i < 5 && !out[i].p) || !aligned16(out[i].p)) return LL_ERR_INVALID_ARG;
+    for (int j = 0; j < 9; ++j)
+      if (ranges_overlap(out[i], in[j]) && !(i == 5 && j == 7 && dstate_in == dstate_out)) return LL_ERR_INVALID_ARG;
+    for (int j = i + 1; j < 6; ++j)
+      if (ranges_overlap(out[i], out[j])) return LL_ERR_INVALID_ARG;
+  }
+  GdrArgs a = gdr_args(s);
+  const size_t need = gdr_bwd_workspace(a);
+  if (!workspace || ws_bytes < need) return LL_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return LL_ERR_WORKSPACE;
+  a.seq_starts = seq_starts;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.log_alpha = log_alpha;
+  a.beta = beta;
+  a.state_in = state_in;
+  a.dout = dout;
+  a.dstate_out = dstate_out;
+  a.dq = dq;
+  a.dkey = dk;
+  a.dval = dv;
+  a.dlog_alpha = dlog_alpha;
+  a.dbeta = dbeta;
+  a.dstate_in = dstate_in;
+  a.ws = workspace;
+  a.ws_bytes = ws_bytes;
+  a.stream = static_cast<cudaStream_t>(stream);
+  a.err = err_word();
+  if (!a.err) return LL_ERR_CUDA;
+  return gdr_bwd_launch(a);
+}
+
+ll_status ll_gdr_decode_step(int B, int H, int Hk, int dk, int dv, ll_dtype io, float scale, const int64_t* slots,
+                             int n_slots, const void* q, const void* k, const void* v, const float* log_alpha,
+                             const float* beta, float* states, void* o, void* stream) {
+  if (B < 1 || H < 1 || Hk < 1 || H % Hk != 0 || n_slots < 1) return LL_ERR_INVALID_ARG;
+  if (!slots && n_slots < B) return LL_ERR_INVALID_ARG;
+  if (io != LL_F32 && io != LL_BF16) return LL_ERR_INVALID_ARG;
+  if (!(scale - scale == 0.f)) return LL_ERR_INVALID_ARG;  // finite
+  if (!head_dim_ok(dk) || !head_dim_ok(dv)) return LL_ERR_UNSUPPORTED;
+  if ((long long)B * H >= (1ll << 28)) return LL_ERR_UNSUPPORTED;
+  if (!q || !k || !v || !log_alpha || !beta || !states || !o) return LL_ERR_INVALID_ARG;
+  if (!aligned16(slots) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(log_alpha) ||
+      !aligned16(beta) || !aligned16(states) || !aligned16(o))
+    return LL_ERR_INVALID_ARG;
+  const size_t es = io == LL_F32 ? 4 : 2;
+  const size_t bk = (size_t)B * Hk * dk * es, bv = (size_t)B * H * dv * es, bg = (size_t)B * H * 4;
+  const Range in[6] = {{q, bk}, {k, bk}, {v, bv}, {log_alpha, bg}, {beta, bg}, {slots, (size_t)B * 8}};
+  const Range out[2] = {{o, bv}, {states, (size_t)n_slots * H * dv * dk * 4}};
+  for (const Range& w : out)
+    for (const Range& r : in)
+      if (ranges_overlap(w, r)) return LL_ERR_INVALID_ARG;
+  if (ranges_overlap(out[0], out[1])) return LL_ERR_INVALID_ARG;
+  unsigned* ew = err_word();
+  if (!ew) return LL_ERR_CUDA;
+  return gdr_decode_launch(B, H, Hk, dk, dv, io, scale, slots, n_slots, q, k, v, log_alpha, beta, states, o,
+                           static_cast<cudaStream_t>(stream), ew);
 }
 
 }  // extern "C"

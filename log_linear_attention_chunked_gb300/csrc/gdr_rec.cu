@@ -1,0 +1,487 @@
+// The gated delta rule token by token, states in registers: the forward, the
+// reverse recurrence of its gradient, and one decode step.
+//
+// Every row r of a state (d_v) follows a recurrence of its own,
+//   e = v[r] - alpha S[r].k,  u = beta e,  S[r] <- alpha S[r] + u k,
+//   o[r] = scale S[r].q = scale (alpha S_old[r].q + u k.q),
+// so a row needs two dot products with the OLD state and no other row: a group
+// of kLpr lanes holds a row (dk / kLpr elements each, four consecutive ones at
+// a time so that the lanes of a group read 16- or 8-byte pieces side by side),
+// and a CTA 16 rows of one (sequence, head).  Likewise backwards, with A_t the
+// adjoint of S_t (o_t's part included):
+//   A <- A + scale do q,  w = A.k,  A <- alpha (A - beta w k).
+#include "gdr.cuh"
+#include "sm100.cuh"
+
+namespace llattn {
+
+namespace {
+
+using sm100::cp_async16;
+using sm100::cp_async_commit;
+using sm100::cp_async_wait;
+
+constexpr int kRows = 16;    // rows of d_v per CTA
+constexpr int kTile = 16;    // tokens staged at a time
+static_assert(kGdrGradChunk % kTile == 0, "kept states lie on tile boundaries");
+
+template <int DK> struct RowCfg {
+  static constexpr int kLpr = DK >= 32 ? 8 : 4;   // lanes per row
+  static constexpr int kEpl = DK / kLpr;          // elements per lane
+  static constexpr int kPieces = kEpl / 4;
+  static constexpr int kThreads = kRows * kLpr;
+};
+
+// four consecutive elements as float
+__device__ __forceinline__ void load4(const float* p, float* x) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* x) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xffff0000u);
+  x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+
+template <int DK, typename P>
+__device__ __forceinline__ void load_row(const P* row, int l, float* x) {
+#pragma unroll
+  for (int c = 0; c < RowCfg<DK>::kPieces; ++c) load4(row + (c * RowCfg<DK>::kLpr + l) * 4, x + 4 * c);
+}
+template <int DK>
+__device__ __forceinline__ void store_row(float* row, int l, const float* x) {
+#pragma unroll
+  for (int c = 0; c < RowCfg<DK>::kPieces; ++c)
+    *reinterpret_cast<float4*>(row + (c * RowCfg<DK>::kLpr + l) * 4) =
+        make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+}
+template <int N>
+__device__ __forceinline__ float dot(const float* a, const float* b) {
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < N; ++i) s[i & 3] = fmaf(a[i], b[i], s[i & 3]);
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
+template <int LPR>
+__device__ __forceinline__ float group_sum(float x) {
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// rows [r0, r0 + n) of a [.., W] matrix, W * sizeof(IO) a multiple of 16, into
+// shared memory; `cols` columns from column c0
+template <typename IO>
+__device__ __forceinline__ void stage(IO* dst, const IO* src, int n, int width, int c0, int cols) {
+  const int per = cols * (int)sizeof(IO) / 16, el = 16 / (int)sizeof(IO);
+  for (int x = threadIdx.x; x < n * per; x += blockDim.x) {
+    const int r = x / per, p = x - r * per;
+    cp_async16(dst + r * cols + p * el, src + (size_t)r * width + c0 + p * el);
+  }
+}
+
+struct RecParams {
+  GdrSeqs seqs;
+  int dv;
+  float scale;
+  const void *q, *k, *v;
+  const float *log_alpha, *beta, *state_in;
+  void* o;
+  float* state_out;
+  // for the gradient: the state before every kGdrGradChunk tokens
+  // [slot, H, dv, dk] and e [B, H, T, dv]; null otherwise
+  float *kept_states, *kept_errors;
+  // the reverse recurrence
+  const void* dout;
+  const float* dstate_out;
+  float* dstate_in;
+  float *kept_adjoints, *kept_w;
+  unsigned* err;
+};
+
+// Bound: the latency of a token's chain (two dot products over a group of
+// lanes, e, the update).
+template <typename IO, int DK>
+__global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_rec_fwd_kernel(RecParams p) {
+  using Cfg = RowCfg<DK>;
+  constexpr int LPR = Cfg::kLpr, EPL = Cfg::kEpl;
+  __shared__ __align__(16) IO ks[2][kTile * DK];
+  __shared__ __align__(16) IO qs[2][kTile * DK];
+  __shared__ __align__(16) IO vs[2][kTile * kRows];
+  __shared__ float os[kTile][kRows], es[kTile][kRows];
+  __shared__ float al[kTile], bt[kTile], kq[kTile];
+
+  const int slices = p.dv / kRows;
+  const int sl = blockIdx.x % slices;
+  const int h = (blockIdx.x / slices) % p.seqs.H;
+  const int seq = blockIdx.x / slices / p.seqs.H;
+  const int tid = threadIdx.x, grp = tid / LPR, l = tid % LPR;
+  const int r0 = sl * kRows;
+  GdrSeq sq;
+  if (!gdr_seq(p.seqs, seq, sq)) {
+    if (tid == 0) raise_error(p.err, kErrDeviceArg);
+    return;
+  }
+  const int hk = h / (p.seqs.H / p.seqs.Hk);
+  const size_t row0 = ((size_t)sq.row_b * p.seqs.H + h) * p.seqs.T + sq.start;
+  const size_t krow0 = ((size_t)sq.row_b * p.seqs.Hk + hk) * p.seqs.T + sq.start;
+  const IO* qg = static_cast<const IO*>(p.q) + krow0 * DK;
+  const IO* kg = static_cast<const IO*>(p.k) + krow0 * DK;
+  const IO* vg = static_cast<const IO*>(p.v) + row0 * p.dv;
+  IO* og = p.o ? static_cast<IO*>(p.o) + row0 * p.dv : nullptr;
+  const size_t st_at = (((size_t)seq * p.seqs.H + h) * p.dv + r0 + grp) * DK;
+
+  float s[EPL];
+  if (p.state_in) load_row<DK>(p.state_in + st_at, l, s);
+  else
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) s[i] = 0.f;
+
+  const int tiles = (sq.len + kTile - 1) / kTile;
+  const int base = gdr_slot_base(p.seqs, seq, sq.start, kGdrGradChunk);
+  float la_n = 0.f, bt_n = 0.f;
+  auto fetch = [&](int j) {
+    const int t0 = j * kTile, n = min(kTile, sq.len - t0), b = j & 1;
+    stage(ks[b], kg + (size_t)t0 * DK, n, DK, 0, DK);
+    stage(qs[b], qg + (size_t)t0 * DK, n, DK, 0, DK);
+    stage(vs[b], vg + (size_t)t0 * p.dv, n, p.dv, r0, kRows);
+    cp_async_commit();
+    if (tid < n) {
+      la_n = p.log_alpha[row0 + t0 + tid];
+      bt_n = p.beta[row0 + t0 + tid];
+    }
+  };
+  if (tiles) fetch(0);
+  for (int j = 0; j < tiles; ++j) {
+    const int t0 = j * kTile, n = min(kTile, sq.len - t0), b = j & 1;
+    if (tid < n) {
+      al[tid] = expf(la_n);
+      bt[tid] = bt_n;
+    }
+    if (j + 1 < tiles) {
+      fetch(j + 1);
+      cp_async_wait<1>();
+    } else {
+      cp_async_wait<0>();
+    }
+    if (p.kept_states && t0 % kGdrGradChunk == 0)
+      store_row<DK>(p.kept_states +
+                        ((((size_t)base + t0 / kGdrGradChunk) * p.seqs.H + h) * p.dv + r0 + grp) * DK, l, s);
+    __syncthreads();
+    {  // k.q of every staged token: one group of lanes each
+      float a[EPL], c[EPL];
+      load_row<DK>(ks[b] + grp * DK, l, a);
+      load_row<DK>(qs[b] + grp * DK, l, c);
+      const float d = group_sum<LPR>(dot<EPL>(a, c));
+      if (l == 0) kq[grp] = d;
+    }
+    __syncthreads();
+    float kc[EPL], qc[EPL];
+    load_row<DK>(ks[b], l, kc);
+    load_row<DK>(qs[b], l, qc);
+    for (int t = 0; t < n; ++t) {
+      const float a = al[t], be = bt[t], v = to_f(vs[b][t * kRows + grp]), c = kq[t];
+      float sk = dot<EPL>(s, kc), sqd = dot<EPL>(s, qc);
+      float kn[EPL], qn[EPL];  // the next token's, on their way during this one's sums
+      const int tn = min(t + 1, kTile - 1);
+      load_row<DK>(ks[b] + tn * DK, l, kn);
+      load_row<DK>(qs[b] + tn * DK, l, qn);
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) {
+        sk += __shfl_xor_sync(0xffffffffu, sk, o);
+        sqd += __shfl_xor_sync(0xffffffffu, sqd, o);
+      }
+      const float e = fmaf(-a, sk, v);
+      const float u = be * e;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) s[i] = fmaf(u, kc[i], a * s[i]);
+      if (l == 0) {
+        os[t][grp] = p.scale * fmaf(a, sqd, u * c);
+        es[t][grp] = e;
+      }
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        kc[i] = kn[i];
+        qc[i] = qn[i];
+      }
+    }
+    __syncthreads();
+    for (int x = tid; x < n * kRows; x += Cfg::kThreads) {
+      const int t = x / kRows, r = x % kRows;
+      const size_t at = (size_t)(t0 + t) * p.dv + r0 + r;
+      if (og) og[at] = from_f<IO>(os[t][r]);
+      if (p.kept_errors) p.kept_errors[row0 * p.dv + at] = es[t][r];
+    }
+  }
+  if (p.state_out) store_row<DK>(p.state_out + st_at, l, s);
+}
+
+// The reverse recurrence: w_t = A_t k_t for every token, the adjoint A after
+// every kGdrGradChunk tokens, and the gradient of the state on entry.
+template <typename IO, int DK>
+__global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_rec_bwd_kernel(RecParams p) {
+  using Cfg = RowCfg<DK>;
+  constexpr int LPR = Cfg::kLpr, EPL = Cfg::kEpl;
+  __shared__ __align__(16) IO ks[2][kTile * DK];
+  __shared__ __align__(16) IO qs[2][kTile * DK];
+  __shared__ __align__(16) IO ds[2][kTile * kRows];
+  __shared__ float ws[kTile][kRows];
+  __shared__ float al[kTile], bt[kTile];
+
+  const int slices = p.dv / kRows;
+  const int sl = blockIdx.x % slices;
+  const int h = (blockIdx.x / slices) % p.seqs.H;
+  const int seq = blockIdx.x / slices / p.seqs.H;
+  const int tid = threadIdx.x, grp = tid / LPR, l = tid % LPR;
+  const int r0 = sl * kRows;
+  GdrSeq sq;
+  if (!gdr_seq(p.seqs, seq, sq)) {
+    if (tid == 0) raise_error(p.err, kErrDeviceArg);
+    return;
+  }
+  const int hk = h / (p.seqs.H / p.seqs.Hk);
+  const size_t row0 = ((size_t)sq.row_b * p.seqs.H + h) * p.seqs.T + sq.start;
+  const size_t krow0 = ((size_t)sq.row_b * p.seqs.Hk + hk) * p.seqs.T + sq.start;
+  const IO* qg = static_cast<const IO*>(p.q) + krow0 * DK;
+  const IO* kg = static_cast<const IO*>(p.k) + krow0 * DK;
+  const IO* dg = static_cast<const IO*>(p.dout) + row0 * p.dv;
+  const size_t st_at = (((size_t)seq * p.seqs.H + h) * p.dv + r0 + grp) * DK;
+
+  float a[EPL];
+  if (p.dstate_out) load_row<DK>(p.dstate_out + st_at, l, a);
+  else
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) a[i] = 0.f;
+
+  const int tiles = (sq.len + kTile - 1) / kTile;
+  const int base = gdr_slot_base(p.seqs, seq, sq.start, kGdrGradChunk);
+  float la_n = 0.f, bt_n = 0.f;
+  auto fetch = [&](int j) {
+    const int t0 = j * kTile, n = min(kTile, sq.len - t0), b = j & 1;
+    stage(ks[b], kg + (size_t)t0 * DK, n, DK, 0, DK);
+    stage(qs[b], qg + (size_t)t0 * DK, n, DK, 0, DK);
+    stage(ds[b], dg + (size_t)t0 * p.dv, n, p.dv, r0, kRows);
+    cp_async_commit();
+    if (tid < n) {
+      la_n = p.log_alpha[row0 + t0 + tid];
+      bt_n = p.beta[row0 + t0 + tid];
+    }
+  };
+  if (tiles) fetch(tiles - 1);
+  for (int j = tiles - 1; j >= 0; --j) {
+    const int t0 = j * kTile, n = min(kTile, sq.len - t0), b = j & 1;
+    if (tid < n) {
+      al[tid] = expf(la_n);
+      bt[tid] = bt_n;
+    }
+    if (j > 0) {
+      fetch(j - 1);
+      cp_async_wait<1>();
+    } else {
+      cp_async_wait<0>();
+    }
+    if (t0 + n == sq.len || (t0 + n) % kGdrGradChunk == 0)
+      store_row<DK>(p.kept_adjoints +
+                        ((((size_t)base + t0 / kGdrGradChunk) * p.seqs.H + h) * p.dv + r0 + grp) * DK, l, a);
+    __syncthreads();
+    float kc[EPL], qc[EPL];
+    load_row<DK>(ks[b] + (n - 1) * DK, l, kc);
+    load_row<DK>(qs[b] + (n - 1) * DK, l, qc);
+    for (int t = n - 1; t >= 0; --t) {
+      const float d = p.scale * to_f(ds[b][t * kRows + grp]);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) a[i] = fmaf(d, qc[i], a[i]);
+      float w = dot<EPL>(a, kc);
+      float kn[EPL], qn[EPL];
+      const int tn = max(t - 1, 0);
+      load_row<DK>(ks[b] + tn * DK, l, kn);
+      load_row<DK>(qs[b] + tn * DK, l, qn);
+      w = group_sum<LPR>(w);
+      const float bw = -bt[t] * w, al_t = al[t];
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) a[i] = al_t * fmaf(bw, kc[i], a[i]);
+      if (l == 0) ws[t][grp] = w;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        kc[i] = kn[i];
+        qc[i] = qn[i];
+      }
+    }
+    __syncthreads();
+    for (int x = tid; x < n * kRows; x += Cfg::kThreads) {
+      const int t = x / kRows, r = x % kRows;
+      p.kept_w[(row0 + t0 + t) * p.dv + r0 + r] = ws[t][r];
+    }
+  }
+  if (p.dstate_in) store_row<DK>(p.dstate_in + st_at, l, a);
+}
+
+// ---------------------------------------------------------------- one decode step
+constexpr int kStepPasses = 2;  // rows in flight per group of lanes
+
+// Per (b, h): the state is read and written once, which is what bounds the
+// step.  A group of lanes takes kStepPasses rows, all their loads issued
+// before any is used; 16 * kStepPasses rows of d_v to a CTA, so that one
+// request of few heads still spreads over the SMs.
+template <typename IO, int DK>
+__global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_decode_kernel(
+    int H, int Hk, int dv, float scale, const int64_t* __restrict__ slots, int n_slots, const IO* __restrict__ q,
+    const IO* __restrict__ k, const IO* __restrict__ v, const float* __restrict__ log_alpha,
+    const float* __restrict__ beta, float* __restrict__ states, IO* __restrict__ o, unsigned* __restrict__ err) {
+  using Cfg = RowCfg<DK>;
+  constexpr int LPR = Cfg::kLpr, EPL = Cfg::kEpl;
+  __shared__ float os[kRows * kStepPasses];
+  const int cta_rows = kRows * kStepPasses;
+  const int slices = (dv + cta_rows - 1) / cta_rows;
+  const int sl = blockIdx.x % slices;
+  const int h = (blockIdx.x / slices) % H;
+  const int b = blockIdx.x / slices / H;
+  const int tid = threadIdx.x, grp = tid / LPR, l = tid % LPR;
+  const size_t bh = (size_t)b * H + h;
+  const size_t bk = (size_t)b * Hk + h / (H / Hk);
+  long long slot = slots ? slots[b] : b;
+  float kv[EPL], qv[EPL];
+  load_row<DK>(k + bk * DK, l, kv);
+  load_row<DK>(q + bk * DK, l, qv);
+  const float la = log_alpha[bh], be = beta[bh];
+  if (slot < 0 || slot >= n_slots) {  // -1 is a row of padding; anything else out of range an error
+    if (slot != -1 && tid == 0) raise_error(err, kErrDeviceArg);
+    return;
+  }
+  float* st = states + ((size_t)slot * H + h) * dv * DK;
+  float s[kStepPasses][EPL], vv[kStepPasses];
+  const int r0 = sl * cta_rows + grp;
+#pragma unroll
+  for (int x = 0; x < kStepPasses; ++x) {
+    const int r = r0 + kRows * x;
+    if (r < dv) {
+      load_row<DK>(st + (size_t)r * DK, l, s[x]);
+      vv[x] = to_f(v[bh * dv + r]);
+    }
+  }
+  // two rows of the batch with one slot would race: one CTA of the row looks
+  if (slots && sl == 0 && h == 0)
+    for (int x = tid; x < b; x += Cfg::kThreads)
+      if (slots[x] == slot) raise_error(err, kErrDeviceArg);
+  const float a = expf(la);
+  const float c = group_sum<LPR>(dot<EPL>(kv, qv));
+#pragma unroll
+  for (int x = 0; x < kStepPasses; ++x) {
+    const int r = r0 + kRows * x;
+    float sk = 0.f, sqd = 0.f;
+    if (r < dv) {
+      sk = dot<EPL>(s[x], kv);
+      sqd = dot<EPL>(s[x], qv);
+    }
+    sk = group_sum<LPR>(sk);
+    sqd = group_sum<LPR>(sqd);
+    if (r < dv) {
+      const float u = be * fmaf(-a, sk, vv[x]);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) s[x][i] = fmaf(u, kv[i], a * s[x][i]);
+      store_row<DK>(st + (size_t)r * DK, l, s[x]);
+      if (l == 0) os[grp + kRows * x] = scale * fmaf(a, sqd, u * c);
+    }
+  }
+  __syncthreads();
+  if (tid < cta_rows && sl * cta_rows + tid < dv) o[bh * dv + sl * cta_rows + tid] = from_f<IO>(os[tid]);
+}
+
+template <template <typename, int> class F, typename... A>
+ll_status by_type(ll_dtype io, int dk, A... args) {
+  const bool f = io == LL_F32;
+  switch (dk) {
+    case 16: return f ? F<float, 16>::run(args...) : F<__nv_bfloat16, 16>::run(args...);
+    case 32: return f ? F<float, 32>::run(args...) : F<__nv_bfloat16, 32>::run(args...);
+    case 64: return f ? F<float, 64>::run(args...) : F<__nv_bfloat16, 64>::run(args...);
+    case 128: return f ? F<float, 128>::run(args...) : F<__nv_bfloat16, 128>::run(args...);
+  }
+  return LL_ERR_UNSUPPORTED;
+}
+
+template <typename IO, int DK> struct RecFwd {
+  static ll_status run(const RecParams& p, unsigned grid, cudaStream_t st) {
+    gdr_rec_fwd_kernel<IO, DK><<<grid, RowCfg<DK>::kThreads, 0, st>>>(p);
+    LL_CUDA_OK(cudaGetLastError());
+    return LL_OK;
+  }
+};
+template <typename IO, int DK> struct RecBwd {
+  static ll_status run(const RecParams& p, unsigned grid, cudaStream_t st) {
+    gdr_rec_bwd_kernel<IO, DK><<<grid, RowCfg<DK>::kThreads, 0, st>>>(p);
+    LL_CUDA_OK(cudaGetLastError());
+    return LL_OK;
+  }
+};
+
+RecParams rec_params(const GdrArgs& a) {
+  RecParams p{};
+  p.seqs = GdrSeqs{a.n_seqs ? a.seq_starts : nullptr, gdr_sequences(a), a.T, a.H, a.Hk};
+  p.dv = a.dv;
+  p.scale = a.scale;
+  p.q = a.q;
+  p.k = a.k;
+  p.v = a.v;
+  p.log_alpha = a.log_alpha;
+  p.beta = a.beta;
+  p.state_in = a.state_in;
+  p.err = a.err;
+  return p;
+}
+unsigned rec_grid(const GdrArgs& a) { return (unsigned)((size_t)gdr_sequences(a) * a.H * (a.dv / kRows)); }
+
+}  // namespace
+
+ll_status gdr_rec_fwd_launch(const GdrArgs& a, float* kept_states, float* kept_errors) {
+  RecParams p = rec_params(a);
+  p.o = a.o;
+  p.state_out = a.state_out;
+  p.kept_states = kept_states;
+  p.kept_errors = kept_errors;
+  return by_type<RecFwd, const RecParams&, unsigned, cudaStream_t>(a.io, a.dk, p, rec_grid(a), a.stream);
+}
+
+ll_status gdr_rec_bwd_launch(const GdrArgs& a, float* kept_adjoints, float* kept_w) {
+  RecParams p = rec_params(a);
+  p.dout = a.dout;
+  p.dstate_out = a.dstate_out;
+  p.dstate_in = a.dstate_in;
+  p.kept_adjoints = kept_adjoints;
+  p.kept_w = kept_w;
+  return by_type<RecBwd, const RecParams&, unsigned, cudaStream_t>(a.io, a.dk, p, rec_grid(a), a.stream);
+}
+
+namespace {
+struct StepArgs {
+  int B, H, Hk, dv;
+  float scale;
+  const int64_t* slots;
+  int n_slots;
+  const void *q, *k, *v;
+  const float *la, *beta;
+  float* states;
+  void* o;
+  cudaStream_t stream;
+  unsigned* err;
+};
+template <typename IO, int DK> struct Step {
+  static ll_status run(const StepArgs& a) {
+    const int rows = kRows * kStepPasses;
+    const unsigned grid = (unsigned)((size_t)a.B * a.H * ((a.dv + rows - 1) / rows));
+    gdr_decode_kernel<IO, DK><<<grid, RowCfg<DK>::kThreads, 0, a.stream>>>(
+        a.H, a.Hk, a.dv, a.scale, a.slots, a.n_slots, static_cast<const IO*>(a.q), static_cast<const IO*>(a.k),
+        static_cast<const IO*>(a.v), a.la, a.beta, a.states, static_cast<IO*>(a.o), a.err);
+    LL_CUDA_OK(cudaGetLastError());
+    return LL_OK;
+  }
+};
+}  // namespace
+
+ll_status gdr_decode_launch(int B, int H, int Hk, int dk, int dv, ll_dtype io, float scale, const int64_t* slots,
+                            int n_slots, const void* q, const void* k, const void* v, const float* log_alpha,
+                            const float* beta, float* states, void* o, cudaStream_t stream, unsigned* err) {
+  const StepArgs a{B, H, Hk, dv, scale, slots, n_slots, q, k, v, log_alpha, beta, states, o, stream, err};
+  return by_type<Step, const StepArgs&>(io, dk, a);
+}
+
+}  // namespace llattn
