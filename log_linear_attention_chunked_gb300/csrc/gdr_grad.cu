@@ -314,9 +314,11 @@ ll_status gdr_grad_launch(const GdrArgs& a, const float* states, const float* er
                         : run_dk<__nv_bfloat16>(a.dk, p, grid, smem, a.stream);
 }
 
-size_t gdr_fwd_workspace(const GdrArgs&) { return 0; }
-int gdr_fwd_launches(const GdrArgs&) { return 1; }
-ll_status gdr_fwd_launch(const GdrArgs& a) { return gdr_rec_fwd_launch(a, nullptr, nullptr); }
+size_t gdr_fwd_workspace(const GdrArgs& a) { return gdr_tc_supported(a) ? gdr_tc_fwd_workspace(a) : 0; }
+int gdr_fwd_launches(const GdrArgs& a) { return gdr_tc_supported(a) ? 3 : 1; }
+ll_status gdr_fwd_launch(const GdrArgs& a) {
+  return gdr_tc_supported(a) ? gdr_tc_fwd_launch(a) : gdr_rec_fwd_launch(a, nullptr, nullptr);
+}
 
 size_t gdr_bwd_workspace(const GdrArgs& a) { return rec_plan(a).total; }
 int gdr_bwd_launches(const GdrArgs&) { return 3; }
