@@ -476,11 +476,27 @@ def ll_gdr_bwd_launches(shape: ll_gdr_shape) -> int:
 
 
 def _need_like(x, name, shape, dtype, device):
+    if x.dtype is dtype and x.shape == shape and x.device == device and x.is_contiguous():
+        return
     _need(x, name, dtype)
-    if tuple(x.shape) != tuple(shape):
+    if x.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(x.shape)}")
-    if x.device != device:
-        raise ValueError(f"{name} must be on {device}, got {x.device}")
+    raise ValueError(f"{name} must be on {device}, got {x.device}")
+
+
+def _addr(x):
+    return None if x is None else x.data_ptr()
+
+
+def _launch(entry, device, *args):
+    """Call an entry point on the device's current stream, that device being current."""
+    fn = getattr(lib(), entry)
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    _check(st, entry)
 
 
 def _gdr_shape(q, k, v, log_alpha, beta, scale, seq_starts):
@@ -489,18 +505,26 @@ def _gdr_shape(q, k, v, log_alpha, beta, scale, seq_starts):
     B, Hk, T, dk = q.shape
     H, dv = v.shape[1], v.shape[3]
     _need(q, "q")
+    dev = q.device
     io = _io(q.dtype)
-    _need_like(k, "k", q.shape, q.dtype, q.device)
-    _need_like(v, "v", (B, H, T, dv), q.dtype, q.device)
-    _need_like(log_alpha, "log_alpha", (B, H, T), torch.float32, q.device)
-    _need_like(beta, "beta", (B, H, T), torch.float32, q.device)
+    _need_like(k, "k", q.shape, q.dtype, dev)
+    _need_like(v, "v", (B, H, T, dv), q.dtype, dev)
+    _need_like(log_alpha, "log_alpha", (B, H, T), torch.float32, dev)
+    _need_like(beta, "beta", (B, H, T), torch.float32, dev)
     n = 0
     if seq_starts is not None:
         n = seq_starts.numel() - 1
         if n < 1:
             raise ValueError("seq_starts must have at least two entries")
-        _need_like(seq_starts, "seq_starts", (n + 1,), torch.int32, q.device)
+        _need_like(seq_starts, "seq_starts", (n + 1,), torch.int32, dev)
     return make_gdr_shape(B, H, Hk, T, dk, dv, n, float(scale), io), (n or B, H, dv, dk)
+
+
+def _gdr_workspace(workspace, nbytes, device):
+    if workspace is None:
+        return alloc_workspace(nbytes, device) if nbytes else None
+    _need_like(workspace, "workspace", workspace.shape, torch.uint8, device)
+    return workspace
 
 
 def ll_gdr_fwd(q, k, v, log_alpha, beta, *, scale=1.0, state_in=None, state_out=None, seq_starts=None, o=None,
@@ -517,15 +541,12 @@ def ll_gdr_fwd(q, k, v, log_alpha, beta, *, scale=1.0, state_in=None, state_out=
             _need_like(x, n, states, torch.float32, q.device)
     if o is None:
         o = torch.empty_like(v)
-    _need_like(o, "o", v.shape, q.dtype, q.device)
-    if workspace is None:
-        workspace = alloc_workspace(ll_gdr_fwd_workspace_size(shape), q.device)
-    _need_like(workspace, "workspace", workspace.shape, torch.uint8, q.device)
-    with torch.cuda.device(q.device):
-        st = lib().ll_gdr_fwd(ctypes.byref(shape), _ptr(seq_starts), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha),
-                              _ptr(beta), _ptr(state_in), _ptr(o), _ptr(state_out), _ptr(workspace),
-                              ctypes.c_size_t(workspace.numel()), _stream(q.device))
-    _check(st, "ll_gdr_fwd")
+    else:
+        _need_like(o, "o", v.shape, q.dtype, q.device)
+    ws = _gdr_workspace(workspace, ll_gdr_fwd_workspace_size(shape), q.device)
+    _launch("ll_gdr_fwd", q.device, ctypes.byref(shape), _addr(seq_starts), _addr(q), _addr(k), _addr(v),
+            _addr(log_alpha), _addr(beta), _addr(state_in), _addr(o), _addr(state_out), _addr(ws),
+            0 if ws is None else ws.numel())
     return o
 
 
@@ -545,15 +566,10 @@ def ll_gdr_bwd(q, k, v, log_alpha, beta, dout, *, scale=1.0, state_in=None, dsta
         grads = tuple(torch.empty_like(x) for x in (q, k, v, log_alpha, beta))
     for x, ref, n in zip(grads, (q, k, v, log_alpha, beta), ("dq", "dk", "dv", "dlog_alpha", "dbeta"), strict=True):
         _need_like(x, n, ref.shape, ref.dtype, q.device)
-    if workspace is None:
-        workspace = alloc_workspace(ll_gdr_bwd_workspace_size(shape), q.device)
-    _need_like(workspace, "workspace", workspace.shape, torch.uint8, q.device)
-    with torch.cuda.device(q.device):
-        st = lib().ll_gdr_bwd(ctypes.byref(shape), _ptr(seq_starts), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha),
-                              _ptr(beta), _ptr(state_in), _ptr(dout), _ptr(dstate_out), *[_ptr(x) for x in grads],
-                              _ptr(dstate_in), _ptr(workspace), ctypes.c_size_t(workspace.numel()),
-                              _stream(q.device))
-    _check(st, "ll_gdr_bwd")
+    ws = _gdr_workspace(workspace, ll_gdr_bwd_workspace_size(shape), q.device)
+    _launch("ll_gdr_bwd", q.device, ctypes.byref(shape), _addr(seq_starts), _addr(q), _addr(k), _addr(v),
+            _addr(log_alpha), _addr(beta), _addr(state_in), _addr(dout), _addr(dstate_out),
+            *[_addr(x) for x in grads], _addr(dstate_in), _addr(ws), 0 if ws is None else ws.numel())
     return tuple(grads)
 
 
@@ -567,22 +583,22 @@ def ll_gdr_decode_step(q, k, v, log_alpha, beta, states, *, scale=1.0, slots=Non
     B, Hk, dk = q.shape
     H, dv = v.shape[1], v.shape[2]
     _need(q, "q")
+    dev = q.device
     io = _io(q.dtype)
-    _need_like(k, "k", q.shape, q.dtype, q.device)
-    _need_like(v, "v", (B, H, dv), q.dtype, q.device)
-    _need_like(log_alpha, "log_alpha", (B, H), torch.float32, q.device)
-    _need_like(beta, "beta", (B, H), torch.float32, q.device)
-    _need_like(states, "states", (states.shape[0], H, dv, dk), torch.float32, q.device)
+    _need_like(k, "k", q.shape, q.dtype, dev)
+    _need_like(v, "v", (B, H, dv), q.dtype, dev)
+    _need_like(log_alpha, "log_alpha", (B, H), torch.float32, dev)
+    _need_like(beta, "beta", (B, H), torch.float32, dev)
+    n = states.shape[0]
+    _need_like(states, "states", (n, H, dv, dk), torch.float32, dev)
     if slots is not None:
-        _need_like(slots, "slots", (B,), torch.int64, q.device)
+        _need_like(slots, "slots", (B,), torch.int64, dev)
     if o is None:
         o = torch.empty_like(v)
-    _need_like(o, "o", v.shape, q.dtype, q.device)
-    with torch.cuda.device(q.device):
-        st = lib().ll_gdr_decode_step(B, H, Hk, dk, dv, io, float(scale), _ptr(slots), states.shape[0], _ptr(q),
-                                      _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(states), _ptr(o),
-                                      _stream(q.device))
-    _check(st, "ll_gdr_decode_step")
+    else:
+        _need_like(o, "o", v.shape, q.dtype, dev)
+    _launch("ll_gdr_decode_step", dev, B, H, Hk, dk, dv, io, float(scale), _addr(slots), n, _addr(q), _addr(k),
+            _addr(v), _addr(log_alpha), _addr(beta), _addr(states), _addr(o))
     return o
 
 

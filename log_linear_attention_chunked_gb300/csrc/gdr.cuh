@@ -108,11 +108,13 @@ ll_status gdr_rec_bwd_launch(const GdrArgs& a, float* kept_adjoints, float* kept
 ll_status gdr_grad_launch(const GdrArgs& a, const float* states, const float* errors, const float* adjoints,
                           const float* w);
 
-// the tensor-core forward (gdr_tc.cu): bf16 io, head sizes 64 and 128, from this many tokens on
+// on the tensor cores (gdr_tc.cu): bf16 io, head sizes 64 and 128, from this many tokens on
 constexpr int kGdrTcMinTokens = 192;
 bool gdr_tc_supported(const GdrArgs& a);
 size_t gdr_tc_fwd_workspace(const GdrArgs& a);
+size_t gdr_tc_bwd_workspace(const GdrArgs& a);
 ll_status gdr_tc_fwd_launch(const GdrArgs& a);
+ll_status gdr_tc_bwd_launch(const GdrArgs& a);
 
 ll_status gdr_decode_launch(int B, int H, int Hk, int dk, int dv, ll_dtype io, float scale, const int64_t* slots,
                             int n_slots, const void* q, const void* k, const void* v, const float* log_alpha,

@@ -1,18 +1,22 @@
-// The gated delta rule's forward on the 5th-generation tensor cores: bf16 io,
-// head sizes 64 and 128, 128-token chunks.
+// The gated delta rule on the 5th-generation tensor cores, forward and
+// gradient: bf16 io, head sizes 64 and 128, 128-token chunks.
 //
-// Chunk (g = running log decay inside it, G_ij = exp(g_i - g_j) for j <= i, S0
-// the state before it, X = S0^T):
-//   T = (I + diag(beta) SL(K K^T . G))^-1      U = T diag(beta) V
-//   W = T diag(beta exp(g)) K                  u = U - W X     (the rows written)
-//   O = scale (diag(exp(g)) Q X + (Q K^T . G) u)
+// Chunk (g = running log decay inside it, G_ij = exp(g_i - g_j) for j <= i, A =
+// SL(K K^T . G); X = S^T, the state before the chunk; D = its adjoint, transposed,
+// behind the chunk):
+//   T' = (I + A diag(beta))^-1       T = (I + diag(beta) A)^-1
+// forward, the prediction errors e and written rows u = beta e:
+//   e = T' V - [T' diag(exp(g)) K] X = U - W X
 //   X <- exp(g_C) X + K^T diag(exp(g_C - g)) u
-// Three kernels: the preparation (U, W; parallel over chunks), the scan (u and
-// the states; sequential over a sequence's chunks, parallel over heads and
-// slices of 32 d_v columns) and the output (parallel over chunks).  The states
-// are float32 results: the first two keep float32 accuracy by split operands
-// (gdr_tc.cuh); the output rounds X, u and the masked scores to bf16 once each,
-// as its own result is.
+//   O = scale (diag(exp(g)) Q X + (Q K^T . G) u)
+// backward, w_t = D_t k_t at every token:
+//   w = T^T P^T dO + [T^T diag(exp(g_C - g)) K] D = w0 + Wd D,   P = scale (Q K^T . G)
+//   D <- exp(g_C) D + Bc - K^T diag(beta exp(g)) w,   Bc = scale Q^T diag(exp(g)) dO
+// so both directions are one kind of scan: a row matrix from a product with the
+// state, the state from a product with the rows.  Kernels: the preparation (W, U;
+// Wd, w0, Bc; parallel over chunks), the scans (sequential over a sequence's
+// chunks, parallel over heads and slices of 32 d_v columns), and the outputs or
+// gradients (parallel over chunks; formulas of the latter in gdr_grad.cu).
 #include <algorithm>
 
 #include "gdr_tc.cuh"
@@ -23,47 +27,64 @@ namespace {
 
 using namespace gdrtc;
 
-// per (chunk, head): decay tables
+// per (chunk, head)
 struct Tables {
   float2 g[kC];    // running log decay
   float into[kC];  // exp(g_t)
   float out[kC];   // exp(g_C - g_t)
+  float rel[kC];   // exp(g_t - g_0): what D takes from a chunk all carries exp(g_0), which may be tiny
+  float ik, iq, id, pad;  // inverse scales of the fp16 tiles of K, Q and dO
 };
 
 struct TcParams {
   GdrSeqs seqs;
   int dk, dv, slots;
   float scale;
-  const __nv_bfloat16 *q, *k, *v;
-  const float *log_alpha, *beta, *state_in;
-  __nv_bfloat16* o;
-  float* state_out;
-  // workspace, per (slot, head) unless said otherwise
-  unsigned char* W;      // two fp16 tiles
-  float* U;              // [slice of 32][piece of 4][token][4]
-  unsigned char* K16;    // per (slot, key head): K in fp16
-  unsigned char* S;      // X before the chunk, bf16 tile [d_k][d_v]
-  unsigned char* E;      // u, bf16 tile [token][d_v]
+  const __nv_bfloat16 *q, *k, *v, *dout;
+  const float *log_alpha, *beta, *state_in, *dstate_out;
+  __nv_bfloat16 *o, *dq, *dkey, *dval;
+  float *state_out, *dstate_in, *dlog_alpha, *dbeta;
+  // workspace, per (slot, head) unless said otherwise; tiles are fp16
+  unsigned char* W;      // two tiles, [token][d_k]
+  float* U;              // [slice of 32][piece of 4][token][4]; the scan for the gradient leaves e there
+  unsigned char* K16;    // per (slot, key head)
+  unsigned char* S;      // X before the chunk, scaled: [d_k][d_v] (for the gradient a high and a low tile)
+  unsigned char* E;      // u, scaled: [token][d_v] (likewise)
   Tables* tab;
-  unsigned* amax;        // [sequence, head]: largest |v|, as bits
+  unsigned *amax_s, *amax_d;  // [sequence, head]: bits of the largest value that scales X and e, D and w
+  // the gradient's
+  unsigned char *Q16, *dO16;  // Q16 per (slot, key head)
+  unsigned char* Wd;
+  float *w0, *Bc;        // as U, Bc's rows being d_k
+  unsigned char* D;      // D behind the chunk, scaled: [d_k][d_v]
+  unsigned char* Y;      // beta w, scaled: [token][d_v]
+  float* final_state;    // [sequence, head, dv, dk]
+  float2* part;          // [8][token]: e.w and v.(beta w) over 16 columns
+  float* bnd;            // [32]: pieces of <S, D> behind the chunk
   unsigned* err;
 };
 
 // ---------------------------------------------------------------- preparation
-constexpr uint32_t kPK = 0;                     // K
-constexpr uint32_t kPV = kPK + kTile;           // V
-constexpr uint32_t kPT = kPV + kTile;           // T's blocks, float32
-constexpr uint32_t kPR = kPT + kBlocksB;        // L's blocks; then three parts of T diag(..); then W
-constexpr uint32_t kPTab = kPR + 3 * kTile;
-constexpr uint32_t kPBars = kPTab + (2 + 1 + 1) * kC * 4 + 32;
-constexpr uint32_t kPrepSmem = kPBars + 24;
-static_assert(kPR % 1024 == 0 && kPBars % 8 == 0, "tile alignment");
-static_assert(kPrepSmem <= 232448, "shared memory budget of one CTA");
+template <bool BWD> struct PrepSm {
+  static constexpr uint32_t kX0 = 0;                               // K; then T (high)
+  static constexpr uint32_t kX1 = kTile;                           // V (forward), Q; then T (low)
+  static constexpr uint32_t kX2 = 2 * kTile;                       // backward: V, dO
+  static constexpr uint32_t kM = (BWD ? 3 : 2) * kTile;            // M's blocks, float32
+  static constexpr uint32_t kR = kM + kBlocksB;                    // A's blocks; then operands in two parts
+  static constexpr uint32_t kTab = kR + 2 * kTile;
+  static constexpr uint32_t kBars = kTab + 5 * kC * 4 + 32 + 3 * 32;
+  static constexpr uint32_t kBytes = kBars + 24;
+};
+static_assert(PrepSm<true>::kR % 1024 == 0 && PrepSm<true>::kBars % 8 == 0, "tile alignment");
+static_assert(PrepSm<true>::kBytes <= 232448, "shared memory budget of one CTA");
 
-// Persistent, one CTA per SM.  T in float32 on the CUDA cores; T diag(beta) and
-// T diag(beta exp(g)) as three bf16 parts, so that U and W (three products
-// each: V and K are bf16 already) have float32 accuracy.
+constexpr float kScoreDown = 1.f / 256.f;  // of the scores Q K^T of scaled tiles, as operands
+constexpr float kRowsDown = 1.f / 16.f;    // of P^T dO, as an operand
+
+// Persistent, one CTA per SM, an item per (chunk, head).
+template <bool BWD>
 __global__ void __launch_bounds__(256, 1) gdr_prep_kernel(TcParams p) {
+  using Sm = PrepSm<BWD>;
   extern __shared__ __align__(1024) unsigned char s[];
   if (smem_u32(s) & 1023u) {
     if (threadIdx.x == 0) atomicOr(p.err, kErrDeviceArg);
@@ -72,15 +93,18 @@ __global__ void __launch_bounds__(256, 1) gdr_prep_kernel(TcParams p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int q = warp & 3, hf = warp >> 2;
   const int i = 32 * q + lane;  // this thread's row (TMEM lane), columns 64 hf ..
-  float2* gs = reinterpret_cast<float2*>(s + kPTab);
+  float2* gs = reinterpret_cast<float2*>(s + Sm::kTab);
   float* bs = reinterpret_cast<float*>(gs + kC);
-  float* es = bs + kC;
-  double* tot = reinterpret_cast<double*>(es + kC);
-  uint64_t* bar = reinterpret_cast<uint64_t*>(s + kPBars);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s + kPBars + 8);
-  float* Lp = reinterpret_cast<float*>(s + kPR);
-  float* Tp = reinterpret_cast<float*>(s + kPT);
-  const uint32_t sK = smem_u32(s + kPK), sV = smem_u32(s + kPV), sR = smem_u32(s + kPR);
+  float* in_s = bs + kC;
+  float* out_s = in_s + kC;
+  double* tot = reinterpret_cast<double*>(out_s + kC);
+  uint32_t* red = reinterpret_cast<uint32_t*>(tot + 4);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(s + Sm::kBars);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s + Sm::kBars + 8);
+  float* Ap = reinterpret_cast<float*>(s + Sm::kR);
+  float* Mp = reinterpret_cast<float*>(s + Sm::kM);
+  unsigned char *X0 = s + Sm::kX0, *X1 = s + Sm::kX1, *XV = s + (BWD ? Sm::kX2 : Sm::kX1), *R = s + Sm::kR;
+  const uint32_t sX0 = smem_u32(X0), sX1 = smem_u32(X1), sXV = smem_u32(XV), sR = smem_u32(R);
   if (tid == 0) {
     mbar_init(bar, 1);
     fence_mbar_init();
@@ -94,13 +118,94 @@ __global__ void __launch_bounds__(256, 1) gdr_prep_kernel(TcParams p) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
+  const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + 64 * hf;
   uint32_t nmma = 0;
   auto wait_mma = [&]() {
     wait_bar(bar, nmma & 1, p.err);
     ++nmma;
     __syncwarp();
     tc_fence_after();
+  };
+  // operands in shared memory are ready: thread 0 issues the products
+  auto issue = [&](auto products) {
+    fence_proxy_async_shared();
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0) {
+      tc_fence_after();
+      products();
+      umma_commit(bar);
+    }
+  };
+  // rows (diag(fr) (I + diag(br) M diag(bc)) diag(fc)), this thread's 64 columns, in two parts
+  auto put_inverse = [&](unsigned char* hi, unsigned char* lo, float fr, float br, const float* bc, const float* fc) {
+    const int I = i >> 4;
+#pragma unroll
+    for (int jb = 0; jb < 4; ++jb) {
+      const int J = 4 * hf + jb;
+      float t[16];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        float4 x4 = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (J <= I) x4 = *reinterpret_cast<const float4*>(Mp + blk(I, J) + (i & 15) * kBS + 4 * v);
+        t[4 * v] = x4.x;
+        t[4 * v + 1] = x4.y;
+        t[4 * v + 2] = x4.z;
+        t[4 * v + 3] = x4.w;
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int j = 16 * J + e;
+        float x = br * t[e];
+        if (bc) x *= bc[j];
+        if (j == i) x = 1.f;
+        if (fc) x *= fc[j];
+        t[e] = fr * x;
+      }
+      put_parts(hi, lo, swz16(i, 2 * J), t, 1.f);
+      put_parts(hi, lo, swz16(i, 2 * J + 1), t + 8, 1.f);
+    }
+  };
+  // this thread's row of an accumulator, times f, as [slice][piece][row][4] floats; returns the largest value's bits
+  auto write_rows = [&](float* dst, int col, float f) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float x[32];
+      tmem_ld32(tl + col + 32 * c, x);
+      tmem_ld_wait();
+      float4* d = reinterpret_cast<float4*>(dst) + (size_t)(2 * hf + c) * 8 * kC + i;
+#pragma unroll
+      for (int v = 0; v < 8; ++v) {
+        const float4 y = make_float4(f * x[4 * v], f * x[4 * v + 1], f * x[4 * v + 2], f * x[4 * v + 3]);
+        m = max(max(m, max(__float_as_uint(fabsf(y.x)), __float_as_uint(fabsf(y.y)))),
+                max(__float_as_uint(fabsf(y.z)), __float_as_uint(fabsf(y.w))));
+        d[v * kC] = y;
+      }
+    }
+    return m;
+  };
+  // likewise as the two tiles of a scan's operand
+  auto write_tiles = [&](unsigned char* dst, int col, float f) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float x[32];
+      tmem_ld32(tl + col + 32 * c, x);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 32; ++j) x[j] *= f;
+#pragma unroll
+      for (int c8 = 0; c8 < 4; ++c8) put_parts(dst, dst + kTile, swz16(i, 8 * hf + 4 * c + c8), x + 8 * c8, kLoScale);
+    }
+  };
+  auto raise_max = [&](unsigned* at, uint32_t m) {
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (lane == 0) atomicMax(at, m);
+  };
+  auto state_max = [&](const float* x) {
+    uint32_t m = 0;
+    for (int e = tid; e < p.dv * p.dk; e += 256) m = max(m, __float_as_uint(fabsf(x[e])));
+    return m;
   };
 
   const int items = p.slots * p.seqs.H, G = p.seqs.H / p.seqs.Hk;
@@ -112,167 +217,181 @@ __global__ void __launch_bounds__(256, 1) gdr_prep_kernel(TcParams p) {
     const int t0 = chunk * kC, n = min(kC, sq.len - t0);
     const size_t row0 = ((size_t)sq.row_b * p.seqs.H + h) * p.seqs.T + sq.start + t0;
     const size_t krow0 = ((size_t)sq.row_b * p.seqs.Hk + hk) * p.seqs.T + sq.start + t0;
+    const size_t sh = (size_t)seq * p.seqs.H + h;
+    unsigned* am_s = p.amax_s + sh;
+    Tables& tb = p.tab[it];
     if (tid == 0) bulk_wait_read0();  // the item before has left shared memory
     __syncthreads();
-    load_tile(s + kPK, p.k + krow0 * p.dk, n, p.dk, tid, 256);
+    load_tile(X0, p.k + krow0 * p.dk, n, p.dk, tid, 256);
+    if (BWD) load_tile(X1, p.q + krow0 * p.dk, n, p.dk, tid, 256);
     cp_async_commit();
-    load_tile(s + kPV, p.v + row0 * p.dv, n, p.dv, tid, 256);
+    load_tile(XV, p.v + row0 * p.dv, n, p.dv, tid, 256);
     cp_async_commit();
     if (tid < kC) bs[tid] = tid < n ? p.beta[row0 + tid] : 0.f;
     chunk_decays(p.log_alpha + row0, n, gs, tot, tid);
-    const float2 gi = gs[i], gC = gs[kC - 1];
-    const float2 zero = make_float2(0.f, 0.f);
+    const float2 gi = gs[i];
     if (hf == 0) {
-      const float in = exp_diff(gi, zero);
-      es[i] = in;
-      Tables& tb = p.tab[it];
+      const float in = exp_diff(gi, make_float2(0.f, 0.f)), out = exp_diff(gs[kC - 1], gi);
+      in_s[i] = in;
+      out_s[i] = out;
       tb.g[i] = gi;
       tb.into[i] = in;
-      tb.out[i] = exp_diff(gC, gi);
+      tb.out[i] = out;
+      if (BWD) tb.rel[i] = exp_diff(gi, gs[0]);
     }
+    if (p.state_in && chunk == 0) raise_max(am_s, state_max(p.state_in + sh * p.dv * p.dk));
     cp_async_wait<1>();
-    fence_proxy_async_shared();
     __syncthreads();
-    // ---- K K^T -> 0
+    const float ik = tile_to_f16(X0, red, tid);
+    float iq = 1.f;
+    if (BWD) iq = tile_to_f16(X1, red + 8, tid);
+    // ---- K K^T -> 0, Q K^T -> 128
+    issue([&]() {
+      mma_tile(tmem, sX0, false, sX0, false, false);
+      if (BWD) mma_tile(tmem + 128, sX1, false, sX0, false, false);
+      if (h % G == 0) {
+        bulk_store(p.K16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, X0, kTile);
+        if (BWD) bulk_store(p.Q16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, X1, kTile);
+        bulk_commit();
+      }
+    });
+    cp_async_wait<0>();
+    __syncthreads();
+    uint32_t vbits;
+    const float iv = tile_to_f16(XV, red + 16, tid, &vbits);
     if (tid == 0) {
-      tc_fence_after();
-      mma_tile(tmem, sK, false, sK, false, false);
-      umma_commit(bar);
+      atomicMax(am_s, vbits);
+      tb.ik = ik;
+      tb.iq = iq;
     }
     wait_mma();
-    // L_ij = beta_i (k_i . k_j) G_ij, j < i
-    {
-      const float bt = bs[i];
+    // A_ij = (k_i . k_j) G_ij, j < i
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int j0 = 64 * hf + 32 * c;
-        if (j0 > 32 * q + 31) continue;  // (warp-uniform) above the diagonal
-        float kk[32];
-        tmem_ld32(tl + j0, kk);
-        tmem_ld_wait();
+    for (int c = 0; c < 2; ++c) {
+      const int j0 = 64 * hf + 32 * c;
+      if (j0 > 32 * q + 31) continue;  // (warp-uniform) above the diagonal
+      float kk[32];
+      tmem_ld32(tl + 32 * c, kk);
+      tmem_ld_wait();
+      const float f = ik * ik;
 #pragma unroll
-        for (int jj = 0; jj < 32; ++jj) kk[jj] = j0 + jj < i ? bt * kk[jj] * exp_diff(gi, gs[j0 + jj]) : 0.f;
+      for (int jj = 0; jj < 32; ++jj) kk[jj] = j0 + jj < i ? f * kk[jj] * exp_diff(gi, gs[j0 + jj]) : 0.f;
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const int J = (j0 >> 4) + b, I = i >> 4;
-          if (J <= I) {
-            float4* dst = reinterpret_cast<float4*>(Lp + blk(I, J) + (i & 15) * kBS);
+      for (int b = 0; b < 2; ++b) {
+        const int J = (j0 >> 4) + b, I = i >> 4;
+        if (J <= I) {
+          float4* dst = reinterpret_cast<float4*>(Ap + blk(I, J) + (i & 15) * kBS);
 #pragma unroll
-            for (int v = 0; v < 4; ++v)
-              dst[v] = make_float4(kk[16 * b + 4 * v], kk[16 * b + 4 * v + 1], kk[16 * b + 4 * v + 2],
-                                   kk[16 * b + 4 * v + 3]);
-          }
+          for (int v = 0; v < 4; ++v)
+            dst[v] = make_float4(kk[16 * b + 4 * v], kk[16 * b + 4 * v + 1], kk[16 * b + 4 * v + 2],
+                                 kk[16 * b + 4 * v + 3]);
         }
       }
     }
-    cp_async_wait<0>();  // V, for the barriers below
     __syncthreads();
-    tri_inverse(Lp, Tp, tid);
-    // the largest |v| of the sequence and head
-    {
-      uint32_t m = 0;
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const uint4 v = *reinterpret_cast<const uint4*>(s + kPV + swz16(tid >> 1, 8 * (tid & 1) + c));
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m = max(m, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-      }
-      m = __reduce_max_sync(0xffffffffu, m);
-      if (lane == 0) atomicMax(p.amax + (size_t)seq * p.seqs.H + h, m << 16);
+    tri_solve(Ap, Mp, bs, tid);
+    // ---- U = T' V -> 256
+    put_inverse(R, R + kTile, 1.f, 1.f, bs, nullptr);
+    issue([&]() {
+      mma_tile(tmem + 256, sR + kTile, false, sXV, true, false);
+      mma_tile(tmem + 256, sR, false, sXV, true, true);
+    });
+    wait_mma();
+    // ---- W = T' diag(exp(g)) K -> 384
+    put_inverse(R, R + kTile, 1.f, 1.f, bs, in_s);
+    issue([&]() {
+      mma_tile(tmem + 384, sR + kTile, false, sX0, true, false);
+      mma_tile(tmem + 384, sR, false, sX0, true, true);
+    });
+    if (BWD) {  // (V has been read)
+      load_tile(XV, p.dout + row0 * p.dv, n, p.dv, tid, 256);
+      cp_async_commit();
     }
-    // ---- U = T diag(beta) V -> 128, then W = T diag(beta exp(g)) K -> 256
-    for (int pass = 0; pass < 2; ++pass) {
-#pragma unroll
-      for (int jb = 0; jb < 4; ++jb) {
-        const int I = i >> 4, J = 4 * hf + jb;
-        float t[16];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          float4 x4 = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (J <= I) x4 = *reinterpret_cast<const float4*>(Tp + blk(I, J) + (i & 15) * kBS + 4 * v);
-          t[4 * v] = x4.x;
-          t[4 * v + 1] = x4.y;
-          t[4 * v + 2] = x4.z;
-          t[4 * v + 3] = x4.w;
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int j = 16 * J + e;
-          t[e] *= pass == 0 ? bs[j] : bs[j] * es[j];
-        }
-#pragma unroll
-        for (int part = 0; part < 3; ++part) {
-          uint32_t w[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = take_bf16x2(t[2 * e], t[2 * e + 1]);
-          unsigned char* d = s + kPR + part * kTile;
-          *reinterpret_cast<uint4*>(d + swz16(i, 2 * J)) = make_uint4(w[0], w[1], w[2], w[3]);
-          *reinterpret_cast<uint4*>(d + swz16(i, 2 * J + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
-        }
-      }
-      fence_proxy_async_shared();
-      tc_fence_before();
+    write_rows(p.U + (size_t)it * kC * kC, 256, iv);
+    wait_mma();
+    if (!BWD) {
+      write_tiles(p.W + (size_t)it * 2 * kTile, 384, ik);
+    } else {
+      const float bi = bs[i];
+      cp_async_wait<0>();
       __syncthreads();
-      if (tid == 0) {
-        tc_fence_after();
-        const uint32_t d = tmem + 128 + 128 * pass, b = pass == 0 ? sV : sK;
-        mma_tile(d, sR + 2 * kTile, false, b, true, false);
-        mma_tile(d, sR + kTile, false, b, true, true);
-        mma_tile(d, sR, false, b, true, true);
-        umma_commit(bar);
-      }
+      const float id = tile_to_f16(XV, red, tid);
+      if (tid == 0) tb.id = id;
+      // ---- Wd = T^T diag(exp(g_C - g)) K -> 256
+      put_inverse(R, R + kTile, out_s[i], bi, nullptr, nullptr);
+      issue([&]() {
+        mma_tile(tmem + 256, sR + kTile, true, sX0, true, false);
+        mma_tile(tmem + 256, sR, true, sX0, true, true);
+        bulk_store(p.dO16 + (size_t)it * kTile, XV, kTile);
+        bulk_commit();
+      });
+      write_tiles(p.W + (size_t)it * 2 * kTile, 384, ik);
       wait_mma();
-    }
-    // ---- U out, W as two fp16 tiles (over T's parts), K as fp16 in place
-    {
-      float* ug = p.U + (size_t)it * kC * kC;
+      // ---- Bc = Q^T diag(exp(g)) dO -> 384, exp(g_0) and its scales below
+      const float rel = exp_diff(gi, gs[0]);
+#pragma unroll
+      for (int c8 = 0; c8 < 8; ++c8) {
+        const uint32_t at = swz16(i, 8 * hf + c8);
+        const uint4 v = *reinterpret_cast<const uint4*>(XV + at);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = unpack_f16x2(w[e]);
+          x[2 * e] = rel * f.x;
+          x[2 * e + 1] = rel * f.y;
+        }
+        put_parts(R, R + kTile, at, x, 1.f);
+      }
+      issue([&]() {
+        mma_tile(tmem + 384, sX1, true, sR + kTile, true, false);
+        mma_tile(tmem + 384, sX1, true, sR, true, true);
+      });
+      write_tiles(p.Wd + (size_t)it * 2 * kTile, 256, ik);
+      wait_mma();
+      // ---- P^T dO -> 0
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int j0 = 64 * hf + 32 * c;
-        float u[32], w[32];
-        tmem_ld32(tl + 128 + j0, u);
-        tmem_ld32(tl + 256 + j0, w);
+        float x[32];
+        tmem_ld32(tl + 128 + 32 * c, x);
         tmem_ld_wait();
-        float4* ud = reinterpret_cast<float4*>(ug) + (size_t)(j0 >> 5) * 8 * kC + i;
 #pragma unroll
-        for (int v = 0; v < 8; ++v) ud[v * kC] = make_float4(u[4 * v], u[4 * v + 1], u[4 * v + 2], u[4 * v + 3]);
+        for (int jj = 0; jj < 32; ++jj) x[jj] = j0 + jj <= i ? kScoreDown * x[jj] * exp_diff(gi, gs[j0 + jj]) : 0.f;
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int c8 = 0; c8 < 4; ++c8) {
-            uint32_t x[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              x[e] = part == 0 ? take_f16x2(w[8 * c8 + 2 * e], w[8 * c8 + 2 * e + 1])
-                               : pack_f16x2(w[8 * c8 + 2 * e], w[8 * c8 + 2 * e + 1]);
-            *reinterpret_cast<uint4*>(s + kPR + part * kTile + swz16(i, (j0 >> 3) + c8)) =
-                make_uint4(x[0], x[1], x[2], x[3]);
-          }
+        for (int c8 = 0; c8 < 4; ++c8) put_parts(R, R + kTile, swz16(i, (j0 >> 3) + c8), x + 8 * c8, 1.f);
       }
-      if (h % G == 0) {
+      issue([&]() {
+        mma_tile(tmem, sR + kTile, true, sXV, true, false);
+        mma_tile(tmem, sR, true, sXV, true, true);
+        bulk_wait_read0();  // K16 and Q16 have left (their place is taken next)
+      });
+      uint32_t m = write_rows(p.Bc + (size_t)it * kC * kC, 384, p.scale * iq * id * in_s[0]);
+      if (p.dstate_out && t0 + n == sq.len) m = max(m, state_max(p.dstate_out + sh * p.dv * p.dk));
+      wait_mma();
+      __syncthreads();
+      // ---- w0 = T^T (P^T dO) -> 128
 #pragma unroll
-        for (int c8 = 0; c8 < 8; ++c8) {
-          uint4* at = reinterpret_cast<uint4*>(s + kPK + swz16(i, 8 * hf + c8));
-          uint4 v = *at;
-          uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+      for (int c = 0; c < 2; ++c) {
+        float x[32];
+        tmem_ld32(tl + 32 * c, x);
+        tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = unpack_bf16x2(w[e]);
-            w[e] = pack_f16x2(f.x, f.y);
-          }
-          *at = v;
-        }
+        for (int jj = 0; jj < 32; ++jj) x[jj] *= kRowsDown;
+#pragma unroll
+        for (int c8 = 0; c8 < 4; ++c8) put_parts(R, R + kTile, swz16(i, 8 * hf + 4 * c + c8), x + 8 * c8, 1.f);
       }
+      put_inverse(X0, X1, 1.f, bi, nullptr, nullptr);
+      issue([&]() {
+        mma_tile(tmem + 128, sX1, true, sR, true, false);
+        mma_tile(tmem + 128, sX0, true, sR + kTile, true, true);
+        mma_tile(tmem + 128, sX0, true, sR, true, true);
+      });
+      wait_mma();
+      m = max(m, write_rows(p.w0 + (size_t)it * kC * kC, 128, p.scale * iq * ik * id / (kScoreDown * kRowsDown)));
+      raise_max(p.amax_d + sh, m);
     }
-    fence_proxy_async_shared();
-    tc_fence_before();
-    __syncthreads();
-    if (tid == 0) {
-      bulk_store(p.W + (size_t)it * 2 * kTile, s + kPR, 2 * kTile);
-      if (h % G == 0) bulk_store(p.K16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, s + kPK, kTile);
-      bulk_commit();
-    }
+    tc_fence_before();  // (for the next item's products, behind its barriers)
   }
   if (tid == 0) bulk_wait0();
   tc_fence_before();
@@ -284,22 +403,24 @@ __global__ void __launch_bounds__(256, 1) gdr_prep_kernel(TcParams p) {
 }
 
 // ---------------------------------------------------------------- scan
-constexpr uint32_t kSW = 0;                  // W of two chunks (two fp16 parts each)
-constexpr uint32_t kSK = kSW + 4 * kTile;    // K of two chunks (fp16)
-constexpr uint32_t kSX = kSK + 2 * kTile;    // X: [d_k][high 32 | low 32] fp16
-constexpr uint32_t kSE = kSX + kHalf;        // exp(g_C - g) u: [token][high 32 | low 32]
+constexpr uint32_t kSW = 0;                  // W (Wd) of two chunks, two parts each
+constexpr uint32_t kSK = kSW + 4 * kTile;    // K of two chunks
+constexpr uint32_t kSX = kSK + 2 * kTile;    // X (D): [d_k][high 32 | low 32]
+constexpr uint32_t kSE = kSX + kHalf;        // the rows: [token][high 32 | low 32]
 constexpr uint32_t kSBars = kSE + kHalf;
-constexpr uint32_t kSRed = kSBars + 8 * 8;
-constexpr uint32_t kScanSmem = kSRed + 64;
+constexpr uint32_t kScanSmem = kSBars + 8 * 8;
 static_assert(kScanSmem <= 232448, "shared memory budget of one CTA");
 enum ScanBar : int { SB_W0 = 0, SB_W1, SB_K0, SB_K1, SB_MMA, kScanBars };
+enum ScanMode : int { kFwd, kFwdKeep, kRev };  // the forward; the forward for the gradient; backwards
 
 // One CTA per (32 d_v columns, head, sequence); thread = (TMEM lane, half of the
 // columns), the lane a token of the chunk or a d_k row of X in turn.  X stays
 // in float32 registers; per chunk two rounds of products, W [Xh | Xl] and
 // K^T [uh | ul] (the parts side by side as N = 64: the 128-row operand, which
 // shared memory feeds at 128 bytes a cycle, is read once for both).
+template <int MODE>
 __global__ void __launch_bounds__(256, 1) gdr_scan_kernel(TcParams p, int slices) {
+  constexpr bool REV = MODE == kRev;
   extern __shared__ __align__(1024) unsigned char s[];
   if (smem_u32(s) & 1023u) {
     if (threadIdx.x == 0) atomicOr(p.err, kErrDeviceArg);
@@ -315,40 +436,40 @@ __global__ void __launch_bounds__(256, 1) gdr_scan_kernel(TcParams p, int slices
   }
   const int hk = h / (p.seqs.H / p.seqs.Hk);
   const int col0 = kSlice * sl + 16 * hf;  // this thread's first d_v column
+  const bool cols_in = col0 < p.dv;
   const int Nc = (sq.len + kC - 1) / kC;
   const int base = gdr_slot_base(p.seqs, seq, sq.start, kC);
-  const size_t st0 = ((size_t)seq * p.seqs.H + h) * p.dv;
+  const size_t row0 = ((size_t)sq.row_b * p.seqs.H + h) * p.seqs.T + sq.start;
+  const size_t sh = (size_t)seq * p.seqs.H + h;
+  auto item = [&](int c) { return (size_t)(base + c) * p.seqs.H + h; };
+  auto at_step = [&](int x) { return REV ? Nc - 1 - x : x; };  // the chunk of step x
+
+  const float* from = REV ? p.dstate_out : p.state_in;
   float X[16];
 #pragma unroll
-  for (int j = 0; j < 16; ++j)
-    X[j] = p.state_in && i < p.dk && col0 + j < p.dv ? p.state_in[(st0 + col0 + j) * p.dk + i] : 0.f;
+  for (int j = 0; j < 16; ++j) X[j] = from && i < p.dk && cols_in ? from[(sh * p.dv + col0 + j) * p.dk + i] : 0.f;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(s + kSBars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s + kSBars + kScanBars * 8);
-  uint32_t* red = reinterpret_cast<uint32_t*>(s + kSRed);
-  auto item = [&](int c) { return (size_t)(base + c) * p.seqs.H + h; };
-  auto load_w = [&](int c) {
-    mbar_arrive_expect_tx(bars + SB_W0 + (c & 1), 2 * kTile);
-    bulk_load(s + kSW + (c & 1) * 2 * kTile, p.W + item(c) * 2 * kTile, 2 * kTile, bars + SB_W0 + (c & 1));
+  auto load_w = [&](int x) {
+    const unsigned char* src = (REV ? p.Wd : p.W) + item(at_step(x)) * 2 * kTile;
+    mbar_arrive_expect_tx(bars + SB_W0 + (x & 1), 2 * kTile);
+    bulk_load(s + kSW + (x & 1) * 2 * kTile, src, 2 * kTile, bars + SB_W0 + (x & 1));
   };
-  auto load_k = [&](int c) {
-    mbar_arrive_expect_tx(bars + SB_K0 + (c & 1), kTile);
-    bulk_load(s + kSK + (c & 1) * kTile, p.K16 + ((size_t)(base + c) * p.seqs.Hk + hk) * kTile, kTile,
-              bars + SB_K0 + (c & 1));
+  auto load_k = [&](int x) {
+    mbar_arrive_expect_tx(bars + SB_K0 + (x & 1), kTile);
+    bulk_load(s + kSK + (x & 1) * kTile, p.K16 + ((size_t)(base + at_step(x)) * p.seqs.Hk + hk) * kTile, kTile,
+              bars + SB_K0 + (x & 1));
   };
   if (tid == 0) {
     for (int b = 0; b < kScanBars; ++b) mbar_init(bars + b, 1);
     fence_mbar_init();
-    for (int c = 0; c < 2 && c < Nc; ++c) {
-      load_w(c);
-      load_k(c);
+    for (int x = 0; x < 2 && x < Nc; ++x) {
+      load_w(x);
+      load_k(x);
     }
   }
-  uint32_t am = 0;
-#pragma unroll
-  for (int j = 0; j < 16; ++j) am = max(am, __float_as_uint(fabsf(X[j])));
-  am = __reduce_max_sync(0xffffffffu, am);
-  if (lane == 0) red[warp] = am;
+  __syncwarp();
   if (warp == 0) {
     tmem_alloc(tmem_slot, 256);
     tmem_relinquish();
@@ -356,17 +477,25 @@ __global__ void __launch_bounds__(256, 1) gdr_scan_kernel(TcParams p, int slices
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  am = Nc ? p.amax[(size_t)seq * p.seqs.H + h] : 0u;
+  const float2 sg =
+      Nc ? operand_scale(__uint_as_float((REV ? p.amax_d : p.amax_s)[sh])) : make_float2(1.f, 1.f);
+  const float isf = REV && Nc ? operand_scale(__uint_as_float(p.amax_s[sh])).y : 1.f;
+  if (REV && Nc) {  // <S_T, its gradient>: what the last chunk's log decays add
+    float d = 0.f;
+    if (p.dstate_out && i < p.dk && cols_in)
 #pragma unroll
-  for (int w = 0; w < 8; ++w) am = max(am, red[w]);
-  const float2 sg = operand_scale(__uint_as_float(am));
+      for (int j = 0; j < 16; ++j) d = fmaf(X[j], p.final_state[(sh * p.dv + col0 + j) * p.dk + i], d);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    if (lane == 0) p.bnd[item(Nc - 1) * 32 + sl * 8 + warp] = d;
+  }
 #pragma unroll
   for (int j = 0; j < 16; ++j) X[j] *= sg.x;
 
   const uint32_t tmem = *tmem_slot;
   const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + 16 * hf;
   const uint32_t sX = smem_u32(s + kSX), sE = smem_u32(s + kSE);
-  constexpr uint32_t idW = idesc(false, 64, false, true), idK = idesc(false, 64, true, true);
+  constexpr uint32_t idW = idesc_f16(64, false, true), idK = idesc_f16(64, true, true);
   uint32_t nmma = 0;
   auto wait_mma = [&]() {
     wait_bar(bars + SB_MMA, nmma & 1, p.err);
@@ -374,56 +503,89 @@ __global__ void __launch_bounds__(256, 1) gdr_scan_kernel(TcParams p, int slices
     __syncwarp();
     tc_fence_after();
   };
-  // x (16 columns of row i) as high and low fp16 parts of a [row][32 | 32] tile
-  auto put = [&](unsigned char* tile, float* x) {
-#pragma unroll
-    for (int part = 0; part < 2; ++part)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          w[e] = part == 0 ? take_f16x2(x[8 * c + 2 * e], x[8 * c + 2 * e + 1])
-                           : pack_f16x2(x[8 * c + 2 * e], x[8 * c + 2 * e + 1]);
-        *reinterpret_cast<uint4*>(tile + swz16(i, 4 * part + 2 * hf + c)) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-  };
-  // x times f, rounded to bf16, into row i of a workspace tile
-  auto keep = [&](unsigned char* tile, const float* x, float f) {
+  // 16 columns of row i as high and low parts of a [row][32 | 32] tile
+  auto put = [&](unsigned char* tile, const float* x, float f) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      uint32_t w[4];
+      float y[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(f * x[8 * c + 2 * e], f * x[8 * c + 2 * e + 1]);
-      *reinterpret_cast<uint4*>(tile + swz16(i, (col0 >> 3) + c)) = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int e = 0; e < 8; ++e) y[e] = f * x[8 * c + e];
+      uint32_t w[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        w[e] = take_f16x2(y[2 * e], y[2 * e + 1], kLoScale);
+        w[4 + e] = pack_f16x2(y[2 * e], y[2 * e + 1]);
+      }
+      *reinterpret_cast<uint4*>(tile + swz16(i, 2 * hf + c)) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(tile + swz16(i, 4 + 2 * hf + c)) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  };
+  // 16 columns of row i into a workspace tile: the high part, or both in two tiles
+  auto keep = [&](unsigned char* tile, const float* x, float f, bool both) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const uint32_t at = swz16(i, (col0 >> 3) + c);
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = f * x[8 * c + e];
+      if (both)
+        put_parts(tile, tile + kTile, at, y, 1.f);
+      else
+        *reinterpret_cast<uint4*>(tile + at) = make_uint4(pack_f16x2(y[0], y[1]), pack_f16x2(y[2], y[3]),
+                                                          pack_f16x2(y[4], y[5]), pack_f16x2(y[6], y[7]));
     }
   };
 
-  float4 un[4];
-  float out_n = 0.f, gam_n = 0.f;
-  auto fetch = [&](int c) {
-    const float4* ug = reinterpret_cast<const float4*>(p.U) + item(c) * (kC * kC / 4) + (size_t)(sl * 8 + 4 * hf) * kC + i;
+  // what this thread needs of a chunk, loaded one step ahead
+  float4 un[4], bn[4], en[4];
+  uint4 vn[2], sn[4];
+  float fac_n = 0.f, gam_n = 0.f, beta_n = 0.f, in0_n = 0.f;
+  const size_t piece = (size_t)(sl * 8 + 4 * hf) * kC + i;
+  auto fetch = [&](int x) {
+    const int c = at_step(x);
+    const size_t it = item(c);
+    const int t = c * kC + i;
+    const float4* ug = reinterpret_cast<const float4*>(REV ? p.w0 : p.U) + it * (kC * kC / 4) + piece;
 #pragma unroll
     for (int v = 0; v < 4; ++v) un[v] = ug[v * kC];
-    const Tables& tb = p.tab[item(c)];
-    out_n = tb.out[i];
+    const Tables& tb = p.tab[it];
+    fac_n = (REV ? tb.rel[i] : tb.out[i]) * tb.ik;
+    if (REV) in0_n = tb.into[0];
     gam_n = tb.into[kC - 1];
+    beta_n = t < sq.len ? p.beta[row0 + t] : 0.f;
+    if (REV) {
+      const float4* bg = reinterpret_cast<const float4*>(p.Bc) + it * (kC * kC / 4) + piece;
+      const float4* eg = reinterpret_cast<const float4*>(p.U) + it * (kC * kC / 4) + piece;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        bn[v] = bg[v * kC];
+        en[v] = eg[v * kC];
+      }
+      vn[0] = vn[1] = make_uint4(0u, 0u, 0u, 0u);
+      if (t < sq.len && cols_in) {
+        const uint4* vg = reinterpret_cast<const uint4*>(p.v + (row0 + t) * p.dv + col0);
+        vn[0] = vg[0];
+        vn[1] = vg[1];
+      }
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          sn[2 * part + e] =
+              *reinterpret_cast<const uint4*>(p.S + (it * 2 + part) * kTile + swz16(i, (col0 >> 3) + e));
+    }
   };
   if (Nc) fetch(0);
-  for (int c = 0; c < Nc; ++c) {
-    const int b = c & 1;
-    // ---- W X
-    {
-      float x[16];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) x[j] = X[j];
-      put(s + kSX, x);
-    }
+  for (int x = 0; x < Nc; ++x) {
+    const int b = x & 1, c = at_step(x);
+    const size_t it = item(c);
+    // ---- W X (Wd D)
+    put(s + kSX, X, 1.f);
     fence_proxy_async_shared();
     tc_fence_before();
     __syncthreads();
     if (tid == 0) {
-      wait_bar(bars + SB_W0 + b, (c >> 1) & 1, p.err);
+      wait_bar(bars + SB_W0 + b, (x >> 1) & 1, p.err);
       tc_fence_after();
       const uint32_t w = smem_u32(s + kSW + b * 2 * kTile);
 #pragma unroll
@@ -433,19 +595,37 @@ __global__ void __launch_bounds__(256, 1) gdr_scan_kernel(TcParams p, int slices
           umma_bf16(tmem + 64 * part, desc_k(w + part * kTile, kk), desc_mn(sX, kk), idW, kk > 0);
       umma_commit(bars + SB_MMA);
     }
-    keep(p.S + item(c) * kTile, X, sg.y);  // (while the products run)
-    float u[16];
+    // (while the products run)
+    if (REV) keep(p.D + it * kTile, X, 1.f, false);
+    else keep(p.S + it * (MODE == kFwdKeep ? 2 : 1) * kTile, X, 1.f, MODE == kFwdKeep);
+    float u[16], bc[16], er[16];
+    uint4 vr[2], sr[4];
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       u[4 * v] = sg.x * un[v].x;
       u[4 * v + 1] = sg.x * un[v].y;
       u[4 * v + 2] = sg.x * un[v].z;
       u[4 * v + 3] = sg.x * un[v].w;
+      if (REV) {
+        bc[4 * v] = sg.x * bn[v].x;
+        bc[4 * v + 1] = sg.x * bn[v].y;
+        bc[4 * v + 2] = sg.x * bn[v].z;
+        bc[4 * v + 3] = sg.x * bn[v].w;
+        er[4 * v] = en[v].x;
+        er[4 * v + 1] = en[v].y;
+        er[4 * v + 2] = en[v].z;
+        er[4 * v + 3] = en[v].w;
+        sr[v] = sn[v];
+      }
     }
-    const float fo = out_n, gam = gam_n;
-    if (c + 1 < Nc) fetch(c + 1);
+    if (REV) {
+      vr[0] = vn[0];
+      vr[1] = vn[1];
+    }
+    const float fac = fac_n, gam = gam_n, bt = beta_n, in0 = in0_n;
+    if (x + 1 < Nc) fetch(x + 1);
     wait_mma();
-    if (tid == 0 && c + 2 < Nc) load_w(c + 2);
+    if (tid == 0 && x + 2 < Nc) load_w(x + 2);
     {
       float hh[16], hl[16], lh[16];
       tmem_ld16(tl, hh);
@@ -453,42 +633,87 @@ __global__ void __launch_bounds__(256, 1) gdr_scan_kernel(TcParams p, int slices
       tmem_ld16(tl + 64, lh);
       tmem_ld_wait();
 #pragma unroll
-      for (int j = 0; j < 16; ++j) u[j] -= fmaf(kLoInv, hl[j] + lh[j], hh[j]);
+      for (int j = 0; j < 16; ++j) {
+        const float y = fmaf(kLoInv, hl[j] + lh[j], hh[j]);
+        u[j] = REV ? u[j] + y : u[j] - y;
+      }
     }
-    // ---- K^T (exp(g_C - g) u)
-    {
-      float x[16];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) x[j] = fo * u[j];
-      put(s + kSE, x);
-    }
+    // ---- K^T (beta exp(g_C - g) e), K^T (beta exp(g - g_0) w)
+    put(s + kSE, u, bt * fac);
     fence_proxy_async_shared();
     tc_fence_before();
     __syncthreads();
     if (tid == 0) {
-      wait_bar(bars + SB_K0 + b, (c >> 1) & 1, p.err);
+      wait_bar(bars + SB_K0 + b, (x >> 1) & 1, p.err);
       tc_fence_after();
       const uint32_t k = smem_u32(s + kSK + b * kTile);
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) umma_bf16(tmem + 128, desc_mn(k, kk), desc_mn(sE, kk), idK, kk > 0);
       umma_commit(bars + SB_MMA);
     }
-    keep(p.E + item(c) * kTile, u, sg.y);
+    if (!REV) {
+      keep(p.E + it * (MODE == kFwdKeep ? 2 : 1) * kTile, u, bt, MODE == kFwdKeep);
+      if (MODE == kFwdKeep) {  // e in U's place
+        float4* eg = reinterpret_cast<float4*>(p.U) + it * (kC * kC / 4) + piece;
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          eg[v * kC] = make_float4(sg.y * u[4 * v], sg.y * u[4 * v + 1], sg.y * u[4 * v + 2], sg.y * u[4 * v + 3]);
+      }
+    } else {
+      keep(p.Y + it * kTile, u, bt, false);
+      float ew = 0.f, vw = 0.f;
+      uint32_t dvw[8];
+      const uint32_t vv[8] = {vr[0].x, vr[0].y, vr[0].z, vr[0].w, vr[1].x, vr[1].y, vr[1].z, vr[1].w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float w0 = sg.y * u[2 * j], w1 = sg.y * u[2 * j + 1], d0 = bt * w0, d1 = bt * w1;
+        ew = fmaf(er[2 * j], w0, fmaf(er[2 * j + 1], w1, ew));
+        const float2 f = unpack_bf16x2(vv[j]);
+        vw = fmaf(f.x, d0, fmaf(f.y, d1, vw));
+        dvw[j] = pack_bf16x2(d0, d1);
+      }
+      const int t = c * kC + i;
+      p.part[(it * 8 + sl * 2 + hf) * kC + i] = make_float2(ew, vw);
+      if (t < sq.len && cols_in) {
+        uint4* dg = reinterpret_cast<uint4*>(p.dval + (row0 + t) * p.dv + col0);
+        dg[0] = make_uint4(dvw[0], dvw[1], dvw[2], dvw[3]);
+        dg[1] = make_uint4(dvw[4], dvw[5], dvw[6], dvw[7]);
+      }
+    }
     wait_mma();
-    if (tid == 0 && c + 2 < Nc) load_k(c + 2);
+    if (tid == 0 && x + 2 < Nc) load_k(x + 2);
     {
       float hi[16], lo[16];
       tmem_ld16(tl + 128, hi);
       tmem_ld16(tl + 160, lo);
       tmem_ld_wait();
 #pragma unroll
-      for (int j = 0; j < 16; ++j) X[j] = fmaf(gam, X[j], fmaf(kLoInv, lo[j], hi[j]));
+      for (int j = 0; j < 16; ++j) {
+        const float y = fmaf(kLoInv, lo[j], hi[j]);
+        X[j] = fmaf(gam, X[j], REV ? fmaf(-in0, y, bc[j]) : y);
+      }
+    }
+    if (REV && c > 0) {  // <S, D> between this chunk and the one before it
+      float d = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t hw[4] = {sr[e].x, sr[e].y, sr[e].z, sr[e].w};
+        const uint32_t lw[4] = {sr[2 + e].x, sr[2 + e].y, sr[2 + e].z, sr[2 + e].w};
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float2 a = unpack_f16x2(hw[v]), l = unpack_f16x2(lw[v]);
+          d = fmaf(X[8 * e + 2 * v], a.x + l.x, fmaf(X[8 * e + 2 * v + 1], a.y + l.y, d));
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+      if (lane == 0) p.bnd[item(c - 1) * 32 + sl * 8 + warp] = d * sg.y * isf;
     }
   }
-  if (p.state_out) {
+  float* to = REV ? p.dstate_in : MODE == kFwdKeep ? p.final_state : p.state_out;
+  if (to && i < p.dk && cols_in) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (i < p.dk && col0 + j < p.dv) p.state_out[(st0 + col0 + j) * p.dk + i] = X[j] * sg.y;
+    for (int j = 0; j < 16; ++j) to[(sh * p.dv + col0 + j) * p.dk + i] = X[j] * sg.y;
   }
   tc_fence_before();
   __syncthreads();
@@ -501,13 +726,13 @@ __global__ void __launch_bounds__(256, 1) gdr_scan_kernel(TcParams p, int slices
 // ---------------------------------------------------------------- output
 constexpr uint32_t kOQ = 0;                  // Q
 constexpr uint32_t kOK = kOQ + kTile;        // K; then the masked scores
-constexpr uint32_t kOS = kOK + kTile;        // X
-constexpr uint32_t kOE = kOS + kTile;        // u
-constexpr uint32_t kOTab = kOE + kTile;
-constexpr uint32_t kOBars = kOTab + 2 * kC * 4;
+constexpr uint32_t kOS = kOK + kTile;        // X; then u
+constexpr uint32_t kOTab = kOS + kTile;
+constexpr uint32_t kOBars = kOTab + 2 * kC * 4 + 32;
 constexpr uint32_t kOutSmem = kOBars + 24;
 
-__global__ void __launch_bounds__(256, 1) gdr_out_kernel(TcParams p) {
+// One CTA per (chunk, head), two per SM.
+__global__ void __launch_bounds__(256, 2) gdr_out_kernel(TcParams p) {
   extern __shared__ __align__(1024) unsigned char s[];
   if (smem_u32(s) & 1023u) {
     if (threadIdx.x == 0) atomicOr(p.err, kErrDeviceArg);
@@ -524,78 +749,88 @@ __global__ void __launch_bounds__(256, 1) gdr_out_kernel(TcParams p) {
   const size_t row0 = ((size_t)sq.row_b * p.seqs.H + h) * p.seqs.T + sq.start + t0;
   const size_t krow0 = ((size_t)sq.row_b * p.seqs.Hk + hk) * p.seqs.T + sq.start + t0;
   float2* gs = reinterpret_cast<float2*>(s + kOTab);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s + kOBars);  // 0: X and u, 1: products
+  uint32_t* red = reinterpret_cast<uint32_t*>(gs + kC);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s + kOBars);  // 0: K and X, then u; 1: products
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s + kOBars + 16);
-  const uint32_t sQ = smem_u32(s + kOQ), sK = smem_u32(s + kOK), sS = smem_u32(s + kOS), sE = smem_u32(s + kOE);
+  const uint32_t sQ = smem_u32(s + kOQ), sK = smem_u32(s + kOK), sS = smem_u32(s + kOS);
   if (tid == 0) {
     mbar_init(bars, 1);
     mbar_init(bars + 1, 1);
     fence_mbar_init();
     mbar_arrive_expect_tx(bars, 2 * kTile);
+    bulk_load(s + kOK, p.K16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, kTile, bars);
     bulk_load(s + kOS, p.S + (size_t)it * kTile, kTile, bars);
-    bulk_load(s + kOE, p.E + (size_t)it * kTile, kTile, bars);
   }
   load_tile(s + kOQ, p.q + krow0 * p.dk, n, p.dk, tid, 256);
-  load_tile(s + kOK, p.k + krow0 * p.dk, n, p.dk, tid, 256);
   cp_async_commit();
   __syncwarp();
   if (warp == 0) {
-    tmem_alloc(tmem_slot, 512);
+    tmem_alloc(tmem_slot, 256);
     tmem_relinquish();
   }
   if (tid < kC) gs[tid] = p.tab[it].g[tid];
+  const float ik = p.tab[it].ik, isf = operand_scale(__uint_as_float(p.amax_s[(size_t)seq * p.seqs.H + h])).y;
   cp_async_wait<0>();
-  fence_proxy_async_shared();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
+  const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + 64 * hf;
+  const float iq = tile_to_f16(s + kOQ, red, tid);
+  __syncthreads();
   if (tid == 0) {
-    mma_tile(tmem, sQ, false, sK, false, false);
-    umma_commit(bars + 1);
     wait_bar(bars, 0, p.err);
-    mma_tile(tmem + 128, sQ, false, sS, true, false);  // Q X
+    tc_fence_after();
+    mma_tile(tmem, sQ, false, sK, false, false);
+    mma_tile(tmem + 128, sQ, false, sS, true, false);
+    umma_commit(bars + 1);
   }
   __syncwarp();
   wait_bar(bars + 1, 0, p.err);
   __syncwarp();
   tc_fence_after();
+  if (tid == 0) {
+    mbar_arrive_expect_tx(bars, kTile);
+    bulk_load(s + kOS, p.E + (size_t)it * kTile, kTile, bars);
+  }
+  __syncwarp();
   const float2 gi = gs[i];
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {  // scale (Q K^T . G), bf16, over K
+  for (int c = 0; c < 2; ++c) {  // Q K^T . G over K
     const int j0 = 64 * hf + 32 * c;
     float a[32];
-    tmem_ld32(tl + j0, a);
+    tmem_ld32(tl + 32 * c, a);
     tmem_ld_wait();
 #pragma unroll
-    for (int jj = 0; jj < 32; ++jj) a[jj] = j0 + jj <= i ? p.scale * a[jj] * exp_diff(gi, gs[j0 + jj]) : 0.f;
+    for (int jj = 0; jj < 32; ++jj) a[jj] = j0 + jj <= i ? kScoreDown * a[jj] * exp_diff(gi, gs[j0 + jj]) : 0.f;
 #pragma unroll
     for (int c8 = 0; c8 < 4; ++c8)
       *reinterpret_cast<uint4*>(s + kOK + swz16(i, (j0 >> 3) + c8)) =
-          make_uint4(pack_bf16x2(a[8 * c8], a[8 * c8 + 1]), pack_bf16x2(a[8 * c8 + 2], a[8 * c8 + 3]),
-                     pack_bf16x2(a[8 * c8 + 4], a[8 * c8 + 5]), pack_bf16x2(a[8 * c8 + 6], a[8 * c8 + 7]));
+          make_uint4(pack_f16x2(a[8 * c8], a[8 * c8 + 1]), pack_f16x2(a[8 * c8 + 2], a[8 * c8 + 3]),
+                     pack_f16x2(a[8 * c8 + 4], a[8 * c8 + 5]), pack_f16x2(a[8 * c8 + 6], a[8 * c8 + 7]));
   }
   fence_proxy_async_shared();
   tc_fence_before();
   __syncthreads();
   if (tid == 0) {
+    wait_bar(bars, 1, p.err);
     tc_fence_after();
-    mma_tile(tmem + 256, sK, false, sE, true, false);
+    mma_tile(tmem, sK, false, sS, true, false);
     umma_commit(bars + 1);
   }
   __syncwarp();
   wait_bar(bars + 1, 1, p.err);
   __syncwarp();
   tc_fence_after();
-  const float fi = p.scale * exp_diff(gi, make_float2(0.f, 0.f));
+  const float fx = p.scale * iq * isf * exp_diff(gi, make_float2(0.f, 0.f));
+  const float fa = p.scale * iq * ik * isf / kScoreDown;
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const int j0 = 64 * hf + 32 * c;
     if (j0 >= p.dv) continue;
     float a[32], x[32];
-    tmem_ld32(tl + 128 + j0, x);
-    tmem_ld32(tl + 256 + j0, a);
+    tmem_ld32(tl + 32 * c, a);
+    tmem_ld32(tl + 128 + 32 * c, x);
     tmem_ld_wait();
     if (i < n) {
       uint4* og = reinterpret_cast<uint4*>(p.o + (row0 + i) * p.dv + j0);
@@ -605,7 +840,7 @@ __global__ void __launch_bounds__(256, 1) gdr_out_kernel(TcParams p) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int j = 8 * v + 2 * e;
-          w[e] = pack_bf16x2(fmaf(fi, x[j], a[j]), fmaf(fi, x[j + 1], a[j + 1]));
+          w[e] = pack_bf16x2(fmaf(fx, x[j], fa * a[j]), fmaf(fx, x[j + 1], fa * a[j + 1]));
         }
         og[v] = make_uint4(w[0], w[1], w[2], w[3]);
       }
@@ -615,17 +850,295 @@ __global__ void __launch_bounds__(256, 1) gdr_out_kernel(TcParams p) {
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, 256);
   }
 }
 
+// ---------------------------------------------------------------- gradients
+constexpr float kGradDown = 1.f / 64.f;  // of R and N, as operands
+constexpr uint32_t kGBars = 7 * kTile;
+constexpr uint32_t kGTab = kGBars + 6 * 8;
+constexpr uint32_t kGradSmem = kGTab + (2 + 2) * kC * 4 + 64;
+static_assert(kGradSmem <= 232448, "shared memory budget of one CTA");
+
+// One CTA per (chunk, key head); the value heads that share it are taken in
+// turn, dq adding up in tensor memory and dk in registers, in a fixed order.
+// Per head three rounds of products over seven tiles of shared memory:
+//   dO S, (beta w) S, u D;   dO u^T, (beta w) u^T, Q K^T;   R K, R^T Q, (N + N^T) K
+// with R = scale (dO u^T . G) and N = ((beta w) u^T . G) strictly lower.  The
+// first and fourth take u and S in two parts: q.dq, which enters dlog_alpha, is
+// then exact to float32; the rest ends in 16-bit gradients.
+__global__ void __launch_bounds__(256, 1) gdr_grad_tc_kernel(TcParams p) {
+  extern __shared__ __align__(1024) unsigned char s[];
+  if (smem_u32(s) & 1023u) {
+    if (threadIdx.x == 0) atomicOr(p.err, kErrDeviceArg);
+    return;
+  }
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int q = warp & 3, hf = warp >> 2, i = 32 * q + lane;
+  const int hk = blockIdx.x % p.seqs.Hk, slot = blockIdx.x / p.seqs.Hk, G = p.seqs.H / p.seqs.Hk;
+  int seq, chunk;
+  GdrSeq sq;
+  if (!gdr_find(p.seqs, slot, kC, seq, chunk, sq)) return;
+  const int t0 = chunk * kC, n = min(kC, sq.len - t0);
+  const size_t krow0 = ((size_t)sq.row_b * p.seqs.Hk + hk) * p.seqs.T + sq.start + t0;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s + kGBars);  // 0: round 1, 1: low u, 2: Q and K, 3: products
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s + kGBars + 4 * 8);
+  float2* gs = reinterpret_cast<float2*>(s + kGTab);
+  float* dg = reinterpret_cast<float*>(gs + kC);        // [2][token]
+  double* tot = reinterpret_cast<double*>(dg + 2 * kC);  // [4]
+  auto slot_at = [&](int x) { return s + x * kTile; };
+  if (tid == 0) {
+    for (int b = 0; b < 4; ++b) mbar_init(bars + b, 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + 64 * hf;
+  const uint32_t s0 = smem_u32(s);
+  uint32_t nmma = 0;
+  auto wait_mma = [&]() {
+    wait_bar(bars + 3, nmma & 1, p.err);
+    ++nmma;
+    __syncwarp();
+    tc_fence_after();
+  };
+  float xk[64];  // dk of this thread's row and columns, over the heads
+#pragma unroll
+  for (int j = 0; j < 64; ++j) xk[j] = 0.f;
+
+  for (int hh = 0; hh < G; ++hh) {
+    const int h = hk * G + hh;
+    const size_t it = (size_t)slot * p.seqs.H + h, sh = (size_t)seq * p.seqs.H + h;
+    const size_t row0 = ((size_t)sq.row_b * p.seqs.H + h) * p.seqs.T + sq.start + t0;
+    const uint32_t par = hh & 1;
+    // slots: 0 dO, then N; 1 S high, then Q; 2 S low, then K; 3 beta w; 4 u high; 5 D, then R; 6 u low
+    if (tid == 0) {
+      mbar_arrive_expect_tx(bars, 6 * kTile);
+      bulk_load(slot_at(0), p.dO16 + it * kTile, kTile, bars);
+      bulk_load(slot_at(1), p.S + it * 2 * kTile, 2 * kTile, bars);
+      bulk_load(slot_at(3), p.Y + it * kTile, kTile, bars);
+      bulk_load(slot_at(4), p.E + it * 2 * kTile, kTile, bars);
+      bulk_load(slot_at(5), p.D + it * kTile, kTile, bars);
+      mbar_arrive_expect_tx(bars + 1, kTile);
+      bulk_load(slot_at(6), p.E + (it * 2 + 1) * kTile, kTile, bars + 1);
+      wait_bar(bars, par, p.err);
+      tc_fence_after();
+      mma_tile(tmem + 128, s0, false, s0 + 2 * kTile, false, false);
+      mma_tile(tmem + 128, s0, false, s0 + kTile, false, true);
+      mma_tile(tmem + 256, s0 + 3 * kTile, false, s0 + kTile, false, false);
+      mma_tile(tmem + 384, s0 + 4 * kTile, false, s0 + 5 * kTile, false, false);
+      umma_commit(bars + 3);
+    }
+    __syncwarp();
+    const Tables& tb = p.tab[it];
+    if (tid < kC) gs[tid] = tb.g[tid];
+    const float ik = tb.ik, iq = tb.iq, id = tb.id, in = tb.into[i], out = tb.out[i];
+    const float isf = operand_scale(__uint_as_float(p.amax_s[sh])).y, isr = operand_scale(__uint_as_float(p.amax_d[sh])).y;
+    wait_mma();
+    if (tid == 0) {
+      mbar_arrive_expect_tx(bars + 2, 2 * kTile);
+      bulk_load(slot_at(1), p.Q16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, kTile, bars + 2);
+      bulk_load(slot_at(2), p.K16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, kTile, bars + 2);
+    }
+    __syncwarp();
+    // ---- round 1: dq's and dk's parts by the states.  q.dq's first part: by Q's row as given
+    float qdot = 0.f;
+    {
+      const float fq = p.scale * in * id * isf, fu = isf * isr * out, fw = -isf * isr * in;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float a[32], x[32];
+        tmem_ld32(tl + 256 + 32 * c, a);
+        tmem_ld32(tl + 384 + 32 * c, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) xk[32 * c + j] += fmaf(fu, x[j], fw * a[j]);
+        const int j0 = 64 * hf + 32 * c;
+        tmem_ld32(tl + 128 + 32 * c, a);
+        if (hh > 0) tmem_ld32(tl + 32 * c, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          a[j] *= fq;
+          if (hh == 0) x[j] = 0.f;
+        }
+        if (i < n && j0 < p.dk) {
+          const uint4* qg = reinterpret_cast<const uint4*>(p.q + (krow0 + i) * p.dk + j0);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const uint4 qv = qg[v];
+            const uint32_t w[4] = {qv.x, qv.y, qv.z, qv.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = unpack_bf16x2(w[e]);
+              qdot = fmaf(f.x, a[8 * v + 2 * e], fmaf(f.y, a[8 * v + 2 * e + 1], qdot));
+            }
+          }
+        }
+        uint32_t w[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(x[j] + a[j]);
+        tmem_st32(tl + 32 * c, w);
+      }
+      tmem_st_wait();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0) {
+      wait_bar(bars + 1, par, p.err);
+      tc_fence_after();
+      mma_tile(tmem + 128, s0, false, s0 + 6 * kTile, false, false);
+      mma_tile(tmem + 128, s0, false, s0 + 4 * kTile, false, true);
+      mma_tile(tmem + 256, s0 + 3 * kTile, false, s0 + 4 * kTile, false, false);
+      wait_bar(bars + 2, par, p.err);
+      mma_tile(tmem + 384, s0 + kTile, false, s0 + 2 * kTile, false, false);
+      umma_commit(bars + 3);
+    }
+    __syncwarp();
+    wait_mma();
+    // ---- round 2: R and N as operands; q.dq's second part, the row sums of R . Q K^T
+    {
+      const float2 gi = gs[i];
+      const float fr = p.scale * id * isf * iq * ik;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int j0 = 64 * hf + 32 * c;
+        float r[32], a[32];
+        tmem_ld32(tl + 128 + 32 * c, r);
+        tmem_ld32(tl + 384 + 32 * c, a);
+        tmem_ld_wait();
+        float dec[32], sum = 0.f;
+#pragma unroll
+        for (int jj = 0; jj < 32; ++jj) {
+          dec[jj] = j0 + jj <= i ? exp_diff(gi, gs[j0 + jj]) : 0.f;
+          r[jj] = dec[jj] == 0.f ? 0.f : r[jj] * dec[jj];
+          sum = fmaf(r[jj], a[jj], sum);
+        }
+        qdot = fmaf(fr, sum, qdot);
+        tmem_ld32(tl + 256 + 32 * c, a);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c8 = 0; c8 < 4; ++c8) {
+          uint32_t rw[4], nw[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = 8 * c8 + 2 * e;
+            rw[e] = pack_f16x2(kGradDown * r[j], kGradDown * r[j + 1]);
+            const float n0 = j0 + j < i ? kGradDown * dec[j] * a[j] : 0.f;
+            const float n1 = j0 + j + 1 < i ? kGradDown * dec[j + 1] * a[j + 1] : 0.f;
+            nw[e] = pack_f16x2(n0, n1);
+          }
+          const uint32_t at = swz16(i, (j0 >> 3) + c8);
+          *reinterpret_cast<uint4*>(slot_at(5) + at) = make_uint4(rw[0], rw[1], rw[2], rw[3]);
+          *reinterpret_cast<uint4*>(slot_at(0) + at) = make_uint4(nw[0], nw[1], nw[2], nw[3]);
+        }
+      }
+      dg[hf * kC + i] = qdot;
+    }
+    fence_proxy_async_shared();
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0) {
+      tc_fence_after();
+      mma_tile(tmem + 128, s0 + 5 * kTile, false, s0 + 2 * kTile, true, false);  // R K
+      mma_tile(tmem + 256, s0 + 5 * kTile, true, s0 + kTile, true, false);       // R^T Q
+      mma_tile(tmem + 384, s0, false, s0 + 2 * kTile, true, false);              // N K
+      mma_tile(tmem + 384, s0, true, s0 + 2 * kTile, true, true);                // N^T K
+      umma_commit(bars + 3);
+    }
+    __syncwarp();
+    // ---- the gates' gradients: sums over the slices, the suffix sum over the chunk
+    if (tid < kC) {
+      float ew = 0.f, vw = 0.f;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const float2 f = p.part[(it * 8 + x) * kC + tid];
+        ew += f.x;
+        vw += f.y;
+      }
+      double y = tid < n ? (double)((dg[tid] + dg[kC + tid]) - vw) : 0.0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double z = __shfl_down_sync(0xffffffffu, y, o);
+        if (lane + o < 32) y += z;
+      }
+      if (lane == 0) tot[warp] = y;
+      float bsum = p.bnd[it * 32 + lane];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) bsum += __shfl_xor_sync(0xffffffffu, bsum, o);
+      named_bar_sync(1, kC);
+      for (int w = warp + 1; w < 4; ++w) y += tot[w];
+      if (tid < n) {
+        p.dlog_alpha[row0 + tid] = (float)(y + (double)bsum);
+        p.dbeta[row0 + tid] = ew;
+      }
+    }
+    wait_mma();
+    // ---- round 3
+    {
+      const float f0 = p.scale * id * isf * ik / kGradDown, f1 = p.scale * id * isf * iq / kGradDown;
+      const float f2 = -isf * isr * ik / kGradDown;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float a[32], x[32];
+        tmem_ld32(tl + 256 + 32 * c, a);
+        tmem_ld32(tl + 384 + 32 * c, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) xk[32 * c + j] += fmaf(f1, a[j], f2 * x[j]);
+        tmem_ld32(tl + 32 * c, a);
+        tmem_ld32(tl + 128 + 32 * c, x);
+        tmem_ld_wait();
+        if (hh + 1 < G) {
+          uint32_t w[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(fmaf(f0, x[j], a[j]));
+          tmem_st32(tl + 32 * c, w);
+        } else if (i < n && 64 * hf + 32 * c < p.dk) {
+          const size_t at = (krow0 + i) * p.dk + 64 * hf + 32 * c;
+          uint4* qg = reinterpret_cast<uint4*>(p.dq + at);
+          uint4* kg = reinterpret_cast<uint4*>(p.dkey + at);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            uint32_t w[4], y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int j = 8 * v + 2 * e;
+              w[e] = pack_bf16x2(fmaf(f0, x[j], a[j]), fmaf(f0, x[j + 1], a[j + 1]));
+              y[e] = pack_bf16x2(xk[32 * c + j], xk[32 * c + j + 1]);
+            }
+            qg[v] = make_uint4(w[0], w[1], w[2], w[3]);
+            kg[v] = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        }
+      }
+      if (hh + 1 < G) tmem_st_wait();
+    }
+    tc_fence_before();
+    __syncthreads();  // the next head's tiles and tables
+    tc_fence_after();
+  }
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- host side
 struct Plan {
-  size_t W, U, K16, S, E, tab, amax, amax_bytes, total;
+  size_t W, U, K16, S, E, tab, amax, amax_bytes;
+  size_t Q16, dO16, Wd, w0, Bc, D, Y, fin, part, bnd;
+  size_t total;
   int slots;
 };
-Plan plan_of(const GdrArgs& a) {
+Plan plan_of(const GdrArgs& a, bool bwd) {
   Plan p{};
-  const size_t slots = gdr_slots(a, kC), items = slots * a.H;
+  const size_t slots = gdr_slots(a, kC), items = slots * a.H, rows = items * kC * kC * 4;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t x = at;
@@ -633,14 +1146,27 @@ Plan plan_of(const GdrArgs& a) {
     return x;
   };
   p.slots = (int)slots;
+  const int parts = bwd ? 2 : 1;
   p.W = take(items * 2 * kTile);
-  p.U = take(items * kC * kC * 4);
+  p.U = take(rows);
   p.K16 = take(slots * a.Hk * kTile);
-  p.S = take(items * kTile);
-  p.E = take(items * kTile);
+  p.S = take(items * parts * kTile);
+  p.E = take(items * parts * kTile);
   p.tab = take(items * sizeof(Tables));
-  p.amax_bytes = (size_t)gdr_sequences(a) * a.H * 4;
+  p.amax_bytes = (size_t)2 * gdr_sequences(a) * a.H * 4;
   p.amax = take(p.amax_bytes);
+  if (bwd) {
+    p.Q16 = take(slots * a.Hk * kTile);
+    p.dO16 = take(items * kTile);
+    p.Wd = take(items * 2 * kTile);
+    p.w0 = take(rows);
+    p.Bc = take(rows);
+    p.D = take(items * kTile);
+    p.Y = take(items * kTile);
+    p.fin = take((size_t)gdr_sequences(a) * a.H * a.dv * a.dk * 4);
+    p.part = take(items * 8 * kC * sizeof(float2));
+    p.bnd = take(items * 32 * 4);
+  }
   p.total = at;
   return p;
 }
@@ -653,15 +1179,7 @@ int sm_count() {
   return sms;
 }
 
-}  // namespace
-
-bool gdr_tc_supported(const GdrArgs& a) {
-  return a.io == LL_BF16 && a.dk >= 64 && a.dv >= 64 && a.T >= kGdrTcMinTokens;
-}
-size_t gdr_tc_fwd_workspace(const GdrArgs& a) { return plan_of(a).total; }
-
-ll_status gdr_tc_fwd_launch(const GdrArgs& a) {
-  const Plan pl = plan_of(a);
+TcParams params_of(const GdrArgs& a, const Plan& pl, bool bwd) {
   unsigned char* ws = static_cast<unsigned char*>(a.ws);
   TcParams p{};
   p.seqs = GdrSeqs{a.n_seqs ? a.seq_starts : nullptr, gdr_sequences(a), a.T, a.H, a.Hk};
@@ -672,30 +1190,90 @@ ll_status gdr_tc_fwd_launch(const GdrArgs& a) {
   p.q = static_cast<const __nv_bfloat16*>(a.q);
   p.k = static_cast<const __nv_bfloat16*>(a.k);
   p.v = static_cast<const __nv_bfloat16*>(a.v);
+  p.dout = static_cast<const __nv_bfloat16*>(a.dout);
   p.log_alpha = a.log_alpha;
   p.beta = a.beta;
   p.state_in = a.state_in;
+  p.dstate_out = a.dstate_out;
   p.o = static_cast<__nv_bfloat16*>(a.o);
   p.state_out = a.state_out;
+  p.dq = static_cast<__nv_bfloat16*>(a.dq);
+  p.dkey = static_cast<__nv_bfloat16*>(a.dkey);
+  p.dval = static_cast<__nv_bfloat16*>(a.dval);
+  p.dlog_alpha = a.dlog_alpha;
+  p.dbeta = a.dbeta;
+  p.dstate_in = a.dstate_in;
   p.W = ws + pl.W;
   p.U = reinterpret_cast<float*>(ws + pl.U);
   p.K16 = ws + pl.K16;
   p.S = ws + pl.S;
   p.E = ws + pl.E;
   p.tab = reinterpret_cast<Tables*>(ws + pl.tab);
-  p.amax = reinterpret_cast<unsigned*>(ws + pl.amax);
+  p.amax_s = reinterpret_cast<unsigned*>(ws + pl.amax);
+  p.amax_d = p.amax_s + (size_t)gdr_sequences(a) * a.H;
+  if (bwd) {
+    p.Q16 = ws + pl.Q16;
+    p.dO16 = ws + pl.dO16;
+    p.Wd = ws + pl.Wd;
+    p.w0 = reinterpret_cast<float*>(ws + pl.w0);
+    p.Bc = reinterpret_cast<float*>(ws + pl.Bc);
+    p.D = ws + pl.D;
+    p.Y = ws + pl.Y;
+    p.final_state = reinterpret_cast<float*>(ws + pl.fin);
+    p.part = reinterpret_cast<float2*>(ws + pl.part);
+    p.bnd = reinterpret_cast<float*>(ws + pl.bnd);
+  }
   p.err = a.err;
-  const int items = pl.slots * a.H, sms = sm_count(), slices = a.dv / kSlice;
+  return p;
+}
+
+template <int MODE> ll_status scan(const GdrArgs& a, const TcParams& p, int slices) {
+  LL_CUDA_OK(cudaFuncSetAttribute(gdr_scan_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScanSmem));
+  gdr_scan_kernel<MODE><<<(unsigned)(gdr_sequences(a) * a.H * slices), 256, kScanSmem, a.stream>>>(p, slices);
+  LL_CUDA_OK(cudaGetLastError());
+  return LL_OK;
+}
+template <bool BWD> ll_status prep(const GdrArgs& a, const TcParams& p, const Plan& pl) {
+  const int items = pl.slots * a.H, sms = sm_count();
   if (sms == 0) return LL_ERR_CUDA;
-  LL_CUDA_OK(cudaFuncSetAttribute(gdr_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPrepSmem));
-  LL_CUDA_OK(cudaFuncSetAttribute(gdr_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScanSmem));
+  LL_CUDA_OK(cudaFuncSetAttribute(gdr_prep_kernel<BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  (int)PrepSm<BWD>::kBytes));
+  LL_CUDA_OK(cudaMemsetAsync(p.amax_s, 0, pl.amax_bytes, a.stream));
+  gdr_prep_kernel<BWD><<<std::min(items, sms), 256, PrepSm<BWD>::kBytes, a.stream>>>(p);
+  LL_CUDA_OK(cudaGetLastError());
+  return LL_OK;
+}
+
+}  // namespace
+
+bool gdr_tc_supported(const GdrArgs& a) {
+  return a.io == LL_BF16 && a.dk >= 64 && a.dv >= 64 && a.T >= kGdrTcMinTokens;
+}
+size_t gdr_tc_fwd_workspace(const GdrArgs& a) { return plan_of(a, false).total; }
+size_t gdr_tc_bwd_workspace(const GdrArgs& a) { return plan_of(a, true).total; }
+
+ll_status gdr_tc_fwd_launch(const GdrArgs& a) {
+  const Plan pl = plan_of(a, false);
+  const TcParams p = params_of(a, pl, false);
+  ll_status st = prep<false>(a, p, pl);
+  if (st == LL_OK) st = scan<kFwd>(a, p, a.dv / kSlice);
+  if (st != LL_OK) return st;
   LL_CUDA_OK(cudaFuncSetAttribute(gdr_out_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kOutSmem));
-  LL_CUDA_OK(cudaMemsetAsync(p.amax, 0, pl.amax_bytes, a.stream));
-  gdr_prep_kernel<<<std::min(items, sms), 256, kPrepSmem, a.stream>>>(p);
+  gdr_out_kernel<<<pl.slots * a.H, 256, kOutSmem, a.stream>>>(p);
   LL_CUDA_OK(cudaGetLastError());
-  gdr_scan_kernel<<<(unsigned)(gdr_sequences(a) * a.H * slices), 256, kScanSmem, a.stream>>>(p, slices);
-  LL_CUDA_OK(cudaGetLastError());
-  gdr_out_kernel<<<items, 256, kOutSmem, a.stream>>>(p);
+  return LL_OK;
+}
+
+ll_status gdr_tc_bwd_launch(const GdrArgs& a) {
+  const Plan pl = plan_of(a, true);
+  const TcParams p = params_of(a, pl, true);
+  ll_status st = prep<true>(a, p, pl);
+  // all slices, so that the columns behind a d_v of 64 are zeros: they are summed over
+  if (st == LL_OK) st = scan<kFwdKeep>(a, p, kC / kSlice);
+  if (st == LL_OK) st = scan<kRev>(a, p, kC / kSlice);
+  if (st != LL_OK) return st;
+  LL_CUDA_OK(cudaFuncSetAttribute(gdr_grad_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGradSmem));
+  gdr_grad_tc_kernel<<<pl.slots * a.Hk, 256, kGradSmem, a.stream>>>(p);
   LL_CUDA_OK(cudaGetLastError());
   return LL_OK;
 }
