@@ -65,25 +65,55 @@ struct TcParams {
 };
 
 // ---------------------------------------------------------------- preparation
+// one (chunk, head): its number (no more when it is the item count), sequence, place and length
+struct Item {
+  int it, seq, chunk, t0, n, len;
+  size_t row0, krow0;
+};
+// the first item at or after `it`, `step` apart, that a chunk owns
+__device__ __forceinline__ void find_item(const TcParams& p, int it, int step, Item* out) {
+  const int items = p.slots * p.seqs.H;
+  for (; it < items; it += step) {
+    const int slot = it / p.seqs.H, h = it - slot * p.seqs.H, hk = h / (p.seqs.H / p.seqs.Hk);
+    int seq, chunk;
+    GdrSeq sq;
+    if (!gdr_find(p.seqs, slot, kC, seq, chunk, sq)) continue;
+    out->seq = seq;
+    out->chunk = chunk;
+    out->t0 = chunk * kC;
+    out->n = min(kC, sq.len - chunk * kC);
+    out->len = sq.len;
+    out->row0 = ((size_t)sq.row_b * p.seqs.H + h) * p.seqs.T + sq.start + chunk * kC;
+    out->krow0 = ((size_t)sq.row_b * p.seqs.Hk + hk) * p.seqs.T + sq.start + chunk * kC;
+    break;
+  }
+  out->it = it;
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 template <bool BWD> struct PrepSm {
   static constexpr uint32_t kX0 = 0;                               // K; then T (high)
   static constexpr uint32_t kX1 = kTile;                           // V (forward), Q; then T (low)
   static constexpr uint32_t kX2 = 2 * kTile;                       // backward: V, dO
-  static constexpr uint32_t kM = (BWD ? 3 : 2) * kTile;            // M's blocks, float32
-  static constexpr uint32_t kR = kM + kBlocksB;                    // A's blocks; then operands in two parts
+  static constexpr uint32_t kM = (BWD ? 3 : 2) * kTile;            // M, float32
+  static constexpr uint32_t kR = kM + kMatB;                       // A, float32; then operands in two parts
   static constexpr uint32_t kTab = kR + 2 * kTile;
-  static constexpr uint32_t kBars = kTab + 5 * kC * 4 + 32 + 3 * 32;
-  static constexpr uint32_t kBytes = kBars + 24;
+  static constexpr uint32_t kBars = kTab + 5 * kC * 4 + 32 + 3 * 64 + 16;
+  static constexpr uint32_t kNext = kBars + 16;
+  static constexpr uint32_t kBytes = kNext + sizeof(Item);
 };
-static_assert(PrepSm<true>::kR % 1024 == 0 && PrepSm<true>::kBars % 8 == 0, "tile alignment");
+static_assert(kMatB == 2 * kTile && PrepSm<true>::kBars % 8 == 0, "tile alignment");
 static_assert(PrepSm<true>::kBytes <= 232448, "shared memory budget of one CTA");
 
 constexpr float kScoreDown = 1.f / 256.f;  // of the scores Q K^T of scaled tiles, as operands
 constexpr float kRowsDown = 1.f / 16.f;    // of P^T dO, as an operand
 
-// Persistent, one CTA per SM, an item per (chunk, head).
+// Persistent, one CTA per SM, an item per (chunk, head).  Thread = (row, quarter
+// of the columns); while warps 0 to 7 solve for M, the others make operands of the
+// inputs that are not needed before, and look for the next item.
+constexpr int kPrepThreads = 512, kPrepBar2 = 2;
 template <bool BWD>
-__global__ void __launch_bounds__(256, 1) gdr_prep_kernel(TcParams p) {
+__global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
   using Sm = PrepSm<BWD>;
   extern __shared__ __align__(1024) unsigned char s[];
   if (smem_u32(s) & 1023u) {
@@ -91,16 +121,18 @@ __global__ void __launch_bounds__(256, 1) gdr_prep_kernel(TcParams p) {
     return;
   }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int q = warp & 3, hf = warp >> 2;
-  const int i = 32 * q + lane;  // this thread's row (TMEM lane), columns 64 hf ..
+  const int q = warp & 3, qt = warp >> 2;
+  const int i = 32 * q + lane;  // this thread's row (TMEM lane), columns 32 qt ..
   float2* gs = reinterpret_cast<float2*>(s + Sm::kTab);
   float* bs = reinterpret_cast<float*>(gs + kC);
   float* in_s = bs + kC;
   float* out_s = in_s + kC;
-  double* tot = reinterpret_cast<double*>(out_s + kC);
-  uint32_t* red = reinterpret_cast<uint32_t*>(tot + 4);
+  float2* tot = reinterpret_cast<float2*>(out_s + kC);
+  uint32_t* red = reinterpret_cast<uint32_t*>(tot + 4);  // 3 x 16
+  float* inv = reinterpret_cast<float*>(red + 48);       // inverse scales of V and Q
   uint64_t* bar = reinterpret_cast<uint64_t*>(s + Sm::kBars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s + Sm::kBars + 8);
+  Item* next = reinterpret_cast<Item*>(s + Sm::kNext);
   float* Ap = reinterpret_cast<float*>(s + Sm::kR);
   float* Mp = reinterpret_cast<float*>(s + Sm::kM);
   unsigned char *X0 = s + Sm::kX0, *X1 = s + Sm::kX1, *XV = s + (BWD ? Sm::kX2 : Sm::kX1), *R = s + Sm::kR;
@@ -108,6 +140,7 @@ __global__ void __launch_bounds__(256, 1) gdr_prep_kernel(TcParams p) {
   if (tid == 0) {
     mbar_init(bar, 1);
     fence_mbar_init();
+    find_item(p, blockIdx.x, gridDim.x, next);
   }
   __syncwarp();
   if (warp == 0) {
@@ -118,7 +151,7 @@ __global__ void __launch_bounds__(256, 1) gdr_prep_kernel(TcParams p) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + 64 * hf;
+  const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + 32 * qt;
   uint32_t nmma = 0;
   auto wait_mma = [&]() {
     wait_bar(bar, nmma & 1, p.err);
@@ -136,67 +169,7 @@ __global__ void __launch_bounds__(256, 1) gdr_prep_kernel(TcParams p) {
       products();
       umma_commit(bar);
     }
-  };
-  // rows (diag(fr) (I + diag(br) M diag(bc)) diag(fc)), this thread's 64 columns, in two parts
-  auto put_inverse = [&](unsigned char* hi, unsigned char* lo, float fr, float br, const float* bc, const float* fc) {
-    const int I = i >> 4;
-#pragma unroll
-    for (int jb = 0; jb < 4; ++jb) {
-      const int J = 4 * hf + jb;
-      float t[16];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        float4 x4 = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (J <= I) x4 = *reinterpret_cast<const float4*>(Mp + blk(I, J) + (i & 15) * kBS + 4 * v);
-        t[4 * v] = x4.x;
-        t[4 * v + 1] = x4.y;
-        t[4 * v + 2] = x4.z;
-        t[4 * v + 3] = x4.w;
-      }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int j = 16 * J + e;
-        float x = br * t[e];
-        if (bc) x *= bc[j];
-        if (j == i) x = 1.f;
-        if (fc) x *= fc[j];
-        t[e] = fr * x;
-      }
-      put_parts(hi, lo, swz16(i, 2 * J), t, 1.f);
-      put_parts(hi, lo, swz16(i, 2 * J + 1), t + 8, 1.f);
-    }
-  };
-  // this thread's row of an accumulator, times f, as [slice][piece][row][4] floats; returns the largest value's bits
-  auto write_rows = [&](float* dst, int col, float f) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      float x[32];
-      tmem_ld32(tl + col + 32 * c, x);
-      tmem_ld_wait();
-      float4* d = reinterpret_cast<float4*>(dst) + (size_t)(2 * hf + c) * 8 * kC + i;
-#pragma unroll
-      for (int v = 0; v < 8; ++v) {
-        const float4 y = make_float4(f * x[4 * v], f * x[4 * v + 1], f * x[4 * v + 2], f * x[4 * v + 3]);
-        m = max(max(m, max(__float_as_uint(fabsf(y.x)), __float_as_uint(fabsf(y.y)))),
-                max(__float_as_uint(fabsf(y.z)), __float_as_uint(fabsf(y.w))));
-        d[v * kC] = y;
-      }
-    }
-    return m;
-  };
-  // likewise as the two tiles of a scan's operand
-  auto write_tiles = [&](unsigned char* dst, int col, float f) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      float x[32];
-      tmem_ld32(tl + col + 32 * c, x);
-      tmem_ld_wait();
-#pragma unroll
-      for (int j = 0; j < 32; ++j) x[j] *= f;
-#pragma unroll
-      for (int c8 = 0; c8 < 4; ++c8) put_parts(dst, dst + kTile, swz16(i, 8 * hf + 4 * c + c8), x + 8 * c8, kLoScale);
-    }
+    __syncwarp();
   };
   auto raise_max = [&](unsigned* at, uint32_t m) {
     m = __reduce_max_sync(0xffffffffu, m);
@@ -204,33 +177,32 @@ __global__ void __launch_bounds__(256, 1) gdr_prep_kernel(TcParams p) {
   };
   auto state_max = [&](const float* x) {
     uint32_t m = 0;
-    for (int e = tid; e < p.dv * p.dk; e += 256) m = max(m, __float_as_uint(fabsf(x[e])));
+    for (int e = tid; e < p.dv * p.dk; e += kPrepThreads) m = max(m, __float_as_uint(fabsf(x[e])));
     return m;
   };
 
   const int items = p.slots * p.seqs.H, G = p.seqs.H / p.seqs.Hk;
-  for (int it = blockIdx.x; it < items; it += gridDim.x) {
+  while (true) {
+    const Item me = *next;
+    const int it = me.it, n = me.n;
+    if (it >= items) break;
     const int slot = it / p.seqs.H, h = it - slot * p.seqs.H, hk = h / G;
-    int seq, chunk;
-    GdrSeq sq;
-    if (!gdr_find(p.seqs, slot, kC, seq, chunk, sq)) continue;
-    const int t0 = chunk * kC, n = min(kC, sq.len - t0);
-    const size_t row0 = ((size_t)sq.row_b * p.seqs.H + h) * p.seqs.T + sq.start + t0;
-    const size_t krow0 = ((size_t)sq.row_b * p.seqs.Hk + hk) * p.seqs.T + sq.start + t0;
-    const size_t sh = (size_t)seq * p.seqs.H + h;
+    const size_t row0 = me.row0, krow0 = me.krow0, sh = (size_t)me.seq * p.seqs.H + h;
     unsigned* am_s = p.amax_s + sh;
     Tables& tb = p.tab[it];
+    unsigned char* Wg = p.W + (size_t)it * 2 * kTile;
+    unsigned char* Wdg = p.Wd + (size_t)it * 2 * kTile;
     if (tid == 0) bulk_wait_read0();  // the item before has left shared memory
     __syncthreads();
-    load_tile(X0, p.k + krow0 * p.dk, n, p.dk, tid, 256);
-    if (BWD) load_tile(X1, p.q + krow0 * p.dk, n, p.dk, tid, 256);
+    load_tile(X0, p.k + krow0 * p.dk, n, p.dk, tid, kPrepThreads);
     cp_async_commit();
-    load_tile(XV, p.v + row0 * p.dv, n, p.dv, tid, 256);
+    load_tile(XV, p.v + row0 * p.dv, n, p.dv, tid, kPrepThreads);
+    if (BWD) load_tile(X1, p.q + krow0 * p.dk, n, p.dk, tid, kPrepThreads);
     cp_async_commit();
     if (tid < kC) bs[tid] = tid < n ? p.beta[row0 + tid] : 0.f;
-    chunk_decays(p.log_alpha + row0, n, gs, tot, tid);
+    chunk_decays(tid < n ? gdr_log(p.log_alpha[row0 + tid]) : 0.f, gs, tot, tid);
     const float2 gi = gs[i];
-    if (hf == 0) {
+    if (qt == 0) {
       const float in = exp_diff(gi, make_float2(0.f, 0.f)), out = exp_diff(gs[kC - 1], gi);
       in_s[i] = in;
       out_s[i] = out;
@@ -239,99 +211,121 @@ __global__ void __launch_bounds__(256, 1) gdr_prep_kernel(TcParams p) {
       tb.out[i] = out;
       if (BWD) tb.rel[i] = exp_diff(gi, gs[0]);
     }
-    if (p.state_in && chunk == 0) raise_max(am_s, state_max(p.state_in + sh * p.dv * p.dk));
+    if (p.state_in && me.chunk == 0) raise_max(am_s, state_max(p.state_in + sh * p.dv * p.dk));
     cp_async_wait<1>();
     __syncthreads();
-    const float ik = tile_to_f16(X0, red, tid);
-    float iq = 1.f;
-    if (BWD) iq = tile_to_f16(X1, red + 8, tid);
-    // ---- K K^T -> 0, Q K^T -> 128
+    const float ik = tile_to_f16<kPrepThreads>(X0, red, tid, 0, nullptr);
+    // ---- K K^T -> 0
     issue([&]() {
       mma_tile(tmem, sX0, false, sX0, false, false);
-      if (BWD) mma_tile(tmem + 128, sX1, false, sX0, false, false);
       if (h % G == 0) {
         bulk_store(p.K16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, X0, kTile);
-        if (BWD) bulk_store(p.Q16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, X1, kTile);
         bulk_commit();
       }
     });
-    cp_async_wait<0>();
-    __syncthreads();
-    uint32_t vbits;
-    const float iv = tile_to_f16(XV, red + 16, tid, &vbits);
-    if (tid == 0) {
-      atomicMax(am_s, vbits);
-      tb.ik = ik;
-      tb.iq = iq;
-    }
+    if (tid == 0) tb.ik = ik;
+    cp_async_wait<0>();  // (for the barrier before the solve)
     wait_mma();
     // A_ij = (k_i . k_j) G_ij, j < i
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < 2; ++c) {
-      const int j0 = 64 * hf + 32 * c;
-      if (j0 > 32 * q + 31) continue;  // (warp-uniform) above the diagonal
-      float kk[32];
-      tmem_ld32(tl + 32 * c, kk);
-      tmem_ld_wait();
-      const float f = ik * ik;
+      const int j0 = 32 * qt + 16 * c;
+      if (j0 > 32 * q + 31) break;  // (warp-uniform) above the diagonal
+      float x[16];
+      decayed16(x, tl + 16 * c, gs, gi, j0, i, ik * ik);
 #pragma unroll
-      for (int jj = 0; jj < 32; ++jj) kk[jj] = j0 + jj < i ? f * kk[jj] * exp_diff(gi, gs[j0 + jj]) : 0.f;
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int J = (j0 >> 4) + b, I = i >> 4;
-        if (J <= I) {
-          float4* dst = reinterpret_cast<float4*>(Ap + blk(I, J) + (i & 15) * kBS);
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-            dst[v] = make_float4(kk[16 * b + 4 * v], kk[16 * b + 4 * v + 1], kk[16 * b + 4 * v + 2],
-                                 kk[16 * b + 4 * v + 3]);
+      for (int v = 0; v < 4; ++v)
+        mat4(Ap, i, (j0 >> 2) + v) = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
+    }
+    __syncthreads();
+    if (warp < 8) {
+      tri_solve(Ap, Mp, bs, tid);
+    } else {
+      const int t = tid - 256;
+      uint32_t vbits;
+      const float iv = tile_to_f16<256>(XV, red + 16, t, kPrepBar2, &vbits);
+      float iq = 1.f;
+      if (BWD) iq = tile_to_f16<256>(X1, red + 32, t, kPrepBar2, nullptr);
+      if (t == 0) {
+        atomicMax(am_s, vbits);
+        inv[0] = iv;
+        inv[1] = iq;
+        tb.iq = iq;
+      }
+      if (warp == 15) {  // the next item: where it is, and its rows on their way into L2
+        if (lane == 0) find_item(p, it + gridDim.x, gridDim.x, next);
+        __syncwarp();
+        if (next->it < items) {
+          const char* kp = reinterpret_cast<const char*>(p.k + next->krow0 * p.dk);
+          const char* qp = reinterpret_cast<const char*>(p.q + next->krow0 * p.dk);
+          const char* vp = reinterpret_cast<const char*>(p.v + next->row0 * p.dv);
+          const char* dp = reinterpret_cast<const char*>(p.dout + next->row0 * p.dv);
+          for (int x = lane * 128; x < next->n * p.dk * 2; x += 32 * 128) {
+            prefetch_l2(kp + x);
+            if (BWD) prefetch_l2(qp + x);
+          }
+          for (int x = lane * 128; x < next->n * p.dv * 2; x += 32 * 128) {
+            prefetch_l2(vp + x);
+            if (BWD) prefetch_l2(dp + x);
+          }
+          if (lane * 32 < next->n) {
+            prefetch_l2(p.log_alpha + next->row0 + lane * 32);
+            prefetch_l2(p.beta + next->row0 + lane * 32);
+          }
         }
       }
     }
     __syncthreads();
-    tri_solve(Ap, Mp, bs, tid);
-    // ---- U = T' V -> 256
-    put_inverse(R, R + kTile, 1.f, 1.f, bs, nullptr);
+    const float iv = inv[0], iq = inv[1];
+    // ---- U = T' V -> 256 (and Q K^T -> 128)
+    put_inverse(R, R + kTile, Mp, i, qt, 1.f, 1.f, bs, nullptr);
     issue([&]() {
       mma_tile(tmem + 256, sR + kTile, false, sXV, true, false);
       mma_tile(tmem + 256, sR, false, sXV, true, true);
+      if (BWD) {
+        mma_tile(tmem + 128, sX1, false, sX0, false, false);
+        if (h % G == 0) {
+          bulk_store(p.Q16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, X1, kTile);
+          bulk_commit();
+        }
+      }
     });
     wait_mma();
     // ---- W = T' diag(exp(g)) K -> 384
-    put_inverse(R, R + kTile, 1.f, 1.f, bs, in_s);
+    put_inverse(R, R + kTile, Mp, i, qt, 1.f, 1.f, bs, in_s);
     issue([&]() {
       mma_tile(tmem + 384, sR + kTile, false, sX0, true, false);
       mma_tile(tmem + 384, sR, false, sX0, true, true);
     });
     if (BWD) {  // (V has been read)
-      load_tile(XV, p.dout + row0 * p.dv, n, p.dv, tid, 256);
+      load_tile(XV, p.dout + row0 * p.dv, n, p.dv, tid, kPrepThreads);
       cp_async_commit();
     }
-    write_rows(p.U + (size_t)it * kC * kC, 256, iv);
+    write_rows(p.U + (size_t)it * kC * kC, tl + 256, i, qt, iv);
     wait_mma();
     if (!BWD) {
-      write_tiles(p.W + (size_t)it * 2 * kTile, 384, ik);
+      write_tiles(Wg, Wg + kTile, tl + 384, i, qt, ik, kLoScale);
     } else {
       const float bi = bs[i];
       cp_async_wait<0>();
       __syncthreads();
-      const float id = tile_to_f16(XV, red, tid);
+      const float id = tile_to_f16<kPrepThreads>(XV, red, tid, 0, nullptr);
       if (tid == 0) tb.id = id;
       // ---- Wd = T^T diag(exp(g_C - g)) K -> 256
-      put_inverse(R, R + kTile, out_s[i], bi, nullptr, nullptr);
+      put_inverse(R, R + kTile, Mp, i, qt, out_s[i], bi, nullptr, nullptr);
       issue([&]() {
         mma_tile(tmem + 256, sR + kTile, true, sX0, true, false);
         mma_tile(tmem + 256, sR, true, sX0, true, true);
         bulk_store(p.dO16 + (size_t)it * kTile, XV, kTile);
         bulk_commit();
       });
-      write_tiles(p.W + (size_t)it * 2 * kTile, 384, ik);
+      write_tiles(Wg, Wg + kTile, tl + 384, i, qt, ik, kLoScale);
       wait_mma();
       // ---- Bc = Q^T diag(exp(g)) dO -> 384, exp(g_0) and its scales below
       const float rel = exp_diff(gi, gs[0]);
-#pragma unroll
-      for (int c8 = 0; c8 < 8; ++c8) {
-        const uint32_t at = swz16(i, 8 * hf + c8);
+#pragma unroll 1
+      for (int c8 = 0; c8 < 4; ++c8) {
+        const uint32_t at = swz16(i, 4 * qt + c8);
         const uint4 v = *reinterpret_cast<const uint4*>(XV + at);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         float x[8];
@@ -347,48 +341,37 @@ __global__ void __launch_bounds__(256, 1) gdr_prep_kernel(TcParams p) {
         mma_tile(tmem + 384, sX1, true, sR + kTile, true, false);
         mma_tile(tmem + 384, sX1, true, sR, true, true);
       });
-      write_tiles(p.Wd + (size_t)it * 2 * kTile, 256, ik);
+      write_tiles(Wdg, Wdg + kTile, tl + 256, i, qt, ik, kLoScale);
       wait_mma();
       // ---- P^T dO -> 0
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < 2; ++c) {
-        const int j0 = 64 * hf + 32 * c;
-        float x[32];
-        tmem_ld32(tl + 128 + 32 * c, x);
-        tmem_ld_wait();
-#pragma unroll
-        for (int jj = 0; jj < 32; ++jj) x[jj] = j0 + jj <= i ? kScoreDown * x[jj] * exp_diff(gi, gs[j0 + jj]) : 0.f;
-#pragma unroll
-        for (int c8 = 0; c8 < 4; ++c8) put_parts(R, R + kTile, swz16(i, (j0 >> 3) + c8), x + 8 * c8, 1.f);
+        float x[16];
+        const int j0 = 32 * qt + 16 * c;
+        decayed16(x, tl + 128 + 16 * c, gs, gi, j0, i + 1, kScoreDown);
+        put_parts(R, R + kTile, swz16(i, j0 >> 3), x, 1.f);
+        put_parts(R, R + kTile, swz16(i, (j0 >> 3) + 1), x + 8, 1.f);
       }
       issue([&]() {
         mma_tile(tmem, sR + kTile, true, sXV, true, false);
         mma_tile(tmem, sR, true, sXV, true, true);
         bulk_wait_read0();  // K16 and Q16 have left (their place is taken next)
       });
-      uint32_t m = write_rows(p.Bc + (size_t)it * kC * kC, 384, p.scale * iq * id * in_s[0]);
-      if (p.dstate_out && t0 + n == sq.len) m = max(m, state_max(p.dstate_out + sh * p.dv * p.dk));
+      uint32_t m = write_rows(p.Bc + (size_t)it * kC * kC, tl + 384, i, qt, p.scale * iq * id * in_s[0]);
+      if (p.dstate_out && me.t0 + n == me.len) m = max(m, state_max(p.dstate_out + sh * p.dv * p.dk));
       wait_mma();
       __syncthreads();
       // ---- w0 = T^T (P^T dO) -> 128
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float x[32];
-        tmem_ld32(tl + 32 * c, x);
-        tmem_ld_wait();
-#pragma unroll
-        for (int jj = 0; jj < 32; ++jj) x[jj] *= kRowsDown;
-#pragma unroll
-        for (int c8 = 0; c8 < 4; ++c8) put_parts(R, R + kTile, swz16(i, 8 * hf + 4 * c + c8), x + 8 * c8, 1.f);
-      }
-      put_inverse(X0, X1, 1.f, bi, nullptr, nullptr);
+      write_tiles(R, R + kTile, tl, i, qt, kRowsDown, 1.f);
+      put_inverse(X0, X1, Mp, i, qt, 1.f, bi, nullptr, nullptr);
       issue([&]() {
         mma_tile(tmem + 128, sX1, true, sR, true, false);
         mma_tile(tmem + 128, sX0, true, sR + kTile, true, true);
         mma_tile(tmem + 128, sX0, true, sR, true, true);
       });
       wait_mma();
-      m = max(m, write_rows(p.w0 + (size_t)it * kC * kC, 128, p.scale * iq * ik * id / (kScoreDown * kRowsDown)));
+      m = max(m, write_rows(p.w0 + (size_t)it * kC * kC, tl + 128, i, qt,
+                            p.scale * iq * ik * id / (kScoreDown * kRowsDown)));
       raise_max(p.amax_d + sh, m);
     }
     tc_fence_before();  // (for the next item's products, behind its barriers)
@@ -776,7 +759,7 @@ __global__ void __launch_bounds__(256, 2) gdr_out_kernel(TcParams p) {
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + 64 * hf;
-  const float iq = tile_to_f16(s + kOQ, red, tid);
+  const float iq = tile_to_f16<256>(s + kOQ, red, tid, 0, nullptr);
   __syncthreads();
   if (tid == 0) {
     wait_bar(bars, 0, p.err);
@@ -1239,7 +1222,7 @@ template <bool BWD> ll_status prep(const GdrArgs& a, const TcParams& p, const Pl
   LL_CUDA_OK(cudaFuncSetAttribute(gdr_prep_kernel<BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   (int)PrepSm<BWD>::kBytes));
   LL_CUDA_OK(cudaMemsetAsync(p.amax_s, 0, pl.amax_bytes, a.stream));
-  gdr_prep_kernel<BWD><<<std::min(items, sms), 256, PrepSm<BWD>::kBytes, a.stream>>>(p);
+  gdr_prep_kernel<BWD><<<std::min(items, sms), kPrepThreads, PrepSm<BWD>::kBytes, a.stream>>>(p);
   LL_CUDA_OK(cudaGetLastError());
   return LL_OK;
 }

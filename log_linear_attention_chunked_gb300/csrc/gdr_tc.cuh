@@ -71,13 +71,20 @@ __host__ __device__ constexpr uint32_t idesc_f16(int N, bool a_mn, bool b_mn) {
   return idesc_bf16(128, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
 }
 
+// The preparation and the gradient run a long sequence of phases once per chunk
+// by eight warps: their code is kept short (loops, functions that are not inlined),
+// because unrolled it left the instruction cache and every phase waited for its
+// own instructions (the solve below: 58 thousand cycles unrolled).
+
 // D (+)= A B over 128 x 128 x 128 fp16; x_mn: that operand's K runs along its rows
-__device__ __forceinline__ void mma_tile(uint32_t d, uint32_t a, bool a_mn, uint32_t b, bool b_mn, bool add) {
+__device__ __noinline__ void mma_tile(uint32_t d, uint32_t a, bool a_mn, uint32_t b, bool b_mn, bool add) {
   const uint32_t id = idesc_f16(128, a_mn, b_mn);
-#pragma unroll
-  for (int kk = 0; kk < 8; ++kk)
-    umma_bf16(d, a_mn ? desc_mn(a, kk) : desc_k(a, kk), b_mn ? desc_mn(b, kk) : desc_k(b, kk), id,
-              (add || kk > 0) ? 1u : 0u);
+  const uint64_t da = a_mn ? desc_mn(a, 0) : desc_k(a, 0), db = b_mn ? desc_mn(b, 0) : desc_k(b, 0);
+#pragma unroll 1
+  for (int kk = 0; kk < 8; ++kk) {
+    const uint64_t ka = (uint64_t)((kk >> 2) * kHalf + (kk & 3) * 32) >> 4, mn = (uint64_t)kk * 128;
+    umma_bf16(d, da + (a_mn ? mn : ka), db + (b_mn ? mn : ka), id, (add || kk > 0) ? 1u : 0u);
+  }
 }
 
 __device__ __forceinline__ void cp_async16_zfill(void* dst, const void* src, bool in) {
@@ -132,105 +139,174 @@ __device__ __forceinline__ void put_parts(unsigned char* hi, unsigned char* lo, 
 // of a 128-token chunk, M solves (I + A diag(beta)) M = -A, so that both inverses
 // are unit triangular and exact for any beta, zero and tiny ones included:
 //   (I + A diag(beta))^-1 = I + M diag(beta),  (I + diag(beta) A)^-1 = I + diag(beta) M.
-// In 16 x 16 blocks: the diagonal blocks by forward substitution (a column per
-// thread); Lam_IM = (I + M_II diag(beta)) A_IM in place of A; then block diagonal
-// by block diagonal, a block per warp,
-//   M_IJ = -(Lam_IJ + sum_{M=J}^{I-1} Lam_IM diag(beta) M_MJ).
-constexpr int kBS = 20;  // row stride (floats) of a block: conflict-free 16-byte reads
-constexpr uint32_t kBlocksB = 36 * 16 * kBS * 4;
-__device__ __forceinline__ int blk(int I, int J) { return (I * (I + 1) / 2 + J) * 16 * kBS; }
-
-__device__ __forceinline__ void tri_solve(float* Ap, float* Mp, const float* beta, int tid) {  // 256 threads, ends in a barrier
-  const int warp = tid >> 5, lane = tid & 31;
-  if (tid < 128) {
-    const int I = tid >> 4, cc = tid & 15;
-    const float* Ab = Ap + blk(I, I);
-    float* Mb = Mp + blk(I, I);
-    float col[16];  // beta_m M_mc
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      float acc = 0.f;
-      if (r > cc) {
-        acc = -Ab[r * kBS + cc];
-#pragma unroll
-        for (int m = 0; m < 16; ++m)
-          if (m > cc && m < r) acc = fmaf(-Ab[r * kBS + m], col[m], acc);
-      }
-      col[r] = beta[16 * I + r] * acc;
-      Mb[r * kBS + cc] = acc;
-    }
-  }
-  __syncthreads();
-  const int r = lane >> 1, c0 = 8 * (lane & 1);
-  // acc[x] += sum_k X[r][k] beta_k Y[k][c0 + x] over one block pair (beta: of X's columns)
-  auto block_fma = [&](float* acc, const float* X, const float* bt, const float* Y) {
-#pragma unroll
-    for (int k4 = 0; k4 < 4; ++k4) {
-      const float4 a = *reinterpret_cast<const float4*>(X + r * kBS + 4 * k4);
-      const float4 bb = *reinterpret_cast<const float4*>(bt + 4 * k4);
-      const float av[4] = {a.x * bb.x, a.y * bb.y, a.z * bb.z, a.w * bb.w};
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        const float4 b0 = *reinterpret_cast<const float4*>(Y + (4 * k4 + kk) * kBS + c0);
-        const float4 b1 = *reinterpret_cast<const float4*>(Y + (4 * k4 + kk) * kBS + c0 + 4);
-        acc[0] = fmaf(av[kk], b0.x, acc[0]); acc[1] = fmaf(av[kk], b0.y, acc[1]);
-        acc[2] = fmaf(av[kk], b0.z, acc[2]); acc[3] = fmaf(av[kk], b0.w, acc[3]);
-        acc[4] = fmaf(av[kk], b1.x, acc[4]); acc[5] = fmaf(av[kk], b1.y, acc[5]);
-        acc[6] = fmaf(av[kk], b1.z, acc[6]); acc[7] = fmaf(av[kk], b1.w, acc[7]);
-      }
-    }
-  };
-  auto load_row = [&](float* acc, const float* src) {
-    const float4 a = *reinterpret_cast<const float4*>(src + r * kBS + c0);
-    const float4 b = *reinterpret_cast<const float4*>(src + r * kBS + c0 + 4);
-    acc[0] = a.x; acc[1] = a.y; acc[2] = a.z; acc[3] = a.w;
-    acc[4] = b.x; acc[5] = b.y; acc[6] = b.z; acc[7] = b.w;
-  };
-  auto store_row = [&](float* dst, const float* acc, float sgn) {
-    *reinterpret_cast<float4*>(dst + r * kBS + c0) = make_float4(sgn * acc[0], sgn * acc[1], sgn * acc[2], sgn * acc[3]);
-    *reinterpret_cast<float4*>(dst + r * kBS + c0 + 4) =
-        make_float4(sgn * acc[4], sgn * acc[5], sgn * acc[6], sgn * acc[7]);
-  };
-  for (int b = warp; b < 28; b += 8) {
-    int I = 1, M = b;
-    while (M >= I) { M -= I; ++I; }  // b enumerates (I, M), M < I, row by row
-    float acc[8];
-    load_row(acc, Ap + blk(I, M));
-    block_fma(acc, Mp + blk(I, I), beta + 16 * I, Ap + blk(I, M));
-    __syncwarp();
-    store_row(Ap + blk(I, M), acc, 1.f);
-  }
-  __syncthreads();
-  for (int d = 1; d < 8; ++d) {
-    if (warp < 8 - d) {
-      const int J = warp, I = J + d;
-      float acc[8];
-      load_row(acc, Ap + blk(I, J));
-      for (int M = J; M < I; ++M) block_fma(acc, Ap + blk(I, M), beta + 16 * M, Mp + blk(M, J));
-      store_row(Mp + blk(I, J), acc, -1.f);
-    }
-    __syncthreads();
-  }
+// The 8 x 8 diagonal blocks by forward substitution (a column per thread), then
+// four doublings: with both halves' M11 and M22 known,
+//   Z = A21 + M22 diag(beta) A21,   M21 = -(Z + Z diag(beta) M11),
+// every thread taking up to 4 x 4 outputs, its rows 16 apart so that all have
+// the same share of the triangle.
+//
+// Both matrices are [128][128] float32 with the 16-byte pieces of a row permuted
+// by the row, which keeps reads of consecutive rows at one column, and of
+// consecutive columns of one row, free of bank conflicts.
+constexpr uint32_t kMatB = kC * kC * 4;
+__device__ __forceinline__ int mat_at(int r, int c4) { return r * kC + ((c4 ^ ((r ^ (r >> 2)) & 7)) << 2); }
+__device__ __forceinline__ float4& mat4(float* m, int r, int c4) { return *reinterpret_cast<float4*>(m + mat_at(r, c4)); }
+__device__ __forceinline__ void fma4(float* acc, float a, const float4& b) {
+  acc[0] = fmaf(a, b.x, acc[0]);
+  acc[1] = fmaf(a, b.y, acc[1]);
+  acc[2] = fmaf(a, b.z, acc[2]);
+  acc[3] = fmaf(a, b.w, acc[3]);
 }
 
-// The running log decay of the chunk's tokens as pairs of floats, by the first
-// 128 threads (float64 scan); rows >= n add nothing.  Ends in a barrier.
-__device__ __forceinline__ void chunk_decays(const float* log_alpha, int n, float2* g, double* tot, int tid) {
-  double x = 0.0;
+// One doubling, N rows to a half; the columns of A's finished diagonal blocks hold
+// M diag(beta).  256 threads, barrier kSolveBar.
+constexpr int kSolveBar = 1;
+template <int N>
+__device__ __forceinline__ void tri_double(float* Ap, float* Mp, const float* beta, int t) {
+  constexpr int RT = N < 16 ? 1 : N / 16, ROWS = N < 16 ? N : 16, PER = ROWS * (N / 4);  // threads of a pair
+  const int u = t % PER, r0 = t / PER * 2 * N;
+  // a warp's lanes share four rows and eight column groups; its schedulers, all shares of the triangle
+  const int cg = N == 64 ? (t & 7) + 8 * (t >> 7) : u % (N / 4);
+  const int rg = N == 64 ? ((t >> 3) & 3) + 4 * ((t >> 5) & 3) : u / (N / 4);
+  const bool on = r0 < kC;
+  const int row = r0 + N + rg, c4 = (r0 >> 2) + cg;  // outputs: rows row + 16 i, columns 4 c4 ..
+  constexpr int KB = N < 16 ? 1 : N / 16, K4 = N < 16 ? N / 4 : 4;
+  float z[RT][4];
+  float4 bc;
+  if (on) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const float4 a = mat4(Ap, row + 16 * i, c4);
+      z[i][0] = a.x; z[i][1] = a.y; z[i][2] = a.z; z[i][3] = a.w;
+    }
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll 1
+      for (int k4 = 0; k4 < K4; ++k4) {
+        const int k = r0 + N + 16 * kb + 4 * k4;
+        const float4 b0 = mat4(Ap, k, c4), b1 = mat4(Ap, k + 1, c4), b2 = mat4(Ap, k + 2, c4), b3 = mat4(Ap, k + 3, c4);
+        float4 a[RT];
+#pragma unroll
+        for (int i = kb; i < RT; ++i) a[i] = mat4(Ap, row + 16 * i, k >> 2);
+#pragma unroll
+        for (int i = kb; i < RT; ++i) fma4(z[i], a[i].x, b0);
+#pragma unroll
+        for (int i = kb; i < RT; ++i) fma4(z[i], a[i].y, b1);
+#pragma unroll
+        for (int i = kb; i < RT; ++i) fma4(z[i], a[i].z, b2);
+#pragma unroll
+        for (int i = kb; i < RT; ++i) fma4(z[i], a[i].w, b3);
+      }
+    bc = *reinterpret_cast<const float4*>(beta + 4 * c4);
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+      mat4(Mp, row + 16 * i, c4) = make_float4(bc.x * z[i][0], bc.y * z[i][1], bc.z * z[i][2], bc.w * z[i][3]);
+  }
+  named_bar_sync(kSolveBar, 256);
+  if (on) {
+#pragma unroll 1
+    for (int kb = cg >> 2; kb < KB; ++kb)  // (from the block on M11's diagonal)
+#pragma unroll 1
+      for (int k4 = 0; k4 < K4; ++k4) {
+        const int k = r0 + 16 * kb + 4 * k4;
+        const float4 b0 = mat4(Mp, k, c4), b1 = mat4(Mp, k + 1, c4), b2 = mat4(Mp, k + 2, c4), b3 = mat4(Mp, k + 3, c4);
+        float4 a[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) a[i] = mat4(Mp, row + 16 * i, k >> 2);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) fma4(z[i], a[i].x, b0);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) fma4(z[i], a[i].y, b1);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) fma4(z[i], a[i].z, b2);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) fma4(z[i], a[i].w, b3);
+      }
+  }
+  named_bar_sync(kSolveBar, 256);
+  if (on) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      mat4(Mp, row + 16 * i, c4) = make_float4(-z[i][0], -z[i][1], -z[i][2], -z[i][3]);
+      if (N < 64)
+        mat4(Ap, row + 16 * i, c4) =
+            make_float4(-bc.x * z[i][0], -bc.y * z[i][1], -bc.z * z[i][2], -bc.w * z[i][3]);
+    }
+  }
+  named_bar_sync(kSolveBar, 256);
+}
+
+// 256 threads
+__device__ __forceinline__ void tri_solve(float* Ap, float* Mp, const float* beta, int t) {
+  if (t < 128) {
+    const int r0 = t & ~7, cc = t & 7;
+    float a[8][8], acc[8];
+#pragma unroll
+    for (int r = 1; r < 8; ++r)
+#pragma unroll
+      for (int v = 0; v < (r + 3) / 4; ++v) {
+        const float4 x = mat4(Ap, r0 + r, (r0 >> 2) + v);
+        a[r][4 * v] = x.x; a[r][4 * v + 1] = x.y; a[r][4 * v + 2] = x.z; a[r][4 * v + 3] = x.w;
+      }
+    __syncwarp();  // (the block's columns are this warp's: all have read it)
+    acc[0] = 0.f;
+#pragma unroll
+    for (int r = 1; r < 8; ++r) {
+      float y = 0.f;  // A[r][cc]
+#pragma unroll
+      for (int m = 0; m < r; ++m)
+        if (m == cc) y = a[r][m];
+      acc[r] = r > cc ? -y : 0.f;
+    }
+    // once row m of the column is known, it goes into the rows below
+#pragma unroll
+    for (int m = 1; m < 7; ++m) {
+      const float c = beta[r0 + m] * acc[m];  // (zero for m <= cc)
+#pragma unroll
+      for (int r = m + 1; r < 8; ++r) acc[r] = fmaf(-a[r][m], c, acc[r]);
+    }
+    const float bc = beta[r0 + cc];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const int at = mat_at(r0 + r, (r0 + cc) >> 2) + (cc & 3);
+      Mp[at] = acc[r];
+      Ap[at] = bc * acc[r];
+    }
+    if (r0 & 8)  // zeros above the diagonal of the 16 x 16 block (A has them)
+#pragma unroll
+      for (int r = 0; r < 8; ++r) Mp[mat_at(r0 - 8 + r, (r0 + cc) >> 2) + (cc & 3)] = 0.f;
+  }
+  named_bar_sync(kSolveBar, 256);
+  tri_double<8>(Ap, Mp, beta, t);
+  tri_double<16>(Ap, Mp, beta, t);
+  tri_double<32>(Ap, Mp, beta, t);
+  tri_double<64>(Ap, Mp, beta, t);
+}
+
+// The running log decay of the chunk's tokens (`la`: this thread's, the first 128
+// threads) as pairs of floats: a scan of error-free sums, since log decays of a
+// hundred tokens leave a float too few digits for their differences.  Ends in a
+// barrier.
+__device__ __forceinline__ float2 pair_add(float2 a, float2 b) {
+  const float s = a.x + b.x, t = s - a.x;
+  const float e = (a.x - (s - t)) + (b.x - t) + (a.y + b.y);
+  const float hi = s + e;
+  return make_float2(hi, e - (hi - s));
+}
+__device__ __forceinline__ void chunk_decays(float la, float2* g, float2* tot, int tid) {
+  float2 x = make_float2(la, 0.f);
   if (tid < kC) {
-    x = tid < n ? (double)gdr_log(log_alpha[tid]) : 0.0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, x, o);
-      if ((tid & 31) >= o) x += y;
+      const float2 y = make_float2(__shfl_up_sync(0xffffffffu, x.x, o), __shfl_up_sync(0xffffffffu, x.y, o));
+      if ((tid & 31) >= o) x = pair_add(x, y);
     }
     if ((tid & 31) == 31) tot[tid >> 5] = x;
   }
   __syncthreads();
   if (tid < kC) {
-    for (int w = 0; w < (tid >> 5); ++w) x += tot[w];
-    const float hi = (float)x;
-    g[tid] = make_float2(hi, (float)(x - (double)hi));
+    for (int w = 0; w < (tid >> 5); ++w) x = pair_add(x, tot[w]);
+    g[tid] = x;
   }
   __syncthreads();
 }
@@ -245,30 +321,32 @@ __device__ __forceinline__ float2 operand_scale(float amax) {
 }
 
 // A bf16 tile in shared memory becomes fp16, scaled as above by its largest
-// value; returns the inverse scale (and that value's bits).  256 threads, the
-// tile complete before; one barrier inside, none after.
-__device__ __forceinline__ float tile_to_f16(unsigned char* tile, uint32_t* red, int tid, uint32_t* bits = nullptr) {
-  unsigned char* at[8];
-  uint4 v[8];
+// value; returns the inverse scale (and that value's bits).  NT threads (`t` among
+// them, barrier `bar`), the tile complete before; one barrier inside, none after.
+template <int NT>
+__device__ __noinline__ float tile_to_f16(unsigned char* tile, uint32_t* red, int t, int bar, uint32_t* bits) {
+  constexpr int PC = kC * 16 / NT;
+  unsigned char* at[PC];
+  uint4 v[PC];
   uint32_t m = 0;
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    at[c] = tile + swz16(tid & 127, 8 * (tid >> 7) + c);
+  for (int c = 0; c < PC; ++c) {
+    at[c] = tile + swz16(t & 127, PC * (t >> 7) + c);
     v[c] = *reinterpret_cast<const uint4*>(at[c]);
     const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) m = max(m, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
   }
   m = __reduce_max_sync(0xffffffffu, m);
-  if ((tid & 31) == 0) red[tid >> 5] = m;
-  __syncthreads();
+  if ((t & 31) == 0) red[t >> 5] = m;
+  named_bar_sync(bar, NT);
 #pragma unroll
-  for (int w = 0; w < 8; ++w) m = max(m, red[w]);
+  for (int w = 0; w < NT / 32; ++w) m = max(m, red[w]);
   m <<= 16;
   if (bits) *bits = m;
   const float2 sc = operand_scale(__uint_as_float(m));
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
+  for (int c = 0; c < PC; ++c) {
     uint32_t* w = reinterpret_cast<uint32_t*>(&v[c]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -279,6 +357,80 @@ __device__ __forceinline__ float tile_to_f16(unsigned char* tile, uint32_t* red,
   }
   fence_proxy_async_shared();
   return sc.y;
+}
+
+// ---- phases of the preparation; i: the thread's row, qt: its quarter of the columns
+// rows of diag(fr) (I + diag(br) M diag(bc)) diag(fc) in two parts (bc, fc may be null)
+__device__ __noinline__ void put_inverse(unsigned char* hi, unsigned char* lo, float* Mp, int i, int qt, float fr,
+                                         float br, const float* bc, const float* fc) {
+#pragma unroll 1
+  for (int jb = 0; jb < 2; ++jb) {
+    const int J = 2 * qt + jb;
+    float t[16];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      float4 x4 = make_float4(0.f, 0.f, 0.f, 0.f), f4 = make_float4(1.f, 1.f, 1.f, 1.f);
+      if (16 * J <= i) x4 = mat4(Mp, i, 4 * J + v);
+      if (bc) f4 = *reinterpret_cast<const float4*>(bc + 16 * J + 4 * v);
+      t[4 * v] = x4.x * f4.x * br;
+      t[4 * v + 1] = x4.y * f4.y * br;
+      t[4 * v + 2] = x4.z * f4.z * br;
+      t[4 * v + 3] = x4.w * f4.w * br;
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      float4 f4 = make_float4(1.f, 1.f, 1.f, 1.f);
+      if (fc) f4 = *reinterpret_cast<const float4*>(fc + 16 * J + 4 * v);
+      const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (16 * J + 4 * v + e == i) t[4 * v + e] = 1.f;
+        t[4 * v + e] *= fr * f[e];
+      }
+    }
+    put_parts(hi, lo, swz16(i, 2 * J), t, 1.f);
+    put_parts(hi, lo, swz16(i, 2 * J + 1), t + 8, 1.f);
+  }
+}
+// an accumulator's row, times f, as [slice of 32][piece of 4][row][4] floats; returns its largest value's bits
+__device__ __noinline__ uint32_t write_rows(float* dst, uint32_t acc, int i, int qt, float f) {
+  uint32_t m = 0;
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    float x[16];
+    tmem_ld16(acc + 16 * c, x);
+    tmem_ld_wait();
+    float4* d = reinterpret_cast<float4*>(dst) + (size_t)(8 * qt + 4 * c) * kC + i;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const float4 y = make_float4(f * x[4 * v], f * x[4 * v + 1], f * x[4 * v + 2], f * x[4 * v + 3]);
+      m = max(max(m, max(__float_as_uint(fabsf(y.x)), __float_as_uint(fabsf(y.y)))),
+              max(__float_as_uint(fabsf(y.z)), __float_as_uint(fabsf(y.w))));
+      d[v * kC] = y;
+    }
+  }
+  return m;
+}
+// an accumulator's row, times f, in two parts: tiles hi and lo
+__device__ __noinline__ void write_tiles(unsigned char* hi, unsigned char* lo, uint32_t acc, int i, int qt, float f,
+                                         float scale_lo) {
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    float x[16];
+    tmem_ld16(acc + 16 * c, x);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[j] *= f;
+    put_parts(hi, lo, swz16(i, 4 * qt + 2 * c), x, scale_lo);
+    put_parts(hi, lo, swz16(i, 4 * qt + 2 * c + 1), x + 8, scale_lo);
+  }
+}
+// 16 columns j0 .. of an accumulator's row i, times f exp(g_i - g_j), zero from the column `end` on
+__device__ __forceinline__ void decayed16(float* x, uint32_t acc, const float2* gs, float2 gi, int j0, int end, float f) {
+  tmem_ld16(acc, x);
+  tmem_ld_wait();
+#pragma unroll
+  for (int j = 0; j < 16; ++j) x[j] = j0 + j < end ? f * x[j] * exp_diff(gi, gs[j0 + j]) : 0.f;
 }
 
 }  // namespace gdrtc
