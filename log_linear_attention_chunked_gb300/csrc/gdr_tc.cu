@@ -92,20 +92,21 @@ __device__ __forceinline__ void find_item(const TcParams& p, int it, int step, I
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 template <bool BWD> struct PrepSm {
-  static constexpr uint32_t kX0 = 0;                               // K; then T (high)
-  static constexpr uint32_t kX1 = kTile;                           // V (forward), Q; then T (low)
+  static constexpr uint32_t kX0 = 0;                               // K
+  static constexpr uint32_t kX1 = kTile;                           // V (forward), Q (backward)
   static constexpr uint32_t kX2 = 2 * kTile;                       // backward: V, dO
-  static constexpr uint32_t kM = (BWD ? 3 : 2) * kTile;            // M, float32
-  static constexpr uint32_t kR = kM + kMatB;                       // A, float32; then operands in two parts
+  static constexpr uint32_t kM = (BWD ? 3 : 2) * kTile;            // M, float32; then operands in two parts
+  static constexpr uint32_t kR = kM + kMatB;                       // A, float32; then likewise
   static constexpr uint32_t kTab = kR + 2 * kTile;
   static constexpr uint32_t kBars = kTab + 5 * kC * 4 + 32 + 3 * 64 + 16;
-  static constexpr uint32_t kNext = kBars + 16;
+  static constexpr uint32_t kNext = kBars + 32;
   static constexpr uint32_t kBytes = kNext + sizeof(Item);
 };
 static_assert(kMatB == 2 * kTile && PrepSm<true>::kBars % 8 == 0, "tile alignment");
 static_assert(PrepSm<true>::kBytes <= 232448, "shared memory budget of one CTA");
 
 constexpr float kScoreDown = 1.f / 256.f;  // of the scores Q K^T of scaled tiles, as operands
+constexpr float kKeysDown = 1.f / 4096.f;   // of K K^T of the scaled tile
 constexpr float kRowsDown = 1.f / 16.f;    // of P^T dO, as an operand
 
 // Persistent, one CTA per SM, an item per (chunk, head).  Thread = (row, quarter
@@ -135,10 +136,13 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
   Item* next = reinterpret_cast<Item*>(s + Sm::kNext);
   float* Ap = reinterpret_cast<float*>(s + Sm::kR);
   float* Mp = reinterpret_cast<float*>(s + Sm::kM);
+  unsigned char* M = s + Sm::kM;
   unsigned char *X0 = s + Sm::kX0, *X1 = s + Sm::kX1, *XV = s + (BWD ? Sm::kX2 : Sm::kX1), *R = s + Sm::kR;
-  const uint32_t sX0 = smem_u32(X0), sX1 = smem_u32(X1), sXV = smem_u32(XV), sR = smem_u32(R);
+  const uint32_t sX0 = smem_u32(X0), sX1 = smem_u32(X1), sXV = smem_u32(XV), sR = smem_u32(R),
+                 sM = smem_u32(M);
   if (tid == 0) {
     mbar_init(bar, 1);
+    mbar_init(bar + 2, 1);
     fence_mbar_init();
     find_item(p, blockIdx.x, gridDim.x, next);
   }
@@ -152,7 +156,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + 32 * qt;
-  uint32_t nmma = 0;
+  uint32_t nmma = 0, items_done = 0;
   auto wait_mma = [&]() {
     wait_bar(bar, nmma & 1, p.err);
     ++nmma;
@@ -182,25 +186,31 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
   };
 
   const int items = p.slots * p.seqs.H, G = p.seqs.H / p.seqs.Hk;
-  while (true) {
-    const Item me = *next;
+  float la = 0.f, bt = 0.f;  // this thread's token's, of the item that is loaded
+  auto load_keys = [&](const Item& x) {
+    load_tile(X0, p.k + x.krow0 * p.dk, x.n, p.dk, tid, kPrepThreads);
+    if (BWD) load_tile(X1, p.q + x.krow0 * p.dk, x.n, p.dk, tid, kPrepThreads);
+    la = tid < x.n ? gdr_log(p.log_alpha[x.row0 + tid]) : 0.f;
+    bt = tid < x.n ? p.beta[x.row0 + tid] : 0.f;
+  };
+  auto load_values = [&](const Item& x) { load_tile(XV, p.v + x.row0 * p.dv, x.n, p.dv, tid, kPrepThreads); };
+  Item me = *next;
+  if (me.it < items) {
+    load_keys(me);
+    load_values(me);
+    cp_async_commit();
+  }
+  while (me.it < items) {
     const int it = me.it, n = me.n;
-    if (it >= items) break;
     const int slot = it / p.seqs.H, h = it - slot * p.seqs.H, hk = h / G;
-    const size_t row0 = me.row0, krow0 = me.krow0, sh = (size_t)me.seq * p.seqs.H + h;
+    const size_t row0 = me.row0, sh = (size_t)me.seq * p.seqs.H + h;
     unsigned* am_s = p.amax_s + sh;
     Tables& tb = p.tab[it];
     unsigned char* Wg = p.W + (size_t)it * 2 * kTile;
     unsigned char* Wdg = p.Wd + (size_t)it * 2 * kTile;
-    if (tid == 0) bulk_wait_read0();  // the item before has left shared memory
-    __syncthreads();
-    load_tile(X0, p.k + krow0 * p.dk, n, p.dk, tid, kPrepThreads);
-    cp_async_commit();
-    load_tile(XV, p.v + row0 * p.dv, n, p.dv, tid, kPrepThreads);
-    if (BWD) load_tile(X1, p.q + krow0 * p.dk, n, p.dk, tid, kPrepThreads);
-    cp_async_commit();
-    if (tid < kC) bs[tid] = tid < n ? p.beta[row0 + tid] : 0.f;
-    chunk_decays(tid < n ? gdr_log(p.log_alpha[row0 + tid]) : 0.f, gs, tot, tid);
+    const float beta_i = bt;
+    const bool t_end = me.t0 + n == me.len;
+    chunk_decays(la, gs, tot, tid);
     const float2 gi = gs[i];
     if (qt == 0) {
       const float in = exp_diff(gi, make_float2(0.f, 0.f)), out = exp_diff(gs[kC - 1], gi);
@@ -212,19 +222,21 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
       if (BWD) tb.rel[i] = exp_diff(gi, gs[0]);
     }
     if (p.state_in && me.chunk == 0) raise_max(am_s, state_max(p.state_in + sh * p.dv * p.dk));
-    cp_async_wait<1>();
+    cp_async_wait<0>();
     __syncthreads();
     const float ik = tile_to_f16<kPrepThreads>(X0, red, tid, 0, nullptr);
+    // A is K K^T of the scaled tile / 4096, beta takes the difference
+    if (tid < kC) bs[tid] = beta_i * (ik * ik / kKeysDown);
     // ---- K K^T -> 0
     issue([&]() {
       mma_tile(tmem, sX0, false, sX0, false, false);
+      bulk_wait_read0();  // (what the item before staged has left)
       if (h % G == 0) {
         bulk_store(p.K16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, X0, kTile);
         bulk_commit();
       }
+      tb.ik = ik;
     });
-    if (tid == 0) tb.ik = ik;
-    cp_async_wait<0>();  // (for the barrier before the solve)
     wait_mma();
     // A_ij = (k_i . k_j) G_ij, j < i
 #pragma unroll 1
@@ -232,7 +244,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
       const int j0 = 32 * qt + 16 * c;
       if (j0 > 32 * q + 31) break;  // (warp-uniform) above the diagonal
       float x[16];
-      decayed16(x, tl + 16 * c, gs, gi, j0, i, ik * ik);
+      decayed16(x, tl + 16 * c, gs, gi, j0, i, kKeysDown);
 #pragma unroll
       for (int v = 0; v < 4; ++v)
         mat4(Ap, i, (j0 >> 2) + v) = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
@@ -276,53 +288,61 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
       }
     }
     __syncthreads();
-    const float iv = inv[0], iq = inv[1];
-    // ---- U = T' V -> 256 (and Q K^T -> 128)
-    put_inverse(R, R + kTile, Mp, i, qt, 1.f, 1.f, bs, nullptr);
+    me = *next;
+    const float iv = inv[0], iq = inv[1], bi = bs[i];
+    // ---- U = T' V -> 256 (with Q K^T -> 128), W = T' diag(exp(g)) K -> 384
+    float m[32];
+    load_m(m, Mp, i, qt);
+    __syncthreads();
+    put_inverse(R, R + kTile, m, i, qt, 1.f, 1.f, bs, nullptr);
+    put_inverse(M, M + kTile, m, i, qt, 1.f, 1.f, bs, in_s);
     issue([&]() {
       mma_tile(tmem + 256, sR + kTile, false, sXV, true, false);
       mma_tile(tmem + 256, sR, false, sXV, true, true);
-      if (BWD) {
-        mma_tile(tmem + 128, sX1, false, sX0, false, false);
-        if (h % G == 0) {
-          bulk_store(p.Q16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, X1, kTile);
-          bulk_commit();
-        }
+      umma_commit(bar + 2);
+      if (BWD) mma_tile(tmem + 128, sX1, false, sX0, false, false);
+      mma_tile(tmem + 384, sM + kTile, false, sX0, true, false);
+      mma_tile(tmem + 384, sM, false, sX0, true, true);
+      if (BWD && h % G == 0) {
+        bulk_store(p.Q16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, X1, kTile);
+        bulk_commit();
       }
     });
-    wait_mma();
-    // ---- W = T' diag(exp(g)) K -> 384
-    put_inverse(R, R + kTile, Mp, i, qt, 1.f, 1.f, bs, in_s);
-    issue([&]() {
-      mma_tile(tmem + 384, sR + kTile, false, sX0, true, false);
-      mma_tile(tmem + 384, sR, false, sX0, true, true);
-    });
-    if (BWD) {  // (V has been read)
-      load_tile(XV, p.dout + row0 * p.dv, n, p.dv, tid, kPrepThreads);
-      cp_async_commit();
-    }
-    write_rows(p.U + (size_t)it * kC * kC, tl + 256, i, qt, iv);
-    wait_mma();
+    wait_bar(bar + 2, items_done++ & 1, p.err);
+    __syncwarp();
+    tc_fence_after();
     if (!BWD) {
-      write_tiles(Wg, Wg + kTile, tl + 384, i, qt, ik, kLoScale);
+      // U and W leave by way of the operands' places, the next item's inputs arrive meanwhile
+      write_rows(reinterpret_cast<float*>(R), tl + 256, i, qt, iv);
+      wait_mma();
+      write_tiles(M, M + kTile, tl + 384, i, qt, ik, kLoScale);
+      if (tid == 0) bulk_wait_read0();  // K16
+      fence_proxy_async_shared();
+      tc_fence_before();
+      __syncthreads();
+      if (tid == 0) {
+        bulk_store(p.U + (size_t)it * kC * kC, R, kMatB);
+        bulk_store(Wg, M, 2 * kTile);
+        bulk_commit();
+      }
+      __syncwarp();
+      if (me.it < items) {
+        load_keys(me);
+        load_values(me);
+        cp_async_commit();
+      }
     } else {
-      const float bi = bs[i];
+      load_tile(XV, p.dout + row0 * p.dv, n, p.dv, tid, kPrepThreads);  // (V has been read)
+      cp_async_commit();
+      write_rows(p.U + (size_t)it * kC * kC, tl + 256, i, qt, iv);
+      const float rel = exp_diff(gi, gs[0]), in0 = in_s[0];
+      // ---- Wd = T^T diag(exp(g_C - g)) K -> 0, Bc = Q^T diag(exp(g)) dO -> 256 (exp(g_0) and its scales below)
+      put_inverse(R, R + kTile, m, i, qt, out_s[i], bi, nullptr, nullptr);
       cp_async_wait<0>();
+      wait_mma();
       __syncthreads();
       const float id = tile_to_f16<kPrepThreads>(XV, red, tid, 0, nullptr);
-      if (tid == 0) tb.id = id;
-      // ---- Wd = T^T diag(exp(g_C - g)) K -> 256
-      put_inverse(R, R + kTile, Mp, i, qt, out_s[i], bi, nullptr, nullptr);
-      issue([&]() {
-        mma_tile(tmem + 256, sR + kTile, true, sX0, true, false);
-        mma_tile(tmem + 256, sR, true, sX0, true, true);
-        bulk_store(p.dO16 + (size_t)it * kTile, XV, kTile);
-        bulk_commit();
-      });
-      write_tiles(Wg, Wg + kTile, tl + 384, i, qt, ik, kLoScale);
-      wait_mma();
-      // ---- Bc = Q^T diag(exp(g)) dO -> 384, exp(g_0) and its scales below
-      const float rel = exp_diff(gi, gs[0]);
+      __syncthreads();
 #pragma unroll 1
       for (int c8 = 0; c8 < 4; ++c8) {
         const uint32_t at = swz16(i, 4 * qt + c8);
@@ -335,15 +355,21 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
           x[2 * e] = rel * f.x;
           x[2 * e + 1] = rel * f.y;
         }
-        put_parts(R, R + kTile, at, x, 1.f);
+        put_parts(M, M + kTile, at, x, 1.f);
       }
       issue([&]() {
-        mma_tile(tmem + 384, sX1, true, sR + kTile, true, false);
-        mma_tile(tmem + 384, sX1, true, sR, true, true);
+        mma_tile(tmem, sR + kTile, true, sX0, true, false);
+        mma_tile(tmem, sR, true, sX0, true, true);
+        mma_tile(tmem + 256, sX1, true, sM + kTile, true, false);
+        mma_tile(tmem + 256, sX1, true, sM, true, true);
+        bulk_store(p.dO16 + (size_t)it * kTile, XV, kTile);
+        bulk_commit();
+        tb.id = id;
       });
-      write_tiles(Wdg, Wdg + kTile, tl + 256, i, qt, ik, kLoScale);
+      write_tiles(Wg, Wg + kTile, tl + 384, i, qt, ik, kLoScale);
+      if (tid == 0) bulk_wait_read0();  // K16, Q16, dO16
       wait_mma();
-      // ---- P^T dO -> 0
+      // ---- P^T dO -> 384
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
         float x[16];
@@ -353,26 +379,34 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
         put_parts(R, R + kTile, swz16(i, (j0 >> 3) + 1), x + 8, 1.f);
       }
       issue([&]() {
-        mma_tile(tmem, sR + kTile, true, sXV, true, false);
-        mma_tile(tmem, sR, true, sXV, true, true);
-        bulk_wait_read0();  // K16 and Q16 have left (their place is taken next)
+        mma_tile(tmem + 384, sR + kTile, true, sXV, true, false);
+        mma_tile(tmem + 384, sR, true, sXV, true, true);
       });
-      uint32_t m = write_rows(p.Bc + (size_t)it * kC * kC, tl + 384, i, qt, p.scale * iq * id * in_s[0]);
-      if (p.dstate_out && me.t0 + n == me.len) m = max(m, state_max(p.dstate_out + sh * p.dv * p.dk));
+      const bool last = p.dstate_out && t_end;
+      if (me.it < items) {  // K and Q have been read
+        load_keys(me);
+        cp_async_commit();
+      }
+      write_tiles(Wdg, Wdg + kTile, tl, i, qt, ik, kLoScale);
       wait_mma();
-      __syncthreads();
-      // ---- w0 = T^T (P^T dO) -> 128
-      write_tiles(R, R + kTile, tl, i, qt, kRowsDown, 1.f);
-      put_inverse(X0, X1, Mp, i, qt, 1.f, bi, nullptr, nullptr);
+      // ---- w0 = T^T (P^T dO) -> 0
+      put_inverse(R, R + kTile, m, i, qt, 1.f, bi, nullptr, nullptr);
+      write_tiles(M, M + kTile, tl + 384, i, qt, kRowsDown, 1.f);
       issue([&]() {
-        mma_tile(tmem + 128, sX1, true, sR, true, false);
-        mma_tile(tmem + 128, sX0, true, sR + kTile, true, true);
-        mma_tile(tmem + 128, sX0, true, sR, true, true);
+        mma_tile(tmem, sR + kTile, true, sM, true, false);
+        mma_tile(tmem, sR, true, sM + kTile, true, true);
+        mma_tile(tmem, sR, true, sM, true, true);
       });
+      if (me.it < items) {
+        load_values(me);
+        cp_async_commit();
+      }
+      uint32_t mx = write_rows(p.Bc + (size_t)it * kC * kC, tl + 256, i, qt, p.scale * iq * id * in0);
+      if (last) mx = max(mx, state_max(p.dstate_out + sh * p.dv * p.dk));
       wait_mma();
-      m = max(m, write_rows(p.w0 + (size_t)it * kC * kC, tl + 128, i, qt,
-                            p.scale * iq * ik * id / (kScoreDown * kRowsDown)));
-      raise_max(p.amax_d + sh, m);
+      mx = max(mx, write_rows(p.w0 + (size_t)it * kC * kC, tl, i, qt,
+                              p.scale * iq * ik * id / (kScoreDown * kRowsDown)));
+      raise_max(p.amax_d + sh, mx);
     }
     tc_fence_before();  // (for the next item's products, behind its barriers)
   }

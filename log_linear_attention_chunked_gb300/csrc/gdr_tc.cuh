@@ -139,11 +139,16 @@ __device__ __forceinline__ void put_parts(unsigned char* hi, unsigned char* lo, 
 // of a 128-token chunk, M solves (I + A diag(beta)) M = -A, so that both inverses
 // are unit triangular and exact for any beta, zero and tiny ones included:
 //   (I + A diag(beta))^-1 = I + M diag(beta),  (I + diag(beta) A)^-1 = I + diag(beta) M.
-// The 8 x 8 diagonal blocks by forward substitution (a column per thread), then
-// four doublings: with both halves' M11 and M22 known,
-//   Z = A21 + M22 diag(beta) A21,   M21 = -(Z + Z diag(beta) M11),
-// every thread taking up to 4 x 4 outputs, its rows 16 apart so that all have
-// the same share of the triangle.
+// (beta here carries the inverse of a scale that A is given.)  The 8 x 8 diagonal
+// blocks by forward substitution (a column per thread), then four doublings: with
+// both halves' M11 and M22 known,
+//   Z = A21 + [M22 diag(beta)] A21,   M21 = -(Z + [Z diag(beta)] M11).
+// From 16 rows on these are products of 16-row blocks on the warp-level matrix
+// instruction, a 16 x (N / 2) piece to a warp, with both operands in two fp16 parts
+// made in registers.  Measured per chunk on one GB300: 2 x 4 thousand cycles for the
+// last doubling in float32 FMAs with 4 x 4 outputs a thread (16-byte reads of
+// shared memory, four cycles each, bound them), and a tcgen05 round costs one
+// more pass of operands through shared memory and back from tensor memory.
 //
 // Both matrices are [128][128] float32 with the 16-byte pieces of a row permuted
 // by the row, which keeps reads of consecutive rows at one column, and of
@@ -151,93 +156,87 @@ __device__ __forceinline__ void put_parts(unsigned char* hi, unsigned char* lo, 
 constexpr uint32_t kMatB = kC * kC * 4;
 __device__ __forceinline__ int mat_at(int r, int c4) { return r * kC + ((c4 ^ ((r ^ (r >> 2)) & 7)) << 2); }
 __device__ __forceinline__ float4& mat4(float* m, int r, int c4) { return *reinterpret_cast<float4*>(m + mat_at(r, c4)); }
-__device__ __forceinline__ void fma4(float* acc, float a, const float4& b) {
-  acc[0] = fmaf(a, b.x, acc[0]);
-  acc[1] = fmaf(a, b.y, acc[1]);
-  acc[2] = fmaf(a, b.z, acc[2]);
-  acc[3] = fmaf(a, b.w, acc[3]);
+__device__ __forceinline__ float2& mat2(float* m, int r, int c) {
+  return *reinterpret_cast<float2*>(m + mat_at(r, c >> 2) + (c & 3));
+}
+__device__ __forceinline__ float mat1(const float* m, int r, int c) { return m[mat_at(r, c >> 2) + (c & 3)]; }
+
+// d += a b, 16 x 8 x 16 fp16
+__device__ __forceinline__ void mma_16816(float* d, const uint32_t* a, const uint32_t* b) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// z[n] += X[rows r ..][k ..] Y[k ..][columns c + 8 n ..], 16 rows, K = 16, NT tiles of 8 columns
+template <int NT>
+__device__ __forceinline__ void block_mma(float (*z)[4], float* X, float* Y, int r, int k, int c, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  uint32_t ah[4], al[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 x = mat2(X, r + g + 8 * (e & 1), k + 2 * t + 8 * (e >> 1));
+    float x0 = x.x, x1 = x.y;
+    ah[e] = take_f16x2(x0, x1, 1.f);
+    al[e] = pack_f16x2(x0, x1);
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    uint32_t bh[2], bl[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float y0 = mat1(Y, k + 2 * t + 8 * e, c + 8 * n + g), y1 = mat1(Y, k + 2 * t + 8 * e + 1, c + 8 * n + g);
+      bh[e] = take_f16x2(y0, y1, 1.f);
+      bl[e] = pack_f16x2(y0, y1);
+    }
+    mma_16816(z[n], al, bh);
+    mma_16816(z[n], ah, bl);
+    mma_16816(z[n], ah, bh);
+  }
 }
 
-// One doubling, N rows to a half; the columns of A's finished diagonal blocks hold
-// M diag(beta).  256 threads, barrier kSolveBar.
+// One doubling, N >= 16 rows to a half; the places of A's finished blocks hold
+// M diag(beta).  Eight warps, barrier kSolveBar: pair, 16-row block and half of
+// the columns to each.
 constexpr int kSolveBar = 1;
 template <int N>
-__device__ __forceinline__ void tri_double(float* Ap, float* Mp, const float* beta, int t) {
-  constexpr int RT = N < 16 ? 1 : N / 16, ROWS = N < 16 ? N : 16, PER = ROWS * (N / 4);  // threads of a pair
-  const int u = t % PER, r0 = t / PER * 2 * N;
-  // a warp's lanes share four rows and eight column groups; its schedulers, all shares of the triangle
-  const int cg = N == 64 ? (t & 7) + 8 * (t >> 7) : u % (N / 4);
-  const int rg = N == 64 ? ((t >> 3) & 3) + 4 * ((t >> 5) & 3) : u / (N / 4);
-  const bool on = r0 < kC;
-  const int row = r0 + N + rg, c4 = (r0 >> 2) + cg;  // outputs: rows row + 16 i, columns 4 c4 ..
-  constexpr int KB = N < 16 ? 1 : N / 16, K4 = N < 16 ? N / 4 : 4;
-  float z[RT][4];
-  float4 bc;
-  if (on) {
+__device__ __noinline__ void tri_double(float* Ap, float* Mp, const float* beta, int warp, int lane) {
+  constexpr int RB = N / 16, NT = N / 16;  // row blocks; column tiles of a warp
+  const int r0 = warp / (2 * RB) * 2 * N, rb = warp / 2 % RB, c = r0 + (warp & 1) * (N / 2);
+  const int row = r0 + N + 16 * rb, g = lane >> 2, t = lane & 3;
+  float z[NT][4];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const float4 a = mat4(Ap, row + 16 * i, c4);
-      z[i][0] = a.x; z[i][1] = a.y; z[i][2] = a.z; z[i][3] = a.w;
-    }
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
+  for (int n = 0; n < NT; ++n) {
+    const float2 x = mat2(Ap, row + g, c + 8 * n + 2 * t), y = mat2(Ap, row + g + 8, c + 8 * n + 2 * t);
+    z[n][0] = x.x; z[n][1] = x.y; z[n][2] = y.x; z[n][3] = y.y;
+  }
 #pragma unroll 1
-      for (int k4 = 0; k4 < K4; ++k4) {
-        const int k = r0 + N + 16 * kb + 4 * k4;
-        const float4 b0 = mat4(Ap, k, c4), b1 = mat4(Ap, k + 1, c4), b2 = mat4(Ap, k + 2, c4), b3 = mat4(Ap, k + 3, c4);
-        float4 a[RT];
+  for (int kb = 0; kb <= rb; ++kb) block_mma<NT>(z, Ap, Ap, row, r0 + N + 16 * kb, c, lane);
 #pragma unroll
-        for (int i = kb; i < RT; ++i) a[i] = mat4(Ap, row + 16 * i, k >> 2);
-#pragma unroll
-        for (int i = kb; i < RT; ++i) fma4(z[i], a[i].x, b0);
-#pragma unroll
-        for (int i = kb; i < RT; ++i) fma4(z[i], a[i].y, b1);
-#pragma unroll
-        for (int i = kb; i < RT; ++i) fma4(z[i], a[i].z, b2);
-#pragma unroll
-        for (int i = kb; i < RT; ++i) fma4(z[i], a[i].w, b3);
-      }
-    bc = *reinterpret_cast<const float4*>(beta + 4 * c4);
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-      mat4(Mp, row + 16 * i, c4) = make_float4(bc.x * z[i][0], bc.y * z[i][1], bc.z * z[i][2], bc.w * z[i][3]);
+  for (int n = 0; n < NT; ++n) {
+    const float2 bt = *reinterpret_cast<const float2*>(beta + c + 8 * n + 2 * t);
+    mat2(Mp, row + g, c + 8 * n + 2 * t) = make_float2(bt.x * z[n][0], bt.y * z[n][1]);
+    mat2(Mp, row + g + 8, c + 8 * n + 2 * t) = make_float2(bt.x * z[n][2], bt.y * z[n][3]);
   }
   named_bar_sync(kSolveBar, 256);
-  if (on) {
 #pragma unroll 1
-    for (int kb = cg >> 2; kb < KB; ++kb)  // (from the block on M11's diagonal)
-#pragma unroll 1
-      for (int k4 = 0; k4 < K4; ++k4) {
-        const int k = r0 + 16 * kb + 4 * k4;
-        const float4 b0 = mat4(Mp, k, c4), b1 = mat4(Mp, k + 1, c4), b2 = mat4(Mp, k + 2, c4), b3 = mat4(Mp, k + 3, c4);
-        float4 a[RT];
-#pragma unroll
-        for (int i = 0; i < RT; ++i) a[i] = mat4(Mp, row + 16 * i, k >> 2);
-#pragma unroll
-        for (int i = 0; i < RT; ++i) fma4(z[i], a[i].x, b0);
-#pragma unroll
-        for (int i = 0; i < RT; ++i) fma4(z[i], a[i].y, b1);
-#pragma unroll
-        for (int i = 0; i < RT; ++i) fma4(z[i], a[i].z, b2);
-#pragma unroll
-        for (int i = 0; i < RT; ++i) fma4(z[i], a[i].w, b3);
-      }
-  }
+  for (int kb = (c - r0) / 16; kb < RB; ++kb) block_mma<NT>(z, Mp, Mp, row, r0 + 16 * kb, c, lane);
   named_bar_sync(kSolveBar, 256);
-  if (on) {
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      mat4(Mp, row + 16 * i, c4) = make_float4(-z[i][0], -z[i][1], -z[i][2], -z[i][3]);
-      if (N < 64)
-        mat4(Ap, row + 16 * i, c4) =
-            make_float4(-bc.x * z[i][0], -bc.y * z[i][1], -bc.z * z[i][2], -bc.w * z[i][3]);
+  for (int n = 0; n < NT; ++n) {
+    const int cc = c + 8 * n + 2 * t;
+    mat2(Mp, row + g, cc) = make_float2(-z[n][0], -z[n][1]);
+    mat2(Mp, row + g + 8, cc) = make_float2(-z[n][2], -z[n][3]);
+    if (N < 64) {
+      const float2 bt = *reinterpret_cast<const float2*>(beta + cc);
+      mat2(Ap, row + g, cc) = make_float2(-bt.x * z[n][0], -bt.y * z[n][1]);
+      mat2(Ap, row + g + 8, cc) = make_float2(-bt.x * z[n][2], -bt.y * z[n][3]);
     }
   }
   named_bar_sync(kSolveBar, 256);
 }
 
 // 256 threads
-__device__ __forceinline__ void tri_solve(float* Ap, float* Mp, const float* beta, int t) {
+__device__ __noinline__ void tri_solve(float* Ap, float* Mp, const float* beta, int t) {
   if (t < 128) {
     const int r0 = t & ~7, cc = t & 7;
     float a[8][8], acc[8];
@@ -248,16 +247,13 @@ __device__ __forceinline__ void tri_solve(float* Ap, float* Mp, const float* bet
         const float4 x = mat4(Ap, r0 + r, (r0 >> 2) + v);
         a[r][4 * v] = x.x; a[r][4 * v + 1] = x.y; a[r][4 * v + 2] = x.z; a[r][4 * v + 3] = x.w;
       }
-    __syncwarp();  // (the block's columns are this warp's: all have read it)
     acc[0] = 0.f;
 #pragma unroll
     for (int r = 1; r < 8; ++r) {
-      float y = 0.f;  // A[r][cc]
-#pragma unroll
-      for (int m = 0; m < r; ++m)
-        if (m == cc) y = a[r][m];
+      const float y = mat1(Ap, r0 + r, r0 + cc);
       acc[r] = r > cc ? -y : 0.f;
     }
+    __syncwarp();  // (the block's columns are this warp's: all have read it)
     // once row m of the column is known, it goes into the rows below
 #pragma unroll
     for (int m = 1; m < 7; ++m) {
@@ -275,12 +271,41 @@ __device__ __forceinline__ void tri_solve(float* Ap, float* Mp, const float* bet
     if (r0 & 8)  // zeros above the diagonal of the 16 x 16 block (A has them)
 #pragma unroll
       for (int r = 0; r < 8; ++r) Mp[mat_at(r0 - 8 + r, (r0 + cc) >> 2) + (cc & 3)] = 0.f;
+  } else {  // and of the 32 x 32 blocks: the last doubling's column halves begin with both
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      mat4(Mp, 32 * ((t - 128) >> 5) + (t & 15), 8 * ((t - 128) >> 5) + 4 + ((t >> 4) & 1) + 2 * e) =
+          make_float4(0.f, 0.f, 0.f, 0.f);
   }
   named_bar_sync(kSolveBar, 256);
-  tri_double<8>(Ap, Mp, beta, t);
-  tri_double<16>(Ap, Mp, beta, t);
-  tri_double<32>(Ap, Mp, beta, t);
-  tri_double<64>(Ap, Mp, beta, t);
+  {  // 8 x 8: a pair to a warp, two outputs to a thread
+    const int r0 = 16 * (t >> 5), row = r0 + 8 + ((t >> 2) & 7), c = r0 + 2 * (t & 3);
+    float2 z = mat2(Ap, row, c);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float a = mat1(Ap, row, r0 + 8 + k);
+      const float2 b = mat2(Ap, r0 + 8 + k, c);
+      z.x = fmaf(a, b.x, z.x);
+      z.y = fmaf(a, b.y, z.y);
+    }
+    const float2 bt = *reinterpret_cast<const float2*>(beta + c);
+    mat2(Mp, row, c) = make_float2(bt.x * z.x, bt.y * z.y);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float a = mat1(Mp, row, r0 + k);
+      const float2 b = mat2(Mp, r0 + k, c);
+      z.x = fmaf(a, b.x, z.x);
+      z.y = fmaf(a, b.y, z.y);
+    }
+    __syncwarp();
+    mat2(Mp, row, c) = make_float2(-z.x, -z.y);
+    mat2(Ap, row, c) = make_float2(-bt.x * z.x, -bt.y * z.y);
+  }
+  named_bar_sync(kSolveBar, 256);
+  tri_double<16>(Ap, Mp, beta, t >> 5, t & 31);
+  tri_double<32>(Ap, Mp, beta, t >> 5, t & 31);
+  tri_double<64>(Ap, Mp, beta, t >> 5, t & 31);
 }
 
 // The running log decay of the chunk's tokens (`la`: this thread's, the first 128
@@ -360,36 +385,35 @@ __device__ __noinline__ float tile_to_f16(unsigned char* tile, uint32_t* red, in
 }
 
 // ---- phases of the preparation; i: the thread's row, qt: its quarter of the columns
+// M's row i, 32 columns (zero above the block on the diagonal)
+__device__ __forceinline__ void load_m(float* m, float* Mp, int i, int qt) {
+#pragma unroll
+  for (int v = 0; v < 8; ++v) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (32 * qt + 4 * v <= (i | 15)) x = mat4(Mp, i, 8 * qt + v);
+    m[4 * v] = x.x;
+    m[4 * v + 1] = x.y;
+    m[4 * v + 2] = x.z;
+    m[4 * v + 3] = x.w;
+  }
+}
 // rows of diag(fr) (I + diag(br) M diag(bc)) diag(fc) in two parts (bc, fc may be null)
-__device__ __noinline__ void put_inverse(unsigned char* hi, unsigned char* lo, float* Mp, int i, int qt, float fr,
-                                         float br, const float* bc, const float* fc) {
-#pragma unroll 1
-  for (int jb = 0; jb < 2; ++jb) {
-    const int J = 2 * qt + jb;
-    float t[16];
+__device__ __forceinline__ void put_inverse(unsigned char* hi, unsigned char* lo, const float* m, int i, int qt,
+                                            float fr, float br, const float* bc, const float* fc) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      float4 x4 = make_float4(0.f, 0.f, 0.f, 0.f), f4 = make_float4(1.f, 1.f, 1.f, 1.f);
-      if (16 * J <= i) x4 = mat4(Mp, i, 4 * J + v);
-      if (bc) f4 = *reinterpret_cast<const float4*>(bc + 16 * J + 4 * v);
-      t[4 * v] = x4.x * f4.x * br;
-      t[4 * v + 1] = x4.y * f4.y * br;
-      t[4 * v + 2] = x4.z * f4.z * br;
-      t[4 * v + 3] = x4.w * f4.w * br;
+  for (int c = 0; c < 4; ++c) {
+    float x[8];
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const int j = 32 * qt + 8 * c + 4 * v;
+      float4 b4 = make_float4(br, br, br, br), f4 = make_float4(fr, fr, fr, fr);
+      if (bc) b4 = *reinterpret_cast<const float4*>(bc + j);
+      if (fc) f4 = *reinterpret_cast<const float4*>(fc + j);
+      const float b[4] = {b4.x, b4.y, b4.z, b4.w}, f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[4 * v + e] = (j + e == i ? 1.f : b[e] * m[8 * c + 4 * v + e]) * f[e];
     }
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      float4 f4 = make_float4(1.f, 1.f, 1.f, 1.f);
-      if (fc) f4 = *reinterpret_cast<const float4*>(fc + 16 * J + 4 * v);
-      const float f[4] = {f4.x, f4.y, f4.z, f4.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (16 * J + 4 * v + e == i) t[4 * v + e] = 1.f;
-        t[4 * v + e] *= fr * f[e];
-      }
-    }
-    put_parts(hi, lo, swz16(i, 2 * J), t, 1.f);
-    put_parts(hi, lo, swz16(i, 2 * J + 1), t + 8, 1.f);
+    put_parts(hi, lo, swz16(i, 4 * qt + c), x, 1.f);
   }
 }
 // an accumulator's row, times f, as [slice of 32][piece of 4][row][4] floats; returns its largest value's bits
