@@ -71,7 +71,7 @@ struct Item {
   size_t row0, krow0;
 };
 // the first item at or after `it`, `step` apart, that a chunk owns
-__device__ __forceinline__ void find_item(const TcParams& p, int it, int step, Item* out) {
+__device__ __noinline__ void find_item(const TcParams& p, int it, int step, Item* out) {
   const int items = p.slots * p.seqs.H;
   for (; it < items; it += step) {
     const int slot = it / p.seqs.H, h = it - slot * p.seqs.H, hk = h / (p.seqs.H / p.seqs.Hk);
@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
   };
   auto state_max = [&](const float* x) {
     uint32_t m = 0;
+#pragma unroll 4
     for (int e = tid; e < p.dv * p.dk; e += kPrepThreads) m = max(m, __float_as_uint(fabsf(x[e])));
     return m;
   };
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
     if (tid < kC) bs[tid] = beta_i * (ik * ik / kKeysDown);
     // ---- K K^T -> 0
     issue([&]() {
-      mma_tile(tmem, sX0, false, sX0, false, false);
+      mma_tile<false, false>(tmem, sX0, sX0, false);
       bulk_wait_read0();  // (what the item before staged has left)
       if (h % G == 0) {
         bulk_store(p.K16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, X0, kTile);
@@ -294,15 +295,14 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
     float m[32];
     load_m(m, Mp, i, qt);
     __syncthreads();
-    put_inverse(R, R + kTile, m, i, qt, 1.f, 1.f, bs, nullptr);
-    put_inverse(M, M + kTile, m, i, qt, 1.f, 1.f, bs, in_s);
+    put_inverse2(R, M, m, i, qt, bs, in_s);
     issue([&]() {
-      mma_tile(tmem + 256, sR + kTile, false, sXV, true, false);
-      mma_tile(tmem + 256, sR, false, sXV, true, true);
+      mma_tile<false, true>(tmem + 256, sR + kTile, sXV, false);
+      mma_tile<false, true>(tmem + 256, sR, sXV, true);
       umma_commit(bar + 2);
-      if (BWD) mma_tile(tmem + 128, sX1, false, sX0, false, false);
-      mma_tile(tmem + 384, sM + kTile, false, sX0, true, false);
-      mma_tile(tmem + 384, sM, false, sX0, true, true);
+      if (BWD) mma_tile<false, false>(tmem + 128, sX1, sX0, false);
+      mma_tile<false, true>(tmem + 384, sM + kTile, sX0, false);
+      mma_tile<false, true>(tmem + 384, sM, sX0, true);
       if (BWD && h % G == 0) {
         bulk_store(p.Q16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, X1, kTile);
         bulk_commit();
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
       write_rows(p.U + (size_t)it * kC * kC, tl + 256, i, qt, iv);
       const float rel = exp_diff(gi, gs[0]), in0 = in_s[0];
       // ---- Wd = T^T diag(exp(g_C - g)) K -> 0, Bc = Q^T diag(exp(g)) dO -> 256 (exp(g_0) and its scales below)
-      put_inverse(R, R + kTile, m, i, qt, out_s[i], bi, nullptr, nullptr);
+      put_inverse(R, R + kTile, m, i, qt, out_s[i], bi);
       cp_async_wait<0>();
       wait_mma();
       __syncthreads();
@@ -358,10 +358,10 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
         put_parts(M, M + kTile, at, x, 1.f);
       }
       issue([&]() {
-        mma_tile(tmem, sR + kTile, true, sX0, true, false);
-        mma_tile(tmem, sR, true, sX0, true, true);
-        mma_tile(tmem + 256, sX1, true, sM + kTile, true, false);
-        mma_tile(tmem + 256, sX1, true, sM, true, true);
+        mma_tile<true, true>(tmem, sR + kTile, sX0, false);
+        mma_tile<true, true>(tmem, sR, sX0, true);
+        mma_tile<true, true>(tmem + 256, sX1, sM + kTile, false);
+        mma_tile<true, true>(tmem + 256, sX1, sM, true);
         bulk_store(p.dO16 + (size_t)it * kTile, XV, kTile);
         bulk_commit();
         tb.id = id;
@@ -379,8 +379,8 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
         put_parts(R, R + kTile, swz16(i, (j0 >> 3) + 1), x + 8, 1.f);
       }
       issue([&]() {
-        mma_tile(tmem + 384, sR + kTile, true, sXV, true, false);
-        mma_tile(tmem + 384, sR, true, sXV, true, true);
+        mma_tile<true, true>(tmem + 384, sR + kTile, sXV, false);
+        mma_tile<true, true>(tmem + 384, sR, sXV, true);
       });
       const bool last = p.dstate_out && t_end;
       if (me.it < items) {  // K and Q have been read
@@ -390,12 +390,12 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
       write_tiles(Wdg, Wdg + kTile, tl, i, qt, ik, kLoScale);
       wait_mma();
       // ---- w0 = T^T (P^T dO) -> 0
-      put_inverse(R, R + kTile, m, i, qt, 1.f, bi, nullptr, nullptr);
+      put_inverse(R, R + kTile, m, i, qt, 1.f, bi);
       write_tiles(M, M + kTile, tl + 384, i, qt, kRowsDown, 1.f);
       issue([&]() {
-        mma_tile(tmem, sR + kTile, true, sM, true, false);
-        mma_tile(tmem, sR, true, sM + kTile, true, true);
-        mma_tile(tmem, sR, true, sM, true, true);
+        mma_tile<true, true>(tmem, sR + kTile, sM, false);
+        mma_tile<true, true>(tmem, sR, sM + kTile, true);
+        mma_tile<true, true>(tmem, sR, sM, true);
       });
       if (me.it < items) {
         load_values(me);
@@ -798,8 +798,8 @@ __global__ void __launch_bounds__(256, 2) gdr_out_kernel(TcParams p) {
   if (tid == 0) {
     wait_bar(bars, 0, p.err);
     tc_fence_after();
-    mma_tile(tmem, sQ, false, sK, false, false);
-    mma_tile(tmem + 128, sQ, false, sS, true, false);
+    mma_tile<false, false>(tmem, sQ, sK, false);
+    mma_tile<false, true>(tmem + 128, sQ, sS, false);
     umma_commit(bars + 1);
   }
   __syncwarp();
@@ -832,7 +832,7 @@ __global__ void __launch_bounds__(256, 2) gdr_out_kernel(TcParams p) {
   if (tid == 0) {
     wait_bar(bars, 1, p.err);
     tc_fence_after();
-    mma_tile(tmem, sK, false, sS, true, false);
+    mma_tile<false, true>(tmem, sK, sS, false);
     umma_commit(bars + 1);
   }
   __syncwarp();
@@ -948,10 +948,10 @@ __global__ void __launch_bounds__(256, 1) gdr_grad_tc_kernel(TcParams p) {
       bulk_load(slot_at(6), p.E + (it * 2 + 1) * kTile, kTile, bars + 1);
       wait_bar(bars, par, p.err);
       tc_fence_after();
-      mma_tile(tmem + 128, s0, false, s0 + 2 * kTile, false, false);
-      mma_tile(tmem + 128, s0, false, s0 + kTile, false, true);
-      mma_tile(tmem + 256, s0 + 3 * kTile, false, s0 + kTile, false, false);
-      mma_tile(tmem + 384, s0 + 4 * kTile, false, s0 + 5 * kTile, false, false);
+      mma_tile<false, false>(tmem + 128, s0, s0 + 2 * kTile, false);
+      mma_tile<false, false>(tmem + 128, s0, s0 + kTile, true);
+      mma_tile<false, false>(tmem + 256, s0 + 3 * kTile, s0 + kTile, false);
+      mma_tile<false, false>(tmem + 384, s0 + 4 * kTile, s0 + 5 * kTile, false);
       umma_commit(bars + 3);
     }
     __syncwarp();
@@ -1012,11 +1012,11 @@ __global__ void __launch_bounds__(256, 1) gdr_grad_tc_kernel(TcParams p) {
     if (tid == 0) {
       wait_bar(bars + 1, par, p.err);
       tc_fence_after();
-      mma_tile(tmem + 128, s0, false, s0 + 6 * kTile, false, false);
-      mma_tile(tmem + 128, s0, false, s0 + 4 * kTile, false, true);
-      mma_tile(tmem + 256, s0 + 3 * kTile, false, s0 + 4 * kTile, false, false);
+      mma_tile<false, false>(tmem + 128, s0, s0 + 6 * kTile, false);
+      mma_tile<false, false>(tmem + 128, s0, s0 + 4 * kTile, true);
+      mma_tile<false, false>(tmem + 256, s0 + 3 * kTile, s0 + 4 * kTile, false);
       wait_bar(bars + 2, par, p.err);
-      mma_tile(tmem + 384, s0 + kTile, false, s0 + 2 * kTile, false, false);
+      mma_tile<false, false>(tmem + 384, s0 + kTile, s0 + 2 * kTile, false);
       umma_commit(bars + 3);
     }
     __syncwarp();
@@ -1065,10 +1065,10 @@ __global__ void __launch_bounds__(256, 1) gdr_grad_tc_kernel(TcParams p) {
     __syncthreads();
     if (tid == 0) {
       tc_fence_after();
-      mma_tile(tmem + 128, s0 + 5 * kTile, false, s0 + 2 * kTile, true, false);  // R K
-      mma_tile(tmem + 256, s0 + 5 * kTile, true, s0 + kTile, true, false);       // R^T Q
-      mma_tile(tmem + 384, s0, false, s0 + 2 * kTile, true, false);              // N K
-      mma_tile(tmem + 384, s0, true, s0 + 2 * kTile, true, true);                // N^T K
+      mma_tile<false, true>(tmem + 128, s0 + 5 * kTile, s0 + 2 * kTile, false);  // R K
+      mma_tile<true, true>(tmem + 256, s0 + 5 * kTile, s0 + kTile, false);       // R^T Q
+      mma_tile<false, true>(tmem + 384, s0, s0 + 2 * kTile, false);              // N K
+      mma_tile<true, true>(tmem + 384, s0, s0 + 2 * kTile, true);                // N^T K
       umma_commit(bars + 3);
     }
     __syncwarp();

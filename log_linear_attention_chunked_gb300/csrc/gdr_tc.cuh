@@ -76,14 +76,16 @@ __host__ __device__ constexpr uint32_t idesc_f16(int N, bool a_mn, bool b_mn) {
 // because unrolled it left the instruction cache and every phase waited for its
 // own instructions (the solve below: 58 thousand cycles unrolled).
 
-// D (+)= A B over 128 x 128 x 128 fp16; x_mn: that operand's K runs along its rows
-__device__ __noinline__ void mma_tile(uint32_t d, uint32_t a, bool a_mn, uint32_t b, bool b_mn, bool add) {
-  const uint32_t id = idesc_f16(128, a_mn, b_mn);
-  const uint64_t da = a_mn ? desc_mn(a, 0) : desc_k(a, 0), db = b_mn ? desc_mn(b, 0) : desc_k(b, 0);
-#pragma unroll 1
+// D (+)= A B over 128 x 128 x 128 fp16; AM, BM: that operand's K runs along its rows.
+// (Eight instructions of about 65 cycles; a loop over them took 140 each.)
+template <bool AM, bool BM>
+__device__ __noinline__ void mma_tile(uint32_t d, uint32_t a, uint32_t b, bool add) {
+  constexpr uint32_t id = idesc_f16(128, AM, BM);
+  const uint64_t da = AM ? desc_mn(a, 0) : desc_k(a, 0), db = BM ? desc_mn(b, 0) : desc_k(b, 0);
+#pragma unroll
   for (int kk = 0; kk < 8; ++kk) {
-    const uint64_t ka = (uint64_t)((kk >> 2) * kHalf + (kk & 3) * 32) >> 4, mn = (uint64_t)kk * 128;
-    umma_bf16(d, da + (a_mn ? mn : ka), db + (b_mn ? mn : ka), id, (add || kk > 0) ? 1u : 0u);
+    const uint32_t ka = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4, mn = kk * 128;
+    umma_bf16(d, da + (AM ? mn : ka), db + (BM ? mn : ka), id, (add || kk > 0) ? 1u : 0u);
   }
 }
 
@@ -99,10 +101,11 @@ __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t 
 // rows 0 .. n - 1 of a [.., d] bf16 matrix into a tile, zeros elsewhere (by
 // all `threads` threads; rows that belong to another sequence stay out, so
 // that nothing of theirs, a NaN say, is multiplied by a zero)
-__device__ __forceinline__ void load_tile(unsigned char* tile, const __nv_bfloat16* src, int n, int d, int tid,
+__device__ __noinline__ void load_tile(unsigned char* tile, const __nv_bfloat16* src, int n, int d, int tid,
                                           int threads) {
-  for (int x = tid; x < kC * 16; x += threads) {
-    const int r = x >> 4, c8 = x & 15;
+  const int c8 = tid & 15;
+#pragma unroll 2
+  for (int r = tid >> 4; r < kC; r += threads >> 4) {
     const bool in = r < n && c8 * 8 < d;
     cp_async16_zfill(tile + swz16(r, c8), in ? src + (size_t)r * d + c8 * 8 : src, in);
   }
@@ -154,7 +157,7 @@ __device__ __forceinline__ void put_parts(unsigned char* hi, unsigned char* lo, 
 // by the row, which keeps reads of consecutive rows at one column, and of
 // consecutive columns of one row, free of bank conflicts.
 constexpr uint32_t kMatB = kC * kC * 4;
-__device__ __forceinline__ int mat_at(int r, int c4) { return r * kC + ((c4 ^ ((r ^ (r >> 2)) & 7)) << 2); }
+__device__ __forceinline__ int mat_at(int r, int c4) { return r * kC + ((c4 ^ (r & 7)) << 2); }
 __device__ __forceinline__ float4& mat4(float* m, int r, int c4) { return *reinterpret_cast<float4*>(m + mat_at(r, c4)); }
 __device__ __forceinline__ float2& mat2(float* m, int r, int c) {
   return *reinterpret_cast<float2*>(m + mat_at(r, c >> 2) + (c & 3));
@@ -163,35 +166,38 @@ __device__ __forceinline__ float mat1(const float* m, int r, int c) { return m[m
 
 // d += a b, 16 x 8 x 16 fp16
 __device__ __forceinline__ void mma_16816(float* d, const uint32_t* a, const uint32_t* b) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
-// z[n] += X[rows r ..][k ..] Y[k ..][columns c + 8 n ..], 16 rows, K = 16, NT tiles of 8 columns
+// z[n] += X Y, 16 rows, K = 16, NT tiles of 8 columns; x: this lane's row and columns
+// of X (xa: its two pieces), y[n][d]: its column of Y in row 2 t + d of the block
 template <int NT>
-__device__ __forceinline__ void block_mma(float (*z)[4], float* X, float* Y, int r, int k, int c, int lane) {
-  const int g = lane >> 2, t = lane & 3;
+__device__ __forceinline__ void block_mma(float (*z)[4], const float* x, const int* xa, const float* y,
+                                          const int (*yc)[2]) {
   uint32_t ah[4], al[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float2 x = mat2(X, r + g + 8 * (e & 1), k + 2 * t + 8 * (e >> 1));
-    float x0 = x.x, x1 = x.y;
+    const float2 v = *reinterpret_cast<const float2*>(x + xa[e >> 1] + 8 * kC * (e & 1));
+    float x0 = v.x, x1 = v.y;
     ah[e] = take_f16x2(x0, x1, 1.f);
     al[e] = pack_f16x2(x0, x1);
   }
+  uint32_t bh[NT][2], bl[NT][2];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    uint32_t bh[2], bl[2];
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float y0 = mat1(Y, k + 2 * t + 8 * e, c + 8 * n + g), y1 = mat1(Y, k + 2 * t + 8 * e + 1, c + 8 * n + g);
-      bh[e] = take_f16x2(y0, y1, 1.f);
-      bl[e] = pack_f16x2(y0, y1);
+      float y0 = y[yc[n][0] + 8 * kC * e], y1 = y[yc[n][1] + 8 * kC * e];
+      bh[n][e] = take_f16x2(y0, y1, 1.f);
+      bl[n][e] = pack_f16x2(y0, y1);
     }
-    mma_16816(z[n], al, bh);
-    mma_16816(z[n], ah, bl);
-    mma_16816(z[n], ah, bh);
-  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) mma_16816(z[n], al, bh[n]);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) mma_16816(z[n], ah, bl[n]);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) mma_16816(z[n], ah, bh[n]);
 }
 
 // One doubling, N >= 16 rows to a half; the places of A's finished blocks hold
@@ -203,6 +209,15 @@ __device__ __noinline__ void tri_double(float* Ap, float* Mp, const float* beta,
   constexpr int RB = N / 16, NT = N / 16;  // row blocks; column tiles of a warp
   const int r0 = warp / (2 * RB) * 2 * N, rb = warp / 2 % RB, c = r0 + (warp & 1) * (N / 2);
   const int row = r0 + N + 16 * rb, g = lane >> 2, t = lane & 3;
+  // (pieces are permuted by the row's low three bits, and blocks of 16 start at multiples of 4 pieces)
+  const int xa[2] = {(((t >> 1) ^ (g & 3)) << 2) + 2 * (t & 1), ((((t >> 1) + 2) ^ (g & 3)) << 2) + 2 * (t & 1)};
+  int yc[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int d = 0; d < 2; ++d)
+      yc[n][d] = (2 * t + d) * kC + ((((c >> 2) + 2 * n + (g >> 2)) ^ (2 * t + d)) << 2) + (g & 3);
+  auto x_at = [&](const float* m, int k) { return m + (row + g) * kC + (((k >> 2) ^ (g & 4)) << 2); };
   float z[NT][4];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -210,7 +225,10 @@ __device__ __noinline__ void tri_double(float* Ap, float* Mp, const float* beta,
     z[n][0] = x.x; z[n][1] = x.y; z[n][2] = y.x; z[n][3] = y.y;
   }
 #pragma unroll 1
-  for (int kb = 0; kb <= rb; ++kb) block_mma<NT>(z, Ap, Ap, row, r0 + N + 16 * kb, c, lane);
+  for (int kb = 0; kb <= rb; ++kb) {
+    const int k = r0 + N + 16 * kb;
+    block_mma<NT>(z, x_at(Ap, k), xa, Ap + k * kC, yc);
+  }
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const float2 bt = *reinterpret_cast<const float2*>(beta + c + 8 * n + 2 * t);
@@ -219,7 +237,10 @@ __device__ __noinline__ void tri_double(float* Ap, float* Mp, const float* beta,
   }
   named_bar_sync(kSolveBar, 256);
 #pragma unroll 1
-  for (int kb = (c - r0) / 16; kb < RB; ++kb) block_mma<NT>(z, Mp, Mp, row, r0 + 16 * kb, c, lane);
+  for (int kb = (c - r0) / 16; kb < RB; ++kb) {
+    const int k = r0 + 16 * kb;
+    block_mma<NT>(z, x_at(Mp, k), xa, Mp + k * kC, yc);
+  }
   named_bar_sync(kSolveBar, 256);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -351,34 +372,35 @@ __device__ __forceinline__ float2 operand_scale(float amax) {
 template <int NT>
 __device__ __noinline__ float tile_to_f16(unsigned char* tile, uint32_t* red, int t, int bar, uint32_t* bits) {
   constexpr int PC = kC * 16 / NT;
-  unsigned char* at[PC];
-  uint4 v[PC];
-  uint32_t m = 0;
+  uint32_t m2 = 0;
 #pragma unroll
   for (int c = 0; c < PC; ++c) {
-    at[c] = tile + swz16(t & 127, PC * (t >> 7) + c);
-    v[c] = *reinterpret_cast<const uint4*>(at[c]);
-    const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) m = max(m, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+    const uint4 v = *reinterpret_cast<const uint4*>(tile + swz16(t & 127, PC * (t >> 7) + c));
+    m2 = __vmaxu2(__vmaxu2(m2, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu);
+    m2 = __vmaxu2(__vmaxu2(m2, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu);
   }
-  m = __reduce_max_sync(0xffffffffu, m);
+  uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
   if ((t & 31) == 0) red[t >> 5] = m;
   named_bar_sync(bar, NT);
 #pragma unroll
-  for (int w = 0; w < NT / 32; ++w) m = max(m, red[w]);
+  for (int w = 0; w < NT / 128; ++w) {
+    const uint4 x = *reinterpret_cast<const uint4*>(red + 4 * w);
+    m = max(max(m, max(x.x, x.y)), max(x.z, x.w));
+  }
   m <<= 16;
   if (bits) *bits = m;
   const float2 sc = operand_scale(__uint_as_float(m));
-#pragma unroll
+#pragma unroll 2
   for (int c = 0; c < PC; ++c) {
-    uint32_t* w = reinterpret_cast<uint32_t*>(&v[c]);
+    uint4* at = reinterpret_cast<uint4*>(tile + swz16(t & 127, PC * (t >> 7) + c));
+    uint4 v = *at;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float2 f = unpack_bf16x2(w[e]);
       w[e] = pack_f16x2(sc.x * f.x, sc.x * f.y);
     }
-    *reinterpret_cast<uint4*>(at[c]) = v[c];
+    *at = v;
   }
   fence_proxy_async_shared();
   return sc.y;
@@ -397,22 +419,35 @@ __device__ __forceinline__ void load_m(float* m, float* Mp, int i, int qt) {
     m[4 * v + 3] = x.w;
   }
 }
-// rows of diag(fr) (I + diag(br) M diag(bc)) diag(fc) in two parts (bc, fc may be null)
-__device__ __forceinline__ void put_inverse(unsigned char* hi, unsigned char* lo, const float* m, int i, int qt,
-                                            float fr, float br, const float* bc, const float* fc) {
+// rows of I + M diag(beta) in two parts, and of that times diag(f2)
+__device__ __forceinline__ void put_inverse2(unsigned char* t1, unsigned char* t2, const float* m, int i, int qt,
+                                             const float* beta, const float* f2) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    float x[8], y[8];
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const int j = 32 * qt + 8 * c + 4 * v;
+      const float4 b4 = *reinterpret_cast<const float4*>(beta + j), f4 = *reinterpret_cast<const float4*>(f2 + j);
+      const float b[4] = {b4.x, b4.y, b4.z, b4.w}, f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[4 * v + e] = j + e == i ? 1.f : b[e] * m[8 * c + 4 * v + e];
+        y[4 * v + e] = x[4 * v + e] * f[e];
+      }
+    }
+    put_parts(t1, t1 + kTile, swz16(i, 4 * qt + c), x, 1.f);
+    put_parts(t2, t2 + kTile, swz16(i, 4 * qt + c), y, 1.f);
+  }
+}
+// rows of diag(f) (I + diag(beta) M) in two parts
+__device__ __forceinline__ void put_inverse(unsigned char* hi, unsigned char* lo, const float* m, int i, int qt, float f,
+                                            float beta) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     float x[8];
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const int j = 32 * qt + 8 * c + 4 * v;
-      float4 b4 = make_float4(br, br, br, br), f4 = make_float4(fr, fr, fr, fr);
-      if (bc) b4 = *reinterpret_cast<const float4*>(bc + j);
-      if (fc) f4 = *reinterpret_cast<const float4*>(fc + j);
-      const float b[4] = {b4.x, b4.y, b4.z, b4.w}, f[4] = {f4.x, f4.y, f4.z, f4.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[4 * v + e] = (j + e == i ? 1.f : b[e] * m[8 * c + 4 * v + e]) * f[e];
-    }
+    for (int e = 0; e < 8; ++e) x[e] = (32 * qt + 8 * c + e == i ? 1.f : beta * m[8 * c + e]) * f;
     put_parts(hi, lo, swz16(i, 4 * qt + c), x, 1.f);
   }
 }
