@@ -27,6 +27,7 @@ namespace {
 
 using namespace gdrtc;
 
+constexpr int kParts = 16, kBnd = 64;
 // per (chunk, head)
 struct Tables {
   float2 g[kC];    // running log decay
@@ -48,19 +49,19 @@ struct TcParams {
   unsigned char* W;      // two tiles, [token][d_k]
   float* U;              // [slice of 32][piece of 4][token][4]; the scan for the gradient leaves e there
   unsigned char* K16;    // per (slot, key head)
-  unsigned char* S;      // X before the chunk, scaled: [d_k][d_v] (for the gradient a high and a low tile)
-  unsigned char* E;      // u, scaled: [token][d_v] (likewise)
+  unsigned char* S;      // X before the chunk, scaled: a tile [d_k][d_v]; for the gradient slice tiles
+  unsigned char* E;      // u, scaled: a tile [token][d_v]; likewise
   Tables* tab;
   unsigned *amax_s, *amax_d;  // [sequence, head]: bits of the largest value that scales X and e, D and w
   // the gradient's
   unsigned char *Q16, *dO16;  // Q16 per (slot, key head)
   unsigned char* Wd;
   float *w0, *Bc;        // as U, Bc's rows being d_k
-  unsigned char* D;      // D behind the chunk, scaled: [d_k][d_v]
-  unsigned char* Y;      // beta w, scaled: [token][d_v]
+  unsigned char* D;      // D behind the chunk, scaled: a tile [d_k][d_v]
+  unsigned char* Y;      // beta w, scaled: a tile [token][d_v]
   float* final_state;    // [sequence, head, dv, dk]
-  float2* part;          // [8][token]: e.w and v.(beta w) over 16 columns
-  float* bnd;            // [32]: pieces of <S, D> behind the chunk
+  float2* part;          // [kParts][token]: e.w and v.(beta w) over 8 columns
+  float* bnd;            // [kBnd]: pieces of <S, D> behind the chunk
   unsigned* err;
 };
 
@@ -420,31 +421,50 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
 }
 
 // ---------------------------------------------------------------- scan
-constexpr uint32_t kSW = 0;                  // W (Wd) of two chunks, two parts each
-constexpr uint32_t kSK = kSW + 4 * kTile;    // K of two chunks
-constexpr uint32_t kSX = kSK + 2 * kTile;    // X (D): [d_k][high 32 | low 32]
-constexpr uint32_t kSE = kSX + kHalf;        // the rows: [token][high 32 | low 32]
-constexpr uint32_t kSBars = kSE + kHalf;
-constexpr uint32_t kScanSmem = kSBars + 8 * 8;
-static_assert(kScanSmem <= 232448, "shared memory budget of one CTA");
-enum ScanBar : int { SB_W0 = 0, SB_W1, SB_K0, SB_K1, SB_MMA, kScanBars };
+// Slice tiles: for each slice of 32 d_v columns a [128 rows][high 32 | low 32] block
+// of 16 KB, as a scan's operands stand in shared memory, from where the copy
+// engine takes them to the workspace.
 enum ScanMode : int { kFwd, kFwdKeep, kRev };  // the forward; the forward for the gradient; backwards
+template <int MODE> struct ScanSm {
+  static constexpr bool kLean = MODE != kFwd;                 // one W and one K, and room for staged rows
+  static constexpr uint32_t kW = 0;                           // W (Wd), two parts (of two chunks)
+  static constexpr uint32_t kK = kW + (kLean ? 2 : 4) * kTile;  // K (of two chunks)
+  static constexpr uint32_t kX = kK + (kLean ? 1 : 2) * kTile;  // X (D)
+  static constexpr uint32_t kE = kX + kHalf;                  // the rows as an operand
+  static constexpr uint32_t kRows = kE + kHalf;               // U (w0) of two chunks: [piece of 4][token][4]
+  static constexpr uint32_t kErr = kRows + 2 * kHalf;         // e, on its way out or in
+  static constexpr uint32_t kU = kErr + kHalf;                // u on its way out
+  static constexpr uint32_t kBc = kErr + kHalf;               // backwards: Bc
+  static constexpr uint32_t kSt = kBc + kHalf;                // S of the chunk behind
+  static constexpr uint32_t kBars = MODE == kFwd ? kRows : MODE == kFwdKeep ? kU + kHalf : kSt + kHalf;
+  static constexpr uint32_t kBytes = kBars + 96;
+  static_assert(kBytes <= 232448, "shared memory budget of one CTA");
+};
+enum ScanBar : int { SB_W0 = 0, SB_W1, SB_K0, SB_K1, SB_R0, SB_R1, SB_ERR, SB_BC, SB_ST, SB_MMA, kScanBars };
 
-// One CTA per (32 d_v columns, head, sequence); thread = (TMEM lane, half of the
+// One CTA per (32 d_v columns, head, sequence); thread = (TMEM lane, 8 of the
 // columns), the lane a token of the chunk or a d_k row of X in turn.  X stays
 // in float32 registers; per chunk two rounds of products, W [Xh | Xl] and
 // K^T [uh | ul] (the parts side by side as N = 64: the 128-row operand, which
-// shared memory feeds at 128 bytes a cycle, is read once for both).
+// shared memory feeds at 128 bytes a cycle, is read once for both).  The chain of
+// a chunk is what bounds it: a warp of its own issues products and copies, and
+// what does not belong to the chain is done in the products' time.  With most of
+// the SM's memory taken as shared memory, little is left for loads in flight
+// through L1 (72 KB of them a chunk took 4 thousand cycles to issue): the modes
+// with many rows have them copied into shared memory instead.
+constexpr int kScanThreads = 512 + 32;
+constexpr int kScanBarX = 1, kScanBarE = 2, kScanBarU = 3;  // named barriers: an operand, the staged rows are ready
 template <int MODE>
-__global__ void __launch_bounds__(256, 1) gdr_scan_kernel(TcParams p, int slices) {
-  constexpr bool REV = MODE == kRev;
+__global__ void __launch_bounds__(kScanThreads, 1) gdr_scan_kernel(TcParams p, int slices) {
+  constexpr bool REV = MODE == kRev, LEAN = MODE != kFwd;
+  using Sm = ScanSm<MODE>;
   extern __shared__ __align__(1024) unsigned char s[];
   if (smem_u32(s) & 1023u) {
     if (threadIdx.x == 0) atomicOr(p.err, kErrDeviceArg);
     return;
   }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int q = warp & 3, hf = warp >> 2, i = 32 * q + lane;
+  const int q = warp & 3, qt = (warp >> 2) & 3, i = 32 * q + lane;
   const int sl = blockIdx.x % slices, h = (blockIdx.x / slices) % p.seqs.H, seq = blockIdx.x / slices / p.seqs.H;
   GdrSeq sq;
   if (!gdr_seq(p.seqs, seq, sq)) {
@@ -452,38 +472,56 @@ __global__ void __launch_bounds__(256, 1) gdr_scan_kernel(TcParams p, int slices
     return;
   }
   const int hk = h / (p.seqs.H / p.seqs.Hk);
-  const int col0 = kSlice * sl + 16 * hf;  // this thread's first d_v column
-  const bool cols_in = col0 < p.dv;
+  const int col0 = kSlice * sl + 8 * qt;  // this thread's first d_v column
+  const bool cols_in = warp < 16 && col0 < p.dv;
   const int Nc = (sq.len + kC - 1) / kC;
   const int base = gdr_slot_base(p.seqs, seq, sq.start, kC);
   const size_t row0 = ((size_t)sq.row_b * p.seqs.H + h) * p.seqs.T + sq.start;
   const size_t sh = (size_t)seq * p.seqs.H + h;
   auto item = [&](int c) { return (size_t)(base + c) * p.seqs.H + h; };
   auto at_step = [&](int x) { return REV ? Nc - 1 - x : x; };  // the chunk of step x
+  auto slice_of = [&](int x) { return (item(at_step(x)) * 4 + sl) * kHalf; };  // in bytes: slice tiles, rows
 
   const float* from = REV ? p.dstate_out : p.state_in;
-  float X[16];
+  float X[8];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) X[j] = from && i < p.dk && cols_in ? from[(sh * p.dv + col0 + j) * p.dk + i] : 0.f;
+  for (int j = 0; j < 8; ++j) X[j] = from && i < p.dk && cols_in ? from[(sh * p.dv + col0 + j) * p.dk + i] : 0.f;
 
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s + kSBars);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s + kSBars + kScanBars * 8);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s + Sm::kBars);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s + Sm::kBars + kScanBars * 8);
+  auto copy_in = [&](int bar, uint32_t at, const void* src, uint32_t bytes) {
+    mbar_arrive_expect_tx(bars + bar, bytes);
+    bulk_load(s + at, src, bytes, bars + bar);
+  };
   auto load_w = [&](int x) {
-    const unsigned char* src = (REV ? p.Wd : p.W) + item(at_step(x)) * 2 * kTile;
-    mbar_arrive_expect_tx(bars + SB_W0 + (x & 1), 2 * kTile);
-    bulk_load(s + kSW + (x & 1) * 2 * kTile, src, 2 * kTile, bars + SB_W0 + (x & 1));
+    const int b = LEAN ? 0 : x & 1;
+    copy_in(SB_W0 + b, Sm::kW + b * 2 * kTile, (REV ? p.Wd : p.W) + item(at_step(x)) * 2 * kTile, 2 * kTile);
   };
   auto load_k = [&](int x) {
-    mbar_arrive_expect_tx(bars + SB_K0 + (x & 1), kTile);
-    bulk_load(s + kSK + (x & 1) * kTile, p.K16 + ((size_t)(base + at_step(x)) * p.seqs.Hk + hk) * kTile, kTile,
-              bars + SB_K0 + (x & 1));
+    const int b = LEAN ? 0 : x & 1;
+    copy_in(SB_K0 + b, Sm::kK + b * kTile, p.K16 + ((size_t)(base + at_step(x)) * p.seqs.Hk + hk) * kTile, kTile);
   };
+  auto bytes_of = [&](float* x) { return reinterpret_cast<unsigned char*>(x); };
+  auto load_rows = [&](int x) {
+    copy_in(SB_R0 + (x & 1), Sm::kRows + (x & 1) * kHalf, bytes_of(REV ? p.w0 : p.U) + slice_of(x), kHalf);
+  };
+  auto load_err = [&](int x) { copy_in(SB_ERR, Sm::kErr, bytes_of(p.U) + slice_of(x), kHalf); };
+  auto load_bc = [&](int x) { copy_in(SB_BC, Sm::kBc, bytes_of(p.Bc) + slice_of(x), kHalf); };
+  auto load_st = [&](int x) { copy_in(SB_ST, Sm::kSt, p.S + slice_of(x), kHalf); };
   if (tid == 0) {
     for (int b = 0; b < kScanBars; ++b) mbar_init(bars + b, 1);
     fence_mbar_init();
     for (int x = 0; x < 2 && x < Nc; ++x) {
-      load_w(x);
-      load_k(x);
+      if (!LEAN || x == 0) {
+        load_w(x);
+        load_k(x);
+      }
+      if (LEAN) load_rows(x);
+    }
+    if (REV && Nc) {
+      load_err(0);
+      load_bc(0);
+      if (Nc > 1) load_st(0);
     }
   }
   __syncwarp();
@@ -497,21 +535,24 @@ __global__ void __launch_bounds__(256, 1) gdr_scan_kernel(TcParams p, int slices
   const float2 sg =
       Nc ? operand_scale(__uint_as_float((REV ? p.amax_d : p.amax_s)[sh])) : make_float2(1.f, 1.f);
   const float isf = REV && Nc ? operand_scale(__uint_as_float(p.amax_s[sh])).y : 1.f;
+  auto write_bnd = [&](int c, float d) {  // a piece of <S, D> behind chunk c
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    if (lane == 0 && warp < 16) p.bnd[item(c) * kBnd + sl * 16 + warp] = d;
+  };
   if (REV && Nc) {  // <S_T, its gradient>: what the last chunk's log decays add
     float d = 0.f;
     if (p.dstate_out && i < p.dk && cols_in)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) d = fmaf(X[j], p.final_state[(sh * p.dv + col0 + j) * p.dk + i], d);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    if (lane == 0) p.bnd[item(Nc - 1) * 32 + sl * 8 + warp] = d;
+      for (int j = 0; j < 8; ++j) d = fmaf(X[j], p.final_state[(sh * p.dv + col0 + j) * p.dk + i], d);
+    write_bnd(Nc - 1, d);
   }
 #pragma unroll
-  for (int j = 0; j < 16; ++j) X[j] *= sg.x;
+  for (int j = 0; j < 8; ++j) X[j] *= sg.x;
 
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + 16 * hf;
-  const uint32_t sX = smem_u32(s + kSX), sE = smem_u32(s + kSE);
+  const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + 8 * qt;
+  const uint32_t sX = smem_u32(s + Sm::kX), sE = smem_u32(s + Sm::kE);
   constexpr uint32_t idW = idesc_f16(64, false, true), idK = idesc_f16(64, true, true);
   uint32_t nmma = 0;
   auto wait_mma = [&]() {
@@ -520,169 +561,189 @@ __global__ void __launch_bounds__(256, 1) gdr_scan_kernel(TcParams p, int slices
     __syncwarp();
     tc_fence_after();
   };
-  // 16 columns of row i as high and low parts of a [row][32 | 32] tile
-  auto put = [&](unsigned char* tile, const float* x, float f) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      float y[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = f * x[8 * c + e];
-      uint32_t w[8];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        w[e] = take_f16x2(y[2 * e], y[2 * e + 1], kLoScale);
-        w[4 + e] = pack_f16x2(y[2 * e], y[2 * e + 1]);
-      }
-      *reinterpret_cast<uint4*>(tile + swz16(i, 2 * hf + c)) = make_uint4(w[0], w[1], w[2], w[3]);
-      *reinterpret_cast<uint4*>(tile + swz16(i, 4 + 2 * hf + c)) = make_uint4(w[4], w[5], w[6], w[7]);
-    }
-  };
-  // 16 columns of row i into a workspace tile: the high part, or both in two tiles
-  auto keep = [&](unsigned char* tile, const float* x, float f, bool both) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const uint32_t at = swz16(i, (col0 >> 3) + c);
-      float y[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = f * x[8 * c + e];
-      if (both)
-        put_parts(tile, tile + kTile, at, y, 1.f);
-      else
-        *reinterpret_cast<uint4*>(tile + at) = make_uint4(pack_f16x2(y[0], y[1]), pack_f16x2(y[2], y[3]),
-                                                          pack_f16x2(y[4], y[5]), pack_f16x2(y[6], y[7]));
-    }
+  auto ready = [&](int bar) {  // this thread's part is in shared memory
+    fence_proxy_async_shared();
+    tc_fence_before();
+    named_bar_arrive(bar, kScanThreads);
   };
 
-  // what this thread needs of a chunk, loaded one step ahead
-  float4 un[4], bn[4], en[4];
-  uint4 vn[2], sn[4];
-  float fac_n = 0.f, gam_n = 0.f, beta_n = 0.f, in0_n = 0.f;
-  const size_t piece = (size_t)(sl * 8 + 4 * hf) * kC + i;
-  auto fetch = [&](int x) {
-    const int c = at_step(x);
-    const size_t it = item(c);
-    const int t = c * kC + i;
-    const float4* ug = reinterpret_cast<const float4*>(REV ? p.w0 : p.U) + it * (kC * kC / 4) + piece;
+  if (warp == 16) {  // products and copies
+    for (int x = 0; x < Nc; ++x) {
+      const int b = LEAN ? 0 : x & 1;
+      const uint32_t par = (LEAN ? x : x >> 1) & 1;
+      named_bar_sync(kScanBarX, kScanThreads);
+      if (lane == 0) {
+        if (MODE == kFwdKeep) bulk_wait_read0();  // the rows staged in the step before have left
+        wait_bar(bars + SB_W0 + b, par, p.err);
+        tc_fence_after();
+        const uint32_t w = smem_u32(s + Sm::kW + b * 2 * kTile);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) un[v] = ug[v * kC];
-    const Tables& tb = p.tab[it];
-    fac_n = (REV ? tb.rel[i] : tb.out[i]) * tb.ik;
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_bf16(tmem + 64 * part, desc_k(w + part * kTile, kk), desc_mn(sX, kk), idW, kk > 0);
+        umma_commit(bars + SB_MMA);
+        if (LEAN) {
+          if (!REV) {
+            bulk_store(p.S + slice_of(x), s + Sm::kX, kHalf);
+            bulk_commit();
+          }
+          // rows of the step before have been read
+          if (x > 0 && x + 1 < Nc) load_rows(x + 1);
+          if (REV && x > 0) {
+            load_err(x);
+            load_bc(x);
+          }
+        }
+      }
+      __syncwarp();
+      wait_mma();
+      if (lane == 0) {
+        if (LEAN ? x + 1 < Nc : x + 2 < Nc) load_w(LEAN ? x + 1 : x + 2);
+      }
+      __syncwarp();
+      named_bar_sync(kScanBarE, kScanThreads);
+      if (lane == 0) {
+        if (REV && x > 0 && x + 1 < Nc) load_st(x);  // (the one behind has been read)
+        wait_bar(bars + SB_K0 + b, par, p.err);
+        if (MODE == kFwdKeep) bulk_wait_read0();  // X has left
+        tc_fence_after();
+        const uint32_t k = smem_u32(s + Sm::kK + b * kTile);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) umma_bf16(tmem + 128, desc_mn(k, kk), desc_mn(sE, kk), idK, kk > 0);
+        umma_commit(bars + SB_MMA);
+      }
+      __syncwarp();
+      if (MODE == kFwdKeep) {
+        named_bar_sync(kScanBarU, kScanThreads);
+        if (lane == 0) {
+          bulk_store(p.E + slice_of(x), s + Sm::kU, kHalf);
+          bulk_store(bytes_of(p.U) + slice_of(x), s + Sm::kErr, kHalf);  // e in U's place
+          bulk_commit();
+        }
+        __syncwarp();
+      }
+      wait_mma();
+      if (lane == 0) {
+        if (LEAN ? x + 1 < Nc : x + 2 < Nc) load_k(LEAN ? x + 1 : x + 2);
+      }
+      __syncwarp();
+    }
+    if (lane == 0) bulk_wait0();
+    __syncthreads();
+    return;
+  }
+
+  // 8 columns of row i, times f, as high and low parts of a [row][32 | 32] tile
+  const uint32_t at_hi = swz16(i, qt), at_lo = swz16(i, 4 + qt);
+  auto put = [&](uint32_t tile, const float* x, float f, float lo) {
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = f * x[e];
+    put_parts(s + tile, s + tile + (at_lo - at_hi), at_hi, y, lo);
+  };
+  // 8 columns of row i, times f, into a workspace tile
+  auto keep = [&](unsigned char* tile, const float* x, float f) {
+    *reinterpret_cast<uint4*>(tile + swz16(i, col0 >> 3)) =
+        make_uint4(pack_f16x2(f * x[0], f * x[1]), pack_f16x2(f * x[2], f * x[3]), pack_f16x2(f * x[4], f * x[5]),
+                   pack_f16x2(f * x[6], f * x[7]));
+  };
+  const uint32_t piece = (uint32_t)(2 * qt * kC + i) * 16;  // of a slice's rows, the next one 16 kC on
+  auto rows8 = [&](const unsigned char* rows, float* x, float f) {
+    const float4 a = *reinterpret_cast<const float4*>(rows + piece);
+    const float4 b = *reinterpret_cast<const float4*>(rows + piece + 16 * kC);
+    x[0] = f * a.x; x[1] = f * a.y; x[2] = f * a.z; x[3] = f * a.w;
+    x[4] = f * b.x; x[5] = f * b.y; x[6] = f * b.z; x[7] = f * b.w;
+  };
+
+  // what this thread loads of a chunk itself, one step ahead
+  float4 un[2];
+  uint4 vn = make_uint4(0u, 0u, 0u, 0u);
+  float fac_n = 0.f, ik_n = 0.f, gam_n = 0.f, beta_n = 0.f, in0_n = 0.f;
+  auto fetch = [&](int x) {
+    const int c = at_step(x), t = c * kC + i;
+    if (!LEAN) {
+      const unsigned char* ug = bytes_of(p.U) + slice_of(x) + piece;
+      un[0] = *reinterpret_cast<const float4*>(ug);
+      un[1] = *reinterpret_cast<const float4*>(ug + 16 * kC);
+    }
+    const Tables& tb = p.tab[item(c)];
+    fac_n = REV ? tb.rel[i] : tb.out[i];
+    ik_n = tb.ik;
     if (REV) in0_n = tb.into[0];
     gam_n = tb.into[kC - 1];
     beta_n = t < sq.len ? p.beta[row0 + t] : 0.f;
-    if (REV) {
-      const float4* bg = reinterpret_cast<const float4*>(p.Bc) + it * (kC * kC / 4) + piece;
-      const float4* eg = reinterpret_cast<const float4*>(p.U) + it * (kC * kC / 4) + piece;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        bn[v] = bg[v * kC];
-        en[v] = eg[v * kC];
-      }
-      vn[0] = vn[1] = make_uint4(0u, 0u, 0u, 0u);
-      if (t < sq.len && cols_in) {
-        const uint4* vg = reinterpret_cast<const uint4*>(p.v + (row0 + t) * p.dv + col0);
-        vn[0] = vg[0];
-        vn[1] = vg[1];
-      }
-#pragma unroll
-      for (int part = 0; part < 2; ++part)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          sn[2 * part + e] =
-              *reinterpret_cast<const uint4*>(p.S + (it * 2 + part) * kTile + swz16(i, (col0 >> 3) + e));
-    }
+    if (REV) vn = t < sq.len && cols_in ? *reinterpret_cast<const uint4*>(p.v + (row0 + t) * p.dv + col0)
+                                        : make_uint4(0u, 0u, 0u, 0u);
   };
   if (Nc) fetch(0);
   for (int x = 0; x < Nc; ++x) {
-    const int b = x & 1, c = at_step(x);
+    const int c = at_step(x);
     const size_t it = item(c);
     // ---- W X (Wd D)
-    put(s + kSX, X, 1.f);
-    fence_proxy_async_shared();
-    tc_fence_before();
-    __syncthreads();
-    if (tid == 0) {
-      wait_bar(bars + SB_W0 + b, (x >> 1) & 1, p.err);
-      tc_fence_after();
-      const uint32_t w = smem_u32(s + kSW + b * 2 * kTile);
-#pragma unroll
-      for (int part = 0; part < 2; ++part)
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_bf16(tmem + 64 * part, desc_k(w + part * kTile, kk), desc_mn(sX, kk), idW, kk > 0);
-      umma_commit(bars + SB_MMA);
-    }
+    put(Sm::kX, X, 1.f, kLoScale);
+    ready(kScanBarX);
     // (while the products run)
-    if (REV) keep(p.D + it * kTile, X, 1.f, false);
-    else keep(p.S + it * (MODE == kFwdKeep ? 2 : 1) * kTile, X, 1.f, MODE == kFwdKeep);
-    float u[16], bc[16], er[16];
-    uint4 vr[2], sr[4];
+    if (MODE != kFwdKeep) keep((REV ? p.D : p.S) + it * kTile, X, 1.f);
+    if (REV && x > 0) {  // <S, D> between this chunk and the one behind it: X here, that one's first state
+      wait_bar(bars + SB_ST, (x - 1) & 1, p.err);
+      const uint4 hv = *reinterpret_cast<const uint4*>(s + Sm::kSt + at_hi);
+      const uint4 lv = *reinterpret_cast<const uint4*>(s + Sm::kSt + at_lo);
+      const uint32_t hw[4] = {hv.x, hv.y, hv.z, hv.w}, lw[4] = {lv.x, lv.y, lv.z, lv.w};
+      float d = 0.f;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      u[4 * v] = sg.x * un[v].x;
-      u[4 * v + 1] = sg.x * un[v].y;
-      u[4 * v + 2] = sg.x * un[v].z;
-      u[4 * v + 3] = sg.x * un[v].w;
-      if (REV) {
-        bc[4 * v] = sg.x * bn[v].x;
-        bc[4 * v + 1] = sg.x * bn[v].y;
-        bc[4 * v + 2] = sg.x * bn[v].z;
-        bc[4 * v + 3] = sg.x * bn[v].w;
-        er[4 * v] = en[v].x;
-        er[4 * v + 1] = en[v].y;
-        er[4 * v + 2] = en[v].z;
-        er[4 * v + 3] = en[v].w;
-        sr[v] = sn[v];
+      for (int v = 0; v < 4; ++v) {
+        const float2 a = unpack_f16x2(hw[v]), l = unpack_f16x2(lw[v]);
+        d = fmaf(X[2 * v], fmaf(kLoInv, l.x, a.x), fmaf(X[2 * v + 1], fmaf(kLoInv, l.y, a.y), d));
       }
+      write_bnd(c, d * sg.y * isf);
     }
-    if (REV) {
-      vr[0] = vn[0];
-      vr[1] = vn[1];
+    float u[8];
+    if (!LEAN) {
+      u[0] = sg.x * un[0].x; u[1] = sg.x * un[0].y; u[2] = sg.x * un[0].z; u[3] = sg.x * un[0].w;
+      u[4] = sg.x * un[1].x; u[5] = sg.x * un[1].y; u[6] = sg.x * un[1].z; u[7] = sg.x * un[1].w;
+    } else {
+      wait_bar(bars + SB_R0 + (x & 1), (x >> 1) & 1, p.err);
+      rows8(s + Sm::kRows + (x & 1) * kHalf, u, sg.x);
     }
-    const float fac = fac_n, gam = gam_n, bt = beta_n, in0 = in0_n;
+    const uint4 vr = vn;
+    const float fac = fac_n * ik_n, gam = gam_n, bt = beta_n, in0 = in0_n;
     if (x + 1 < Nc) fetch(x + 1);
     wait_mma();
-    if (tid == 0 && x + 2 < Nc) load_w(x + 2);
     {
-      float hh[16], hl[16], lh[16];
-      tmem_ld16(tl, hh);
-      tmem_ld16(tl + 32, hl);
-      tmem_ld16(tl + 64, lh);
+      float hh[8], hl[8], lh[8];
+      tmem_ld8(tl, hh);
+      tmem_ld8(tl + 32, hl);
+      tmem_ld8(tl + 64, lh);
       tmem_ld_wait();
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
+      for (int j = 0; j < 8; ++j) {
         const float y = fmaf(kLoInv, hl[j] + lh[j], hh[j]);
         u[j] = REV ? u[j] + y : u[j] - y;
       }
     }
     // ---- K^T (beta exp(g_C - g) e), K^T (beta exp(g - g_0) w)
-    put(s + kSE, u, bt * fac);
-    fence_proxy_async_shared();
-    tc_fence_before();
-    __syncthreads();
-    if (tid == 0) {
-      wait_bar(bars + SB_K0 + b, (x >> 1) & 1, p.err);
-      tc_fence_after();
-      const uint32_t k = smem_u32(s + kSK + b * kTile);
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk) umma_bf16(tmem + 128, desc_mn(k, kk), desc_mn(sE, kk), idK, kk > 0);
-      umma_commit(bars + SB_MMA);
-    }
-    if (!REV) {
-      keep(p.E + it * (MODE == kFwdKeep ? 2 : 1) * kTile, u, bt, MODE == kFwdKeep);
-      if (MODE == kFwdKeep) {  // e in U's place
-        float4* eg = reinterpret_cast<float4*>(p.U) + it * (kC * kC / 4) + piece;
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-          eg[v * kC] = make_float4(sg.y * u[4 * v], sg.y * u[4 * v + 1], sg.y * u[4 * v + 2], sg.y * u[4 * v + 3]);
-      }
+    put(Sm::kE, u, bt * fac, kLoScale);
+    ready(kScanBarE);
+    if (MODE == kFwdKeep) {
+      put(Sm::kU, u, bt, 1.f);
+      float4* eg = reinterpret_cast<float4*>(s + Sm::kErr + piece);
+      eg[0] = make_float4(sg.y * u[0], sg.y * u[1], sg.y * u[2], sg.y * u[3]);
+      eg[kC] = make_float4(sg.y * u[4], sg.y * u[5], sg.y * u[6], sg.y * u[7]);
+      ready(kScanBarU);
     } else {
-      keep(p.Y + it * kTile, u, bt, false);
+      keep((REV ? p.Y : p.E) + it * kTile, u, bt);
+    }
+    float bc[8];
+    if (REV) {
+      float er[8];
+      wait_bar(bars + SB_ERR, x & 1, p.err);
+      rows8(s + Sm::kErr, er, 1.f);
       float ew = 0.f, vw = 0.f;
-      uint32_t dvw[8];
-      const uint32_t vv[8] = {vr[0].x, vr[0].y, vr[0].z, vr[0].w, vr[1].x, vr[1].y, vr[1].z, vr[1].w};
+      uint32_t dvw[4];
+      const uint32_t vv[4] = {vr.x, vr.y, vr.z, vr.w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 4; ++j) {
         const float w0 = sg.y * u[2 * j], w1 = sg.y * u[2 * j + 1], d0 = bt * w0, d1 = bt * w1;
         ew = fmaf(er[2 * j], w0, fmaf(er[2 * j + 1], w1, ew));
         const float2 f = unpack_bf16x2(vv[j]);
@@ -690,47 +751,29 @@ __global__ void __launch_bounds__(256, 1) gdr_scan_kernel(TcParams p, int slices
         dvw[j] = pack_bf16x2(d0, d1);
       }
       const int t = c * kC + i;
-      p.part[(it * 8 + sl * 2 + hf) * kC + i] = make_float2(ew, vw);
-      if (t < sq.len && cols_in) {
-        uint4* dg = reinterpret_cast<uint4*>(p.dval + (row0 + t) * p.dv + col0);
-        dg[0] = make_uint4(dvw[0], dvw[1], dvw[2], dvw[3]);
-        dg[1] = make_uint4(dvw[4], dvw[5], dvw[6], dvw[7]);
-      }
+      p.part[(it * kParts + sl * 4 + qt) * kC + i] = make_float2(ew, vw);
+      if (t < sq.len && cols_in)
+        *reinterpret_cast<uint4*>(p.dval + (row0 + t) * p.dv + col0) = make_uint4(dvw[0], dvw[1], dvw[2], dvw[3]);
+      wait_bar(bars + SB_BC, x & 1, p.err);
+      rows8(s + Sm::kBc, bc, sg.x);
     }
     wait_mma();
-    if (tid == 0 && x + 2 < Nc) load_k(x + 2);
     {
-      float hi[16], lo[16];
-      tmem_ld16(tl + 128, hi);
-      tmem_ld16(tl + 160, lo);
+      float hi[8], lo[8];
+      tmem_ld8(tl + 128, hi);
+      tmem_ld8(tl + 160, lo);
       tmem_ld_wait();
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
+      for (int j = 0; j < 8; ++j) {
         const float y = fmaf(kLoInv, lo[j], hi[j]);
         X[j] = fmaf(gam, X[j], REV ? fmaf(-in0, y, bc[j]) : y);
       }
-    }
-    if (REV && c > 0) {  // <S, D> between this chunk and the one before it
-      float d = 0.f;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t hw[4] = {sr[e].x, sr[e].y, sr[e].z, sr[e].w};
-        const uint32_t lw[4] = {sr[2 + e].x, sr[2 + e].y, sr[2 + e].z, sr[2 + e].w};
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float2 a = unpack_f16x2(hw[v]), l = unpack_f16x2(lw[v]);
-          d = fmaf(X[8 * e + 2 * v], a.x + l.x, fmaf(X[8 * e + 2 * v + 1], a.y + l.y, d));
-        }
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-      if (lane == 0) p.bnd[item(c - 1) * 32 + sl * 8 + warp] = d * sg.y * isf;
     }
   }
   float* to = REV ? p.dstate_in : MODE == kFwdKeep ? p.final_state : p.state_out;
   if (to && i < p.dk && cols_in) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) to[(sh * p.dv + col0 + j) * p.dk + i] = X[j] * sg.y;
+    for (int j = 0; j < 8; ++j) to[(sh * p.dv + col0 + j) * p.dk + i] = X[j] * sg.y;
   }
   tc_fence_before();
   __syncthreads();
@@ -875,38 +918,42 @@ __global__ void __launch_bounds__(256, 2) gdr_out_kernel(TcParams p) {
 constexpr float kGradDown = 1.f / 64.f;  // of R and N, as operands
 constexpr uint32_t kGBars = 7 * kTile;
 constexpr uint32_t kGTab = kGBars + 6 * 8;
-constexpr uint32_t kGradSmem = kGTab + (2 + 2) * kC * 4 + 64;
+constexpr uint32_t kGradSmem = kGTab + 2 * kC * 4 + 32;
 static_assert(kGradSmem <= 232448, "shared memory budget of one CTA");
+constexpr int kGradThreads = 512;
 
 // One CTA per (chunk, key head); the value heads that share it are taken in
-// turn, dq adding up in tensor memory and dk in registers, in a fixed order.
-// Per head three rounds of products over seven tiles of shared memory:
+// turn, dq and dk adding up in registers in a fixed order.  Thread = (row, quarter
+// of the columns).  Per head three rounds of products over seven tiles of shared
+// memory:
 //   dO S, (beta w) S, u D;   dO u^T, (beta w) u^T, Q K^T;   R K, R^T Q, (N + N^T) K
 // with R = scale (dO u^T . G) and N = ((beta w) u^T . G) strictly lower.  The
-// first and fourth take u and S in two parts: q.dq, which enters dlog_alpha, is
+// first and fourth take S and u in two parts: q.dq, which enters dlog_alpha, is
 // then exact to float32; the rest ends in 16-bit gradients.
-__global__ void __launch_bounds__(256, 1) gdr_grad_tc_kernel(TcParams p) {
+__global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p) {
   extern __shared__ __align__(1024) unsigned char s[];
   if (smem_u32(s) & 1023u) {
     if (threadIdx.x == 0) atomicOr(p.err, kErrDeviceArg);
     return;
   }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int q = warp & 3, hf = warp >> 2, i = 32 * q + lane;
+  const int q = warp & 3, qt = warp >> 2, i = 32 * q + lane, j0 = 32 * qt;
   const int hk = blockIdx.x % p.seqs.Hk, slot = blockIdx.x / p.seqs.Hk, G = p.seqs.H / p.seqs.Hk;
   int seq, chunk;
   GdrSeq sq;
   if (!gdr_find(p.seqs, slot, kC, seq, chunk, sq)) return;
   const int t0 = chunk * kC, n = min(kC, sq.len - t0);
   const size_t krow0 = ((size_t)sq.row_b * p.seqs.Hk + hk) * p.seqs.T + sq.start + t0;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s + kGBars);  // 0: round 1, 1: low u, 2: Q and K, 3: products
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s + kGBars);  // 0: round 1, 1: Q and K, 2: products
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s + kGBars + 4 * 8);
   float2* gs = reinterpret_cast<float2*>(s + kGTab);
-  float* dg = reinterpret_cast<float*>(gs + kC);        // [2][token]
-  double* tot = reinterpret_cast<double*>(dg + 2 * kC);  // [4]
-  auto slot_at = [&](int x) { return s + x * kTile; };
+  double* tot = reinterpret_cast<double*>(gs + kC);        // [4]
+  // tiles: 0 dO, then N; 1-2 S, then Q and K; 3 beta w; 4-5 u; 6 D, then R
+  constexpr uint32_t tO = 0, tS = kTile, tQ = kTile, tK = 2 * kTile, tY = 3 * kTile, tU = 4 * kTile, tD = 6 * kTile;
+  constexpr uint32_t kLow = 64;  // of a slice tile's low part
+  float* dg = reinterpret_cast<float*>(s + tY);  // [4][token], behind round 2
   if (tid == 0) {
-    for (int b = 0; b < 4; ++b) mbar_init(bars + b, 1);
+    for (int b = 0; b < 3; ++b) mbar_init(bars + b, 1);
     fence_mbar_init();
   }
   __syncwarp();
@@ -918,184 +965,173 @@ __global__ void __launch_bounds__(256, 1) gdr_grad_tc_kernel(TcParams p) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + 64 * hf;
+  const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + j0;
   const uint32_t s0 = smem_u32(s);
   uint32_t nmma = 0;
   auto wait_mma = [&]() {
-    wait_bar(bars + 3, nmma & 1, p.err);
+    wait_bar(bars + 2, nmma & 1, p.err);
     ++nmma;
     __syncwarp();
     tc_fence_after();
   };
-  float xk[64];  // dk of this thread's row and columns, over the heads
+  float xq[32], xk[32];  // dq and dk of this thread's row and columns, over the heads
 #pragma unroll
-  for (int j = 0; j < 64; ++j) xk[j] = 0.f;
+  for (int j = 0; j < 32; ++j) xq[j] = xk[j] = 0.f;
 
   for (int hh = 0; hh < G; ++hh) {
     const int h = hk * G + hh;
     const size_t it = (size_t)slot * p.seqs.H + h, sh = (size_t)seq * p.seqs.H + h;
     const size_t row0 = ((size_t)sq.row_b * p.seqs.H + h) * p.seqs.T + sq.start + t0;
     const uint32_t par = hh & 1;
-    // slots: 0 dO, then N; 1 S high, then Q; 2 S low, then K; 3 beta w; 4 u high; 5 D, then R; 6 u low
     if (tid == 0) {
-      mbar_arrive_expect_tx(bars, 6 * kTile);
-      bulk_load(slot_at(0), p.dO16 + it * kTile, kTile, bars);
-      bulk_load(slot_at(1), p.S + it * 2 * kTile, 2 * kTile, bars);
-      bulk_load(slot_at(3), p.Y + it * kTile, kTile, bars);
-      bulk_load(slot_at(4), p.E + it * 2 * kTile, kTile, bars);
-      bulk_load(slot_at(5), p.D + it * kTile, kTile, bars);
-      mbar_arrive_expect_tx(bars + 1, kTile);
-      bulk_load(slot_at(6), p.E + (it * 2 + 1) * kTile, kTile, bars + 1);
+      mbar_arrive_expect_tx(bars, 7 * kTile);
+      bulk_load(s + tO, p.dO16 + it * kTile, kTile, bars);
+      bulk_load(s + tS, p.S + it * 2 * kTile, 2 * kTile, bars);
+      bulk_load(s + tY, p.Y + it * kTile, kTile, bars);
+      bulk_load(s + tU, p.E + it * 2 * kTile, 2 * kTile, bars);
+      bulk_load(s + tD, p.D + it * kTile, kTile, bars);
       wait_bar(bars, par, p.err);
       tc_fence_after();
-      mma_tile<false, false>(tmem + 128, s0, s0 + 2 * kTile, false);
-      mma_tile<false, false>(tmem + 128, s0, s0 + kTile, true);
-      mma_tile<false, false>(tmem + 256, s0 + 3 * kTile, s0 + kTile, false);
-      mma_tile<false, false>(tmem + 384, s0 + 4 * kTile, s0 + 5 * kTile, false);
-      umma_commit(bars + 3);
+      mma_slices<false, true>(tmem, s0 + tO, s0 + tS, false);
+      mma_slices<false, true>(tmem + 128, s0 + tO, s0 + tS + kLow, false);
+      mma_slices<false, true>(tmem + 256, s0 + tY, s0 + tS, false);
+      mma_slices<true, false>(tmem + 384, s0 + tU, s0 + tD, false);
+      umma_commit(bars + 2);
     }
     __syncwarp();
     const Tables& tb = p.tab[it];
     if (tid < kC) gs[tid] = tb.g[tid];
     const float ik = tb.ik, iq = tb.iq, id = tb.id, in = tb.into[i], out = tb.out[i];
     const float isf = operand_scale(__uint_as_float(p.amax_s[sh])).y, isr = operand_scale(__uint_as_float(p.amax_d[sh])).y;
+    uint4 qv[4];  // this thread's piece of Q's row
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      qv[v] = i < n && j0 < p.dk ? *reinterpret_cast<const uint4*>(p.q + (krow0 + i) * p.dk + j0 + 8 * v)
+                                 : make_uint4(0u, 0u, 0u, 0u);
     wait_mma();
     if (tid == 0) {
-      mbar_arrive_expect_tx(bars + 2, 2 * kTile);
-      bulk_load(slot_at(1), p.Q16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, kTile, bars + 2);
-      bulk_load(slot_at(2), p.K16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, kTile, bars + 2);
+      mbar_arrive_expect_tx(bars + 1, 2 * kTile);
+      bulk_load(s + tQ, p.Q16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, kTile, bars + 1);
+      bulk_load(s + tK, p.K16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, kTile, bars + 1);
     }
     __syncwarp();
-    // ---- round 1: dq's and dk's parts by the states.  q.dq's first part: by Q's row as given
+    // ---- round 1: dq's and dk's parts by the states, q.dq's first part
     float qdot = 0.f;
     {
       const float fq = p.scale * in * id * isf, fu = isf * isr * out, fw = -isf * isr * in;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float a[32], x[32];
-        tmem_ld32(tl + 256 + 32 * c, a);
-        tmem_ld32(tl + 384 + 32 * c, x);
+        float a[16], x[16];
+        tmem_ld16(tl + 256 + 16 * c, a);
+        tmem_ld16(tl + 384 + 16 * c, x);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) xk[32 * c + j] += fmaf(fu, x[j], fw * a[j]);
-        const int j0 = 64 * hf + 32 * c;
-        tmem_ld32(tl + 128 + 32 * c, a);
-        if (hh > 0) tmem_ld32(tl + 32 * c, x);
+        for (int j = 0; j < 16; ++j) xk[16 * c + j] += fmaf(fu, x[j], fw * a[j]);
+        tmem_ld16(tl + 16 * c, a);
+        tmem_ld16(tl + 128 + 16 * c, x);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          a[j] *= fq;
-          if (hh == 0) x[j] = 0.f;
-        }
-        if (i < n && j0 < p.dk) {
-          const uint4* qg = reinterpret_cast<const uint4*>(p.q + (krow0 + i) * p.dk + j0);
+        for (int v = 0; v < 2; ++v) {
+          const uint4 qq = qv[2 * c + v];
+          const uint32_t w[4] = {qq.x, qq.y, qq.z, qq.w};
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const uint4 qv = qg[v];
-            const uint32_t w[4] = {qv.x, qv.y, qv.z, qv.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = unpack_bf16x2(w[e]);
-              qdot = fmaf(f.x, a[8 * v + 2 * e], fmaf(f.y, a[8 * v + 2 * e + 1], qdot));
-            }
+          for (int e = 0; e < 4; ++e) {
+            const int j = 8 * v + 2 * e;
+            const float y0 = fq * fmaf(kLoInv, x[j], a[j]), y1 = fq * fmaf(kLoInv, x[j + 1], a[j + 1]);
+            const float2 f = unpack_bf16x2(w[e]);
+            qdot = fmaf(f.x, y0, fmaf(f.y, y1, qdot));
+            xq[16 * c + j] += y0;
+            xq[16 * c + j + 1] += y1;
           }
         }
-        uint32_t w[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(x[j] + a[j]);
-        tmem_st32(tl + 32 * c, w);
       }
-      tmem_st_wait();
     }
     tc_fence_before();
     __syncthreads();
     if (tid == 0) {
-      wait_bar(bars + 1, par, p.err);
       tc_fence_after();
-      mma_tile<false, false>(tmem + 128, s0, s0 + 6 * kTile, false);
-      mma_tile<false, false>(tmem + 128, s0, s0 + 4 * kTile, true);
-      mma_tile<false, false>(tmem + 256, s0 + 3 * kTile, s0 + 4 * kTile, false);
-      wait_bar(bars + 2, par, p.err);
-      mma_tile<false, false>(tmem + 384, s0 + kTile, s0 + 2 * kTile, false);
-      umma_commit(bars + 3);
+      mma_slices<false, true>(tmem + 128, s0 + tO, s0 + tU + kLow, false);
+      mma_slices<false, true>(tmem + 128, s0 + tO, s0 + tU, true);
+      mma_slices<false, true>(tmem + 256, s0 + tY, s0 + tU, false);
+      wait_bar(bars + 1, par, p.err);
+      mma_slices<false, false>(tmem + 384, s0 + tQ, s0 + tK, false);
+      umma_commit(bars + 2);
     }
     __syncwarp();
     wait_mma();
     // ---- round 2: R and N as operands; q.dq's second part, the row sums of R . Q K^T
     {
       const float2 gi = gs[i];
-      const float fr = p.scale * id * isf * iq * ik;
+      float sum = 0.f;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int j0 = 64 * hf + 32 * c;
-        float r[32], a[32];
-        tmem_ld32(tl + 128 + 32 * c, r);
-        tmem_ld32(tl + 384 + 32 * c, a);
+        float r[16], a[16], dec[16];
+        tmem_ld16(tl + 128 + 16 * c, r);
+        tmem_ld16(tl + 384 + 16 * c, a);
         tmem_ld_wait();
-        float dec[32], sum = 0.f;
 #pragma unroll
-        for (int jj = 0; jj < 32; ++jj) {
-          dec[jj] = j0 + jj <= i ? exp_diff(gi, gs[j0 + jj]) : 0.f;
-          r[jj] = dec[jj] == 0.f ? 0.f : r[jj] * dec[jj];
-          sum = fmaf(r[jj], a[jj], sum);
+        for (int jj = 0; jj < 16; ++jj) {
+          const int j = j0 + 16 * c + jj;
+          dec[jj] = j <= i ? exp_diff(gi, gs[j]) : 0.f;
+          r[jj] = j <= i ? r[jj] * dec[jj] : 0.f;
+          if (j <= i) sum = fmaf(r[jj], a[jj], sum);
         }
-        qdot = fmaf(fr, sum, qdot);
-        tmem_ld32(tl + 256 + 32 * c, a);
+        tmem_ld16(tl + 256 + 16 * c, a);
         tmem_ld_wait();
 #pragma unroll
-        for (int c8 = 0; c8 < 4; ++c8) {
+        for (int c8 = 0; c8 < 2; ++c8) {
           uint32_t rw[4], nw[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int j = 8 * c8 + 2 * e;
-            rw[e] = pack_f16x2(kGradDown * r[j], kGradDown * r[j + 1]);
-            const float n0 = j0 + j < i ? kGradDown * dec[j] * a[j] : 0.f;
-            const float n1 = j0 + j + 1 < i ? kGradDown * dec[j + 1] * a[j + 1] : 0.f;
-            nw[e] = pack_f16x2(n0, n1);
+            const int jj = 8 * c8 + 2 * e, j = j0 + 16 * c + jj;
+            rw[e] = pack_f16x2(kGradDown * r[jj], kGradDown * r[jj + 1]);
+            nw[e] = pack_f16x2(j < i ? kGradDown * dec[jj] * a[jj] : 0.f,
+                               j + 1 < i ? kGradDown * dec[jj + 1] * a[jj + 1] : 0.f);
           }
-          const uint32_t at = swz16(i, (j0 >> 3) + c8);
-          *reinterpret_cast<uint4*>(slot_at(5) + at) = make_uint4(rw[0], rw[1], rw[2], rw[3]);
-          *reinterpret_cast<uint4*>(slot_at(0) + at) = make_uint4(nw[0], nw[1], nw[2], nw[3]);
+          const uint32_t at = swz16(i, 4 * qt + 2 * c + c8);
+          *reinterpret_cast<uint4*>(s + tD + at) = make_uint4(rw[0], rw[1], rw[2], rw[3]);
+          *reinterpret_cast<uint4*>(s + tO + at) = make_uint4(nw[0], nw[1], nw[2], nw[3]);
         }
       }
-      dg[hf * kC + i] = qdot;
+      dg[qt * kC + i] = fmaf(p.scale * id * isf * iq * ik, sum, qdot);
     }
     fence_proxy_async_shared();
     tc_fence_before();
     __syncthreads();
     if (tid == 0) {
       tc_fence_after();
-      mma_tile<false, true>(tmem + 128, s0 + 5 * kTile, s0 + 2 * kTile, false);  // R K
-      mma_tile<true, true>(tmem + 256, s0 + 5 * kTile, s0 + kTile, false);       // R^T Q
-      mma_tile<false, true>(tmem + 384, s0, s0 + 2 * kTile, false);              // N K
-      mma_tile<true, true>(tmem + 384, s0, s0 + 2 * kTile, true);                // N^T K
-      umma_commit(bars + 3);
+      mma_tile<false, true>(tmem + 128, s0 + tD, s0 + tK, false);  // R K
+      mma_tile<true, true>(tmem + 256, s0 + tD, s0 + tQ, false);   // R^T Q
+      mma_tile<false, true>(tmem + 384, s0 + tO, s0 + tK, false);  // N K
+      mma_tile<true, true>(tmem + 384, s0 + tO, s0 + tK, true);    // N^T K
+      umma_commit(bars + 2);
     }
     __syncwarp();
     // ---- the gates' gradients: sums over the slices, the suffix sum over the chunk
-    if (tid < kC) {
+    if (warp >= 12) {
+      const int t = tid - 384;
       float ew = 0.f, vw = 0.f;
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const float2 f = p.part[(it * 8 + x) * kC + tid];
+      for (int x = 0; x < kParts; ++x) {
+        const float2 f = p.part[(it * kParts + x) * kC + t];
         ew += f.x;
         vw += f.y;
       }
-      double y = tid < n ? (double)((dg[tid] + dg[kC + tid]) - vw) : 0.0;
+      double y = t < n ? (double)(((dg[t] + dg[kC + t]) + (dg[2 * kC + t] + dg[3 * kC + t])) - vw) : 0.0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const double z = __shfl_down_sync(0xffffffffu, y, o);
         if (lane + o < 32) y += z;
       }
-      if (lane == 0) tot[warp] = y;
-      float bsum = p.bnd[it * 32 + lane];
+      if (lane == 0) tot[q] = y;
+      float bsum = p.bnd[it * kBnd + lane] + p.bnd[it * kBnd + 32 + lane];
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) bsum += __shfl_xor_sync(0xffffffffu, bsum, o);
       named_bar_sync(1, kC);
-      for (int w = warp + 1; w < 4; ++w) y += tot[w];
-      if (tid < n) {
-        p.dlog_alpha[row0 + tid] = (float)(y + (double)bsum);
-        p.dbeta[row0 + tid] = ew;
+      for (int w = q + 1; w < 4; ++w) y += tot[w];
+      if (t < n) {
+        p.dlog_alpha[row0 + t] = (float)(y + (double)bsum);
+        p.dbeta[row0 + t] = ew;
       }
     }
     wait_mma();
@@ -1105,43 +1141,32 @@ __global__ void __launch_bounds__(256, 1) gdr_grad_tc_kernel(TcParams p) {
       const float f2 = -isf * isr * ik / kGradDown;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float a[32], x[32];
-        tmem_ld32(tl + 256 + 32 * c, a);
-        tmem_ld32(tl + 384 + 32 * c, x);
+        float a[16], x[16], y[16];
+        tmem_ld16(tl + 128 + 16 * c, y);
+        tmem_ld16(tl + 256 + 16 * c, a);
+        tmem_ld16(tl + 384 + 16 * c, x);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) xk[32 * c + j] += fmaf(f1, a[j], f2 * x[j]);
-        tmem_ld32(tl + 32 * c, a);
-        tmem_ld32(tl + 128 + 32 * c, x);
-        tmem_ld_wait();
-        if (hh + 1 < G) {
-          uint32_t w[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(fmaf(f0, x[j], a[j]));
-          tmem_st32(tl + 32 * c, w);
-        } else if (i < n && 64 * hf + 32 * c < p.dk) {
-          const size_t at = (krow0 + i) * p.dk + 64 * hf + 32 * c;
-          uint4* qg = reinterpret_cast<uint4*>(p.dq + at);
-          uint4* kg = reinterpret_cast<uint4*>(p.dkey + at);
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            uint32_t w[4], y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int j = 8 * v + 2 * e;
-              w[e] = pack_bf16x2(fmaf(f0, x[j], a[j]), fmaf(f0, x[j + 1], a[j + 1]));
-              y[e] = pack_bf16x2(xk[32 * c + j], xk[32 * c + j + 1]);
-            }
-            qg[v] = make_uint4(w[0], w[1], w[2], w[3]);
-            kg[v] = make_uint4(y[0], y[1], y[2], y[3]);
-          }
+        for (int j = 0; j < 16; ++j) {
+          xk[16 * c + j] += fmaf(f1, a[j], f2 * x[j]);
+          xq[16 * c + j] = fmaf(f0, y[j], xq[16 * c + j]);
         }
       }
-      if (hh + 1 < G) tmem_st_wait();
     }
     tc_fence_before();
     __syncthreads();  // the next head's tiles and tables
     tc_fence_after();
+  }
+  if (i < n && j0 < p.dk) {
+    uint4* qg = reinterpret_cast<uint4*>(p.dq + (krow0 + i) * p.dk + j0);
+    uint4* kg = reinterpret_cast<uint4*>(p.dkey + (krow0 + i) * p.dk + j0);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      qg[v] = make_uint4(pack_bf16x2(xq[8 * v], xq[8 * v + 1]), pack_bf16x2(xq[8 * v + 2], xq[8 * v + 3]),
+                         pack_bf16x2(xq[8 * v + 4], xq[8 * v + 5]), pack_bf16x2(xq[8 * v + 6], xq[8 * v + 7]));
+      kg[v] = make_uint4(pack_bf16x2(xk[8 * v], xk[8 * v + 1]), pack_bf16x2(xk[8 * v + 2], xk[8 * v + 3]),
+                         pack_bf16x2(xk[8 * v + 4], xk[8 * v + 5]), pack_bf16x2(xk[8 * v + 6], xk[8 * v + 7]));
+    }
   }
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
@@ -1181,8 +1206,8 @@ Plan plan_of(const GdrArgs& a, bool bwd) {
     p.D = take(items * kTile);
     p.Y = take(items * kTile);
     p.fin = take((size_t)gdr_sequences(a) * a.H * a.dv * a.dk * 4);
-    p.part = take(items * 8 * kC * sizeof(float2));
-    p.bnd = take(items * 32 * 4);
+    p.part = take(items * kParts * kC * sizeof(float2));
+    p.bnd = take(items * kBnd * 4);
   }
   p.total = at;
   return p;
@@ -1245,8 +1270,9 @@ TcParams params_of(const GdrArgs& a, const Plan& pl, bool bwd) {
 }
 
 template <int MODE> ll_status scan(const GdrArgs& a, const TcParams& p, int slices) {
-  LL_CUDA_OK(cudaFuncSetAttribute(gdr_scan_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScanSmem));
-  gdr_scan_kernel<MODE><<<(unsigned)(gdr_sequences(a) * a.H * slices), 256, kScanSmem, a.stream>>>(p, slices);
+  LL_CUDA_OK(cudaFuncSetAttribute(gdr_scan_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  (int)ScanSm<MODE>::kBytes));
+  gdr_scan_kernel<MODE><<<(unsigned)(gdr_sequences(a) * a.H * slices), kScanThreads, ScanSm<MODE>::kBytes, a.stream>>>(p, slices);
   LL_CUDA_OK(cudaGetLastError());
   return LL_OK;
 }
@@ -1290,7 +1316,7 @@ ll_status gdr_tc_bwd_launch(const GdrArgs& a) {
   if (st == LL_OK) st = scan<kRev>(a, p, kC / kSlice);
   if (st != LL_OK) return st;
   LL_CUDA_OK(cudaFuncSetAttribute(gdr_grad_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGradSmem));
-  gdr_grad_tc_kernel<<<pl.slots * a.Hk, 256, kGradSmem, a.stream>>>(p);
+  gdr_grad_tc_kernel<<<pl.slots * a.Hk, kGradThreads, kGradSmem, a.stream>>>(p);
   LL_CUDA_OK(cudaGetLastError());
   return LL_OK;
 }

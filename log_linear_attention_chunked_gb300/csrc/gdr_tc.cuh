@@ -89,6 +89,19 @@ __device__ __noinline__ void mma_tile(uint32_t d, uint32_t a, uint32_t b, bool a
   }
 }
 
+// The same with K along the columns of both; an operand `SL` lies in slice tiles, 32 of
+// its columns in every 16 KB, 16-bit parts of 64 bytes side by side in a row.
+template <bool ASL, bool BSL>
+__device__ __noinline__ void mma_slices(uint32_t d, uint32_t a, uint32_t b, bool add) {
+  constexpr uint32_t id = idesc_f16(128, false, false);
+  const uint64_t da = desc_k(a, 0), db = desc_k(b, 0);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk) {
+    const uint32_t k = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4, ks = ((kk >> 1) * kHalf + (kk & 1) * 32) >> 4;
+    umma_bf16(d, da + (ASL ? ks : k), db + (BSL ? ks : k), id, (add || kk > 0) ? 1u : 0u);
+  }
+}
+
 __device__ __forceinline__ void cp_async16_zfill(void* dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16u : 0u));
 }
