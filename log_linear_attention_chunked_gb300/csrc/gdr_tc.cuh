@@ -45,8 +45,7 @@ __device__ __forceinline__ float exp_diff(float2 a, float2 b) { return ex2(((a.x
 
 // Bounded wait (every thread): the waits of these kernels are on their own
 // copies and products, which always complete.
-__device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t par, unsigned* err) {
-  if (mbar_try_wait(bar, par)) return;
+__device__ __noinline__ void wait_bar_long(uint64_t* bar, uint32_t par, unsigned* err) {
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, par)) {
     if (globaltimer_ns() - t0 > kTimeoutNs) {
@@ -54,6 +53,9 @@ __device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t par, unsigned* 
       return;
     }
   }
+}
+__device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t par, unsigned* err) {
+  if (!mbar_try_wait(bar, par)) wait_bar_long(bar, par, err);
 }
 
 // byte offset of the 16-byte piece c8 (columns 8 c8 ..) of row r of a tile
