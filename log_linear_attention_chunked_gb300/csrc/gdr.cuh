@@ -93,6 +93,14 @@ inline size_t gdr_slots(const GdrArgs& a, int C) {
 constexpr float kGdrMinLog = -1e4f;
 __device__ __forceinline__ float gdr_log(float la) { return la < kGdrMinLog ? kGdrMinLog : la; }
 
+// sums of floats as pairs (value and what its rounding left)
+__device__ __forceinline__ float2 pair_add(float2 a, float2 b) {
+  const float s = a.x + b.x, t = s - a.x;
+  const float e = (a.x - (s - t)) + (b.x - t) + (a.y + b.y);
+  const float hi = s + e;
+  return make_float2(hi, e - (hi - s));
+}
+
 // ---- launchers
 size_t gdr_fwd_workspace(const GdrArgs& a);
 ll_status gdr_fwd_launch(const GdrArgs& a);

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kThreads) gdr_grad_kernel(GradParams p) {
   float* ws = es + kC * ldv;   // w
   float* R = ws + kC * ldv;
   float* N = R + kC * kLdC;
-  float* ghi = N + kC * kLdC;  // running log decay, high and low parts
+  float* ghi = N + kC * kLdC;  // running log decay, a pair
   float* glo = ghi + kC;
   float* into = glo + kC;      // exp(g_i)
   float* out = into + kC;      // exp(g_C - g_i)
@@ -107,13 +107,24 @@ __global__ void __launch_bounds__(kThreads) gdr_grad_kernel(GradParams p) {
       es[t * ldv + r] = in ? p.errors[row0 * DV + x] : 0.f;
       ws[t * ldv + r] = in ? p.w[row0 * DV + x] : 0.f;
     }
-    if (tid == 0) {  // (64 steps; float64, kept as a pair of floats)
-      double g = 0.0;
-      for (int t = 0; t < kC; ++t) {
-        if (t < n) g += (double)gdr_log(p.log_alpha[row0 + t]);
-        ghi[t] = (float)g;
-        glo[t] = (float)(g - (double)ghi[t]);
+    if (tid < 32) {  // two tokens to a lane
+      const int t = 2 * tid;
+      const float2 x = make_float2(t < n ? gdr_log(p.log_alpha[row0 + t]) : 0.f, 0.f);
+      const float2 y = make_float2(t + 1 < n ? gdr_log(p.log_alpha[row0 + t + 1]) : 0.f, 0.f);
+      const float2 own = pair_add(x, y);
+      float2 g = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float2 z = make_float2(__shfl_up_sync(0xffffffffu, g.x, o), __shfl_up_sync(0xffffffffu, g.y, o));
+        if (tid >= o) g = pair_add(g, z);
       }
+      float2 before = make_float2(__shfl_up_sync(0xffffffffu, g.x, 1), __shfl_up_sync(0xffffffffu, g.y, 1));
+      if (tid == 0) before = make_float2(0.f, 0.f);
+      before = pair_add(before, x);
+      ghi[t] = before.x;
+      glo[t] = before.y;
+      ghi[t + 1] = g.x;
+      glo[t + 1] = g.y;
     }
     if (tid < kC) bs[tid] = tid < n ? p.beta[row0 + tid] : 0.f;
     __syncthreads();
@@ -246,13 +257,25 @@ __global__ void __launch_bounds__(kThreads) gdr_grad_kernel(GradParams p) {
     dot = sum16(dot);
     if (tx == 0) red[ty] = dot;
     __syncthreads();
-    if (tid < n) {
-      double s = 0.0;
-      for (int x = 0; x < 16; ++x) s += (double)red[x];
-      s *= (double)into[kC - 1];
-      for (int t = 0; t < n; ++t) s += (double)kd[t];
-      for (int t = tid; t < n; ++t) s += (double)dg[t];
-      p.dlog_alpha[row0 + tid] = (float)s;
+    if (tid < 32) {
+      float2 sd = make_float2(tid < 16 ? red[tid] * into[kC - 1] : 0.f, 0.f);
+      sd = pair_add(sd, make_float2(kd[2 * tid], 0.f));
+      sd = pair_add(sd, make_float2(kd[2 * tid + 1], 0.f));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        sd = pair_add(sd, make_float2(__shfl_xor_sync(0xffffffffu, sd.x, o), __shfl_xor_sync(0xffffffffu, sd.y, o)));
+      const float2 d1 = make_float2(dg[2 * tid + 1], 0.f);
+      float2 g = pair_add(make_float2(dg[2 * tid], 0.f), d1);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float2 z = make_float2(__shfl_down_sync(0xffffffffu, g.x, o), __shfl_down_sync(0xffffffffu, g.y, o));
+        if (tid + o < 32) g = pair_add(g, z);
+      }
+      float2 behind = make_float2(__shfl_down_sync(0xffffffffu, g.x, 1), __shfl_down_sync(0xffffffffu, g.y, 1));
+      if (tid == 31) behind = make_float2(0.f, 0.f);
+      behind = pair_add(behind, d1);
+      if (2 * tid < n) p.dlog_alpha[row0 + 2 * tid] = pair_add(g, sd).x;
+      if (2 * tid + 1 < n) p.dlog_alpha[row0 + 2 * tid + 1] = pair_add(behind, sd).x;
     }
   }
 #pragma unroll

@@ -4,12 +4,19 @@
 // Every row r of a state (d_v) follows a recurrence of its own,
 //   e = v[r] - alpha S[r].k,  u = beta e,  S[r] <- alpha S[r] + u k,
 //   o[r] = scale S[r].q = scale (alpha S_old[r].q + u k.q),
-// so a row needs two dot products with the OLD state and no other row: a group
+// so a row needs dot products with the old state and no other row: a group
 // of kLpr lanes holds a row (dk / kLpr elements each, four consecutive ones at
 // a time so that the lanes of a group read 16- or 8-byte pieces side by side),
-// and a CTA 16 rows of one (sequence, head).  Likewise backwards, with A_t the
-// adjoint of S_t (o_t's part included):
-//   A <- A + scale do q,  w = A.k,  A <- alpha (A - beta w k).
+// and a CTA 16 rows of one (sequence, head).  Likewise backwards, with C_t the
+// adjoint of S_t by the tokens behind t and d = scale do:
+//   w = C.k + d q.k,  C <- alpha (C + d q - beta w k).
+//
+// A token's chain (dot product, sum over the lanes, update) is what bounds these
+// kernels, so the sums run one token ahead: S_{t-1}.k_t is
+// alpha_{t-1} S_{t-2}.k_t + u_{t-1} k_{t-1}.k_t, whose first product is summed
+// while token t - 1 updates the state; likewise backwards.  The products of
+// neighbouring keys are made once per staged tile.  Arithmetic is on pairs of
+// floats (one instruction for two).
 #include "gdr.cuh"
 #include "sm100.cuh"
 
@@ -24,9 +31,10 @@ using sm100::cp_async_wait;
 constexpr int kRows = 16;    // rows of d_v per CTA
 constexpr int kTile = 16;    // tokens staged at a time
 static_assert(kGdrGradChunk % kTile == 0, "kept states lie on tile boundaries");
+static_assert(kTile % 3 == 1, "the loops over a whole tile take three tokens at a time and one more");
 
 template <int DK> struct RowCfg {
-  static constexpr int kLpr = DK >= 32 ? 8 : 4;   // lanes per row
+  static constexpr int kLpr = DK >= 128 ? 8 : DK >= 32 ? 4 : 2;  // lanes per row
   static constexpr int kEpl = DK / kLpr;          // elements per lane
   static constexpr int kPieces = kEpl / 4;
   static constexpr int kThreads = kRows * kLpr;
@@ -69,6 +77,46 @@ __device__ __forceinline__ float group_sum(float x) {
   return x;
 }
 
+// ---- pairs of floats
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pair(float x, float y) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float sum2(f2 a) {
+  float x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a));
+  return x + y;
+}
+template <int DK, typename P>
+__device__ __forceinline__ void load_pairs(const P* row, int l, f2* x) {
+  float y[RowCfg<DK>::kEpl];
+  load_row<DK>(row, l, y);
+#pragma unroll
+  for (int i = 0; i < RowCfg<DK>::kEpl / 2; ++i) x[i] = pair(y[2 * i], y[2 * i + 1]);
+}
+template <int N>
+__device__ __forceinline__ float dot2(const f2* a, const f2* b) {  // of N pairs
+  f2 s = mul2(a[0], b[0]), t = mul2(a[1], b[1]);
+#pragma unroll
+  for (int i = 2; i < N; i += 2) {
+    s = fma2(a[i], b[i], s);
+    t = fma2(a[i + 1], b[i + 1], t);
+  }
+  return sum2(s) + sum2(t);
+}
+
 // rows [r0, r0 + n) of a [.., W] matrix, W * sizeof(IO) a multiple of 16, into
 // shared memory; `cols` columns from column c0
 template <typename IO>
@@ -99,17 +147,15 @@ struct RecParams {
   unsigned* err;
 };
 
-// Bound: the latency of a token's chain (two dot products over a group of
-// lanes, e, the update).
 template <typename IO, int DK>
 __global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_rec_fwd_kernel(RecParams p) {
   using Cfg = RowCfg<DK>;
-  constexpr int LPR = Cfg::kLpr, EPL = Cfg::kEpl;
+  constexpr int LPR = Cfg::kLpr, EPL = Cfg::kEpl, NP = EPL / 2;
   __shared__ __align__(16) IO ks[2][kTile * DK];
   __shared__ __align__(16) IO qs[2][kTile * DK];
   __shared__ __align__(16) IO vs[2][kTile * kRows];
   __shared__ float os[kTile][kRows], es[kTile][kRows];
-  __shared__ float al[kTile], bt[kTile], kq[kTile];
+  __shared__ float4 tok[kTile];  // alpha_t, beta_t, k_t.q_t, k_{t-1}.k_t
 
   const int slices = p.dv / kRows;
   const int sl = blockIdx.x % slices;
@@ -131,11 +177,11 @@ __global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_rec_fwd_kernel(RecPa
   IO* og = p.o ? static_cast<IO*>(p.o) + row0 * p.dv : nullptr;
   const size_t st_at = (((size_t)seq * p.seqs.H + h) * p.dv + r0 + grp) * DK;
 
-  float s[EPL];
-  if (p.state_in) load_row<DK>(p.state_in + st_at, l, s);
+  f2 s[NP];
+  if (p.state_in) load_pairs<DK>(p.state_in + st_at, l, s);
   else
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) s[i] = 0.f;
+    for (int i = 0; i < NP; ++i) s[i] = 0;
 
   const int tiles = (sq.len + kTile - 1) / kTile;
   const int base = gdr_slot_base(p.seqs, seq, sq.start, kGdrGradChunk);
@@ -146,18 +192,15 @@ __global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_rec_fwd_kernel(RecPa
     stage(qs[b], qg + (size_t)t0 * DK, n, DK, 0, DK);
     stage(vs[b], vg + (size_t)t0 * p.dv, n, p.dv, r0, kRows);
     cp_async_commit();
-    if (tid < n) {
-      la_n = p.log_alpha[row0 + t0 + tid];
-      bt_n = p.beta[row0 + t0 + tid];
+    if (l == 0 && grp < n) {
+      la_n = p.log_alpha[row0 + t0 + grp];
+      bt_n = p.beta[row0 + t0 + grp];
     }
   };
   if (tiles) fetch(0);
   for (int j = 0; j < tiles; ++j) {
     const int t0 = j * kTile, n = min(kTile, sq.len - t0), b = j & 1;
-    if (tid < n) {
-      al[tid] = expf(la_n);
-      bt[tid] = bt_n;
-    }
+    const float al = expf(la_n), bt = bt_n;
     if (j + 1 < tiles) {
       fetch(j + 1);
       cp_async_wait<1>();
@@ -166,43 +209,73 @@ __global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_rec_fwd_kernel(RecPa
     }
     if (p.kept_states && t0 % kGdrGradChunk == 0)
       store_row<DK>(p.kept_states +
-                        ((((size_t)base + t0 / kGdrGradChunk) * p.seqs.H + h) * p.dv + r0 + grp) * DK, l, s);
+                        ((((size_t)base + t0 / kGdrGradChunk) * p.seqs.H + h) * p.dv + r0 + grp) * DK, l,
+                    reinterpret_cast<const float*>(s));
     __syncthreads();
-    {  // k.q of every staged token: one group of lanes each
-      float a[EPL], c[EPL];
-      load_row<DK>(ks[b] + grp * DK, l, a);
-      load_row<DK>(qs[b] + grp * DK, l, c);
-      const float d = group_sum<LPR>(dot<EPL>(a, c));
-      if (l == 0) kq[grp] = d;
+    {  // the staged tokens' scalars: one group of lanes each
+      f2 x[NP], y[NP];
+      load_pairs<DK>(ks[b] + grp * DK, l, x);
+      load_pairs<DK>(qs[b] + grp * DK, l, y);
+      const float kq = group_sum<LPR>(dot2<NP>(x, y));
+      load_pairs<DK>(ks[b] + max(grp - 1, 0) * DK, l, y);
+      const float kk = group_sum<LPR>(dot2<NP>(x, y));
+      if (l == 0) tok[grp] = make_float4(al, bt, kq, kk);
     }
     __syncthreads();
-    float kc[EPL], qc[EPL];
-    load_row<DK>(ks[b], l, kc);
-    load_row<DK>(qs[b], l, qc);
-    for (int t = 0; t < n; ++t) {
-      const float a = al[t], be = bt[t], v = to_f(vs[b][t * kRows + grp]), c = kq[t];
-      float sk = dot<EPL>(s, kc), sqd = dot<EPL>(s, qc);
-      float kn[EPL], qn[EPL];  // the next token's, on their way during this one's sums
-      const int tn = min(t + 1, kTile - 1);
-      load_row<DK>(ks[b] + tn * DK, l, kn);
-      load_row<DK>(qs[b] + tn * DK, l, qn);
+    // one token's work, its operands loaded before; k2 and q1 are loaded for the tokens ahead
+    f2 ka[NP], kb[NP], kc[NP], qa[NP], qb[NP];
+    load_pairs<DK>(ks[b], l, ka);
+    load_pairs<DK>(ks[b] + min(1, kTile - 1) * DK, l, kb);
+    load_pairs<DK>(qs[b], l, qa);
+    float4 c = tok[0];
+    float v = to_f(vs[b][grp]);
+    float dn = group_sum<LPR>(dot2<NP>(s, ka));  // of the state one token back (here: the present one) with this key
+    float a_p = 1.f, u_p = 0.f;
+    auto token = [&](int t, f2* k0, f2* k1, f2* k2, f2* q0, f2* q1) {
+      float d1 = dot2<NP>(s, k1), d2 = dot2<NP>(s, q0);
+      const float e = fmaf(-c.x, fmaf(a_p, dn, c.w * u_p), v);
+      const float u = c.y * e;
+      const float al_t = c.x, kq_t = c.z;
+      c = tok[min(t + 1, kTile - 1)];
+      v = to_f(vs[b][min(t + 1, kTile - 1) * kRows + grp]);
+      load_pairs<DK>(ks[b] + min(t + 2, kTile - 1) * DK, l, k2);
+      load_pairs<DK>(qs[b] + min(t + 1, kTile - 1) * DK, l, q1);
+      const f2 a2 = pair(al_t, al_t), u2 = pair(u, u);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) s[i] = fma2(u2, k0[i], mul2(a2, s[i]));
 #pragma unroll
       for (int o = LPR / 2; o > 0; o >>= 1) {
-        sk += __shfl_xor_sync(0xffffffffu, sk, o);
-        sqd += __shfl_xor_sync(0xffffffffu, sqd, o);
+        d1 += __shfl_xor_sync(0xffffffffu, d1, o);
+        d2 += __shfl_xor_sync(0xffffffffu, d2, o);
       }
-      const float e = fmaf(-a, sk, v);
-      const float u = be * e;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) s[i] = fmaf(u, kc[i], a * s[i]);
       if (l == 0) {
-        os[t][grp] = p.scale * fmaf(a, sqd, u * c);
+        os[t][grp] = p.scale * fmaf(al_t, d2, u * kq_t);
         es[t][grp] = e;
       }
+      dn = d1;
+      a_p = al_t;
+      u_p = u;
+    };
+    if (n == kTile) {  // (the operands change places, no copies)
+#pragma unroll 1
+      for (int t = 0; t < kTile - 1; t += 3) {
+        token(t, ka, kb, kc, qa, qb);
+        token(t + 1, kb, kc, ka, qb, qa);
+        token(t + 2, kc, ka, kb, qa, qb);
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        kc[i] = kn[i];
-        qc[i] = qn[i];
+        for (int i = 0; i < NP; ++i) qa[i] = qb[i];
+      }
+      token(kTile - 1, ka, kb, kc, qa, qb);
+    } else {
+#pragma unroll 1
+      for (int t = 0; t < n; ++t) {
+        token(t, ka, kb, kc, qa, qb);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          ka[i] = kb[i];
+          kb[i] = kc[i];
+          qa[i] = qb[i];
+        }
       }
     }
     __syncthreads();
@@ -213,20 +286,21 @@ __global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_rec_fwd_kernel(RecPa
       if (p.kept_errors) p.kept_errors[row0 * p.dv + at] = es[t][r];
     }
   }
-  if (p.state_out) store_row<DK>(p.state_out + st_at, l, s);
+  if (p.state_out) store_row<DK>(p.state_out + st_at, l, reinterpret_cast<const float*>(s));
 }
 
-// The reverse recurrence: w_t = A_t k_t for every token, the adjoint A after
-// every kGdrGradChunk tokens, and the gradient of the state on entry.
+// The reverse recurrence: w_t for every token, the adjoint C behind every
+// kGdrGradChunk tokens, and the gradient of the state on entry.
 template <typename IO, int DK>
 __global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_rec_bwd_kernel(RecParams p) {
   using Cfg = RowCfg<DK>;
-  constexpr int LPR = Cfg::kLpr, EPL = Cfg::kEpl;
+  constexpr int LPR = Cfg::kLpr, EPL = Cfg::kEpl, NP = EPL / 2;
   __shared__ __align__(16) IO ks[2][kTile * DK];
   __shared__ __align__(16) IO qs[2][kTile * DK];
   __shared__ __align__(16) IO ds[2][kTile * kRows];
   __shared__ float ws[kTile][kRows];
-  __shared__ float al[kTile], bt[kTile];
+  __shared__ float4 tok[kTile];  // alpha_t, beta_t, q_t.k_t, q_t.k_{t-1}
+  __shared__ float kks[kTile];   // k_t.k_{t-1}
 
   const int slices = p.dv / kRows;
   const int sl = blockIdx.x % slices;
@@ -247,11 +321,11 @@ __global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_rec_bwd_kernel(RecPa
   const IO* dg = static_cast<const IO*>(p.dout) + row0 * p.dv;
   const size_t st_at = (((size_t)seq * p.seqs.H + h) * p.dv + r0 + grp) * DK;
 
-  float a[EPL];
-  if (p.dstate_out) load_row<DK>(p.dstate_out + st_at, l, a);
+  f2 a[NP];
+  if (p.dstate_out) load_pairs<DK>(p.dstate_out + st_at, l, a);
   else
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) a[i] = 0.f;
+    for (int i = 0; i < NP; ++i) a[i] = 0;
 
   const int tiles = (sq.len + kTile - 1) / kTile;
   const int base = gdr_slot_base(p.seqs, seq, sq.start, kGdrGradChunk);
@@ -262,18 +336,15 @@ __global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_rec_bwd_kernel(RecPa
     stage(qs[b], qg + (size_t)t0 * DK, n, DK, 0, DK);
     stage(ds[b], dg + (size_t)t0 * p.dv, n, p.dv, r0, kRows);
     cp_async_commit();
-    if (tid < n) {
-      la_n = p.log_alpha[row0 + t0 + tid];
-      bt_n = p.beta[row0 + t0 + tid];
+    if (l == 0 && grp < n) {
+      la_n = p.log_alpha[row0 + t0 + grp];
+      bt_n = p.beta[row0 + t0 + grp];
     }
   };
   if (tiles) fetch(tiles - 1);
   for (int j = tiles - 1; j >= 0; --j) {
     const int t0 = j * kTile, n = min(kTile, sq.len - t0), b = j & 1;
-    if (tid < n) {
-      al[tid] = expf(la_n);
-      bt[tid] = bt_n;
-    }
+    const float al = expf(la_n), bt = bt_n;
     if (j > 0) {
       fetch(j - 1);
       cp_async_wait<1>();
@@ -282,29 +353,67 @@ __global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_rec_bwd_kernel(RecPa
     }
     if (t0 + n == sq.len || (t0 + n) % kGdrGradChunk == 0)
       store_row<DK>(p.kept_adjoints +
-                        ((((size_t)base + t0 / kGdrGradChunk) * p.seqs.H + h) * p.dv + r0 + grp) * DK, l, a);
+                        ((((size_t)base + t0 / kGdrGradChunk) * p.seqs.H + h) * p.dv + r0 + grp) * DK, l,
+                    reinterpret_cast<const float*>(a));
     __syncthreads();
-    float kc[EPL], qc[EPL];
-    load_row<DK>(ks[b] + (n - 1) * DK, l, kc);
-    load_row<DK>(qs[b] + (n - 1) * DK, l, qc);
-    for (int t = n - 1; t >= 0; --t) {
-      const float d = p.scale * to_f(ds[b][t * kRows + grp]);
+    {
+      f2 x[NP], y[NP], z[NP];
+      load_pairs<DK>(ks[b] + grp * DK, l, x);
+      load_pairs<DK>(qs[b] + grp * DK, l, y);
+      load_pairs<DK>(ks[b] + max(grp - 1, 0) * DK, l, z);
+      const float qk = group_sum<LPR>(dot2<NP>(x, y)), qk1 = group_sum<LPR>(dot2<NP>(y, z));
+      const float kk = group_sum<LPR>(dot2<NP>(x, z));
+      if (l == 0) {
+        tok[grp] = make_float4(al, bt, qk, qk1);
+        kks[grp] = kk;
+      }
+    }
+    __syncthreads();
+    f2 ka[NP], kb[NP], kc[NP], qa[NP], qb[NP];
+    load_pairs<DK>(ks[b] + (n - 1) * DK, l, ka);
+    load_pairs<DK>(ks[b] + max(n - 2, 0) * DK, l, kb);
+    load_pairs<DK>(qs[b] + (n - 1) * DK, l, qa);
+    float4 c = tok[n - 1];
+    float kk = kks[n - 1], d = p.scale * to_f(ds[b][(n - 1) * kRows + grp]);
+    float ck = group_sum<LPR>(dot2<NP>(a, ka));  // C_t.k_t
+    auto token = [&](int t, f2* k0, f2* k1, f2* k2, f2* q0, f2* q1) {
+      float d1 = dot2<NP>(a, k1);
+      const float w = fmaf(d, c.z, ck);
+      const float bw = -c.y * w, al_t = c.x;
+      const float rest = fmaf(d, c.w, bw * kk);
+      const f2 al2 = pair(al_t, al_t), d2 = pair(d, d), w2 = pair(bw, bw);
+      const int t1 = max(t - 1, 0);
+      c = tok[t1];
+      kk = kks[t1];
+      d = p.scale * to_f(ds[b][t1 * kRows + grp]);
+      load_pairs<DK>(ks[b] + max(t - 2, 0) * DK, l, k2);
+      load_pairs<DK>(qs[b] + t1 * DK, l, q1);
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) a[i] = fmaf(d, qc[i], a[i]);
-      float w = dot<EPL>(a, kc);
-      float kn[EPL], qn[EPL];
-      const int tn = max(t - 1, 0);
-      load_row<DK>(ks[b] + tn * DK, l, kn);
-      load_row<DK>(qs[b] + tn * DK, l, qn);
-      w = group_sum<LPR>(w);
-      const float bw = -bt[t] * w, al_t = al[t];
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) a[i] = al_t * fmaf(bw, kc[i], a[i]);
+      for (int i = 0; i < NP; ++i) a[i] = mul2(al2, fma2(w2, k0[i], fma2(d2, q0[i], a[i])));
+      d1 = group_sum<LPR>(d1);
+      ck = al_t * (d1 + rest);
       if (l == 0) ws[t][grp] = w;
+    };
+    if (n == kTile) {
+#pragma unroll 1
+      for (int t = kTile - 1; t > 0; t -= 3) {
+        token(t, ka, kb, kc, qa, qb);
+        token(t - 1, kb, kc, ka, qb, qa);
+        token(t - 2, kc, ka, kb, qa, qb);
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        kc[i] = kn[i];
-        qc[i] = qn[i];
+        for (int i = 0; i < NP; ++i) qa[i] = qb[i];
+      }
+      token(0, ka, kb, kc, qa, qb);
+    } else {
+#pragma unroll 1
+      for (int t = n - 1; t >= 0; --t) {
+        token(t, ka, kb, kc, qa, qb);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          ka[i] = kb[i];
+          kb[i] = kc[i];
+          qa[i] = qb[i];
+        }
       }
     }
     __syncthreads();
@@ -313,7 +422,7 @@ __global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_rec_bwd_kernel(RecPa
       p.kept_w[(row0 + t0 + t) * p.dv + r0 + r] = ws[t][r];
     }
   }
-  if (p.dstate_in) store_row<DK>(p.dstate_in + st_at, l, a);
+  if (p.dstate_in) store_row<DK>(p.dstate_in + st_at, l, reinterpret_cast<const float*>(a));
 }
 
 // ---------------------------------------------------------------- one decode step

@@ -348,12 +348,6 @@ __device__ __noinline__ void tri_solve(float* Ap, float* Mp, const float* beta, 
 // threads) as pairs of floats: a scan of error-free sums, since log decays of a
 // hundred tokens leave a float too few digits for their differences.  Ends in a
 // barrier.
-__device__ __forceinline__ float2 pair_add(float2 a, float2 b) {
-  const float s = a.x + b.x, t = s - a.x;
-  const float e = (a.x - (s - t)) + (b.x - t) + (a.y + b.y);
-  const float hi = s + e;
-  return make_float2(hi, e - (hi - s));
-}
 __device__ __forceinline__ void chunk_decays(float la, float2* g, float2* tot, int tid) {
   float2 x = make_float2(la, 0.f);
   if (tid < kC) {
