@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(kThreads) gdr_grad_kernel(GradParams p) {
     // ---- R and N
     {
       float r[4][4] = {}, m[4][4] = {};
+#pragma unroll 4
       for (int d = 0; d < DV; ++d) {
         float ev[4], dv_[4], wv[4];
 #pragma unroll
@@ -170,7 +171,8 @@ __global__ void __launch_bounds__(kThreads) gdr_grad_kernel(GradParams p) {
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < NC; ++j) x0[i][j] = x1[i][j] = x2[i][j] = 0.f;
-    for (int d = 0; d < DV; ++d) {
+#pragma unroll 8
+    for (int d = 0; d < DV; ++d) {  // (unrolled for the loads in flight)
       float sv[NC], av[NC];
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
@@ -204,6 +206,7 @@ __global__ void __launch_bounds__(kThreads) gdr_grad_kernel(GradParams p) {
       if (tx == 0) kd[row] = kdot;
     }
     // ---- R K, and R^T Q - (N + N^T) K
+#pragma unroll 4
     for (int c = 0; c < kC; ++c) {
       float kv[NC], qv[NC];
 #pragma unroll
@@ -253,6 +256,7 @@ __global__ void __launch_bounds__(kThreads) gdr_grad_kernel(GradParams p) {
     }
     // ---- <S1, D1>
     float dot = 0.f;
+#pragma unroll 8
     for (int x = tid; x < DV * DK; x += kThreads) dot = fmaf(S0[x], D1[x], dot);
     dot = sum16(dot);
     if (tx == 0) red[ty] = dot;

@@ -16,7 +16,9 @@
 // alpha_{t-1} S_{t-2}.k_t + u_{t-1} k_{t-1}.k_t, whose first product is summed
 // while token t - 1 updates the state; likewise backwards.  The products of
 // neighbouring keys are made once per staged tile.  Arithmetic is on pairs of
-// floats (one instruction for two).
+// floats (one instruction for two).  Half of a CTA's threads walk over the tokens;
+// the others stage the tile after the next, make the next tile's products of
+// neighbours and write the last tile's results, one barrier a tile.
 #include "gdr.cuh"
 #include "sm100.cuh"
 
@@ -27,6 +29,7 @@ namespace {
 using sm100::cp_async16;
 using sm100::cp_async_commit;
 using sm100::cp_async_wait;
+using sm100::named_bar_sync;
 
 constexpr int kRows = 16;    // rows of d_v per CTA
 constexpr int kTile = 16;    // tokens staged at a time
@@ -118,11 +121,11 @@ __device__ __forceinline__ float dot2(const f2* a, const f2* b) {  // of N pairs
 }
 
 // rows [r0, r0 + n) of a [.., W] matrix, W * sizeof(IO) a multiple of 16, into
-// shared memory; `cols` columns from column c0
+// shared memory, `cols` columns from column c0, by `threads` threads
 template <typename IO>
-__device__ __forceinline__ void stage(IO* dst, const IO* src, int n, int width, int c0, int cols) {
+__device__ __forceinline__ void stage(IO* dst, const IO* src, int n, int width, int c0, int cols, int t, int threads) {
   const int per = cols * (int)sizeof(IO) / 16, el = 16 / (int)sizeof(IO);
-  for (int x = threadIdx.x; x < n * per; x += blockDim.x) {
+  for (int x = t; x < n * per; x += threads) {
     const int r = x / per, p = x - r * per;
     cp_async16(dst + r * cols + p * el, src + (size_t)r * width + c0 + p * el);
   }
@@ -147,88 +150,130 @@ struct RecParams {
   unsigned* err;
 };
 
+// what a tile of tokens needs, three of them in flight
+template <typename IO, int DK> struct RecTile {
+  IO k[kTile * DK], q[kTile * DK], x[kTile * kRows];  // x: v, or do
+};
+// results and products of neighbours, two tiles in flight
+struct RecSide {
+  float4 tok[kTile];
+  float more[kTile];
+  float out[kTile][kRows], err[kTile][kRows];
+};
+template <typename IO, int DK> struct RecSm {
+  RecTile<IO, DK> tile[3];
+  RecSide side[2];
+};
+constexpr int kHelpBar = 1;
+
 template <typename IO, int DK>
-__global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_rec_fwd_kernel(RecParams p) {
+__global__ void __launch_bounds__(2 * RowCfg<DK>::kThreads) gdr_rec_fwd_kernel(RecParams p) {
   using Cfg = RowCfg<DK>;
-  constexpr int LPR = Cfg::kLpr, EPL = Cfg::kEpl, NP = EPL / 2;
-  __shared__ __align__(16) IO ks[2][kTile * DK];
-  __shared__ __align__(16) IO qs[2][kTile * DK];
-  __shared__ __align__(16) IO vs[2][kTile * kRows];
-  __shared__ float os[kTile][kRows], es[kTile][kRows];
-  __shared__ float4 tok[kTile];  // alpha_t, beta_t, k_t.q_t, k_{t-1}.k_t
+  constexpr int LPR = Cfg::kLpr, NP = Cfg::kEpl / 2, NT = Cfg::kThreads;
+  extern __shared__ __align__(16) unsigned char raw[];
+  RecSm<IO, DK>& sm = *reinterpret_cast<RecSm<IO, DK>*>(raw);
 
   const int slices = p.dv / kRows;
   const int sl = blockIdx.x % slices;
   const int h = (blockIdx.x / slices) % p.seqs.H;
   const int seq = blockIdx.x / slices / p.seqs.H;
-  const int tid = threadIdx.x, grp = tid / LPR, l = tid % LPR;
+  const bool helper = threadIdx.x >= NT;
+  const int tid = threadIdx.x % NT, grp = tid / LPR, l = tid % LPR;
   const int r0 = sl * kRows;
   GdrSeq sq;
   if (!gdr_seq(p.seqs, seq, sq)) {
-    if (tid == 0) raise_error(p.err, kErrDeviceArg);
+    if (threadIdx.x == 0) raise_error(p.err, kErrDeviceArg);
     return;
   }
   const int hk = h / (p.seqs.H / p.seqs.Hk);
   const size_t row0 = ((size_t)sq.row_b * p.seqs.H + h) * p.seqs.T + sq.start;
   const size_t krow0 = ((size_t)sq.row_b * p.seqs.Hk + hk) * p.seqs.T + sq.start;
-  const IO* qg = static_cast<const IO*>(p.q) + krow0 * DK;
-  const IO* kg = static_cast<const IO*>(p.k) + krow0 * DK;
-  const IO* vg = static_cast<const IO*>(p.v) + row0 * p.dv;
-  IO* og = p.o ? static_cast<IO*>(p.o) + row0 * p.dv : nullptr;
-  const size_t st_at = (((size_t)seq * p.seqs.H + h) * p.dv + r0 + grp) * DK;
+  const int tiles = (sq.len + kTile - 1) / kTile;
 
+  if (helper) {
+    const IO* qg = static_cast<const IO*>(p.q) + krow0 * DK;
+    const IO* kg = static_cast<const IO*>(p.k) + krow0 * DK;
+    const IO* vg = static_cast<const IO*>(p.v) + row0 * p.dv;
+    IO* og = p.o ? static_cast<IO*>(p.o) + row0 * p.dv : nullptr;
+    float la = 0.f, bt = 0.f;
+    auto fetch = [&](int j) {  // (one group of copies a tile, an empty one behind the last)
+      if (j < tiles) {
+        const int t0 = j * kTile, n = min(kTile, sq.len - t0);
+        RecTile<IO, DK>& t = sm.tile[j % 3];
+        stage(t.k, kg + (size_t)t0 * DK, n, DK, 0, DK, tid, NT);
+        stage(t.q, qg + (size_t)t0 * DK, n, DK, 0, DK, tid, NT);
+        stage(t.x, vg + (size_t)t0 * p.dv, n, p.dv, r0, kRows, tid, NT);
+      }
+      cp_async_commit();
+    };
+    auto gates = [&](int j) {
+      const int t = j * kTile + grp;
+      if (l == 0 && t < sq.len) {
+        la = p.log_alpha[row0 + t];
+        bt = p.beta[row0 + t];
+      }
+    };
+    // tile j is there: its products of neighbours, one group of lanes to a token
+    auto products = [&](int j) {
+      cp_async_wait<1>();
+      named_bar_sync(kHelpBar, NT);
+      const RecTile<IO, DK>& t = sm.tile[j % 3];
+      f2 x[NP], y[NP];
+      load_pairs<DK>(t.k + grp * DK, l, x);
+      load_pairs<DK>(t.q + grp * DK, l, y);
+      const float kq = group_sum<LPR>(dot2<NP>(x, y));
+      load_pairs<DK>(t.k + max(grp - 1, 0) * DK, l, y);
+      const float kk = group_sum<LPR>(dot2<NP>(x, y));
+      if (l == 0) sm.side[j & 1].tok[grp] = make_float4(expf(la), bt, kq, kk);
+    };
+    gates(0);
+    fetch(0);
+    fetch(1);
+    if (tiles) products(0);
+    __syncthreads();
+    for (int j = 0; j <= tiles; ++j) {
+      if (j > 0) {  // the results of tile j - 1
+        const int t0 = (j - 1) * kTile, n = min(kTile, sq.len - t0);
+        const RecSide& side = sm.side[(j - 1) & 1];
+        for (int x = tid; x < n * kRows; x += NT) {
+          const int t = x / kRows, r = x % kRows;
+          const size_t at = (size_t)(t0 + t) * p.dv + r0 + r;
+          if (og) og[at] = from_f<IO>(side.out[t][r]);
+          if (p.kept_errors) p.kept_errors[row0 * p.dv + at] = side.err[t][r];
+        }
+      }
+      gates(j + 1);
+      fetch(j + 2);
+      if (j + 1 < tiles) products(j + 1);
+      __syncthreads();
+    }
+    cp_async_wait<0>();
+    return;
+  }
+
+  const size_t st_at = (((size_t)seq * p.seqs.H + h) * p.dv + r0 + grp) * DK;
+  const int base = gdr_slot_base(p.seqs, seq, sq.start, kGdrGradChunk);
   f2 s[NP];
   if (p.state_in) load_pairs<DK>(p.state_in + st_at, l, s);
   else
 #pragma unroll
     for (int i = 0; i < NP; ++i) s[i] = 0;
-
-  const int tiles = (sq.len + kTile - 1) / kTile;
-  const int base = gdr_slot_base(p.seqs, seq, sq.start, kGdrGradChunk);
-  float la_n = 0.f, bt_n = 0.f;
-  auto fetch = [&](int j) {
-    const int t0 = j * kTile, n = min(kTile, sq.len - t0), b = j & 1;
-    stage(ks[b], kg + (size_t)t0 * DK, n, DK, 0, DK);
-    stage(qs[b], qg + (size_t)t0 * DK, n, DK, 0, DK);
-    stage(vs[b], vg + (size_t)t0 * p.dv, n, p.dv, r0, kRows);
-    cp_async_commit();
-    if (l == 0 && grp < n) {
-      la_n = p.log_alpha[row0 + t0 + grp];
-      bt_n = p.beta[row0 + t0 + grp];
-    }
-  };
-  if (tiles) fetch(0);
+  __syncthreads();
   for (int j = 0; j < tiles; ++j) {
-    const int t0 = j * kTile, n = min(kTile, sq.len - t0), b = j & 1;
-    const float al = expf(la_n), bt = bt_n;
-    if (j + 1 < tiles) {
-      fetch(j + 1);
-      cp_async_wait<1>();
-    } else {
-      cp_async_wait<0>();
-    }
+    const int t0 = j * kTile, n = min(kTile, sq.len - t0);
+    const RecTile<IO, DK>& tl = sm.tile[j % 3];
+    RecSide& side = sm.side[j & 1];
     if (p.kept_states && t0 % kGdrGradChunk == 0)
       store_row<DK>(p.kept_states +
                         ((((size_t)base + t0 / kGdrGradChunk) * p.seqs.H + h) * p.dv + r0 + grp) * DK, l,
                     reinterpret_cast<const float*>(s));
-    __syncthreads();
-    {  // the staged tokens' scalars: one group of lanes each
-      f2 x[NP], y[NP];
-      load_pairs<DK>(ks[b] + grp * DK, l, x);
-      load_pairs<DK>(qs[b] + grp * DK, l, y);
-      const float kq = group_sum<LPR>(dot2<NP>(x, y));
-      load_pairs<DK>(ks[b] + max(grp - 1, 0) * DK, l, y);
-      const float kk = group_sum<LPR>(dot2<NP>(x, y));
-      if (l == 0) tok[grp] = make_float4(al, bt, kq, kk);
-    }
-    __syncthreads();
     // one token's work, its operands loaded before; k2 and q1 are loaded for the tokens ahead
     f2 ka[NP], kb[NP], kc[NP], qa[NP], qb[NP];
-    load_pairs<DK>(ks[b], l, ka);
-    load_pairs<DK>(ks[b] + min(1, kTile - 1) * DK, l, kb);
-    load_pairs<DK>(qs[b], l, qa);
-    float4 c = tok[0];
-    float v = to_f(vs[b][grp]);
+    load_pairs<DK>(tl.k, l, ka);
+    load_pairs<DK>(tl.k + min(1, kTile - 1) * DK, l, kb);
+    load_pairs<DK>(tl.q, l, qa);
+    float4 c = side.tok[0];
+    float v = to_f(tl.x[grp]);
     float dn = group_sum<LPR>(dot2<NP>(s, ka));  // of the state one token back (here: the present one) with this key
     float a_p = 1.f, u_p = 0.f;
     auto token = [&](int t, f2* k0, f2* k1, f2* k2, f2* q0, f2* q1) {
@@ -236,10 +281,11 @@ __global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_rec_fwd_kernel(RecPa
       const float e = fmaf(-c.x, fmaf(a_p, dn, c.w * u_p), v);
       const float u = c.y * e;
       const float al_t = c.x, kq_t = c.z;
-      c = tok[min(t + 1, kTile - 1)];
-      v = to_f(vs[b][min(t + 1, kTile - 1) * kRows + grp]);
-      load_pairs<DK>(ks[b] + min(t + 2, kTile - 1) * DK, l, k2);
-      load_pairs<DK>(qs[b] + min(t + 1, kTile - 1) * DK, l, q1);
+      const int t1 = min(t + 1, kTile - 1);
+      c = side.tok[t1];
+      v = to_f(tl.x[t1 * kRows + grp]);
+      load_pairs<DK>(tl.k + min(t + 2, kTile - 1) * DK, l, k2);
+      load_pairs<DK>(tl.q + t1 * DK, l, q1);
       const f2 a2 = pair(al_t, al_t), u2 = pair(u, u);
 #pragma unroll
       for (int i = 0; i < NP; ++i) s[i] = fma2(u2, k0[i], mul2(a2, s[i]));
@@ -249,8 +295,8 @@ __global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_rec_fwd_kernel(RecPa
         d2 += __shfl_xor_sync(0xffffffffu, d2, o);
       }
       if (l == 0) {
-        os[t][grp] = p.scale * fmaf(al_t, d2, u * kq_t);
-        es[t][grp] = e;
+        side.out[t][grp] = p.scale * fmaf(al_t, d2, u * kq_t);
+        side.err[t][grp] = e;
       }
       dn = d1;
       a_p = al_t;
@@ -279,102 +325,120 @@ __global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_rec_fwd_kernel(RecPa
       }
     }
     __syncthreads();
-    for (int x = tid; x < n * kRows; x += Cfg::kThreads) {
-      const int t = x / kRows, r = x % kRows;
-      const size_t at = (size_t)(t0 + t) * p.dv + r0 + r;
-      if (og) og[at] = from_f<IO>(os[t][r]);
-      if (p.kept_errors) p.kept_errors[row0 * p.dv + at] = es[t][r];
-    }
   }
+  __syncthreads();
   if (p.state_out) store_row<DK>(p.state_out + st_at, l, reinterpret_cast<const float*>(s));
 }
 
 // The reverse recurrence: w_t for every token, the adjoint C behind every
-// kGdrGradChunk tokens, and the gradient of the state on entry.
+// kGdrGradChunk tokens, and the gradient of the state on entry.  Step x takes
+// tile tiles - 1 - x.
 template <typename IO, int DK>
-__global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_rec_bwd_kernel(RecParams p) {
+__global__ void __launch_bounds__(2 * RowCfg<DK>::kThreads) gdr_rec_bwd_kernel(RecParams p) {
   using Cfg = RowCfg<DK>;
-  constexpr int LPR = Cfg::kLpr, EPL = Cfg::kEpl, NP = EPL / 2;
-  __shared__ __align__(16) IO ks[2][kTile * DK];
-  __shared__ __align__(16) IO qs[2][kTile * DK];
-  __shared__ __align__(16) IO ds[2][kTile * kRows];
-  __shared__ float ws[kTile][kRows];
-  __shared__ float4 tok[kTile];  // alpha_t, beta_t, q_t.k_t, q_t.k_{t-1}
-  __shared__ float kks[kTile];   // k_t.k_{t-1}
+  constexpr int LPR = Cfg::kLpr, NP = Cfg::kEpl / 2, NT = Cfg::kThreads;
+  extern __shared__ __align__(16) unsigned char raw[];
+  RecSm<IO, DK>& sm = *reinterpret_cast<RecSm<IO, DK>*>(raw);
 
   const int slices = p.dv / kRows;
   const int sl = blockIdx.x % slices;
   const int h = (blockIdx.x / slices) % p.seqs.H;
   const int seq = blockIdx.x / slices / p.seqs.H;
-  const int tid = threadIdx.x, grp = tid / LPR, l = tid % LPR;
+  const bool helper = threadIdx.x >= NT;
+  const int tid = threadIdx.x % NT, grp = tid / LPR, l = tid % LPR;
   const int r0 = sl * kRows;
   GdrSeq sq;
   if (!gdr_seq(p.seqs, seq, sq)) {
-    if (tid == 0) raise_error(p.err, kErrDeviceArg);
+    if (threadIdx.x == 0) raise_error(p.err, kErrDeviceArg);
     return;
   }
   const int hk = h / (p.seqs.H / p.seqs.Hk);
   const size_t row0 = ((size_t)sq.row_b * p.seqs.H + h) * p.seqs.T + sq.start;
   const size_t krow0 = ((size_t)sq.row_b * p.seqs.Hk + hk) * p.seqs.T + sq.start;
-  const IO* qg = static_cast<const IO*>(p.q) + krow0 * DK;
-  const IO* kg = static_cast<const IO*>(p.k) + krow0 * DK;
-  const IO* dg = static_cast<const IO*>(p.dout) + row0 * p.dv;
-  const size_t st_at = (((size_t)seq * p.seqs.H + h) * p.dv + r0 + grp) * DK;
+  const int tiles = (sq.len + kTile - 1) / kTile;
 
+  if (helper) {
+    const IO* qg = static_cast<const IO*>(p.q) + krow0 * DK;
+    const IO* kg = static_cast<const IO*>(p.k) + krow0 * DK;
+    const IO* dg = static_cast<const IO*>(p.dout) + row0 * p.dv;
+    float la = 0.f, bt = 0.f;
+    auto fetch = [&](int x) {
+      if (x < tiles) {
+        const int t0 = (tiles - 1 - x) * kTile, n = min(kTile, sq.len - t0);
+        RecTile<IO, DK>& t = sm.tile[x % 3];
+        stage(t.k, kg + (size_t)t0 * DK, n, DK, 0, DK, tid, NT);
+        stage(t.q, qg + (size_t)t0 * DK, n, DK, 0, DK, tid, NT);
+        stage(t.x, dg + (size_t)t0 * p.dv, n, p.dv, r0, kRows, tid, NT);
+      }
+      cp_async_commit();
+    };
+    auto gates = [&](int x) {
+      const int t = (tiles - 1 - x) * kTile + grp;
+      if (l == 0 && x < tiles && t < sq.len) {
+        la = p.log_alpha[row0 + t];
+        bt = p.beta[row0 + t];
+      }
+    };
+    auto products = [&](int x) {
+      cp_async_wait<1>();
+      named_bar_sync(kHelpBar, NT);
+      const RecTile<IO, DK>& t = sm.tile[x % 3];
+      f2 a[NP], b[NP], z[NP];
+      load_pairs<DK>(t.k + grp * DK, l, a);
+      load_pairs<DK>(t.q + grp * DK, l, b);
+      load_pairs<DK>(t.k + max(grp - 1, 0) * DK, l, z);
+      const float qk = group_sum<LPR>(dot2<NP>(a, b)), qk1 = group_sum<LPR>(dot2<NP>(b, z));
+      const float kk = group_sum<LPR>(dot2<NP>(a, z));
+      if (l == 0) {
+        sm.side[x & 1].tok[grp] = make_float4(expf(la), bt, qk, qk1);
+        sm.side[x & 1].more[grp] = kk;
+      }
+    };
+    gates(0);
+    fetch(0);
+    fetch(1);
+    if (tiles) products(0);
+    __syncthreads();
+    for (int x = 0; x <= tiles; ++x) {
+      if (x > 0) {
+        const int t0 = (tiles - x) * kTile, n = min(kTile, sq.len - t0);
+        const RecSide& side = sm.side[(x - 1) & 1];
+        for (int e = tid; e < n * kRows; e += NT) {
+          const int t = e / kRows, r = e % kRows;
+          p.kept_w[(row0 + t0 + t) * p.dv + r0 + r] = side.out[t][r];
+        }
+      }
+      gates(x + 1);
+      fetch(x + 2);
+      if (x + 1 < tiles) products(x + 1);
+      __syncthreads();
+    }
+    cp_async_wait<0>();
+    return;
+  }
+
+  const size_t st_at = (((size_t)seq * p.seqs.H + h) * p.dv + r0 + grp) * DK;
+  const int base = gdr_slot_base(p.seqs, seq, sq.start, kGdrGradChunk);
   f2 a[NP];
   if (p.dstate_out) load_pairs<DK>(p.dstate_out + st_at, l, a);
   else
 #pragma unroll
     for (int i = 0; i < NP; ++i) a[i] = 0;
-
-  const int tiles = (sq.len + kTile - 1) / kTile;
-  const int base = gdr_slot_base(p.seqs, seq, sq.start, kGdrGradChunk);
-  float la_n = 0.f, bt_n = 0.f;
-  auto fetch = [&](int j) {
-    const int t0 = j * kTile, n = min(kTile, sq.len - t0), b = j & 1;
-    stage(ks[b], kg + (size_t)t0 * DK, n, DK, 0, DK);
-    stage(qs[b], qg + (size_t)t0 * DK, n, DK, 0, DK);
-    stage(ds[b], dg + (size_t)t0 * p.dv, n, p.dv, r0, kRows);
-    cp_async_commit();
-    if (l == 0 && grp < n) {
-      la_n = p.log_alpha[row0 + t0 + grp];
-      bt_n = p.beta[row0 + t0 + grp];
-    }
-  };
-  if (tiles) fetch(tiles - 1);
-  for (int j = tiles - 1; j >= 0; --j) {
-    const int t0 = j * kTile, n = min(kTile, sq.len - t0), b = j & 1;
-    const float al = expf(la_n), bt = bt_n;
-    if (j > 0) {
-      fetch(j - 1);
-      cp_async_wait<1>();
-    } else {
-      cp_async_wait<0>();
-    }
+  __syncthreads();
+  for (int x = 0; x < tiles; ++x) {
+    const int t0 = (tiles - 1 - x) * kTile, n = min(kTile, sq.len - t0);
+    const RecTile<IO, DK>& tl = sm.tile[x % 3];
+    RecSide& side = sm.side[x & 1];
     if (t0 + n == sq.len || (t0 + n) % kGdrGradChunk == 0)
       store_row<DK>(p.kept_adjoints +
                         ((((size_t)base + t0 / kGdrGradChunk) * p.seqs.H + h) * p.dv + r0 + grp) * DK, l,
                     reinterpret_cast<const float*>(a));
-    __syncthreads();
-    {
-      f2 x[NP], y[NP], z[NP];
-      load_pairs<DK>(ks[b] + grp * DK, l, x);
-      load_pairs<DK>(qs[b] + grp * DK, l, y);
-      load_pairs<DK>(ks[b] + max(grp - 1, 0) * DK, l, z);
-      const float qk = group_sum<LPR>(dot2<NP>(x, y)), qk1 = group_sum<LPR>(dot2<NP>(y, z));
-      const float kk = group_sum<LPR>(dot2<NP>(x, z));
-      if (l == 0) {
-        tok[grp] = make_float4(al, bt, qk, qk1);
-        kks[grp] = kk;
-      }
-    }
-    __syncthreads();
     f2 ka[NP], kb[NP], kc[NP], qa[NP], qb[NP];
-    load_pairs<DK>(ks[b] + (n - 1) * DK, l, ka);
-    load_pairs<DK>(ks[b] + max(n - 2, 0) * DK, l, kb);
-    load_pairs<DK>(qs[b] + (n - 1) * DK, l, qa);
-    float4 c = tok[n - 1];
-    float kk = kks[n - 1], d = p.scale * to_f(ds[b][(n - 1) * kRows + grp]);
+    load_pairs<DK>(tl.k + (n - 1) * DK, l, ka);
+    load_pairs<DK>(tl.k + max(n - 2, 0) * DK, l, kb);
+    load_pairs<DK>(tl.q + (n - 1) * DK, l, qa);
+    float4 c = side.tok[n - 1];
+    float kk = side.more[n - 1], d = p.scale * to_f(tl.x[(n - 1) * kRows + grp]);
     float ck = group_sum<LPR>(dot2<NP>(a, ka));  // C_t.k_t
     auto token = [&](int t, f2* k0, f2* k1, f2* k2, f2* q0, f2* q1) {
       float d1 = dot2<NP>(a, k1);
@@ -383,16 +447,16 @@ __global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_rec_bwd_kernel(RecPa
       const float rest = fmaf(d, c.w, bw * kk);
       const f2 al2 = pair(al_t, al_t), d2 = pair(d, d), w2 = pair(bw, bw);
       const int t1 = max(t - 1, 0);
-      c = tok[t1];
-      kk = kks[t1];
-      d = p.scale * to_f(ds[b][t1 * kRows + grp]);
-      load_pairs<DK>(ks[b] + max(t - 2, 0) * DK, l, k2);
-      load_pairs<DK>(qs[b] + t1 * DK, l, q1);
+      c = side.tok[t1];
+      kk = side.more[t1];
+      d = p.scale * to_f(tl.x[t1 * kRows + grp]);
+      load_pairs<DK>(tl.k + max(t - 2, 0) * DK, l, k2);
+      load_pairs<DK>(tl.q + t1 * DK, l, q1);
 #pragma unroll
       for (int i = 0; i < NP; ++i) a[i] = mul2(al2, fma2(w2, k0[i], fma2(d2, q0[i], a[i])));
       d1 = group_sum<LPR>(d1);
       ck = al_t * (d1 + rest);
-      if (l == 0) ws[t][grp] = w;
+      if (l == 0) side.out[t][grp] = w;
     };
     if (n == kTile) {
 #pragma unroll 1
@@ -417,11 +481,8 @@ __global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_rec_bwd_kernel(RecPa
       }
     }
     __syncthreads();
-    for (int x = tid; x < n * kRows; x += Cfg::kThreads) {
-      const int t = x / kRows, r = x % kRows;
-      p.kept_w[(row0 + t0 + t) * p.dv + r0 + r] = ws[t][r];
-    }
   }
+  __syncthreads();
   if (p.dstate_in) store_row<DK>(p.dstate_in + st_at, l, reinterpret_cast<const float*>(a));
 }
 
@@ -510,14 +571,20 @@ ll_status by_type(ll_dtype io, int dk, A... args) {
 
 template <typename IO, int DK> struct RecFwd {
   static ll_status run(const RecParams& p, unsigned grid, cudaStream_t st) {
-    gdr_rec_fwd_kernel<IO, DK><<<grid, RowCfg<DK>::kThreads, 0, st>>>(p);
+    constexpr int smem = (int)sizeof(RecSm<IO, DK>);
+    if (smem > 48 * 1024)
+      LL_CUDA_OK(cudaFuncSetAttribute(gdr_rec_fwd_kernel<IO, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    gdr_rec_fwd_kernel<IO, DK><<<grid, 2 * RowCfg<DK>::kThreads, smem, st>>>(p);
     LL_CUDA_OK(cudaGetLastError());
     return LL_OK;
   }
 };
 template <typename IO, int DK> struct RecBwd {
   static ll_status run(const RecParams& p, unsigned grid, cudaStream_t st) {
-    gdr_rec_bwd_kernel<IO, DK><<<grid, RowCfg<DK>::kThreads, 0, st>>>(p);
+    constexpr int smem = (int)sizeof(RecSm<IO, DK>);
+    if (smem > 48 * 1024)
+      LL_CUDA_OK(cudaFuncSetAttribute(gdr_rec_bwd_kernel<IO, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    gdr_rec_bwd_kernel<IO, DK><<<grid, 2 * RowCfg<DK>::kThreads, smem, st>>>(p);
     LL_CUDA_OK(cudaGetLastError());
     return LL_OK;
   }
