@@ -17,7 +17,10 @@
 // Wd, w0, Bc; parallel over chunks), the scans (sequential over a sequence's
 // chunks, parallel over heads and slices of 32 d_v columns), and the outputs or
 // gradients (parallel over chunks; formulas of the latter in gdr_grad.cu).
+#include <cudaTypedefs.h>
+
 #include <algorithm>
+#include <atomic>
 
 #include "gdr_tc.cuh"
 
@@ -92,31 +95,236 @@ __device__ __noinline__ void find_item(const TcParams& p, int it, int step, Item
 }
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-template <bool BWD> struct PrepSm {
-  static constexpr uint32_t kX0 = 0;                               // K
-  static constexpr uint32_t kX1 = kTile;                           // V (forward), Q (backward)
-  static constexpr uint32_t kX2 = 2 * kTile;                       // backward: V, dO
-  static constexpr uint32_t kM = (BWD ? 3 : 2) * kTile;            // M, float32; then operands in two parts
+struct PrepSm {
+  static constexpr uint32_t kX0 = 0;                               // K (forward: of every other chunk)
+  static constexpr uint32_t kX1 = kTile;                           // Q (forward: K of the others)
+  static constexpr uint32_t kX2 = 2 * kTile;                       // V; backward then dO
+  static constexpr uint32_t kM = 3 * kTile;                        // M, float32; then operands in two parts
   static constexpr uint32_t kR = kM + kMatB;                       // A, float32; then likewise
   static constexpr uint32_t kTab = kR + 2 * kTile;
   static constexpr uint32_t kBars = kTab + 5 * kC * 4 + 32 + 3 * 64 + 16;
-  static constexpr uint32_t kNext = kBars + 32;
-  static constexpr uint32_t kBytes = kNext + sizeof(Item);
+  static constexpr uint32_t kNext = kBars + 7 * 8;
+  static constexpr uint32_t kBytes = kNext + 2 * sizeof(Item);
 };
-static_assert(kMatB == 2 * kTile && PrepSm<true>::kBars % 8 == 0, "tile alignment");
-static_assert(PrepSm<true>::kBytes <= 232448, "shared memory budget of one CTA");
+static_assert(kMatB == 2 * kTile && PrepSm::kBars % 8 == 0, "tile alignment");
+static_assert(PrepSm::kBytes <= 232448, "shared memory budget of one CTA");
+struct TcMaps {  // [rows, d] bf16, boxes of 64 columns and 128 rows
+  CUtensorMap q, k, v, dout;
+};
 
 constexpr float kScoreDown = 1.f / 256.f;  // of the scores Q K^T of scaled tiles, as operands
 constexpr float kKeysDown = 1.f / 4096.f;   // of K K^T of the scaled tile
 constexpr float kRowsDown = 1.f / 16.f;    // of P^T dO, as an operand
 
-// Persistent, one CTA per SM, an item per (chunk, head).  Thread = (row, quarter
-// of the columns); while warps 0 to 7 solve for M, the others make operands of the
-// inputs that are not needed before, and look for the next item.
+// Both are persistent, one CTA per SM, an item per (chunk, head).  Thread = (row,
+// quarter of the columns); while warps 0 to 7 solve for M, the others prepare
+// what is needed next.
 constexpr int kPrepThreads = 512, kPrepBar2 = 2;
-template <bool BWD>
-__global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
-  using Sm = PrepSm<BWD>;
+
+// The forward's.  Warps 8 to 15 make V's operand and, a whole item ahead, everything
+// of the next chunk up to K K^T.
+__global__ void __launch_bounds__(kPrepThreads, 1)
+    gdr_prep_fwd_kernel(const __grid_constant__ TcMaps maps, TcParams p) {
+  using Sm = PrepSm;
+  extern __shared__ __align__(1024) unsigned char s[];
+  if (smem_u32(s) & 1023u) {
+    if (threadIdx.x == 0) atomicOr(p.err, kErrDeviceArg);
+    return;
+  }
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int q = warp & 3, qt = warp >> 2;
+  const int i = 32 * q + lane;  // this thread's row (TMEM lane), columns 32 qt ..
+  float2* gs = reinterpret_cast<float2*>(s + Sm::kTab);
+  float* bs = reinterpret_cast<float*>(gs + kC);
+  float* in_s = bs + kC;
+  float2* tot = reinterpret_cast<float2*>(in_s + kC);
+  uint32_t* red = reinterpret_cast<uint32_t*>(tot + 4);  // 2 x 8
+  float* inv = reinterpret_cast<float*>(red + 16);       // inverse scales: V, K of both buffers
+  uint64_t* bar = reinterpret_cast<uint64_t*>(s + Sm::kBars);  // K K^T, U, W, K loads 0 and 1, V load
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s + Sm::kBars + 6 * 8);
+  Item* next = reinterpret_cast<Item*>(s + Sm::kNext);
+  float* Ap = reinterpret_cast<float*>(s + Sm::kR);
+  float* Mp = reinterpret_cast<float*>(s + Sm::kM);
+  unsigned char *M = s + Sm::kM, *X0 = s + Sm::kX0, *XV = s + Sm::kX2, *R = s + Sm::kR;
+  const uint32_t sX0 = smem_u32(X0), sXV = smem_u32(XV), sR = smem_u32(R), sM = smem_u32(M);
+  const int items = p.slots * p.seqs.H, G = p.seqs.H / p.seqs.Hk;
+  if (tid == 0) {
+    for (int b = 0; b < 6; ++b) mbar_init(bar + b, 1);
+    fence_mbar_init();
+    find_item(p, blockIdx.x, gridDim.x, next);
+    find_item(p, next->it + gridDim.x, gridDim.x, next + 1);
+  }
+  __syncwarp();
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + 32 * qt;
+
+  const int t = tid - 256;  // of the threads of warps 8 to 15
+  float beta_n = 0.f;       // thread t < 128: the next item's token's beta, scaled
+  auto load_k = [&](const Item& x, int b) { load_tile(X0 + b * kTile, &maps.k, (int)x.krow0, bar + 3 + b); };
+  // decays, K's operand and K K^T of item x, number j of this CTA (warps 8 to 15)
+  auto stage_keys = [&](const Item& x, int j) {
+    const int b = j & 1, slot = x.it / p.seqs.H, h = x.it - slot * p.seqs.H;
+    const bool mine = t < x.n;
+    const float la = mine ? gdr_log(p.log_alpha[x.row0 + t]) : 0.f, bt = mine ? p.beta[x.row0 + t] : 0.f;
+    chunk_decays(la, gs, tot, t, kPrepBar2, 256);
+    wait_bar(bar + 3 + b, (j >> 1) & 1, p.err);
+    const float ik = tile_to_f16<256>(X0 + b * kTile, x.n, red, t, kPrepBar2, nullptr);
+    // A is K K^T of the scaled tile / 4096, beta takes the difference
+    beta_n = bt * (ik * ik / kKeysDown);
+    Tables& tb = p.tab[x.it];
+    if (t < kC) {
+      const float2 g = gs[t];
+      tb.g[t] = g;
+      tb.into[t] = exp_diff(g, make_float2(0.f, 0.f));
+      tb.out[t] = exp_diff(gs[kC - 1], g);
+    }
+    tc_fence_before();
+    named_bar_sync(kPrepBar2, 256);
+    if (t == 0) {
+      inv[1 + b] = ik;
+      tb.ik = ik;
+      tc_fence_after();
+      mma_tile<false, false>(tmem, sX0 + b * kTile, sX0 + b * kTile, false);
+      umma_commit(bar);
+      if (h % G == 0) {
+        bulk_store(p.K16 + ((size_t)slot * p.seqs.Hk + h / G) * kTile, X0 + b * kTile, kTile);
+        bulk_commit();
+      }
+    }
+    __syncwarp();
+  };
+
+  Item me = next[0];
+  if (me.it < items) {
+    if (t == 0) {
+      load_k(me, 0);
+      load_tile(XV, &maps.v, (int)me.row0, bar + 5);
+      if (next[1].it < items) load_k(next[1], 1);
+    }
+    __syncwarp();
+    if (warp >= 8) stage_keys(me, 0);
+  }
+  for (int j = 0; me.it < items; ++j) {
+    const int it = me.it, b = j & 1;
+    const int slot = it / p.seqs.H, h = it - slot * p.seqs.H;
+    const size_t sh = (size_t)me.seq * p.seqs.H + h;
+    wait_bar(bar, j & 1, p.err);
+    __syncwarp();
+    tc_fence_after();
+    if (tid == 0) bulk_wait_read0();  // U and W of the item before have left
+    __syncthreads();
+    const Item nx = next[b ^ 1];
+    const float2 gi = gs[i];
+    if (t >= 0 && t < kC) {
+      bs[t] = beta_n;
+      in_s[t] = exp_diff(gs[t], make_float2(0.f, 0.f));
+    }
+    // A_ij = (k_i . k_j) G_ij, j < i
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c) {
+      const int j0 = 32 * qt + 16 * c;
+      if (j0 > 32 * q + 31) break;  // (warp-uniform) above the diagonal
+      float x[16];
+      decayed16(x, tl + 16 * c, gs, gi, j0, i, kKeysDown);
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        mat4(Ap, i, (j0 >> 2) + v) = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp < 8) {
+      tri_solve(Ap, Mp, bs, tid);
+    } else {
+      wait_bar(bar + 5, j & 1, p.err);
+      uint32_t vbits;
+      const float iv = tile_to_f16<256>(XV, me.n, red + 8, t, kPrepBar2, &vbits);
+      if (t == 0) {
+        atomicMax(p.amax_s + sh, vbits);
+        inv[0] = iv;
+      }
+      if (p.state_in && me.chunk == 0) {
+        const float* st = p.state_in + sh * p.dv * p.dk;
+        uint32_t m = 0;
+#pragma unroll 4
+        for (int e = t; e < p.dv * p.dk; e += 256) m = max(m, __float_as_uint(fabsf(st[e])));
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0) atomicMax(p.amax_s + sh, m);
+      }
+      if (nx.it < items) {
+        stage_keys(nx, j + 1);
+        if (t == 255) {  // the item after the next, V of the next on its way into L2
+          find_item(p, nx.it + gridDim.x, gridDim.x, next + b);
+          bulk_prefetch_l2(p.v + nx.row0 * p.dv, (uint32_t)(nx.n * p.dv * 2));
+        }
+      }
+    }
+    __syncthreads();
+    // ---- U = T' V -> 256, W = T' diag(exp(g)) K -> 384
+    const float iv = inv[0], ik = inv[1 + b];
+    float m[32];
+    load_m(m, Mp, i, qt);
+    __syncthreads();
+    put_inverse2(R, M, m, i, qt, bs, in_s);
+    fence_proxy_async_shared();
+    __syncthreads();
+    if (tid == 0) {
+      tc_fence_after();
+      mma_tile<false, true>(tmem + 256, sR + kTile, sXV, false);
+      mma_tile<false, true>(tmem + 256, sR, sXV, true);
+      umma_commit(bar + 1);
+      mma_tile<false, true>(tmem + 384, sM + kTile, sX0 + b * kTile, false);
+      mma_tile<false, true>(tmem + 384, sM, sX0 + b * kTile, true);
+      umma_commit(bar + 2);
+    }
+    __syncwarp();
+    wait_bar(bar + 1, j & 1, p.err);
+    __syncwarp();
+    tc_fence_after();
+    if (t == 0 && nx.it < items) load_tile(XV, &maps.v, (int)nx.row0, bar + 5);
+    __syncwarp();
+    // U and W leave by way of the operands' places
+    write_rows(reinterpret_cast<float*>(R), tl + 256, i, qt, iv);
+    wait_bar(bar + 2, j & 1, p.err);
+    __syncwarp();
+    tc_fence_after();
+    if (t == 0 && nx.it < items && next[b].it < items) {
+      bulk_wait_read0();  // this item's K16 (and the next one's)
+      load_k(next[b], b);
+    }
+    __syncwarp();
+    write_tiles(M, M + kTile, tl + 384, i, qt, ik, kLoScale);
+    fence_proxy_async_shared();
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0) {
+      bulk_store(p.U + (size_t)it * kC * kC, R, kMatB);
+      bulk_store(p.W + (size_t)it * 2 * kTile, M, 2 * kTile);
+      bulk_commit();
+    }
+    __syncwarp();
+    me = nx;
+  }
+  if (tid == 0 || t == 0) bulk_wait0();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// The backward's.
+__global__ void __launch_bounds__(kPrepThreads, 1)
+    gdr_prep_bwd_kernel(const __grid_constant__ TcMaps maps, TcParams p) {
+  using Sm = PrepSm;
   extern __shared__ __align__(1024) unsigned char s[];
   if (smem_u32(s) & 1023u) {
     if (threadIdx.x == 0) atomicOr(p.err, kErrDeviceArg);
@@ -133,17 +341,17 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
   uint32_t* red = reinterpret_cast<uint32_t*>(tot + 4);  // 3 x 16
   float* inv = reinterpret_cast<float*>(red + 48);       // inverse scales of V and Q
   uint64_t* bar = reinterpret_cast<uint64_t*>(s + Sm::kBars);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s + Sm::kBars + 8);
+  // bar: products, K, U, Q, V and dO
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s + Sm::kBars + 6 * 8);
   Item* next = reinterpret_cast<Item*>(s + Sm::kNext);
   float* Ap = reinterpret_cast<float*>(s + Sm::kR);
   float* Mp = reinterpret_cast<float*>(s + Sm::kM);
   unsigned char* M = s + Sm::kM;
-  unsigned char *X0 = s + Sm::kX0, *X1 = s + Sm::kX1, *XV = s + (BWD ? Sm::kX2 : Sm::kX1), *R = s + Sm::kR;
+  unsigned char *X0 = s + Sm::kX0, *X1 = s + Sm::kX1, *XV = s + Sm::kX2, *R = s + Sm::kR;
   const uint32_t sX0 = smem_u32(X0), sX1 = smem_u32(X1), sXV = smem_u32(XV), sR = smem_u32(R),
                  sM = smem_u32(M);
   if (tid == 0) {
-    mbar_init(bar, 1);
-    mbar_init(bar + 2, 1);
+    for (int b = 0; b < 5; ++b) mbar_init(bar + b, 1);
     fence_mbar_init();
     find_item(p, blockIdx.x, gridDim.x, next);
   }
@@ -190,17 +398,23 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
   const int items = p.slots * p.seqs.H, G = p.seqs.H / p.seqs.Hk;
   float la = 0.f, bt = 0.f;  // this thread's token's, of the item that is loaded
   auto load_keys = [&](const Item& x) {
-    load_tile(X0, p.k + x.krow0 * p.dk, x.n, p.dk, tid, kPrepThreads);
-    if (BWD) load_tile(X1, p.q + x.krow0 * p.dk, x.n, p.dk, tid, kPrepThreads);
+    if (tid == 0) {
+      load_tile(X0, &maps.k, (int)x.krow0, bar + 1);
+      load_tile(X1, &maps.q, (int)x.krow0, bar + 3);
+    }
+    __syncwarp();
     la = tid < x.n ? gdr_log(p.log_alpha[x.row0 + tid]) : 0.f;
     bt = tid < x.n ? p.beta[x.row0 + tid] : 0.f;
   };
-  auto load_values = [&](const Item& x) { load_tile(XV, p.v + x.row0 * p.dv, x.n, p.dv, tid, kPrepThreads); };
+  uint32_t nv = 0, nkq = 0;  // loads of V and dO, and of K, waited for
+  auto load_values = [&](const CUtensorMap* map, size_t row) {
+    if (tid == 0) load_tile(XV, map, (int)row, bar + 4);
+    __syncwarp();
+  };
   Item me = *next;
   if (me.it < items) {
     load_keys(me);
-    load_values(me);
-    cp_async_commit();
+    load_values(&maps.v, me.row0);
   }
   while (me.it < items) {
     const int it = me.it, n = me.n;
@@ -212,7 +426,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
     unsigned char* Wdg = p.Wd + (size_t)it * 2 * kTile;
     const float beta_i = bt;
     const bool t_end = me.t0 + n == me.len;
-    chunk_decays(la, gs, tot, tid);
+    chunk_decays(la, gs, tot, tid, 0, kPrepThreads);
     const float2 gi = gs[i];
     if (qt == 0) {
       const float in = exp_diff(gi, make_float2(0.f, 0.f)), out = exp_diff(gs[kC - 1], gi);
@@ -221,12 +435,11 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
       tb.g[i] = gi;
       tb.into[i] = in;
       tb.out[i] = out;
-      if (BWD) tb.rel[i] = exp_diff(gi, gs[0]);
+      tb.rel[i] = exp_diff(gi, gs[0]);
     }
     if (p.state_in && me.chunk == 0) raise_max(am_s, state_max(p.state_in + sh * p.dv * p.dk));
-    cp_async_wait<0>();
-    __syncthreads();
-    const float ik = tile_to_f16<kPrepThreads>(X0, red, tid, 0, nullptr);
+    wait_bar(bar + 1, nkq & 1, p.err);
+    const float ik = tile_to_f16<kPrepThreads>(X0, n, red, tid, 0, nullptr);
     // A is K K^T of the scaled tile / 4096, beta takes the difference
     if (tid < kC) bs[tid] = beta_i * (ik * ik / kKeysDown);
     // ---- K K^T -> 0
@@ -257,9 +470,10 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
     } else {
       const int t = tid - 256;
       uint32_t vbits;
-      const float iv = tile_to_f16<256>(XV, red + 16, t, kPrepBar2, &vbits);
-      float iq = 1.f;
-      if (BWD) iq = tile_to_f16<256>(X1, red + 32, t, kPrepBar2, nullptr);
+      wait_bar(bar + 4, nv & 1, p.err);
+      const float iv = tile_to_f16<256>(XV, n, red + 16, t, kPrepBar2, &vbits);
+      wait_bar(bar + 3, nkq & 1, p.err);
+      const float iq = tile_to_f16<256>(X1, n, red + 32, t, kPrepBar2, nullptr);
       if (t == 0) {
         atomicMax(am_s, vbits);
         inv[0] = iv;
@@ -276,11 +490,11 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
           const char* dp = reinterpret_cast<const char*>(p.dout + next->row0 * p.dv);
           for (int x = lane * 128; x < next->n * p.dk * 2; x += 32 * 128) {
             prefetch_l2(kp + x);
-            if (BWD) prefetch_l2(qp + x);
+            prefetch_l2(qp + x);
           }
           for (int x = lane * 128; x < next->n * p.dv * 2; x += 32 * 128) {
             prefetch_l2(vp + x);
-            if (BWD) prefetch_l2(dp + x);
+            prefetch_l2(dp + x);
           }
           if (lane * 32 < next->n) {
             prefetch_l2(p.log_alpha + next->row0 + lane * 32);
@@ -291,6 +505,8 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
     }
     __syncthreads();
     me = *next;
+    ++nv;
+    ++nkq;
     const float iv = inv[0], iq = inv[1], bi = bs[i];
     // ---- U = T' V -> 256 (with Q K^T -> 128), W = T' diag(exp(g)) K -> 384
     float m[32];
@@ -301,10 +517,10 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
       mma_tile<false, true>(tmem + 256, sR + kTile, sXV, false);
       mma_tile<false, true>(tmem + 256, sR, sXV, true);
       umma_commit(bar + 2);
-      if (BWD) mma_tile<false, false>(tmem + 128, sX1, sX0, false);
+      mma_tile<false, false>(tmem + 128, sX1, sX0, false);
       mma_tile<false, true>(tmem + 384, sM + kTile, sX0, false);
       mma_tile<false, true>(tmem + 384, sM, sX0, true);
-      if (BWD && h % G == 0) {
+      if (h % G == 0) {
         bulk_store(p.Q16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, X1, kTile);
         bulk_commit();
       }
@@ -312,37 +528,16 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
     wait_bar(bar + 2, items_done++ & 1, p.err);
     __syncwarp();
     tc_fence_after();
-    if (!BWD) {
-      // U and W leave by way of the operands' places, the next item's inputs arrive meanwhile
-      write_rows(reinterpret_cast<float*>(R), tl + 256, i, qt, iv);
-      wait_mma();
-      write_tiles(M, M + kTile, tl + 384, i, qt, ik, kLoScale);
-      if (tid == 0) bulk_wait_read0();  // K16
-      fence_proxy_async_shared();
-      tc_fence_before();
-      __syncthreads();
-      if (tid == 0) {
-        bulk_store(p.U + (size_t)it * kC * kC, R, kMatB);
-        bulk_store(Wg, M, 2 * kTile);
-        bulk_commit();
-      }
-      __syncwarp();
-      if (me.it < items) {
-        load_keys(me);
-        load_values(me);
-        cp_async_commit();
-      }
-    } else {
-      load_tile(XV, p.dout + row0 * p.dv, n, p.dv, tid, kPrepThreads);  // (V has been read)
-      cp_async_commit();
+    {
+      load_values(&maps.dout, row0);  // (V has been read)
       write_rows(p.U + (size_t)it * kC * kC, tl + 256, i, qt, iv);
       const float rel = exp_diff(gi, gs[0]), in0 = in_s[0];
       // ---- Wd = T^T diag(exp(g_C - g)) K -> 0, Bc = Q^T diag(exp(g)) dO -> 256 (exp(g_0) and its scales below)
       put_inverse(R, R + kTile, m, i, qt, out_s[i], bi);
-      cp_async_wait<0>();
       wait_mma();
-      __syncthreads();
-      const float id = tile_to_f16<kPrepThreads>(XV, red, tid, 0, nullptr);
+      wait_bar(bar + 4, nv & 1, p.err);
+      ++nv;
+      const float id = tile_to_f16<kPrepThreads>(XV, n, red, tid, 0, nullptr);
       __syncthreads();
 #pragma unroll 1
       for (int c8 = 0; c8 < 4; ++c8) {
@@ -386,7 +581,6 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
       const bool last = p.dstate_out && t_end;
       if (me.it < items) {  // K and Q have been read
         load_keys(me);
-        cp_async_commit();
       }
       write_tiles(Wdg, Wdg + kTile, tl, i, qt, ik, kLoScale);
       wait_mma();
@@ -399,8 +593,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1) gdr_prep_kernel(TcParams p) {
         mma_tile<true, true>(tmem, sR, sM, true);
       });
       if (me.it < items) {
-        load_values(me);
-        cp_async_commit();
+        load_values(&maps.v, me.row0);
       }
       uint32_t mx = write_rows(p.Bc + (size_t)it * kC * kC, tl + 256, i, qt, p.scale * iq * id * in0);
       if (last) mx = max(mx, state_max(p.dstate_out + sh * p.dv * p.dk));
@@ -789,10 +982,10 @@ constexpr uint32_t kOK = kOQ + kTile;        // K; then the masked scores
 constexpr uint32_t kOS = kOK + kTile;        // X; then u
 constexpr uint32_t kOTab = kOS + kTile;
 constexpr uint32_t kOBars = kOTab + 2 * kC * 4 + 32;
-constexpr uint32_t kOutSmem = kOBars + 24;
+constexpr uint32_t kOutSmem = kOBars + 32;
 
 // One CTA per (chunk, head), two per SM.
-__global__ void __launch_bounds__(256, 2) gdr_out_kernel(TcParams p) {
+__global__ void __launch_bounds__(256, 2) gdr_out_kernel(const __grid_constant__ TcMaps maps, TcParams p) {
   extern __shared__ __align__(1024) unsigned char s[];
   if (smem_u32(s) & 1023u) {
     if (threadIdx.x == 0) atomicOr(p.err, kErrDeviceArg);
@@ -810,19 +1003,17 @@ __global__ void __launch_bounds__(256, 2) gdr_out_kernel(TcParams p) {
   const size_t krow0 = ((size_t)sq.row_b * p.seqs.Hk + hk) * p.seqs.T + sq.start + t0;
   float2* gs = reinterpret_cast<float2*>(s + kOTab);
   uint32_t* red = reinterpret_cast<uint32_t*>(gs + kC);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s + kOBars);  // 0: K and X, then u; 1: products
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s + kOBars + 16);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s + kOBars);  // 0: K and X, then u; 1: products; 2: Q
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s + kOBars + 24);
   const uint32_t sQ = smem_u32(s + kOQ), sK = smem_u32(s + kOK), sS = smem_u32(s + kOS);
   if (tid == 0) {
-    mbar_init(bars, 1);
-    mbar_init(bars + 1, 1);
+    for (int b = 0; b < 3; ++b) mbar_init(bars + b, 1);
     fence_mbar_init();
+    load_tile(s + kOQ, &maps.q, (int)krow0, bars + 2);
     mbar_arrive_expect_tx(bars, 2 * kTile);
     bulk_load(s + kOK, p.K16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, kTile, bars);
     bulk_load(s + kOS, p.S + (size_t)it * kTile, kTile, bars);
   }
-  load_tile(s + kOQ, p.q + krow0 * p.dk, n, p.dk, tid, 256);
-  cp_async_commit();
   __syncwarp();
   if (warp == 0) {
     tmem_alloc(tmem_slot, 256);
@@ -830,13 +1021,13 @@ __global__ void __launch_bounds__(256, 2) gdr_out_kernel(TcParams p) {
   }
   if (tid < kC) gs[tid] = p.tab[it].g[tid];
   const float ik = p.tab[it].ik, isf = operand_scale(__uint_as_float(p.amax_s[(size_t)seq * p.seqs.H + h])).y;
-  cp_async_wait<0>();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + 64 * hf;
-  const float iq = tile_to_f16<256>(s + kOQ, red, tid, 0, nullptr);
+  wait_bar(bars + 2, 0, p.err);
+  const float iq = tile_to_f16<256>(s + kOQ, n, red, tid, 0, nullptr);
   __syncthreads();
   if (tid == 0) {
     wait_bar(bars, 0, p.err);
@@ -1276,13 +1467,44 @@ template <int MODE> ll_status scan(const GdrArgs& a, const TcParams& p, int slic
   LL_CUDA_OK(cudaGetLastError());
   return LL_OK;
 }
-template <bool BWD> ll_status prep(const GdrArgs& a, const TcParams& p, const Plan& pl) {
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::atomic<bool> ready{false};
+  if (!ready.load(std::memory_order_acquire)) {  // (idempotent: threads may look it up at once)
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult qr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &qr) !=
+            cudaSuccess ||
+        qr != cudaDriverEntryPointSuccess)
+      return nullptr;
+    fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    ready.store(true, std::memory_order_release);
+  }
+  return fn;
+}
+bool make_map(CUtensorMap* m, const void* base, uint64_t rows, int d) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)d * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)kC};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool maps_of(const GdrArgs& a, TcMaps* m) {
+  const uint64_t rows = (uint64_t)a.B * a.H * a.T, krows = (uint64_t)a.B * a.Hk * a.T;
+  return make_map(&m->q, a.q, krows, a.dk) && make_map(&m->k, a.k, krows, a.dk) && make_map(&m->v, a.v, rows, a.dv) &&
+         make_map(&m->dout, a.dout ? a.dout : a.v, rows, a.dv);
+}
+ll_status prep(const GdrArgs& a, const TcMaps& m, const TcParams& p, const Plan& pl, bool bwd) {
   const int items = pl.slots * a.H, sms = sm_count();
   if (sms == 0) return LL_ERR_CUDA;
-  LL_CUDA_OK(cudaFuncSetAttribute(gdr_prep_kernel<BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  (int)PrepSm<BWD>::kBytes));
+  auto kernel = bwd ? gdr_prep_bwd_kernel : gdr_prep_fwd_kernel;
+  LL_CUDA_OK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PrepSm::kBytes));
   LL_CUDA_OK(cudaMemsetAsync(p.amax_s, 0, pl.amax_bytes, a.stream));
-  gdr_prep_kernel<BWD><<<std::min(items, sms), kPrepThreads, PrepSm<BWD>::kBytes, a.stream>>>(p);
+  kernel<<<std::min(items, sms), kPrepThreads, PrepSm::kBytes, a.stream>>>(m, p);
   LL_CUDA_OK(cudaGetLastError());
   return LL_OK;
 }
@@ -1290,7 +1512,8 @@ template <bool BWD> ll_status prep(const GdrArgs& a, const TcParams& p, const Pl
 }  // namespace
 
 bool gdr_tc_supported(const GdrArgs& a) {
-  return a.io == LL_BF16 && a.dk >= 64 && a.dv >= 64 && a.T >= kGdrTcMinTokens;
+  return a.io == LL_BF16 && a.dk >= 64 && a.dv >= 64 && a.T >= kGdrTcMinTokens &&
+         (long long)a.B * a.H * a.T <= (1ll << 31) - 1 - kC;  // (rows are 32-bit coordinates of the copies)
 }
 size_t gdr_tc_fwd_workspace(const GdrArgs& a) { return plan_of(a, false).total; }
 size_t gdr_tc_bwd_workspace(const GdrArgs& a) { return plan_of(a, true).total; }
@@ -1298,11 +1521,13 @@ size_t gdr_tc_bwd_workspace(const GdrArgs& a) { return plan_of(a, true).total; }
 ll_status gdr_tc_fwd_launch(const GdrArgs& a) {
   const Plan pl = plan_of(a, false);
   const TcParams p = params_of(a, pl, false);
-  ll_status st = prep<false>(a, p, pl);
+  TcMaps m;
+  if (!maps_of(a, &m)) return LL_ERR_CUDA;
+  ll_status st = prep(a, m, p, pl, false);
   if (st == LL_OK) st = scan<kFwd>(a, p, a.dv / kSlice);
   if (st != LL_OK) return st;
   LL_CUDA_OK(cudaFuncSetAttribute(gdr_out_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kOutSmem));
-  gdr_out_kernel<<<pl.slots * a.H, 256, kOutSmem, a.stream>>>(p);
+  gdr_out_kernel<<<pl.slots * a.H, 256, kOutSmem, a.stream>>>(m, p);
   LL_CUDA_OK(cudaGetLastError());
   return LL_OK;
 }
@@ -1310,7 +1535,9 @@ ll_status gdr_tc_fwd_launch(const GdrArgs& a) {
 ll_status gdr_tc_bwd_launch(const GdrArgs& a) {
   const Plan pl = plan_of(a, true);
   const TcParams p = params_of(a, pl, true);
-  ll_status st = prep<true>(a, p, pl);
+  TcMaps m;
+  if (!maps_of(a, &m)) return LL_ERR_CUDA;
+  ll_status st = prep(a, m, p, pl, true);
   // all slices, so that the columns behind a d_v of 64 are zeros: they are summed over
   if (st == LL_OK) st = scan<kFwdKeep>(a, p, kC / kSlice);
   if (st == LL_OK) st = scan<kRev>(a, p, kC / kSlice);

@@ -104,26 +104,17 @@ __device__ __noinline__ void mma_slices(uint32_t d, uint32_t a, uint32_t b, bool
   }
 }
 
-__device__ __forceinline__ void cp_async16_zfill(void* dst, const void* src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16u : 0u));
-}
 __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)),
                "r"(bytes)
                : "memory");
 }
 
-// rows 0 .. n - 1 of a [.., d] bf16 matrix into a tile, zeros elsewhere (by
-// all `threads` threads; rows that belong to another sequence stay out, so
-// that nothing of theirs, a NaN say, is multiplied by a zero)
-__device__ __noinline__ void load_tile(unsigned char* tile, const __nv_bfloat16* src, int n, int d, int tid,
-                                          int threads) {
-  const int c8 = tid & 15;
-#pragma unroll 2
-  for (int r = tid >> 4; r < kC; r += threads >> 4) {
-    const bool in = r < n && c8 * 8 < d;
-    cp_async16_zfill(tile + swz16(r, c8), in ? src + (size_t)r * d + c8 * 8 : src, in);
-  }
+// 128 rows of a [.., d] bf16 matrix into a tile (columns from d on are zeros)
+__device__ __forceinline__ void load_tile(unsigned char* tile, const CUtensorMap* map, int row, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, kTile);
+  tma_load_2d(tile, map, bar, 0, row);
+  tma_load_2d(tile + kHalf, map, bar, 64, row);
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -187,25 +178,34 @@ __device__ __forceinline__ void mma_16816(float* d, const uint32_t* a, const uin
 }
 // z[n] += X Y, 16 rows, K = 16, NT tiles of 8 columns; x: this lane's row and columns
 // of X (xa: its two pieces), y[n][d]: its column of Y in row 2 t + d of the block
+template <int NT> struct BlockRaw {
+  float2 x[4], y[NT][2];
+};
 template <int NT>
-__device__ __forceinline__ void block_mma(float (*z)[4], const float* x, const int* xa, const float* y,
-                                          const int (*yc)[2]) {
+__device__ __forceinline__ void block_load(BlockRaw<NT>& v, const float* x, const int* xa, const float* y,
+                                           const int (*yc)[2]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v.x[e] = *reinterpret_cast<const float2*>(x + xa[e >> 1] + 8 * kC * (e & 1));
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) v.y[n][e] = make_float2(y[yc[n][0] + 8 * kC * e], y[yc[n][1] + 8 * kC * e]);
+}
+template <int NT>
+__device__ __forceinline__ void block_mma(float (*z)[4], BlockRaw<NT>& v) {
   uint32_t ah[4], al[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float2 v = *reinterpret_cast<const float2*>(x + xa[e >> 1] + 8 * kC * (e & 1));
-    float x0 = v.x, x1 = v.y;
-    ah[e] = take_f16x2(x0, x1, 1.f);
-    al[e] = pack_f16x2(x0, x1);
+    ah[e] = take_f16x2(v.x[e].x, v.x[e].y, 1.f);
+    al[e] = pack_f16x2(v.x[e].x, v.x[e].y);
   }
   uint32_t bh[NT][2], bl[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float y0 = y[yc[n][0] + 8 * kC * e], y1 = y[yc[n][1] + 8 * kC * e];
-      bh[n][e] = take_f16x2(y0, y1, 1.f);
-      bl[n][e] = pack_f16x2(y0, y1);
+      bh[n][e] = take_f16x2(v.y[n][e].x, v.y[n][e].y, 1.f);
+      bl[n][e] = pack_f16x2(v.y[n][e].x, v.y[n][e].y);
     }
 #pragma unroll
   for (int n = 0; n < NT; ++n) mma_16816(z[n], al, bh[n]);
@@ -239,10 +239,14 @@ __device__ __noinline__ void tri_double(float* Ap, float* Mp, const float* beta,
     const float2 x = mat2(Ap, row + g, c + 8 * n + 2 * t), y = mat2(Ap, row + g + 8, c + 8 * n + 2 * t);
     z[n][0] = x.x; z[n][1] = x.y; z[n][2] = y.x; z[n][3] = y.y;
   }
+  BlockRaw<NT> cur, nxt;  // (the next block's values are on their way during this one's products)
+  block_load<NT>(nxt, x_at(Ap, r0 + N), xa, Ap + (r0 + N) * kC, yc);
 #pragma unroll 1
   for (int kb = 0; kb <= rb; ++kb) {
-    const int k = r0 + N + 16 * kb;
-    block_mma<NT>(z, x_at(Ap, k), xa, Ap + k * kC, yc);
+    cur = nxt;
+    const int k = r0 + N + 16 * min(kb + 1, rb);
+    block_load<NT>(nxt, x_at(Ap, k), xa, Ap + k * kC, yc);
+    block_mma<NT>(z, cur);
   }
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -251,10 +255,14 @@ __device__ __noinline__ void tri_double(float* Ap, float* Mp, const float* beta,
     mat2(Mp, row + g + 8, c + 8 * n + 2 * t) = make_float2(bt.x * z[n][2], bt.y * z[n][3]);
   }
   named_bar_sync(kSolveBar, 256);
+  const int kb0 = (c - r0) / 16;
+  block_load<NT>(nxt, x_at(Mp, r0 + 16 * kb0), xa, Mp + (r0 + 16 * kb0) * kC, yc);
 #pragma unroll 1
-  for (int kb = (c - r0) / 16; kb < RB; ++kb) {
-    const int k = r0 + 16 * kb;
-    block_mma<NT>(z, x_at(Mp, k), xa, Mp + k * kC, yc);
+  for (int kb = kb0; kb < RB; ++kb) {
+    cur = nxt;
+    const int k = r0 + 16 * min(kb + 1, RB - 1);
+    block_load<NT>(nxt, x_at(Mp, k), xa, Mp + k * kC, yc);
+    block_mma<NT>(z, cur);
   }
   named_bar_sync(kSolveBar, 256);
 #pragma unroll
@@ -346,9 +354,9 @@ __device__ __noinline__ void tri_solve(float* Ap, float* Mp, const float* beta, 
 
 // The running log decay of the chunk's tokens (`la`: this thread's, the first 128
 // threads) as pairs of floats: a scan of error-free sums, since log decays of a
-// hundred tokens leave a float too few digits for their differences.  Ends in a
-// barrier.
-__device__ __forceinline__ void chunk_decays(float la, float2* g, float2* tot, int tid) {
+// hundred tokens leave a float too few digits for their differences.  Ends in
+// barrier `bar` of `threads`.
+__device__ __forceinline__ void chunk_decays(float la, float2* g, float2* tot, int tid, int bar, int threads) {
   float2 x = make_float2(la, 0.f);
   if (tid < kC) {
 #pragma unroll
@@ -358,12 +366,12 @@ __device__ __forceinline__ void chunk_decays(float la, float2* g, float2* tot, i
     }
     if ((tid & 31) == 31) tot[tid >> 5] = x;
   }
-  __syncthreads();
+  named_bar_sync(bar, threads);
   if (tid < kC) {
     for (int w = 0; w < (tid >> 5); ++w) x = pair_add(x, tot[w]);
     g[tid] = x;
   }
-  __syncthreads();
+  named_bar_sync(bar, threads);
 }
 
 // the power of two that brings values up to `amax` to at most 16 (growth up to
@@ -376,10 +384,12 @@ __device__ __forceinline__ float2 operand_scale(float amax) {
 }
 
 // A bf16 tile in shared memory becomes fp16, scaled as above by its largest
-// value; returns the inverse scale (and that value's bits).  NT threads (`t` among
+// value; returns the inverse scale (and that value's bits).  Rows from n on belong to
+// other sequences: they become zeros, whatever they hold.  NT threads (`t` among
 // them, barrier `bar`), the tile complete before; one barrier inside, none after.
 template <int NT>
-__device__ __noinline__ float tile_to_f16(unsigned char* tile, uint32_t* red, int t, int bar, uint32_t* bits) {
+__device__ __noinline__ float tile_to_f16(unsigned char* tile, int n, uint32_t* red, int t, int bar, uint32_t* bits) {
+  const bool in = (t & 127) < n;
   constexpr int PC = kC * 16 / NT;
   uint32_t m2 = 0;
 #pragma unroll
@@ -388,7 +398,7 @@ __device__ __noinline__ float tile_to_f16(unsigned char* tile, uint32_t* red, in
     m2 = __vmaxu2(__vmaxu2(m2, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu);
     m2 = __vmaxu2(__vmaxu2(m2, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu);
   }
-  uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
+  uint32_t m = __reduce_max_sync(0xffffffffu, in ? max(m2 & 0xffffu, m2 >> 16) : 0u);
   if ((t & 31) == 0) red[t >> 5] = m;
   named_bar_sync(bar, NT);
 #pragma unroll
@@ -406,7 +416,7 @@ __device__ __noinline__ float tile_to_f16(unsigned char* tile, uint32_t* red, in
     uint32_t* w = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float2 f = unpack_bf16x2(w[e]);
+      const float2 f = unpack_bf16x2(in ? w[e] : 0u);
       w[e] = pack_f16x2(sc.x * f.x, sc.x * f.y);
     }
     *at = v;
