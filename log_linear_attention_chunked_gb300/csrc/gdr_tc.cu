@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     wait_bar(bar, j & 1, p.err);
     __syncwarp();
     tc_fence_after();
-    if (tid == 0) bulk_wait_read0();  // U and W of the item before have left
+    if (tid == 0) bulk_wait_read1();  // U of the item before has left
     __syncthreads();
     const Item nx = next[b ^ 1];
     const float2 gi = gs[i];
@@ -237,6 +237,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
       for (int v = 0; v < 4; ++v)
         mat4(Ap, i, (j0 >> 2) + v) = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
     }
+    if (tid == 0) bulk_wait_read0();  // and W
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -292,6 +293,13 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     __syncwarp();
     // U and W leave by way of the operands' places
     write_rows(reinterpret_cast<float*>(R), tl + 256, i, qt, iv);
+    fence_proxy_async_shared();
+    __syncthreads();
+    if (tid == 0) {
+      bulk_store(p.U + (size_t)it * kC * kC, R, kMatB);
+      bulk_commit();
+    }
+    __syncwarp();
     wait_bar(bar + 2, j & 1, p.err);
     __syncwarp();
     tc_fence_after();
@@ -305,7 +313,6 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     tc_fence_before();
     __syncthreads();
     if (tid == 0) {
-      bulk_store(p.U + (size_t)it * kC * kC, R, kMatB);
       bulk_store(p.W + (size_t)it * 2 * kTile, M, 2 * kTile);
       bulk_commit();
     }
