@@ -30,7 +30,7 @@ namespace {
 
 using namespace gdrtc;
 
-constexpr int kParts = 16, kBnd = 64;
+constexpr int kParts = 18, kBnd = 64;
 // per (chunk, head)
 struct Tables {
   float2 g[kC];    // running log decay
@@ -63,7 +63,7 @@ struct TcParams {
   unsigned char* D;      // D behind the chunk, scaled: a tile [d_k][d_v]
   unsigned char* Y;      // beta w, scaled: a tile [token][d_v]
   float* final_state;    // [sequence, head, dv, dk]
-  float2* part;          // [kParts][token]: e.w and v.(beta w) over 8 columns
+  float2* part;          // [16][token]: e.w and v.(beta w) over 8 columns; then [4][token] floats, parts of q.dq
   float* bnd;            // [kBnd]: pieces of <S, D> behind the chunk
   unsigned* err;
 };
@@ -79,6 +79,25 @@ __device__ __noinline__ void find_item(const TcParams& p, int it, int step, Item
   const int items = p.slots * p.seqs.H;
   for (; it < items; it += step) {
     const int slot = it / p.seqs.H, h = it - slot * p.seqs.H, hk = h / (p.seqs.H / p.seqs.Hk);
+    int seq, chunk;
+    GdrSeq sq;
+    if (!gdr_find(p.seqs, slot, kC, seq, chunk, sq)) continue;
+    out->seq = seq;
+    out->chunk = chunk;
+    out->t0 = chunk * kC;
+    out->n = min(kC, sq.len - chunk * kC);
+    out->len = sq.len;
+    out->row0 = ((size_t)sq.row_b * p.seqs.H + h) * p.seqs.T + sq.start + chunk * kC;
+    out->krow0 = ((size_t)sq.row_b * p.seqs.Hk + hk) * p.seqs.T + sq.start + chunk * kC;
+    break;
+  }
+  out->it = it;
+}
+// likewise of (chunk, key head): number slot Hk + head, row0 that of its first value head
+__device__ __noinline__ void find_unit(const TcParams& p, int it, int step, Item* out) {
+  const int units = p.slots * p.seqs.Hk;
+  for (; it < units; it += step) {
+    const int slot = it / p.seqs.Hk, hk = it - slot * p.seqs.Hk, h = hk * (p.seqs.H / p.seqs.Hk);
     int seq, chunk;
     GdrSeq sq;
     if (!gdr_find(p.seqs, slot, kC, seq, chunk, sq)) continue;
@@ -989,7 +1008,8 @@ constexpr uint32_t kOK = kOQ + kTile;        // K; then the masked scores
 constexpr uint32_t kOS = kOK + kTile;        // X; then u
 constexpr uint32_t kOTab = kOS + kTile;
 constexpr uint32_t kOBars = kOTab + 2 * kC * 4 + 32;
-constexpr uint32_t kOutSmem = kOBars + 32;
+constexpr uint32_t kOCol = kOBars + 32;
+constexpr uint32_t kOutSmem = kOCol + kColDecays * 4;
 
 // One CTA per (chunk, head), two per SM.
 __global__ void __launch_bounds__(256, 2) gdr_out_kernel(const __grid_constant__ TcMaps maps, TcParams p) {
@@ -1026,7 +1046,9 @@ __global__ void __launch_bounds__(256, 2) gdr_out_kernel(const __grid_constant__
     tmem_alloc(tmem_slot, 256);
     tmem_relinquish();
   }
+  float* cf = reinterpret_cast<float*>(s + kOCol);
   if (tid < kC) gs[tid] = p.tab[it].g[tid];
+  column_decays(cf, p.tab[it].g, tid);
   const float ik = p.tab[it].ik, isf = operand_scale(__uint_as_float(p.amax_s[(size_t)seq * p.seqs.H + h])).y;
   tc_fence_before();
   __syncthreads();
@@ -1056,11 +1078,12 @@ __global__ void __launch_bounds__(256, 2) gdr_out_kernel(const __grid_constant__
 #pragma unroll
   for (int c = 0; c < 2; ++c) {  // Q K^T . G over K
     const int j0 = 64 * hf + 32 * c;
-    float a[32];
+    float a[32], dec[32];
     tmem_ld32(tl + 32 * c, a);
+    row_decays<32>(dec, cf, gs, gi, i, q, j0);
     tmem_ld_wait();
 #pragma unroll
-    for (int jj = 0; jj < 32; ++jj) a[jj] = j0 + jj <= i ? kScoreDown * a[jj] * exp_diff(gi, gs[j0 + jj]) : 0.f;
+    for (int jj = 0; jj < 32; ++jj) a[jj] = j0 + jj <= i ? kScoreDown * a[jj] * dec[jj] : 0.f;
 #pragma unroll
     for (int c8 = 0; c8 < 4; ++c8)
       *reinterpret_cast<uint4*>(s + kOK + swz16(i, (j0 >> 3) + c8)) =
@@ -1090,22 +1113,21 @@ __global__ void __launch_bounds__(256, 2) gdr_out_kernel(const __grid_constant__
     tmem_ld32(tl + 32 * c, a);
     tmem_ld32(tl + 128 + 32 * c, x);
     tmem_ld_wait();
-    if (i < n) {
-      uint4* og = reinterpret_cast<uint4*>(p.o + (row0 + i) * p.dv + j0);
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        uint32_t w[4];
+    for (int v = 0; v < 4; ++v) {  // by way of Q's place, whole rows to half a warp
+      uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = 8 * v + 2 * e;
-          w[e] = pack_bf16x2(fmaf(fx, x[j], fa * a[j]), fmaf(fx, x[j + 1], fa * a[j + 1]));
-        }
-        og[v] = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int e = 0; e < 4; ++e) {
+        const int j = 8 * v + 2 * e;
+        w[e] = pack_bf16x2(fmaf(fx, x[j], fa * a[j]), fmaf(fx, x[j + 1], fa * a[j + 1]));
       }
+      *reinterpret_cast<uint4*>(s + kOQ + swz16(i, (j0 >> 3) + v)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
   tc_fence_before();
   __syncthreads();
+  store_rows(p.o + row0 * p.dv, s + kOQ, n, p.dv, tid, 256);
+  __syncwarp();
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 256);
@@ -1116,13 +1138,16 @@ __global__ void __launch_bounds__(256, 2) gdr_out_kernel(const __grid_constant__
 constexpr float kGradDown = 1.f / 64.f;  // of R and N, as operands
 constexpr uint32_t kGBars = 7 * kTile;
 constexpr uint32_t kGTab = kGBars + 6 * 8;
-constexpr uint32_t kGradSmem = kGTab + 2 * kC * 4 + 32;
+constexpr uint32_t kGNext = kGTab + 2 * kC * 4 + 32;
+constexpr uint32_t kGCol = (kGNext + sizeof(Item) + 15) / 16 * 16;
+constexpr uint32_t kGradSmem = kGCol + kColDecays * 4;
 static_assert(kGradSmem <= 232448, "shared memory budget of one CTA");
 constexpr int kGradThreads = 512;
 
-// One CTA per (chunk, key head); the value heads that share it are taken in
-// turn, dq and dk adding up in registers in a fixed order.  Thread = (row, quarter
-// of the columns).  Per head three rounds of products over seven tiles of shared
+// Persistent, one CTA per SM, an item per (chunk, key head); the value heads that
+// share it are taken in turn, dq and dk adding up in registers in a fixed order.
+// Thread = (row, quarter of the columns).  The next head's or item's tiles are
+// loaded as soon as a tile's last product is done.  Per head three rounds of products over seven tiles of shared
 // memory:
 //   dO S, (beta w) S, u D;   dO u^T, (beta w) u^T, Q K^T;   R K, R^T Q, (N + N^T) K
 // with R = scale (dO u^T . G) and N = ((beta w) u^T . G) strictly lower.  The
@@ -1136,23 +1161,20 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
   }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int q = warp & 3, qt = warp >> 2, i = 32 * q + lane, j0 = 32 * qt;
-  const int hk = blockIdx.x % p.seqs.Hk, slot = blockIdx.x / p.seqs.Hk, G = p.seqs.H / p.seqs.Hk;
-  int seq, chunk;
-  GdrSeq sq;
-  if (!gdr_find(p.seqs, slot, kC, seq, chunk, sq)) return;
-  const int t0 = chunk * kC, n = min(kC, sq.len - t0);
-  const size_t krow0 = ((size_t)sq.row_b * p.seqs.Hk + hk) * p.seqs.T + sq.start + t0;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s + kGBars);  // 0: round 1, 1: Q and K, 2: products
+  const int G = p.seqs.H / p.seqs.Hk, units = p.slots * p.seqs.Hk;
+  Item* next = reinterpret_cast<Item*>(s + kGNext);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s + kGBars);  // 0: Y and u, 1: dO, S and D, 2: Q and K, 3: products
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s + kGBars + 4 * 8);
   float2* gs = reinterpret_cast<float2*>(s + kGTab);
   double* tot = reinterpret_cast<double*>(gs + kC);        // [4]
   // tiles: 0 dO, then N; 1-2 S, then Q and K; 3 beta w; 4-5 u; 6 D, then R
   constexpr uint32_t tO = 0, tS = kTile, tQ = kTile, tK = 2 * kTile, tY = 3 * kTile, tU = 4 * kTile, tD = 6 * kTile;
   constexpr uint32_t kLow = 64;  // of a slice tile's low part
-  float* dg = reinterpret_cast<float*>(s + tY);  // [4][token], behind round 2
+  float* cf = reinterpret_cast<float*>(s + kGCol);  // the columns' decay factors
   if (tid == 0) {
-    for (int b = 0; b < 3; ++b) mbar_init(bars + b, 1);
+    for (int b = 0; b < 4; ++b) mbar_init(bars + b, 1);
     fence_mbar_init();
+    find_unit(p, blockIdx.x, gridDim.x, next);
   }
   __syncwarp();
   if (warp == 0) {
@@ -1167,38 +1189,60 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
   const uint32_t s0 = smem_u32(s);
   uint32_t nmma = 0;
   auto wait_mma = [&]() {
-    wait_bar(bars + 2, nmma & 1, p.err);
+    wait_bar(bars + 3, nmma & 1, p.err);
     ++nmma;
     __syncwarp();
     tc_fence_after();
   };
+  // loads of (slot, head) item `it`, by thread 0
+  auto load_rows = [&](size_t it) {
+    mbar_arrive_expect_tx(bars, 3 * kTile);
+    bulk_load(s + tY, p.Y + it * kTile, kTile, bars);
+    bulk_load(s + tU, p.E + it * 2 * kTile, 2 * kTile, bars);
+  };
+  auto load_states = [&](size_t it) {
+    mbar_arrive_expect_tx(bars + 1, 4 * kTile);
+    bulk_load(s + tO, p.dO16 + it * kTile, kTile, bars + 1);
+    bulk_load(s + tS, p.S + it * 2 * kTile, 2 * kTile, bars + 1);
+    bulk_load(s + tD, p.D + it * kTile, kTile, bars + 1);
+  };
+  auto head_of = [&](int unit, int hh) {  // (slot, head) of a unit's head
+    const int slot = unit / p.seqs.Hk;
+    return (size_t)slot * p.seqs.H + (unit - slot * p.seqs.Hk) * G + hh;
+  };
   float xq[32], xk[32];  // dq and dk of this thread's row and columns, over the heads
+  Item me = *next;
+  if (tid == 0 && me.it < units) {
+    load_rows(head_of(me.it, 0));
+    load_states(head_of(me.it, 0));
+  }
+  __syncwarp();
+  uint32_t par = 0;
+  while (me.it < units) {
+    __syncthreads();  // (the item has been read)
+    if (tid == 511) find_unit(p, me.it + gridDim.x, gridDim.x, next);
+    const int unit = me.it, n = me.n;
+    const size_t krow0 = me.krow0;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) xq[j] = xk[j] = 0.f;
-
-  for (int hh = 0; hh < G; ++hh) {
-    const int h = hk * G + hh;
-    const size_t it = (size_t)slot * p.seqs.H + h, sh = (size_t)seq * p.seqs.H + h;
-    const size_t row0 = ((size_t)sq.row_b * p.seqs.H + h) * p.seqs.T + sq.start + t0;
-    const uint32_t par = hh & 1;
+    for (int j = 0; j < 32; ++j) xq[j] = xk[j] = 0.f;
+  for (int hh = 0; hh < G; ++hh, par ^= 1) {
+    const size_t it = head_of(unit, hh), sh = (size_t)me.seq * p.seqs.H + (unit % p.seqs.Hk) * G + hh;
+    const size_t row0 = me.row0 + (size_t)hh * p.seqs.T;
     if (tid == 0) {
-      mbar_arrive_expect_tx(bars, 7 * kTile);
-      bulk_load(s + tO, p.dO16 + it * kTile, kTile, bars);
-      bulk_load(s + tS, p.S + it * 2 * kTile, 2 * kTile, bars);
-      bulk_load(s + tY, p.Y + it * kTile, kTile, bars);
-      bulk_load(s + tU, p.E + it * 2 * kTile, 2 * kTile, bars);
-      bulk_load(s + tD, p.D + it * kTile, kTile, bars);
       wait_bar(bars, par, p.err);
+      wait_bar(bars + 1, par, p.err);
       tc_fence_after();
       mma_slices<false, true>(tmem, s0 + tO, s0 + tS, false);
       mma_slices<false, true>(tmem + 128, s0 + tO, s0 + tS + kLow, false);
       mma_slices<false, true>(tmem + 256, s0 + tY, s0 + tS, false);
       mma_slices<true, false>(tmem + 384, s0 + tU, s0 + tD, false);
-      umma_commit(bars + 2);
+      umma_commit(bars + 3);
     }
     __syncwarp();
     const Tables& tb = p.tab[it];
     if (tid < kC) gs[tid] = tb.g[tid];
+    column_decays(cf, tb.g, tid - 256 < 0 ? kColDecays : tid - 256);
+    float* dg = reinterpret_cast<float*>(p.part + (it * kParts + 16) * kC);  // [4][token]
     const float ik = tb.ik, iq = tb.iq, id = tb.id, in = tb.into[i], out = tb.out[i];
     const float isf = operand_scale(__uint_as_float(p.amax_s[sh])).y, isr = operand_scale(__uint_as_float(p.amax_d[sh])).y;
     uint4 qv[4];  // this thread's piece of Q's row
@@ -1208,9 +1252,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
                                  : make_uint4(0u, 0u, 0u, 0u);
     wait_mma();
     if (tid == 0) {
-      mbar_arrive_expect_tx(bars + 1, 2 * kTile);
-      bulk_load(s + tQ, p.Q16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, kTile, bars + 1);
-      bulk_load(s + tK, p.K16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, kTile, bars + 1);
+      mbar_arrive_expect_tx(bars + 2, 2 * kTile);
+      bulk_load(s + tQ, p.Q16 + (size_t)unit * kTile, kTile, bars + 2);
+      bulk_load(s + tK, p.K16 + (size_t)unit * kTile, kTile, bars + 2);
     }
     __syncwarp();
     // ---- round 1: dq's and dk's parts by the states, q.dq's first part
@@ -1251,12 +1295,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
       mma_slices<false, true>(tmem + 128, s0 + tO, s0 + tU + kLow, false);
       mma_slices<false, true>(tmem + 128, s0 + tO, s0 + tU, true);
       mma_slices<false, true>(tmem + 256, s0 + tY, s0 + tU, false);
-      wait_bar(bars + 1, par, p.err);
+      wait_bar(bars + 2, par, p.err);
       mma_slices<false, false>(tmem + 384, s0 + tQ, s0 + tK, false);
-      umma_commit(bars + 2);
+      umma_commit(bars + 3);
     }
     __syncwarp();
     wait_mma();
+    if (tid == 0 && (hh + 1 < G || next->it < units)) load_rows(hh + 1 < G ? it + 1 : head_of(next->it, 0));
+    __syncwarp();
     // ---- round 2: R and N as operands; q.dq's second part, the row sums of R . Q K^T
     {
       const float2 gi = gs[i];
@@ -1264,13 +1310,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         float r[16], a[16], dec[16];
+        row_decays<16>(dec, cf, gs, gi, i, q, j0 + 16 * c);
         tmem_ld16(tl + 128 + 16 * c, r);
         tmem_ld16(tl + 384 + 16 * c, a);
         tmem_ld_wait();
 #pragma unroll
         for (int jj = 0; jj < 16; ++jj) {
           const int j = j0 + 16 * c + jj;
-          dec[jj] = j <= i ? exp_diff(gi, gs[j]) : 0.f;
           r[jj] = j <= i ? r[jj] * dec[jj] : 0.f;
           if (j <= i) sum = fmaf(r[jj], a[jj], sum);
         }
@@ -1302,7 +1348,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
       mma_tile<true, true>(tmem + 256, s0 + tD, s0 + tQ, false);   // R^T Q
       mma_tile<false, true>(tmem + 384, s0 + tO, s0 + tK, false);  // N K
       mma_tile<true, true>(tmem + 384, s0 + tO, s0 + tK, true);    // N^T K
-      umma_commit(bars + 2);
+      umma_commit(bars + 3);
     }
     __syncwarp();
     // ---- the gates' gradients: sums over the slices, the suffix sum over the chunk
@@ -1310,7 +1356,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
       const int t = tid - 384;
       float ew = 0.f, vw = 0.f;
 #pragma unroll
-      for (int x = 0; x < kParts; ++x) {
+      for (int x = 0; x < 16; ++x) {
         const float2 f = p.part[(it * kParts + x) * kC + t];
         ew += f.x;
         vw += f.y;
@@ -1351,21 +1397,31 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
         }
       }
     }
+    if (hh + 1 == G) {  // the gradients leave by way of Q's and K's places, whole rows to a warp
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const uint32_t at = swz16(i, 4 * qt + v);
+        *reinterpret_cast<uint4*>(s + tQ + at) =
+            make_uint4(pack_bf16x2(xq[8 * v], xq[8 * v + 1]), pack_bf16x2(xq[8 * v + 2], xq[8 * v + 3]),
+                       pack_bf16x2(xq[8 * v + 4], xq[8 * v + 5]), pack_bf16x2(xq[8 * v + 6], xq[8 * v + 7]));
+        *reinterpret_cast<uint4*>(s + tK + at) =
+            make_uint4(pack_bf16x2(xk[8 * v], xk[8 * v + 1]), pack_bf16x2(xk[8 * v + 2], xk[8 * v + 3]),
+                       pack_bf16x2(xk[8 * v + 4], xk[8 * v + 5]), pack_bf16x2(xk[8 * v + 6], xk[8 * v + 7]));
+      }
+      __syncthreads();
+      store_rows(p.dq + krow0 * p.dk, s + tQ, n, p.dk, tid, kGradThreads);
+      store_rows(p.dkey + krow0 * p.dk, s + tK, n, p.dk, tid, kGradThreads);
+    }
+    fence_proxy_async_shared();
     tc_fence_before();
     __syncthreads();  // the next head's tiles and tables
     tc_fence_after();
+    if (tid == 0 && (hh + 1 < G || next->it < units)) load_states(hh + 1 < G ? it + 1 : head_of(next->it, 0));
+    __syncwarp();
   }
-  if (i < n && j0 < p.dk) {
-    uint4* qg = reinterpret_cast<uint4*>(p.dq + (krow0 + i) * p.dk + j0);
-    uint4* kg = reinterpret_cast<uint4*>(p.dkey + (krow0 + i) * p.dk + j0);
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      qg[v] = make_uint4(pack_bf16x2(xq[8 * v], xq[8 * v + 1]), pack_bf16x2(xq[8 * v + 2], xq[8 * v + 3]),
-                         pack_bf16x2(xq[8 * v + 4], xq[8 * v + 5]), pack_bf16x2(xq[8 * v + 6], xq[8 * v + 7]));
-      kg[v] = make_uint4(pack_bf16x2(xk[8 * v], xk[8 * v + 1]), pack_bf16x2(xk[8 * v + 2], xk[8 * v + 3]),
-                         pack_bf16x2(xk[8 * v + 4], xk[8 * v + 5]), pack_bf16x2(xk[8 * v + 6], xk[8 * v + 7]));
-    }
+    me = *next;
   }
+  __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
@@ -1550,7 +1606,9 @@ ll_status gdr_tc_bwd_launch(const GdrArgs& a) {
   if (st == LL_OK) st = scan<kRev>(a, p, kC / kSlice);
   if (st != LL_OK) return st;
   LL_CUDA_OK(cudaFuncSetAttribute(gdr_grad_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGradSmem));
-  gdr_grad_tc_kernel<<<pl.slots * a.Hk, kGradThreads, kGradSmem, a.stream>>>(p);
+  const int sms = sm_count();
+  if (sms == 0) return LL_ERR_CUDA;
+  gdr_grad_tc_kernel<<<std::min(pl.slots * a.Hk, sms), kGradThreads, kGradSmem, a.stream>>>(p);
   LL_CUDA_OK(cudaGetLastError());
   return LL_OK;
 }

@@ -425,6 +425,16 @@ __device__ __noinline__ float tile_to_f16(unsigned char* tile, int n, uint32_t* 
   return sc.y;
 }
 
+// rows 0 .. n - 1 of a tile of 16-bit values into a [.., d] matrix, whole rows to half a warp
+__device__ __noinline__ void store_rows(void* dst, const unsigned char* tile, int n, int d, int tid, int threads) {
+  const int c8 = tid & 15;
+  if (c8 * 8 < d)
+#pragma unroll 4
+    for (int r = tid >> 4; r < n; r += threads >> 4)
+      *reinterpret_cast<uint4*>(static_cast<char*>(dst) + ((size_t)r * d + c8 * 8) * 2) =
+          *reinterpret_cast<const uint4*>(tile + swz16(r, c8));
+}
+
 // ---- phases of the preparation; i: the thread's row, qt: its quarter of the columns
 // M's row i, 32 columns (zero above the block on the diagonal)
 __device__ __forceinline__ void load_m(float* m, float* Mp, int i, int qt) {
@@ -503,6 +513,37 @@ __device__ __noinline__ void write_tiles(unsigned char* hi, unsigned char* lo, u
     put_parts(hi, lo, swz16(i, 4 * qt + 2 * c + 1), x + 8, scale_lo);
   }
 }
+// exp(g_i - g_j) = exp(g_i - g_m) exp(g_m - g_j), m the first row of i's 32: one factor of
+// the row and one of the column, both at most 1 for j < m (log decays are at most 0),
+// so that only the 32 x 32 blocks on the diagonal take an exponential per element.
+// The columns' factors: of row block q = 1, 2, 3 those of the columns below 32 q.
+constexpr int kColDecays = 32 + 64 + 96;
+__device__ __forceinline__ int col_at(int q) { return 16 * q * (q - 1); }
+__device__ __forceinline__ void column_decays(float* cf, const float2* g, int tid) {  // 192 threads
+  if (tid < kColDecays) {
+    const int q = tid < 32 ? 1 : tid < 96 ? 2 : 3;
+    cf[tid] = exp_diff(g[32 * q], g[tid - col_at(q)]);
+  }
+}
+// x[k] = exp(g_i - g_{j0 + k}) for N columns of a row i in row block q (0 above the diagonal)
+template <int N>
+__device__ __forceinline__ void row_decays(float* x, const float* cf, const float2* gs, float2 gi, int i, int q, int j0) {
+  if (j0 < 32 * q) {  // (warp-uniform)
+    const float f = exp_diff(gi, gs[32 * q]);
+#pragma unroll
+    for (int k = 0; k < N; k += 4) {
+      const float4 c = *reinterpret_cast<const float4*>(cf + col_at(q) + j0 + k);
+      x[k] = f * c.x;
+      x[k + 1] = f * c.y;
+      x[k + 2] = f * c.z;
+      x[k + 3] = f * c.w;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) x[k] = j0 + k <= i ? exp_diff(gi, gs[j0 + k]) : 0.f;
+  }
+}
+
 // 16 columns j0 .. of an accumulator's row i, times f exp(g_i - g_j), zero from the column `end` on
 __device__ __forceinline__ void decayed16(float* x, uint32_t acc, const float2* gs, float2 gi, int j0, int end, float f) {
   tmem_ld16(acc, x);
