@@ -116,9 +116,9 @@ ll_status gdr_rec_bwd_launch(const GdrArgs& a, float* kept_adjoints, float* kept
 ll_status gdr_grad_launch(const GdrArgs& a, const float* states, const float* errors, const float* adjoints,
                           const float* w);
 
-// on the tensor cores (gdr_tc.cu): bf16 io, head sizes 64 and 128, from this many tokens on
-constexpr int kGdrTcMinTokens = 192;
-bool gdr_tc_supported(const GdrArgs& a);
+// on the tensor cores (gdr_tc.cu), where its formats allow and its time is the shorter
+bool gdr_tc_fwd_use(const GdrArgs& a);
+bool gdr_tc_bwd_use(const GdrArgs& a);
 size_t gdr_tc_fwd_workspace(const GdrArgs& a);
 size_t gdr_tc_bwd_workspace(const GdrArgs& a);
 ll_status gdr_tc_fwd_launch(const GdrArgs& a);

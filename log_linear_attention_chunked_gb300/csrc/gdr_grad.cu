@@ -341,16 +341,16 @@ ll_status gdr_grad_launch(const GdrArgs& a, const float* states, const float* er
                         : run_dk<__nv_bfloat16>(a.dk, p, grid, smem, a.stream);
 }
 
-size_t gdr_fwd_workspace(const GdrArgs& a) { return gdr_tc_supported(a) ? gdr_tc_fwd_workspace(a) : 0; }
-int gdr_fwd_launches(const GdrArgs& a) { return gdr_tc_supported(a) ? 3 : 1; }
+size_t gdr_fwd_workspace(const GdrArgs& a) { return gdr_tc_fwd_use(a) ? gdr_tc_fwd_workspace(a) : 0; }
+int gdr_fwd_launches(const GdrArgs& a) { return gdr_tc_fwd_use(a) ? 3 : 1; }
 ll_status gdr_fwd_launch(const GdrArgs& a) {
-  return gdr_tc_supported(a) ? gdr_tc_fwd_launch(a) : gdr_rec_fwd_launch(a, nullptr, nullptr);
+  return gdr_tc_fwd_use(a) ? gdr_tc_fwd_launch(a) : gdr_rec_fwd_launch(a, nullptr, nullptr);
 }
 
-size_t gdr_bwd_workspace(const GdrArgs& a) { return gdr_tc_supported(a) ? gdr_tc_bwd_workspace(a) : rec_plan(a).total; }
-int gdr_bwd_launches(const GdrArgs& a) { return gdr_tc_supported(a) ? 4 : 3; }
+size_t gdr_bwd_workspace(const GdrArgs& a) { return gdr_tc_bwd_use(a) ? gdr_tc_bwd_workspace(a) : rec_plan(a).total; }
+int gdr_bwd_launches(const GdrArgs& a) { return gdr_tc_bwd_use(a) ? 4 : 3; }
 ll_status gdr_bwd_launch(const GdrArgs& a) {
-  if (gdr_tc_supported(a)) return gdr_tc_bwd_launch(a);
+  if (gdr_tc_bwd_use(a)) return gdr_tc_bwd_launch(a);
   const RecPlan p = rec_plan(a);
   unsigned char* ws = static_cast<unsigned char*>(a.ws);
   float* states = reinterpret_cast<float*>(ws + p.states);

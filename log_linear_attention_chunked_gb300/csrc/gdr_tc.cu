@@ -21,6 +21,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "gdr_tc.cuh"
 
@@ -1574,9 +1575,43 @@ ll_status prep(const GdrArgs& a, const TcMaps& m, const TcParams& p, const Plan&
 
 }  // namespace
 
-bool gdr_tc_supported(const GdrArgs& a) {
-  return a.io == LL_BF16 && a.dk >= 64 && a.dv >= 64 && a.T >= kGdrTcMinTokens &&
-         (long long)a.B * a.H * a.T <= (1ll << 31) - 1 - kC;  // (rows are 32-bit coordinates of the copies)
+// bf16 io, head sizes of 64 and 128; rows are 32-bit coordinates of the copies
+static bool tc_formats(const GdrArgs& a) {
+  return a.io == LL_BF16 && a.dk >= 64 && a.dv >= 64 && (long long)a.B * a.H * a.T <= (1ll << 31) - 1 - kC;
+}
+// Which of the two ways is faster follows from both measured, in us, for 4 to
+// 1024 (sequence, head) pairs of 1 to 1024 tokens and for packed batches of 512
+// to 8192 tokens.  Token by token a forward takes 4 plus the larger of its longest
+// sequence's tokens (0.12 each at d_k = 128, 0.095 at 64, 1.6 times that once the
+// rows of all states are 4096 and more and blocks share an SM) and of all of them
+// (0.0058 a token and head at 128 x 128, less in proportion to the state); in
+// chunks it takes three launches (34 in all, however small), or 0.18 an item and 0.06 a
+// state (0.15 and 0.05 with a side of 64).  For 16 heads of one sequence (128 x 128,
+// token by token / in chunks): 19.5 / 34.8 at 128 tokens, 35.1 / 37.1 at 256, 50.8 / 38.3 at
+// 384; for 1024 heads: 202 / 257 at 32 tokens, 363 / 262 at 64.  Only the device
+// knows the lengths of packed sequences: their mean is T / n, the longest is
+// taken for twice that.  The choice is the slower one, by 10 % or more, in 12 of
+// 451 shapes measured, by 1.53 times at most.
+bool gdr_tc_fwd_use(const GdrArgs& a) {
+  if (!tc_formats(a)) return false;
+  const double seqs = gdr_sequences(a), states = seqs * a.H, wide = a.dk * a.dv / 4096.;
+  const double mean = a.n_seqs ? std::ceil(a.T / seqs) : a.T, longest = a.n_seqs > 1 ? std::min<double>(a.T, 2 * mean) : a.T;
+  const double token = (a.dk > 64 ? 0.12 : 0.095) * (!a.n_seqs && states * a.dv >= 4096 ? 1.6 : 1.);
+  const double by_token = 4 + std::max(token * longest, 0.00145 * wide * mean * states);
+  const double items = states * std::ceil(mean / kC);
+  const double in_chunks = std::max(34., 18 + (wide == 4 ? 0.18 : 0.15) * items + (wide == 4 ? 0.06 : 0.05) * states);
+  return in_chunks < by_token;
+}
+// The gradient: token by token it takes a launch over all states, one over all their
+// gradients and one over chunks of 64.  At 128 x 128 the tensor cores are the faster
+// at every length measured (16 heads: 81 / 61 us at 1 token, 132 / 67 at 192; 256 heads: 212 / 182
+// at 16, 5435 / 973 at 1024); the bound of 16 is for the workspace, whose items
+// are padded to 128 tokens.  With a side of 64 they are from 64 tokens on (256 heads,
+// 64 x 128: 164 / 183 at 32, 214 / 186 at 64), with two from 96 (126 / 180 at 64, 213 / 182 at
+// 96; 20 packed sequences of 102 on 4 heads 109 / 84, 32 of 64 69 / 141).
+bool gdr_tc_bwd_use(const GdrArgs& a) {
+  const int mean = a.n_seqs ? (a.T + a.n_seqs - 1) / a.n_seqs : a.T;
+  return tc_formats(a) && mean >= (a.dk * a.dv > 64 * 128 ? 16 : a.dk * a.dv > 64 * 64 ? 64 : 96);
 }
 size_t gdr_tc_fwd_workspace(const GdrArgs& a) { return plan_of(a, false).total; }
 size_t gdr_tc_bwd_workspace(const GdrArgs& a) { return plan_of(a, true).total; }

@@ -43,6 +43,21 @@ __device__ __forceinline__ float ex2(float x) {
 // exp of a difference of two log decays kept as pairs of floats
 __device__ __forceinline__ float exp_diff(float2 a, float2 b) { return ex2(((a.x - b.x) + (a.y - b.y)) * kLog2e); }
 
+// Wait until all but the latest committed group of bulk stores have read their source.
+__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+// 32 lanes x 8 consecutive 32-bit columns (thread i: lane base + i).
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void named_bar_arrive(int id, int nthreads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
 // Bounded wait (every thread): the waits of these kernels are on their own
 // copies and products, which always complete.
 __device__ __noinline__ void wait_bar_long(uint64_t* bar, uint32_t par, unsigned* err) {
