@@ -122,9 +122,12 @@ struct PrepSm {
   static constexpr uint32_t kM = 3 * kTile;                        // M, float32; then operands in two parts
   static constexpr uint32_t kR = kM + kMatB;                       // A, float32; then likewise
   static constexpr uint32_t kTab = kR + 2 * kTile;
-  static constexpr uint32_t kBars = kTab + 5 * kC * 4 + 32 + 3 * 64 + 16;
+  static constexpr uint32_t kCol = kTab + 4 * kC * 4 + 32 + 64 + 16;  // forward: the columns' decay factors
+  static constexpr uint32_t kBars = kCol + kColDecays * 4;
+  static_assert(kBars >= kTab + 5 * kC * 4 + 32 + 3 * 64 + 16, "the backward's tables");
   static constexpr uint32_t kNext = kBars + 7 * 8;
   static constexpr uint32_t kBytes = kNext + 2 * sizeof(Item);
+  static_assert(kCol % 16 == 0, "read as float4");
 };
 static_assert(kMatB == 2 * kTile && PrepSm::kBars % 8 == 0, "tile alignment");
 static_assert(PrepSm::kBytes <= 232448, "shared memory budget of one CTA");
@@ -160,6 +163,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
   float2* tot = reinterpret_cast<float2*>(in_s + kC);
   uint32_t* red = reinterpret_cast<uint32_t*>(tot + 4);  // 2 x 8
   float* inv = reinterpret_cast<float*>(red + 16);       // inverse scales: V, K of both buffers
+  float* cf = reinterpret_cast<float*>(s + Sm::kCol);
   uint64_t* bar = reinterpret_cast<uint64_t*>(s + Sm::kBars);  // K K^T, U, W, K loads 0 and 1, V load
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s + Sm::kBars + 6 * 8);
   Item* next = reinterpret_cast<Item*>(s + Sm::kNext);
@@ -194,6 +198,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     const bool mine = t < x.n;
     const float la = mine ? gdr_log(p.log_alpha[x.row0 + t]) : 0.f, bt = mine ? p.beta[x.row0 + t] : 0.f;
     chunk_decays(la, gs, tot, t, kPrepBar2, 256);
+    column_decays(cf, gs, t);
     wait_bar(bar + 3 + b, (j >> 1) & 1, p.err);
     const float ik = tile_to_f16<256>(X0 + b * kTile, x.n, red, t, kPrepBar2, nullptr);
     // A is K K^T of the scaled tile / 4096, beta takes the difference
@@ -211,7 +216,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
       inv[1 + b] = ik;
       tb.ik = ik;
       tc_fence_after();
-      mma_tile<false, false>(tmem, sX0 + b * kTile, sX0 + b * kTile, false);
+      mma_tile<kAlong, kAlong>(tmem, sX0 + b * kTile, sX0 + b * kTile, false);
       umma_commit(bar);
       if (h % G == 0) {
         bulk_store(p.K16 + ((size_t)slot * p.seqs.Hk + h / G) * kTile, X0 + b * kTile, kTile);
@@ -252,7 +257,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
       const int j0 = 32 * qt + 16 * c;
       if (j0 > 32 * q + 31) break;  // (warp-uniform) above the diagonal
       float x[16];
-      decayed16(x, tl + 16 * c, gs, gi, j0, i, kKeysDown);
+      decayed16(x, tl + 16 * c, cf, gs, gi, i, q, j0, i, kKeysDown);
 #pragma unroll
       for (int v = 0; v < 4; ++v)
         mat4(Ap, i, (j0 >> 2) + v) = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
@@ -298,11 +303,11 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     __syncthreads();
     if (tid == 0) {
       tc_fence_after();
-      mma_tile<false, true>(tmem + 256, sR + kTile, sXV, false);
-      mma_tile<false, true>(tmem + 256, sR, sXV, true);
+      mma_tile<kAlong, kDown>(tmem + 256, sR + kTile, sXV, false);
+      mma_tile<kAlong, kDown>(tmem + 256, sR, sXV, true);
       umma_commit(bar + 1);
-      mma_tile<false, true>(tmem + 384, sM + kTile, sX0 + b * kTile, false);
-      mma_tile<false, true>(tmem + 384, sM, sX0 + b * kTile, true);
+      mma_tile<kAlong, kDown>(tmem + 384, sM + kTile, sX0 + b * kTile, false);
+      mma_tile<kAlong, kDown>(tmem + 384, sM, sX0 + b * kTile, true);
       umma_commit(bar + 2);
     }
     __syncwarp();
@@ -328,7 +333,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
       load_k(next[b], b);
     }
     __syncwarp();
-    write_tiles(M, M + kTile, tl + 384, i, qt, ik, kLoScale);
+    write_tiles<true>(M, M + kTile, tl + 384, i, qt, ik, kLoScale);
     fence_proxy_async_shared();
     tc_fence_before();
     __syncthreads();
@@ -367,6 +372,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
   float2* tot = reinterpret_cast<float2*>(out_s + kC);
   uint32_t* red = reinterpret_cast<uint32_t*>(tot + 4);  // 3 x 16
   float* inv = reinterpret_cast<float*>(red + 48);       // inverse scales of V and Q
+  float* cf = reinterpret_cast<float*>(s + Sm::kM);  // the columns' decay factors, where M comes to stand
   uint64_t* bar = reinterpret_cast<uint64_t*>(s + Sm::kBars);
   // bar: products, K, U, Q, V and dO
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s + Sm::kBars + 6 * 8);
@@ -454,6 +460,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     const float beta_i = bt;
     const bool t_end = me.t0 + n == me.len;
     chunk_decays(la, gs, tot, tid, 0, kPrepThreads);
+    column_decays(cf, gs, tid);
     const float2 gi = gs[i];
     if (qt == 0) {
       const float in = exp_diff(gi, make_float2(0.f, 0.f)), out = exp_diff(gs[kC - 1], gi);
@@ -471,7 +478,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     if (tid < kC) bs[tid] = beta_i * (ik * ik / kKeysDown);
     // ---- K K^T -> 0
     issue([&]() {
-      mma_tile<false, false>(tmem, sX0, sX0, false);
+      mma_tile<kAlong, kAlong>(tmem, sX0, sX0, false);
       bulk_wait_read0();  // (what the item before staged has left)
       if (h % G == 0) {
         bulk_store(p.K16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, X0, kTile);
@@ -486,7 +493,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
       const int j0 = 32 * qt + 16 * c;
       if (j0 > 32 * q + 31) break;  // (warp-uniform) above the diagonal
       float x[16];
-      decayed16(x, tl + 16 * c, gs, gi, j0, i, kKeysDown);
+      decayed16(x, tl + 16 * c, cf, gs, gi, i, q, j0, i, kKeysDown);
 #pragma unroll
       for (int v = 0; v < 4; ++v)
         mat4(Ap, i, (j0 >> 2) + v) = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
@@ -541,12 +548,12 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     __syncthreads();
     put_inverse2(R, M, m, i, qt, bs, in_s);
     issue([&]() {
-      mma_tile<false, true>(tmem + 256, sR + kTile, sXV, false);
-      mma_tile<false, true>(tmem + 256, sR, sXV, true);
+      mma_tile<kAlong, kDown>(tmem + 256, sR + kTile, sXV, false);
+      mma_tile<kAlong, kDown>(tmem + 256, sR, sXV, true);
       umma_commit(bar + 2);
-      mma_tile<false, false>(tmem + 128, sX1, sX0, false);
-      mma_tile<false, true>(tmem + 384, sM + kTile, sX0, false);
-      mma_tile<false, true>(tmem + 384, sM, sX0, true);
+      mma_tile<kAlong, kAlong>(tmem + 128, sX1, sX0, false);
+      mma_tile<kAlong, kDown>(tmem + 384, sM + kTile, sX0, false);
+      mma_tile<kAlong, kDown>(tmem + 384, sM, sX0, true);
       if (h % G == 0) {
         bulk_store(p.Q16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, X1, kTile);
         bulk_commit();
@@ -566,6 +573,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
       ++nv;
       const float id = tile_to_f16<kPrepThreads>(XV, n, red, tid, 0, nullptr);
       __syncthreads();
+      column_decays(bs, gs, tid);  // (the tables' values have been read)
 #pragma unroll 1
       for (int c8 = 0; c8 < 4; ++c8) {
         const uint32_t at = swz16(i, 4 * qt + c8);
@@ -581,15 +589,15 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
         put_parts(M, M + kTile, at, x, 1.f);
       }
       issue([&]() {
-        mma_tile<true, true>(tmem, sR + kTile, sX0, false);
-        mma_tile<true, true>(tmem, sR, sX0, true);
-        mma_tile<true, true>(tmem + 256, sX1, sM + kTile, false);
-        mma_tile<true, true>(tmem + 256, sX1, sM, true);
+        mma_tile<kDown, kDown>(tmem, sR + kTile, sX0, false);
+        mma_tile<kDown, kDown>(tmem, sR, sX0, true);
+        mma_tile<kDown, kDown>(tmem + 256, sX1, sM + kTile, false);
+        mma_tile<kDown, kDown>(tmem + 256, sX1, sM, true);
         bulk_store(p.dO16 + (size_t)it * kTile, XV, kTile);
         bulk_commit();
         tb.id = id;
       });
-      write_tiles(Wg, Wg + kTile, tl + 384, i, qt, ik, kLoScale);
+      write_tiles<true>(Wg, Wg + kTile, tl + 384, i, qt, ik, kLoScale);
       if (tid == 0) bulk_wait_read0();  // K16, Q16, dO16
       wait_mma();
       // ---- P^T dO -> 384
@@ -597,27 +605,27 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
       for (int c = 0; c < 2; ++c) {
         float x[16];
         const int j0 = 32 * qt + 16 * c;
-        decayed16(x, tl + 128 + 16 * c, gs, gi, j0, i + 1, kScoreDown);
+        decayed16(x, tl + 128 + 16 * c, bs, gs, gi, i, q, j0, i + 1, kScoreDown);
         put_parts(R, R + kTile, swz16(i, j0 >> 3), x, 1.f);
         put_parts(R, R + kTile, swz16(i, (j0 >> 3) + 1), x + 8, 1.f);
       }
       issue([&]() {
-        mma_tile<true, true>(tmem + 384, sR + kTile, sXV, false);
-        mma_tile<true, true>(tmem + 384, sR, sXV, true);
+        mma_tile<kDown, kDown>(tmem + 384, sR + kTile, sXV, false);
+        mma_tile<kDown, kDown>(tmem + 384, sR, sXV, true);
       });
       const bool last = p.dstate_out && t_end;
       if (me.it < items) {  // K and Q have been read
         load_keys(me);
       }
-      write_tiles(Wdg, Wdg + kTile, tl, i, qt, ik, kLoScale);
+      write_tiles<true>(Wdg, Wdg + kTile, tl, i, qt, ik, kLoScale);
       wait_mma();
       // ---- w0 = T^T (P^T dO) -> 0
       put_inverse(R, R + kTile, m, i, qt, 1.f, bi);
-      write_tiles(M, M + kTile, tl + 384, i, qt, kRowsDown, 1.f);
+      write_tiles<false>(M, M + kTile, tl + 384, i, qt, kRowsDown, 1.f);
       issue([&]() {
-        mma_tile<true, true>(tmem, sR + kTile, sM, false);
-        mma_tile<true, true>(tmem, sR, sM + kTile, true);
-        mma_tile<true, true>(tmem, sR, sM, true);
+        mma_tile<kDown, kDown>(tmem, sR + kTile, sM, false);
+        mma_tile<kDown, kDown>(tmem, sR, sM + kTile, true);
+        mma_tile<kDown, kDown>(tmem, sR, sM, true);
       });
       if (me.it < items) {
         load_values(&maps.v, me.row0);
@@ -801,7 +809,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdr_scan_kernel(TcParams p, i
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            umma_bf16(tmem + 64 * part, desc_k(w + part * kTile, kk), desc_mn(sX, kk), idW, kk > 0);
+            umma_bf16(tmem + 64 * part, desc_of<kPlain>(w + part * kTile) + step_of<kPlain>(kk), desc_mn(sX, kk), idW, kk > 0);
         umma_commit(bars + SB_MMA);
         if (LEAN) {
           if (!REV) {
@@ -862,9 +870,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdr_scan_kernel(TcParams p, i
     for (int e = 0; e < 8; ++e) y[e] = f * x[e];
     put_parts(s + tile, s + tile + (at_lo - at_hi), at_hi, y, lo);
   };
-  // 8 columns of row i, times f, into a workspace tile
+  // 8 columns of row i, times f, into a plain tile of the workspace
   auto keep = [&](unsigned char* tile, const float* x, float f) {
-    *reinterpret_cast<uint4*>(tile + swz16(i, col0 >> 3)) =
+    *reinterpret_cast<uint4*>(tile + plain16(i, col0 >> 3)) =
         make_uint4(pack_f16x2(f * x[0], f * x[1]), pack_f16x2(f * x[2], f * x[3]), pack_f16x2(f * x[4], f * x[5]),
                    pack_f16x2(f * x[6], f * x[7]));
   };
@@ -1062,8 +1070,8 @@ __global__ void __launch_bounds__(256, 2) gdr_out_kernel(const __grid_constant__
   if (tid == 0) {
     wait_bar(bars, 0, p.err);
     tc_fence_after();
-    mma_tile<false, false>(tmem, sQ, sK, false);
-    mma_tile<false, true>(tmem + 128, sQ, sS, false);
+    mma_tile<kAlong, kAlong>(tmem, sQ, sK, false);
+    mma_tile<kAlong, kPlainDown>(tmem + 128, sQ, sS, false);
     umma_commit(bars + 1);
   }
   __syncwarp();
@@ -1097,7 +1105,7 @@ __global__ void __launch_bounds__(256, 2) gdr_out_kernel(const __grid_constant__
   if (tid == 0) {
     wait_bar(bars, 1, p.err);
     tc_fence_after();
-    mma_tile<false, true>(tmem, sK, sS, false);
+    mma_tile<kAlong, kPlainDown>(tmem, sK, sS, false);
     umma_commit(bars + 1);
   }
   __syncwarp();
@@ -1233,10 +1241,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
       wait_bar(bars, par, p.err);
       wait_bar(bars + 1, par, p.err);
       tc_fence_after();
-      mma_slices<false, true>(tmem, s0 + tO, s0 + tS, false);
-      mma_slices<false, true>(tmem + 128, s0 + tO, s0 + tS + kLow, false);
-      mma_slices<false, true>(tmem + 256, s0 + tY, s0 + tS, false);
-      mma_slices<true, false>(tmem + 384, s0 + tU, s0 + tD, false);
+      mma_tile<kAlong, kSlices>(tmem, s0 + tO, s0 + tS, false);
+      mma_tile<kAlong, kSlices>(tmem + 128, s0 + tO, s0 + tS + kLow, false);
+      mma_tile<kPlain, kSlices>(tmem + 256, s0 + tY, s0 + tS, false);
+      mma_tile<kSlices, kPlain>(tmem + 384, s0 + tU, s0 + tD, false);
       umma_commit(bars + 3);
     }
     __syncwarp();
@@ -1293,11 +1301,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
     __syncthreads();
     if (tid == 0) {
       tc_fence_after();
-      mma_slices<false, true>(tmem + 128, s0 + tO, s0 + tU + kLow, false);
-      mma_slices<false, true>(tmem + 128, s0 + tO, s0 + tU, true);
-      mma_slices<false, true>(tmem + 256, s0 + tY, s0 + tU, false);
+      mma_tile<kAlong, kSlices>(tmem + 128, s0 + tO, s0 + tU + kLow, false);
+      mma_tile<kAlong, kSlices>(tmem + 128, s0 + tO, s0 + tU, true);
+      mma_tile<kPlain, kSlices>(tmem + 256, s0 + tY, s0 + tU, false);
       wait_bar(bars + 2, par, p.err);
-      mma_slices<false, false>(tmem + 384, s0 + tQ, s0 + tK, false);
+      mma_tile<kAlong, kAlong>(tmem + 384, s0 + tQ, s0 + tK, false);
       umma_commit(bars + 3);
     }
     __syncwarp();
@@ -1345,10 +1353,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
     __syncthreads();
     if (tid == 0) {
       tc_fence_after();
-      mma_tile<false, true>(tmem + 128, s0 + tD, s0 + tK, false);  // R K
-      mma_tile<true, true>(tmem + 256, s0 + tD, s0 + tQ, false);   // R^T Q
-      mma_tile<false, true>(tmem + 384, s0 + tO, s0 + tK, false);  // N K
-      mma_tile<true, true>(tmem + 384, s0 + tO, s0 + tK, true);    // N^T K
+      mma_tile<kAlong, kDown>(tmem + 128, s0 + tD, s0 + tK, false);  // R K
+      mma_tile<kDown, kDown>(tmem + 256, s0 + tD, s0 + tQ, false);   // R^T Q
+      mma_tile<kAlong, kDown>(tmem + 384, s0 + tO, s0 + tK, false);  // N K
+      mma_tile<kDown, kDown>(tmem + 384, s0 + tO, s0 + tK, true);    // N^T K
       umma_commit(bars + 3);
     }
     __syncwarp();

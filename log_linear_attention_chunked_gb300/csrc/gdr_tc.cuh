@@ -93,30 +93,34 @@ __host__ __device__ constexpr uint32_t idesc_f16(int N, bool a_mn, bool b_mn) {
 // because unrolled it left the instruction cache and every phase waited for its
 // own instructions (the solve below: 58 thousand cycles unrolled).
 
-// D (+)= A B over 128 x 128 x 128 fp16; AM, BM: that operand's K runs along its rows.
-// (Eight instructions of about 65 cycles; a loop over them took 140 each.)
-template <bool AM, bool BM>
-__device__ __noinline__ void mma_tile(uint32_t d, uint32_t a, uint32_t b, bool add) {
-  constexpr uint32_t id = idesc_f16(128, AM, BM);
-  const uint64_t da = AM ? desc_mn(a, 0) : desc_k(a, 0), db = BM ? desc_mn(b, 0) : desc_k(b, 0);
-#pragma unroll
-  for (int kk = 0; kk < 8; ++kk) {
-    const uint32_t ka = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4, mn = kk * 128;
-    umma_bf16(d, da + (AM ? mn : ka), db + (BM ? mn : ka), id, (add || kk > 0) ? 1u : 0u);
-  }
+// How an operand of 128 x 128 lies in shared memory: in a tile with K along its
+// columns or down its rows; in slice tiles, K along the columns, 32 of them in every
+// 16 KB (16-bit parts of 64 bytes side by side in a row); in a plain tile, which is
+// written straight to the workspace from registers: [piece of 8 columns][row][8], a warp's
+// 16-byte stores to consecutive rows being 512 bytes in a row (with the swizzled
+// rows each of the 32 was a line of its own: 240 ns more a chunk of the scan).
+enum Lay : int { kAlong, kDown, kSlices, kPlain, kPlainDown };
+__device__ __forceinline__ uint32_t plain16(int r, int c8) { return (uint32_t)c8 * 2048u + (uint32_t)r * 16u; }
+// no swizzle: blocks of 8 rows x 16 bytes; `lbo` apart along K and `sbo` along M or N, for K down the rows likewise
+__device__ __forceinline__ uint64_t plain_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return (sw128_desc(saddr, lbo, sbo) & ~((uint64_t)7 << 61));
 }
-
-// The same with K along the columns of both; an operand `SL` lies in slice tiles, 32 of
-// its columns in every 16 KB, 16-bit parts of 64 bytes side by side in a row.
-template <bool ASL, bool BSL>
-__device__ __noinline__ void mma_slices(uint32_t d, uint32_t a, uint32_t b, bool add) {
-  constexpr uint32_t id = idesc_f16(128, false, false);
-  const uint64_t da = desc_k(a, 0), db = desc_k(b, 0);
+template <int L> __device__ __forceinline__ uint64_t desc_of(uint32_t tile) {
+  return L == kDown ? desc_mn(tile, 0) : L == kPlain ? plain_desc(tile, 2048, 128)
+         : L == kPlainDown ? plain_desc(tile, 128, 2048) : desc_k(tile, 0);
+}
+template <int L> __device__ __forceinline__ uint32_t step_of(int kk) {  // of the descriptor, to k-step kk
+  return (L == kDown ? kk * 2048 : L == kPlain ? kk * 4096 : L == kPlainDown ? kk * 256
+          : L == kSlices ? (kk >> 1) * kHalf + (kk & 1) * 32 : (kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+}
+// D (+)= A B over 128 x 128 x 128 fp16.
+// (Eight instructions of about 65 cycles; a loop over them took 140 each.)
+template <int AL, int BL>
+__device__ __noinline__ void mma_tile(uint32_t d, uint32_t a, uint32_t b, bool add) {
+  constexpr uint32_t id = idesc_f16(128, AL == kDown || AL == kPlainDown, BL == kDown || BL == kPlainDown);
+  const uint64_t da = desc_of<AL>(a), db = desc_of<BL>(b);
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk) {
-    const uint32_t k = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4, ks = ((kk >> 1) * kHalf + (kk & 1) * 32) >> 4;
-    umma_bf16(d, da + (ASL ? ks : k), db + (BSL ? ks : k), id, (add || kk > 0) ? 1u : 0u);
-  }
+  for (int kk = 0; kk < 8; ++kk) umma_bf16(d, da + step_of<AL>(kk), db + step_of<BL>(kk), id, (add || kk > 0) ? 1u : 0u);
 }
 
 __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
@@ -514,7 +518,8 @@ __device__ __noinline__ uint32_t write_rows(float* dst, uint32_t acc, int i, int
   }
   return m;
 }
-// an accumulator's row, times f, in two parts: tiles hi and lo
+// an accumulator's row, times f, in two parts: tiles hi and lo, plain ones or not
+template <bool PLAIN>
 __device__ __noinline__ void write_tiles(unsigned char* hi, unsigned char* lo, uint32_t acc, int i, int qt, float f,
                                          float scale_lo) {
 #pragma unroll 1
@@ -524,8 +529,9 @@ __device__ __noinline__ void write_tiles(unsigned char* hi, unsigned char* lo, u
     tmem_ld_wait();
 #pragma unroll
     for (int j = 0; j < 16; ++j) x[j] *= f;
-    put_parts(hi, lo, swz16(i, 4 * qt + 2 * c), x, scale_lo);
-    put_parts(hi, lo, swz16(i, 4 * qt + 2 * c + 1), x + 8, scale_lo);
+    const int c8 = 4 * qt + 2 * c;
+    put_parts(hi, lo, PLAIN ? plain16(i, c8) : swz16(i, c8), x, scale_lo);
+    put_parts(hi, lo, PLAIN ? plain16(i, c8 + 1) : swz16(i, c8 + 1), x + 8, scale_lo);
   }
 }
 // exp(g_i - g_j) = exp(g_i - g_m) exp(g_m - g_j), m the first row of i's 32: one factor of
@@ -560,11 +566,14 @@ __device__ __forceinline__ void row_decays(float* x, const float* cf, const floa
 }
 
 // 16 columns j0 .. of an accumulator's row i, times f exp(g_i - g_j), zero from the column `end` on
-__device__ __forceinline__ void decayed16(float* x, uint32_t acc, const float2* gs, float2 gi, int j0, int end, float f) {
+__device__ __forceinline__ void decayed16(float* x, uint32_t acc, const float* cf, const float2* gs, float2 gi, int i, int q,
+                                          int j0, int end, float f) {
+  float dec[16];
+  row_decays<16>(dec, cf, gs, gi, i, q, j0);
   tmem_ld16(acc, x);
   tmem_ld_wait();
 #pragma unroll
-  for (int j = 0; j < 16; ++j) x[j] = j0 + j < end ? f * x[j] * exp_diff(gi, gs[j0 + j]) : 0.f;
+  for (int j = 0; j < 16; ++j) x[j] = j0 + j < end ? f * x[j] * dec[j] : 0.f;
 }
 
 }  // namespace gdrtc
