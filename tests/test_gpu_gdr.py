@@ -5,7 +5,7 @@ Tolerances, relative to a (sequence, head) slice's largest value.  float32
 values: TOL_F32, as every float32 path here (rounding of float32 sums).  bf16
 outputs of float32 arithmetic (the token-by-token path, the decode step): half a
 step of bf16, 2^-8, on top of that.  bf16 outputs of the tensor-core path, whose
-operands (states, written rows, masked scores) are rounded to bf16 once each:
+operands (states, written rows, masked scores) are rounded to 16 bits once each:
 TOL_BF16, as every bf16 tensor-core path here."""
 
 import numpy as np
@@ -465,3 +465,186 @@ def test_wrapper_refusals(B):
     with pytest.raises(TypeError):
         B.ll_gdr_decode_step(*one, x["state_in"], slots=torch.zeros(2, dtype=torch.int32, device=DEV))
     assert B.ll_last_device_error() == 0
+
+
+# ------------------------------------------------------------------ in chunks or token by token
+def launches(B, x, n=0):
+    Bn, Hk, T, dk = x["q"].shape
+    s = B.make_gdr_shape(Bn, x["v"].shape[1], Hk, T, dk, x["v"].shape[3], n, 1.0, B._io(x["q"].dtype))
+    return B.ll_gdr_fwd_launches(s), B.ll_gdr_bwd_launches(s)
+
+
+# many heads, where short sequences run in chunks as well; 3 and 8 value heads to a key head
+@pytest.mark.parametrize("Bn,H,Hk,T,dk,dv", [
+    (4, 32, 32, 70, 128, 128), (8, 24, 8, 63, 128, 128), (16, 8, 1, 128, 128, 128), (16, 16, 16, 190, 64, 128),
+    (16, 8, 4, 250, 128, 64), (2, 8, 1, 300, 128, 128)])
+def test_short_sequences_of_many_heads(B, Bn, H, Hk, T, dk, dv):
+    x = draw(Bn, H, Hk, T, dk, dv, seed=T)
+    assert launches(B, x) == (3, 4)
+    check_fwd(B, x)
+    check_bwd(B, x)
+
+
+@pytest.mark.parametrize("starts", [[5, 6, 6, 134, 135, 300, 428, 700], [0, 0, 0, 0, 128, 128, 256, 511, 700]])
+def test_packed_many_heads(B, starts):
+    n = len(starts) - 1
+    x = draw(1, 32, 16, 707, 128, 128, n=n, seed=n)
+    for m in ("q", "k", "v", "log_alpha", "beta", "dout"):
+        x[m][:, :, starts[-1]:] = float("inf")
+        x[m][:, :, :starts[0]] = float("nan")
+    assert launches(B, x, n) == (3, 4)
+    check_fwd(B, x, starts)
+    check_bwd(B, x, starts)
+
+
+def test_more_sequences_than_tokens(B):
+    starts = [0] * 9 + [1] * 20 + [17] * 3 + [30] * 12
+    for io in ("bf16", "f32"):
+        x = draw(1, 2, 1, 33, 128, 128, io, n=len(starts) - 1, seed=5)
+        check_fwd(B, x, starts)
+        check_bwd(B, x, starts)
+
+
+@pytest.mark.parametrize("dk,dv,lo,hi", [(128, 128, 240, 260), (64, 64, 300, 330), (64, 128, 300, 330)])
+def test_both_sides_of_the_choice(B, dk, dv, lo, hi):
+    for T, n in ((lo, 1), (hi, 3)):
+        x = draw(1, 2, 1, T, dk, dv, seed=T)
+        assert launches(B, x)[0] == n
+        check_fwd(B, x)
+    for T, n in (((15, 3), (16, 4)) if dk * dv > 64 * 128 else ((63, 3), (96, 4))):
+        x = draw(1, 2, 1, T, dk, dv, seed=T)
+        assert launches(B, x)[1] == n
+        check_bwd(B, x)
+
+
+@pytest.mark.parametrize("T,io", [(50, "bf16"), (500, "bf16"), (100, "f32")])
+@pytest.mark.parametrize("k", [-30, 20])
+def test_scaling_by_powers_of_two_is_exact(B, T, io, k):
+    """Values and states scaled by 2^k scale every result by it, bit for bit:
+    no operand's range is used up or lost, whatever their size."""
+    d, f = 128, 2.0 ** k
+    x = draw(2, 4, 2, T, d, d, io, seed=23)
+    y = {n: t * f if n in ("v", "state_in") else t for n, t in x.items()}
+    z = {n: t * f if n in ("dout", "dstate_out") else t for n, t in x.items()}
+    o, s = gpu_fwd(B, x)
+    o2, s2 = gpu_fwd(B, y)
+    assert np.array_equal(o2, o * f) and np.array_equal(s2, s * f)
+    g, gy, gz = gpu_bwd(B, x), gpu_bwd(B, y), gpu_bwd(B, z)
+    for i, (a, b, c) in enumerate(zip(g, gy, gz)):  # dq, dk, dv, dlog_alpha, dbeta, dstate_in
+        assert np.array_equal(b, a if i in (2, 5) else a * f), i
+        assert np.array_equal(c, a * f), i
+
+
+@pytest.mark.parametrize("f", [2.0 ** -7, 1.375])
+def test_keys_of_other_lengths(B, f):
+    """Short ones, and long ones with beta |k|^2 still below 2, where a transition contracts."""
+    x = draw(1, 4, 2, 520, 128, 128, seed=24)
+    x["k"] = x["k"] * f
+    check_fwd(B, x)
+    check_bwd(B, x)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_bad_state_stays_alone(B, bad):
+    starts = [0, 100, 300, 700]
+    x = draw(1, 8, 4, 700, 128, 128, n=3, seed=25)
+    ref_o, ref_s = gpu_fwd(B, x, starts)
+    ref_g = gpu_bwd(B, x, starts)
+    x["state_in"][1, 3, 5, 7] = bad
+    x["dstate_out"][1, 3, 100, 2] = bad
+    o, s = gpu_fwd(B, x, starts)
+    g = gpu_bwd(B, x, starts)
+    other = [h for h in range(8) if h != 3]
+    assert not np.isfinite(s[1, 3]).all()
+    for got, ref in ((o, ref_o), (g[2], ref_g[2]), (g[3], ref_g[3]), (g[4], ref_g[4])):
+        assert np.array_equal(got[:, other], ref[:, other])
+        assert np.array_equal(got[:, 3, :100], ref[:, 3, :100]) and np.array_equal(got[:, 3, 300:], ref[:, 3, 300:])
+    for got, ref in ((s, ref_s), (g[5], ref_g[5])):
+        assert np.array_equal(got[:, other], ref[:, other]) and np.array_equal(got[[0, 2], 3], ref[[0, 2], 3])
+    for got, ref in ((g[0], ref_g[0]), (g[1], ref_g[1])):
+        assert np.array_equal(got[:, [0, 2, 3]], ref[:, [0, 2, 3]])
+
+
+@pytest.mark.parametrize("T", [60, 600])
+def test_two_graphs_and_an_eager_call_at_once(B, T):
+    names = ("q", "k", "v", "log_alpha", "beta")
+    xs = [{n: t.to(DEV) for n, t in draw(1, 4, 2, T, 128, 128, "bf16", seed=s).items()} for s in (26, 27, 28)]
+
+    def run(x):
+        a = [x[n] for n in names]
+        return [B.ll_gdr_fwd(*a, state_in=x["state_in"]), *B.ll_gdr_bwd(*a, x["dout"], state_in=x["state_in"])]
+
+    want = [run(x) for x in xs]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for x in xs[:2]:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(run(x))
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(4):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        with torch.cuda.stream(streams[2]):
+            eager = run(xs[2])
+        torch.cuda.synchronize()
+        for got, ref in zip([*outs, eager], want):
+            assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    assert B.ll_last_device_error() == 0
+
+
+@pytest.mark.parametrize("io,H,T", [("bf16", 16, (1 << 20) + 37), ("f32", 64, (1 << 18) + 5)])
+def test_more_than_two_to_the_31_elements(B, io, H, T):
+    """Both ends against the recurrence over 500 tokens: log_alpha = -0.5 leaves
+    e^-150 of what is 300 tokens away."""
+    d, near, far = 128, 200, 500
+    g = torch.Generator(device=DEV).manual_seed(29)
+    dt = torch.bfloat16 if io == "bf16" else torch.float32
+
+    def r(*s):
+        return torch.randn(*s, generator=g, device=DEV, dtype=dt)
+
+    x = dict(q=r(1, 1, T, d), k=torch.nn.functional.normalize(r(1, 1, T, d), dim=-1), v=r(1, H, T, d),
+             log_alpha=torch.full((1, H, T), -0.5, device=DEV),
+             beta=torch.rand(1, H, T, generator=g, device=DEV), dout=r(1, H, T, d))
+    a = [x[n] for n in ("q", "k", "v", "log_alpha", "beta")]
+    assert x["v"].numel() > 1 << 31
+    o = B.ll_gdr_fwd(*a, scale=0.5)
+    dq, dk, dv, dla, db = B.ll_gdr_bwd(*a, x["dout"], scale=0.5)
+    assert B.ll_last_device_error() == 0
+    for first, at in ((0, slice(0, near)), (T - far, slice(far - near, far))):
+        c = {n: t[:, :, first:first + far].cpu() for n, t in x.items()}
+        tol = tol_out(c)
+        for (i, b, h, hk, lo, hi), aa, do, _, _ in slices(c, None):
+            if h not in (0, H - 1):
+                continue
+            ref = gdr.backward(*aa, do, scale=0.5)
+            for got, want in ((o, gdr.forward(*aa, scale=0.5)[0]), (dv, ref["dv"])):
+                assert rel_err(got[0, h, first:first + far][at].float().cpu().numpy(), want[at], 0) <= tol, (h, first)
+            terms = np.abs((aa[2] * ref["dv"]).sum(-1)).max()
+            for got, want in ((dla, ref["dlog_alpha"]), (db, ref["dbeta"])):
+                den = max(np.abs(want).max(), terms)
+                assert np.abs(got[0, h, first:first + far][at].cpu().numpy() - want[at]).max() <= TOL_F32 * den
+        assert torch.isfinite(dq[0, 0, first:first + far]).all() and torch.isfinite(dk[0, 0, first:first + far]).all()
+
+
+def test_decode_far_into_a_pool(B):
+    """A pool of more than 2^31 elements."""
+    H, d, n = 32, 128, 4110
+    x = draw(3, H, 16, 1, d, d, "bf16", seed=30, init=False)
+    states = torch.zeros(n, H, d, d, device=DEV)
+    slots = [n - 1, 2, 4097]
+    x["state_in"] = 0.5 * torch.randn(3, H, d, d, generator=torch.Generator().manual_seed(4))
+    for b, s in enumerate(slots):
+        states[s] = x["state_in"][b].to(DEV)
+    args = [x[m][:, :, 0].contiguous().to(DEV) for m in ("q", "k", "v", "log_alpha", "beta")]
+    o = B.ll_gdr_decode_step(*args, states, scale=0.25, slots=torch.tensor(slots, device=DEV))
+    assert B.ll_last_device_error() == 0
+    for (i, b, h, hk, lo, hi), a, _, s0, _ in slices(x, None):
+        ro, rs = gdr.forward(*a, scale=0.25, state=s0)
+        assert rel_err(o[b, h].float().cpu().numpy(), ro[0], 0) <= 2.0 ** -8 + TOL_F32
+        assert rel_err(states[slots[b], h].cpu().numpy(), rs, 0) <= TOL_F32
+    rest = torch.ones(n, dtype=torch.bool)
+    rest[slots] = False
+    assert not states[rest.to(DEV)].any()
