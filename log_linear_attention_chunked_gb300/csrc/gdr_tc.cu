@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
   float* inv = reinterpret_cast<float*>(red + 48);       // inverse scales of V and Q
   float* cf = reinterpret_cast<float*>(s + Sm::kM);  // the columns' decay factors, where M comes to stand
   uint64_t* bar = reinterpret_cast<uint64_t*>(s + Sm::kBars);
-  // bar: products, K, U, Q, V and dO
+  // bar: products, K, U, Q, V and dO, Q K^T
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s + Sm::kBars + 6 * 8);
   Item* next = reinterpret_cast<Item*>(s + Sm::kNext);
   float* Ap = reinterpret_cast<float*>(s + Sm::kR);
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
   const uint32_t sX0 = smem_u32(X0), sX1 = smem_u32(X1), sXV = smem_u32(XV), sR = smem_u32(R),
                  sM = smem_u32(M);
   if (tid == 0) {
-    for (int b = 0; b < 5; ++b) mbar_init(bar + b, 1);
+    for (int b = 0; b < 6; ++b) mbar_init(bar + b, 1);
     fence_mbar_init();
     find_item(p, blockIdx.x, gridDim.x, next);
   }
@@ -436,18 +436,18 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
       load_tile(X1, &maps.q, (int)x.krow0, bar + 3);
     }
     __syncwarp();
-    la = tid < x.n ? gdr_log(p.log_alpha[x.row0 + tid]) : 0.f;
+    la = tid < x.n ? p.log_alpha[x.row0 + tid] : 0.f;  // (not used before the next item)
     bt = tid < x.n ? p.beta[x.row0 + tid] : 0.f;
   };
   uint32_t nv = 0, nkq = 0;  // loads of V and dO, and of K, waited for
-  auto load_values = [&](const CUtensorMap* map, size_t row) {
-    if (tid == 0) load_tile(XV, map, (int)row, bar + 4);
+  auto load_values = [&](const CUtensorMap* map, size_t row, int by) {
+    if (tid == by) load_tile(XV, map, (int)row, bar + 4);
     __syncwarp();
   };
   Item me = *next;
   if (me.it < items) {
     load_keys(me);
-    load_values(&maps.v, me.row0);
+    load_values(&maps.v, me.row0, 0);
   }
   while (me.it < items) {
     const int it = me.it, n = me.n;
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     unsigned char* Wdg = p.Wd + (size_t)it * 2 * kTile;
     const float beta_i = bt;
     const bool t_end = me.t0 + n == me.len;
-    chunk_decays(la, gs, tot, tid, 0, kPrepThreads);
+    chunk_decays(gdr_log(la), gs, tot, tid, 0, kPrepThreads);
     column_decays(cf, gs, tid);
     const float2 gi = gs[i];
     if (qt == 0) {
@@ -508,7 +508,12 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
       const float iv = tile_to_f16<256>(XV, n, red + 16, t, kPrepBar2, &vbits);
       wait_bar(bar + 3, nkq & 1, p.err);
       const float iq = tile_to_f16<256>(X1, n, red + 32, t, kPrepBar2, nullptr);
-      if (t == 0) {
+      tc_fence_before();
+      named_bar_sync(kPrepBar2, 256);
+      if (t == 0) {  // Q K^T -> 128, while the tensor cores are free
+        tc_fence_after();
+        mma_tile<kAlong, kAlong>(tmem + 128, sX1, sX0, false);
+        umma_commit(bar + 5);
         atomicMax(am_s, vbits);
         inv[0] = iv;
         inv[1] = iq;
@@ -542,7 +547,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     ++nv;
     ++nkq;
     const float iv = inv[0], iq = inv[1], bi = bs[i];
-    // ---- U = T' V -> 256 (with Q K^T -> 128), W = T' diag(exp(g)) K -> 384
+    // ---- U = T' V -> 256, W = T' diag(exp(g)) K -> 384
     float m[32];
     load_m(m, Mp, i, qt);
     __syncthreads();
@@ -551,7 +556,6 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
       mma_tile<kAlong, kDown>(tmem + 256, sR + kTile, sXV, false);
       mma_tile<kAlong, kDown>(tmem + 256, sR, sXV, true);
       umma_commit(bar + 2);
-      mma_tile<kAlong, kAlong>(tmem + 128, sX1, sX0, false);
       mma_tile<kAlong, kDown>(tmem + 384, sM + kTile, sX0, false);
       mma_tile<kAlong, kDown>(tmem + 384, sM, sX0, true);
       if (h % G == 0) {
@@ -563,7 +567,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     __syncwarp();
     tc_fence_after();
     {
-      load_values(&maps.dout, row0);  // (V has been read)
+      load_values(&maps.dout, row0, 256);  // (V has been read; thread 0 may still be issuing products)
       write_rows(p.U + (size_t)it * kC * kC, tl + 256, i, qt, iv);
       const float rel = exp_diff(gi, gs[0]), in0 = in_s[0];
       // ---- Wd = T^T diag(exp(g_C - g)) K -> 0, Bc = Q^T diag(exp(g)) dO -> 256 (exp(g_0) and its scales below)
@@ -601,6 +605,9 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
       if (tid == 0) bulk_wait_read0();  // K16, Q16, dO16
       wait_mma();
       // ---- P^T dO -> 384
+      wait_bar(bar + 5, (nkq - 1) & 1, p.err);
+      __syncwarp();
+      tc_fence_after();
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
         float x[16];
@@ -628,7 +635,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
         mma_tile<kDown, kDown>(tmem, sR, sM, true);
       });
       if (me.it < items) {
-        load_values(&maps.v, me.row0);
+        load_values(&maps.v, me.row0, 0);
       }
       uint32_t mx = write_rows(p.Bc + (size_t)it * kC * kC, tl + 256, i, qt, p.scale * iq * id * in0);
       if (last) mx = max(mx, state_max(p.dstate_out + sh * p.dv * p.dk));
