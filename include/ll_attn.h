@@ -388,7 +388,24 @@ LL_API ll_status ll_gdn_fwd_b(const ll_shape* shape, const void* q, const void* 
  * the base model of the log-linear Gated DeltaNet above, whose level states
  * follow the same transition: states have the layout of ll_gdn_decode_step's.
  * Sequences run from given states to returned ones, can be packed end to end,
- * and several value heads can share a key head. */
+ * and several value heads can share a key head.
+ *
+ * Two ways of computing, chosen by types and sizes alone (ll_gdr_*_launches
+ * tells which).  Token by token, every io dtype and head size: float32
+ * arithmetic throughout.  In chunks of 128 tokens on the tensor cores, bf16 io
+ * with dk and dv of 64 or 128, where it is the faster: operands are scaled by
+ * powers of two to fp16, in two parts (22 bits) where a state or a gate's
+ * gradient depends on them, sums are float32; states, dlog_alpha and dbeta keep
+ * float32 accuracy, o, dq, dk and dv that of a 16-bit operand.  beta |k|^2 <= 2
+ * is expected (L2-normalised keys keep it), so that a token's transition does
+ * not grow its state; not checked.  In chunks a state has room for 4096 times
+ * the largest |v| and |state_in| of its sequence and head, its gradient likewise
+ * for 4096 times the largest value that a chunk or dstate_out adds to it.
+ * Infinities and NaN stay within their sequence and, in v, gates, states and
+ * upstream gradients, within their head (and its key head's dq and dk).
+ *
+ * Calls allocate nothing, do not synchronise and can be captured; a workspace
+ * serves one call at a time. */
 
 /* Problem shape of ll_gdr_fwd and ll_gdr_bwd.
  *   B, T      batch rows and tokens per row (>= 1)
@@ -410,7 +427,8 @@ typedef struct {
 /* Bytes of workspace ll_gdr_fwd needs (0 when it needs none, or on an invalid shape). */
 LL_API size_t ll_gdr_fwd_workspace_size(const ll_gdr_shape* shape);
 
-/* Kernel launches of one ll_gdr_fwd call (0 on an invalid shape). */
+/* Kernel launches of one ll_gdr_fwd call: 1 token by token, 3 in chunks (which
+ * also clear a few bytes of the workspace by a memset); 0 on an invalid shape. */
 LL_API int ll_gdr_fwd_launches(const ll_gdr_shape* shape);
 
 /* Forward of the gated delta rule over whole sequences.
@@ -419,8 +437,7 @@ LL_API int ll_gdr_fwd_launches(const ll_gdr_shape* shape);
  *              written.  A sequence with bounds that break this sets the device
  *              error word (LL_ERR_DEVICE) and is skipped.
  *   q, k       [B,Hk,T,dk]  io dtype;   v, o [B,H,T,dv] io dtype
- *   log_alpha, beta [B,H,T] float32 (log_alpha = -inf forgets the state; keys
- *              are expected to be L2-normalised, not checked)
+ *   log_alpha, beta [B,H,T] float32, log_alpha <= 0 (-inf forgets the state)
  *   state_in   [N,H,dv,dk]  float32 or NULL (zero states), N = n_seqs or B
  *   state_out  [N,H,dv,dk]  float32 or NULL: the states after the last token
  *              (state_in's for an empty sequence).  May be state_in itself.
@@ -435,7 +452,8 @@ LL_API ll_status ll_gdr_fwd(const ll_gdr_shape* shape, const int32_t* seq_starts
 /* Bytes of workspace ll_gdr_bwd needs (0 on an invalid shape). */
 LL_API size_t ll_gdr_bwd_workspace_size(const ll_gdr_shape* shape);
 
-/* Kernel launches of one ll_gdr_bwd call (0 on an invalid shape). */
+/* Kernel launches of one ll_gdr_bwd call: 3 token by token, 4 in chunks (and a
+ * memset, as above); 0 on an invalid shape. */
 LL_API int ll_gdr_bwd_launches(const ll_gdr_shape* shape);
 
 /* Backward of ll_gdr_fwd: for f = sum(o . dout) + sum(state_out . dstate_out)

@@ -136,7 +136,7 @@ struct TcMaps {  // [rows, d] bf16, boxes of 64 columns and 128 rows
 };
 
 constexpr float kScoreDown = 1.f / 256.f;  // of the scores Q K^T of scaled tiles, as operands
-constexpr float kKeysDown = 1.f / 4096.f;   // of K K^T of the scaled tile
+constexpr float kKeysDown = 1.f / 64.f;    // of K K^T of the scaled tile (at most 128 x 16^2)
 constexpr float kRowsDown = 1.f / 16.f;    // of P^T dO, as an operand
 
 // Both are persistent, one CTA per SM, an item per (chunk, head).  Thread = (row,
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     column_decays(cf, gs, t);
     wait_bar(bar + 3 + b, (j >> 1) & 1, p.err);
     const float ik = tile_to_f16<256>(X0 + b * kTile, x.n, red, t, kPrepBar2, nullptr);
-    // A is K K^T of the scaled tile / 4096, beta takes the difference
+    // A is K K^T of the scaled tile, beta takes the scale
     beta_n = bt * (ik * ik / kKeysDown);
     Tables& tb = p.tab[x.it];
     if (t < kC) {
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     if (t == 0 && nx.it < items) load_tile(XV, &maps.v, (int)nx.row0, bar + 5);
     __syncwarp();
     // U and W leave by way of the operands' places
-    write_rows(reinterpret_cast<float*>(R), tl + 256, i, qt, iv);
+    write_rows(reinterpret_cast<float*>(R), tl + 256, i, qt, iv / kInvUp);
     fence_proxy_async_shared();
     __syncthreads();
     if (tid == 0) {
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
       load_k(next[b], b);
     }
     __syncwarp();
-    write_tiles<true>(M, M + kTile, tl + 384, i, qt, ik, kLoScale);
+    write_tiles<true>(M, M + kTile, tl + 384, i, qt, ik / kInvUp, kLoScale);
     fence_proxy_async_shared();
     tc_fence_before();
     __syncthreads();
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     if (p.state_in && me.chunk == 0) raise_max(am_s, state_max(p.state_in + sh * p.dv * p.dk));
     wait_bar(bar + 1, nkq & 1, p.err);
     const float ik = tile_to_f16<kPrepThreads>(X0, n, red, tid, 0, nullptr);
-    // A is K K^T of the scaled tile / 4096, beta takes the difference
+    // A is K K^T of the scaled tile, beta takes the scale
     if (tid < kC) bs[tid] = beta_i * (ik * ik / kKeysDown);
     // ---- K K^T -> 0
     issue([&]() {
@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     tc_fence_after();
     {
       load_values(&maps.dout, row0, 256);  // (V has been read; thread 0 may still be issuing products)
-      write_rows(p.U + (size_t)it * kC * kC, tl + 256, i, qt, iv);
+      write_rows(p.U + (size_t)it * kC * kC, tl + 256, i, qt, iv / kInvUp);
       const float rel = exp_diff(gi, gs[0]), in0 = in_s[0];
       // ---- Wd = T^T diag(exp(g_C - g)) K -> 0, Bc = Q^T diag(exp(g)) dO -> 256 (exp(g_0) and its scales below)
       put_inverse(R, R + kTile, m, i, qt, out_s[i], bi);
@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
         bulk_commit();
         tb.id = id;
       });
-      write_tiles<true>(Wg, Wg + kTile, tl + 384, i, qt, ik, kLoScale);
+      write_tiles<true>(Wg, Wg + kTile, tl + 384, i, qt, ik / kInvUp, kLoScale);
       if (tid == 0) bulk_wait_read0();  // K16, Q16, dO16
       wait_mma();
       // ---- P^T dO -> 384
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
       if (me.it < items) {  // K and Q have been read
         load_keys(me);
       }
-      write_tiles<true>(Wdg, Wdg + kTile, tl, i, qt, ik, kLoScale);
+      write_tiles<true>(Wdg, Wdg + kTile, tl, i, qt, ik / kInvUp, kLoScale);
       wait_mma();
       // ---- w0 = T^T (P^T dO) -> 0
       put_inverse(R, R + kTile, m, i, qt, 1.f, bi);
@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
       if (last) mx = max(mx, state_max(p.dstate_out + sh * p.dv * p.dk));
       wait_mma();
       mx = max(mx, write_rows(p.w0 + (size_t)it * kC * kC, tl, i, qt,
-                              p.scale * iq * ik * id / (kScoreDown * kRowsDown)));
+                              p.scale * iq * ik * id / (kScoreDown * kRowsDown * kInvUp)));
       raise_max(p.amax_d + sh, mx);
     }
     tc_fence_before();  // (for the next item's products, behind its barriers)

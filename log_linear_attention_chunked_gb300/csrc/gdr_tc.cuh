@@ -163,6 +163,12 @@ __device__ __forceinline__ void put_parts(unsigned char* hi, unsigned char* lo, 
   *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
+// What is of the size of an inverse's entries (at most beta |k| |k|, mostly far below 1) is
+// split into fp16 parts times this: the low part of a value below 1/4 would be
+// subnormal, with an error of 2^-25 whatever the value (gate gradients 1.3e-6 off
+// instead of 7e-7, B 2, T 4096).  Entries up to 1000 fit.
+constexpr float kInvUp = 64.f;
+
 // ---- the triangular solve, float32 on the CUDA cores.  With A = SL(K K^T . G)
 // of a 128-token chunk, M solves (I + A diag(beta)) M = -A, so that both inverses
 // are unit triangular and exact for any beta, zero and tiny ones included:
@@ -235,7 +241,7 @@ __device__ __forceinline__ void block_mma(float (*z)[4], BlockRaw<NT>& v) {
 }
 
 // One doubling, N >= 16 rows to a half; the places of A's finished blocks hold
-// M diag(beta).  Eight warps, barrier kSolveBar: pair, 16-row block and half of
+// kInvUp M diag(beta).  Eight warps, barrier kSolveBar: pair, 16-row block and half of
 // the columns to each.
 constexpr int kSolveBar = 1;
 template <int N>
@@ -256,7 +262,7 @@ __device__ __noinline__ void tri_double(float* Ap, float* Mp, const float* beta,
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const float2 x = mat2(Ap, row + g, c + 8 * n + 2 * t), y = mat2(Ap, row + g + 8, c + 8 * n + 2 * t);
-    z[n][0] = x.x; z[n][1] = x.y; z[n][2] = y.x; z[n][3] = y.y;
+    z[n][0] = kInvUp * x.x; z[n][1] = kInvUp * x.y; z[n][2] = kInvUp * y.x; z[n][3] = kInvUp * y.y;
   }
   BlockRaw<NT> cur, nxt;  // (the next block's values are on their way during this one's products)
   block_load<NT>(nxt, x_at(Ap, r0 + N), xa, Ap + (r0 + N) * kC, yc);
@@ -287,8 +293,8 @@ __device__ __noinline__ void tri_double(float* Ap, float* Mp, const float* beta,
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int cc = c + 8 * n + 2 * t;
-    mat2(Mp, row + g, cc) = make_float2(-z[n][0], -z[n][1]);
-    mat2(Mp, row + g + 8, cc) = make_float2(-z[n][2], -z[n][3]);
+    mat2(Mp, row + g, cc) = make_float2(-z[n][0] / kInvUp, -z[n][1] / kInvUp);
+    mat2(Mp, row + g + 8, cc) = make_float2(-z[n][2] / kInvUp, -z[n][3] / kInvUp);
     if (N < 64) {
       const float2 bt = *reinterpret_cast<const float2*>(beta + cc);
       mat2(Ap, row + g, cc) = make_float2(-bt.x * z[n][0], -bt.y * z[n][1]);
@@ -329,7 +335,7 @@ __device__ __noinline__ void tri_solve(float* Ap, float* Mp, const float* beta, 
     for (int r = 0; r < 8; ++r) {
       const int at = mat_at(r0 + r, (r0 + cc) >> 2) + (cc & 3);
       Mp[at] = acc[r];
-      Ap[at] = bc * acc[r];
+      Ap[at] = kInvUp * bc * acc[r];
     }
     if (r0 & 8)  // zeros above the diagonal of the 16 x 16 block (A has them)
 #pragma unroll
@@ -344,6 +350,8 @@ __device__ __noinline__ void tri_solve(float* Ap, float* Mp, const float* beta, 
   {  // 8 x 8: a pair to a warp, two outputs to a thread
     const int r0 = 16 * (t >> 5), row = r0 + 8 + ((t >> 2) & 7), c = r0 + 2 * (t & 3);
     float2 z = mat2(Ap, row, c);
+    z.x *= kInvUp;
+    z.y *= kInvUp;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float a = mat1(Ap, row, r0 + 8 + k);
@@ -362,7 +370,7 @@ __device__ __noinline__ void tri_solve(float* Ap, float* Mp, const float* beta, 
       z.y = fmaf(a, b.y, z.y);
     }
     __syncwarp();
-    mat2(Mp, row, c) = make_float2(-z.x, -z.y);
+    mat2(Mp, row, c) = make_float2(-z.x / kInvUp, -z.y / kInvUp);
     mat2(Ap, row, c) = make_float2(-bt.x * z.x, -bt.y * z.y);
   }
   named_bar_sync(kSolveBar, 256);
@@ -467,7 +475,7 @@ __device__ __forceinline__ void load_m(float* m, float* Mp, int i, int qt) {
     m[4 * v + 3] = x.w;
   }
 }
-// rows of I + M diag(beta) in two parts, and of that times diag(f2)
+// rows of kInvUp (I + M diag(beta)) in two parts, and of that times diag(f2)
 __device__ __forceinline__ void put_inverse2(unsigned char* t1, unsigned char* t2, const float* m, int i, int qt,
                                              const float* beta, const float* f2) {
 #pragma unroll
@@ -480,7 +488,7 @@ __device__ __forceinline__ void put_inverse2(unsigned char* t1, unsigned char* t
       const float b[4] = {b4.x, b4.y, b4.z, b4.w}, f[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        x[4 * v + e] = j + e == i ? 1.f : b[e] * m[8 * c + 4 * v + e];
+        x[4 * v + e] = j + e == i ? kInvUp : kInvUp * b[e] * m[8 * c + 4 * v + e];
         y[4 * v + e] = x[4 * v + e] * f[e];
       }
     }
@@ -488,14 +496,14 @@ __device__ __forceinline__ void put_inverse2(unsigned char* t1, unsigned char* t
     put_parts(t2, t2 + kTile, swz16(i, 4 * qt + c), y, 1.f);
   }
 }
-// rows of diag(f) (I + diag(beta) M) in two parts
+// rows of kInvUp diag(f) (I + diag(beta) M) in two parts
 __device__ __forceinline__ void put_inverse(unsigned char* hi, unsigned char* lo, const float* m, int i, int qt, float f,
                                             float beta) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = (32 * qt + 8 * c + e == i ? 1.f : beta * m[8 * c + e]) * f;
+    for (int e = 0; e < 8; ++e) x[e] = (32 * qt + 8 * c + e == i ? kInvUp : kInvUp * beta * m[8 * c + e]) * f;
     put_parts(hi, lo, swz16(i, 4 * qt + c), x, 1.f);
   }
 }
