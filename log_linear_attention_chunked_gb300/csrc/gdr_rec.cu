@@ -18,7 +18,9 @@
 // neighbouring keys are made once per staged tile.  Arithmetic is on pairs of
 // floats (one instruction for two).  Half of a CTA's threads walk over the tokens;
 // the others stage the tile after the next, make the next tile's products of
-// neighbours and write the last tile's results, one barrier a tile.
+// neighbours and write the last tile's results, one barrier a tile.  A token takes
+// 0.12 us at d_k = 128 (0.08 at 32) while every CTA has an SM's schedulers to
+// itself: T = 1001, 8 heads of 32 x 64, float32, 80 us, from 133 with the sums in line.
 #include "gdr.cuh"
 #include "sm100.cuh"
 
@@ -36,6 +38,12 @@ constexpr int kTile = 16;    // tokens staged at a time
 static_assert(kGdrGradChunk % kTile == 0, "kept states lie on tile boundaries");
 static_assert(kTile % 3 == 1, "the loops over a whole tile take three tokens at a time and one more");
 
+// Lanes per row: fewer make a longer dot product of a lane, more a longer sum
+// over the lanes (and threads that share an SM's issue slots).  Measured, forward / gradient in
+// us, float32, 512 tokens, 8 and 256 heads: d = 128 with 4 lanes 96 / 250 and 1006 / 3248, with 8
+// 69 / 206 and 745 / 2823, with 16 93 / 242 and 1269 / 3522; d = 64 with 2, 4, 8: 81 / 188, 50 / 135, 53 / 134
+// and 294 / 1208, 200 / 1035, 247 / 1114; d = 32 with 2, 4, 8: 44 / 104, 42 / 97, 42 / 100 and 84 / 363, 73 / 341,
+// 96 / 383; d = 16 with 2, 4: 30 / 72, 31 / 73 and 31 / 175, 41 / 189.
 template <int DK> struct RowCfg {
   static constexpr int kLpr = DK >= 128 ? 8 : DK >= 32 ? 4 : 2;  // lanes per row
   static constexpr int kEpl = DK / kLpr;          // elements per lane
@@ -487,12 +495,15 @@ __global__ void __launch_bounds__(2 * RowCfg<DK>::kThreads) gdr_rec_bwd_kernel(R
 }
 
 // ---------------------------------------------------------------- one decode step
-constexpr int kStepPasses = 2;  // rows in flight per group of lanes
+// Rows in flight per group of lanes.  Measured with 1, 2 and 4 (128 x 128): 32 states 3.2, 3.1 and 3.8
+// us, 256 states 6.8, 6.2 and 6.3, 2048 states 44.8, 44.7 and 44.9.
+constexpr int kStepPasses = 2;
 
 // Per (b, h): the state is read and written once, which is what bounds the
 // step.  A group of lanes takes kStepPasses rows, all their loads issued
 // before any is used; 16 * kStepPasses rows of d_v to a CTA, so that one
-// request of few heads still spreads over the SMs.
+// request of few heads still spreads over the SMs.  268 MB (2048 states of 128 x 128)
+// in 47 us behind a flushed L2, 85 % of a copy's rate; 885 MB in 141 us, 93 %.
 template <typename IO, int DK>
 __global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_decode_kernel(
     int H, int Hk, int dv, float scale, const int64_t* __restrict__ slots, int n_slots, const IO* __restrict__ q,

@@ -141,7 +141,10 @@ constexpr float kRowsDown = 1.f / 16.f;    // of P^T dO, as an operand
 
 // Both are persistent, one CTA per SM, an item per (chunk, head).  Thread = (row,
 // quarter of the columns); while warps 0 to 7 solve for M, the others prepare
-// what is needed next.
+// what is needed next.  The latency of an item's chain bounds them, the solve half
+// of it: seven tiles fill the shared memory, so that no second item is in
+// work beside it.  Measured: forward 13.2 us an item and SM (178 us for 2048 items),
+// backward 28 (188 us for 1024), 3 TB/s of its own traffic.
 constexpr int kPrepThreads = 512, kPrepBar2 = 2;
 
 // The forward's.  Warps 8 to 15 make V's operand and, a whole item ahead, everything
@@ -353,7 +356,9 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
   }
 }
 
-// The backward's.
+// The backward's.  Products are issued by thread 0, which they hold for as long as they
+// run (about 100 cycles each); with a warp of its own for that, 544 threads leave 96
+// registers each, and an item took 31 us.
 __global__ void __launch_bounds__(kPrepThreads, 1)
     gdr_prep_bwd_kernel(const __grid_constant__ TcMaps maps, TcParams p) {
   using Sm = PrepSm;
@@ -686,7 +691,10 @@ enum ScanBar : int { SB_W0 = 0, SB_W1, SB_K0, SB_K1, SB_R0, SB_R1, SB_ERR, SB_BC
 // what does not belong to the chain is done in the products' time.  With most of
 // the SM's memory taken as shared memory, little is left for loads in flight
 // through L1 (72 KB of them a chunk took 4 thousand cycles to issue): the modes
-// with many rows have them copied into shared memory instead.
+// with many rows have them copied into shared memory instead.  Measured per chunk:
+// forward 1.77 us (226 us for 128 chunks of 16 heads, 64 CTAs); with 128 CTAs,
+// for the gradient 2.3 us forwards and 3.2 backwards, whose rows and tiles, 350 and 510 KB
+// a chunk and head, go at 4.8 and 5.2 TB/s.
 constexpr int kScanThreads = 512 + 32;
 constexpr int kScanBarX = 1, kScanBarE = 2, kScanBarU = 3;  // named barriers: an operand, the staged rows are ready
 template <int MODE>
@@ -1027,7 +1035,8 @@ constexpr uint32_t kOBars = kOTab + 2 * kC * 4 + 32;
 constexpr uint32_t kOCol = kOBars + 32;
 constexpr uint32_t kOutSmem = kOCol + kColDecays * 4;
 
-// One CTA per (chunk, head), two per SM.
+// One CTA per (chunk, head), two per SM, so that one's loads and stores run beside the
+// other's products.  Bound by memory: 160 KB an item, 336 MB for 2048 items in 64 us, 5.2 TB/s.
 __global__ void __launch_bounds__(256, 2) gdr_out_kernel(const __grid_constant__ TcMaps maps, TcParams p) {
   extern __shared__ __align__(1024) unsigned char s[];
   if (smem_u32(s) & 1023u) {
@@ -1163,8 +1172,10 @@ constexpr int kGradThreads = 512;
 // Persistent, one CTA per SM, an item per (chunk, key head); the value heads that
 // share it are taken in turn, dq and dk adding up in registers in a fixed order.
 // Thread = (row, quarter of the columns).  The next head's or item's tiles are
-// loaded as soon as a tile's last product is done.  Per head three rounds of products over seven tiles of shared
-// memory:
+// loaded as soon as a tile's last product is done.  Measured: 114 us for 1024 items (390 MB,
+// 3.4 TB/s; 140 with a CTA per item, whose loads nothing overlapped), bound by the
+// chain of its three rounds.  Per head three rounds of products over seven tiles of
+// shared memory:
 //   dO S, (beta w) S, u D;   dO u^T, (beta w) u^T, Q K^T;   R K, R^T Q, (N + N^T) K
 // with R = scale (dO u^T . G) and N = ((beta w) u^T . G) strictly lower.  The
 // first and fourth take S and u in two parts: q.dq, which enters dlog_alpha, is
@@ -1241,200 +1252,200 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
     const size_t krow0 = me.krow0;
 #pragma unroll
     for (int j = 0; j < 32; ++j) xq[j] = xk[j] = 0.f;
-  for (int hh = 0; hh < G; ++hh, par ^= 1) {
-    const size_t it = head_of(unit, hh), sh = (size_t)me.seq * p.seqs.H + (unit % p.seqs.Hk) * G + hh;
-    const size_t row0 = me.row0 + (size_t)hh * p.seqs.T;
-    if (tid == 0) {
-      wait_bar(bars, par, p.err);
-      wait_bar(bars + 1, par, p.err);
-      tc_fence_after();
-      mma_tile<kAlong, kSlices>(tmem, s0 + tO, s0 + tS, false);
-      mma_tile<kAlong, kSlices>(tmem + 128, s0 + tO, s0 + tS + kLow, false);
-      mma_tile<kPlain, kSlices>(tmem + 256, s0 + tY, s0 + tS, false);
-      mma_tile<kSlices, kPlain>(tmem + 384, s0 + tU, s0 + tD, false);
-      umma_commit(bars + 3);
-    }
-    __syncwarp();
-    const Tables& tb = p.tab[it];
-    if (tid < kC) gs[tid] = tb.g[tid];
-    column_decays(cf, tb.g, tid - 256 < 0 ? kColDecays : tid - 256);
-    float* dg = reinterpret_cast<float*>(p.part + (it * kParts + 16) * kC);  // [4][token]
-    const float ik = tb.ik, iq = tb.iq, id = tb.id, in = tb.into[i], out = tb.out[i];
-    const float isf = operand_scale(__uint_as_float(p.amax_s[sh])).y, isr = operand_scale(__uint_as_float(p.amax_d[sh])).y;
-    uint4 qv[4];  // this thread's piece of Q's row
+    for (int hh = 0; hh < G; ++hh, par ^= 1) {
+      const size_t it = head_of(unit, hh), sh = (size_t)me.seq * p.seqs.H + (unit % p.seqs.Hk) * G + hh;
+      const size_t row0 = me.row0 + (size_t)hh * p.seqs.T;
+      if (tid == 0) {
+        wait_bar(bars, par, p.err);
+        wait_bar(bars + 1, par, p.err);
+        tc_fence_after();
+        mma_tile<kAlong, kSlices>(tmem, s0 + tO, s0 + tS, false);
+        mma_tile<kAlong, kSlices>(tmem + 128, s0 + tO, s0 + tS + kLow, false);
+        mma_tile<kPlain, kSlices>(tmem + 256, s0 + tY, s0 + tS, false);
+        mma_tile<kSlices, kPlain>(tmem + 384, s0 + tU, s0 + tD, false);
+        umma_commit(bars + 3);
+      }
+      __syncwarp();
+      const Tables& tb = p.tab[it];
+      if (tid < kC) gs[tid] = tb.g[tid];
+      column_decays(cf, tb.g, tid - 256 < 0 ? kColDecays : tid - 256);
+      float* dg = reinterpret_cast<float*>(p.part + (it * kParts + 16) * kC);  // [4][token]
+      const float ik = tb.ik, iq = tb.iq, id = tb.id, in = tb.into[i], out = tb.out[i];
+      const float isf = operand_scale(__uint_as_float(p.amax_s[sh])).y, isr = operand_scale(__uint_as_float(p.amax_d[sh])).y;
+      uint4 qv[4];  // this thread's piece of Q's row
 #pragma unroll
-    for (int v = 0; v < 4; ++v)
-      qv[v] = i < n && j0 < p.dk ? *reinterpret_cast<const uint4*>(p.q + (krow0 + i) * p.dk + j0 + 8 * v)
-                                 : make_uint4(0u, 0u, 0u, 0u);
-    wait_mma();
-    if (tid == 0) {
-      mbar_arrive_expect_tx(bars + 2, 2 * kTile);
-      bulk_load(s + tQ, p.Q16 + (size_t)unit * kTile, kTile, bars + 2);
-      bulk_load(s + tK, p.K16 + (size_t)unit * kTile, kTile, bars + 2);
-    }
-    __syncwarp();
-    // ---- round 1: dq's and dk's parts by the states, q.dq's first part
-    float qdot = 0.f;
-    {
-      const float fq = p.scale * in * id * isf, fu = isf * isr * out, fw = -isf * isr * in;
+      for (int v = 0; v < 4; ++v)
+        qv[v] = i < n && j0 < p.dk ? *reinterpret_cast<const uint4*>(p.q + (krow0 + i) * p.dk + j0 + 8 * v)
+                                   : make_uint4(0u, 0u, 0u, 0u);
+      wait_mma();
+      if (tid == 0) {
+        mbar_arrive_expect_tx(bars + 2, 2 * kTile);
+        bulk_load(s + tQ, p.Q16 + (size_t)unit * kTile, kTile, bars + 2);
+        bulk_load(s + tK, p.K16 + (size_t)unit * kTile, kTile, bars + 2);
+      }
+      __syncwarp();
+      // ---- round 1: dq's and dk's parts by the states, q.dq's first part
+      float qdot = 0.f;
+      {
+        const float fq = p.scale * in * id * isf, fu = isf * isr * out, fw = -isf * isr * in;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float a[16], x[16];
-        tmem_ld16(tl + 256 + 16 * c, a);
-        tmem_ld16(tl + 384 + 16 * c, x);
-        tmem_ld_wait();
+        for (int c = 0; c < 2; ++c) {
+          float a[16], x[16];
+          tmem_ld16(tl + 256 + 16 * c, a);
+          tmem_ld16(tl + 384 + 16 * c, x);
+          tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) xk[16 * c + j] += fmaf(fu, x[j], fw * a[j]);
-        tmem_ld16(tl + 16 * c, a);
-        tmem_ld16(tl + 128 + 16 * c, x);
-        tmem_ld_wait();
+          for (int j = 0; j < 16; ++j) xk[16 * c + j] += fmaf(fu, x[j], fw * a[j]);
+          tmem_ld16(tl + 16 * c, a);
+          tmem_ld16(tl + 128 + 16 * c, x);
+          tmem_ld_wait();
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const uint4 qq = qv[2 * c + v];
-          const uint32_t w[4] = {qq.x, qq.y, qq.z, qq.w};
+          for (int v = 0; v < 2; ++v) {
+            const uint4 qq = qv[2 * c + v];
+            const uint32_t w[4] = {qq.x, qq.y, qq.z, qq.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = 8 * v + 2 * e;
-            const float y0 = fq * fmaf(kLoInv, x[j], a[j]), y1 = fq * fmaf(kLoInv, x[j + 1], a[j + 1]);
-            const float2 f = unpack_bf16x2(w[e]);
-            qdot = fmaf(f.x, y0, fmaf(f.y, y1, qdot));
-            xq[16 * c + j] += y0;
-            xq[16 * c + j + 1] += y1;
+            for (int e = 0; e < 4; ++e) {
+              const int j = 8 * v + 2 * e;
+              const float y0 = fq * fmaf(kLoInv, x[j], a[j]), y1 = fq * fmaf(kLoInv, x[j + 1], a[j + 1]);
+              const float2 f = unpack_bf16x2(w[e]);
+              qdot = fmaf(f.x, y0, fmaf(f.y, y1, qdot));
+              xq[16 * c + j] += y0;
+              xq[16 * c + j + 1] += y1;
+            }
           }
         }
       }
-    }
-    tc_fence_before();
-    __syncthreads();
-    if (tid == 0) {
-      tc_fence_after();
-      mma_tile<kAlong, kSlices>(tmem + 128, s0 + tO, s0 + tU + kLow, false);
-      mma_tile<kAlong, kSlices>(tmem + 128, s0 + tO, s0 + tU, true);
-      mma_tile<kPlain, kSlices>(tmem + 256, s0 + tY, s0 + tU, false);
-      wait_bar(bars + 2, par, p.err);
-      mma_tile<kAlong, kAlong>(tmem + 384, s0 + tQ, s0 + tK, false);
-      umma_commit(bars + 3);
-    }
-    __syncwarp();
-    wait_mma();
-    if (tid == 0 && (hh + 1 < G || next->it < units)) load_rows(hh + 1 < G ? it + 1 : head_of(next->it, 0));
-    __syncwarp();
-    // ---- round 2: R and N as operands; q.dq's second part, the row sums of R . Q K^T
-    {
-      const float2 gi = gs[i];
-      float sum = 0.f;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float r[16], a[16], dec[16];
-        row_decays<16>(dec, cf, gs, gi, i, q, j0 + 16 * c);
-        tmem_ld16(tl + 128 + 16 * c, r);
-        tmem_ld16(tl + 384 + 16 * c, a);
-        tmem_ld_wait();
-#pragma unroll
-        for (int jj = 0; jj < 16; ++jj) {
-          const int j = j0 + 16 * c + jj;
-          r[jj] = j <= i ? r[jj] * dec[jj] : 0.f;
-          if (j <= i) sum = fmaf(r[jj], a[jj], sum);
-        }
-        tmem_ld16(tl + 256 + 16 * c, a);
-        tmem_ld_wait();
-#pragma unroll
-        for (int c8 = 0; c8 < 2; ++c8) {
-          uint32_t rw[4], nw[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int jj = 8 * c8 + 2 * e, j = j0 + 16 * c + jj;
-            rw[e] = pack_f16x2(kGradDown * r[jj], kGradDown * r[jj + 1]);
-            nw[e] = pack_f16x2(j < i ? kGradDown * dec[jj] * a[jj] : 0.f,
-                               j + 1 < i ? kGradDown * dec[jj + 1] * a[jj + 1] : 0.f);
-          }
-          const uint32_t at = swz16(i, 4 * qt + 2 * c + c8);
-          *reinterpret_cast<uint4*>(s + tD + at) = make_uint4(rw[0], rw[1], rw[2], rw[3]);
-          *reinterpret_cast<uint4*>(s + tO + at) = make_uint4(nw[0], nw[1], nw[2], nw[3]);
-        }
-      }
-      dg[qt * kC + i] = fmaf(p.scale * id * isf * iq * ik, sum, qdot);
-    }
-    fence_proxy_async_shared();
-    tc_fence_before();
-    __syncthreads();
-    if (tid == 0) {
-      tc_fence_after();
-      mma_tile<kAlong, kDown>(tmem + 128, s0 + tD, s0 + tK, false);  // R K
-      mma_tile<kDown, kDown>(tmem + 256, s0 + tD, s0 + tQ, false);   // R^T Q
-      mma_tile<kAlong, kDown>(tmem + 384, s0 + tO, s0 + tK, false);  // N K
-      mma_tile<kDown, kDown>(tmem + 384, s0 + tO, s0 + tK, true);    // N^T K
-      umma_commit(bars + 3);
-    }
-    __syncwarp();
-    // ---- the gates' gradients: sums over the slices, the suffix sum over the chunk
-    if (warp >= 12) {
-      const int t = tid - 384;
-      float ew = 0.f, vw = 0.f;
-#pragma unroll
-      for (int x = 0; x < 16; ++x) {
-        const float2 f = p.part[(it * kParts + x) * kC + t];
-        ew += f.x;
-        vw += f.y;
-      }
-      double y = t < n ? (double)(((dg[t] + dg[kC + t]) + (dg[2 * kC + t] + dg[3 * kC + t])) - vw) : 0.0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double z = __shfl_down_sync(0xffffffffu, y, o);
-        if (lane + o < 32) y += z;
-      }
-      if (lane == 0) tot[q] = y;
-      float bsum = p.bnd[it * kBnd + lane] + p.bnd[it * kBnd + 32 + lane];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) bsum += __shfl_xor_sync(0xffffffffu, bsum, o);
-      named_bar_sync(1, kC);
-      for (int w = q + 1; w < 4; ++w) y += tot[w];
-      if (t < n) {
-        p.dlog_alpha[row0 + t] = (float)(y + (double)bsum);
-        p.dbeta[row0 + t] = ew;
-      }
-    }
-    wait_mma();
-    // ---- round 3
-    {
-      const float f0 = p.scale * id * isf * ik / kGradDown, f1 = p.scale * id * isf * iq / kGradDown;
-      const float f2 = -isf * isr * ik / kGradDown;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float a[16], x[16], y[16];
-        tmem_ld16(tl + 128 + 16 * c, y);
-        tmem_ld16(tl + 256 + 16 * c, a);
-        tmem_ld16(tl + 384 + 16 * c, x);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          xk[16 * c + j] += fmaf(f1, a[j], f2 * x[j]);
-          xq[16 * c + j] = fmaf(f0, y[j], xq[16 * c + j]);
-        }
-      }
-    }
-    if (hh + 1 == G) {  // the gradients leave by way of Q's and K's places, whole rows to a warp
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const uint32_t at = swz16(i, 4 * qt + v);
-        *reinterpret_cast<uint4*>(s + tQ + at) =
-            make_uint4(pack_bf16x2(xq[8 * v], xq[8 * v + 1]), pack_bf16x2(xq[8 * v + 2], xq[8 * v + 3]),
-                       pack_bf16x2(xq[8 * v + 4], xq[8 * v + 5]), pack_bf16x2(xq[8 * v + 6], xq[8 * v + 7]));
-        *reinterpret_cast<uint4*>(s + tK + at) =
-            make_uint4(pack_bf16x2(xk[8 * v], xk[8 * v + 1]), pack_bf16x2(xk[8 * v + 2], xk[8 * v + 3]),
-                       pack_bf16x2(xk[8 * v + 4], xk[8 * v + 5]), pack_bf16x2(xk[8 * v + 6], xk[8 * v + 7]));
-      }
+      tc_fence_before();
       __syncthreads();
-      store_rows(p.dq + krow0 * p.dk, s + tQ, n, p.dk, tid, kGradThreads);
-      store_rows(p.dkey + krow0 * p.dk, s + tK, n, p.dk, tid, kGradThreads);
+      if (tid == 0) {
+        tc_fence_after();
+        mma_tile<kAlong, kSlices>(tmem + 128, s0 + tO, s0 + tU + kLow, false);
+        mma_tile<kAlong, kSlices>(tmem + 128, s0 + tO, s0 + tU, true);
+        mma_tile<kPlain, kSlices>(tmem + 256, s0 + tY, s0 + tU, false);
+        wait_bar(bars + 2, par, p.err);
+        mma_tile<kAlong, kAlong>(tmem + 384, s0 + tQ, s0 + tK, false);
+        umma_commit(bars + 3);
+      }
+      __syncwarp();
+      wait_mma();
+      if (tid == 0 && (hh + 1 < G || next->it < units)) load_rows(hh + 1 < G ? it + 1 : head_of(next->it, 0));
+      __syncwarp();
+      // ---- round 2: R and N as operands; q.dq's second part, the row sums of R . Q K^T
+      {
+        const float2 gi = gs[i];
+        float sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float r[16], a[16], dec[16];
+          row_decays<16>(dec, cf, gs, gi, i, q, j0 + 16 * c);
+          tmem_ld16(tl + 128 + 16 * c, r);
+          tmem_ld16(tl + 384 + 16 * c, a);
+          tmem_ld_wait();
+#pragma unroll
+          for (int jj = 0; jj < 16; ++jj) {
+            const int j = j0 + 16 * c + jj;
+            r[jj] = j <= i ? r[jj] * dec[jj] : 0.f;
+            if (j <= i) sum = fmaf(r[jj], a[jj], sum);
+          }
+          tmem_ld16(tl + 256 + 16 * c, a);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c8 = 0; c8 < 2; ++c8) {
+            uint32_t rw[4], nw[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int jj = 8 * c8 + 2 * e, j = j0 + 16 * c + jj;
+              rw[e] = pack_f16x2(kGradDown * r[jj], kGradDown * r[jj + 1]);
+              nw[e] = pack_f16x2(j < i ? kGradDown * dec[jj] * a[jj] : 0.f,
+                                 j + 1 < i ? kGradDown * dec[jj + 1] * a[jj + 1] : 0.f);
+            }
+            const uint32_t at = swz16(i, 4 * qt + 2 * c + c8);
+            *reinterpret_cast<uint4*>(s + tD + at) = make_uint4(rw[0], rw[1], rw[2], rw[3]);
+            *reinterpret_cast<uint4*>(s + tO + at) = make_uint4(nw[0], nw[1], nw[2], nw[3]);
+          }
+        }
+        dg[qt * kC + i] = fmaf(p.scale * id * isf * iq * ik, sum, qdot);
+      }
+      fence_proxy_async_shared();
+      tc_fence_before();
+      __syncthreads();
+      if (tid == 0) {
+        tc_fence_after();
+        mma_tile<kAlong, kDown>(tmem + 128, s0 + tD, s0 + tK, false);  // R K
+        mma_tile<kDown, kDown>(tmem + 256, s0 + tD, s0 + tQ, false);   // R^T Q
+        mma_tile<kAlong, kDown>(tmem + 384, s0 + tO, s0 + tK, false);  // N K
+        mma_tile<kDown, kDown>(tmem + 384, s0 + tO, s0 + tK, true);    // N^T K
+        umma_commit(bars + 3);
+      }
+      __syncwarp();
+      // ---- the gates' gradients: sums over the slices, the suffix sum over the chunk
+      if (warp >= 12) {
+        const int t = tid - 384;
+        float ew = 0.f, vw = 0.f;
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          const float2 f = p.part[(it * kParts + x) * kC + t];
+          ew += f.x;
+          vw += f.y;
+        }
+        double y = t < n ? (double)(((dg[t] + dg[kC + t]) + (dg[2 * kC + t] + dg[3 * kC + t])) - vw) : 0.0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const double z = __shfl_down_sync(0xffffffffu, y, o);
+          if (lane + o < 32) y += z;
+        }
+        if (lane == 0) tot[q] = y;
+        float bsum = p.bnd[it * kBnd + lane] + p.bnd[it * kBnd + 32 + lane];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) bsum += __shfl_xor_sync(0xffffffffu, bsum, o);
+        named_bar_sync(1, kC);
+        for (int w = q + 1; w < 4; ++w) y += tot[w];
+        if (t < n) {
+          p.dlog_alpha[row0 + t] = (float)(y + (double)bsum);
+          p.dbeta[row0 + t] = ew;
+        }
+      }
+      wait_mma();
+      // ---- round 3
+      {
+        const float f0 = p.scale * id * isf * ik / kGradDown, f1 = p.scale * id * isf * iq / kGradDown;
+        const float f2 = -isf * isr * ik / kGradDown;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float a[16], x[16], y[16];
+          tmem_ld16(tl + 128 + 16 * c, y);
+          tmem_ld16(tl + 256 + 16 * c, a);
+          tmem_ld16(tl + 384 + 16 * c, x);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            xk[16 * c + j] += fmaf(f1, a[j], f2 * x[j]);
+            xq[16 * c + j] = fmaf(f0, y[j], xq[16 * c + j]);
+          }
+        }
+      }
+      if (hh + 1 == G) {  // the gradients leave by way of Q's and K's places, whole rows to a warp
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const uint32_t at = swz16(i, 4 * qt + v);
+          *reinterpret_cast<uint4*>(s + tQ + at) =
+              make_uint4(pack_bf16x2(xq[8 * v], xq[8 * v + 1]), pack_bf16x2(xq[8 * v + 2], xq[8 * v + 3]),
+                         pack_bf16x2(xq[8 * v + 4], xq[8 * v + 5]), pack_bf16x2(xq[8 * v + 6], xq[8 * v + 7]));
+          *reinterpret_cast<uint4*>(s + tK + at) =
+              make_uint4(pack_bf16x2(xk[8 * v], xk[8 * v + 1]), pack_bf16x2(xk[8 * v + 2], xk[8 * v + 3]),
+                         pack_bf16x2(xk[8 * v + 4], xk[8 * v + 5]), pack_bf16x2(xk[8 * v + 6], xk[8 * v + 7]));
+        }
+        __syncthreads();
+        store_rows(p.dq + krow0 * p.dk, s + tQ, n, p.dk, tid, kGradThreads);
+        store_rows(p.dkey + krow0 * p.dk, s + tK, n, p.dk, tid, kGradThreads);
+      }
+      fence_proxy_async_shared();
+      tc_fence_before();
+      __syncthreads();  // the next head's tiles and tables
+      tc_fence_after();
+      if (tid == 0 && (hh + 1 < G || next->it < units)) load_states(hh + 1 < G ? it + 1 : head_of(next->it, 0));
+      __syncwarp();
     }
-    fence_proxy_async_shared();
-    tc_fence_before();
-    __syncthreads();  // the next head's tiles and tables
-    tc_fence_after();
-    if (tid == 0 && (hh + 1 < G || next->it < units)) load_states(hh + 1 < G ? it + 1 : head_of(next->it, 0));
-    __syncwarp();
-  }
     me = *next;
   }
   __syncthreads();

@@ -169,7 +169,7 @@ __device__ __forceinline__ void put_parts(unsigned char* hi, unsigned char* lo, 
 // instead of 7e-7, B 2, T 4096).  Entries up to 1000 fit.
 constexpr float kInvUp = 64.f;
 
-// ---- the triangular solve, float32 on the CUDA cores.  With A = SL(K K^T . G)
+// ---- the triangular solve, float32 values and sums.  With A = SL(K K^T . G)
 // of a 128-token chunk, M solves (I + A diag(beta)) M = -A, so that both inverses
 // are unit triangular and exact for any beta, zero and tiny ones included:
 //   (I + A diag(beta))^-1 = I + M diag(beta),  (I + diag(beta) A)^-1 = I + diag(beta) M.
@@ -179,10 +179,12 @@ constexpr float kInvUp = 64.f;
 //   Z = A21 + [M22 diag(beta)] A21,   M21 = -(Z + [Z diag(beta)] M11).
 // From 16 rows on these are products of 16-row blocks on the warp-level matrix
 // instruction, a 16 x (N / 2) piece to a warp, with both operands in two fp16 parts
-// made in registers.  Measured per chunk on one GB300: 2 x 4 thousand cycles for the
-// last doubling in float32 FMAs with 4 x 4 outputs a thread (16-byte reads of
-// shared memory, four cycles each, bound them), and a tcgen05 round costs one
-// more pass of operands through shared memory and back from tensor memory.
+// made in registers.  A chunk takes 12 thousand cycles, half of its preparation;
+// the warp-level instructions, 26 cycles each on a scheduler, bound the two last
+// doublings.  In float32 FMAs with 4 x 4 outputs a thread the last doubling alone took
+// 8 thousand (16-byte reads of shared memory, four cycles each, bound it), and a
+// tcgen05 round costs one more pass of operands through shared memory and back from
+// tensor memory.
 //
 // Both matrices are [128][128] float32 with the 16-byte pieces of a row permuted
 // by the row, which keeps reads of consecutive rows at one column, and of
