@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     gdr_prep_fwd_kernel(const __grid_constant__ TcMaps maps, TcParams p) {
   using Sm = PrepSm;
   extern __shared__ __align__(1024) unsigned char s[];
+  let_next_launch();
   if (smem_u32(s) & 1023u) {
     if (threadIdx.x == 0) atomicOr(p.err, kErrDeviceArg);
     return;
@@ -363,6 +364,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     gdr_prep_bwd_kernel(const __grid_constant__ TcMaps maps, TcParams p) {
   using Sm = PrepSm;
   extern __shared__ __align__(1024) unsigned char s[];
+  let_next_launch();
   if (smem_u32(s) & 1023u) {
     if (threadIdx.x == 0) atomicOr(p.err, kErrDeviceArg);
     return;
@@ -702,6 +704,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdr_scan_kernel(TcParams p, i
   constexpr bool REV = MODE == kRev, LEAN = MODE != kFwd;
   using Sm = ScanSm<MODE>;
   extern __shared__ __align__(1024) unsigned char s[];
+  wait_for_previous();
+  let_next_launch();
   if (smem_u32(s) & 1023u) {
     if (threadIdx.x == 0) atomicOr(p.err, kErrDeviceArg);
     return;
@@ -1039,6 +1043,7 @@ constexpr uint32_t kOutSmem = kOCol + kColDecays * 4;
 // other's products.  Bound by memory: 160 KB an item, 336 MB for 2048 items in 64 us, 5.2 TB/s.
 __global__ void __launch_bounds__(256, 2) gdr_out_kernel(const __grid_constant__ TcMaps maps, TcParams p) {
   extern __shared__ __align__(1024) unsigned char s[];
+  wait_for_previous();
   if (smem_u32(s) & 1023u) {
     if (threadIdx.x == 0) atomicOr(p.err, kErrDeviceArg);
     return;
@@ -1182,6 +1187,7 @@ constexpr int kGradThreads = 512;
 // then exact to float32; the rest ends in 16-bit gradients.
 __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p) {
   extern __shared__ __align__(1024) unsigned char s[];
+  wait_for_previous();
   if (smem_u32(s) & 1023u) {
     if (threadIdx.x == 0) atomicOr(p.err, kErrDeviceArg);
     return;
@@ -1550,27 +1556,43 @@ TcParams params_of(const GdrArgs& a, const Plan& pl, bool bwd) {
   return p;
 }
 
+// a kernel that begins with wait_for_previous()
+template <typename... P, typename... A>
+ll_status launch_next(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
+                      const A&... args) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = stream;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  LL_CUDA_OK(cudaLaunchKernelEx(&c, kernel, args...));
+  return LL_OK;
+}
 template <int MODE> ll_status scan(const GdrArgs& a, const TcParams& p, int slices) {
   LL_CUDA_OK(cudaFuncSetAttribute(gdr_scan_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   (int)ScanSm<MODE>::kBytes));
-  gdr_scan_kernel<MODE><<<(unsigned)(gdr_sequences(a) * a.H * slices), kScanThreads, ScanSm<MODE>::kBytes, a.stream>>>(p, slices);
-  LL_CUDA_OK(cudaGetLastError());
-  return LL_OK;
+  return launch_next(gdr_scan_kernel<MODE>, (unsigned)(gdr_sequences(a) * a.H * slices), kScanThreads,
+                     ScanSm<MODE>::kBytes, a.stream, p, slices);
 }
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::atomic<bool> ready{false};
-  if (!ready.load(std::memory_order_acquire)) {  // (idempotent: threads may look it up at once)
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
+  auto f = fn.load(std::memory_order_acquire);
+  if (!f) {  // (threads may look it up at once)
     void* ptr = nullptr;
     cudaDriverEntryPointQueryResult qr;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &qr) !=
             cudaSuccess ||
         qr != cudaDriverEntryPointSuccess)
       return nullptr;
-    fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    ready.store(true, std::memory_order_release);
+    f = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    fn.store(f, std::memory_order_release);
   }
-  return fn;
+  return f;
 }
 bool make_map(CUtensorMap* m, const void* base, uint64_t rows, int d) {
   auto fn = encode_fn();
@@ -1651,9 +1673,7 @@ ll_status gdr_tc_fwd_launch(const GdrArgs& a) {
   if (st == LL_OK) st = scan<kFwd>(a, p, a.dv / kSlice);
   if (st != LL_OK) return st;
   LL_CUDA_OK(cudaFuncSetAttribute(gdr_out_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kOutSmem));
-  gdr_out_kernel<<<pl.slots * a.H, 256, kOutSmem, a.stream>>>(m, p);
-  LL_CUDA_OK(cudaGetLastError());
-  return LL_OK;
+  return launch_next(gdr_out_kernel, (unsigned)(pl.slots * a.H), 256, kOutSmem, a.stream, m, p);
 }
 
 ll_status gdr_tc_bwd_launch(const GdrArgs& a) {
@@ -1669,9 +1689,7 @@ ll_status gdr_tc_bwd_launch(const GdrArgs& a) {
   LL_CUDA_OK(cudaFuncSetAttribute(gdr_grad_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGradSmem));
   const int sms = sm_count();
   if (sms == 0) return LL_ERR_CUDA;
-  gdr_grad_tc_kernel<<<std::min(pl.slots * a.Hk, sms), kGradThreads, kGradSmem, a.stream>>>(p);
-  LL_CUDA_OK(cudaGetLastError());
-  return LL_OK;
+  return launch_next(gdr_grad_tc_kernel, (unsigned)std::min(pl.slots * a.Hk, sms), kGradThreads, kGradSmem, a.stream, p);
 }
 
 }  // namespace llattn

@@ -58,6 +58,13 @@ __device__ __forceinline__ void named_bar_arrive(int id, int nthreads) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// The kernels of a call follow one another closely: each lets the next one be set up
+// once all of its CTAs run, and the next waits (first of all, in every CTA, so that
+// "before" holds along the whole chain) until the one before has ended and its writes
+// can be read.
+__device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Bounded wait (every thread): the waits of these kernels are on their own
 // copies and products, which always complete.
 __device__ __noinline__ void wait_bar_long(uint64_t* bar, uint32_t par, unsigned* err) {
