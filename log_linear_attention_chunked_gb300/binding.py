@@ -571,8 +571,9 @@ def ll_gdr_bwd(q, k, v, log_alpha, beta, dout, *, scale=1.0, state_in=None, dsta
             _need_like(x, n, states, torch.float32, q.device)
     if grads is None:
         grads = tuple(torch.empty_like(x) for x in (q, k, v, log_alpha, beta))
-    for x, ref, n in zip(grads, (q, k, v, log_alpha, beta), ("dq", "dk", "dv", "dlog_alpha", "dbeta"), strict=True):
-        _need_like(x, n, ref.shape, ref.dtype, q.device)
+    else:
+        for x, ref, n in zip(grads, (q, k, v, log_alpha, beta), ("dq", "dk", "dv", "dlog_alpha", "dbeta"), strict=True):
+            _need_like(x, n, ref.shape, ref.dtype, q.device)
     ws = _gdr_workspace(workspace, ll_gdr_bwd_workspace_size(shape), q.device)
     _launch("ll_gdr_bwd", q.device, ctypes.byref(shape), _addr(seq_starts), _addr(q), _addr(k), _addr(v),
             _addr(log_alpha), _addr(beta), _addr(state_in), _addr(dout), _addr(dstate_out),
