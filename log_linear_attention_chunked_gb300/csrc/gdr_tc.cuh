@@ -186,12 +186,12 @@ constexpr float kInvUp = 64.f;
 //   Z = A21 + [M22 diag(beta)] A21,   M21 = -(Z + [Z diag(beta)] M11).
 // From 16 rows on these are products of 16-row blocks on the warp-level matrix
 // instruction, a 16 x (N / 2) piece to a warp, with both operands in two fp16 parts
-// made in registers.  A chunk takes 12 thousand cycles, half of its preparation;
-// the warp-level instructions, 26 cycles each on a scheduler, bound the two last
-// doublings.  In float32 FMAs with 4 x 4 outputs a thread the last doubling alone took
-// 8 thousand (16-byte reads of shared memory, four cycles each, bound it), and a
-// tcgen05 round costs one more pass of operands through shared memory and back from
-// tensor memory.
+// made in registers.  A chunk takes 11 to 12 thousand cycles, half of its preparation:
+// 1.4 to the 8 x 8 pairs, then 1.5, 3.3 and 4.9 for the doublings, each a chain of loads,
+// conversions and products (two schedulers' shares of the work made equal changed
+// nothing).  The last one in float32 FMAs with 4 x 4 outputs a thread took 8 thousand
+// (16-byte reads of shared memory, four cycles each, bound it), and on tcgen05 6:
+// 0.85 for each product, the rest for operands through shared memory and back.
 //
 // Both matrices are [128][128] float32 with the 16-byte pieces of a row permuted
 // by the row, which keeps reads of consecutive rows at one column, and of
