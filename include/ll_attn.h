@@ -452,7 +452,7 @@ LL_API ll_status ll_gdr_fwd(const ll_gdr_shape* shape, const int32_t* seq_starts
 /* Bytes of workspace ll_gdr_bwd needs (0 on an invalid shape). */
 LL_API size_t ll_gdr_bwd_workspace_size(const ll_gdr_shape* shape);
 
-/* Kernel launches of one ll_gdr_bwd call: 3 token by token, 4 in chunks (and a
+/* Kernel launches of one ll_gdr_bwd call: 2 token by token, 4 in chunks (and a
  * memset, as above); 0 on an invalid shape. */
 LL_API int ll_gdr_bwd_launches(const ll_gdr_shape* shape);
 

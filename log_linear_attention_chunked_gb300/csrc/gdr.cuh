@@ -111,8 +111,9 @@ int gdr_bwd_launches(const GdrArgs& a);
 
 // token by token, states in registers (gdr_rec.cu)
 constexpr int kGdrGradChunk = 64;  // tokens between the states kept for the gradient
-ll_status gdr_rec_fwd_launch(const GdrArgs& a, float* kept_states, float* kept_errors);
-ll_status gdr_rec_bwd_launch(const GdrArgs& a, float* kept_adjoints, float* kept_w);
+ll_status gdr_rec_fwd_launch(const GdrArgs& a);
+ll_status gdr_rec_both_launch(const GdrArgs& a, float* kept_states, float* kept_errors, float* kept_adjoints,
+                              float* kept_w);
 ll_status gdr_grad_launch(const GdrArgs& a, const float* states, const float* errors, const float* adjoints,
                           const float* w);
 

@@ -344,11 +344,11 @@ ll_status gdr_grad_launch(const GdrArgs& a, const float* states, const float* er
 size_t gdr_fwd_workspace(const GdrArgs& a) { return gdr_tc_fwd_use(a) ? gdr_tc_fwd_workspace(a) : 0; }
 int gdr_fwd_launches(const GdrArgs& a) { return gdr_tc_fwd_use(a) ? 3 : 1; }
 ll_status gdr_fwd_launch(const GdrArgs& a) {
-  return gdr_tc_fwd_use(a) ? gdr_tc_fwd_launch(a) : gdr_rec_fwd_launch(a, nullptr, nullptr);
+  return gdr_tc_fwd_use(a) ? gdr_tc_fwd_launch(a) : gdr_rec_fwd_launch(a);
 }
 
 size_t gdr_bwd_workspace(const GdrArgs& a) { return gdr_tc_bwd_use(a) ? gdr_tc_bwd_workspace(a) : rec_plan(a).total; }
-int gdr_bwd_launches(const GdrArgs& a) { return gdr_tc_bwd_use(a) ? 4 : 3; }
+int gdr_bwd_launches(const GdrArgs& a) { return gdr_tc_bwd_use(a) ? 4 : 2; }
 ll_status gdr_bwd_launch(const GdrArgs& a) {
   if (gdr_tc_bwd_use(a)) return gdr_tc_bwd_launch(a);
   const RecPlan p = rec_plan(a);
@@ -357,8 +357,7 @@ ll_status gdr_bwd_launch(const GdrArgs& a) {
   float* adjoints = reinterpret_cast<float*>(ws + p.adjoints);
   float* errors = reinterpret_cast<float*>(ws + p.errors);
   float* w = reinterpret_cast<float*>(ws + p.w);
-  ll_status st = gdr_rec_fwd_launch(a, states, errors);
-  if (st == LL_OK) st = gdr_rec_bwd_launch(a, adjoints, w);
+  ll_status st = gdr_rec_both_launch(a, states, errors, adjoints, w);
   if (st == LL_OK) st = gdr_grad_launch(a, states, errors, adjoints, w);
   return st;
 }

@@ -174,8 +174,9 @@ template <typename IO, int DK> struct RecSm {
 };
 constexpr int kHelpBar = 1;
 
+// The recurrence.
 template <typename IO, int DK>
-__global__ void __launch_bounds__(2 * RowCfg<DK>::kThreads) gdr_rec_fwd_kernel(RecParams p) {
+__device__ __forceinline__ void rec_forward(const RecParams& p) {
   using Cfg = RowCfg<DK>;
   constexpr int LPR = Cfg::kLpr, NP = Cfg::kEpl / 2, NT = Cfg::kThreads;
   extern __shared__ __align__(16) unsigned char raw[];
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(2 * RowCfg<DK>::kThreads) gdr_rec_fwd_kernel(R
 // kGdrGradChunk tokens, and the gradient of the state on entry.  Step x takes
 // tile tiles - 1 - x.
 template <typename IO, int DK>
-__global__ void __launch_bounds__(2 * RowCfg<DK>::kThreads) gdr_rec_bwd_kernel(RecParams p) {
+__device__ __forceinline__ void rec_reverse(const RecParams& p) {
   using Cfg = RowCfg<DK>;
   constexpr int LPR = Cfg::kLpr, NP = Cfg::kEpl / 2, NT = Cfg::kThreads;
   extern __shared__ __align__(16) unsigned char raw[];
@@ -494,6 +495,18 @@ __global__ void __launch_bounds__(2 * RowCfg<DK>::kThreads) gdr_rec_bwd_kernel(R
   if (p.dstate_in) store_row<DK>(p.dstate_in + st_at, l, reinterpret_cast<const float*>(a));
 }
 
+template <typename IO, int DK>
+__global__ void __launch_bounds__(2 * RowCfg<DK>::kThreads) gdr_rec_fwd_kernel(RecParams p) {
+  rec_forward<IO, DK>(p);
+}
+// For the gradient both at once: neither needs the other, and a sequence's chain
+// bounds each (y = 0: the recurrence, y = 1: the reverse one).
+template <typename IO, int DK>
+__global__ void __launch_bounds__(2 * RowCfg<DK>::kThreads) gdr_rec_both_kernel(RecParams p) {
+  if (blockIdx.y == 0) rec_forward<IO, DK>(p);
+  else rec_reverse<IO, DK>(p);
+}
+
 // ---------------------------------------------------------------- one decode step
 // Rows in flight per group of lanes.  Measured with 1, 2 and 4 (128 x 128): 32 states 3.2, 3.1 and 3.8
 // us, 256 states 6.8, 6.2 and 6.3, 2048 states 44.8, 44.7 and 44.9.
@@ -580,22 +593,12 @@ ll_status by_type(ll_dtype io, int dk, A... args) {
   return LL_ERR_UNSUPPORTED;
 }
 
-template <typename IO, int DK> struct RecFwd {
-  static ll_status run(const RecParams& p, unsigned grid, cudaStream_t st) {
+template <typename IO, int DK> struct Rec {
+  static ll_status run(const RecParams& p, unsigned grid, bool both, cudaStream_t st) {
     constexpr int smem = (int)sizeof(RecSm<IO, DK>);
-    if (smem > 48 * 1024)
-      LL_CUDA_OK(cudaFuncSetAttribute(gdr_rec_fwd_kernel<IO, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    gdr_rec_fwd_kernel<IO, DK><<<grid, 2 * RowCfg<DK>::kThreads, smem, st>>>(p);
-    LL_CUDA_OK(cudaGetLastError());
-    return LL_OK;
-  }
-};
-template <typename IO, int DK> struct RecBwd {
-  static ll_status run(const RecParams& p, unsigned grid, cudaStream_t st) {
-    constexpr int smem = (int)sizeof(RecSm<IO, DK>);
-    if (smem > 48 * 1024)
-      LL_CUDA_OK(cudaFuncSetAttribute(gdr_rec_bwd_kernel<IO, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    gdr_rec_bwd_kernel<IO, DK><<<grid, 2 * RowCfg<DK>::kThreads, smem, st>>>(p);
+    auto kernel = both ? gdr_rec_both_kernel<IO, DK> : gdr_rec_fwd_kernel<IO, DK>;
+    if (smem > 48 * 1024) LL_CUDA_OK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    kernel<<<dim3(grid, both ? 2 : 1), 2 * RowCfg<DK>::kThreads, smem, st>>>(p);
     LL_CUDA_OK(cudaGetLastError());
     return LL_OK;
   }
@@ -619,23 +622,24 @@ unsigned rec_grid(const GdrArgs& a) { return (unsigned)((size_t)gdr_sequences(a)
 
 }  // namespace
 
-ll_status gdr_rec_fwd_launch(const GdrArgs& a, float* kept_states, float* kept_errors) {
+ll_status gdr_rec_fwd_launch(const GdrArgs& a) {
   RecParams p = rec_params(a);
   p.o = a.o;
   p.state_out = a.state_out;
-  p.kept_states = kept_states;
-  p.kept_errors = kept_errors;
-  return by_type<RecFwd, const RecParams&, unsigned, cudaStream_t>(a.io, a.dk, p, rec_grid(a), a.stream);
+  return by_type<Rec, const RecParams&, unsigned, bool, cudaStream_t>(a.io, a.dk, p, rec_grid(a), false, a.stream);
 }
 
-ll_status gdr_rec_bwd_launch(const GdrArgs& a, float* kept_adjoints, float* kept_w) {
+ll_status gdr_rec_both_launch(const GdrArgs& a, float* kept_states, float* kept_errors, float* kept_adjoints,
+                              float* kept_w) {
   RecParams p = rec_params(a);
+  p.kept_states = kept_states;
+  p.kept_errors = kept_errors;
   p.dout = a.dout;
   p.dstate_out = a.dstate_out;
   p.dstate_in = a.dstate_in;
   p.kept_adjoints = kept_adjoints;
   p.kept_w = kept_w;
-  return by_type<RecBwd, const RecParams&, unsigned, cudaStream_t>(a.io, a.dk, p, rec_grid(a), a.stream);
+  return by_type<Rec, const RecParams&, unsigned, bool, cudaStream_t>(a.io, a.dk, p, rec_grid(a), true, a.stream);
 }
 
 namespace {

@@ -1650,16 +1650,17 @@ bool gdr_tc_fwd_use(const GdrArgs& a) {
   const double in_chunks = std::max(34., 18 + (wide == 4 ? 0.18 : 0.15) * items + (wide == 4 ? 0.06 : 0.05) * states);
   return in_chunks < by_token;
 }
-// The gradient: token by token it takes a launch over all states, one over all their
-// gradients and one over chunks of 64.  At 128 x 128 the tensor cores are the faster
-// at every length measured (16 heads: 81 / 61 us at 1 token, 132 / 67 at 192; 256 heads: 212 / 182
-// at 16, 5435 / 973 at 1024); the bound of 16 is for the workspace, whose items
-// are padded to 128 tokens.  With a side of 64 they are from 64 tokens on (256 heads,
-// 64 x 128: 164 / 183 at 32, 214 / 186 at 64), with two from 96 (126 / 180 at 64, 213 / 182 at
-// 96; 20 packed sequences of 102 on 4 heads 109 / 84, 32 of 64 69 / 141).
+// The gradient: token by token it takes a launch over both recurrences and one over
+// chunks of 64.  At 128 x 128 the tensor cores are the faster at every length but a
+// token of many heads (16 heads: 78 / 58 us at 1 token, 82 / 58 at 16; 256 heads: 174 / 179 at 1,
+// 207 / 179 at 16); the bound of 16 is for the workspace too, whose items
+// are padded to 128 tokens.  With one side of 64 they are from 64 tokens on (64 x 128, 256 heads:
+// 168 / 181 at 32, 219 / 182 at 64; 128 x 64, 16 heads: 52 / 59 at 32, 59 / 59 at 64), with two from
+// 128 (16 heads: 52 / 60 at 128, 66 / 64 at 256; 64 heads: 68 / 70 at 128, 111 / 90 at 192; 256 heads:
+// 244 / 180 at 128).
 bool gdr_tc_bwd_use(const GdrArgs& a) {
   const int mean = a.n_seqs ? (a.T + a.n_seqs - 1) / a.n_seqs : a.T;
-  return tc_formats(a) && mean >= (a.dk * a.dv > 64 * 128 ? 16 : a.dk * a.dv > 64 * 64 ? 64 : 96);
+  return tc_formats(a) && mean >= (a.dk * a.dv > 64 * 128 ? 16 : a.dk * a.dv > 64 * 64 ? 64 : 128);
 }
 size_t gdr_tc_fwd_workspace(const GdrArgs& a) { return plan_of(a, false).total; }
 size_t gdr_tc_bwd_workspace(const GdrArgs& a) { return plan_of(a, true).total; }

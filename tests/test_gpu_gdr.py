@@ -511,7 +511,7 @@ def test_both_sides_of_the_choice(B, dk, dv, lo, hi):
         x = draw(1, 2, 1, T, dk, dv, seed=T)
         assert launches(B, x)[0] == n
         check_fwd(B, x)
-    for T, n in (((15, 3), (16, 4)) if dk * dv > 64 * 128 else ((63, 3), (96, 4))):
+    for T, n in (((15, 2), (16, 4)) if dk * dv > 64 * 128 else ((63, 2), (128, 4))):
         x = draw(1, 2, 1, T, dk, dv, seed=T)
         assert launches(B, x)[1] == n
         check_bwd(B, x)
