@@ -40,10 +40,10 @@ static_assert(kTile % 3 == 1, "the loops over a whole tile take three tokens at 
 
 // Lanes per row: fewer make a longer dot product of a lane, more a longer sum
 // over the lanes (and threads that share an SM's issue slots).  Measured, forward / gradient in
-// us, float32, 512 tokens, 8 and 256 heads: d = 128 with 4 lanes 96 / 250 and 1006 / 3248, with 8
-// 69 / 206 and 745 / 2823, with 16 93 / 242 and 1269 / 3522; d = 64 with 2, 4, 8: 81 / 188, 50 / 135, 53 / 134
-// and 294 / 1208, 200 / 1035, 247 / 1114; d = 32 with 2, 4, 8: 44 / 104, 42 / 97, 42 / 100 and 84 / 363, 73 / 341,
-// 96 / 383; d = 16 with 2, 4: 30 / 72, 31 / 73 and 31 / 175, 41 / 189.
+// us, float32, 512 tokens, 8 and 256 heads: d = 128 with 4 lanes 96 / 171 and 1005 / 3163, with 8
+// 69 / 146 and 745 / 2790, with 16 93 / 168 and 1267 / 3605; d = 64 with 2, 4, 8: 81 / 116, 50 / 86, 53 / 92
+// and 295 / 1122, 200 / 1040, 247 / 1093; d = 32 with 2, 4, 8: 44 / 65, 42 / 57, 42 / 61 and 84 / 350, 73 / 332,
+// 96 / 369; d = 16 with 2, 4: 30 / 44, 31 / 49 and 31 / 160, 41 / 164.
 template <int DK> struct RowCfg {
   static constexpr int kLpr = DK >= 128 ? 8 : DK >= 32 ? 4 : 2;  // lanes per row
   static constexpr int kEpl = DK / kLpr;          // elements per lane
