@@ -400,7 +400,8 @@ LL_API ll_status ll_gdn_fwd_b(const ll_shape* shape, const void* q, const void* 
  * is expected (L2-normalised keys keep it), so that a token's transition does
  * not grow its state; not checked.  In chunks a state has room for 4096 times
  * the largest |v| and |state_in| of its sequence and head, its gradient likewise
- * for 4096 times the largest value that a chunk or dstate_out adds to it.
+ * for 4096 times the largest value that a chunk or dstate_out adds to it; what is
+ * below 2^-28 of these counts as zero in o, dq, dk and dv.
  * Infinities and NaN stay within their sequence and, in v, gates, states and
  * upstream gradients, within their head (and its key head's dq and dk).
  *
