@@ -32,7 +32,7 @@ constexpr uint32_t kHalf = kC * 128;     // [128 rows x 64] block: 16 KB
 constexpr uint32_t kTile = 2 * kHalf;    // 32 KB
 constexpr int kSlice = 32;               // d_v columns of a scan CTA
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr uint64_t kTimeoutNs = 4000000000ull, kShortNs = 1000000ull;
+constexpr uint64_t kTimeoutNs = 4000000000ull;
 constexpr float kLoScale = 2048.f, kLoInv = 1.f / 2048.f;  // of the low fp16 part
 
 __device__ __forceinline__ float ex2(float x) {
@@ -66,13 +66,11 @@ __device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Bounded wait (every thread): the waits of these kernels are on their own
-// copies and products, which always complete.  Once one has run out, the ones
-// behind it get a short limit, so that the kernel ends all the same.
+// copies and products, which always complete.
 __device__ __noinline__ void wait_bar_long(uint64_t* bar, uint32_t par, unsigned* err) {
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, par)) {
-    const uint64_t dt = globaltimer_ns() - t0;
-    if (dt > kShortNs && (dt > kTimeoutNs || (*static_cast<volatile unsigned*>(err) & kErrTimeout))) {
+    if (globaltimer_ns() - t0 > kTimeoutNs) {
       atomicOr(err, kErrTimeout);
       return;
     }
