@@ -1177,8 +1177,8 @@ constexpr int kGradThreads = 512;
 // Persistent, one CTA per SM, an item per (chunk, key head); the value heads that
 // share it are taken in turn, dq and dk adding up in registers in a fixed order.
 // Thread = (row, quarter of the columns).  The next head's or item's tiles are
-// loaded as soon as a tile's last product is done.  Measured: 114 us for 1024 items (390 MB,
-// 3.4 TB/s; 140 with a CTA per item, whose loads nothing overlapped), bound by the
+// loaded as soon as a tile's last product is done.  Measured: 111 us for 1024 items (390 MB,
+// 3.5 TB/s; 140 with a CTA per item, whose loads nothing overlapped), bound by the
 // chain of its three rounds.  Per head three rounds of products over seven tiles of
 // shared memory:
 //   dO S, (beta w) S, u D;   dO u^T, (beta w) u^T, Q K^T;   R K, R^T Q, (N + N^T) K
@@ -1233,12 +1233,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
     bulk_load(s + tY, p.Y + it * kTile, kTile, bars);
     bulk_load(s + tU, p.E + it * 2 * kTile, 2 * kTile, bars);
   };
-  auto load_states = [&](size_t it) {
+  auto load_do = [&](size_t it) {  // and D, as soon as N and R have been read
     mbar_arrive_expect_tx(bars + 1, 4 * kTile);
     bulk_load(s + tO, p.dO16 + it * kTile, kTile, bars + 1);
-    bulk_load(s + tS, p.S + it * 2 * kTile, 2 * kTile, bars + 1);
     bulk_load(s + tD, p.D + it * kTile, kTile, bars + 1);
   };
+  auto load_s = [&](size_t it) { bulk_load(s + tS, p.S + it * 2 * kTile, 2 * kTile, bars + 1); };
   auto head_of = [&](int unit, int hh) {  // (slot, head) of a unit's head
     const int slot = unit / p.seqs.Hk;
     return (size_t)slot * p.seqs.H + (unit - slot * p.seqs.Hk) * G + hh;
@@ -1247,7 +1247,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
   Item me = *next;
   if (tid == 0 && me.it < units) {
     load_rows(head_of(me.it, 0));
-    load_states(head_of(me.it, 0));
+    load_do(head_of(me.it, 0));
+    load_s(head_of(me.it, 0));
   }
   __syncwarp();
   uint32_t par = 0;
@@ -1412,6 +1413,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
         }
       }
       wait_mma();
+      if (tid == 0 && (hh + 1 < G || next->it < units)) load_do(hh + 1 < G ? it + 1 : head_of(next->it, 0));
+      __syncwarp();
       // ---- round 3
       {
         const float f0 = p.scale * id * isf * ik / kGradDown, f1 = p.scale * id * isf * iq / kGradDown;
@@ -1449,7 +1452,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
       tc_fence_before();
       __syncthreads();  // the next head's tiles and tables
       tc_fence_after();
-      if (tid == 0 && (hh + 1 < G || next->it < units)) load_states(hh + 1 < G ? it + 1 : head_of(next->it, 0));
+      if (tid == 0 && (hh + 1 < G || next->it < units)) load_s(hh + 1 < G ? it + 1 : head_of(next->it, 0));
       __syncwarp();
     }
     me = *next;
