@@ -281,11 +281,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
         inv[0] = iv;
       }
       if (p.state_in && me.chunk == 0) {
-        const float* st = p.state_in + sh * p.dv * p.dk;
-        uint32_t m = 0;
-#pragma unroll 4
-        for (int e = t; e < p.dv * p.dk; e += 256) m = max(m, __float_as_uint(fabsf(st[e])));
-        m = __reduce_max_sync(0xffffffffu, m);
+        const uint32_t m = __reduce_max_sync(0xffffffffu, state_max(p.state_in + sh * p.dv * p.dk, p.dv * p.dk, t, 256));
         if (lane == 0) atomicMax(p.amax_s + sh, m);
       }
       if (nx.it < items) {
@@ -428,12 +424,6 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     m = __reduce_max_sync(0xffffffffu, m);
     if (lane == 0) atomicMax(at, m);
   };
-  auto state_max = [&](const float* x) {
-    uint32_t m = 0;
-#pragma unroll 4
-    for (int e = tid; e < p.dv * p.dk; e += kPrepThreads) m = max(m, __float_as_uint(fabsf(x[e])));
-    return m;
-  };
 
   const int items = p.slots * p.seqs.H, G = p.seqs.H / p.seqs.Hk;
   float la = 0.f, bt = 0.f;  // this thread's token's, of the item that is loaded
@@ -478,7 +468,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
       tb.out[i] = out;
       tb.rel[i] = exp_diff(gi, gs[0]);
     }
-    if (p.state_in && me.chunk == 0) raise_max(am_s, state_max(p.state_in + sh * p.dv * p.dk));
+    if (p.state_in && me.chunk == 0) raise_max(am_s, state_max(p.state_in + sh * p.dv * p.dk, p.dv * p.dk, tid, kPrepThreads));
     wait_bar(bar + 1, nkq & 1, p.err);
     const float ik = tile_to_f16<kPrepThreads>(X0, n, red, tid, 0, nullptr);
     // A is K K^T of the scaled tile, beta takes the scale
@@ -645,7 +635,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
         load_values(&maps.v, me.row0, 0);
       }
       uint32_t mx = write_rows(p.Bc + (size_t)it * kC * kC, tl + 256, i, qt, p.scale * iq * id * in0);
-      if (last) mx = max(mx, state_max(p.dstate_out + sh * p.dv * p.dk));
+      if (last) mx = max(mx, state_max(p.dstate_out + sh * p.dv * p.dk, p.dv * p.dk, tid, kPrepThreads));
       wait_mma();
       mx = max(mx, write_rows(p.w0 + (size_t)it * kC * kC, tl, i, qt,
                               p.scale * iq * ik * id / (kScoreDown * kRowsDown * kInvUp)));

@@ -461,6 +461,19 @@ __device__ __noinline__ float tile_to_f16(unsigned char* tile, int n, uint32_t* 
   return sc.y;
 }
 
+// the bits of the largest of a state's n values that this thread of `threads` sees
+// (16 bytes a load: with four the 64 KB took longer than a chunk's solve)
+__device__ __noinline__ uint32_t state_max(const float* x, int n, int t, int threads) {
+  uint32_t m = 0;
+#pragma unroll 4
+  for (int e = t; e < n / 4; e += threads) {
+    const float4 v = reinterpret_cast<const float4*>(x)[e];
+    m = max(max(m, max(__float_as_uint(fabsf(v.x)), __float_as_uint(fabsf(v.y)))),
+            max(__float_as_uint(fabsf(v.z)), __float_as_uint(fabsf(v.w))));
+  }
+  return m;
+}
+
 // rows 0 .. n - 1 of a tile of 16-bit values into a [.., d] matrix, whole rows to half a warp
 __device__ __noinline__ void store_rows(void* dst, const unsigned char* tile, int n, int d, int tid, int threads) {
   const int c8 = tid & 15;
