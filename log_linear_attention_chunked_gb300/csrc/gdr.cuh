@@ -61,6 +61,26 @@ __device__ __forceinline__ bool gdr_seq(const GdrSeqs& s, int i, GdrSeq& r) {
   r = GdrSeq{0, ok ? a : 0, ok ? b - a : 0};
   return ok;
 }
+// The sequence that a kernel with CTAs per sequence takes as its r-th (whole warps).  Up
+// to 32 packed ones go from the longest down, so that a long one does not begin when the
+// others are done (7 sequences, 448 CTAs: scans of 55 and 73 us became 53 and 71; a
+// forward of 13, 832 CTAs, 234 us became 231).  Over many waves of CTAs they even out by
+// themselves, and 0.8 us a CTA for the lengths cost more (17 sequences, 4352 CTAs: 205
+// us became 227).
+constexpr unsigned kGdrPickMost = 1216;  // eight CTAs to an SM
+__device__ __forceinline__ int gdr_pick(const GdrSeqs& s, int r) {
+  if (!s.starts || s.n > 32 || gridDim.x > kGdrPickMost) return r;
+  const int lane = threadIdx.x & 31;
+  GdrSeq q{0, 0, -1};
+  if (lane < s.n) gdr_seq(s, lane, q);
+  int rank = 0;
+#pragma unroll 8
+  for (int j = 0; j < 32; ++j) {
+    const int l = __shfl_sync(0xffffffffu, q.len, j);
+    rank += l > q.len || (l == q.len && j < lane);
+  }
+  return __ffs(__ballot_sync(0xffffffffu, rank == r)) - 1;
+}
 __device__ __forceinline__ int gdr_slot_base(const GdrSeqs& s, int i, int start, int C) {
   return s.starts ? start / C + i : i * ((s.T + C - 1) / C);
 }

@@ -185,7 +185,7 @@ __device__ __forceinline__ void rec_forward(const RecParams& p) {
   const int slices = p.dv / kRows;
   const int sl = blockIdx.x % slices;
   const int h = (blockIdx.x / slices) % p.seqs.H;
-  const int seq = blockIdx.x / slices / p.seqs.H;
+  const int seq = gdr_pick(p.seqs, blockIdx.x / slices / p.seqs.H);
   const bool helper = threadIdx.x >= NT;
   const int tid = threadIdx.x % NT, grp = tid / LPR, l = tid % LPR;
   const int r0 = sl * kRows;
@@ -352,7 +352,7 @@ __device__ __forceinline__ void rec_reverse(const RecParams& p) {
   const int slices = p.dv / kRows;
   const int sl = blockIdx.x % slices;
   const int h = (blockIdx.x / slices) % p.seqs.H;
-  const int seq = blockIdx.x / slices / p.seqs.H;
+  const int seq = gdr_pick(p.seqs, blockIdx.x / slices / p.seqs.H);
   const bool helper = threadIdx.x >= NT;
   const int tid = threadIdx.x % NT, grp = tid / LPR, l = tid % LPR;
   const int r0 = sl * kRows;

@@ -702,7 +702,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdr_scan_kernel(TcParams p, i
   }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int q = warp & 3, qt = (warp >> 2) & 3, i = 32 * q + lane;
-  const int sl = blockIdx.x % slices, h = (blockIdx.x / slices) % p.seqs.H, seq = blockIdx.x / slices / p.seqs.H;
+  const int sl = blockIdx.x % slices, h = (blockIdx.x / slices) % p.seqs.H, seq = gdr_pick(p.seqs, blockIdx.x / slices / p.seqs.H);
   GdrSeq sq;
   if (!gdr_seq(p.seqs, seq, sq)) {
     if (tid == 0) raise_error(p.err, kErrDeviceArg);
