@@ -233,7 +233,7 @@ __device__ __forceinline__ void rec_forward(const RecParams& p) {
       const float kq = group_sum<LPR>(dot2<NP>(x, y));
       load_pairs<DK>(t.k + max(grp - 1, 0) * DK, l, y);
       const float kk = group_sum<LPR>(dot2<NP>(x, y));
-      if (l == 0) sm.side[j & 1].tok[grp] = make_float4(expf(la), bt, kq, kk);
+      if (l == 0) sm.side[j & 1].tok[grp] = make_float4(gdr_alpha(la), bt, kq, kk);
     };
     gates(0);
     fetch(0);
@@ -399,7 +399,7 @@ __device__ __forceinline__ void rec_reverse(const RecParams& p) {
       const float qk = group_sum<LPR>(dot2<NP>(a, b)), qk1 = group_sum<LPR>(dot2<NP>(b, z));
       const float kk = group_sum<LPR>(dot2<NP>(a, z));
       if (l == 0) {
-        sm.side[x & 1].tok[grp] = make_float4(expf(la), bt, qk, qk1);
+        sm.side[x & 1].tok[grp] = make_float4(gdr_alpha(la), bt, qk, qk1);
         sm.side[x & 1].more[grp] = kk;
       }
     };
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_decode_kernel(
   if (slots && sl == 0 && h == 0)
     for (int x = tid; x < b; x += Cfg::kThreads)
       if (slots[x] == slot) raise_error(err, kErrDeviceArg);
-  const float a = expf(la);
+  const float a = gdr_alpha(la);
   const float c = group_sum<LPR>(dot<EPL>(kv, qv));
 #pragma unroll
   for (int x = 0; x < kStepPasses; ++x) {
