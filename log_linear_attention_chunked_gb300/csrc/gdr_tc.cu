@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     if (t < kC) {
       const float2 g = gs[t];
       tb.g[t] = g;
-      tb.into[t] = exp_diff(g, make_float2(0.f, 0.f));
+      tb.into[t] = gdr_alpha(g.x + g.y);  // (the last one scales the state, chunk after chunk)
       tb.out[t] = exp_diff(gs[kC - 1], g);
     }
     tc_fence_before();
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
       in_s[i] = in;
       out_s[i] = out;
       tb.g[i] = gi;
-      tb.into[i] = in;
+      tb.into[i] = gdr_alpha(gi.x + gi.y);  // (the last one scales the state, chunk after chunk)
       tb.out[i] = out;
       tb.rel[i] = exp_diff(gi, gs[0]);
     }
