@@ -238,6 +238,16 @@ def test_gates_at_their_limits(B, dk, io, T, what):
     check_bwd(B, x)
 
 
+def test_decay_near_one_in_chunks(B):
+    """alpha = 0.9999 and faint writes: a state is scaled by thousands of decays, whose
+    errors must not lean to one side."""
+    x = draw(1, 2, 1, 3000, 128, 128, seed=32)
+    x["log_alpha"][:] = -1e-4
+    x["beta"] *= 0.02
+    check_fwd(B, x)
+    check_bwd(B, x)
+
+
 def test_padding_after_a_prompt_changes_nothing(B):
     """beta = 0 and log_alpha = 0 behind the real tokens: the state stays."""
     x = draw(2, 2, 2, 300, 128, 128, "bf16", seed=12)
