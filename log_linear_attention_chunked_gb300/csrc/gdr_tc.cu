@@ -35,10 +35,14 @@ constexpr int kParts = 18, kBnd = 64;
 // per (chunk, head)
 struct Tables {
   float2 g[kC];    // running log decay
-  float into[kC];  // exp(g_t)
-  float out[kC];   // exp(g_C - g_t)
+  float into[kC];  // exp(g_t) (of the gradient)
   float rel[kC];   // exp(g_t - g_0): what D takes from a chunk all carries exp(g_0), which may be tiny
-  float ik, iq, id, pad;  // inverse scales of the fp16 tiles of K, Q and dO
+  float p[kC];     // inverse scales of the rows of the fp16 tile of K
+  float out[kC];   // exp(g_C - g_t)
+  float row[kC];   // beta p: what makes u' and p beta w of e and w
+  float4 all;      // exp(g_C), exp(g_0), eps, 1 / eps
+  float iq, id;    // inverse scales of the fp16 tiles of Q and dO
+  float2 pad;
 };
 
 struct TcParams {
@@ -52,9 +56,9 @@ struct TcParams {
   // workspace, per (slot, head) unless said otherwise; tiles are fp16
   unsigned char* W;      // two tiles, [token][d_k]
   float* U;              // [slice of 32][piece of 4][token][4]; the scan for the gradient leaves e there
-  unsigned char* K16;    // per (slot, key head)
+  unsigned char* K16;    // per (slot, key head), a scale to each row
   unsigned char* S;      // X before the chunk, scaled: a tile [d_k][d_v]; for the gradient slice tiles
-  unsigned char* E;      // u, scaled: a tile [token][d_v]; likewise
+  unsigned char* E;      // p eps u, scaled: a tile [token][d_v]; likewise
   Tables* tab;
   unsigned *amax_s, *amax_d;  // [sequence, head]: bits of the largest value that scales X and e, D and w
   // the gradient's
@@ -62,7 +66,7 @@ struct TcParams {
   unsigned char* Wd;
   float *w0, *Bc;        // as U, Bc's rows being d_k
   unsigned char* D;      // D behind the chunk, scaled: a tile [d_k][d_v]
-  unsigned char* Y;      // beta w, scaled: a tile [token][d_v]
+  unsigned char* Y;      // p eps beta w, scaled: a tile [token][d_v]
   float* final_state;    // [sequence, head, dv, dk]
   float2* part;          // [16][token]: e.w and v.(beta w) over 8 columns; then [4][token] floats, parts of q.dq
   float* bnd;            // [kBnd]: pieces of <S, D> behind the chunk
@@ -70,6 +74,11 @@ struct TcParams {
 };
 
 // ---------------------------------------------------------------- preparation
+__device__ __forceinline__ float4 chunk_factors(const float2* gs, float eps) {
+  const float2 g0 = gs[0], g = gs[kC - 1];
+  // (exp(g_C) scales the state, chunk after chunk)
+  return make_float4(gdr_alpha(g.x + g.y), gdr_alpha(g0.x + g0.y), eps, pow2_inverse(eps));
+}
 // one (chunk, head): its number (no more when it is the item count), sequence, place and length
 struct Item {
   int it, seq, chunk, t0, n, len;
@@ -124,7 +133,7 @@ struct PrepSm {
   static constexpr uint32_t kTab = kR + 2 * kTile;
   static constexpr uint32_t kCol = kTab + 4 * kC * 4 + 32 + 64 + 16;  // forward: the columns' decay factors
   static constexpr uint32_t kBars = kCol + kColDecays * 4;
-  static_assert(kBars >= kTab + 5 * kC * 4 + 32 + 3 * 64 + 16, "the backward's tables");
+  static_assert(kBars >= kTab + 5 * kC * 4 + 32 + 4 * 64 + 16, "the backward's tables");
   static constexpr uint32_t kNext = kBars + 7 * 8;
   static constexpr uint32_t kBytes = kNext + 2 * sizeof(Item);
   static_assert(kCol % 16 == 0, "read as float4");
@@ -135,8 +144,8 @@ struct TcMaps {  // [rows, d] bf16, boxes of 64 columns and 128 rows
   CUtensorMap q, k, v, dout;
 };
 
-constexpr float kScoreDown = 1.f / 256.f;  // of the scores Q K^T of scaled tiles, as operands
-constexpr float kKeysDown = 1.f / 64.f;    // of K K^T of the scaled tile (at most 128 x 16^2)
+constexpr float kScoreDown = 1.f / 1024.f;  // of the scores Q K^T of scaled tiles, as operands
+constexpr float kKeysDown = 1.f / 1024.f;  // of K K^T of the scaled rows (at most 128 x 64^2)
 constexpr float kRowsDown = 1.f / 16.f;    // of P^T dO, as an operand
 
 // Both are persistent, one CTA per SM, an item per (chunk, head).  Thread = (row,
@@ -166,7 +175,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
   float* in_s = bs + kC;
   float2* tot = reinterpret_cast<float2*>(in_s + kC);
   uint32_t* red = reinterpret_cast<uint32_t*>(tot + 4);  // 2 x 8
-  float* inv = reinterpret_cast<float*>(red + 16);       // inverse scales: V, K of both buffers
+  float* inv = reinterpret_cast<float*>(red + 16);       // inverse scale of V
   float* cf = reinterpret_cast<float*>(s + Sm::kCol);
   uint64_t* bar = reinterpret_cast<uint64_t*>(s + Sm::kBars);  // K K^T, U, W, K loads 0 and 1, V load
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s + Sm::kBars + 6 * 8);
@@ -194,31 +203,37 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
   const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + 32 * qt;
 
   const int t = tid - 256;  // of the threads of warps 8 to 15
-  float beta_n = 0.f;       // thread t < 128: the next item's token's beta, scaled
+  float beta_n = 0.f, p_n = 1.f;  // beta, scaled, and the key's inverse scale of the next item's token t / 2
   auto load_k = [&](const Item& x, int b) { load_tile(X0 + b * kTile, &maps.k, (int)x.krow0, bar + 3 + b); };
   // decays, K's operand and K K^T of item x, number j of this CTA (warps 8 to 15)
   auto stage_keys = [&](const Item& x, int j) {
     const int b = j & 1, slot = x.it / p.seqs.H, h = x.it - slot * p.seqs.H;
-    const bool mine = t < x.n;
-    const float la = mine ? gdr_log(p.log_alpha[x.row0 + t]) : 0.f, bt = mine ? p.beta[x.row0 + t] : 0.f;
+    const float la = t < x.n ? gdr_log(p.log_alpha[x.row0 + t]) : 0.f;
+    const float bt = t / 2 < x.n ? p.beta[x.row0 + t / 2] : 0.f;
     chunk_decays(la, gs, tot, t, kPrepBar2, 256);
     column_decays(cf, gs, t);
     wait_bar(bar + 3 + b, (j >> 1) & 1, p.err);
-    const float ik = tile_to_f16<256>(X0 + b * kTile, x.n, red, t, kPrepBar2, nullptr);
-    // A is K K^T of the scaled tile, beta takes the scale
-    beta_n = bt * (ik * ik / kKeysDown);
+    float l1;
+    p_n = keys_to_f16<256>(X0 + b * kTile, x.n, red, t, kPrepBar2, l1);
+    // A is K K^T of the scaled rows, beta takes the scales
+    beta_n = bt * (p_n * p_n / kKeysDown);
     Tables& tb = p.tab[x.it];
+    uint32_t* bounds = reinterpret_cast<uint32_t*>(tot);  // (the decays' sums have been read)
+    const uint32_t most = __reduce_max_sync(0xffffffffu, rows_bound(bt, p_n, l1));
+    if (lane == 0) bounds[warp - 8] = most;
+    if ((t & 1) == 0) {
+      tb.p[t / 2] = p_n;
+      tb.row[t / 2] = bt * p_n;
+    }
     if (t < kC) {
       const float2 g = gs[t];
       tb.g[t] = g;
-      tb.into[t] = gdr_alpha(g.x + g.y);  // (the last one scales the state, chunk after chunk)
       tb.out[t] = exp_diff(gs[kC - 1], g);
     }
     tc_fence_before();
     named_bar_sync(kPrepBar2, 256);
+    if (t == 32) tb.all = chunk_factors(gs, rows_scale(max_of<8>(bounds)));
     if (t == 0) {
-      inv[1 + b] = ik;
-      tb.ik = ik;
       tc_fence_after();
       mma_tile<kAlong, kAlong>(tmem, sX0 + b * kTile, sX0 + b * kTile, false);
       umma_commit(bar);
@@ -251,10 +266,9 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     __syncthreads();
     const Item nx = next[b ^ 1];
     const float2 gi = gs[i];
-    if (t >= 0 && t < kC) {
-      bs[t] = beta_n;
-      in_s[t] = exp_diff(gs[t], make_float2(0.f, 0.f));
-    }
+    const float pi = p.tab[it].p[i];
+    if (t >= 0 && (t & 1) == 0) bs[t / 2] = beta_n;
+    if (t >= 0 && t < kC) in_s[t] = exp_diff(gs[t], make_float2(0.f, 0.f));
     // A_ij = (k_i . k_j) G_ij, j < i
 #pragma unroll 1
     for (int c = 0; c < 2; ++c) {
@@ -275,11 +289,9 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     } else {
       wait_bar(bar + 5, j & 1, p.err);
       uint32_t vbits;
-      const float iv = tile_to_f16<256>(XV, me.n, red + 8, t, kPrepBar2, &vbits);
-      if (t == 0) {
-        atomicMax(p.amax_s + sh, vbits);
-        inv[0] = iv;
-      }
+      const float iv = values_to_f16<256>(XV, me.n, p_n, red + 8, t, kPrepBar2, &vbits);
+      if (lane == 0) atomicMax(p.amax_s + sh, vbits);
+      if (t == 0) inv[0] = iv;
       if (p.state_in && me.chunk == 0) {
         const uint32_t m = __reduce_max_sync(0xffffffffu, state_max(p.state_in + sh * p.dv * p.dk, p.dv * p.dk, t, 256));
         if (lane == 0) atomicMax(p.amax_s + sh, m);
@@ -293,8 +305,8 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
       }
     }
     __syncthreads();
-    // ---- U = T' V -> 256, W = T' diag(exp(g)) K -> 384
-    const float iv = inv[0], ik = inv[1 + b];
+    // ---- U = T' V -> 256, W = T' diag(exp(g)) K -> 384 (of v' and k', a row's p in the end)
+    const float iv = inv[0];
     float m[32];
     load_m(m, Mp, i, qt);
     __syncthreads();
@@ -317,7 +329,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     if (t == 0 && nx.it < items) load_tile(XV, &maps.v, (int)nx.row0, bar + 5);
     __syncwarp();
     // U and W leave by way of the operands' places
-    write_rows(reinterpret_cast<float*>(R), tl + 256, i, qt, iv / kInvUp);
+    write_rows(reinterpret_cast<float*>(R), tl + 256, i, qt, iv * pi / kInvUp);
     fence_proxy_async_shared();
     __syncthreads();
     if (tid == 0) {
@@ -333,7 +345,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
       load_k(next[b], b);
     }
     __syncwarp();
-    write_tiles<true>(M, M + kTile, tl + 384, i, qt, ik / kInvUp, kLoScale);
+    write_tiles<true>(M, M + kTile, tl + 384, i, qt, pi / kInvUp, kLoScale);
     fence_proxy_async_shared();
     tc_fence_before();
     __syncthreads();
@@ -375,6 +387,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
   float2* tot = reinterpret_cast<float2*>(out_s + kC);
   uint32_t* red = reinterpret_cast<uint32_t*>(tot + 4);  // 3 x 16
   float* inv = reinterpret_cast<float*>(red + 48);       // inverse scales of V and Q
+  uint32_t* bounds = red + 52;                           // 16
   float* cf = reinterpret_cast<float*>(s + Sm::kM);  // the columns' decay factors, where M comes to stand
   uint64_t* bar = reinterpret_cast<uint64_t*>(s + Sm::kBars);
   // bar: products, K, U, Q, V and dO, Q K^T
@@ -454,8 +467,8 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     Tables& tb = p.tab[it];
     unsigned char* Wg = p.W + (size_t)it * 2 * kTile;
     unsigned char* Wdg = p.Wd + (size_t)it * 2 * kTile;
-    const float beta_i = bt;
     const bool t_end = me.t0 + n == me.len;
+    if (tid < kC) bs[tid] = bt;
     chunk_decays(gdr_log(la), gs, tot, tid, 0, kPrepThreads);
     column_decays(cf, gs, tid);
     const float2 gi = gs[i];
@@ -464,15 +477,14 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
       in_s[i] = in;
       out_s[i] = out;
       tb.g[i] = gi;
-      tb.into[i] = gdr_alpha(gi.x + gi.y);  // (the last one scales the state, chunk after chunk)
+      tb.into[i] = gdr_alpha(gi.x + gi.y);
       tb.out[i] = out;
       tb.rel[i] = exp_diff(gi, gs[0]);
     }
     if (p.state_in && me.chunk == 0) raise_max(am_s, state_max(p.state_in + sh * p.dv * p.dk, p.dv * p.dk, tid, kPrepThreads));
     wait_bar(bar + 1, nkq & 1, p.err);
-    const float ik = tile_to_f16<kPrepThreads>(X0, n, red, tid, 0, nullptr);
-    // A is K K^T of the scaled tile, beta takes the scale
-    if (tid < kC) bs[tid] = beta_i * (ik * ik / kKeysDown);
+    float l1;
+    const float pk = keys_to_f16<kPrepThreads>(X0, n, red, tid, 0, l1);
     // ---- K K^T -> 0
     issue([&]() {
       mma_tile<kAlong, kAlong>(tmem, sX0, sX0, false);
@@ -481,8 +493,17 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
         bulk_store(p.K16 + ((size_t)slot * p.seqs.Hk + hk) * kTile, X0, kTile);
         bulk_commit();
       }
-      tb.ik = ik;
     });
+    {  // A is K K^T of the scaled rows, beta takes the scales
+      const float bk = bs[tid / 4];
+      const uint32_t most = __reduce_max_sync(0xffffffffu, rows_bound(bk, pk, l1));
+      if (lane == 0) bounds[warp] = most;
+      if ((tid & 3) == 0) {
+        bs[tid / 4] = bk * (pk * pk / kKeysDown);
+        tb.p[tid / 4] = pk;
+        tb.row[tid / 4] = bk * pk;
+      }
+    }
     wait_mma();
     // A_ij = (k_i . k_j) G_ij, j < i
 #pragma unroll 1
@@ -496,22 +517,25 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
         mat4(Ap, i, (j0 >> 2) + v) = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
     }
     __syncthreads();
+    const float pi = tb.p[i];
     if (warp < 8) {
       tri_solve(Ap, Mp, bs, tid);
     } else {
       const int t = tid - 256;
       uint32_t vbits;
+      const float pv = tb.p[t / 2];
+      if (t == 0) tb.all = chunk_factors(gs, rows_scale(max_of<16>(bounds)));
       wait_bar(bar + 4, nv & 1, p.err);
-      const float iv = tile_to_f16<256>(XV, n, red + 16, t, kPrepBar2, &vbits);
+      const float iv = values_to_f16<256>(XV, n, pv, red + 16, t, kPrepBar2, &vbits);
+      if (lane == 0) atomicMax(am_s, vbits);
       wait_bar(bar + 3, nkq & 1, p.err);
-      const float iq = tile_to_f16<256>(X1, n, red + 32, t, kPrepBar2, nullptr);
+      const float iq = tile_to_f16<256>(X1, n, red + 32, t, kPrepBar2);
       tc_fence_before();
       named_bar_sync(kPrepBar2, 256);
       if (t == 0) {  // Q K^T -> 128, while the tensor cores are free
         tc_fence_after();
         mma_tile<kAlong, kAlong>(tmem + 128, sX1, sX0, false);
         umma_commit(bar + 5);
-        atomicMax(am_s, vbits);
         inv[0] = iv;
         inv[1] = iq;
         tb.iq = iq;
@@ -544,7 +568,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     ++nv;
     ++nkq;
     const float iv = inv[0], iq = inv[1], bi = bs[i];
-    // ---- U = T' V -> 256, W = T' diag(exp(g)) K -> 384
+    // ---- U = T' V -> 256, W = T' diag(exp(g)) K -> 384 (of v' and k', a row's p in the end)
     float m[32];
     load_m(m, Mp, i, qt);
     __syncthreads();
@@ -565,14 +589,14 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     tc_fence_after();
     {
       load_values(&maps.dout, row0, 256);  // (V has been read; thread 0 may still be issuing products)
-      write_rows(p.U + (size_t)it * kC * kC, tl + 256, i, qt, iv / kInvUp);
+      write_rows(p.U + (size_t)it * kC * kC, tl + 256, i, qt, iv * pi / kInvUp);
       const float rel = exp_diff(gi, gs[0]), in0 = in_s[0];
       // ---- Wd = T^T diag(exp(g_C - g)) K -> 0, Bc = Q^T diag(exp(g)) dO -> 256 (exp(g_0) and its scales below)
       put_inverse(R, R + kTile, m, i, qt, out_s[i], bi);
       wait_mma();
       wait_bar(bar + 4, nv & 1, p.err);
       ++nv;
-      const float id = tile_to_f16<kPrepThreads>(XV, n, red, tid, 0, nullptr);
+      const float id = tile_to_f16<kPrepThreads>(XV, n, red, tid, 0);
       __syncthreads();
       column_decays(bs, gs, tid);  // (the tables' values have been read)
 #pragma unroll 1
@@ -598,7 +622,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
         bulk_commit();
         tb.id = id;
       });
-      write_tiles<true>(Wg, Wg + kTile, tl + 384, i, qt, ik / kInvUp, kLoScale);
+      write_tiles<true>(Wg, Wg + kTile, tl + 384, i, qt, pi / kInvUp, kLoScale);
       if (tid == 0) bulk_wait_read0();  // K16, Q16, dO16
       wait_mma();
       // ---- P^T dO -> 384
@@ -621,7 +645,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
       if (me.it < items) {  // K and Q have been read
         load_keys(me);
       }
-      write_tiles<true>(Wdg, Wdg + kTile, tl, i, qt, ik / kInvUp, kLoScale);
+      write_tiles<true>(Wdg, Wdg + kTile, tl, i, qt, pi / kInvUp, kLoScale);
       wait_mma();
       // ---- w0 = T^T (P^T dO) -> 0
       put_inverse(R, R + kTile, m, i, qt, 1.f, bi);
@@ -638,7 +662,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
       if (last) mx = max(mx, state_max(p.dstate_out + sh * p.dv * p.dk, p.dv * p.dk, tid, kPrepThreads));
       wait_mma();
       mx = max(mx, write_rows(p.w0 + (size_t)it * kC * kC, tl, i, qt,
-                              p.scale * iq * ik * id / (kScoreDown * kRowsDown * kInvUp)));
+                              p.scale * iq * pi * id / (kScoreDown * kRowsDown * kInvUp)));
       raise_max(p.amax_d + sh, mx);
     }
     tc_fence_before();  // (for the next item's products, behind its barriers)
@@ -896,7 +920,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdr_scan_kernel(TcParams p, i
   // what this thread loads of a chunk itself, one step ahead
   float4 un[2];
   uint4 vn = make_uint4(0u, 0u, 0u, 0u);
-  float fac_n = 0.f, ik_n = 0.f, gam_n = 0.f, beta_n = 0.f, in0_n = 0.f;
+  float fac_n = 0.f, row_n = 0.f, beta_n = 0.f, gam_n = 0.f, in0_n = 0.f;
   auto fetch = [&](int x) {
     const int c = at_step(x), t = c * kC + i;
     if (!LEAN) {
@@ -905,11 +929,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdr_scan_kernel(TcParams p, i
       un[1] = *reinterpret_cast<const float4*>(ug + 16 * kC);
     }
     const Tables& tb = p.tab[item(c)];
-    fac_n = REV ? tb.rel[i] : tb.out[i];
-    ik_n = tb.ik;
-    if (REV) in0_n = tb.into[0];
-    gam_n = tb.into[kC - 1];
-    beta_n = t < sq.len ? p.beta[row0 + t] : 0.f;
+    const float4 all = tb.all;
+    const float row = tb.row[i];
+    gam_n = all.x;
+    if (REV) in0_n = all.y;
+    row_n = row * all.z;
+    fac_n = row * (REV ? tb.rel[i] : tb.out[i]);
+    if (REV) beta_n = t < sq.len ? p.beta[row0 + t] : 0.f;
     if (REV) vn = t < sq.len && cols_in ? *reinterpret_cast<const uint4*>(p.v + (row0 + t) * p.dv + col0)
                                         : make_uint4(0u, 0u, 0u, 0u);
   };
@@ -944,7 +970,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdr_scan_kernel(TcParams p, i
       rows8(s + Sm::kRows + (x & 1) * kHalf, u, sg.x);
     }
     const uint4 vr = vn;
-    const float fac = fac_n * ik_n, gam = gam_n, bt = beta_n, in0 = in0_n;
+    const float fac = fac_n, row = row_n, bt = beta_n, gam = gam_n, in0 = in0_n;
     if (x + 1 < Nc) fetch(x + 1);
     wait_mma();
     {
@@ -960,16 +986,16 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdr_scan_kernel(TcParams p, i
       }
     }
     // ---- K^T (beta exp(g_C - g) e), K^T (beta exp(g - g_0) w)
-    put(Sm::kE, u, bt * fac, kLoScale);
+    put(Sm::kE, u, fac, kLoScale);
     ready(kScanBarE);
     if (MODE == kFwdKeep) {
-      put(Sm::kU, u, bt, 1.f);
+      put(Sm::kU, u, row, 1.f);
       float4* eg = reinterpret_cast<float4*>(s + Sm::kErr + piece);
       eg[0] = make_float4(sg.y * u[0], sg.y * u[1], sg.y * u[2], sg.y * u[3]);
       eg[kC] = make_float4(sg.y * u[4], sg.y * u[5], sg.y * u[6], sg.y * u[7]);
       ready(kScanBarU);
     } else {
-      keep((REV ? p.Y : p.E) + it * kTile, u, bt);
+      keep((REV ? p.Y : p.E) + it * kTile, u, row);
     }
     float bc[8];
     if (REV) {
@@ -1069,14 +1095,14 @@ __global__ void __launch_bounds__(256, 2) gdr_out_kernel(const __grid_constant__
   float* cf = reinterpret_cast<float*>(s + kOCol);
   if (tid < kC) gs[tid] = p.tab[it].g[tid];
   column_decays(cf, p.tab[it].g, tid);
-  const float ik = p.tab[it].ik, isf = operand_scale(__uint_as_float(p.amax_s[(size_t)seq * p.seqs.H + h])).y;
+  const float ie = p.tab[it].all.w, isf = operand_scale(__uint_as_float(p.amax_s[(size_t)seq * p.seqs.H + h])).y;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + 64 * hf;
   wait_bar(bars + 2, 0, p.err);
-  const float iq = tile_to_f16<256>(s + kOQ, n, red, tid, 0, nullptr);
+  const float iq = tile_to_f16<256>(s + kOQ, n, red, tid, 0);
   __syncthreads();
   if (tid == 0) {
     wait_bar(bars, 0, p.err);
@@ -1124,7 +1150,7 @@ __global__ void __launch_bounds__(256, 2) gdr_out_kernel(const __grid_constant__
   __syncwarp();
   tc_fence_after();
   const float fx = p.scale * iq * isf * exp_diff(gi, make_float2(0.f, 0.f));
-  const float fa = p.scale * iq * ik * isf / kScoreDown;
+  const float fa = p.scale * iq * ie * isf / kScoreDown;
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const int j0 = 64 * hf + 32 * c;
@@ -1267,7 +1293,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
       if (tid < kC) gs[tid] = tb.g[tid];
       column_decays(cf, tb.g, tid - 256 < 0 ? kColDecays : tid - 256);
       float* dg = reinterpret_cast<float*>(p.part + (it * kParts + 16) * kC);  // [4][token]
-      const float ik = tb.ik, iq = tb.iq, id = tb.id, in = tb.into[i], out = tb.out[i];
+      const float ie = tb.all.w, ip = pow2_inverse(tb.p[i]), iq = tb.iq, id = tb.id, in = tb.into[i], out = tb.out[i];
       const float isf = operand_scale(__uint_as_float(p.amax_s[sh])).y, isr = operand_scale(__uint_as_float(p.amax_d[sh])).y;
       uint4 qv[4];  // this thread's piece of Q's row
 #pragma unroll
@@ -1284,7 +1310,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
       // ---- round 1: dq's and dk's parts by the states, q.dq's first part
       float qdot = 0.f;
       {
-        const float fq = p.scale * in * id * isf, fu = isf * isr * out, fw = -isf * isr * in;
+        const float fq = p.scale * in * id * isf, fu = isf * isr * ie * ip * out, fw = -isf * isr * ie * ip * in;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float a[16], x[16];
@@ -1361,7 +1387,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
             *reinterpret_cast<uint4*>(s + tO + at) = make_uint4(nw[0], nw[1], nw[2], nw[3]);
           }
         }
-        dg[qt * kC + i] = fmaf(p.scale * id * isf * iq * ik, sum, qdot);
+        dg[qt * kC + i] = fmaf(p.scale * id * isf * iq * ie, sum, qdot);
       }
       fence_proxy_async_shared();
       tc_fence_before();
@@ -1407,8 +1433,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
       __syncwarp();
       // ---- round 3
       {
-        const float f0 = p.scale * id * isf * ik / kGradDown, f1 = p.scale * id * isf * iq / kGradDown;
-        const float f2 = -isf * isr * ik / kGradDown;
+        const float f0 = p.scale * id * isf * ie / kGradDown, f1 = p.scale * id * isf * iq * ie * ip / kGradDown;
+        const float f2 = -isf * isr * ie * ie * ip / kGradDown;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float a[16], x[16], y[16];

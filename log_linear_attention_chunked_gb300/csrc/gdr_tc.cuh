@@ -15,6 +15,21 @@
 // value's order; where one scale has to last over a whole sequence, l is kept
 // 2^11 times larger, in a range of its own.  The products h h', h l' and l h' are
 // accumulated in float32; l l' is below 2^-22 of the result.
+//
+// Range.  The recurrence does not change when a key is multiplied by c, its value and
+// error by c and its beta by c^-2, and the chunks are computed in the form where every
+// key has its largest element in [32, 64): k = p k', p a power of two per token, with
+//   beta' = beta p^2,   v' = v / p,   e' = e / p,   u' = p u,   w' = w / p,   p beta w.
+// A' = K' K'^T then has no entries but for |k'| in [32, 724], whatever the lengths of the
+// keys, and with beta |k|^2 <= 2 (transitions that do not grow a state) an entry of the
+// inverses is at most beta'_j |k'_i| |k'_j| <= 2 x 724 / 32.  (Keys shorter than 2^-12 of
+// the chunk's longest keep that p, so that their v' does not push the others' out of
+// range: an entry passes fp16's range when they are shorter than 2^-16.)  u and beta w
+// are at most beta |k|_1 of a state's largest element (and beta of the largest value, far
+// below a state's room), so u' and p beta w at most 2 |k'|_1 / |k'|^2 <= 2 x 11.4 / 32 of it
+// and have the state's room.  Where they stand in fp16 alone or without a second
+// range they carry one more power of two per chunk and head, eps (Tables), which brings the
+// bound to 1, so that faint writes keep their digits.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -420,11 +435,11 @@ __device__ __forceinline__ float2 operand_scale(float amax) {
 }
 
 // A bf16 tile in shared memory becomes fp16, scaled as above by its largest
-// value; returns the inverse scale (and that value's bits).  Rows from n on belong to
+// value; returns the inverse scale.  Rows from n on belong to
 // other sequences: they become zeros, whatever they hold.  NT threads (`t` among
 // them, barrier `bar`), the tile complete before; one barrier inside, none after.
 template <int NT>
-__device__ __noinline__ float tile_to_f16(unsigned char* tile, int n, uint32_t* red, int t, int bar, uint32_t* bits) {
+__device__ __noinline__ float tile_to_f16(unsigned char* tile, int n, uint32_t* red, int t, int bar) {
   const bool in = (t & 127) < n;
   constexpr int PC = kC * 16 / NT;
   uint32_t m2 = 0;
@@ -442,9 +457,7 @@ __device__ __noinline__ float tile_to_f16(unsigned char* tile, int n, uint32_t* 
     const uint4 x = *reinterpret_cast<const uint4*>(red + 4 * w);
     m = max(max(m, max(x.x, x.y)), max(x.z, x.w));
   }
-  m <<= 16;
-  if (bits) *bits = m;
-  const float2 sc = operand_scale(__uint_as_float(m));
+  const float2 sc = operand_scale(__uint_as_float(m << 16));
 #pragma unroll 2
   for (int c = 0; c < PC; ++c) {
     uint4* at = reinterpret_cast<uint4*>(tile + swz16(t & 127, PC * (t >> 7) + c));
@@ -459,6 +472,126 @@ __device__ __noinline__ float tile_to_f16(unsigned char* tile, int n, uint32_t* 
   }
   fence_proxy_async_shared();
   return sc.y;
+}
+
+// The same for K, a scale to each row, and the rows' sums of absolute values.  Thread =
+// part of a row (NT / 128 neighbouring threads to a row, which take its pieces in an
+// order that keeps a quarter of a warp free of bank conflicts); returns the inverse
+// scale p of the thread's row, in l1 the sum over the scaled row.
+template <int NT> __device__ __forceinline__ int row_piece(int t, int c) {
+  constexpr int W = NT / 128, PC = 16 / W;  // threads to a row, pieces to a thread
+  const int part = t % W, turn = part >= W / 2 ? W == 2 ? 4 : 2 : 0;
+  return PC * part + (c ^ turn);
+}
+__device__ __forceinline__ float pow2_inverse(float p) { return __uint_as_float((254u << 23) - __float_as_uint(p)); }
+constexpr float kKeysUp = 4.f;  // rows of K go up to 64
+constexpr float kShortest = 1.f / 4096.f;
+template <int NT>
+__device__ __noinline__ float keys_to_f16(unsigned char* tile, int n, uint32_t* red, int t, int bar, float& l1) {
+  constexpr int W = NT / 128, PC = 16 / W;
+  const int r = t / W;
+  const bool in = r < n;
+  uint32_t m2 = 0;
+#pragma unroll
+  for (int c = 0; c < PC; ++c) {
+    const uint4 v = *reinterpret_cast<const uint4*>(tile + swz16(r, row_piece<NT>(t, c)));
+    m2 = __vmaxu2(__vmaxu2(m2, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu);
+    m2 = __vmaxu2(__vmaxu2(m2, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu);
+  }
+  uint32_t row = in ? max(m2 & 0xffffu, m2 >> 16) : 0u;
+#pragma unroll
+  for (int o = 1; o < W; o <<= 1) row = max(row, __shfl_xor_sync(0xffffffffu, row, o));
+  uint32_t m = __reduce_max_sync(0xffffffffu, row);
+  if ((t & 31) == 0) red[t >> 5] = m;
+  named_bar_sync(bar, NT);
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    const uint4 x = *reinterpret_cast<const uint4*>(red + 4 * w);
+    m = max(max(m, max(x.x, x.y)), max(x.z, x.w));
+  }
+  const float all = __uint_as_float(m << 16), own = __uint_as_float(row << 16);
+  float2 sc = operand_scale(row == 0 || !(all < INFINITY) ? all : fmaxf(own, all * kShortest));
+  sc.x *= kKeysUp;
+  sc.y /= kKeysUp;
+  float sum = 0.f;
+#pragma unroll 2
+  for (int c = 0; c < PC; ++c) {
+    uint4* at = reinterpret_cast<uint4*>(tile + swz16(r, row_piece<NT>(t, c)));
+    uint4 v = *at;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float2 f = unpack_bf16x2(in ? w[e] : 0u);
+      f.x *= sc.x;
+      f.y *= sc.x;
+      sum += fabsf(f.x) + fabsf(f.y);
+      w[e] = pack_f16x2(f.x, f.y);
+    }
+    *at = v;
+  }
+#pragma unroll
+  for (int o = 1; o < W; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  l1 = sum;
+  fence_proxy_async_shared();
+  return sc.y;
+}
+// And for V / p, one scale to the tile; returns its inverse.  `p` is that of the thread's row,
+// `bits` those of the largest |v| that the thread's warp sees.
+template <int NT>
+__device__ __noinline__ float values_to_f16(unsigned char* tile, int n, float p, uint32_t* red, int t, int bar,
+                                            uint32_t* bits) {
+  constexpr int W = NT / 128, PC = 16 / W;
+  const int r = t / W;
+  const bool in = r < n;
+  uint32_t m2 = 0;
+#pragma unroll
+  for (int c = 0; c < PC; ++c) {
+    const uint4 v = *reinterpret_cast<const uint4*>(tile + swz16(r, row_piece<NT>(t, c)));
+    m2 = __vmaxu2(__vmaxu2(m2, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu);
+    m2 = __vmaxu2(__vmaxu2(m2, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu);
+  }
+  const uint32_t own = in ? max(m2 & 0xffffu, m2 >> 16) << 16 : 0u;
+  const float ip = pow2_inverse(p);
+  *bits = __reduce_max_sync(0xffffffffu, own);
+  uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(__uint_as_float(own) * ip));
+  if ((t & 31) == 0) red[t >> 5] = m;
+  named_bar_sync(bar, NT);
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    const uint4 x = *reinterpret_cast<const uint4*>(red + 4 * w);
+    m = max(max(m, max(x.x, x.y)), max(x.z, x.w));
+  }
+  const float2 sc = operand_scale(__uint_as_float(m));
+#pragma unroll 2
+  for (int c = 0; c < PC; ++c) {
+    uint4* at = reinterpret_cast<uint4*>(tile + swz16(r, row_piece<NT>(t, c)));
+    uint4 v = *at;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = unpack_bf16x2(in ? w[e] : 0u);
+      w[e] = pack_f16x2(ip * f.x * sc.x, ip * f.y * sc.x);
+    }
+    *at = v;
+  }
+  fence_proxy_async_shared();
+  return sc.y;
+}
+// the bits of a bound of a token's rows u' and p beta w: beta p |k|_1 of a state's largest element
+// (|k|_1 = p l1) and beta p of the largest value, whose own scale leaves it 4096 times more room
+__device__ __forceinline__ uint32_t rows_bound(float beta, float p, float l1) {
+  return __float_as_uint(fabsf(beta) * p * fmaxf(p * l1, 1.f / 128.f));
+}
+template <int N> __device__ __forceinline__ uint32_t max_of(const uint32_t* x) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) m = max(m, x[i]);
+  return m;
+}
+// eps: the power of two that brings a bound of the rows u' of a chunk to at most 1
+__device__ __forceinline__ float rows_scale(uint32_t bits) {
+  const int e = (int)(bits >> 23);  // the bound is below 2^(e - 126)
+  return e == 0 || e >= 255 ? 1.f : __uint_as_float((uint32_t)min(max(253 - e, 1), 187) << 23);
 }
 
 // the bits of the largest of a state's n values that this thread of `threads` sees
