@@ -42,3 +42,31 @@ def test_key_lengths_that_differ(B, ratio):
     assert launches(B, x) == (3, 4)
     check_fwd(B, x)
     check_bwd(B, x)
+
+
+# ------------------------------------------------------------------ bf16 token by token
+TOKENWISE = [(1, 4, 2, 16, 64, 64), (1, 1, 1, 1, 128, 128), (2, 2, 1, 31, 128, 128), (2, 2, 2, 63, 64, 128),
+             (1, 2, 1, 64, 128, 64), (1, 2, 2, 127, 128, 128), (1, 2, 1, 128, 128, 128), (1, 2, 1, 240, 128, 128),
+             (1, 2, 1, 300, 64, 64), (1, 2, 2, 700, 32, 16), (2, 4, 1, 333, 16, 128)]
+
+
+@pytest.mark.parametrize("Bn,H,Hk,T,dk,dv", TOKENWISE)
+def test_bf16_outputs_of_float32_arithmetic(B, monkeypatch, Bn, H, Hk, T, dk, dv):
+    """Token by token a bf16 output is a float32 value rounded once, at every head size."""
+    monkeypatch.setattr(base, "tol_out", lambda x: 2.0 ** -8 + TOL_F32)
+    x = draw(Bn, H, Hk, T, dk, dv, seed=50)
+    fwd, bwd = launches(B, x)
+    assert fwd == 1
+    check_fwd(B, x)
+    if bwd == 2:
+        check_bwd(B, x)
+
+
+def test_the_same_call_twice(B):
+    """Nothing in a call depends on the order in which its blocks run."""
+    for starts in (None, [0, 130, 131, 700, 900]):
+        x = draw(1, 16, 8, 900, 128, 128, n=4 if starts else None, seed=51)
+        f, g = gpu_fwd(B, x, starts), gpu_bwd(B, x, starts)
+        for _ in range(3):
+            assert all(np.array_equal(a, b) for a, b in zip(gpu_fwd(B, x, starts), f))
+            assert all(np.array_equal(a, b) for a, b in zip(gpu_bwd(B, x, starts), g))
