@@ -42,7 +42,7 @@ struct Tables {
   float row[kC];   // beta p: what makes u' and p beta w of e and w
   float4 all;      // exp(g_C), exp(g_0), eps, 1 / eps
   float iq, id;    // inverse scales of the fp16 tiles of Q and dO
-  float2 pad;
+  unsigned mu, mw; // bits of the largest element of the rows u' and p beta w (of the gradient)
 };
 
 struct TcParams {
@@ -524,7 +524,10 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
       const int t = tid - 256;
       uint32_t vbits;
       const float pv = tb.p[t / 2];
-      if (t == 0) tb.all = chunk_factors(gs, rows_scale(max_of<16>(bounds)));
+      if (t == 0) {
+        tb.all = chunk_factors(gs, rows_scale(max_of<16>(bounds)));
+        tb.mu = tb.mw = 0u;
+      }
       wait_bar(bar + 4, nv & 1, p.err);
       const float iv = values_to_f16<256>(XV, n, pv, red + 16, t, kPrepBar2, &vbits);
       if (lane == 0) atomicMax(am_s, vbits);
@@ -997,6 +1000,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdr_scan_kernel(TcParams p, i
     } else {
       keep((REV ? p.Y : p.E) + it * kTile, u, row);
     }
+    if (LEAN) {  // what the gradient scales their products by
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(fabsf(row * u[j])));
+      m = __reduce_max_sync(0xffffffffu, m);
+      if (lane == 0) atomicMax(REV ? &p.tab[it].mw : &p.tab[it].mu, m);
+    }
     float bc[8];
     if (REV) {
       float er[8];
@@ -1181,7 +1191,6 @@ __global__ void __launch_bounds__(256, 2) gdr_out_kernel(const __grid_constant__
 }
 
 // ---------------------------------------------------------------- gradients
-constexpr float kGradDown = 1.f / 64.f;  // of R and N, as operands
 constexpr uint32_t kGBars = 7 * kTile;
 constexpr uint32_t kGTab = kGBars + 6 * 8;
 constexpr uint32_t kGNext = kGTab + 2 * kC * 4 + 32;
@@ -1198,7 +1207,9 @@ constexpr int kGradThreads = 512;
 // chain of its three rounds.  Per head three rounds of products over seven tiles of
 // shared memory:
 //   dO S, (beta w) S, u D;   dO u^T, (beta w) u^T, Q K^T;   R K, R^T Q, (N + N^T) K
-// with R = scale (dO u^T . G) and N = ((beta w) u^T . G) strictly lower.  The
+// with R = scale (dO u^T . G) and N = ((beta w) u^T . G) strictly lower, as operands
+// scaled by what brings the largest elements of u' and p beta w (known from the scans) to 16,
+// as that of dO is: a sum of 128 products stays below 2^15, however far states grew.  The
 // first and fourth take S and u in two parts: q.dq, which enters dlog_alpha, is
 // then exact to float32; the rest ends in 16-bit gradients.
 __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p) {
@@ -1293,8 +1304,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
       if (tid < kC) gs[tid] = tb.g[tid];
       column_decays(cf, tb.g, tid - 256 < 0 ? kColDecays : tid - 256);
       float* dg = reinterpret_cast<float*>(p.part + (it * kParts + 16) * kC);  // [4][token]
-      const float ie = tb.all.w, ip = pow2_inverse(tb.p[i]), iq = tb.iq, id = tb.id, in = tb.into[i], out = tb.out[i];
+      // factors of products: fo of dO S, fr of dO (eps u')^T, fn of (eps p beta w) (eps u')^T, fs of eps u' D and
+      // eps p beta w S, with 1 / p of a row of dk
       const float isf = operand_scale(__uint_as_float(p.amax_s[sh])).y, isr = operand_scale(__uint_as_float(p.amax_d[sh])).y;
+      const float ie = tb.all.w, ip = pow2_inverse(tb.p[i]), iq = tb.iq, fo = p.scale * tb.id * isf, fr = fo * ie;
+      const float fs = isf * isr * ie * ip, fn = -fs * ie, fq = fo * tb.into[i], fu = fs * tb.out[i], fw = -fs * tb.into[i];
+      // of R and N as operands (what is below 2^-24 is zero in fp16)
+      const float up_r = operand_scale(fmaxf(__uint_as_float(tb.mu), 0x1p-24f)).x;
+      const float up_n = up_r * operand_scale(fmaxf(__uint_as_float(tb.mw), 0x1p-24f)).x;
       uint4 qv[4];  // this thread's piece of Q's row
 #pragma unroll
       for (int v = 0; v < 4; ++v)
@@ -1310,7 +1327,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
       // ---- round 1: dq's and dk's parts by the states, q.dq's first part
       float qdot = 0.f;
       {
-        const float fq = p.scale * in * id * isf, fu = isf * isr * ie * ip * out, fw = -isf * isr * ie * ip * in;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float a[16], x[16];
@@ -1374,20 +1390,19 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
           tmem_ld_wait();
 #pragma unroll
           for (int c8 = 0; c8 < 2; ++c8) {
-            uint32_t rw[4], nw[4];
+            uint32_t rr[4], nw[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int jj = 8 * c8 + 2 * e, j = j0 + 16 * c + jj;
-              rw[e] = pack_f16x2(kGradDown * r[jj], kGradDown * r[jj + 1]);
-              nw[e] = pack_f16x2(j < i ? kGradDown * dec[jj] * a[jj] : 0.f,
-                                 j + 1 < i ? kGradDown * dec[jj + 1] * a[jj + 1] : 0.f);
+              rr[e] = pack_f16x2(up_r * r[jj], up_r * r[jj + 1]);
+              nw[e] = pack_f16x2(j < i ? up_n * dec[jj] * a[jj] : 0.f, j + 1 < i ? up_n * dec[jj + 1] * a[jj + 1] : 0.f);
             }
             const uint32_t at = swz16(i, 4 * qt + 2 * c + c8);
-            *reinterpret_cast<uint4*>(s + tD + at) = make_uint4(rw[0], rw[1], rw[2], rw[3]);
+            *reinterpret_cast<uint4*>(s + tD + at) = make_uint4(rr[0], rr[1], rr[2], rr[3]);
             *reinterpret_cast<uint4*>(s + tO + at) = make_uint4(nw[0], nw[1], nw[2], nw[3]);
           }
         }
-        dg[qt * kC + i] = fmaf(p.scale * id * isf * iq * ie, sum, qdot);
+        dg[qt * kC + i] = fmaf(fr * iq, sum, qdot);
       }
       fence_proxy_async_shared();
       tc_fence_before();
@@ -1433,8 +1448,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
       __syncwarp();
       // ---- round 3
       {
-        const float f0 = p.scale * id * isf * ie / kGradDown, f1 = p.scale * id * isf * iq * ie * ip / kGradDown;
-        const float f2 = -isf * isr * ie * ie * ip / kGradDown;
+        const float f0 = fr * pow2_inverse(up_r), f1 = f0 * iq * ip, f2 = fn * pow2_inverse(up_n);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float a[16], x[16], y[16];

@@ -9,11 +9,82 @@ import torch
 
 from oracle import gdr
 from tests import test_gpu_gdr as base
-from tests._parity import TOL_F32, rel_err
+from tests._parity import TOL_BF16, TOL_F32, rel_err
 from tests.test_gpu_gdr import B, DEV, check_bwd, check_fwd, draw, gpu_bwd, gpu_fwd, launches  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 NAMES = ("q", "k", "v", "log_alpha", "beta")
+
+
+# ------------------------------------------------------------------ products of the gradient
+def repeated(n):
+    """Tolerance of states and gates' gradients where n tokens (of a chunk) have one key and beta |k|^2
+    up to 2.  Their rows e solve (I + A diag(beta)) e = ..., whose entries and whose inverse's are 2 at
+    most: 2 n to a row.  The computed ones solve it up to 2^-21 of its terms (operands in two fp16 parts,
+    3 x 2^-24 each product, and its sum), so that they are off by 2^-21 (2 n) (2 n) of the largest."""
+    return 2.0 ** -21 * (2 * n) ** 2
+
+
+def terms_of_dk(x, scale):
+    """The largest sum of magnitudes that make up an element of dk, over the largest |dk|, for sequences
+    of one chunk without decay: R^T Q, u D, (N + N^T) K and (beta w) S, N = (beta w) u^T below the diagonal."""
+    terms, dk = 0.0, 0.0
+    for _, (q, k, v, la, b), do, S, D in base.slices(x, None):
+        dk = dk + gdr.backward(q, k, v, la, b, do, scale=scale, state=S, dstate=D)["dk"]
+        S0, D1, u, w = np.abs(S), np.abs(D), np.zeros_like(v), np.zeros_like(v)
+        for t in range(len(q)):
+            u[t] = b[t] * (v[t] - S @ k[t])
+            S = S + np.outer(u[t], k[t])
+        for t in reversed(range(len(q))):
+            D = D + scale * np.outer(do[t], q[t])
+            w[t] = b[t] * D @ k[t]
+            D = D - np.outer(w[t], k[t])
+        u, w = np.abs(u), np.abs(w)
+        N, R = np.tril(w @ u.T, -1), np.tril(scale * np.abs(do) @ u.T)
+        terms = terms + R.T @ np.abs(q) + u @ D1 + (N + N.T) @ np.abs(k) + w @ S0
+    return terms.max() / np.abs(dk).max()
+
+
+def flat_key(T, d, length):
+    """One key of equal elements at every token."""
+    return torch.full((1, 1, T, d), length / d ** 0.5, dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("T", [64, 512])
+def test_gradient_of_repeated_keys(B, monkeypatch, T):
+    """beta |k|^2 just below 2, one key throughout and values of alternating sign: at 512 tokens the
+    state grows 71-fold and the written rows 1600-fold over the largest value."""
+    x = draw(1, 1, 1, T, 128, 128, seed=40)
+    x["k"] = flat_key(T, 128, 1.0)
+    x["beta"][:] = 1.999
+    x["log_alpha"][:] = 0.0
+    x["v"] = (1.0 - 2.0 * (torch.arange(T) % 2)).view(1, 1, T, 1).expand(1, 1, T, 128).contiguous().to(torch.bfloat16)
+    x["dout"] = torch.ones_like(x["v"])
+    del x["state_in"], x["dstate_out"]
+    assert launches(B, x)[1] == 4
+    monkeypatch.setattr(base, "TOL_F32", repeated(min(T, 128)))
+    check_fwd(B, x)
+    check_bwd(B, x)
+
+
+@pytest.mark.parametrize("sq", [1.0, 1.89])
+def test_gradient_of_constant_states(B, monkeypatch, sq):
+    """Flat states and adjoints that do not grow, flat keys with beta |k|^2 up to 1.89: a written row is
+    11 times any element of the state, and so is a row of w."""
+    x = draw(1, 2, 1, 64, 128, 128, seed=41)
+    x["k"] = flat_key(64, 128, sq ** 0.5)
+    x["beta"][:] = 2.0 if sq == 1.0 else 1.0
+    x["log_alpha"][:] = 0.0
+    x["state_in"][:] = 1.9
+    x["dstate_out"][:] = 1.9
+    assert launches(B, x)[1] == 4
+    monkeypatch.setattr(base, "TOL_F32", repeated(64))
+    check_fwd(B, x)
+    # dk is a sum of terms that cancel: operands of one fp16 part, half a step (2^-11) each, three of them in N's
+    # terms (its two factors and itself), two in the others
+    terms = terms_of_dk(x, 0.5)
+    monkeypatch.setattr(base, "tol_out", lambda x: max(TOL_BF16, 2.0 ** -8 + 3 * 2.0 ** -11 * terms))
+    check_bwd(B, x)
 
 
 # ------------------------------------------------------------------ written rows
