@@ -113,9 +113,8 @@ inline size_t gdr_slots(const GdrArgs& a, int C) {
 constexpr float kGdrMinLog = -1e4f;
 __device__ __forceinline__ float gdr_log(float la) { return la < kGdrMinLog ? kGdrMinLog : la; }
 
-// alpha of one token, for states that are multiplied by hundreds of them in turn: near 1
-// expf's error, though within its bound, leans to one side and adds up (the reverse
-// recurrence over 526 tokens with alpha = 0.998: 5e-6 off); 1 + expm1f is off by its rounding.
+// exp of a log decay that a state is multiplied by again and again: near 1 expf's error,
+// though within its bound, leans to one side and adds up; 1 + expm1f is off by its rounding.
 __device__ __forceinline__ float gdr_alpha(float la) { return la > -0.5f ? 1.f + expm1f(la) : expf(la); }
 
 // sums of floats as pairs (value and what its rounding left)

@@ -17,10 +17,10 @@
 // while token t - 1 updates the state; likewise backwards.  The products of
 // neighbouring keys are made once per staged tile.  Arithmetic is on pairs of
 // floats (one instruction for two).  Half of a CTA's threads walk over the tokens;
-// the others stage the tile after the next, make the next tile's products of
+// the others stage the tile after the next, make the next tile's decays and products of
 // neighbours and write the last tile's results, one barrier a tile.  A token takes
-// 0.12 us at d_k = 128 (0.08 at 32) while every CTA has an SM's schedulers to
-// itself: T = 1001, 8 heads of 32 x 64, float32, 80 us, from 133 with the sums in line.
+// 0.12 us at d_k = 128 (0.075 at 32) while every CTA has an SM's schedulers to
+// itself: T = 1001, 8 heads of 32 x 64, float32, 76 us, from 133 with the sums in line.
 #include "gdr.cuh"
 #include "sm100.cuh"
 
@@ -174,6 +174,26 @@ template <typename IO, int DK> struct RecSm {
 };
 constexpr int kHelpBar = 1;
 
+// The decays of a tile's tokens (lane t's is `la` of token t; whole warp), from the last one back if
+// REV.  A state is multiplied by one after another, so that a rounding that repeats (0.9999, token
+// after token) would add up over its memory: what the product so far is off by, `off` (relative), is
+// taken out of the next factor before that is rounded, and the product of any run of them is within
+// a few roundings of the exact one.  exp(la) - 1 keeps a factor near 1 exact until it is rounded; those
+// that are not leave `off` to the next one.  It takes 300 cycles a tile, beside the recurrence.
+template <bool REV> __device__ __forceinline__ float tile_decays(float la, float& off, int lane) {
+  const bool near = la > -0.5f;
+  const float m = near ? expm1f(la) : 0.f;
+  float own = 0.f;
+#pragma unroll
+  for (int x = 0; x < kTile; ++x) {
+    const int t = REV ? kTile - 1 - x : x;
+    const float c = __shfl_sync(0xffffffffu, m, t) - off, r = 1.f + c;
+    off = (r - 1.f) - c;
+    if (lane == t) own = r;
+  }
+  return near ? own : expf(la);
+}
+
 // The recurrence.
 template <typename IO, int DK>
 __device__ __forceinline__ void rec_forward(const RecParams& p) {
@@ -204,7 +224,7 @@ __device__ __forceinline__ void rec_forward(const RecParams& p) {
     const IO* kg = static_cast<const IO*>(p.k) + krow0 * DK;
     const IO* vg = static_cast<const IO*>(p.v) + row0 * p.dv;
     IO* og = p.o ? static_cast<IO*>(p.o) + row0 * p.dv : nullptr;
-    float la = 0.f, bt = 0.f;
+    float la = 0.f, bt = 0.f, off = 0.f;
     auto fetch = [&](int j) {  // (one group of copies a tile, an empty one behind the last)
       if (j < tiles) {
         const int t0 = j * kTile, n = min(kTile, sq.len - t0);
@@ -216,14 +236,17 @@ __device__ __forceinline__ void rec_forward(const RecParams& p) {
       cp_async_commit();
     };
     auto gates = [&](int j) {
-      const int t = j * kTile + grp;
-      if (l == 0 && t < sq.len) {
-        la = p.log_alpha[row0 + t];
-        bt = p.beta[row0 + t];
-      }
+      const int t = j * kTile + grp, ta = j * kTile + tid;
+      if (l == 0 && t < sq.len) bt = p.beta[row0 + t];
+      if (tid < kTile) la = ta < sq.len ? p.log_alpha[row0 + ta] : 0.f;
     };
-    // tile j is there: its products of neighbours, one group of lanes to a token
+    // tile j: its decays and, once it is there, its products of neighbours, one group of lanes to a token
     auto products = [&](int j) {
+      float4* tok = sm.side[j & 1].tok;
+      if (tid < 32) {
+        const float d = tile_decays<false>(la, off, tid);
+        if (tid < kTile) tok[tid].x = d;
+      }
       cp_async_wait<1>();
       named_bar_sync(kHelpBar, NT);
       const RecTile<IO, DK>& t = sm.tile[j % 3];
@@ -233,7 +256,12 @@ __device__ __forceinline__ void rec_forward(const RecParams& p) {
       const float kq = group_sum<LPR>(dot2<NP>(x, y));
       load_pairs<DK>(t.k + max(grp - 1, 0) * DK, l, y);
       const float kk = group_sum<LPR>(dot2<NP>(x, y));
-      if (l == 0) sm.side[j & 1].tok[grp] = make_float4(gdr_alpha(la), bt, kq, kk);
+      if (l == 0) {
+        tok[grp].y = bt;
+        tok[grp].z = kq;
+        tok[grp].w = kk;
+      }
+      gates(j + 1);  // (on their way until the next tile's products)
     };
     gates(0);
     fetch(0);
@@ -251,7 +279,6 @@ __device__ __forceinline__ void rec_forward(const RecParams& p) {
           if (p.kept_errors) p.kept_errors[row0 * p.dv + at] = side.err[t][r];
         }
       }
-      gates(j + 1);
       fetch(j + 2);
       if (j + 1 < tiles) products(j + 1);
       __syncthreads();
@@ -370,7 +397,7 @@ __device__ __forceinline__ void rec_reverse(const RecParams& p) {
     const IO* qg = static_cast<const IO*>(p.q) + krow0 * DK;
     const IO* kg = static_cast<const IO*>(p.k) + krow0 * DK;
     const IO* dg = static_cast<const IO*>(p.dout) + row0 * p.dv;
-    float la = 0.f, bt = 0.f;
+    float la = 0.f, bt = 0.f, off = 0.f;
     auto fetch = [&](int x) {
       if (x < tiles) {
         const int t0 = (tiles - 1 - x) * kTile, n = min(kTile, sq.len - t0);
@@ -382,13 +409,16 @@ __device__ __forceinline__ void rec_reverse(const RecParams& p) {
       cp_async_commit();
     };
     auto gates = [&](int x) {
-      const int t = (tiles - 1 - x) * kTile + grp;
-      if (l == 0 && x < tiles && t < sq.len) {
-        la = p.log_alpha[row0 + t];
-        bt = p.beta[row0 + t];
-      }
+      const int t = (tiles - 1 - x) * kTile + grp, ta = (tiles - 1 - x) * kTile + tid;
+      if (l == 0 && x < tiles && t < sq.len) bt = p.beta[row0 + t];
+      if (tid < kTile) la = x < tiles && ta < sq.len ? p.log_alpha[row0 + ta] : 0.f;
     };
     auto products = [&](int x) {
+      float4* tok = sm.side[x & 1].tok;
+      if (tid < 32) {
+        const float d = tile_decays<true>(la, off, tid);
+        if (tid < kTile) tok[tid].x = d;
+      }
       cp_async_wait<1>();
       named_bar_sync(kHelpBar, NT);
       const RecTile<IO, DK>& t = sm.tile[x % 3];
@@ -399,9 +429,12 @@ __device__ __forceinline__ void rec_reverse(const RecParams& p) {
       const float qk = group_sum<LPR>(dot2<NP>(a, b)), qk1 = group_sum<LPR>(dot2<NP>(b, z));
       const float kk = group_sum<LPR>(dot2<NP>(a, z));
       if (l == 0) {
-        sm.side[x & 1].tok[grp] = make_float4(gdr_alpha(la), bt, qk, qk1);
+        tok[grp].y = bt;
+        tok[grp].z = qk;
+        tok[grp].w = qk1;
         sm.side[x & 1].more[grp] = kk;
       }
+      gates(x + 1);
     };
     gates(0);
     fetch(0);
@@ -417,7 +450,6 @@ __device__ __forceinline__ void rec_reverse(const RecParams& p) {
           p.kept_w[(row0 + t0 + t) * p.dv + r0 + r] = side.out[t][r];
         }
       }
-      gates(x + 1);
       fetch(x + 2);
       if (x + 1 < tiles) products(x + 1);
       __syncthreads();
@@ -557,7 +589,10 @@ __global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_decode_kernel(
   if (slots && sl == 0 && h == 0)
     for (int x = tid; x < b; x += Cfg::kThreads)
       if (slots[x] == slot) raise_error(err, kErrDeviceArg);
-  const float a = gdr_alpha(la);
+  // alpha x, near 1 as x + (alpha - 1) x: step after step a rounded alpha would add up over the state's memory
+  const bool near = la > -0.5f;
+  const float a = near ? expm1f(la) : expf(la);
+  auto decayed = [&](float x) { return fmaf(a, x, near ? x : 0.f); };
   const float c = group_sum<LPR>(dot<EPL>(kv, qv));
 #pragma unroll
   for (int x = 0; x < kStepPasses; ++x) {
@@ -570,11 +605,11 @@ __global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_decode_kernel(
     sk = group_sum<LPR>(sk);
     sqd = group_sum<LPR>(sqd);
     if (r < dv) {
-      const float u = be * fmaf(-a, sk, vv[x]);
+      const float u = be * (vv[x] - decayed(sk));
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) s[x][i] = fmaf(u, kv[i], a * s[x][i]);
+      for (int i = 0; i < EPL; ++i) s[x][i] = fmaf(u, kv[i], decayed(s[x][i]));
       store_row<DK>(st + (size_t)r * DK, l, s[x]);
-      if (l == 0) os[grp + kRows * x] = scale * fmaf(a, sqd, u * c);
+      if (l == 0) os[grp + kRows * x] = scale * fmaf(u, c, decayed(sqd));
     }
   }
   __syncthreads();

@@ -115,6 +115,43 @@ def test_key_lengths_that_differ(B, ratio):
     check_bwd(B, x)
 
 
+# ------------------------------------------------------------------ long memories
+@pytest.mark.parametrize("d,io,T", [(32, "f32", 4000), (128, "f32", 1500), (16, "bf16", 4000), (64, "bf16", 250)])
+def test_decay_near_one_token_by_token(B, d, io, T):
+    """alpha = 0.9999 and faint writes: a state is scaled by thousands of decays, whose
+    roundings must not lean to one side."""
+    x = draw(1, 2, 1, T, d, d, io, seed=44)
+    x["log_alpha"][:] = -1e-4
+    x["beta"] *= 0.02
+    assert launches(B, x)[0] == 1
+    check_fwd(B, x)
+    if launches(B, x)[1] == 2:
+        check_bwd(B, x)
+
+
+@pytest.mark.parametrize("la", [-1e-4, -0.37, -0.53, -3.0, -90.0, -float("inf")])
+def test_constant_decays_token_by_token(B, la):
+    x = draw(1, 2, 1, 300, 32, 32, "f32", seed=45)
+    x["log_alpha"][:] = la
+    check_fwd(B, x)
+    check_bwd(B, x)
+
+
+def test_decay_near_one_in_decode_steps(B):
+    T, H, d = 3000, 2, 32
+    x = draw(1, H, 1, T, d, d, "f32", seed=46)
+    x["log_alpha"][:] = -1e-4
+    x["beta"] *= 0.02
+    g = {n: x[n].to(DEV) for n in NAMES}
+    st = x["state_in"].to(DEV)
+    steps = [g[n].transpose(1, 2).transpose(0, 1).contiguous() for n in NAMES]  # [T, 1, heads, ...]
+    for t in range(T):
+        B.ll_gdr_decode_step(*[s[t] for s in steps[:3]], steps[3][t].clone(), steps[4][t].clone(), st)
+    assert B.ll_last_device_error() == 0
+    for (i, b, h, hk, lo, hi), a, _, s0, _ in base.slices(x, None):
+        assert rel_err(st[i, h].cpu().numpy(), gdr.forward(*a, state=s0)[1], 0) <= TOL_F32
+
+
 # ------------------------------------------------------------------ bf16 token by token
 TOKENWISE = [(1, 4, 2, 16, 64, 64), (1, 1, 1, 1, 128, 128), (2, 2, 1, 31, 128, 128), (2, 2, 2, 63, 64, 128),
              (1, 2, 1, 64, 128, 64), (1, 2, 2, 127, 128, 128), (1, 2, 1, 128, 128, 128), (1, 2, 1, 240, 128, 128),
