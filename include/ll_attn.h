@@ -392,7 +392,7 @@ LL_API ll_status ll_gdn_fwd_b(const ll_shape* shape, const void* q, const void* 
  *
  * Two ways of computing, chosen by types and sizes alone (ll_gdr_*_launches
  * tells which).  Token by token, every io dtype and head size: float32
- * arithmetic throughout.  In chunks of 128 tokens on the tensor cores, bf16 io
+ * arithmetic throughout, a state rounded once a token.  In chunks of 128 tokens on the tensor cores, bf16 io
  * with dk and dv of 64 or 128, where it is the faster: operands are scaled by
  * powers of two to fp16, in two parts (22 bits) where a state or a gate's
  * gradient depends on them, sums are float32; states, dlog_alpha and dbeta keep

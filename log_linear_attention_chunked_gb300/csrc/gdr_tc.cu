@@ -40,7 +40,7 @@ struct Tables {
   float p[kC];     // inverse scales of the rows of the fp16 tile of K
   float out[kC];   // exp(g_C - g_t)
   float row[kC];   // beta p: what makes u' and p beta w of e and w
-  float4 all;      // exp(g_C), exp(g_0), eps, 1 / eps
+  float4 all;      // what exp(g_C) is made of (below), exp(g_0), eps
   float iq, id;    // inverse scales of the fp16 tiles of Q and dO
   unsigned mu, mw; // bits of the largest element of the rows u' and p beta w (of the gradient)
 };
@@ -76,8 +76,16 @@ struct TcParams {
 // ---------------------------------------------------------------- preparation
 __device__ __forceinline__ float4 chunk_factors(const float2* gs, float eps) {
   const float2 g0 = gs[0], g = gs[kC - 1];
-  // (exp(g_C) scales the state, chunk after chunk)
-  return make_float4(gdr_alpha(g.x + g.y), gdr_alpha(g0.x + g0.y), eps, pow2_inverse(eps));
+  const float d = g.x + g.y;
+  return make_float4(d > -0.5f ? expm1f(d) : 0.f, d > -0.5f ? -1.f : expf(d), gdr_alpha(g0.x + g0.y), eps);
+}
+// exp(g_C), by which the state is multiplied chunk after chunk: what the product of the rounded
+// factors so far is off by, `off` (relative), is taken out of one near 1 before that is rounded, so that
+// roundings which repeat do not add up (log alpha = -1.3e-6: 3e-8 a chunk, 3e-5 after 131072 tokens).
+__device__ __forceinline__ float chunk_decay(float4 all, float& off) {
+  const float c = all.x - off, r = 1.f + c;
+  off = (r - 1.f) - c;
+  return all.y < 0.f ? r : all.y;
 }
 // one (chunk, head): its number (no more when it is the item count), sequence, place and length
 struct Item {
@@ -923,7 +931,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdr_scan_kernel(TcParams p, i
   // what this thread loads of a chunk itself, one step ahead
   float4 un[2];
   uint4 vn = make_uint4(0u, 0u, 0u, 0u);
-  float fac_n = 0.f, row_n = 0.f, beta_n = 0.f, gam_n = 0.f, in0_n = 0.f;
+  float fac_n = 0.f, row_n = 0.f, beta_n = 0.f, gam_n = 0.f, in0_n = 0.f, off = 0.f;
   auto fetch = [&](int x) {
     const int c = at_step(x), t = c * kC + i;
     if (!LEAN) {
@@ -934,9 +942,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdr_scan_kernel(TcParams p, i
     const Tables& tb = p.tab[item(c)];
     const float4 all = tb.all;
     const float row = tb.row[i];
-    gam_n = all.x;
-    if (REV) in0_n = all.y;
-    row_n = row * all.z;
+    gam_n = chunk_decay(all, off);
+    if (REV) in0_n = all.z;
+    row_n = row * all.w;
     fac_n = row * (REV ? tb.rel[i] : tb.out[i]);
     if (REV) beta_n = t < sq.len ? p.beta[row0 + t] : 0.f;
     if (REV) vn = t < sq.len && cols_in ? *reinterpret_cast<const uint4*>(p.v + (row0 + t) * p.dv + col0)
@@ -1105,7 +1113,7 @@ __global__ void __launch_bounds__(256, 2) gdr_out_kernel(const __grid_constant__
   float* cf = reinterpret_cast<float*>(s + kOCol);
   if (tid < kC) gs[tid] = p.tab[it].g[tid];
   column_decays(cf, p.tab[it].g, tid);
-  const float ie = p.tab[it].all.w, isf = operand_scale(__uint_as_float(p.amax_s[(size_t)seq * p.seqs.H + h])).y;
+  const float ie = pow2_inverse(p.tab[it].all.w), isf = operand_scale(__uint_as_float(p.amax_s[(size_t)seq * p.seqs.H + h])).y;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1307,7 +1315,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
       // factors of products: fo of dO S, fr of dO (eps u')^T, fn of (eps p beta w) (eps u')^T, fs of eps u' D and
       // eps p beta w S, with 1 / p of a row of dk
       const float isf = operand_scale(__uint_as_float(p.amax_s[sh])).y, isr = operand_scale(__uint_as_float(p.amax_d[sh])).y;
-      const float ie = tb.all.w, ip = pow2_inverse(tb.p[i]), iq = tb.iq, fo = p.scale * tb.id * isf, fr = fo * ie;
+      const float ie = pow2_inverse(tb.all.w), ip = pow2_inverse(tb.p[i]), iq = tb.iq, fo = p.scale * tb.id * isf, fr = fo * ie;
       const float fs = isf * isr * ie * ip, fn = -fs * ie, fq = fo * tb.into[i], fu = fs * tb.out[i], fw = -fs * tb.into[i];
       // of R and N as operands (what is below 2^-24 is zero in fp16)
       const float up_r = operand_scale(fmaxf(__uint_as_float(tb.mu), 0x1p-24f)).x;

@@ -129,6 +129,28 @@ def test_decay_near_one_token_by_token(B, d, io, T):
         check_bwd(B, x)
 
 
+@pytest.mark.parametrize("la", [-1.3e-6, -1e-4])
+@pytest.mark.parametrize("d,io,T", [(64, "bf16", 131072), (32, "f32", 131072)])
+def test_long_memories(B, d, io, T, la):
+    """Nothing is written: a state and its adjoint are what T decays leave of them.  Token by token a float32
+    state itself is rounded T times, by up to 2^-24 each; as it moves by the same few steps a token, to the
+    same side for long."""
+    g = torch.Generator(device=DEV).manual_seed(52)
+    dt = torch.bfloat16 if io == "bf16" else torch.float32
+    q, k, v = (torch.nn.functional.normalize(torch.randn(1, 1, T, d, generator=g, device=DEV), dim=-1).to(dt) for _ in range(3))
+    gate, zero = torch.full((1, 1, T), la, device=DEV), torch.zeros(1, 1, T, device=DEV)
+    s, ds = (torch.randn(1, 1, d, d, generator=g, device=DEV) for _ in range(2))
+    left = np.exp(T * np.float64(np.float32(la)))
+    out, tol = torch.empty_like(s), TOL_F32 if io == "bf16" else TOL_F32 + T * 2.0 ** -24
+    B.ll_gdr_fwd(q, k, v, gate, zero, state_in=s, state_out=out)
+    err = rel_err(out.cpu().numpy(), s.double().cpu().numpy() * left, 0)
+    assert err <= tol
+    B.ll_gdr_bwd(q, k, v, gate, zero, torch.zeros_like(v), state_in=s, dstate_out=ds, dstate_in=out)
+    assert B.ll_last_device_error() == 0
+    err = rel_err(out.cpu().numpy(), ds.double().cpu().numpy() * left, 0)
+    assert err <= tol
+
+
 @pytest.mark.parametrize("la", [-1e-4, -0.37, -0.53, -3.0, -90.0, -float("inf")])
 def test_constant_decays_token_by_token(B, la):
     x = draw(1, 2, 1, 300, 32, 32, "f32", seed=45)
