@@ -113,6 +113,10 @@ inline size_t gdr_slots(const GdrArgs& a, int C) {
 constexpr float kGdrMinLog = -1e4f;
 __device__ __forceinline__ float gdr_log(float la) { return la < kGdrMinLog ? kGdrMinLog : la; }
 
+// Is alpha zero in float32 (2^-149 is its smallest value)?  Then nothing depends on its
+// logarithm, whose gradient the kernels otherwise have as a sum that ends in rounding.
+__device__ __forceinline__ bool gdr_forgets(float la) { return la < -104.f; }
+
 // exp of a log decay that a state is multiplied by again and again: near 1 expf's error,
 // though within its bound, leans to one side and adds up; 1 + expm1f is off by its rounding.
 __device__ __forceinline__ float gdr_alpha(float la) { return la > -0.5f ? 1.f + expm1f(la) : expf(la); }

@@ -278,8 +278,12 @@ __global__ void __launch_bounds__(kThreads) gdr_grad_kernel(GradParams p) {
       float2 behind = make_float2(__shfl_down_sync(0xffffffffu, g.x, 1), __shfl_down_sync(0xffffffffu, g.y, 1));
       if (tid == 31) behind = make_float2(0.f, 0.f);
       behind = pair_add(behind, d1);
-      if (2 * tid < n) p.dlog_alpha[row0 + 2 * tid] = pair_add(g, sd).x;
-      if (2 * tid + 1 < n) p.dlog_alpha[row0 + 2 * tid + 1] = pair_add(behind, sd).x;
+      const float2 at[2] = {pair_add(g, sd), pair_add(behind, sd)};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const size_t t = row0 + 2 * tid + e;
+        if (2 * tid + e < n) p.dlog_alpha[t] = gdr_forgets(p.log_alpha[t]) ? 0.f : at[e].x;
+      }
     }
   }
 #pragma unroll

@@ -1427,6 +1427,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
       // ---- the gates' gradients: sums over the slices, the suffix sum over the chunk
       if (warp >= 12) {
         const int t = tid - 384;
+        const float la = t < n ? p.log_alpha[row0 + t] : 0.f;
         float ew = 0.f, vw = 0.f;
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
@@ -1447,7 +1448,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grad_tc_kernel(TcParams p
         named_bar_sync(1, kC);
         for (int w = q + 1; w < 4; ++w) y += tot[w];
         if (t < n) {
-          p.dlog_alpha[row0 + t] = (float)(y + (double)bsum);
+          p.dlog_alpha[row0 + t] = gdr_forgets(la) ? 0.f : (float)(y + (double)bsum);
           p.dbeta[row0 + t] = ew;
         }
       }

@@ -174,6 +174,19 @@ def test_decay_near_one_in_decode_steps(B):
         assert rel_err(st[i, h].cpu().numpy(), gdr.forward(*a, state=s0)[1], 0) <= TOL_F32
 
 
+# ------------------------------------------------------------------ alpha = 0
+@pytest.mark.parametrize("d,io,T", [(128, "bf16", 700), (64, "f32", 300), (32, "bf16", 200)])
+@pytest.mark.parametrize("la", [-float("inf"), -200.0])
+def test_no_gradient_by_a_decay_of_zero(B, d, io, T, la):
+    """alpha = 0 in float32: what came before does not matter, and neither does alpha's logarithm."""
+    x = draw(1, 2, 1, T, d, d, io, seed=47)
+    at = [0, 1, 50, 127, 128, T - 1]
+    x["log_alpha"][:, :, at] = la
+    got = gpu_bwd(B, x)[3]
+    assert (got[:, :, at] == 0.0).all()
+    assert (got != 0.0).sum() > got.size // 2
+
+
 # ------------------------------------------------------------------ bf16 token by token
 TOKENWISE = [(1, 4, 2, 16, 64, 64), (1, 1, 1, 1, 128, 128), (2, 2, 1, 31, 128, 128), (2, 2, 2, 63, 64, 128),
              (1, 2, 1, 64, 128, 64), (1, 2, 2, 127, 128, 128), (1, 2, 1, 128, 128, 128), (1, 2, 1, 240, 128, 128),
