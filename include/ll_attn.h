@@ -406,7 +406,11 @@ LL_API ll_status ll_gdn_fwd_b(const ll_shape* shape, const void* q, const void* 
  * not zero should have at least 2^-12 of the longest one's (largest elements compared):
  * below that accuracy falls, below 2^-16 results may be infinite.
  * Infinities and NaN stay within their sequence and, in v, gates, states and
- * upstream gradients, within their head (and its key head's dq and dk).
+ * upstream gradients, within their head (and its key head's dq and dk).  In
+ * ll_gdr_fwd tokens before a bad one do not see it, but in chunks those of its own
+ * chunk (tokens 128 c .. 128 c + 127 of the sequence) do; in ll_gdr_bwd a bad v reaches
+ * no chunk (of 64 or 128) before its own and a bad dout none behind it.  So padding
+ * behind the tokens of a row has to be finite, or left out by seq_starts.
  *
  * Calls allocate nothing, do not synchronise and can be captured; a workspace
  * serves one call at a time. */

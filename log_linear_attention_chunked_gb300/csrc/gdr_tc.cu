@@ -1009,11 +1009,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdr_scan_kernel(TcParams p, i
       keep((REV ? p.Y : p.E) + it * kTile, u, row);
     }
     if (LEAN) {  // what the gradient scales their products by
-      uint32_t m = 0;
+      uint32_t m = kNoMax;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(fabsf(row * u[j])));
+      for (int j = 0; j < 8; ++j) m = max_finite(m, row * u[j]);
       m = __reduce_max_sync(0xffffffffu, m);
-      if (lane == 0) atomicMax(REV ? &p.tab[it].mw : &p.tab[it].mu, m);
+      if (lane == 0) atomicMax(REV ? &p.tab[it].mw : &p.tab[it].mu, max_bits(m));
     }
     float bc[8];
     if (REV) {

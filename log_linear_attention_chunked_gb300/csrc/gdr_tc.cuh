@@ -434,6 +434,15 @@ __device__ __forceinline__ float2 operand_scale(float amax) {
   return make_float2(__uint_as_float((uint32_t)s << 23), __uint_as_float((uint32_t)(254 - s) << 23));
 }
 
+// Maxima of magnitudes that decide scales leave infinities and NaN out (a bad value must not
+// take range from chunks that it does not reach): of the bits without the sign plus one step of
+// the exponent, which wrap (float) or turn negative (bf16 pairs) for these.
+constexpr uint32_t kNoMax = 0x01000000u, kNoMax2 = 0x00800080u;
+__device__ __forceinline__ uint32_t max_finite(uint32_t m, float x) { return max(m, (__float_as_uint(x) << 1) + kNoMax); }
+__device__ __forceinline__ uint32_t max_bits(uint32_t m) { return (m - kNoMax) >> 1; }
+__device__ __forceinline__ uint32_t max_finite2(uint32_t m, uint32_t v) { return __vmaxs2(m, (v & 0x7fff7fffu) + kNoMax2); }
+__device__ __forceinline__ uint32_t max_bits2(uint32_t m) { return max(m & 0xffffu, m >> 16) - 0x80u; }
+
 // A bf16 tile in shared memory becomes fp16, scaled as above by its largest
 // value; returns the inverse scale.  Rows from n on belong to
 // other sequences: they become zeros, whatever they hold.  NT threads (`t` among
@@ -442,14 +451,13 @@ template <int NT>
 __device__ __noinline__ float tile_to_f16(unsigned char* tile, int n, uint32_t* red, int t, int bar) {
   const bool in = (t & 127) < n;
   constexpr int PC = kC * 16 / NT;
-  uint32_t m2 = 0;
+  uint32_t m2 = kNoMax2;
 #pragma unroll
   for (int c = 0; c < PC; ++c) {
     const uint4 v = *reinterpret_cast<const uint4*>(tile + swz16(t & 127, PC * (t >> 7) + c));
-    m2 = __vmaxu2(__vmaxu2(m2, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu);
-    m2 = __vmaxu2(__vmaxu2(m2, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu);
+    m2 = max_finite2(max_finite2(max_finite2(max_finite2(m2, v.x), v.y), v.z), v.w);
   }
-  uint32_t m = __reduce_max_sync(0xffffffffu, in ? max(m2 & 0xffffu, m2 >> 16) : 0u);
+  uint32_t m = __reduce_max_sync(0xffffffffu, in ? max_bits2(m2) : 0u);
   if ((t & 31) == 0) red[t >> 5] = m;
   named_bar_sync(bar, NT);
 #pragma unroll
@@ -491,14 +499,13 @@ __device__ __noinline__ float keys_to_f16(unsigned char* tile, int n, uint32_t* 
   constexpr int W = NT / 128, PC = 16 / W;
   const int r = t / W;
   const bool in = r < n;
-  uint32_t m2 = 0;
+  uint32_t m2 = kNoMax2;
 #pragma unroll
   for (int c = 0; c < PC; ++c) {
     const uint4 v = *reinterpret_cast<const uint4*>(tile + swz16(r, row_piece<NT>(t, c)));
-    m2 = __vmaxu2(__vmaxu2(m2, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu);
-    m2 = __vmaxu2(__vmaxu2(m2, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu);
+    m2 = max_finite2(max_finite2(max_finite2(max_finite2(m2, v.x), v.y), v.z), v.w);
   }
-  uint32_t row = in ? max(m2 & 0xffffu, m2 >> 16) : 0u;
+  uint32_t row = in ? max_bits2(m2) : 0u;
 #pragma unroll
   for (int o = 1; o < W; o <<= 1) row = max(row, __shfl_xor_sync(0xffffffffu, row, o));
   uint32_t m = __reduce_max_sync(0xffffffffu, row);
@@ -510,7 +517,7 @@ __device__ __noinline__ float keys_to_f16(unsigned char* tile, int n, uint32_t* 
     m = max(max(m, max(x.x, x.y)), max(x.z, x.w));
   }
   const float all = __uint_as_float(m << 16), own = __uint_as_float(row << 16);
-  float2 sc = operand_scale(row == 0 || !(all < INFINITY) ? all : fmaxf(own, all * kShortest));
+  float2 sc = operand_scale(row == 0 ? all : fmaxf(own, all * kShortest));
   sc.x *= kKeysUp;
   sc.y /= kKeysUp;
   float sum = 0.f;
@@ -543,14 +550,13 @@ __device__ __noinline__ float values_to_f16(unsigned char* tile, int n, float p,
   constexpr int W = NT / 128, PC = 16 / W;
   const int r = t / W;
   const bool in = r < n;
-  uint32_t m2 = 0;
+  uint32_t m2 = kNoMax2;
 #pragma unroll
   for (int c = 0; c < PC; ++c) {
     const uint4 v = *reinterpret_cast<const uint4*>(tile + swz16(r, row_piece<NT>(t, c)));
-    m2 = __vmaxu2(__vmaxu2(m2, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu);
-    m2 = __vmaxu2(__vmaxu2(m2, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu);
+    m2 = max_finite2(max_finite2(max_finite2(max_finite2(m2, v.x), v.y), v.z), v.w);
   }
-  const uint32_t own = in ? max(m2 & 0xffffu, m2 >> 16) << 16 : 0u;
+  const uint32_t own = in ? max_bits2(m2) << 16 : 0u;
   const float ip = pow2_inverse(p);
   *bits = __reduce_max_sync(0xffffffffu, own);
   uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(__uint_as_float(own) * ip));
@@ -597,14 +603,13 @@ __device__ __forceinline__ float rows_scale(uint32_t bits) {
 // the bits of the largest of a state's n values that this thread of `threads` sees
 // (16 bytes a load: with four the 64 KB took longer than a chunk's solve)
 __device__ __noinline__ uint32_t state_max(const float* x, int n, int t, int threads) {
-  uint32_t m = 0;
+  uint32_t m = kNoMax;
 #pragma unroll 4
   for (int e = t; e < n / 4; e += threads) {
     const float4 v = reinterpret_cast<const float4*>(x)[e];
-    m = max(max(m, max(__float_as_uint(fabsf(v.x)), __float_as_uint(fabsf(v.y)))),
-            max(__float_as_uint(fabsf(v.z)), __float_as_uint(fabsf(v.w))));
+    m = max_finite(max_finite(max_finite(max_finite(m, v.x), v.y), v.z), v.w);
   }
-  return m;
+  return max_bits(m);
 }
 
 // rows 0 .. n - 1 of a tile of 16-bit values into a [.., d] matrix, whole rows to half a warp
@@ -664,7 +669,7 @@ __device__ __forceinline__ void put_inverse(unsigned char* hi, unsigned char* lo
 }
 // an accumulator's row, times f, as [slice of 32][piece of 4][row][4] floats; returns its largest value's bits
 __device__ __noinline__ uint32_t write_rows(float* dst, uint32_t acc, int i, int qt, float f) {
-  uint32_t m = 0;
+  uint32_t m = kNoMax;
 #pragma unroll 1
   for (int c = 0; c < 2; ++c) {
     float x[16];
@@ -674,12 +679,11 @@ __device__ __noinline__ uint32_t write_rows(float* dst, uint32_t acc, int i, int
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const float4 y = make_float4(f * x[4 * v], f * x[4 * v + 1], f * x[4 * v + 2], f * x[4 * v + 3]);
-      m = max(max(m, max(__float_as_uint(fabsf(y.x)), __float_as_uint(fabsf(y.y)))),
-              max(__float_as_uint(fabsf(y.z)), __float_as_uint(fabsf(y.w))));
+      m = max_finite(max_finite(max_finite(max_finite(m, y.x), y.y), y.z), y.w);
       d[v * kC] = y;
     }
   }
-  return m;
+  return max_bits(m);
 }
 // an accumulator's row, times f, in two parts: tiles hi and lo, plain ones or not
 template <bool PLAIN>

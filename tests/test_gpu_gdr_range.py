@@ -187,6 +187,59 @@ def test_no_gradient_by_a_decay_of_zero(B, d, io, T, la):
     assert (got != 0.0).sum() > got.size // 2
 
 
+# ------------------------------------------------------------------ bad values inside a sequence
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("d,io,T,at,first", [(128, "bf16", 700, 300, 256), (64, "bf16", 600, 390, 384),
+                                             (128, "f32", 100, 37, 37), (128, "bf16", 60, 37, 37)])
+def test_a_bad_value_leaves_what_is_before_it(B, d, io, T, at, first, bad):
+    """In chunks: whole chunks before the bad token's; token by token: every token before it."""
+    x = draw(1, 2, 1, T, d, d, io, seed=48)
+    x["v"][:, 0, at, 3] = 0.0
+    ref = gpu_fwd(B, x)[0]
+    x["v"][:, 0, at, 3] = bad
+    o, s = gpu_fwd(B, x)
+    assert np.array_equal(o[:, 0, :first], ref[:, 0, :first]) and np.array_equal(o[:, 1], ref[:, 1])
+    assert not np.isfinite(o[0, 0, at, 3]) and not np.isfinite(s[0, 0, 3]).all()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("name", ["q", "k", "log_alpha", "beta"])
+@pytest.mark.parametrize("d,io,T,at,first", [(128, "bf16", 700, 300, 256), (128, "f32", 100, 37, 37)])
+def test_a_bad_key_or_gate_leaves_what_is_before_it(B, d, io, T, at, first, name, bad):
+    x = draw(1, 2, 1, T, d, d, io, seed=53)
+    x[name][(0, 0, at, 3) if name in "qk" else (0, 0, at)] = 0.0
+    ref = gpu_fwd(B, x)[0]
+    x[name][(0, 0, at, 3) if name in "qk" else (0, 0, at)] = bad
+    o = gpu_fwd(B, x)[0]
+    assert np.array_equal(o[:, :, :first], ref[:, :, :first]) and not np.isfinite(o[0, 0, at]).all()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("d,io,T,at", [(128, "bf16", 700, 300), (64, "f32", 200, 70)])
+def test_gradients_beside_a_bad_value(B, d, io, T, at, bad):
+    """A bad v reaches no chunk before its own, a bad dout none behind it."""
+    C = 128 if io == "bf16" else 64
+    x = draw(1, 2, 1, T, d, d, io, seed=49)
+    x["v"][:, 0, at, 3] = 0.0
+    x["dout"][:, 0, at, 3] = 0.0
+    ref = gpu_bwd(B, x)
+    before, behind = at // C * C, (at // C + 1) * C
+    y = {n: t.clone() for n, t in x.items()}
+    y["v"][:, 0, at, 3] = bad
+    got = gpu_bwd(B, y)
+    for a, b in zip(got[:5], ref[:5]):
+        assert np.array_equal(a[:, 0, :before], b[:, 0, :before])
+    for a, b in zip(got[2:5], ref[2:5]):
+        assert np.array_equal(a[:, 1], b[:, 1])
+    y = {n: t.clone() for n, t in x.items()}
+    y["dout"][:, 0, at, 3] = bad
+    got = gpu_bwd(B, y)
+    for a, b in zip(got[:5], ref[:5]):
+        assert np.array_equal(a[:, 0, behind:], b[:, 0, behind:])
+    for a, b in zip(got[2:5], ref[2:5]):
+        assert np.array_equal(a[:, 1], b[:, 1])
+
+
 # ------------------------------------------------------------------ bf16 token by token
 TOKENWISE = [(1, 4, 2, 16, 64, 64), (1, 1, 1, 1, 128, 128), (2, 2, 1, 31, 128, 128), (2, 2, 2, 63, 64, 128),
              (1, 2, 1, 64, 128, 64), (1, 2, 2, 127, 128, 128), (1, 2, 1, 128, 128, 128), (1, 2, 1, 240, 128, 128),
