@@ -416,7 +416,7 @@ LL_API ll_status ll_gdn_fwd_b(const ll_shape* shape, const void* q, const void* 
  * serves one call at a time. */
 
 /* Problem shape of ll_gdr_fwd and ll_gdr_bwd.
- *   B, T      batch rows and tokens per row (>= 1)
+ *   B, T      batch rows and tokens per row (>= 1; T below 2^31 - 1024)
  *   H, Hk     value heads and query/key heads, H a multiple of Hk: value head
  *             h reads query/key head h / (H / Hk)
  *   dk, dv    key / value head dims, each in {16, 32, 64, 128}

@@ -596,6 +596,8 @@ static ll_status check_gdr_shape(const ll_gdr_shape* s) {
   if (s->io != LL_F32 && s->io != LL_BF16) return LL_ERR_INVALID_ARG;
   if (!(s->scale - s->scale == 0.f)) return LL_ERR_INVALID_ARG;  // finite
   if (!head_dim_ok(s->dk) || !head_dim_ok(s->dv)) return LL_ERR_UNSUPPORTED;
+  // tokens are counted in 31 bits, in whole chunks and a few tiles ahead
+  if (s->T > 0x7fffffff - 1024) return LL_ERR_UNSUPPORTED;
   // CTAs are counted in 31 bits: at most (sequences or 16-token pieces) x heads x 8 of them
   const long long units = s->n_seqs ? (long long)s->T / 16 + s->n_seqs : (long long)s->B * ((s->T + 15ll) / 16);
   if (units >= (1ll << 31) || units * s->H >= (1ll << 28)) return LL_ERR_UNSUPPORTED;

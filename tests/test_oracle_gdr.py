@@ -168,3 +168,13 @@ def test_decode_arguments_are_refused(B):
     assert step(p=p[:6] + [p[2]]) == 1                   # o on v
     assert step(p=p[:5] + [p[1], p[6]]) == 1             # states on k
     assert step(p=p[:6] + [p[5] + 64]) == 1              # o inside the states
+
+
+@pytest.mark.parametrize("T", [(1 << 31) - 1, (1 << 31) - 128])
+def test_lengths_at_the_end_of_31_bits_are_refused(B, T):
+    """One head: few enough CTAs, but a length rounded up to whole chunks passes 2^31."""
+    for io in (B.LL_F32, B.LL_BF16):
+        s = _shape(B, B=1, H=1, Hk=1, T=T, dk=16, dv=16, io=io)
+        assert _call(B, "ll_gdr_fwd", s, [0] + [FAKE + (i << 40) for i in range(8)], ws=FAKE + (30 << 40)) == 2
+        assert _call(B, "ll_gdr_bwd", s, [0] + [FAKE + (i << 40) for i in range(14)], ws=FAKE + (30 << 40)) == 2
+        assert B.ll_gdr_bwd_workspace_size(s) == 0 and B.ll_gdr_fwd_launches(s) == 0
