@@ -455,7 +455,14 @@ def ll_gdn_fwd_b(q, k, v, log_alpha, beta, lam, chunk: int, *, o=None, workspace
                         workspace)
 
 
+def _int32(*sizes):
+    # (ctypes takes a larger one modulo 2^32)
+    if max(sizes) > 0x7fffffff or min(sizes) < -0x80000000:
+        raise ValueError(f"sizes beyond 32 bits: {sizes}")
+
+
 def make_gdr_shape(B, H, Hk, T, dk, dv, n_seqs=0, scale=1.0, io=LL_BF16) -> ll_gdr_shape:
+    _int32(B, H, Hk, T, dk, dv, n_seqs)
     return ll_gdr_shape(B, H, Hk, T, dk, dv, n_seqs, scale, io)
 
 
@@ -598,6 +605,7 @@ def ll_gdr_decode_step(q, k, v, log_alpha, beta, states, *, scale=1.0, slots=Non
     _need_like(log_alpha, "log_alpha", (B, H), torch.float32, dev)
     _need_like(beta, "beta", (B, H), torch.float32, dev)
     n = states.shape[0]
+    _int32(B, H, Hk, n)
     _need_like(states, "states", (n, H, dv, dk), torch.float32, dev)
     if slots is not None:
         _need_like(slots, "slots", (B,), torch.int64, dev)

@@ -178,3 +178,10 @@ def test_lengths_at_the_end_of_31_bits_are_refused(B, T):
         assert _call(B, "ll_gdr_fwd", s, [0] + [FAKE + (i << 40) for i in range(8)], ws=FAKE + (30 << 40)) == 2
         assert _call(B, "ll_gdr_bwd", s, [0] + [FAKE + (i << 40) for i in range(14)], ws=FAKE + (30 << 40)) == 2
         assert B.ll_gdr_bwd_workspace_size(s) == 0 and B.ll_gdr_fwd_launches(s) == 0
+
+
+@pytest.mark.parametrize("name", ["B", "H", "Hk", "T", "dk", "dv", "n_seqs"])
+def test_sizes_beyond_32_bits_are_refused(B, name):
+    """Taken modulo 2^32 such a call would work on a few of its tokens and return."""
+    with pytest.raises(ValueError):
+        _shape(B, **{name: (1 << 32) + 16})
