@@ -442,8 +442,9 @@ LL_API int ll_gdr_fwd_launches(const ll_gdr_shape* shape);
 /* Forward of the gated delta rule over whole sequences.
  *   seq_starts [n_seqs+1]  int32, required iff n_seqs > 0: non-decreasing, within
  *              0 .. T.  Tokens outside every sequence are neither read nor
- *              written.  A sequence with bounds that break this sets the device
- *              error word (LL_ERR_DEVICE) and is skipped.
+ *              written.  Starts that break this set the device error word
+ *              (LL_ERR_DEVICE); what the call then leaves in its outputs is unspecified
+ *              for every sequence (nothing outside of them is touched).
  *   q, k       [B,Hk,T,dk]  io dtype;   v, o [B,H,T,dv] io dtype
  *   log_alpha, beta [B,H,T] float32, log_alpha <= 0 (-inf forgets the state)
  *   state_in   [N,H,dv,dk]  float32 or NULL (zero states), N = n_seqs or B

@@ -11,7 +11,10 @@
 // + i.  Since floor(a) + ceil(b) <= floor(a + b) + 1 these ranges never overlap
 // and end below T / C + n, so no pass over the starts is needed to place them,
 // and a slot finds its sequence by bisection.  A sequence whose bounds are not
-// 0 <= start <= end <= T sets the device error word and is skipped.
+// 0 <= start <= end <= T sets the device error word and is skipped.  Starts that are not
+// ordered have at least one such; the others' slots may then overlap or go to another
+// sequence, which spoils their results, but every slot stays below T / C + n and every
+// chunk within its sequence's rows.
 #pragma once
 
 #include "common.cuh"
