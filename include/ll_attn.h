@@ -432,7 +432,9 @@ typedef struct {
   ll_dtype io;
 } ll_gdr_shape;
 
-/* Bytes of workspace ll_gdr_fwd needs (0 when it needs none, or on an invalid shape). */
+/* Bytes of workspace ll_gdr_fwd needs (0 when it needs none, or on an invalid shape).
+ * In chunks 196 KB for every started 128 tokens of a sequence and value head and
+ * 32 KB of a sequence and key head. */
 LL_API size_t ll_gdr_fwd_workspace_size(const ll_gdr_shape* shape);
 
 /* Kernel launches of one ll_gdr_fwd call: 1 token by token, 3 in chunks (which
@@ -458,7 +460,12 @@ LL_API ll_status ll_gdr_fwd(const ll_gdr_shape* shape, const int32_t* seq_starts
                             const void* v, const float* log_alpha, const float* beta, const float* state_in,
                             void* o, float* state_out, void* workspace, size_t ws_bytes, void* stream);
 
-/* Bytes of workspace ll_gdr_bwd needs (0 on an invalid shape). */
+/* Bytes of workspace ll_gdr_bwd needs (0 on an invalid shape).  In chunks 566 KB for
+ * every started 128 tokens of a sequence and value head, 64 KB of a sequence and key
+ * head, and a state for every sequence and value head: a batch of short sequences
+ * needs that much however short they are (512 of 16 tokens and 16 heads of 128 x 128:
+ * 5.8 GB; in parts a caller can do with less).  Token by token 2 states for every
+ * started 64 tokens and 8 dv bytes a token and head. */
 LL_API size_t ll_gdr_bwd_workspace_size(const ll_gdr_shape* shape);
 
 /* Kernel launches of one ll_gdr_bwd call: 2 token by token, 4 in chunks (and a

@@ -1695,8 +1695,8 @@ bool gdr_tc_fwd_use(const GdrArgs& a) {
 // The gradient: token by token it takes a launch over both recurrences and one over
 // chunks of 64.  At 128 x 128 the tensor cores are the faster at every length but a
 // token of many heads (16 heads: 78 / 58 us at 1 token, 82 / 58 at 16; 256 heads: 174 / 179 at 1,
-// 207 / 179 at 16); the bound of 16 is for the workspace too, whose items
-// are padded to 128 tokens.  With one side of 64 they are from 64 tokens on (64 x 128, 256 heads:
+// 207 / 179 at 16; 8192 heads: 7008 / 4417 at 16, 11323 / 4504 at 64); the bound of 16 is for the workspace
+// too, whose items are padded to 128 tokens (8192 heads of 16 tokens: 1.2 / 5.8 GB).  With one side of 64 they are from 64 tokens on (64 x 128, 256 heads:
 // 168 / 181 at 32, 219 / 182 at 64; 128 x 64, 16 heads: 52 / 59 at 32, 59 / 59 at 64), with two from
 // 128 (16 heads: 52 / 60 at 128, 66 / 64 at 256; 64 heads: 68 / 70 at 128, 111 / 90 at 192; 256 heads:
 // 244 / 180 at 128).
