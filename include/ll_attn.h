@@ -391,7 +391,8 @@ LL_API ll_status ll_gdn_fwd_b(const ll_shape* shape, const void* q, const void* 
  * and several value heads can share a key head.
  *
  * Two ways of computing, chosen by types and sizes alone (ll_gdr_*_launches
- * tells which).  Token by token, every io dtype and head size: float32
+ * tells which; lengths of packed sequences are not among them, and a batch of few heads
+ * whose tokens are nearly all one sequence's is slow: pass that one by itself).  Token by token, every io dtype and head size: float32
  * arithmetic throughout, a state rounded once a token.  In chunks of 128 tokens on the tensor cores, bf16 io
  * with dk and dv of 64 or 128, where it is the faster: operands are scaled by
  * powers of two to fp16, in two parts (22 bits) where a state or a gate's

@@ -1681,7 +1681,11 @@ static bool tc_formats(const GdrArgs& a) {
 // 384; for 1024 heads: 202 / 257 at 32 tokens, 363 / 262 at 64.  Only the device
 // knows the lengths of packed sequences: their mean is T / n, the longest is
 // taken for twice that.  The choice is the slower one, by 10 % or more, in 12 of
-// 451 shapes measured, by 1.53 times at most.
+// 451 shapes measured, by 1.53 times at most.  None of these is a packed batch of few
+// heads with nearly all of its tokens in one sequence, which goes token by token and is
+// one long chain: 64 sequences of 4096 tokens on one head 605 us, in chunks 101 (of even
+// lengths 38 and 49), 256 of them on two heads 823 and 216 (74 and 163).  Either choice is
+// the slower one for some lengths; a caller who knows of such a sequence can pass it alone.
 bool gdr_tc_fwd_use(const GdrArgs& a) {
   if (!tc_formats(a)) return false;
   const double seqs = gdr_sequences(a), states = seqs * a.H, wide = a.dk * a.dv / 4096.;
