@@ -403,7 +403,7 @@ LL_API ll_status ll_gdn_fwd_b(const ll_shape* shape, const void* q, const void* 
  * the largest |v| and |state_in| of its sequence and head, its gradient likewise
  * for 4096 times the largest value that a chunk or dstate_out adds to it; what is
  * below 2^-28 of these counts as zero in o, dq, dk and dv.  Keys may have any length
- * (beta small or large to match); of the keys of 128 neighbouring tokens one that is
+ * from 2^-12 to 2^14 (beta small or large to match); of the keys of 128 neighbouring tokens one that is
  * not zero should have at least 2^-12 of the longest one's (largest elements compared):
  * below that accuracy falls, below 2^-16 results may be infinite.
  * Infinities and NaN stay within their sequence and, in v, gates, states and

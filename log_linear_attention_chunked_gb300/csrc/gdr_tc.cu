@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
   float* in_s = bs + kC;
   float2* tot = reinterpret_cast<float2*>(in_s + kC);
   uint32_t* red = reinterpret_cast<uint32_t*>(tot + 4);  // 2 x 8
-  float* inv = reinterpret_cast<float*>(red + 16);       // inverse scale of V
+  float* inv = reinterpret_cast<float*>(red + 16);       // inverse scales of V and of p_all
   float* cf = reinterpret_cast<float*>(s + Sm::kCol);
   uint64_t* bar = reinterpret_cast<uint64_t*>(s + Sm::kBars);  // K K^T, U, W, K loads 0 and 1, V load
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s + Sm::kBars + 6 * 8);
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
   const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + 32 * qt;
 
   const int t = tid - 256;  // of the threads of warps 8 to 15
-  float beta_n = 0.f, p_n = 1.f;  // beta, scaled, and the key's inverse scale of the next item's token t / 2
+  float beta_n = 0.f, p_n = 1.f, all_n = 1.f;  // beta, scaled, and p of the next item's token t / 2, p_all
   auto load_k = [&](const Item& x, int b) { load_tile(X0 + b * kTile, &maps.k, (int)x.krow0, bar + 3 + b); };
   // decays, K's operand and K K^T of item x, number j of this CTA (warps 8 to 15)
   auto stage_keys = [&](const Item& x, int j) {
@@ -221,13 +221,14 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     chunk_decays(la, gs, tot, t, kPrepBar2, 256);
     column_decays(cf, gs, t);
     wait_bar(bar + 3 + b, (j >> 1) & 1, p.err);
-    float l1;
-    p_n = keys_to_f16<256>(X0 + b * kTile, x.n, red, t, kPrepBar2, l1);
+    const Keys key = keys_to_f16<256>(X0 + b * kTile, x.n, red, t, kPrepBar2);
+    p_n = key.p;
+    all_n = key.p_all;
     // A is K K^T of the scaled rows, beta takes the scales
-    beta_n = bt * (p_n * p_n / kKeysDown);
+    beta_n = bt * p_n * p_n / kKeysDown;
     Tables& tb = p.tab[x.it];
     uint32_t* bounds = reinterpret_cast<uint32_t*>(tot);  // (the decays' sums have been read)
-    const uint32_t most = __reduce_max_sync(0xffffffffu, rows_bound(bt, p_n, l1));
+    const uint32_t most = __reduce_max_sync(0xffffffffu, rows_bound(bt, p_n, key.l1));
     if (lane == 0) bounds[warp - 8] = most;
     if ((t & 1) == 0) {
       tb.p[t / 2] = p_n;
@@ -297,9 +298,12 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     } else {
       wait_bar(bar + 5, j & 1, p.err);
       uint32_t vbits;
-      const float iv = values_to_f16<256>(XV, me.n, p_n, red + 8, t, kPrepBar2, &vbits);
+      const float iv = values_to_f16<256>(XV, me.n, p_n * pow2_inverse(all_n), red + 8, t, kPrepBar2, &vbits);
       if (lane == 0) atomicMax(p.amax_s + sh, vbits);
-      if (t == 0) inv[0] = iv;
+      if (t == 0) {
+        inv[0] = iv;
+        inv[1] = pow2_inverse(all_n);
+      }
       if (p.state_in && me.chunk == 0) {
         const uint32_t m = __reduce_max_sync(0xffffffffu, state_max(p.state_in + sh * p.dv * p.dk, p.dv * p.dk, t, 256));
         if (lane == 0) atomicMax(p.amax_s + sh, m);
@@ -314,7 +318,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     }
     __syncthreads();
     // ---- U = T' V -> 256, W = T' diag(exp(g)) K -> 384 (of v' and k', a row's p in the end)
-    const float iv = inv[0];
+    const float iv = inv[0] * (pi * inv[1]);
     float m[32];
     load_m(m, Mp, i, qt);
     __syncthreads();
@@ -337,7 +341,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     if (t == 0 && nx.it < items) load_tile(XV, &maps.v, (int)nx.row0, bar + 5);
     __syncwarp();
     // U and W leave by way of the operands' places
-    write_rows(reinterpret_cast<float*>(R), tl + 256, i, qt, iv * pi / kInvUp);
+    write_rows(reinterpret_cast<float*>(R), tl + 256, i, qt, iv / kInvUp);
     fence_proxy_async_shared();
     __syncthreads();
     if (tid == 0) {
@@ -394,7 +398,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
   float* out_s = in_s + kC;
   float2* tot = reinterpret_cast<float2*>(out_s + kC);
   uint32_t* red = reinterpret_cast<uint32_t*>(tot + 4);  // 3 x 16
-  float* inv = reinterpret_cast<float*>(red + 48);       // inverse scales of V and Q
+  float* inv = reinterpret_cast<float*>(red + 48);       // inverse scales of V, Q and of p_all
   uint32_t* bounds = red + 52;                           // 16
   float* cf = reinterpret_cast<float*>(s + Sm::kM);  // the columns' decay factors, where M comes to stand
   uint64_t* bar = reinterpret_cast<uint64_t*>(s + Sm::kBars);
@@ -491,8 +495,8 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     }
     if (p.state_in && me.chunk == 0) raise_max(am_s, state_max(p.state_in + sh * p.dv * p.dk, p.dv * p.dk, tid, kPrepThreads));
     wait_bar(bar + 1, nkq & 1, p.err);
-    float l1;
-    const float pk = keys_to_f16<kPrepThreads>(X0, n, red, tid, 0, l1);
+    const Keys key = keys_to_f16<kPrepThreads>(X0, n, red, tid, 0);
+    if (tid == 0) inv[2] = pow2_inverse(key.p_all);
     // ---- K K^T -> 0
     issue([&]() {
       mma_tile<kAlong, kAlong>(tmem, sX0, sX0, false);
@@ -503,11 +507,11 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
       }
     });
     {  // A is K K^T of the scaled rows, beta takes the scales
-      const float bk = bs[tid / 4];
-      const uint32_t most = __reduce_max_sync(0xffffffffu, rows_bound(bk, pk, l1));
+      const float bk = bs[tid / 4], pk = key.p;
+      const uint32_t most = __reduce_max_sync(0xffffffffu, rows_bound(bk, pk, key.l1));
       if (lane == 0) bounds[warp] = most;
       if ((tid & 3) == 0) {
-        bs[tid / 4] = bk * (pk * pk / kKeysDown);
+        bs[tid / 4] = bk * pk * pk / kKeysDown;
         tb.p[tid / 4] = pk;
         tb.row[tid / 4] = bk * pk;
       }
@@ -537,7 +541,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
         tb.mu = tb.mw = 0u;
       }
       wait_bar(bar + 4, nv & 1, p.err);
-      const float iv = values_to_f16<256>(XV, n, pv, red + 16, t, kPrepBar2, &vbits);
+      const float iv = values_to_f16<256>(XV, n, pv * inv[2], red + 16, t, kPrepBar2, &vbits);
       if (lane == 0) atomicMax(am_s, vbits);
       wait_bar(bar + 3, nkq & 1, p.err);
       const float iq = tile_to_f16<256>(X1, n, red + 32, t, kPrepBar2);
@@ -578,7 +582,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     me = *next;
     ++nv;
     ++nkq;
-    const float iv = inv[0], iq = inv[1], bi = bs[i];
+    const float iv = inv[0] * (pi * inv[2]), iq = inv[1], bi = bs[i];
     // ---- U = T' V -> 256, W = T' diag(exp(g)) K -> 384 (of v' and k', a row's p in the end)
     float m[32];
     load_m(m, Mp, i, qt);
@@ -600,7 +604,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
     tc_fence_after();
     {
       load_values(&maps.dout, row0, 256);  // (V has been read; thread 0 may still be issuing products)
-      write_rows(p.U + (size_t)it * kC * kC, tl + 256, i, qt, iv * pi / kInvUp);
+      write_rows(p.U + (size_t)it * kC * kC, tl + 256, i, qt, iv / kInvUp);
       const float rel = exp_diff(gi, gs[0]), in0 = in_s[0];
       // ---- Wd = T^T diag(exp(g_C - g)) K -> 0, Bc = Q^T diag(exp(g)) dO -> 256 (exp(g_0) and its scales below)
       put_inverse(R, R + kTile, m, i, qt, out_s[i], bi);

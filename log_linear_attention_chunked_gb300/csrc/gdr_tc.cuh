@@ -484,8 +484,11 @@ __device__ __noinline__ float tile_to_f16(unsigned char* tile, int n, uint32_t* 
 
 // The same for K, a scale to each row, and the rows' sums of absolute values.  Thread =
 // part of a row (NT / 128 neighbouring threads to a row, which take its pieces in an
-// order that keeps a quarter of a warp free of bank conflicts); returns the inverse
-// scale p of the thread's row, in l1 the sum over the scaled row.
+// order that keeps a quarter of a warp free of bank conflicts).
+struct Keys {
+  float p, l1;  // of the thread's row: the inverse scale, the sum over the scaled row
+  float p_all;  // the longest key's p
+};
 template <int NT> __device__ __forceinline__ int row_piece(int t, int c) {
   constexpr int W = NT / 128, PC = 16 / W;  // threads to a row, pieces to a thread
   const int part = t % W, turn = part >= W / 2 ? W == 2 ? 4 : 2 : 0;
@@ -495,7 +498,7 @@ __device__ __forceinline__ float pow2_inverse(float p) { return __uint_as_float(
 constexpr float kKeysUp = 4.f;  // rows of K go up to 64
 constexpr float kShortest = 1.f / 4096.f;
 template <int NT>
-__device__ __noinline__ float keys_to_f16(unsigned char* tile, int n, uint32_t* red, int t, int bar, float& l1) {
+__device__ __noinline__ Keys keys_to_f16(unsigned char* tile, int n, uint32_t* red, int t, int bar) {
   constexpr int W = NT / 128, PC = 16 / W;
   const int r = t / W;
   const bool in = r < n;
@@ -538,12 +541,13 @@ __device__ __noinline__ float keys_to_f16(unsigned char* tile, int n, uint32_t* 
   }
 #pragma unroll
   for (int o = 1; o < W; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  l1 = sum;
   fence_proxy_async_shared();
-  return sc.y;
+  return Keys{sc.y, sum, operand_scale(all).y / kKeysUp};
 }
 // And for V / p, one scale to the tile; returns its inverse.  `p` is that of the thread's row,
-// `bits` those of the largest |v| that the thread's warp sees.
+// relative to the longest key's (1 to kShortest: kValuesDown keeps v / p below float's end whatever
+// v is), `bits` those of the largest |v| that the thread's warp sees.
+constexpr float kValuesDown = 1.f / 8192.f;
 template <int NT>
 __device__ __noinline__ float values_to_f16(unsigned char* tile, int n, float p, uint32_t* red, int t, int bar,
                                             uint32_t* bits) {
@@ -557,7 +561,7 @@ __device__ __noinline__ float values_to_f16(unsigned char* tile, int n, float p,
     m2 = max_finite2(max_finite2(max_finite2(max_finite2(m2, v.x), v.y), v.z), v.w);
   }
   const uint32_t own = in ? max_bits2(m2) << 16 : 0u;
-  const float ip = pow2_inverse(p);
+  const float ip = pow2_inverse(p) * kValuesDown;
   *bits = __reduce_max_sync(0xffffffffu, own);
   uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(__uint_as_float(own) * ip));
   if ((t & 31) == 0) red[t >> 5] = m;
@@ -581,7 +585,7 @@ __device__ __noinline__ float values_to_f16(unsigned char* tile, int n, float p,
     *at = v;
   }
   fence_proxy_async_shared();
-  return sc.y;
+  return sc.y / kValuesDown;
 }
 // the bits of a bound of a token's rows u' and p beta w: beta p |k|_1 of a state's largest element
 // (|k|_1 = p l1) and beta p of the largest value, whose own scale leaves it 4096 times more room

@@ -99,6 +99,27 @@ def test_short_keys_with_large_gates(B, shift):
     check_bwd(B, x)
 
 
+@pytest.mark.parametrize("shift", [6, 12])
+def test_long_keys_with_small_gates(B, shift):
+    """Keys of length 2^shift, beta |k|^2 below 1 as before."""
+    x = draw(1, 2, 1, 520, 128, 128, seed=54)
+    x["k"] = x["k"] * 2.0 ** shift
+    x["beta"] = x["beta"] * 4.0 ** -shift
+    assert launches(B, x) == (3, 4)
+    check_fwd(B, x)
+    check_bwd(B, x)
+
+
+@pytest.mark.parametrize("k", [-90, 120])
+def test_values_at_the_ends_of_float(B, k):
+    """Values and states scaled by 2^k scale the outputs by it (as test_scaling_by_powers_of_two_is_exact,
+    further out): an intermediate of their size times that of a key's inverse length must not overflow."""
+    x = draw(2, 4, 2, 300, 128, 128, seed=55)
+    y = {n: t * 2.0 ** k if n in ("v", "state_in") else t for n, t in x.items()}
+    for a, b in zip(gpu_fwd(B, x), gpu_fwd(B, y)):
+        assert np.array_equal(b, a * np.float32(2.0 ** k))
+
+
 # ------------------------------------------------------------------ the inverse
 @pytest.mark.parametrize("ratio", [2.0 ** 6, 2.0 ** 11])
 def test_key_lengths_that_differ(B, ratio):
