@@ -449,7 +449,7 @@ LL_API int ll_gdr_fwd_launches(const ll_gdr_shape* shape);
  *              (LL_ERR_DEVICE); what the call then leaves in its outputs is unspecified
  *              for every sequence (nothing outside of them is touched).
  *   q, k       [B,Hk,T,dk]  io dtype;   v, o [B,H,T,dv] io dtype
- *   log_alpha, beta [B,H,T] float32, log_alpha <= 0 (-inf forgets the state)
+ *   log_alpha, beta [B,H,T] float32, log_alpha <= 0 (-inf forgets the state, if that is finite)
  *   state_in   [N,H,dv,dk]  float32 or NULL (zero states), N = n_seqs or B
  *   state_out  [N,H,dv,dk]  float32 or NULL: the states after the last token
  *              (state_in's for an empty sequence).  May be state_in itself.
@@ -507,7 +507,8 @@ LL_API ll_status ll_gdr_bwd(const ll_gdr_shape* shape, const int32_t* seq_starts
  *           row is left as it is, the latter's rows and state are unspecified.
  *   n_slots states in the pool (>= B when slots is NULL)
  *   q, k    [B,Hk,dk] io dtype;   v, o [B,H,dv] io dtype
- *   log_alpha, beta [B,H] float32
+ *   log_alpha, beta [B,H] float32 (log_alpha = -inf forgets the state whatever it
+ *           holds, so that a slot can be handed on without being cleared)
  *   states  [n_slots,H,dv,dk] float32, in/out, each named state read and written once */
 LL_API ll_status ll_gdr_decode_step(int B, int H, int Hk, int dk, int dv, ll_dtype io, float scale,
                                     const int64_t* slots, int n_slots, const void* q, const void* k,

@@ -593,12 +593,16 @@ __global__ void __launch_bounds__(RowCfg<DK>::kThreads) gdr_decode_kernel(
   const bool near = la > -0.5f;
   const float a = near ? expm1f(la) : expf(la);
   auto decayed = [&](float x) { return fmaf(a, x, near ? x : 0.f); };
+  const bool forget = a == 0.f && !near;  // whatever the state holds: slots are handed on
   const float c = group_sum<LPR>(dot<EPL>(kv, qv));
 #pragma unroll
   for (int x = 0; x < kStepPasses; ++x) {
     const int r = r0 + kRows * x;
     float sk = 0.f, sqd = 0.f;
     if (r < dv) {
+      if (forget)
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) s[x][i] = 0.f;
       sk = dot<EPL>(s[x], kv);
       sqd = dot<EPL>(s[x], qv);
     }

@@ -287,3 +287,19 @@ def test_the_same_call_twice(B):
         for _ in range(3):
             assert all(np.array_equal(a, b) for a, b in zip(gpu_fwd(B, x, starts), f))
             assert all(np.array_equal(a, b) for a, b in zip(gpu_bwd(B, x, starts), g))
+
+
+# ------------------------------------------------------------------ a slot handed on
+@pytest.mark.parametrize("io,d", [("bf16", 128), ("f32", 32)])
+def test_decode_forgets_whatever_a_slot_holds(B, io, d):
+    H = 2
+    x = {n: t.to(DEV) for n, t in draw(3, H, 1, 1, d, d, io, seed=56).items()}
+    args = [x[n][:, :, 0].contiguous() for n in NAMES]
+    args[3][1] = -float("inf")
+    states = torch.randn(3, H, d, d, device=DEV)
+    clean = states.clone()
+    clean[1] = 0.0
+    want = B.ll_gdr_decode_step(*args, clean)
+    states[1, 0, :, ::3], states[1, 1] = float("nan"), float("inf")
+    o = B.ll_gdr_decode_step(*args, states)
+    assert torch.equal(o, want) and torch.equal(states, clean) and B.ll_last_device_error() == 0
