@@ -160,8 +160,8 @@ constexpr float kRowsDown = 1.f / 16.f;    // of P^T dO, as an operand
 // quarter of the columns); while warps 0 to 7 solve for M, the others prepare
 // what is needed next.  The latency of an item's chain bounds them, the solve half
 // of it: seven tiles fill the shared memory, so that no second item is in
-// work beside it.  Measured: forward 13.2 us an item and SM (178 us for 2048 items),
-// backward 28 (188 us for 1024), 3 TB/s of its own traffic.
+// work beside it.  Measured: forward 13.5 us an item and SM (183 us for 2048 items),
+// backward 29 (195 us for 1024), 2.8 TB/s of its own traffic.
 constexpr int kPrepThreads = 512, kPrepBar2 = 2;
 
 // The forward's.  Warps 8 to 15 make V's operand and, a whole item ahead, everything
@@ -723,8 +723,8 @@ enum ScanBar : int { SB_W0 = 0, SB_W1, SB_K0, SB_K1, SB_R0, SB_R1, SB_ERR, SB_BC
 // the SM's memory taken as shared memory, little is left for loads in flight
 // through L1 (72 KB of them a chunk took 4 thousand cycles to issue): the modes
 // with many rows have them copied into shared memory instead.  Measured per chunk:
-// forward 1.77 us (226 us for 128 chunks of 16 heads, 64 CTAs); with 128 CTAs,
-// for the gradient 2.3 us forwards and 3.2 backwards, whose rows and tiles, 350 and 510 KB
+// forward 1.70 us (218 us for 128 chunks of 16 heads, 64 CTAs); with 128 CTAs,
+// for the gradient 2.4 us forwards and 3.2 backwards, whose rows and tiles, 350 and 510 KB
 // a chunk and head, go at 4.8 and 5.2 TB/s.
 constexpr int kScanThreads = 512 + 32;
 constexpr int kScanBarX = 1, kScanBarE = 2, kScanBarU = 3;  // named barriers: an operand, the staged rows are ready
@@ -1214,8 +1214,8 @@ constexpr int kGradThreads = 512;
 // Persistent, one CTA per SM, an item per (chunk, key head); the value heads that
 // share it are taken in turn, dq and dk adding up in registers in a fixed order.
 // Thread = (row, quarter of the columns).  The next head's or item's tiles are
-// loaded as soon as a tile's last product is done.  Measured: 111 us for 1024 items (390 MB,
-// 3.5 TB/s; 140 with a CTA per item, whose loads nothing overlapped), bound by the
+// loaded as soon as a tile's last product is done.  Measured: 113 us for 1024 items (415 MB,
+// 3.7 TB/s; 140 with a CTA per item, whose loads nothing overlapped), bound by the
 // chain of its three rounds.  Per head three rounds of products over seven tiles of
 // shared memory:
 //   dO S, (beta w) S, u D;   dO u^T, (beta w) u^T, Q K^T;   R K, R^T Q, (N + N^T) K

@@ -201,7 +201,7 @@ constexpr float kInvUp = 64.f;
 //   Z = A21 + [M22 diag(beta)] A21,   M21 = -(Z + [Z diag(beta)] M11).
 // From 16 rows on these are products of 16-row blocks on the warp-level matrix
 // instruction, a 16 x (N / 2) piece to a warp, with both operands in two fp16 parts
-// made in registers.  A chunk takes 11 to 12 thousand cycles, half of its preparation:
+// made in registers.  A chunk takes 12 thousand cycles, half of its preparation:
 // 1.4 to the 8 x 8 pairs, then 1.5, 3.3 and 4.9 for the doublings, each a chain of loads,
 // conversions and products (two schedulers' shares of the work made equal changed
 // nothing).  The last one in float32 FMAs with 4 x 4 outputs a thread took 8 thousand
