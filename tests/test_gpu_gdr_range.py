@@ -87,6 +87,29 @@ def test_gradient_of_constant_states(B, monkeypatch, sq):
     check_bwd(B, x)
 
 
+def test_gradient_of_aligned_rows(B):
+    """The shortest keys, all one, and values of alternating sign: the rows u that every token writes
+    are 4096 in the scale of the operands, and with dout constant their product adds up over d_v:
+    128 x 15.5 x 3928."""
+    T = 300
+    x = draw(1, 2, 1, T, 128, 128, seed=57, init=False)
+    x["k"] = flat_key(T, 128, 2.0 ** -12)
+    x["beta"][:] = 0.99 * 4.0 ** 12
+    x["log_alpha"][:] = 0.0
+    sign = (1.0 - 2.0 * (torch.arange(T) % 2)).view(1, 1, T, 1)
+    x["v"] = (1.9375 * sign).expand(1, 2, T, 128).contiguous().to(torch.bfloat16)
+    x["dout"] = torch.full_like(x["dout"], 1.9375)
+    assert launches(B, x) == (3, 4)
+    check_fwd(B, x)
+    got = gpu_bwd(B, x)
+    ref = [np.zeros(got[0].shape), np.zeros(got[1].shape)]
+    for _, a, do, _, _ in base.slices(x, None):
+        r = gdr.backward(*a, do, scale=0.5)
+        ref[0][0, 0] += r["dq"]
+        ref[1][0, 0] += r["dk"]
+    assert all(rel_err(y, z, 1) <= TOL_BF16 for y, z in zip(got, ref)) and all(np.isfinite(y).all() for y in got)
+
+
 # ------------------------------------------------------------------ written rows
 @pytest.mark.parametrize("shift", [4, 8])
 def test_short_keys_with_large_gates(B, shift):
