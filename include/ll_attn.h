@@ -390,28 +390,34 @@ LL_API ll_status ll_gdn_fwd_b(const ll_shape* shape, const void* q, const void* 
  * Sequences run from given states to returned ones, can be packed end to end,
  * and several value heads can share a key head.
  *
- * Two ways of computing, chosen by types and sizes alone (ll_gdr_*_launches
- * tells which; lengths of packed sequences are not among them, and a batch of few heads
- * whose tokens are nearly all one sequence's is slow: pass that one by itself).  Token by token, every io dtype and head size: float32
- * arithmetic throughout, a state rounded once a token.  In chunks of 128 tokens on the tensor cores, bf16 io
- * with dk and dv of 64 or 128, where it is the faster: operands are scaled by
- * powers of two to fp16, in two parts (22 bits) where a state or a gate's
- * gradient depends on them, sums are float32; states, dlog_alpha and dbeta keep
- * float32 accuracy, o, dq, dk and dv that of a 16-bit operand.  beta |k|^2 <= 2
- * is expected (L2-normalised keys keep it), so that a token's transition does
- * not grow its state; not checked.  In chunks a state has room for 4096 times
- * the largest |v| and |state_in| of its sequence and head, its gradient likewise
- * for 4096 times the largest value that a chunk or dstate_out adds to it; what is
- * below 2^-28 of these counts as zero in o, dq, dk and dv.  Keys may have any length
- * from 2^-12 to 2^14 (beta small or large to match); of the keys of 128 neighbouring tokens one that is
- * not zero should have at least 2^-12 of the longest one's (largest elements compared):
- * below that accuracy falls, below 2^-16 results may be infinite.
+ * Two ways of computing, chosen by types and sizes alone (ll_gdr_*_launches tells
+ * which; lengths of packed sequences are not among them, and a batch of few heads
+ * whose tokens are nearly all one sequence's is slow: pass that one by itself).
+ * Token by token, every io dtype and head size: float32 arithmetic throughout, a
+ * state rounded once a token. In chunks of 128 tokens on the tensor cores, bf16 io
+ * with dk and dv of 64 or 128, where it is the faster: operands are scaled by powers
+ * of two to fp16, in two parts (22 bits) where a state or a gate's gradient depends
+ * on them, sums are float32; states, dlog_alpha and dbeta keep float32 accuracy, o,
+ * dq, dk and dv that of a 16-bit operand, both relative to the terms that they are
+ * sums of (a chunk whose keys repeat with beta |k|^2 near 2 sums terms that cancel:
+ * one key at 512 tokens and 1.999 leave 3e-4 of a state, where token by token it is
+ * 1e-6). beta |k|^2 <= 2 is expected (L2-normalised keys keep it), so that a token's
+ * transition does not grow its state; not checked.
+ *
+ * In chunks a state has room for 4096 times the largest |v| and |state_in| of its
+ * sequence and head, its gradient likewise for 4096 times the largest value that a
+ * chunk or dstate_out adds to it; what is below 2^-28 of these counts as zero in o,
+ * dq, dk and dv. Keys may have any length from 2^-12 to 2^14 (beta small or large to
+ * match); of the keys of 128 neighbouring tokens one that is not zero should have at
+ * least 2^-12 of the longest one's (largest elements compared): below that accuracy
+ * falls, below 2^-16 results may be infinite.
+ *
  * Infinities and NaN stay within their sequence and, in v, gates, states and
- * upstream gradients, within their head (and its key head's dq and dk).  In
+ * upstream gradients, within their head (and its key head's dq and dk). In
  * ll_gdr_fwd tokens before a bad one do not see it, but in chunks those of its own
- * chunk (tokens 128 c .. 128 c + 127 of the sequence) do; in ll_gdr_bwd a bad v reaches
- * no chunk (of 64 or 128) before its own and a bad dout none behind it.  So padding
- * behind the tokens of a row has to be finite, or left out by seq_starts.
+ * chunk (tokens 128 c .. 128 c + 127 of the sequence) do; in ll_gdr_bwd a bad v
+ * reaches no chunk (of 64 or 128) before its own and a bad dout none behind it. So
+ * padding behind the tokens of a row has to be finite, or left out by seq_starts.
  *
  * Calls allocate nothing, do not synchronise and can be captured; a workspace
  * serves one call at a time. */
@@ -489,7 +495,8 @@ LL_API int ll_gdr_bwd_launches(const ll_gdr_shape* shape);
  * over the tokens behind t of its chunk (of 64 or 128) of do.o - v.dv and the product
  * of state and adjoint at the chunk's end, and is as accurate as these: where a head
  * forgets within a few tokens they cancel (a mean log_alpha of -4: 7e-6 of its norm
- * token by token, 2e-5 in chunks; of -12: 2e-5 and 1e-4).  Where alpha is zero in float32 (log_alpha < -104) it is zero.
+ * token by token, 2e-5 in chunks; of -12: 2e-5 and 1e-4).  Where alpha is zero in
+ * float32 (log_alpha < -104) it is zero.
  * Rows outside every sequence are not written.  No output may overlap an input
  * or another output, but dstate_in may be dstate_out itself. */
 LL_API ll_status ll_gdr_bwd(const ll_gdr_shape* shape, const int32_t* seq_starts, const void* q, const void* k,
