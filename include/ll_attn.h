@@ -37,6 +37,14 @@
  *                        no delta-rule equations, the standard ones are stated at
  *                        the declarations): chunk-wise forward from and to states,
  *                        its gradient, one token of decoding.
+ *   ll_la_fwd, ll_la_bwd, ll_la_decode_step
+ *                        linear attention with one decayed state per head, the base
+ *                        model of ll_attn_* (study note §3-5 builds Log-Linear Mamba-2
+ *                        on its mask M^S): forward from and to states, its gradient,
+ *                        one token of decoding.
+ *   ll_rope_fwd, ll_rope_bwd, ll_rope_freqs
+ *                        rotary positions of queries and keys, for any of the above
+ *                        (ll_la_decode_step applies them itself); not on the pages.
  *   ll_attn_fwd_level_decay, ll_attn_decode_step_level_decay
  *                        the forward and the decode step with one decay per level
  *                        (study note §7 "Follow-up design" names a learned memory
@@ -521,6 +529,154 @@ LL_API ll_status ll_gdr_decode_step(int B, int H, int Hk, int dk, int dv, ll_dty
                                     const int64_t* slots, int n_slots, const void* q, const void* k,
                                     const void* v, const float* log_alpha, const float* beta, float* states,
                                     void* o, void* stream);
+
+/* ---- rotary positions ----
+ * Pairs (a, b) of the first `rot` elements of a head become
+ *   (a', b') = amp (a cos x - b sin x, a sin x + b cos x),   x = position inv_freq[i],
+ * i the pair's number; the other elements stay as they are.  x is taken modulo a turn
+ * in integers, exact to 2^-31 of a turn at any position of up to 2^40. */
+
+/*   rot          rotated elements of a head, even, 2 .. the head dim
+ *   interleaved  0: pair i is elements i and i + rot/2;  1: elements 2i and 2i + 1
+ *   amp          factor of the rotated elements (1, or the factor that a scaling for
+ *                long contexts asks for)
+ *   inv_freq     [rot/2] float32, DEVICE, radians per position                    */
+typedef struct {
+  int rot, interleaved;
+  float amp;
+  const float* inv_freq;
+} ll_rope;
+
+/* Writes inv_freq[rot/2] (HOST memory; no GPU is used):
+ *   theta_i = base^(-2i/rot), scaled for contexts `factor` times as long as the
+ *   model was trained on (1: not at all).  length = 0: all are divided by factor.
+ *   length > 0, the trained context: a frequency that makes at least fast_turns turns
+ *   within it is kept, one that makes at most slow_turns is divided by factor, and
+ *   those between go from one to the other in proportion to their turns.
+ * rot <= 128, base > 1, factor >= 1, 0 <= slow_turns < fast_turns. */
+LL_API ll_status ll_rope_freqs(int rot, double base, double factor, double length, double slow_turns,
+                               double fast_turns, float* inv_freq);
+
+/* Rotates queries and (k not NULL) keys, in one launch.
+ *   q, q_out   [B,H,T,d]   io dtype;  k, k_out [B,Hk,T,d] io dtype or both NULL (Hk = 0)
+ *   positions  [B,T] int64, any sign; NULL: 0 .. T-1 in every row
+ *   d          head dim, one of {16, 32, 64, 128}
+ * Computed in float32, rounded once.  q_out may be q and k_out may be k; no other
+ * overlap is allowed (LL_ERR_INVALID_ARG). */
+LL_API ll_status ll_rope_fwd(int B, int H, int Hk, int T, int d, ll_dtype io, const ll_rope* rope,
+                             const int64_t* positions, const void* q, const void* k, void* q_out, void* k_out,
+                             void* stream);
+
+/* Backward of ll_rope_fwd: dq [B,H,T,d] and dk [B,Hk,T,d] from the gradients of
+ * q_out and k_out (the transposed rotation, amp included).  Arguments as there. */
+LL_API ll_status ll_rope_bwd(int B, int H, int Hk, int T, int d, ll_dtype io, const ll_rope* rope,
+                             const int64_t* positions, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                             void* stream);
+
+/* ---- linear attention with a decay per head (one state per head) ----
+ *   S_t = alpha_t S_{t-1} + v_t k_t^T     S_t [dv,dk]
+ *   o_t = scale S_t q_t
+ * the base model of the log-linear attention above: ll_attn_fwd with every lambda 1
+ * computes the same o.  The decay is given per token (log_alpha [B,H,T], as there) or,
+ * constant, per head ([H]).  Sequences run from given states to returned ones, can be
+ * packed end to end, and several value heads can share a query/key head; states have the
+ * layout of ll_gdr_*'s.
+ *
+ * States, their gradients and dlog_alpha keep float32 accuracy relative to the terms
+ * that they are sums of; o, dq, dk and dv that of their type.
+ *
+ * Infinities and NaN stay within their sequence and head (and its key head's dq and dk).
+ * log_alpha <= 0 is expected; -inf forgets the state, if that is finite.  Larger values
+ * are computed as given and may overflow.
+ *
+ * Calls allocate nothing, do not synchronise and can be captured; a workspace
+ * serves one call at a time. */
+
+/* Problem shape of ll_la_fwd and ll_la_bwd.
+ *   B, T      batch rows and tokens per row (>= 1; T below 2^31 - 1024)
+ *   H, Hk     value heads and query/key heads, H a multiple of Hk: value head
+ *             h reads query/key head h / (H / Hk)
+ *   dk, dv    key / value head dims, each in {16, 32, 64, 128}
+ *   n_seqs    0: every batch row is one sequence of T tokens.
+ *             n >= 1 (B == 1): n sequences packed along the row, sequence i
+ *             the tokens seq_starts[i] .. seq_starts[i+1] - 1 (may be empty)
+ *   per_head  0: log_alpha is [B,H,T]; 1: it is [H]
+ *   scale     factor of the output
+ *   io        dtype of q, k, v, o and their gradients; log_alpha and the states
+ *             are always float32                                              */
+typedef struct {
+  int B, H, Hk, T, dk, dv, n_seqs, per_head;
+  float scale;
+  ll_dtype io;
+} ll_la_shape;
+
+/* Bytes of workspace ll_la_fwd needs (0 when it needs none, or on an invalid shape). */
+LL_API size_t ll_la_fwd_workspace_size(const ll_la_shape* shape);
+
+/* Kernel launches of one ll_la_fwd call; 0 on an invalid shape. */
+LL_API int ll_la_fwd_launches(const ll_la_shape* shape);
+
+/* Forward over whole sequences.
+ *   seq_starts [n_seqs+1]  int32, required iff n_seqs > 0: non-decreasing, within
+ *              0 .. T.  Tokens outside every sequence are neither read nor
+ *              written.  Starts that break this set the device error word
+ *              (LL_ERR_DEVICE); what the call then leaves in its outputs is unspecified
+ *              for every sequence (nothing outside of them is touched).
+ *   q, k       [B,Hk,T,dk]  io dtype;   v, o [B,H,T,dv] io dtype
+ *   log_alpha  [B,H,T] or [H] float32
+ *   state_in   [N,H,dv,dk]  float32 or NULL (zero states), N = n_seqs or B
+ *   state_out  [N,H,dv,dk]  float32 or NULL: the states after the last token
+ *              (state_in's for an empty sequence).  May be state_in itself.
+ *   workspace  >= ll_la_fwd_workspace_size(shape) bytes, 256-byte aligned
+ *              (NULL when that is 0)
+ * o and state_out may not overlap the inputs (but state_out = state_in) or
+ * one another (LL_ERR_INVALID_ARG). */
+LL_API ll_status ll_la_fwd(const ll_la_shape* shape, const int32_t* seq_starts, const void* q, const void* k,
+                           const void* v, const float* log_alpha, const float* state_in, void* o, float* state_out,
+                           void* workspace, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace ll_la_bwd needs (0 on an invalid shape). */
+LL_API size_t ll_la_bwd_workspace_size(const ll_la_shape* shape);
+
+/* Kernel launches of one ll_la_bwd call at most; 0 on an invalid shape. */
+LL_API int ll_la_bwd_launches(const ll_la_shape* shape);
+
+/* Backward of ll_la_fwd: for f = sum(o . dout) + sum(state_out . dstate_out)
+ * writes the exact gradients of q, k, v, log_alpha and state_in.
+ *   seq_starts, q, k, v, log_alpha, state_in   the forward's inputs
+ *   dout       [B,H,T,dv]  io dtype
+ *   dstate_out [N,H,dv,dk] float32 or NULL (zero)
+ *   dq, dk     [B,Hk,T,dk] io dtype, written: summed over the value heads that
+ *              share the key head, rounded once
+ *   dv         [B,H,T,dv]  io dtype, written
+ *   dlog_alpha [B,H,T] float32, written; of log_alpha [H]: [H], the sum over every
+ *              sequence's tokens, in a fixed order.  Where alpha is zero in float32
+ *              (log_alpha < -104) a token's is zero.
+ *   dstate_in  [N,H,dv,dk] float32 or NULL, written
+ *   workspace  >= ll_la_bwd_workspace_size(shape) bytes, 256-byte aligned
+ * Rows outside every sequence are not written.  No output may overlap an input
+ * or another output, but dstate_in may be dstate_out itself. */
+LL_API ll_status ll_la_bwd(const ll_la_shape* shape, const int32_t* seq_starts, const void* q, const void* k,
+                           const void* v, const float* log_alpha, const float* state_in, const void* dout,
+                           const float* dstate_out, void* dq, void* dk, void* dv, float* dlog_alpha, float* dstate_in,
+                           void* workspace, size_t ws_bytes, void* stream);
+
+/* One decode step for every batch row.
+ *   B, H, Hk, dk, dv, io, per_head, scale: as ll_la_shape
+ *   slots, n_slots  as ll_gdr_decode_step: row b's state is states[slots[b]] (slots
+ *           NULL: states[b]), -1 a row of padding that is left as it is; any other
+ *           slot outside 0 .. n_slots-1, and one that two rows name, sets the device
+ *           error word (LL_ERR_DEVICE)
+ *   rope, positions [B] int64: queries and keys are turned to their position on the
+ *           way, in float32 and not rounded in between (rope->rot <= dk); both NULL: not
+ *   q, k    [B,Hk,dk] io dtype;   v, o [B,H,dv] io dtype
+ *   log_alpha [B,H] float32 or, per_head, [H] (-inf forgets the state whatever it
+ *           holds, so that a slot can be handed on without being cleared)
+ *   states  [n_slots,H,dv,dk] float32, in/out, each named state read and written once */
+LL_API ll_status ll_la_decode_step(int B, int H, int Hk, int dk, int dv, ll_dtype io, int per_head, float scale,
+                                   const int64_t* slots, int n_slots, const ll_rope* rope, const int64_t* positions,
+                                   const void* q, const void* k, const void* v, const float* log_alpha, float* states,
+                                   void* o, void* stream);
 
 #ifdef __cplusplus
 }

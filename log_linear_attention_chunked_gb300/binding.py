@@ -30,6 +30,8 @@ SYMBOLS = ("ll_version", "ll_status_str", "ll_last_device_error", "ll_attn_fwd_w
            "ll_attn_fwd_level_decay_workspace_size", "ll_attn_fwd_level_decay_launches", "ll_attn_fwd_level_decay",
            "ll_attn_decode_step_level_decay", "ll_gdr_fwd_workspace_size", "ll_gdr_fwd_launches", "ll_gdr_fwd",
            "ll_gdr_bwd_workspace_size", "ll_gdr_bwd_launches", "ll_gdr_bwd", "ll_gdr_decode_step",
+           "ll_rope_freqs", "ll_rope_fwd", "ll_rope_bwd", "ll_la_fwd_workspace_size", "ll_la_fwd_launches", "ll_la_fwd",
+           "ll_la_bwd_workspace_size", "ll_la_bwd_launches", "ll_la_bwd", "ll_la_decode_step",
            # test hooks (include/ll_attn_test.h)
            "ll_test_fwd_withhold_node")
 
@@ -50,6 +52,17 @@ class ll_gdr_shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("Hk", ctypes.c_int), ("T", ctypes.c_int),
                 ("dk", ctypes.c_int), ("dv", ctypes.c_int), ("n_seqs", ctypes.c_int), ("scale", ctypes.c_float),
                 ("io", ctypes.c_int)]
+
+
+class ll_la_shape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("Hk", ctypes.c_int), ("T", ctypes.c_int),
+                ("dk", ctypes.c_int), ("dv", ctypes.c_int), ("n_seqs", ctypes.c_int), ("per_head", ctypes.c_int),
+                ("scale", ctypes.c_float), ("io", ctypes.c_int)]
+
+
+class ll_rope(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int), ("interleaved", ctypes.c_int), ("amp", ctypes.c_float),
+                ("inv_freq", ctypes.c_void_p)]
 
 
 _lib = None
@@ -124,6 +137,25 @@ def lib() -> ctypes.CDLL:
     L.ll_gdr_decode_step.restype = i32
     L.ll_gdr_decode_step.argtypes = [i32, i32, i32, i32, i32, i32, ctypes.c_float, vp, i32, vp, vp, vp, fp, fp, fp,
                                      vp, vp]
+    dbl = ctypes.c_double
+    L.ll_rope_freqs.restype = i32
+    L.ll_rope_freqs.argtypes = [i32, dbl, dbl, dbl, dbl, dbl, vp]
+    for n in ("ll_rope_fwd", "ll_rope_bwd"):
+        getattr(L, n).restype = i32
+        getattr(L, n).argtypes = [i32] * 6 + [ctypes.POINTER(ll_rope)] + [vp] * 6
+    lshp = ctypes.POINTER(ll_la_shape)
+    for n in ("ll_la_fwd_workspace_size", "ll_la_bwd_workspace_size"):
+        getattr(L, n).restype = sz
+        getattr(L, n).argtypes = [lshp]
+    for n in ("ll_la_fwd_launches", "ll_la_bwd_launches"):
+        getattr(L, n).restype = i32
+        getattr(L, n).argtypes = [lshp]
+    L.ll_la_fwd.restype = i32
+    L.ll_la_fwd.argtypes = [lshp] + [vp] * 9 + [sz, vp]
+    L.ll_la_bwd.restype = i32
+    L.ll_la_bwd.argtypes = [lshp] + [vp] * 14 + [sz, vp]
+    L.ll_la_decode_step.restype = i32
+    L.ll_la_decode_step.argtypes = [i32] * 7 + [ctypes.c_float, vp, i32, ctypes.POINTER(ll_rope)] + [vp] * 8
     L.ll_test_fwd_withhold_node.restype = i32
     L.ll_test_fwd_withhold_node.argtypes = [shp, vp, vp, vp, fp, fp, vp, vp, sz, ctypes.c_longlong,
                                             ctypes.c_ulonglong, vp]
@@ -616,6 +648,200 @@ def ll_gdr_decode_step(q, k, v, log_alpha, beta, states, *, scale=1.0, slots=Non
     _launch("ll_gdr_decode_step", dev, B, H, Hk, dk, dv, io, float(scale), _addr(slots), n, _addr(q), _addr(k),
             _addr(v), _addr(log_alpha), _addr(beta), _addr(states), _addr(o))
     return o
+
+
+def make_la_shape(B, H, Hk, T, dk, dv, n_seqs=0, scale=1.0, io=LL_BF16, per_head=False) -> ll_la_shape:
+    _int32(B, H, Hk, T, dk, dv, n_seqs)
+    return ll_la_shape(B, H, Hk, T, dk, dv, n_seqs, 1 if per_head else 0, scale, io)
+
+
+def ll_la_fwd_workspace_size(shape: ll_la_shape) -> int:
+    return int(lib().ll_la_fwd_workspace_size(ctypes.byref(shape)))
+
+
+def ll_la_fwd_launches(shape: ll_la_shape) -> int:
+    return int(lib().ll_la_fwd_launches(ctypes.byref(shape)))
+
+
+def ll_la_bwd_workspace_size(shape: ll_la_shape) -> int:
+    return int(lib().ll_la_bwd_workspace_size(ctypes.byref(shape)))
+
+
+def ll_la_bwd_launches(shape: ll_la_shape) -> int:
+    return int(lib().ll_la_bwd_launches(ctypes.byref(shape)))
+
+
+def _la_shape(q, k, v, log_alpha, scale, seq_starts):
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q and v must be [B,Hk,T,dk] and [B,H,T,dv]")
+    B, Hk, T, dk = q.shape
+    H, dv = v.shape[1], v.shape[3]
+    _need(q, "q")
+    dev = q.device
+    io = _io(q.dtype)
+    _need_like(k, "k", q.shape, q.dtype, dev)
+    _need_like(v, "v", (B, H, T, dv), q.dtype, dev)
+    per_head = log_alpha.dim() == 1
+    _need_like(log_alpha, "log_alpha", (H,) if per_head else (B, H, T), torch.float32, dev)
+    n = 0
+    if seq_starts is not None:
+        n = seq_starts.numel() - 1
+        if n < 1:
+            raise ValueError("seq_starts must have at least two entries")
+        _need_like(seq_starts, "seq_starts", (n + 1,), torch.int32, dev)
+    return make_la_shape(B, H, Hk, T, dk, dv, n, float(scale), io, per_head), (n or B, H, dv, dk)
+
+
+def ll_la_fwd(q, k, v, log_alpha, *, scale=1.0, state_in=None, state_out=None, seq_starts=None, o=None, workspace=None):
+    """Linear attention with a decay per head over whole sequences.  q, k
+    [B,Hk,T,dk]; v [B,H,T,dv] (f32 or bf16; H a multiple of Hk); log_alpha [B,H,T]
+    or, constant, [H] float32.  state_in / state_out [N,H,dv,dk] float32 (N =
+    sequences): the states before and after, optional; state_out may be state_in.
+    seq_starts [n+1] int32 packs n sequences along the tokens (B = 1).  Returns o
+    [B,H,T,dv]; rows outside every packed sequence are left as they are."""
+    shape, states = _la_shape(q, k, v, log_alpha, scale, seq_starts)
+    for x, n in ((state_in, "state_in"), (state_out, "state_out")):
+        if x is not None:
+            _need_like(x, n, states, torch.float32, q.device)
+    if o is None:
+        o = torch.empty_like(v)
+    else:
+        _need_like(o, "o", v.shape, q.dtype, q.device)
+    ws = _gdr_workspace(workspace, ll_la_fwd_workspace_size(shape), q.device)
+    _launch("ll_la_fwd", q.device, ctypes.byref(shape), _addr(seq_starts), _addr(q), _addr(k), _addr(v),
+            _addr(log_alpha), _addr(state_in), _addr(o), _addr(state_out), _addr(ws), 0 if ws is None else ws.numel())
+    return o
+
+
+def ll_la_bwd(q, k, v, log_alpha, dout, *, scale=1.0, state_in=None, dstate_out=None, seq_starts=None, grads=None,
+              dstate_in=None, workspace=None):
+    """Backward of ll_la_fwd for the gradients dout [B,H,T,dv] of o and (optional)
+    dstate_out of state_out.  Returns (dq, dk, dv, dlog_alpha), with dq and dk summed
+    over the value heads of a key head and dlog_alpha of log_alpha's shape; ``grads``
+    may pass those four to be written in place, dstate_in [N,H,dv,dk] receives
+    state_in's gradient (it may be dstate_out)."""
+    shape, states = _la_shape(q, k, v, log_alpha, scale, seq_starts)
+    _need_like(dout, "dout", v.shape, q.dtype, q.device)
+    for x, n in ((state_in, "state_in"), (dstate_out, "dstate_out"), (dstate_in, "dstate_in")):
+        if x is not None:
+            _need_like(x, n, states, torch.float32, q.device)
+    if grads is None:
+        grads = tuple(torch.empty_like(x) for x in (q, k, v, log_alpha))
+    else:
+        for x, ref, n in zip(grads, (q, k, v, log_alpha), ("dq", "dk", "dv", "dlog_alpha"), strict=True):
+            _need_like(x, n, ref.shape, ref.dtype, q.device)
+    ws = _gdr_workspace(workspace, ll_la_bwd_workspace_size(shape), q.device)
+    _launch("ll_la_bwd", q.device, ctypes.byref(shape), _addr(seq_starts), _addr(q), _addr(k), _addr(v),
+            _addr(log_alpha), _addr(state_in), _addr(dout), _addr(dstate_out), *[_addr(x) for x in grads],
+            _addr(dstate_in), _addr(ws), 0 if ws is None else ws.numel())
+    return tuple(grads)
+
+
+def _rope_spec(inv_freq, interleaved, amp, device) -> ll_rope:
+    _need_like(inv_freq, "inv_freq", (inv_freq.numel(),), torch.float32, device)
+    return ll_rope(2 * inv_freq.numel(), 1 if interleaved else 0, float(amp), inv_freq.data_ptr())
+
+
+def ll_la_decode_step(q, k, v, log_alpha, states, *, scale=1.0, slots=None, inv_freq=None, positions=None,
+                      interleaved=False, amp=1.0, o=None):
+    """One decode step.  q, k [B,Hk,dk]; v [B,H,dv]; log_alpha [B,H] or [H]
+    float32; states [n_slots,H,dv,dk] float32, updated in place.  Row b uses
+    states[slots[b]] (slots [B] int64, distinct; -1 = a row of padding, left as it
+    is) or states[b].  With inv_freq [rot/2] and positions [B] int64, queries and keys
+    are turned as ll_rope_fwd does, without a rounding in between.  Returns o [B,H,dv]."""
+    if q.dim() != 3 or v.dim() != 3 or states.dim() != 4:
+        raise ValueError("q, v and states must be [B,Hk,dk], [B,H,dv] and [n_slots,H,dv,dk]")
+    B, Hk, dk = q.shape
+    H, dv = v.shape[1], v.shape[2]
+    _need(q, "q")
+    dev = q.device
+    io = _io(q.dtype)
+    _need_like(k, "k", q.shape, q.dtype, dev)
+    _need_like(v, "v", (B, H, dv), q.dtype, dev)
+    per_head = log_alpha.dim() == 1
+    _need_like(log_alpha, "log_alpha", (H,) if per_head else (B, H), torch.float32, dev)
+    n = states.shape[0]
+    _int32(B, H, Hk, n)
+    _need_like(states, "states", (n, H, dv, dk), torch.float32, dev)
+    if slots is not None:
+        _need_like(slots, "slots", (B,), torch.int64, dev)
+    if (inv_freq is None) != (positions is None):
+        raise ValueError("inv_freq and positions come together")
+    rope = None
+    if inv_freq is not None:
+        rope = ctypes.byref(_rope_spec(inv_freq, interleaved, amp, dev))
+        _need_like(positions, "positions", (B,), torch.int64, dev)
+    if o is None:
+        o = torch.empty_like(v)
+    else:
+        _need_like(o, "o", v.shape, q.dtype, dev)
+    _launch("ll_la_decode_step", dev, B, H, Hk, dk, dv, io, 1 if per_head else 0, float(scale), _addr(slots), n, rope,
+            _addr(positions), _addr(q), _addr(k), _addr(v), _addr(log_alpha), _addr(states), _addr(o))
+    return o
+
+
+def ll_rope_freqs(rot: int, base: float = 10000.0, *, factor: float = 1.0, length: float = 0.0,
+                  slow_turns: float = 1.0, fast_turns: float = 32.0, device=None) -> torch.Tensor:
+    """inv_freq [rot/2] float32 of rotary positions: base^(-2i/rot), scaled for
+    contexts ``factor`` times as long: all divided by it, or (length: the trained
+    context) only those that turn at most slow_turns times within length, with a ramp
+    to those that turn fast_turns times and stay."""
+    _int32(rot)
+    out = torch.empty(max(rot // 2, 0), dtype=torch.float32)
+    _check(lib().ll_rope_freqs(rot, float(base), float(factor), float(length), float(slow_turns), float(fast_turns),
+                               out.data_ptr() or None), "ll_rope_freqs")
+    return out if device is None else out.to(device)
+
+
+def _rope(entry, q, k, inv_freq, positions, interleaved, amp, q_out, k_out):
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [B,H,T,d] or [B,H,d]")
+    B, H, d = q.shape[0], q.shape[1], q.shape[-1]
+    T = q.shape[2] if q.dim() == 4 else 1
+    _need(q, "q")
+    dev = q.device
+    io = _io(q.dtype)
+    Hk = 0
+    if k is not None:
+        if k.dim() != q.dim():
+            raise ValueError("k must have as many dimensions as q")
+        Hk = k.shape[1]
+        _need_like(k, "k", (B, Hk, *q.shape[2:]), q.dtype, dev)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _int32(B, H, Hk, T, d)
+    spec = _rope_spec(inv_freq, interleaved, amp, dev)
+    if positions is not None:
+        _need_like(positions, "positions", (B, T) if q.dim() == 4 else (B,), torch.int64, dev)
+    elif q.dim() == 3:
+        raise ValueError("single tokens need their positions")
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    else:
+        _need_like(q_out, "q_out", q.shape, q.dtype, dev)
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty_like(k)
+        else:
+            _need_like(k_out, "k_out", k.shape, q.dtype, dev)
+    _launch(entry, dev, B, H, Hk, T, d, io, ctypes.byref(spec), _addr(positions), _addr(q), _addr(k), _addr(q_out),
+            _addr(k_out))
+    return q_out if k is None else (q_out, k_out)
+
+
+def ll_rope_fwd(q, k, inv_freq, *, positions=None, interleaved=False, amp=1.0, q_out=None, k_out=None):
+    """Rotary positions of queries q [B,H,T,d] (or [B,H,d], single tokens) and keys
+    k [B,Hk,T,d] (or None), f32 or bf16.  inv_freq [rot/2] float32, rot <= d: the first
+    rot elements are turned, as pairs (i, i + rot/2) or, interleaved, (2i, 2i + 1), and
+    multiplied by amp.  positions [B,T] (or [B]) int64; None: 0 .. T-1.  q_out may be q
+    and k_out may be k.  Returns q_out, or (q_out, k_out) with keys."""
+    return _rope("ll_rope_fwd", q, k, inv_freq, positions, interleaved, amp, q_out, k_out)
+
+
+def ll_rope_bwd(dq_out, dk_out, inv_freq, *, positions=None, interleaved=False, amp=1.0, dq=None, dk=None):
+    """Backward of ll_rope_fwd: the gradients of q and k from those of q_out and
+    k_out.  Arguments as there.  Returns dq, or (dq, dk) with keys."""
+    return _rope("ll_rope_bwd", dq_out, dk_out, inv_freq, positions, interleaved, amp, dq, dk)
 
 
 def ll_test_fwd_withhold_node(q, k, v, log_alpha, lam, chunk: int, node: int, timeout_ns: int, *, o=None,

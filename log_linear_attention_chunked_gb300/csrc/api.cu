@@ -29,8 +29,6 @@ unsigned* err_word() {
   return addr[dev];
 }
 
-static bool head_dim_ok(int d) { return is_pow2_in(d, 16, 128); }
-
 // Shape checks shared by the forward entry points.
 static ll_status check_shape(const ll_shape* s) {
   if (!s) return LL_ERR_INVALID_ARG;
@@ -617,18 +615,6 @@ static GdrArgs gdr_args(const ll_gdr_shape* s) {
   a.scale = s->scale;
   return a;
 }
-
-namespace {
-struct Range {
-  const void* p;
-  size_t n;
-};
-bool ranges_overlap(const Range& a, const Range& b) {
-  if (!a.p || !b.p) return false;
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return x < y + b.n && y < x + a.n;
-}
-}  // namespace
 
 extern "C" {
 

@@ -47,7 +47,20 @@ inline int levels_needed(int T) {
   return b + 1;
 }
 
+inline bool head_dim_ok(int d) { return is_pow2_in(d, 16, 128); }
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// `n` bytes from `p` (null: nothing)
+struct Range {
+  const void* p;
+  size_t n;
+};
+inline bool ranges_overlap(const Range& a, const Range& b) {
+  if (!a.p || !b.p) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x < y + b.n && y < x + a.n;
+}
 
 #define LL_CUDA_OK(expr)                          \
   do {                                            \

@@ -1,0 +1,159 @@
+// Linear attention with a decay per head: shared declarations of its kernels.
+//
+//   S_t = alpha_t S_{t-1} + v_t k_t^T,   o_t = scale S_t q_t
+// and, with A_t the gradient of S_t by everything behind token t,
+//   A_t = alpha_{t+1} A_{t+1} + scale do_t q_t^T,
+//   dq_t = scale S_t^T do_t,  dk_t = A_t^T v_t,  dv_t = A_t k_t,
+//   dlog_alpha_t = alpha_t <S_{t-1}, A_t>.
+//
+// The recurrence is linear, so a sequence is cut into segments that are worked
+// on side by side: what a segment adds to the state behind it (its sum) comes
+// first, a short pass along the segments turns the sums into the states on
+// entry, and then every segment runs with its own.  Segments are dealt by slot
+// in the way of the gated delta rule's chunks (gdr.cuh), a segment in the place
+// of a chunk.
+//
+// A decay's logarithm in a segment is summed in float32 over at most a tile or
+// chunk of tokens at a time.
+#pragma once
+
+#include "gdr.cuh"
+
+namespace llattn {
+
+struct LaArgs {
+  int B, H, Hk, T, dk, dv, n_seqs;  // n_seqs = 0: unpacked
+  ll_dtype io;
+  int per_head;  // log_alpha is [H], else [B,H,T]
+  float scale;
+  const int32_t* seq_starts;
+  const void *q, *k, *v;
+  const float *log_alpha, *state_in;
+  // forward
+  void* o;
+  float* state_out;
+  // backward
+  const void* dout;
+  const float* dstate_out;
+  void *dq, *dkey, *dval;
+  float *dlog_alpha, *dstate_in;
+  void* ws;
+  size_t ws_bytes;
+  cudaStream_t stream;
+  unsigned* err;
+};
+
+inline int la_sequences(const LaArgs& a) { return a.n_seqs ? a.n_seqs : a.B; }
+inline GdrSeqs la_seqs(const LaArgs& a) {
+  return GdrSeqs{a.n_seqs ? a.seq_starts : nullptr, la_sequences(a), a.T, a.H, a.Hk};
+}
+inline size_t la_slots(const LaArgs& a, int seg) {
+  return a.n_seqs ? (size_t)(a.T / seg) + a.n_seqs : (size_t)a.B * (((size_t)a.T + seg - 1) / seg);
+}
+// Can a sequence have more than one segment?
+inline bool la_split(const LaArgs& a, int seg) { return a.T > seg; }
+
+// The segment of slot `c`: its sequence, number within it, first row and length;
+// `seq_len` that of the sequence (0: nothing of it but its state, on its first
+// slot).  False when no valid segment owns the slot.
+struct LaSegment {
+  int seq, num, row_b, start, n, seq_len;
+};
+__device__ __forceinline__ bool la_find(const GdrSeqs& s, int c, int seg, LaSegment& r, unsigned* err) {
+  GdrSeq q;
+  if (!s.starts) {
+    const int per = (s.T + seg - 1) / seg;
+    r.seq = c / per;
+    r.num = c - r.seq * per;
+    q = GdrSeq{r.seq, 0, s.T};
+  } else {
+    int lo = 0, hi = s.n - 1;  // the last sequence with base <= c
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s.starts[mid] / seg + mid <= c) lo = mid;
+      else hi = mid - 1;
+    }
+    if (!gdr_seq(s, lo, q)) {
+      if (err && threadIdx.x == 0) raise_error(err, kErrDeviceArg);
+      return false;
+    }
+    r.seq = lo;
+    r.num = c - (q.start / seg + lo);
+    if (r.num < 0) return false;
+  }
+  const long long at = (long long)r.num * seg;
+  r.row_b = q.row_b;
+  r.seq_len = q.len;
+  r.start = q.start + (int)(at < q.len ? at : 0);
+  r.n = at < q.len ? (int)(q.len - at < seg ? q.len - at : seg) : 0;
+  return r.n > 0 || r.num == 0;
+}
+
+// What an element of a state is multiplied by over some tokens of log decay g:
+// near 1 as x + expm1(g) x, since a rounded factor applied again and again adds up.
+struct LaDecay {
+  float f;
+  bool near;
+};
+__device__ __forceinline__ LaDecay la_decay(float g) {
+  const bool near = g > -0.5f;
+  return LaDecay{near ? expm1f(g) : expf(g), near};
+}
+__device__ __forceinline__ float la_apply(const LaDecay& d, float x) { return d.near ? fmaf(d.f, x, x) : d.f * x; }
+
+// ---- launchers
+size_t la_fwd_workspace(const LaArgs& a);
+ll_status la_fwd_launch(const LaArgs& a);
+int la_fwd_launches(const LaArgs& a);
+size_t la_bwd_workspace(const LaArgs& a);
+ll_status la_bwd_launch(const LaArgs& a);
+int la_bwd_launches(const LaArgs& a);
+
+// the states on entry to every segment from the sums of the segments (la_rec.cu)
+struct LaCarry {
+  GdrSeqs seqs;
+  int seg, elems;                        // tokens of a segment, elements of a state
+  float* sums[2];                        // [slot, H, elems]: forwards, backwards (null: not wanted); in place
+  const float* log_decay;                // [slot, H]
+  const float* init[2];                  // [sequence, H, elems] or null
+  float* last[2];                        // what leaves the last (backwards the first) segment, or null
+  unsigned* err;
+};
+ll_status la_carry_launch(const LaCarry& c, int sequences, cudaStream_t stream);
+
+struct LaRope {
+  int rot, interleaved;
+  const float* inv_freq;
+  float amp;
+};
+struct LaStepArgs {
+  int B, H, Hk, dk, dv;
+  ll_dtype io;
+  int per_head;
+  float scale;
+  const int64_t* slots;
+  int n_slots;
+  const void *q, *k, *v;
+  const float *log_alpha;
+  float* states;
+  LaRope rope;  // rot = 0: none
+  const int64_t* positions;
+  void* o;
+  cudaStream_t stream;
+  unsigned* err;
+};
+ll_status la_step_launch(const LaStepArgs& a);
+
+struct RopeArgs {
+  int B, H, Hk, T, d;
+  ll_dtype io;
+  LaRope rope;
+  const int64_t* positions;  // [B,T] or null: 0 .. T-1
+  const void *q, *k;
+  void *q_out, *k_out;
+  bool back;
+  cudaStream_t stream;
+};
+ll_status rope_launch(const RopeArgs& a);
+
+}  // namespace llattn

@@ -1,0 +1,799 @@
+// Linear attention with a decay per head token by token, states in registers:
+// every type and head size, float32 arithmetic throughout.
+//
+// The forward and all three gradients are the same recurrence over a matrix M
+// [rows, columns] with different roles,
+//   M_t = a_t M_{t-1} + y_t z_t^T,   out_t = f M_t x_t:
+//   o    rows d_v   y = v         z = k    x = q    forwards
+//   dq   rows d_k   y = k         z = v    x = do   forwards
+//   dk   rows d_k   y = scale q   z = do   x = v    backwards
+//   dv   rows d_v   y = scale do  z = q    x = k    backwards
+// and a row needs no other row.  A group of kLpr lanes holds kRt rows (kEpl elements
+// of each a lane), a CTA a block of rows of one (segment, head).  An element takes
+// three operations a token (decay, dot product with the decayed row, update), on
+// pairs of floats, and these bound it; M_t x_t is a M_{t-1} x_t + y_t (z_t . x_t) with the
+// scalar products z . x made once per staged tile, which keeps the update out of the
+// sum's chain, and gives the part of the sum that lies before token t by itself:
+// that is what the decay's gradient is made of,
+//   dlog_alpha_t = sum_{s >= t} q_s.dq'_s - sum_{j >= t} k_j.dk'_j + <S, B>,
+// over the tokens of the segment, the primes leaving out a token's own pair, S and B the
+// state and its gradient at the segment's end.  Sums over the lanes are taken for kLpr
+// tokens at once: each step of a butterfly halves the values that a lane carries.
+//
+// alpha_t is rounded to float32 once a token; what the roundings so far are off by
+// is taken out of the next one near 1, so that those of a constant decay do not add up.
+#include <algorithm>
+
+#include "la.cuh"
+#include "sm100.cuh"
+
+namespace llattn {
+namespace {
+
+using sm100::cp_async16;
+using sm100::cp_async_commit;
+using sm100::cp_async_wait;
+
+constexpr int kTile = 16;  // tokens staged at a time
+constexpr int kMaxThreads = 128;
+
+template <int NC> struct Cfg {
+  static constexpr int kEpl = NC >= 64 ? 16 : 8;     // elements of a row in a lane
+  static constexpr int kLpr = NC / kEpl;             // lanes per row
+  static constexpr int kRt = NC >= 64 ? 2 : 1;       // rows per lane
+  static constexpr int kMaxRows = kMaxThreads / kLpr * kRt;
+  static constexpr int kPieces = kEpl / 4;
+};
+// threads and rows of a CTA for `rows` rows in all
+template <int NC> int threads_for(int rows) {
+  const int t = rows / Cfg<NC>::kRt * Cfg<NC>::kLpr;
+  return std::min(kMaxThreads, (t + 31) / 32 * 32);
+}
+template <int NC> int rows_for(int rows) { return threads_for<NC>(rows) / Cfg<NC>::kLpr * Cfg<NC>::kRt; }
+int row_blocks(int rows, int cols) {
+  const int r = cols == 128 ? rows_for<128>(rows) : cols == 64 ? rows_for<64>(rows) : cols == 32 ? rows_for<32>(rows)
+                                                                                             : rows_for<16>(rows);
+  return (rows + r - 1) / r;
+}
+
+// ---- pairs of floats
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pair(float x, float y) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(f2 a) {
+  float x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a));
+  return make_float2(x, y);
+}
+
+struct RecJob {
+  const void *y, *z, *x, *w;  // w: rows of the scalar products behind `part`, or null
+  bool y_key, z_key, x_key;   // of key heads ([B,Hk,T,..]), else of value heads
+  bool rev, trans;            // backwards; rows are d_k (states lie [d_v][d_k])
+  int rows;
+  float y_scale, f;
+  const float* in;            // states on entry, by slot or by sequence; null: zero
+  bool in_by_slot;
+  void* out;                  // [.., rows] of value heads, io type or float
+  bool out_f32;
+  float* part;                // [row block][B H T]: w . (a M_{t-1} x_t) f
+  float* sum;                 // [slot, H]: the state behind the segment (no outputs)
+  float* last;                // [sequence, H]: the state behind the sequence, or null
+};
+constexpr int kMaxJobs = 3;
+struct RecParams {
+  GdrSeqs seqs;
+  int seg, per_head, dk, dv;
+  size_t part_stride;  // B H T
+  const float* log_alpha;
+  float* log_decay;    // [slot, H], written by the job that sums forwards, or null
+  unsigned* err;
+  RecJob job[kMaxJobs];
+};
+
+template <typename IO> struct Load4;
+template <> struct Load4<float> {
+  static __device__ __forceinline__ void pairs(const float* p, f2* x) {
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
+    x[0] = v.x;
+    x[1] = v.y;
+  }
+};
+template <> struct Load4<__nv_bfloat16> {
+  static __device__ __forceinline__ void pairs(const __nv_bfloat16* p, f2* x) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    x[0] = pair(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u));
+    x[1] = pair(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+  }
+};
+
+template <typename IO, int NC> struct RecSm {
+  IO z[2][kTile][NC];
+  IO x[2][kTile][NC];
+  IO y[2][kTile][Cfg<NC>::kMaxRows];
+  IO w[2][kTile][Cfg<NC>::kMaxRows];
+  float out[kTile][Cfg<NC>::kMaxRows];
+  float red[kTile][4];
+  float alpha[2][kTile], zx[kTile];
+};
+
+template <typename IO, int NC, bool OUT>
+__global__ void __launch_bounds__(kMaxThreads) la_rec_kernel(const __grid_constant__ RecParams p) {
+  using C = Cfg<NC>;
+  constexpr int LPR = C::kLpr, EPL = C::kEpl, RT = C::kRt;
+  __shared__ __align__(16) RecSm<IO, NC> sm;
+  const RecJob& job = p.job[blockIdx.y];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
+  const int l = tid % LPR, g = tid / LPR, groups = threads / LPR, cta_rows = groups * RT;
+  const int blocks = (job.rows + cta_rows - 1) / cta_rows;
+  if ((int)blockIdx.x == 0 && blockIdx.y == 0 && p.seqs.starts)  // every sequence's bounds, whoever finds it
+    for (int i = tid; i < p.seqs.n; i += threads) {
+      GdrSeq q;
+      if (!gdr_seq(p.seqs, i, q)) raise_error(p.err, kErrDeviceArg);
+    }
+  const long long unit = blockIdx.x / (unsigned)blocks;
+  const int rb = (int)(blockIdx.x - unit * blocks), r0 = rb * cta_rows;
+  const int h = (int)(unit % p.seqs.H), slot = (int)(unit / p.seqs.H), hk = h / (p.seqs.H / p.seqs.Hk);
+  if (rb >= blocks) return;
+  LaSegment s;
+  if (!la_find(p.seqs, slot, p.seg, s, p.err)) return;
+  const int elems = p.dk * p.dv;
+  const size_t row = ((size_t)s.row_b * p.seqs.H + h) * p.seqs.T + s.start;
+  const size_t krow = ((size_t)s.row_b * p.seqs.Hk + hk) * p.seqs.T + s.start;
+  const IO* z = static_cast<const IO*>(job.z) + (job.z_key ? krow : row) * NC;
+  const IO* x = static_cast<const IO*>(job.x) + (job.x_key ? krow : row) * NC;
+  const IO* y = static_cast<const IO*>(job.y) + (job.y_key ? krow : row) * job.rows + r0;
+  const IO* w = OUT && job.w ? static_cast<const IO*>(job.w) + krow * job.rows + r0 : nullptr;
+  const float* la = p.log_alpha + (p.per_head ? (size_t)h : row);
+
+  // the state on entry
+  f2 m[RT][EPL / 2];
+  const float* in = job.in ? job.in + ((size_t)(job.in_by_slot ? slot : s.seq) * p.seqs.H + h) * elems : nullptr;
+  auto at = [&](int r, int c) { return job.trans ? (size_t)c * p.dk + r : (size_t)r * p.dk + c; };
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int r = r0 + i * groups + g;
+#pragma unroll
+    for (int e = 0; e < EPL / 2; ++e) {
+      const int c = ((e >> 1) * LPR + l) * 4 + 2 * (e & 1);
+      m[i][e] = in && r < job.rows ? pair(in[at(r, c)], in[at(r, c + 1)]) : 0ull;
+    }
+  }
+
+  auto token = [&](int i) { return job.rev ? s.n - 1 - i : i; };
+  auto stage = [&](int tile) {
+    const int b = tile & 1, n = min(kTile, s.n - tile * kTile);
+    constexpr int PC = NC * (int)sizeof(IO) / 16;
+    for (int e = tid; e < n * PC; e += threads) {
+      const int u = e / PC, c = e % PC;
+      const size_t o = (size_t)token(tile * kTile + u) * NC;
+      cp_async16(reinterpret_cast<char*>(sm.z[b][u]) + 16 * c, reinterpret_cast<const char*>(z + o) + 16 * c);
+      if (OUT) cp_async16(reinterpret_cast<char*>(sm.x[b][u]) + 16 * c, reinterpret_cast<const char*>(x + o) + 16 * c);
+    }
+    const int pr = min(cta_rows, job.rows - r0) * (int)sizeof(IO) / 16;
+    for (int e = tid; e < n * pr; e += threads) {
+      const int u = e / pr, c = e % pr;
+      const size_t o = (size_t)token(tile * kTile + u) * job.rows;
+      cp_async16(reinterpret_cast<char*>(sm.y[b][u]) + 16 * c, reinterpret_cast<const char*>(y + o) + 16 * c);
+      if (OUT && w) cp_async16(reinterpret_cast<char*>(sm.w[b][u]) + 16 * c, reinterpret_cast<const char*>(w + o) + 16 * c);
+    }
+    cp_async_commit();
+  };
+  // the log decay that M is multiplied by before its i-th token: backwards that of the
+  // token just done (what comes in is already decayed to the segment's border)
+  auto log_alpha = [&](int i) {
+    if (i >= s.n || (job.rev && i == 0)) return 0.f;
+    return gdr_log(la[p.per_head ? 0 : job.rev ? s.n - i : i]);
+  };
+  const int tiles = (s.n + kTile - 1) / kTile;
+  float g_next = 0.f, off = 0.f;
+  double g_all = 0.;
+  if (tiles > 0) {
+    stage(0);
+    if (warp == 0 && lane < kTile) g_next = log_alpha(lane);
+  }
+  for (int tile = 0; tile < tiles; ++tile) {
+    const int b = tile & 1, n = min(kTile, s.n - tile * kTile);
+    cp_async_wait<0>();
+    if (warp == 0) {  // this tile's decays
+      const float ga = g_next;
+      if (lane < kTile) g_next = log_alpha((tile + 1) * kTile + lane);
+      g_all += lane < kTile ? (double)ga : 0.;
+      const bool near = ga > -0.5f;
+      const float f = near ? expm1f(ga) : expf(ga);
+      const uint32_t nears = __ballot_sync(0xffffffffu, near);
+      float a = f;
+#pragma unroll
+      for (int u = 0; u < kTile; ++u) {
+        const float c = __shfl_sync(0xffffffffu, f, u);
+        if (nears >> u & 1) {
+          const float d = c - off, r = 1.f + d;
+          off = (r - 1.f) - d;
+          if (lane == u) a = r;
+        }
+      }
+      if (lane < kTile) sm.alpha[b][lane] = a;
+    }
+    __syncthreads();
+    if (tile + 1 < tiles) stage(tile + 1);
+    if (OUT) {  // z . x, a token to LPR lanes
+      for (int u = g; u < kTile; u += groups) {
+        float t = 0.f;
+        if (u < n) {
+          f2 acc = 0ull;
+#pragma unroll
+          for (int c = 0; c < C::kPieces; ++c) {
+            f2 zz[2], xx[2];
+            Load4<IO>::pairs(&sm.z[b][u][(c * LPR + l) * 4], zz);
+            Load4<IO>::pairs(&sm.x[b][u][(c * LPR + l) * 4], xx);
+            acc = fma2(zz[0], xx[0], acc);
+            acc = fma2(zz[1], xx[1], acc);
+          }
+          const float2 v = unpair(acc);
+          t = v.x + v.y;
+        }
+        // (groups divides kTile or is a multiple of it: whole groups come here, and LPR lanes of a warp together)
+        const uint32_t mask = (LPR == 32 ? 0xffffffffu : ((1u << LPR) - 1u) << (lane / LPR * LPR));
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) t += __shfl_xor_sync(mask, t, o);
+        if (l == 0) sm.zx[u] = t;
+      }
+      __syncthreads();
+    }
+#pragma unroll 1
+    for (int u0 = 0; u0 < kTile; u0 += LPR) {
+      if (u0 >= n) break;
+      float pre[RT][LPR];
+#pragma unroll
+      for (int u = 0; u < LPR; ++u) {
+        if (u0 + u >= n) {
+#pragma unroll
+          for (int i = 0; i < RT; ++i) pre[i][u] = 0.f;
+          continue;
+        }
+        const float a = sm.alpha[b][u0 + u];
+        const f2 aa = pair(a, a);
+        f2 yy[RT], acc[RT][2];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const float yv = to_f(sm.y[b][u0 + u][i * groups + g]) * job.y_scale;
+          yy[i] = pair(yv, yv);
+          acc[i][0] = acc[i][1] = 0ull;
+        }
+#pragma unroll
+        for (int c = 0; c < C::kPieces; ++c) {
+          f2 zz[2], xx[2];
+          Load4<IO>::pairs(&sm.z[b][u0 + u][(c * LPR + l) * 4], zz);
+          if (OUT) Load4<IO>::pairs(&sm.x[b][u0 + u][(c * LPR + l) * 4], xx);
+#pragma unroll
+          for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const f2 d = mul2(m[i][2 * c + e], aa);
+              if (OUT) acc[i][e] = fma2(d, xx[e], acc[i][e]);
+              m[i][2 * c + e] = fma2(yy[i], zz[e], d);
+            }
+        }
+        if (OUT)
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            const float2 v0 = unpair(acc[i][0]), v1 = unpair(acc[i][1]);
+            pre[i][u] = (v0.x + v0.y) + (v1.x + v1.y);
+          }
+      }
+      if (OUT) {
+        // lane l of a group ends with the sum of token u0 + l
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          int cnt = LPR;
+#pragma unroll
+          for (int o = LPR / 2; o > 0; o >>= 1) {
+            const bool up = l & o;
+            cnt /= 2;
+#pragma unroll
+            for (int j = 0; j < LPR / 2; ++j)
+              if (j < cnt) {
+                const float keep = up ? pre[i][j + cnt] : pre[i][j], send = up ? pre[i][j] : pre[i][j + cnt];
+                pre[i][j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+              }
+          }
+          const int u = u0 + l, rr = i * groups + g;
+          if (u < n && r0 + rr < job.rows) {
+            const float own = to_f(sm.y[b][u][rr]) * job.y_scale * sm.zx[u];
+            sm.out[u][rr] = job.f * (pre[i][0] + own);
+            if (w) dot = fmaf(to_f(sm.w[b][u][rr]), pre[i][0], dot);
+          }
+        }
+        if (w) {
+#pragma unroll
+          for (int o = LPR; o < 32; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+          if (lane < LPR && u0 + lane < kTile) sm.red[u0 + lane][warp] = dot;
+        }
+      }
+    }
+    if (OUT) {
+      __syncthreads();
+      const int nr = min(cta_rows, job.rows - r0);
+      for (int e = tid; e < n * nr; e += threads) {
+        const int u = e / nr, rr = e % nr;
+        const size_t o = (row + token(tile * kTile + u)) * job.rows + r0 + rr;
+        if (job.out_f32) static_cast<float*>(job.out)[o] = sm.out[u][rr];
+        else static_cast<IO*>(job.out)[o] = from_f<IO>(sm.out[u][rr]);
+      }
+      if (w && tid < n) {
+        float t = 0.f;
+        for (int k = 0; k < threads / 32; ++k) t += sm.red[tid][k];
+        job.part[rb * p.part_stride + row + token(tile * kTile + tid)] = job.f * t;
+      }
+    }
+  }
+
+  // what leaves the segment (backwards: at the border before its first token)
+  float* dst = !OUT ? job.sum + ((size_t)slot * p.seqs.H + h) * elems
+               : job.last && (job.rev ? s.num == 0 : (long long)s.num * p.seg + s.n == s.seq_len)
+                   ? job.last + ((size_t)s.seq * p.seqs.H + h) * elems : nullptr;
+  if (dst) {
+    const LaDecay d = job.rev && s.n > 0 ? la_decay(gdr_log(la[0])) : LaDecay{0.f, true};
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int r = r0 + i * groups + g;
+      if (r < job.rows)
+#pragma unroll
+        for (int e = 0; e < EPL / 2; ++e) {
+          const int c = ((e >> 1) * LPR + l) * 4 + 2 * (e & 1);
+          const float2 v = unpair(m[i][e]);
+          dst[at(r, c)] = la_apply(d, v.x);
+          dst[at(r, c + 1)] = la_apply(d, v.y);
+        }
+    }
+  }
+  if (!OUT && !job.rev && rb == 0 && warp == 0 && p.log_decay) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) g_all += __shfl_xor_sync(0xffffffffu, g_all, o);
+    if (lane == 0) p.log_decay[(size_t)slot * p.seqs.H + h] = (float)g_all;
+  }
+}
+
+// ---------------------------------------------------------------- along the segments
+// Four elements to a thread, some CTAs to a (sequence, head).  The loads of four
+// segments travel together.
+constexpr int kCarryThreads = 128;
+__global__ void __launch_bounds__(kCarryThreads) la_carry_kernel(LaCarry c) {
+  const int dir = blockIdx.y;
+  float* sums = c.sums[dir];
+  if (!sums) return;
+  const int per = (c.elems / 4 + kCarryThreads - 1) / kCarryThreads, row = blockIdx.x / per;
+  const int h = row % c.seqs.H, seq = row / c.seqs.H;
+  const int e = ((int)(blockIdx.x - (unsigned)row * per) * kCarryThreads + threadIdx.x) * 4;
+  if (e >= c.elems) return;
+  GdrSeq q;
+  if (!gdr_seq(c.seqs, seq, q)) return;
+  const int base = gdr_slot_base(c.seqs, seq, q.start, c.seg), n = (q.len + c.seg - 1) / c.seg;
+  const size_t sh = (size_t)seq * c.seqs.H + h;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (c.init[dir]) x = *reinterpret_cast<const float4*>(c.init[dir] + sh * c.elems + e);
+  if (n == 0) *reinterpret_cast<float4*>(sums + ((size_t)base * c.seqs.H + h) * c.elems + e) = x;  // (an empty sequence's slot)
+  for (int i0 = 0; i0 < n; i0 += 4) {
+    float4 y[4];
+    LaDecay d[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i0 + j < n) {
+        const size_t at = (size_t)(base + (dir ? n - 1 - i0 - j : i0 + j)) * c.seqs.H + h;
+        y[j] = *reinterpret_cast<const float4*>(sums + at * c.elems + e);
+        d[j] = la_decay(c.log_decay[at]);
+      }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i0 + j < n) {
+        const size_t at = (size_t)(base + (dir ? n - 1 - i0 - j : i0 + j)) * c.seqs.H + h;
+        *reinterpret_cast<float4*>(sums + at * c.elems + e) = x;
+        x.x = la_apply(d[j], x.x) + y[j].x;
+        x.y = la_apply(d[j], x.y) + y[j].y;
+        x.z = la_apply(d[j], x.z) + y[j].z;
+        x.w = la_apply(d[j], x.w) + y[j].w;
+      }
+  }
+  if (c.last[dir]) *reinterpret_cast<float4*>(c.last[dir] + sh * c.elems + e) = x;
+}
+
+// ---------------------------------------------------------------- the decay's gradient, shared heads
+struct FinishParams {
+  GdrSeqs seqs;
+  int seg, dk, dv, per_head, q_parts, k_parts, sum_heads, slots;
+  size_t part_stride;
+  const float *log_alpha, *part_q, *part_k;  // [row block][B H T]
+  const float *entry, *final_state;          // states on entry by slot, behind the sequences (null: <S, B> is zero)
+  const float* behind;                       // gradients at the segments' ends, by slot or by sequence
+  bool behind_by_slot;
+  float* dlog_alpha;
+  double* head_sums;                         // [slot, H] when log_alpha is one to a head
+  const float *dq, *dkey;                    // [B,H,T,dk] float32 (sum_heads)
+  void *dq_out, *dk_out;
+};
+constexpr int kFinishThreads = 128;
+__device__ __forceinline__ double warp_sum(double x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+template <typename IO>
+__global__ void __launch_bounds__(kFinishThreads) la_rec_finish_kernel(FinishParams p) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int h = blockIdx.x % p.seqs.H, slot = blockIdx.x / p.seqs.H;
+  LaSegment s;
+  const bool found = la_find(p.seqs, slot, p.seg, s, nullptr) && s.n > 0;
+  if (!found) {
+    if (p.per_head && blockIdx.y == 0 && tid == 0) p.head_sums[(size_t)slot * p.seqs.H + h] = 0.;
+    return;
+  }
+  const size_t row = ((size_t)s.row_b * p.seqs.H + h) * p.seqs.T + s.start;
+  if (blockIdx.y > 0) {  // dq, dk: the value heads of a key head in their order
+    const int G = p.seqs.H / p.seqs.Hk;
+    if (h % G) return;
+    const float* src = blockIdx.y == 1 ? p.dq : p.dkey;
+    IO* dst = static_cast<IO*>(blockIdx.y == 1 ? p.dq_out : p.dk_out);
+    const size_t krow = ((size_t)s.row_b * p.seqs.Hk + h / G) * p.seqs.T + s.start;
+    const int n4 = p.dk / 4;
+    for (long long e = tid; e < (long long)s.n * n4; e += kFinishThreads) {
+      const float4* a = reinterpret_cast<const float4*>(src + row * p.dk) + e;
+      float4 x = *a;
+      for (int i = 1; i < G; ++i) {
+        const float4 y = a[(size_t)i * p.seqs.T * n4];
+        x.x += y.x;
+        x.y += y.y;
+        x.z += y.z;
+        x.w += y.w;
+      }
+      IO* d = dst + krow * p.dk + 4 * e;
+      d[0] = from_f<IO>(x.x);
+      d[1] = from_f<IO>(x.y);
+      d[2] = from_f<IO>(x.z);
+      d[3] = from_f<IO>(x.w);
+    }
+    return;
+  }
+  __shared__ double red[2][kFinishThreads / 32];
+  const int elems = p.dk * p.dv;
+  double border = 0.;
+  if (p.entry || p.final_state) {
+    const bool last = (long long)s.num * p.seg + s.n == s.seq_len;
+    const float* S = last ? p.final_state + ((size_t)s.seq * p.seqs.H + h) * elems
+                          : p.entry + ((size_t)(slot + 1) * p.seqs.H + h) * elems;
+    const float* B = p.behind + ((size_t)(p.behind_by_slot ? slot : s.seq) * p.seqs.H + h) * elems;
+    float2 t = make_float2(0.f, 0.f);  // (with what its roundings leave)
+    for (int e = tid; e < elems; e += kFinishThreads) {
+      const float a = S[e], b = B[e], m = a * b;
+      t = pair_add(t, make_float2(m, fmaf(a, b, -m)));
+    }
+    border = warp_sum((double)t.x + (double)t.y);
+    if (lane == 0) red[0][warp] = border;
+    __syncthreads();
+    border = red[0][0] + red[0][1] + red[0][2] + red[0][3];
+  }
+  double run = border, all = 0.;
+  const int tiles = (s.n + kFinishThreads - 1) / kFinishThreads;
+  for (int tile = 0; tile < tiles; ++tile) {  // from the segment's end
+    const int t = s.n - 1 - (tile * kFinishThreads + tid);
+    double x = 0.;
+    if (t >= 0) {
+      for (int i = 0; i < p.q_parts; ++i) x += p.part_q[i * p.part_stride + row + t];
+      for (int i = 0; i < p.k_parts; ++i) x -= p.part_k[i * p.part_stride + row + t];
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) red[1][warp] = x;
+    __syncthreads();
+    double sum = run;
+    for (int k = 0; k < kFinishThreads / 32; ++k) {
+      if (k < warp) x += red[1][k];
+      sum += red[1][k];
+    }
+    if (t >= 0) {
+      const double v = gdr_forgets(p.log_alpha[p.per_head ? (size_t)h : row + t]) ? 0. : run + x;
+      if (p.per_head) all += v;
+      else p.dlog_alpha[row + t] = (float)v;
+    }
+    run = sum;
+    __syncthreads();
+  }
+  if (p.per_head) {
+    all = warp_sum(all);
+    if (lane == 0) red[0][warp] = all;
+    __syncthreads();
+    if (tid == 0) p.head_sums[(size_t)slot * p.seqs.H + h] = red[0][0] + red[0][1] + red[0][2] + red[0][3];
+  }
+}
+__global__ void __launch_bounds__(128) la_head_sum_kernel(const double* sums, int slots, int H, float* out) {
+  __shared__ double red[4];
+  const int h = blockIdx.x;
+  double x = 0.;
+  for (int i = threadIdx.x; i < slots; i += 128) x += sums[(size_t)i * H + h];
+  x = warp_sum(x);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+  __syncthreads();
+  if (threadIdx.x == 0) out[h] = (float)(red[0] + red[1] + red[2] + red[3]);
+}
+
+// ---------------------------------------------------------------- host
+// Tokens of a segment: as many segments as keep about four CTAs on every SM (a
+// split costs another pass over keys and values, half of the forward's work),
+// none below 64 tokens.
+int rec_segment(const LaArgs& a) {
+  const int blocks = row_blocks(a.dv, a.dk);
+  const long long per = ((long long)a.B * a.T * a.H * blocks + 607) / 608;
+  const long long seg = std::max<long long>(64, (per + kTile - 1) / kTile * kTile);
+  return (int)std::min<long long>(seg, a.T);
+}
+
+template <typename IO, int NC, bool OUT>
+ll_status rec_run(const RecParams& p, int jobs, size_t slots, cudaStream_t stream) {
+  const int rows = p.job[0].rows, threads = threads_for<NC>(rows), cta = rows_for<NC>(rows);
+  const size_t grid = slots * p.seqs.H * ((rows + cta - 1) / cta);
+  if (grid > 0x7fffffffull) return LL_ERR_UNSUPPORTED;
+  la_rec_kernel<IO, NC, OUT><<<dim3((unsigned)grid, jobs), threads, 0, stream>>>(p);
+  LL_CUDA_OK(cudaGetLastError());
+  return LL_OK;
+}
+// jobs of one launch have the same numbers of rows and columns
+template <bool OUT>
+ll_status rec_launch(ll_dtype io, int cols, const RecParams& p, int jobs, size_t slots, cudaStream_t st) {
+  const bool f = io == LL_F32;
+  switch (cols) {
+    case 16: return f ? rec_run<float, 16, OUT>(p, jobs, slots, st) : rec_run<__nv_bfloat16, 16, OUT>(p, jobs, slots, st);
+    case 32: return f ? rec_run<float, 32, OUT>(p, jobs, slots, st) : rec_run<__nv_bfloat16, 32, OUT>(p, jobs, slots, st);
+    case 64: return f ? rec_run<float, 64, OUT>(p, jobs, slots, st) : rec_run<__nv_bfloat16, 64, OUT>(p, jobs, slots, st);
+    case 128: return f ? rec_run<float, 128, OUT>(p, jobs, slots, st) : rec_run<__nv_bfloat16, 128, OUT>(p, jobs, slots, st);
+  }
+  return LL_ERR_UNSUPPORTED;
+}
+RecParams rec_params(const LaArgs& a, int seg) {
+  RecParams p{};
+  p.seqs = la_seqs(a);
+  p.seg = seg;
+  p.per_head = a.per_head;
+  p.dk = a.dk;
+  p.dv = a.dv;
+  p.part_stride = (size_t)a.B * a.H * a.T;
+  p.log_alpha = a.log_alpha;
+  p.err = a.err;
+  return p;
+}
+RecJob job_o(const LaArgs& a) {
+  RecJob j{};
+  j.y = a.v;
+  j.z = a.k;
+  j.x = a.q;
+  j.z_key = j.x_key = true;
+  j.rows = a.dv;
+  j.y_scale = 1.f;
+  j.f = a.scale;
+  return j;
+}
+RecJob job_dv(const LaArgs& a) {
+  RecJob j{};
+  j.y = a.dout;
+  j.z = a.q;
+  j.x = a.k;
+  j.z_key = j.x_key = true;
+  j.rev = true;
+  j.rows = a.dv;
+  j.y_scale = a.scale;
+  j.f = 1.f;
+  return j;
+}
+size_t elems_of(const LaArgs& a) { return (size_t)a.dk * a.dv; }
+
+struct Plan {
+  int seg;
+  size_t slots, sum_s, sum_a, fin, dec, part_q, part_k, dq, dk, heads, total;
+  int q_parts;
+  bool split, states;  // more than one segment; the sums of the states are wanted
+};
+Plan fwd_plan(const LaArgs& a) {
+  Plan pl{};
+  pl.seg = rec_segment(a);
+  pl.slots = la_slots(a, pl.seg);
+  pl.split = la_split(a, pl.seg);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += align_up(bytes, 256);
+    return o;
+  };
+  if (pl.split) {
+    pl.sum_s = take(pl.slots * a.H * elems_of(a) * 4);
+    pl.dec = take(pl.slots * a.H * 4);
+  }
+  pl.total = at;
+  return pl;
+}
+// (the workspace cannot depend on which optional tensors a call brings)
+Plan bwd_plan(const LaArgs& a) {
+  Plan pl{};
+  pl.seg = rec_segment(a);
+  pl.slots = la_slots(a, pl.seg);
+  pl.split = la_split(a, pl.seg);
+  pl.q_parts = row_blocks(a.dk, a.dv);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += align_up(bytes, 256);
+    return o;
+  };
+  const size_t states = pl.slots * a.H * elems_of(a) * 4, tokens = (size_t)a.B * a.H * a.T;
+  pl.sum_s = take(states);
+  pl.sum_a = pl.split ? take(states) : 0;
+  pl.fin = take((size_t)la_sequences(a) * a.H * elems_of(a) * 4);
+  pl.dec = take(pl.slots * a.H * 4);
+  pl.part_q = take(tokens * pl.q_parts * 4);
+  pl.part_k = take(tokens * pl.q_parts * 4);
+  if (a.H != a.Hk) {
+    pl.dq = take(tokens * a.dk * 4);
+    pl.dk = take(tokens * a.dk * 4);
+  }
+  if (a.per_head) pl.heads = take(pl.slots * a.H * 8);
+  pl.total = at;
+  return pl;
+}
+
+}  // namespace
+
+ll_status la_carry_launch(const LaCarry& c, int sequences, cudaStream_t stream) {
+  const size_t grid = (size_t)sequences * c.seqs.H * ((c.elems / 4 + kCarryThreads - 1) / kCarryThreads);
+  if (grid > 0x7fffffffull) return LL_ERR_UNSUPPORTED;
+  la_carry_kernel<<<dim3((unsigned)grid, 2), kCarryThreads, 0, stream>>>(c);
+  LL_CUDA_OK(cudaGetLastError());
+  return LL_OK;
+}
+
+size_t la_fwd_workspace(const LaArgs& a) { return fwd_plan(a).total; }
+int la_fwd_launches(const LaArgs& a) { return fwd_plan(a).split ? 3 : 1; }
+
+ll_status la_fwd_launch(const LaArgs& a) {
+  const Plan pl = fwd_plan(a);
+  char* ws = static_cast<char*>(a.ws);
+  RecParams p = rec_params(a, pl.seg);
+  float* sums = reinterpret_cast<float*>(ws + pl.sum_s);
+  if (pl.split) {
+    p.job[0] = job_o(a);
+    p.job[0].sum = sums;
+    p.log_decay = reinterpret_cast<float*>(ws + pl.dec);
+    ll_status st = rec_launch<false>(a.io, a.dk, p, 1, pl.slots, a.stream);
+    if (st != LL_OK) return st;
+    const LaCarry c{p.seqs, pl.seg, (int)elems_of(a), {sums, nullptr}, p.log_decay, {a.state_in, nullptr},
+                    {nullptr, nullptr}, a.err};
+    st = la_carry_launch(c, la_sequences(a), a.stream);
+    if (st != LL_OK) return st;
+    p.log_decay = nullptr;
+  }
+  p.job[0] = job_o(a);
+  p.job[0].in = pl.split ? sums : a.state_in;
+  p.job[0].in_by_slot = pl.split;
+  p.job[0].out = a.o;
+  p.job[0].last = a.state_out;
+  return rec_launch<true>(a.io, a.dk, p, 1, pl.slots, a.stream);
+}
+
+size_t la_bwd_workspace(const LaArgs& a) { return bwd_plan(a).total; }
+int la_bwd_launches(const LaArgs& a) {
+  return (la_split(a, rec_segment(a)) ? 2 : 0) + (a.dk == a.dv ? 1 : 2) + 1 + (a.per_head ? 1 : 0);
+}
+
+ll_status la_bwd_launch(const LaArgs& a) {
+  const Plan pl = bwd_plan(a);
+  char* ws = static_cast<char*>(a.ws);
+  RecParams p = rec_params(a, pl.seg);
+  float* sum_s = reinterpret_cast<float*>(ws + pl.sum_s);
+  float* sum_a = reinterpret_cast<float*>(ws + pl.sum_a);
+  float* fin = reinterpret_cast<float*>(ws + pl.fin);
+  float* dec = reinterpret_cast<float*>(ws + pl.dec);
+  ll_status st;
+  const bool states = pl.split || a.dstate_out;
+  if (states) {
+    p.job[0] = job_o(a);
+    p.job[0].sum = sum_s;
+    p.job[1] = job_dv(a);
+    p.job[1].sum = sum_a;
+    p.log_decay = dec;
+    st = rec_launch<false>(a.io, a.dk, p, pl.split ? 2 : 1, pl.slots, a.stream);
+    if (st != LL_OK) return st;
+    const LaCarry c{p.seqs, pl.seg, (int)elems_of(a), {sum_s, pl.split ? sum_a : nullptr}, dec,
+                    {a.state_in, a.dstate_out}, {fin, nullptr}, a.err};
+    st = la_carry_launch(c, la_sequences(a), a.stream);
+    if (st != LL_OK) return st;
+    p.log_decay = nullptr;
+  }
+  const bool own = a.H == a.Hk;
+  RecJob v = job_dv(a), q{}, k{};
+  v.in = pl.split ? sum_a : a.dstate_out;
+  v.in_by_slot = pl.split;
+  v.out = a.dval;
+  v.last = a.dstate_in;
+  q.y = a.k;
+  q.z = a.v;
+  q.x = a.dout;
+  q.w = a.q;
+  q.y_key = true;
+  q.trans = true;
+  q.rows = a.dk;
+  q.y_scale = 1.f;
+  q.f = a.scale;
+  q.in = pl.split ? sum_s : a.state_in;
+  q.in_by_slot = pl.split;
+  q.out = own ? a.dq : ws + pl.dq;
+  q.out_f32 = !own;
+  q.part = reinterpret_cast<float*>(ws + pl.part_q);
+  k = q;
+  k.y = a.q;
+  k.z = a.dout;
+  k.x = a.v;
+  k.w = a.k;
+  k.rev = true;
+  k.y_scale = a.scale;
+  k.f = 1.f;
+  k.in = v.in;
+  k.out = own ? a.dkey : ws + pl.dk;
+  k.part = reinterpret_cast<float*>(ws + pl.part_k);
+  p.job[0] = q;
+  p.job[1] = k;
+  p.job[2] = v;
+  st = rec_launch<true>(a.io, a.dv, p, a.dk == a.dv ? 3 : 2, pl.slots, a.stream);
+  if (st != LL_OK) return st;
+  if (a.dk != a.dv) {
+    p.job[0] = v;
+    st = rec_launch<true>(a.io, a.dk, p, 1, pl.slots, a.stream);
+    if (st != LL_OK) return st;
+  }
+  FinishParams f{};
+  f.seqs = p.seqs;
+  f.seg = pl.seg;
+  f.dk = a.dk;
+  f.dv = a.dv;
+  f.per_head = a.per_head;
+  f.q_parts = f.k_parts = pl.q_parts;
+  f.part_stride = p.part_stride;
+  f.log_alpha = a.log_alpha;
+  f.part_q = q.part;
+  f.part_k = k.part;
+  f.entry = states ? sum_s : nullptr;
+  f.final_state = states ? fin : nullptr;
+  f.behind = pl.split ? sum_a : a.dstate_out;
+  f.behind_by_slot = pl.split;
+  f.dlog_alpha = a.dlog_alpha;
+  f.head_sums = reinterpret_cast<double*>(ws + pl.heads);
+  f.dq = static_cast<const float*>(q.out);
+  f.dkey = static_cast<const float*>(k.out);
+  f.dq_out = a.dq;
+  f.dk_out = a.dkey;
+  const size_t grid = pl.slots * a.H;
+  if (grid > 0x7fffffffull) return LL_ERR_UNSUPPORTED;
+  const dim3 g((unsigned)grid, own ? 1 : 3);
+  if (a.io == LL_F32) la_rec_finish_kernel<float><<<g, kFinishThreads, 0, a.stream>>>(f);
+  else la_rec_finish_kernel<__nv_bfloat16><<<g, kFinishThreads, 0, a.stream>>>(f);
+  LL_CUDA_OK(cudaGetLastError());
+  if (a.per_head) {
+    la_head_sum_kernel<<<a.H, 128, 0, a.stream>>>(f.head_sums, (int)pl.slots, a.H, a.dlog_alpha);
+    LL_CUDA_OK(cudaGetLastError());
+  }
+  return LL_OK;
+}
+
+}  // namespace llattn
