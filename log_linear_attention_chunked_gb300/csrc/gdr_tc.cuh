@@ -82,7 +82,7 @@ __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontr
 
 // Bounded wait (every thread): the waits of these kernels are on their own
 // copies and products, which always complete.
-__device__ __noinline__ void wait_bar_long(uint64_t* bar, uint32_t par, unsigned* err) {
+static __device__ __noinline__ void wait_bar_long(uint64_t* bar, uint32_t par, unsigned* err) {
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, par)) {
     if (globaltimer_ns() - t0 > kTimeoutNs) {
@@ -138,7 +138,7 @@ template <int L> __device__ __forceinline__ uint32_t step_of(int kk) {  // of th
 // D (+)= A B over 128 x 128 x 128 fp16.
 // (Eight instructions of about 65 cycles; a loop over them took 140 each.)
 template <int AL, int BL>
-__device__ __noinline__ void mma_tile(uint32_t d, uint32_t a, uint32_t b, bool add) {
+static __device__ __noinline__ void mma_tile(uint32_t d, uint32_t a, uint32_t b, bool add) {
   constexpr uint32_t id = idesc_f16(128, AL == kDown || AL == kPlainDown, BL == kDown || BL == kPlainDown);
   const uint64_t da = desc_of<AL>(a), db = desc_of<BL>(b);
 #pragma unroll
@@ -269,7 +269,7 @@ __device__ __forceinline__ void block_mma(float (*z)[4], BlockRaw<NT>& v) {
 // the columns to each.
 constexpr int kSolveBar = 1;
 template <int N>
-__device__ __noinline__ void tri_double(float* Ap, float* Mp, const float* beta, int warp, int lane) {
+static __device__ __noinline__ void tri_double(float* Ap, float* Mp, const float* beta, int warp, int lane) {
   constexpr int RB = N / 16, NT = N / 16;  // row blocks; column tiles of a warp
   const int r0 = warp / (2 * RB) * 2 * N, rb = warp / 2 % RB, c = r0 + (warp & 1) * (N / 2);
   const int row = r0 + N + 16 * rb, g = lane >> 2, t = lane & 3;
@@ -329,7 +329,7 @@ __device__ __noinline__ void tri_double(float* Ap, float* Mp, const float* beta,
 }
 
 // 256 threads
-__device__ __noinline__ void tri_solve(float* Ap, float* Mp, const float* beta, int t) {
+static __device__ __noinline__ void tri_solve(float* Ap, float* Mp, const float* beta, int t) {
   if (t < 128) {
     const int r0 = t & ~7, cc = t & 7;
     float a[8][8], acc[8];
@@ -448,7 +448,7 @@ __device__ __forceinline__ uint32_t max_bits2(uint32_t m) { return max(m & 0xfff
 // other sequences: they become zeros, whatever they hold.  NT threads (`t` among
 // them, barrier `bar`), the tile complete before; one barrier inside, none after.
 template <int NT>
-__device__ __noinline__ float tile_to_f16(unsigned char* tile, int n, uint32_t* red, int t, int bar) {
+static __device__ __noinline__ float tile_to_f16(unsigned char* tile, int n, uint32_t* red, int t, int bar) {
   const bool in = (t & 127) < n;
   constexpr int PC = kC * 16 / NT;
   uint32_t m2 = kNoMax2;
@@ -498,7 +498,7 @@ __device__ __forceinline__ float pow2_inverse(float p) { return __uint_as_float(
 constexpr float kKeysUp = 4.f;  // rows of K go up to 64
 constexpr float kShortest = 1.f / 4096.f;
 template <int NT>
-__device__ __noinline__ Keys keys_to_f16(unsigned char* tile, int n, uint32_t* red, int t, int bar) {
+static __device__ __noinline__ Keys keys_to_f16(unsigned char* tile, int n, uint32_t* red, int t, int bar) {
   constexpr int W = NT / 128, PC = 16 / W;
   const int r = t / W;
   const bool in = r < n;
@@ -549,7 +549,7 @@ __device__ __noinline__ Keys keys_to_f16(unsigned char* tile, int n, uint32_t* r
 // v is), `bits` those of the largest |v| that the thread's warp sees.
 constexpr float kValuesDown = 1.f / 8192.f;
 template <int NT>
-__device__ __noinline__ float values_to_f16(unsigned char* tile, int n, float p, uint32_t* red, int t, int bar,
+static __device__ __noinline__ float values_to_f16(unsigned char* tile, int n, float p, uint32_t* red, int t, int bar,
                                             uint32_t* bits) {
   constexpr int W = NT / 128, PC = 16 / W;
   const int r = t / W;
@@ -606,7 +606,7 @@ __device__ __forceinline__ float rows_scale(uint32_t bits) {
 
 // the bits of the largest of a state's n values that this thread of `threads` sees
 // (16 bytes a load: with four the 64 KB took longer than a chunk's solve)
-__device__ __noinline__ uint32_t state_max(const float* x, int n, int t, int threads) {
+static __device__ __noinline__ uint32_t state_max(const float* x, int n, int t, int threads) {
   uint32_t m = kNoMax;
 #pragma unroll 4
   for (int e = t; e < n / 4; e += threads) {
@@ -617,7 +617,7 @@ __device__ __noinline__ uint32_t state_max(const float* x, int n, int t, int thr
 }
 
 // rows 0 .. n - 1 of a tile of 16-bit values into a [.., d] matrix, whole rows to half a warp
-__device__ __noinline__ void store_rows(void* dst, const unsigned char* tile, int n, int d, int tid, int threads) {
+static __device__ __noinline__ void store_rows(void* dst, const unsigned char* tile, int n, int d, int tid, int threads) {
   const int c8 = tid & 15;
   if (c8 * 8 < d)
 #pragma unroll 4
@@ -672,7 +672,7 @@ __device__ __forceinline__ void put_inverse(unsigned char* hi, unsigned char* lo
   }
 }
 // an accumulator's row, times f, as [slice of 32][piece of 4][row][4] floats; returns its largest value's bits
-__device__ __noinline__ uint32_t write_rows(float* dst, uint32_t acc, int i, int qt, float f) {
+static __device__ __noinline__ uint32_t write_rows(float* dst, uint32_t acc, int i, int qt, float f) {
   uint32_t m = kNoMax;
 #pragma unroll 1
   for (int c = 0; c < 2; ++c) {
@@ -691,7 +691,7 @@ __device__ __noinline__ uint32_t write_rows(float* dst, uint32_t acc, int i, int
 }
 // an accumulator's row, times f, in two parts: tiles hi and lo, plain ones or not
 template <bool PLAIN>
-__device__ __noinline__ void write_tiles(unsigned char* hi, unsigned char* lo, uint32_t acc, int i, int qt, float f,
+static __device__ __noinline__ void write_tiles(unsigned char* hi, unsigned char* lo, uint32_t acc, int i, int qt, float f,
                                          float scale_lo) {
 #pragma unroll 1
   for (int c = 0; c < 2; ++c) {

@@ -13,8 +13,7 @@
 // in the way of the gated delta rule's chunks (gdr.cuh), a segment in the place
 // of a chunk.
 //
-// A decay's logarithm in a segment is summed in float32 over at most a tile or
-// chunk of tokens at a time.
+// A segment's log decay is summed in float64 (token by token) or as an integer (in chunks).
 #pragma once
 
 #include "gdr.cuh"
@@ -89,6 +88,10 @@ __device__ __forceinline__ bool la_find(const GdrSeqs& s, int c, int seg, LaSegm
   return r.n > 0 || r.num == 0;
 }
 
+// log alpha below -1e4 is alpha = 0 in float32 either way; the bound keeps sums finite for
+// alpha = 0 (log alpha = -inf).  A NaN stays one.
+__device__ __forceinline__ float la_log(float la) { return la < kGdrMinLog ? kGdrMinLog : la; }
+
 // What an element of a state is multiplied by over some tokens of log decay g:
 // near 1 as x + expm1(g) x, since a rounded factor applied again and again adds up.
 struct LaDecay {
@@ -100,6 +103,33 @@ __device__ __forceinline__ LaDecay la_decay(float g) {
   return LaDecay{near ? expm1f(g) : expf(g), near};
 }
 __device__ __forceinline__ float la_apply(const LaDecay& d, float x) { return d.near ? fmaf(d.f, x, x) : d.f * x; }
+
+// The kernels of a call follow one another closely: each lets the next one be set up
+// once all of its CTAs run, and the next waits, first of all and in every CTA, until
+// the one before has ended and its writes can be read.  (No effect in the first.)
+__device__ __forceinline__ void la_chain() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// `after`: the kernel follows another of the same call
+template <typename... P, typename... A>
+ll_status la_launch(bool after, void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
+                    const A&... args) {
+  if (smem > 48 * 1024)
+    LL_CUDA_OK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = stream;
+  c.attrs = &at;
+  c.numAttrs = after ? 1 : 0;
+  LL_CUDA_OK(cudaLaunchKernelEx(&c, kernel, args...));
+  return LL_OK;
+}
 
 // ---- launchers
 size_t la_fwd_workspace(const LaArgs& a);
@@ -116,10 +146,15 @@ struct LaCarry {
   float* sums[2];                        // [slot, H, elems]: forwards, backwards (null: not wanted); in place
   const float* log_decay;                // [slot, H]
   const float* init[2];                  // [sequence, H, elems] or null
-  float* last[2];                        // what leaves the last (backwards the first) segment, or null
-  unsigned* err;
 };
-ll_status la_carry_launch(const LaCarry& c, int sequences, cudaStream_t stream);
+
+// in chunks on the tensor cores (la_tc.cu)
+bool la_tc_formats(const LaArgs& a);
+ll_status la_tc_sum_launch(const LaArgs& a, int seg, size_t slots, int dirs, float* sum_s, float* sum_a,
+                           float* log_decay);
+ll_status la_tc_fwd_main(const LaArgs& a, int seg, size_t slots, const float* states, bool by_slot, bool after);
+ll_status la_tc_bwd_main(const LaArgs& a, int seg, size_t slots, const float* states, const float* adjoints,
+                         bool by_slot, float* before, float* dq32, float* dk32, float* part_q, float* part_v, bool after);
 
 struct LaRope {
   int rot, interleaved;

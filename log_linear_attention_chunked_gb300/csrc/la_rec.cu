@@ -15,9 +15,11 @@
 // scalar products z . x made once per staged tile, which keeps the update out of the
 // sum's chain, and gives the part of the sum that lies before token t by itself:
 // that is what the decay's gradient is made of,
-//   dlog_alpha_t = sum_{s >= t} q_s.dq'_s - sum_{j >= t} k_j.dk'_j + <S, B>,
+//   dlog_alpha_t = <S, B> + sum_{j < t} (k_j.dk'_j - q_j.dq'_j),
 // over the tokens of the segment, the primes leaving out a token's own pair, S and B the
-// state and its gradient at the segment's end.  Sums over the lanes are taken for kLpr
+// state and its gradient at the segment's start.  (Every partial sum is a dlog_alpha
+// itself: from the segment's end they would be taken from a state that no decay has
+// touched yet, and cancel.)  Sums over the lanes are taken for kLpr
 // tokens at once: each step of a butterfly halves the values that a lane carries.
 //
 // alpha_t is rounded to float32 once a token; what the roundings so far are off by
@@ -135,6 +137,7 @@ __global__ void __launch_bounds__(kMaxThreads) la_rec_kernel(const __grid_consta
   using C = Cfg<NC>;
   constexpr int LPR = C::kLpr, EPL = C::kEpl, RT = C::kRt;
   __shared__ __align__(16) RecSm<IO, NC> sm;
+  la_chain();
   const RecJob& job = p.job[blockIdx.y];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   const int l = tid % LPR, g = tid / LPR, groups = threads / LPR, cta_rows = groups * RT;
@@ -196,7 +199,7 @@ __global__ void __launch_bounds__(kMaxThreads) la_rec_kernel(const __grid_consta
   // token just done (what comes in is already decayed to the segment's border)
   auto log_alpha = [&](int i) {
     if (i >= s.n || (job.rev && i == 0)) return 0.f;
-    return gdr_log(la[p.per_head ? 0 : job.rev ? s.n - i : i]);
+    return la_log(la[p.per_head ? 0 : job.rev ? s.n - i : i]);
   };
   const int tiles = (s.n + kTile - 1) / kTile;
   float g_next = 0.f, off = 0.f;
@@ -347,7 +350,7 @@ __global__ void __launch_bounds__(kMaxThreads) la_rec_kernel(const __grid_consta
                : job.last && (job.rev ? s.num == 0 : (long long)s.num * p.seg + s.n == s.seq_len)
                    ? job.last + ((size_t)s.seq * p.seqs.H + h) * elems : nullptr;
   if (dst) {
-    const LaDecay d = job.rev && s.n > 0 ? la_decay(gdr_log(la[0])) : LaDecay{0.f, true};
+    const LaDecay d = job.rev && s.n > 0 ? la_decay(la_log(la[0])) : LaDecay{0.f, true};
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       const int r = r0 + i * groups + g;
@@ -373,6 +376,7 @@ __global__ void __launch_bounds__(kMaxThreads) la_rec_kernel(const __grid_consta
 // segments travel together.
 constexpr int kCarryThreads = 128;
 __global__ void __launch_bounds__(kCarryThreads) la_carry_kernel(LaCarry c) {
+  la_chain();
   const int dir = blockIdx.y;
   float* sums = c.sums[dir];
   if (!sums) return;
@@ -392,7 +396,7 @@ __global__ void __launch_bounds__(kCarryThreads) la_carry_kernel(LaCarry c) {
     LaDecay d[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (i0 + j < n) {
+      if (i0 + j < n - 1) {  // (nothing needs the last one's sum)
         const size_t at = (size_t)(base + (dir ? n - 1 - i0 - j : i0 + j)) * c.seqs.H + h;
         y[j] = *reinterpret_cast<const float4*>(sums + at * c.elems + e);
         d[j] = la_decay(c.log_decay[at]);
@@ -402,126 +406,157 @@ __global__ void __launch_bounds__(kCarryThreads) la_carry_kernel(LaCarry c) {
       if (i0 + j < n) {
         const size_t at = (size_t)(base + (dir ? n - 1 - i0 - j : i0 + j)) * c.seqs.H + h;
         *reinterpret_cast<float4*>(sums + at * c.elems + e) = x;
+        if (i0 + j == n - 1) break;
         x.x = la_apply(d[j], x.x) + y[j].x;
         x.y = la_apply(d[j], x.y) + y[j].y;
         x.z = la_apply(d[j], x.z) + y[j].z;
         x.w = la_apply(d[j], x.w) + y[j].w;
       }
   }
-  if (c.last[dir]) *reinterpret_cast<float4*>(c.last[dir] + sh * c.elems + e) = x;
 }
 
 // ---------------------------------------------------------------- the decay's gradient, shared heads
 struct FinishParams {
   GdrSeqs seqs;
-  int seg, dk, dv, per_head, q_parts, k_parts, sum_heads, slots;
+  int seg, dk, dv, per_head, parts;
   size_t part_stride;
   const float *log_alpha, *part_q, *part_k;  // [row block][B H T]
-  const float *entry, *final_state;          // states on entry by slot, behind the sequences (null: <S, B> is zero)
-  const float* behind;                       // gradients at the segments' ends, by slot or by sequence
-  bool behind_by_slot;
+  const float* entry;                        // states on entry, by slot or by sequence; null: zero
+  bool by_slot;
+  const float* behind;                       // gradients at the segments' ends by slot,
+  const float* first;                        // before the sequences
+  float* copy_first;                         // where `first` goes, or null
+  bool close, followed;                      // sums are closed at the segments' ends; the sequences' gradients go on behind them
   float* dlog_alpha;
   double* head_sums;                         // [slot, H] when log_alpha is one to a head
-  const float *dq, *dkey;                    // [B,H,T,dk] float32 (sum_heads)
+  const float *dq, *dkey;                    // [B,H,T,dk] float32, shared heads
   void *dq_out, *dk_out;
 };
-constexpr int kFinishThreads = 128;
+constexpr int kFinishThreads = 256;
 __device__ __forceinline__ double warp_sum(double x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
-template <typename IO>
-__global__ void __launch_bounds__(kFinishThreads) la_rec_finish_kernel(FinishParams p) {
+// the decay's gradient of one (segment, head): a thread sums a run of tokens, then goes over it again
+__global__ void __launch_bounds__(kFinishThreads) la_finish_kernel(FinishParams p) {
+  la_chain();
+  constexpr int W = kFinishThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = blockIdx.x % p.seqs.H, slot = blockIdx.x / p.seqs.H;
   LaSegment s;
   const bool found = la_find(p.seqs, slot, p.seg, s, nullptr) && s.n > 0;
   if (!found) {
-    if (p.per_head && blockIdx.y == 0 && tid == 0) p.head_sums[(size_t)slot * p.seqs.H + h] = 0.;
+    if (p.per_head && tid == 0) p.head_sums[(size_t)slot * p.seqs.H + h] = 0.;
     return;
   }
   const size_t row = ((size_t)s.row_b * p.seqs.H + h) * p.seqs.T + s.start;
-  if (blockIdx.y > 0) {  // dq, dk: the value heads of a key head in their order
-    const int G = p.seqs.H / p.seqs.Hk;
-    if (h % G) return;
-    const float* src = blockIdx.y == 1 ? p.dq : p.dkey;
-    IO* dst = static_cast<IO*>(blockIdx.y == 1 ? p.dq_out : p.dk_out);
-    const size_t krow = ((size_t)s.row_b * p.seqs.Hk + h / G) * p.seqs.T + s.start;
-    const int n4 = p.dk / 4;
-    for (long long e = tid; e < (long long)s.n * n4; e += kFinishThreads) {
-      const float4* a = reinterpret_cast<const float4*>(src + row * p.dk) + e;
-      float4 x = *a;
-      for (int i = 1; i < G; ++i) {
-        const float4 y = a[(size_t)i * p.seqs.T * n4];
-        x.x += y.x;
-        x.y += y.y;
-        x.z += y.z;
-        x.w += y.w;
-      }
-      IO* d = dst + krow * p.dk + 4 * e;
-      d[0] = from_f<IO>(x.x);
-      d[1] = from_f<IO>(x.y);
-      d[2] = from_f<IO>(x.z);
-      d[3] = from_f<IO>(x.w);
-    }
-    return;
-  }
-  __shared__ double red[2][kFinishThreads / 32];
+  __shared__ double red[3][W];
   const int elems = p.dk * p.dv;
-  double border = 0.;
-  if (p.entry || p.final_state) {
-    const bool last = (long long)s.num * p.seg + s.n == s.seq_len;
-    const float* S = last ? p.final_state + ((size_t)s.seq * p.seqs.H + h) * elems
-                          : p.entry + ((size_t)(slot + 1) * p.seqs.H + h) * elems;
-    const float* B = p.behind + ((size_t)(p.behind_by_slot ? slot : s.seq) * p.seqs.H + h) * elems;
-    float2 t = make_float2(0.f, 0.f);  // (with what its roundings leave)
-    for (int e = tid; e < elems; e += kFinishThreads) {
-      const float a = S[e], b = B[e], m = a * b;
-      t = pair_add(t, make_float2(m, fmaf(a, b, -m)));
+  const float* B = s.num > 0 ? p.behind + ((size_t)(slot - 1) * p.seqs.H + h) * elems
+                   : p.first ? p.first + ((size_t)s.seq * p.seqs.H + h) * elems : nullptr;
+  if (p.copy_first && s.num == 0)
+    for (int e = tid; e < elems / 4; e += kFinishThreads)
+      reinterpret_cast<float4*>(p.copy_first + ((size_t)s.seq * p.seqs.H + h) * elems)[e] = reinterpret_cast<const float4*>(B)[e];
+  // <S, B> at the segment's start; `close`: and at its end, where it is known
+  const bool last = (long long)s.num * p.seg + s.n == s.seq_len, close = p.close && (!last || !p.followed);
+  auto product = [&](const float* a, const float* b) {
+    const float4 *S = reinterpret_cast<const float4*>(a), *G = reinterpret_cast<const float4*>(b);
+    float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int e = tid; e < elems / 4; e += kFinishThreads) {
+      const float4 x = S[e], y = G[e];
+      t[0] = fmaf(x.x, y.x, t[0]);
+      t[1] = fmaf(x.y, y.y, t[1]);
+      t[2] = fmaf(x.z, y.z, t[2]);
+      t[3] = fmaf(x.w, y.w, t[3]);
     }
-    border = warp_sum((double)t.x + (double)t.y);
-    if (lane == 0) red[0][warp] = border;
-    __syncthreads();
-    border = red[0][0] + red[0][1] + red[0][2] + red[0][3];
-  }
-  double run = border, all = 0.;
-  const int tiles = (s.n + kFinishThreads - 1) / kFinishThreads;
-  for (int tile = 0; tile < tiles; ++tile) {  // from the segment's end
-    const int t = s.n - 1 - (tile * kFinishThreads + tid);
+    return ((double)t[0] + t[1]) + ((double)t[2] + t[3]);
+  };
+  double border = 0., end = 0.;
+  if (p.entry && B) border = product(p.entry + ((size_t)(p.by_slot ? slot : s.seq) * p.seqs.H + h) * elems, B);
+  if (close && !last) end = product(p.entry + ((size_t)(slot + 1) * p.seqs.H + h) * elems, p.behind + ((size_t)slot * p.seqs.H + h) * elems);
+  const int run = (s.n + kFinishThreads - 1) / kFinishThreads, t0 = min(tid * run, s.n), t1 = min(t0 + run, s.n);
+  auto token = [&](int t) {
     double x = 0.;
-    if (t >= 0) {
-      for (int i = 0; i < p.q_parts; ++i) x += p.part_q[i * p.part_stride + row + t];
-      for (int i = 0; i < p.k_parts; ++i) x -= p.part_k[i * p.part_stride + row + t];
-    }
+    for (int i = 0; i < p.parts; ++i) x += (double)p.part_k[i * p.part_stride + row + t] - (double)p.part_q[i * p.part_stride + row + t];
+    return x;
+  };
+  double own = 0.;
+#pragma unroll 4
+  for (int t = t0; t < t1; ++t) own += token(t);
+  double x = own;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) red[1][warp] = x;
-    __syncthreads();
-    double sum = run;
-    for (int k = 0; k < kFinishThreads / 32; ++k) {
-      if (k < warp) x += red[1][k];
-      sum += red[1][k];
-    }
-    if (t >= 0) {
-      const double v = gdr_forgets(p.log_alpha[p.per_head ? (size_t)h : row + t]) ? 0. : run + x;
-      if (p.per_head) all += v;
-      else p.dlog_alpha[row + t] = (float)v;
-    }
-    run = sum;
-    __syncthreads();
+  for (int o = 1; o < 32; o <<= 1) {
+    const double y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  border = warp_sum(border);
+  end = warp_sum(end);
+  if (lane == 31) {
+    red[0][warp] = x;
+    red[1][warp] = border;
+    red[2][warp] = end;
+  }
+  __syncthreads();
+  double v = x - own, off = 0.;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    v += red[1][w];
+    if (w < warp) v += red[0][w];
+    off += red[0][w] + red[1][w] - red[2][w];
+  }
+  // what the sum over the whole segment is off by is taken out in proportion to the tokens
+  off = close ? off / s.n : 0.;
+  double all = 0.;
+#pragma unroll 4
+  for (int t = t0; t < t1; ++t) {
+    const double y = gdr_forgets(p.log_alpha[p.per_head ? (size_t)h : row + t]) ? 0. : v - off * t;
+    if (p.per_head) all += y;
+    else p.dlog_alpha[row + t] = (float)y;
+    v += token(t);
   }
   if (p.per_head) {
+    __syncthreads();
     all = warp_sum(all);
     if (lane == 0) red[0][warp] = all;
     __syncthreads();
-    if (tid == 0) p.head_sums[(size_t)slot * p.seqs.H + h] = red[0][0] + red[0][1] + red[0][2] + red[0][3];
+    if (tid == 0) {
+      double sum = 0.;
+      for (int w = 0; w < W; ++w) sum += red[0][w];
+      p.head_sums[(size_t)slot * p.seqs.H + h] = sum;
+    }
   }
 }
+// dq and dk of a key head: its value heads' in their order, four elements to a thread
+template <typename IO> __device__ __forceinline__ void store4(IO* d, float4 x);
+template <> __device__ __forceinline__ void store4<float>(float* d, float4 x) { *reinterpret_cast<float4*>(d) = x; }
+template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* d, float4 x) {
+  *reinterpret_cast<uint2*>(d) = make_uint2(sm100::pack_bf16x2(x.x, x.y), sm100::pack_bf16x2(x.z, x.w));
+}
+template <typename IO>
+__global__ void __launch_bounds__(kFinishThreads) la_heads_kernel(FinishParams p, int B) {
+  la_chain();
+  const long long e = (long long)blockIdx.x * kFinishThreads + threadIdx.x;
+  const int n4 = p.dk / 4, G = p.seqs.H / p.seqs.Hk;
+  const long long krow = e / n4;
+  if (krow >= (long long)B * p.seqs.Hk * p.seqs.T) return;
+  const long long bk = krow / p.seqs.T;
+  const int t = (int)(krow - bk * p.seqs.T);
+  if (p.seqs.starts && (t < p.seqs.starts[0] || t >= p.seqs.starts[p.seqs.n])) return;  // of no sequence
+  const float4* a = reinterpret_cast<const float4*>((blockIdx.y ? p.dkey : p.dq) + ((size_t)bk * G * p.seqs.T + t) * p.dk) + e % n4;
+  float4 x = *a;
+  for (int i = 1; i < G; ++i) {
+    const float4 y = a[(size_t)i * p.seqs.T * n4];
+    x.x += y.x;
+    x.y += y.y;
+    x.z += y.z;
+    x.w += y.w;
+  }
+  store4(static_cast<IO*>(blockIdx.y ? p.dk_out : p.dq_out) + krow * p.dk + 4 * (e % n4), x);
+}
 __global__ void __launch_bounds__(128) la_head_sum_kernel(const double* sums, int slots, int H, float* out) {
+  la_chain();
   __shared__ double red[4];
   const int h = blockIdx.x;
   double x = 0.;
@@ -544,23 +579,25 @@ int rec_segment(const LaArgs& a) {
 }
 
 template <typename IO, int NC, bool OUT>
-ll_status rec_run(const RecParams& p, int jobs, size_t slots, cudaStream_t stream) {
+ll_status rec_run(const RecParams& p, int jobs, size_t slots, cudaStream_t stream, bool after) {
   const int rows = p.job[0].rows, threads = threads_for<NC>(rows), cta = rows_for<NC>(rows);
   const size_t grid = slots * p.seqs.H * ((rows + cta - 1) / cta);
   if (grid > 0x7fffffffull) return LL_ERR_UNSUPPORTED;
-  la_rec_kernel<IO, NC, OUT><<<dim3((unsigned)grid, jobs), threads, 0, stream>>>(p);
-  LL_CUDA_OK(cudaGetLastError());
-  return LL_OK;
+  return la_launch(after, la_rec_kernel<IO, NC, OUT>, dim3((unsigned)grid, jobs), threads, 0, stream, p);
 }
 // jobs of one launch have the same numbers of rows and columns
 template <bool OUT>
-ll_status rec_launch(ll_dtype io, int cols, const RecParams& p, int jobs, size_t slots, cudaStream_t st) {
+ll_status rec_launch(ll_dtype io, int cols, const RecParams& p, int jobs, size_t slots, cudaStream_t st, bool after) {
   const bool f = io == LL_F32;
   switch (cols) {
-    case 16: return f ? rec_run<float, 16, OUT>(p, jobs, slots, st) : rec_run<__nv_bfloat16, 16, OUT>(p, jobs, slots, st);
-    case 32: return f ? rec_run<float, 32, OUT>(p, jobs, slots, st) : rec_run<__nv_bfloat16, 32, OUT>(p, jobs, slots, st);
-    case 64: return f ? rec_run<float, 64, OUT>(p, jobs, slots, st) : rec_run<__nv_bfloat16, 64, OUT>(p, jobs, slots, st);
-    case 128: return f ? rec_run<float, 128, OUT>(p, jobs, slots, st) : rec_run<__nv_bfloat16, 128, OUT>(p, jobs, slots, st);
+    case 16:
+      return f ? rec_run<float, 16, OUT>(p, jobs, slots, st, after) : rec_run<__nv_bfloat16, 16, OUT>(p, jobs, slots, st, after);
+    case 32:
+      return f ? rec_run<float, 32, OUT>(p, jobs, slots, st, after) : rec_run<__nv_bfloat16, 32, OUT>(p, jobs, slots, st, after);
+    case 64:
+      return f ? rec_run<float, 64, OUT>(p, jobs, slots, st, after) : rec_run<__nv_bfloat16, 64, OUT>(p, jobs, slots, st, after);
+    case 128:
+      return f ? rec_run<float, 128, OUT>(p, jobs, slots, st, after) : rec_run<__nv_bfloat16, 128, OUT>(p, jobs, slots, st, after);
   }
   return LL_ERR_UNSUPPORTED;
 }
@@ -601,37 +638,49 @@ RecJob job_dv(const LaArgs& a) {
 }
 size_t elems_of(const LaArgs& a) { return (size_t)a.dk * a.dv; }
 
-struct Plan {
-  int seg;
-  size_t slots, sum_s, sum_a, fin, dec, part_q, part_k, dq, dk, heads, total;
-  int q_parts;
-  bool split, states;  // more than one segment; the sums of the states are wanted
-};
-Plan fwd_plan(const LaArgs& a) {
-  Plan pl{};
-  pl.seg = rec_segment(a);
-  pl.slots = la_slots(a, pl.seg);
-  pl.split = la_split(a, pl.seg);
-  size_t at = 0;
-  auto take = [&](size_t bytes) {
-    const size_t o = at;
-    at += align_up(bytes, 256);
-    return o;
-  };
-  if (pl.split) {
-    pl.sum_s = take(pl.slots * a.H * elems_of(a) * 4);
-    pl.dec = take(pl.slots * a.H * 4);
-  }
-  pl.total = at;
-  return pl;
+ll_status carry_launch(const LaCarry& c, int sequences, cudaStream_t stream) {
+  const size_t grid = (size_t)sequences * c.seqs.H * ((c.elems / 4 + kCarryThreads - 1) / kCarryThreads);
+  if (grid > 0x7fffffffull) return LL_ERR_UNSUPPORTED;
+  return la_launch(true, la_carry_kernel, dim3((unsigned)grid, c.sums[1] ? 2 : 1), kCarryThreads, 0, stream, c);
 }
+
+// ---- in chunks: tokens of a segment, a multiple of a chunk.  More segments fill more
+// SMs, and each costs the states' way between them and the filling of its pipeline.
+constexpr int kChunk = 128;
+int tc_segment(const LaArgs& a, bool bwd) {
+  const double chunk_us = bwd ? 5. : 2.8, fill_us = 7., sum_us = 1.4;
+  const long long chunks = ((long long)a.T + kChunk - 1) / kChunk;
+  const int jobs = bwd ? 3 : 1, dirs = bwd ? 2 : 1, sms = 152;
+  double best = 1e30;
+  long long seg = chunks;
+  for (long long n = 1; n <= chunks && n <= 2 * sms; ++n) {
+    const long long per = (chunks + n - 1) / n;
+    if (bwd && per > 12 && n < chunks) continue;  // (the decay's gradient is summed over a segment)
+    const double slots = (a.n_seqs ? (double)chunks / per + a.n_seqs : (double)a.B * ((chunks + per - 1) / per)) * a.H;
+    const double waves = std::ceil(slots * jobs / sms), sum_waves = std::ceil(slots * dirs / sms);
+    double t = waves * (per * chunk_us + fill_us);
+    if (n > 1) t += sum_waves * (per * sum_us + fill_us) + 3. + 0.1 * n;
+    if (t < best) {
+      best = t;
+      seg = per;
+    }
+  }
+  return (int)std::min<long long>(seg * kChunk, (1ll << 30));
+}
+bool tc_use(const LaArgs& a, bool bwd) { return la_tc_formats(a); }
+
+struct Plan {
+  bool tc, split;  // in chunks; more than one segment
+  int seg, parts;
+  size_t slots, sum_s, sum_a, first, dec, part_q, part_k, dq, dk, heads, total;
+};
 // (the workspace cannot depend on which optional tensors a call brings)
-Plan bwd_plan(const LaArgs& a) {
+Plan plan_of(const LaArgs& a, bool bwd) {
   Plan pl{};
-  pl.seg = rec_segment(a);
+  pl.tc = tc_use(a, bwd);
+  pl.seg = pl.tc ? tc_segment(a, bwd) : rec_segment(a);
   pl.slots = la_slots(a, pl.seg);
   pl.split = la_split(a, pl.seg);
-  pl.q_parts = row_blocks(a.dk, a.dv);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -639,128 +688,148 @@ Plan bwd_plan(const LaArgs& a) {
     return o;
   };
   const size_t states = pl.slots * a.H * elems_of(a) * 4, tokens = (size_t)a.B * a.H * a.T;
-  pl.sum_s = take(states);
-  pl.sum_a = pl.split ? take(states) : 0;
-  pl.fin = take((size_t)la_sequences(a) * a.H * elems_of(a) * 4);
-  pl.dec = take(pl.slots * a.H * 4);
-  pl.part_q = take(tokens * pl.q_parts * 4);
-  pl.part_k = take(tokens * pl.q_parts * 4);
-  if (a.H != a.Hk) {
-    pl.dq = take(tokens * a.dk * 4);
-    pl.dk = take(tokens * a.dk * 4);
+  if (pl.split) {
+    pl.sum_s = take(states);
+    pl.dec = take(pl.slots * a.H * 4);
   }
-  if (a.per_head) pl.heads = take(pl.slots * a.H * 8);
+  if (bwd) {
+    pl.parts = pl.tc ? 2 : row_blocks(a.dk, a.dv);
+    if (pl.split) pl.sum_a = take(states);
+    pl.first = take((size_t)la_sequences(a) * a.H * elems_of(a) * 4);
+    pl.part_q = take(tokens * pl.parts * 4);
+    pl.part_k = take(tokens * pl.parts * 4);
+    if (a.H != a.Hk) {
+      pl.dq = take(tokens * a.dk * 4);
+      pl.dk = take(tokens * a.dk * 4);
+    }
+    if (a.per_head) pl.heads = take(pl.slots * a.H * 8);
+  }
   pl.total = at;
   return pl;
 }
 
 }  // namespace
 
-ll_status la_carry_launch(const LaCarry& c, int sequences, cudaStream_t stream) {
-  const size_t grid = (size_t)sequences * c.seqs.H * ((c.elems / 4 + kCarryThreads - 1) / kCarryThreads);
-  if (grid > 0x7fffffffull) return LL_ERR_UNSUPPORTED;
-  la_carry_kernel<<<dim3((unsigned)grid, 2), kCarryThreads, 0, stream>>>(c);
-  LL_CUDA_OK(cudaGetLastError());
-  return LL_OK;
-}
-
-size_t la_fwd_workspace(const LaArgs& a) { return fwd_plan(a).total; }
-int la_fwd_launches(const LaArgs& a) { return fwd_plan(a).split ? 3 : 1; }
+size_t la_fwd_workspace(const LaArgs& a) { return plan_of(a, false).total; }
+int la_fwd_launches(const LaArgs& a) { return plan_of(a, false).split ? 3 : 1; }
 
 ll_status la_fwd_launch(const LaArgs& a) {
-  const Plan pl = fwd_plan(a);
+  const Plan pl = plan_of(a, false);
   char* ws = static_cast<char*>(a.ws);
   RecParams p = rec_params(a, pl.seg);
   float* sums = reinterpret_cast<float*>(ws + pl.sum_s);
+  ll_status st;
   if (pl.split) {
-    p.job[0] = job_o(a);
-    p.job[0].sum = sums;
     p.log_decay = reinterpret_cast<float*>(ws + pl.dec);
-    ll_status st = rec_launch<false>(a.io, a.dk, p, 1, pl.slots, a.stream);
+    if (pl.tc) {
+      st = la_tc_sum_launch(a, pl.seg, pl.slots, 1, sums, nullptr, p.log_decay);
+    } else {
+      p.job[0] = job_o(a);
+      p.job[0].sum = sums;
+      st = rec_launch<false>(a.io, a.dk, p, 1, pl.slots, a.stream, false);
+    }
     if (st != LL_OK) return st;
-    const LaCarry c{p.seqs, pl.seg, (int)elems_of(a), {sums, nullptr}, p.log_decay, {a.state_in, nullptr},
-                    {nullptr, nullptr}, a.err};
-    st = la_carry_launch(c, la_sequences(a), a.stream);
+    const LaCarry c{p.seqs, pl.seg, (int)elems_of(a), {sums, nullptr}, p.log_decay, {a.state_in, nullptr}};
+    st = carry_launch(c, la_sequences(a), a.stream);
     if (st != LL_OK) return st;
     p.log_decay = nullptr;
   }
+  const float* in = pl.split ? sums : a.state_in;
+  if (pl.tc) return la_tc_fwd_main(a, pl.seg, pl.slots, in, pl.split, pl.split);
   p.job[0] = job_o(a);
-  p.job[0].in = pl.split ? sums : a.state_in;
+  p.job[0].in = in;
   p.job[0].in_by_slot = pl.split;
   p.job[0].out = a.o;
   p.job[0].last = a.state_out;
-  return rec_launch<true>(a.io, a.dk, p, 1, pl.slots, a.stream);
+  return rec_launch<true>(a.io, a.dk, p, 1, pl.slots, a.stream, pl.split);
 }
 
-size_t la_bwd_workspace(const LaArgs& a) { return bwd_plan(a).total; }
+size_t la_bwd_workspace(const LaArgs& a) { return plan_of(a, true).total; }
 int la_bwd_launches(const LaArgs& a) {
-  return (la_split(a, rec_segment(a)) ? 2 : 0) + (a.dk == a.dv ? 1 : 2) + 1 + (a.per_head ? 1 : 0);
+  const Plan pl = plan_of(a, true);
+  return (pl.split ? 2 : 0) + (pl.tc || a.dk == a.dv ? 1 : 2) + 1 + (a.H != a.Hk ? 1 : 0) + (a.per_head ? 1 : 0);
 }
 
 ll_status la_bwd_launch(const LaArgs& a) {
-  const Plan pl = bwd_plan(a);
+  const Plan pl = plan_of(a, true);
   char* ws = static_cast<char*>(a.ws);
   RecParams p = rec_params(a, pl.seg);
   float* sum_s = reinterpret_cast<float*>(ws + pl.sum_s);
   float* sum_a = reinterpret_cast<float*>(ws + pl.sum_a);
-  float* fin = reinterpret_cast<float*>(ws + pl.fin);
   float* dec = reinterpret_cast<float*>(ws + pl.dec);
   ll_status st;
-  const bool states = pl.split || a.dstate_out;
-  if (states) {
-    p.job[0] = job_o(a);
-    p.job[0].sum = sum_s;
-    p.job[1] = job_dv(a);
-    p.job[1].sum = sum_a;
+  if (pl.split) {
     p.log_decay = dec;
-    st = rec_launch<false>(a.io, a.dk, p, pl.split ? 2 : 1, pl.slots, a.stream);
+    if (pl.tc) {
+      st = la_tc_sum_launch(a, pl.seg, pl.slots, 2, sum_s, sum_a, dec);
+    } else {
+      p.job[0] = job_o(a);
+      p.job[0].sum = sum_s;
+      p.job[1] = job_dv(a);
+      p.job[1].sum = sum_a;
+      st = rec_launch<false>(a.io, a.dk, p, 2, pl.slots, a.stream, false);
+    }
     if (st != LL_OK) return st;
-    const LaCarry c{p.seqs, pl.seg, (int)elems_of(a), {sum_s, pl.split ? sum_a : nullptr}, dec,
-                    {a.state_in, a.dstate_out}, {fin, nullptr}, a.err};
-    st = la_carry_launch(c, la_sequences(a), a.stream);
+    const LaCarry c{p.seqs, pl.seg, (int)elems_of(a), {sum_s, sum_a}, dec, {a.state_in, a.dstate_out}};
+    st = carry_launch(c, la_sequences(a), a.stream);
     if (st != LL_OK) return st;
     p.log_decay = nullptr;
   }
-  const bool own = a.H == a.Hk;
-  RecJob v = job_dv(a), q{}, k{};
-  v.in = pl.split ? sum_a : a.dstate_out;
-  v.in_by_slot = pl.split;
-  v.out = a.dval;
-  v.last = a.dstate_in;
-  q.y = a.k;
-  q.z = a.v;
-  q.x = a.dout;
-  q.w = a.q;
-  q.y_key = true;
-  q.trans = true;
-  q.rows = a.dk;
-  q.y_scale = 1.f;
-  q.f = a.scale;
-  q.in = pl.split ? sum_s : a.state_in;
-  q.in_by_slot = pl.split;
-  q.out = own ? a.dq : ws + pl.dq;
-  q.out_f32 = !own;
-  q.part = reinterpret_cast<float*>(ws + pl.part_q);
-  k = q;
-  k.y = a.q;
-  k.z = a.dout;
-  k.x = a.v;
-  k.w = a.k;
-  k.rev = true;
-  k.y_scale = a.scale;
-  k.f = 1.f;
-  k.in = v.in;
-  k.out = own ? a.dkey : ws + pl.dk;
-  k.part = reinterpret_cast<float*>(ws + pl.part_k);
-  p.job[0] = q;
-  p.job[1] = k;
-  p.job[2] = v;
-  st = rec_launch<true>(a.io, a.dv, p, a.dk == a.dv ? 3 : 2, pl.slots, a.stream);
-  if (st != LL_OK) return st;
-  if (a.dk != a.dv) {
-    p.job[0] = v;
-    st = rec_launch<true>(a.io, a.dk, p, 1, pl.slots, a.stream);
+  const bool own = a.H == a.Hk, chained = pl.split;
+  const float* states = pl.split ? sum_s : a.state_in;
+  const float* adjoints = pl.split ? sum_a : a.dstate_out;
+  // The gradient before a sequence is what its first decay's gradient is made of with the
+  // state there, and dstate_in.  In dstate_out's place it has to wait until all have read that.
+  const bool aside = !pl.split && a.dstate_in == a.dstate_out;
+  float* first = a.dstate_in && !aside ? a.dstate_in : a.dstate_in || a.state_in ? reinterpret_cast<float*>(ws + pl.first) : nullptr;
+  float* part_q = reinterpret_cast<float*>(ws + pl.part_q);
+  float* part_k = reinterpret_cast<float*>(ws + pl.part_k);
+  float* dq32 = own ? nullptr : reinterpret_cast<float*>(ws + pl.dq);
+  float* dk32 = own ? nullptr : reinterpret_cast<float*>(ws + pl.dk);
+  if (pl.tc) {
+    st = la_tc_bwd_main(a, pl.seg, pl.slots, states, adjoints, pl.split, first, dq32, dk32, part_q, part_k, chained);
     if (st != LL_OK) return st;
+  } else {
+    RecJob v = job_dv(a), q{}, k{};
+    v.in = adjoints;
+    v.in_by_slot = pl.split;
+    v.out = a.dval;
+    v.last = first;
+    q.y = a.k;
+    q.z = a.v;
+    q.x = a.dout;
+    q.w = a.q;
+    q.y_key = true;
+    q.trans = true;
+    q.rows = a.dk;
+    q.y_scale = 1.f;
+    q.f = a.scale;
+    q.in = states;
+    q.in_by_slot = pl.split;
+    q.out = own ? a.dq : dq32;
+    q.out_f32 = !own;
+    q.part = part_q;
+    k = q;
+    k.y = a.q;
+    k.z = a.dout;
+    k.x = a.v;
+    k.w = a.k;
+    k.rev = true;
+    k.y_scale = a.scale;
+    k.f = 1.f;
+    k.in = adjoints;
+    k.out = own ? a.dkey : dk32;
+    k.part = part_k;
+    p.job[0] = q;
+    p.job[1] = k;
+    p.job[2] = v;
+    st = rec_launch<true>(a.io, a.dv, p, a.dk == a.dv ? 3 : 2, pl.slots, a.stream, chained);
+    if (st != LL_OK) return st;
+    if (a.dk != a.dv) {
+      p.job[0] = v;
+      st = rec_launch<true>(a.io, a.dk, p, 1, pl.slots, a.stream, true);
+      if (st != LL_OK) return st;
+    }
   }
   FinishParams f{};
   f.seqs = p.seqs;
@@ -768,32 +837,37 @@ ll_status la_bwd_launch(const LaArgs& a) {
   f.dk = a.dk;
   f.dv = a.dv;
   f.per_head = a.per_head;
-  f.q_parts = f.k_parts = pl.q_parts;
+  f.parts = pl.parts;
   f.part_stride = p.part_stride;
   f.log_alpha = a.log_alpha;
-  f.part_q = q.part;
-  f.part_k = k.part;
-  f.entry = states ? sum_s : nullptr;
-  f.final_state = states ? fin : nullptr;
-  f.behind = pl.split ? sum_a : a.dstate_out;
-  f.behind_by_slot = pl.split;
+  f.part_q = part_q;
+  f.part_k = part_k;
+  f.entry = states;
+  f.by_slot = pl.split;
+  f.behind = sum_a;
+  f.first = first;
+  f.copy_first = aside ? a.dstate_in : nullptr;
+  f.close = pl.tc;
+  f.followed = a.dstate_out != nullptr;
   f.dlog_alpha = a.dlog_alpha;
   f.head_sums = reinterpret_cast<double*>(ws + pl.heads);
-  f.dq = static_cast<const float*>(q.out);
-  f.dkey = static_cast<const float*>(k.out);
+  f.dq = dq32;
+  f.dkey = dk32;
   f.dq_out = a.dq;
   f.dk_out = a.dkey;
   const size_t grid = pl.slots * a.H;
   if (grid > 0x7fffffffull) return LL_ERR_UNSUPPORTED;
-  const dim3 g((unsigned)grid, own ? 1 : 3);
-  if (a.io == LL_F32) la_rec_finish_kernel<float><<<g, kFinishThreads, 0, a.stream>>>(f);
-  else la_rec_finish_kernel<__nv_bfloat16><<<g, kFinishThreads, 0, a.stream>>>(f);
-  LL_CUDA_OK(cudaGetLastError());
-  if (a.per_head) {
-    la_head_sum_kernel<<<a.H, 128, 0, a.stream>>>(f.head_sums, (int)pl.slots, a.H, a.dlog_alpha);
-    LL_CUDA_OK(cudaGetLastError());
+  st = la_launch(true, la_finish_kernel, dim3((unsigned)grid), kFinishThreads, 0, a.stream, f);
+  if (st == LL_OK && !own) {
+    const long long blocks = ((long long)a.B * a.Hk * a.T * (a.dk / 4) + kFinishThreads - 1) / kFinishThreads;
+    if (blocks > 0x7fffffffll) return LL_ERR_UNSUPPORTED;
+    const dim3 g((unsigned)blocks, 2);
+    st = a.io == LL_F32 ? la_launch(true, la_heads_kernel<float>, g, kFinishThreads, 0, a.stream, f, a.B)
+                        : la_launch(true, la_heads_kernel<__nv_bfloat16>, g, kFinishThreads, 0, a.stream, f, a.B);
   }
-  return LL_OK;
+  if (st != LL_OK || !a.per_head) return st;
+  const double* sums = f.head_sums;
+  return la_launch(true, la_head_sum_kernel, dim3((unsigned)a.H), 128, 0, a.stream, sums, (int)pl.slots, a.H, a.dlog_alpha);
 }
 
 }  // namespace llattn

@@ -31,7 +31,8 @@ def forward(q, k, v, log_alpha, scale=1.0, state=None):
 
 def backward(q, k, v, log_alpha, dout, scale=1.0, state=None, dstate=None):
     """Gradients of sum(o . dout) + sum(S_T . dstate): a dict with dq, dk, dv,
-    dlog_alpha, dstate_in."""
+    dlog_alpha, dstate_in; and "terms" [T], the 2-norm of the products that a token's
+    dlog_alpha = sum(alpha_t S_{t-1} * A_t) is the sum of."""
     q, k, v, la, do = _f(q, k, v, log_alpha, dout)
     S = np.zeros((v.shape[1], k.shape[1])) if state is None else np.array(state, np.float64)
     before = []
@@ -39,7 +40,7 @@ def backward(q, k, v, log_alpha, dout, scale=1.0, state=None, dstate=None):
         before.append(S)
         S = np.exp(la[t]) * S + np.outer(v[t], k[t])
     A = np.zeros_like(S) if dstate is None else np.array(dstate, np.float64)
-    g = {n: np.zeros_like(x) for n, x in (("dq", q), ("dk", k), ("dv", v), ("dlog_alpha", la))}
+    g = {n: np.zeros_like(x) for n, x in (("dq", q), ("dk", k), ("dv", v), ("dlog_alpha", la), ("terms", la))}
     for t in reversed(range(len(q))):
         a = np.exp(la[t])
         g["dq"][t] = scale * ((a * before[t] + np.outer(v[t], k[t])).T @ do[t])
@@ -47,6 +48,7 @@ def backward(q, k, v, log_alpha, dout, scale=1.0, state=None, dstate=None):
         g["dv"][t] = A @ k[t]
         g["dk"][t] = A.T @ v[t]
         g["dlog_alpha"][t] = a * np.sum(A * before[t])
+        g["terms"][t] = a * np.sqrt(np.sum((A * before[t]) ** 2))
         A = a * A
     g["dstate_in"] = A
     return g
