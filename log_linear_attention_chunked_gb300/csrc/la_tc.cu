@@ -37,7 +37,7 @@ namespace {
 
 using namespace gdrtc;
 
-// Bounded wait, as a call: inlined, the waits alone were a fifth of the code.
+// Bounded wait, as a call.
 static __device__ __noinline__ void wait_at(uint32_t bar, uint32_t par, unsigned* err) {
   const uint64_t t0 = globaltimer_ns();
   uint32_t ok;
@@ -54,6 +54,17 @@ static __device__ __noinline__ void wait_at(uint32_t bar, uint32_t par, unsigned
       return;
     }
   } while (!ok);
+}
+__device__ __forceinline__ bool try_wait_at(uint32_t bar, uint32_t par) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(par)
+      : "memory");
+  return ok != 0;
 }
 // A group waits by one of its warps, the others at a named barrier: twenty warps that poll took most of
 // the issue slots, and the products and the scores beside them twice their time (18 thousand cycles a chunk
@@ -133,79 +144,121 @@ struct Tab {
   float2 decay;         // of the state: M <- x M + y M
 };
 static_assert(sizeof(Tab) <= 2624, "");
-// One warp, a token of each block of 32 to a lane; la: theirs, n: the tokens that are there
+// One warp, four neighbouring tokens to a lane; la: theirs
 struct ChunkLog {
-  long long block[4];   // from the block's first token to this one, inclusive
-  long long sum[4];     // of the blocks
+  long long past[4];    // from the chunk's first token to this one, inclusive
+  long long first, sum; // in front of this lane's block; of the block
   long long total;
-  bool nan;
+  float bad;            // 0, or NaN
 };
 __device__ __forceinline__ ChunkLog chunk_log(const float* la, int lane) {
   ChunkLog g;
   bool nan = false;
+  long long x = 0;
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    nan = nan || la[b] != la[b];
-    g.block[b] = __float2ll_rn(fminf(la[b], 1e4f) * 68719476736.f);
+  for (int e = 0; e < 4; ++e) {
+    nan = nan || la[e] != la[e];
+    x += __float2ll_rn(fminf(la[e], 1e4f) * 68719476736.f);
+    g.past[e] = x;
   }
-#pragma unroll 1
+  long long y = x;
+#pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const long long y = __shfl_up_sync(0xffffffffu, g.block[b], o);
-      if (lane >= o) g.block[b] += y;
-    }
+    const long long z = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) y += z;
   }
 #pragma unroll
-  for (int b = 0; b < 4; ++b) g.sum[b] = __shfl_sync(0xffffffffu, g.block[b], 31);
-  g.total = (g.sum[0] + g.sum[1]) + (g.sum[2] + g.sum[3]);
-  g.nan = __any_sync(0xffffffffu, nan);
+  for (int e = 0; e < 4; ++e) g.past[e] += y - x;
+  g.first = __shfl_sync(0xffffffffu, y - x, lane & 24);
+  g.sum = __shfl_sync(0xffffffffu, y, lane | 7) - g.first;
+  g.total = __shfl_sync(0xffffffffu, y, 31);
+  g.bad = __any_sync(0xffffffffu, nan) ? __int_as_float(0x7fffffff) : 0.f;
   return g;
 }
-template <bool REV>  // the weights of absent tokens are zero
-__device__ __forceinline__ void write_tab(Tab* t, const ChunkLog& g, int lane, int n, float scale) {
-  const float bad = g.nan ? __int_as_float(0x7fffffff) : 0.f;
-  long long before = 0;
-#pragma unroll 1
-  for (int b = 0; b < 4; ++b) {
-    const int i = 32 * b + lane;
-    const long long block = b == 0 ? g.block[0] : b == 1 ? g.block[1] : b == 2 ? g.block[2] : g.block[3];
-    const long long sum = b == 0 ? g.sum[0] : b == 1 ? g.sum[1] : b == 2 ? g.sum[2] : g.sum[3];
-    const float2 p = log2_pair(block, bad);
-    const long long past = before + block;
-    const float to = expf(log_float(past) + bad), from = expf(log_float(g.total - past) + bad);
-    t->in_block[i] = p;
-    t->col[i] = ex2(REV ? p.x : log_float(sum - block) * kLog2e) + bad;
-    t->c1[i] = REV ? from : scale * to;
-    t->weight[i] = i >= n ? 0.f : REV ? scale * to : from;
-    if (lane == 31) t->blk[b] = p;
-    before += sum;
-  }
+// a token's entries (an absent token's weight is zero)
+struct TabEntry {
+  float2 in_block;
+  float col, c1, weight;
+};
+template <bool REV>
+__device__ __forceinline__ TabEntry make_entry(const ChunkLog& g, long long past, bool there, float scale) {
+  TabEntry t;
+  const long long block = past - g.first;
+  const float to = expf(log_float(past) + g.bad), from = expf(log_float(g.total - past) + g.bad);
+  t.in_block = log2_pair(block, g.bad);
+  t.col = ex2(REV ? t.in_block.x : log_float(g.sum - block) * kLog2e) + g.bad;
+  t.c1 = REV ? from : scale * to;
+  t.weight = !there ? 0.f : REV ? scale * to : from;
+  return t;
+}
+__device__ __forceinline__ void store_whole(Tab* tab, const ChunkLog& g, int lane) {
+  if ((lane & 7) == 0) tab->blk[lane >> 3] = log2_pair(g.sum, g.bad);
   if (lane == 0) {
-    const LaDecay d = la_decay(log_float(g.total) + bad);
-    t->decay = make_float2(d.f, d.near ? 1.f : 0.f);
+    const LaDecay d = la_decay(log_float(g.total) + g.bad);
+    tab->decay = make_float2(d.f, d.near ? 1.f : 0.f);
   }
+}
+// Made at once, or (SHORT) one after another once the groups are done with the last ones.
+template <bool REV>
+__device__ __forceinline__ void store_short(Tab* tab, const ChunkLog& g, int lane, int n, float scale) {
+#pragma unroll 1
+  for (int e = 0; e < 4; ++e) {
+    const int i = 4 * lane + e;
+    const TabEntry t = make_entry<REV>(g, e == 0 ? g.past[0] : e == 1 ? g.past[1] : e == 2 ? g.past[2] : g.past[3], i < n, scale);
+    tab->in_block[i] = t.in_block;
+    tab->col[i] = t.col;
+    tab->c1[i] = t.c1;
+    tab->weight[i] = t.weight;
+  }
+  store_whole(tab, g, lane);
+}
+__device__ __forceinline__ void store_tab(Tab* tab, const TabEntry* t, const ChunkLog& g, int lane) {
+  float4* p = reinterpret_cast<float4*>(tab->in_block + 4 * lane);
+  p[0] = make_float4(t[0].in_block.x, t[0].in_block.y, t[1].in_block.x, t[1].in_block.y);
+  p[1] = make_float4(t[2].in_block.x, t[2].in_block.y, t[3].in_block.x, t[3].in_block.y);
+  *reinterpret_cast<float4*>(tab->col + 4 * lane) = make_float4(t[0].col, t[1].col, t[2].col, t[3].col);
+  *reinterpret_cast<float4*>(tab->c1 + 4 * lane) = make_float4(t[0].c1, t[1].c1, t[2].c1, t[3].c1);
+  *reinterpret_cast<float4*>(tab->weight + 4 * lane) = make_float4(t[0].weight, t[1].weight, t[2].weight, t[3].weight);
+  store_whole(tab, g, lane);
 }
 
 // Products over operands in 128-row tiles; the descriptor of the first k-step is made once and the others
 // are sums with constants (made anew each they took the issuing thread 125 cycles an instruction, twice what
-// it takes to run).  Not inlined: see run_job on the length of the code.  N = 64: the second block is not there, or its rows of the result are not used.
-template <int K> static __device__ __noinline__ void mma_kk(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool add) {  // both K-major
+// it takes to run).  N = 64: the second block is not there, or its rows of the result are not used.
+template <int K> __device__ __forceinline__ void mma_kk_body(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool add) {  // both K-major
   const uint64_t da = desc_k(a, 0), db = desc_k(b, 0);
 #pragma unroll
   for (int kk = 0; kk < K / 16; ++kk)
     umma_bf16(d, da + step_of<kAlong>(kk), db + step_of<kAlong>(kk), id, (add || kk > 0) ? 1u : 0u);
 }
-static __device__ __noinline__ void mma_mm(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool add) {  // K down the rows of both
+__device__ __forceinline__ void mma_mm_body(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool add) {  // K down the rows of both
   const uint64_t da = desc_mn(a, 0), db = desc_mn(b, 0);
 #pragma unroll
   for (int kk = 0; kk < kC / 16; ++kk)
     umma_bf16(d, da + step_of<kDown>(kk), db + step_of<kDown>(kk), id, (add || kk > 0) ? 1u : 0u);
 }
-static __device__ __noinline__ void mma_tm(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t id) {  // A in tensor memory
+__device__ __forceinline__ void mma_tm_body(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t id) {  // A in tensor memory
   const uint64_t db = desc_mn(b, 0);
 #pragma unroll
   for (int kk = 0; kk < kC / 16; ++kk) umma_bf16_ta(d, a_tmem + kk * 8, db + step_of<kDown>(kk), id, kk > 0 ? 1u : 0u);
+}
+// SHORT: as calls (see run_job on the length of the code)
+template <int K> static __device__ __noinline__ void mma_kk_call(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool add) {
+  mma_kk_body<K>(d, a, b, id, add);
+}
+static __device__ __noinline__ void mma_mm_call(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool add) { mma_mm_body(d, a, b, id, add); }
+static __device__ __noinline__ void mma_tm_call(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t id) { mma_tm_body(d, a_tmem, b, id); }
+template <bool SHORT, int K> __device__ __forceinline__ void mma_kk(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool add) {
+  if (SHORT) mma_kk_call<K>(d, a, b, id, add);
+  else mma_kk_body<K>(d, a, b, id, add);
+}
+template <bool SHORT> __device__ __forceinline__ void mma_mm(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool add) {
+  if (SHORT) mma_mm_call(d, a, b, id, add);
+  else mma_mm_body(d, a, b, id, add);
+}
+template <bool SHORT> __device__ __forceinline__ void mma_tm(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t id) {
+  if (SHORT) mma_tm_call(d, a_tmem, b, id);
+  else mma_tm_body(d, a_tmem, b, id);
 }
 
 // ---- pairs of floats
@@ -264,13 +317,15 @@ static __device__ __noinline__ void zero_rows(unsigned char* tile, uint32_t full
 // Tiles go through a ring of buffers in the order of use.  Of the buffers that are left one
 // holds the state and another its low part, and once q M^T is done that of k' (k' high takes k's place).
 // The output is staged in v's place, with NT = 4 in w's.  The roles' code is kept short, in loops: unrolled
-// (90 KB) it left the instruction cache and every phase waited for its instructions.  What a chunk adds
+// (90 KB) it left the instruction cache and every phase waited for its instructions.  With NT = 4 it has to be
+// shorter still, products and waits as calls (SHORT: 155 us where 190, 63 % of requests hit instead of 52; without
+// them the forward takes 57 us where 69).  What a chunk adds
 // to the state is summed by itself in tensor memory and added to the state in registers: the tensor
 // cores' sums round towards zero, which over the chunks of a long memory adds up (6e-6 of a state
 // at 16384 tokens).  The chain from chunk to chunk is this addition alone.
 //
 // Only the state on entry comes from the kernels before: everything else starts without them.
-template <int DX, int DY, int NT, bool REV>
+template <int DX, int DY, int NT, bool REV, bool SHORT>
 __device__ __forceinline__ void run_job(const TcParams& p, const TcJob& job, const CUtensorMap* mq, const CUtensorMap* mk,
                                         const CUtensorMap* mv, const CUtensorMap* mw, const CUtensorMap* mo, bool q_key,
                                         bool k_key, bool v_key, bool w_key, bool trans, const LaSegment& sg, int slot, int h,
@@ -301,6 +356,9 @@ __device__ __forceinline__ void run_job(const TcParams& p, const TcJob& job, con
   };
   auto buf = [&](int j) { return rb + j >= kRing ? rb + j - kRing : rb + j; };
   auto par = [&](int j) { return (rb + j >= kRing ? rn + 1 : rn) & 1; };
+  auto wait = [&](int b, uint32_t parity) {
+    if (SHORT || !try_wait_at(sbars + 8 * b, parity)) wait_at(sbars + 8 * b, parity, p.err);
+  };
   constexpr int Q = 0, K = 1, V = 2, W = 3, OUT = LO ? W : V;
 
   if (tid == 0) {
@@ -326,7 +384,7 @@ __device__ __forceinline__ void run_job(const TcParams& p, const TcJob& job, con
 #pragma unroll 1
         for (int j = 0; j < NT; ++j) {
           const int b = buf(j), n = rb + j >= kRing ? rn + 1 : rn;
-          if (n > 0) wait_at(sbars + 8 * (kEmpty + b), (n - 1) & 1, p.err);
+          if (n > 0) wait(kEmpty + b, (n - 1) & 1);
           const CUtensorMap* m = j == W ? mw : j == Q ? mq : j == K ? mk : mv;
           const bool key = j == W ? w_key : j == Q ? q_key : j == K ? k_key : v_key;
           const int cols = j == W || j == V ? DY : DX;
@@ -344,38 +402,38 @@ __device__ __forceinline__ void run_job(const TcParams& p, const TcJob& job, con
       for (int x = 0; x < chunks; ++x, next_chunk()) {
         const int ph = x & 1;
         const uint32_t q = sbuf + buf(Q) * kTile, k = sbuf + buf(K) * kTile, v = sbuf + buf(V) * kTile;
-        wait_at(sbars + 8 * (kFull + buf(Q)), par(Q), p.err);
-        wait_at(sbars + 8 * (kFull + buf(K)), par(K), p.err);
+        wait(kFull + buf(Q), par(Q));
+        wait(kFull + buf(K), par(K));
         tc_fence_after();
-        mma_kk<DX>(tmem + kTmP, q, k, idesc_bf16(128, kC, false, false), false);
+        mma_kk<SHORT, DX>(tmem + kTmP, q, k, idesc_bf16(128, kC, false, false), false);
         if (LO) {
-          if (x > 0) wait_at(sbars + 8 * (kRead), (x - 1) & 1, p.err);  // the last outputs have been read
-          wait_at(sbars + 8 * (kFull + buf(W)), par(W), p.err);
-          wait_at(sbars + 8 * (kFull + buf(V)), par(V), p.err);
+          if (x > 0) wait(kRead, (x - 1) & 1);  // the last outputs have been read
+          wait(kFull + buf(W), par(W));
+          wait(kFull + buf(V), par(V));
           tc_fence_after();
-          mma_kk<DY>(tmem + kTmO2, sbuf + buf(W) * kTile, v, idesc_bf16(128, kC, false, false), false);
+          mma_kk<SHORT, DY>(tmem + kTmO2, sbuf + buf(W) * kTile, v, idesc_bf16(128, kC, false, false), false);
         }
         umma_commit(bars + kS1);
-        wait_at(sbars + 8 * (kMb), ph, p.err);
-        if (!LO && x > 0) wait_at(sbars + 8 * (kRead), (x - 1) & 1, p.err);
+        wait(kMb, ph);
+        if (!LO && x > 0) wait(kRead, (x - 1) & 1);
         tc_fence_after();
-        mma_kk<DX>(tmem + kTmO1, q, smb, idesc_bf16(128, DY, false, false), false);
-        if (LO) mma_kk<DX>(tmem + kTmO1, q, low, idesc_bf16(128, DY, false, false), true);
+        mma_kk<SHORT, DX>(tmem + kTmO1, q, smb, idesc_bf16(128, DY, false, false), false);
+        if (LO) mma_kk<SHORT, DX>(tmem + kTmO1, q, low, idesc_bf16(128, DY, false, false), true);
         umma_commit(bars + kS2);
         umma_commit(bars + kEmpty + buf(Q));
         auto output = [&]() {
-          wait_at(sbars + 8 * (kP), ph, p.err);
+          wait(kP, ph);
           tc_fence_after();
-          mma_tm(tmem + kTmO2, tmem + kTmPb, v, idesc_bf16(128, DY, false, true));
+          mma_tm<SHORT>(tmem + kTmO2, tmem + kTmPb, v, idesc_bf16(128, DY, false, true));
           umma_commit(bars + kS3);
         };
         if (LO) output();
-        wait_at(sbars + 8 * (kKp), ph, p.err);
-        if (!LO) wait_at(sbars + 8 * (kFull + buf(V)), par(V), p.err);
+        wait(kKp, ph);
+        if (!LO) wait(kFull + buf(V), par(V));
         tc_fence_after();
-        mma_mm(tmem + kTmM, v, k, idesc_bf16(128, DX, true, true), false);
-        mma_mm(tmem + kTmM, v, low, idesc_bf16(128, DX, true, true), true);
-        if (LO) mma_mm(tmem + kTmM, v, smb, idesc_bf16(128, DX, true, true), true);
+        mma_mm<SHORT>(tmem + kTmM, v, k, idesc_bf16(128, DX, true, true), false);
+        mma_mm<SHORT>(tmem + kTmM, v, low, idesc_bf16(128, DX, true, true), true);
+        if (LO) mma_mm<SHORT>(tmem + kTmM, v, smb, idesc_bf16(128, DX, true, true), true);
         umma_commit(bars + kS4);
         umma_commit(bars + kEmpty + buf(K));
         if (LO) umma_commit(bars + kEmpty + buf(V));
@@ -387,7 +445,7 @@ __device__ __forceinline__ void run_job(const TcParams& p, const TcJob& job, con
 #pragma unroll 1
       for (int x = 0; x < chunks; ++x, next_chunk()) {
         const int t0 = chunk_at(x) * kC;
-        wait_at(sbars + 8 * (kStaged), x & 1, p.err);
+        wait(kStaged, x & 1);
         if (!job.out_f32 && sg.n - t0 >= kC) {
           for (int c = 0; c < DY / 64; ++c) tma_store_2d(mo, s + buf(OUT) * kTile + c * kHalf, 64 * c, (int)(row + t0));
           bulk_commit();
@@ -404,7 +462,7 @@ __device__ __forceinline__ void run_job(const TcParams& p, const TcJob& job, con
     auto load = [&](int x) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int t = chunk_at(x) * kC + 32 * e + lane;
+        const int t = chunk_at(x) * kC + 4 * lane + e;
         next[e] = t < sg.n ? la_log(la[p.per_head ? 0 : t]) : 0.f;
       }
     };
@@ -412,12 +470,18 @@ __device__ __forceinline__ void run_job(const TcParams& p, const TcJob& job, con
 #pragma unroll 1
     for (int x = 0; x < chunks; ++x) {
       const ChunkLog g = chunk_log(next, lane);
+      const int n = min(kC, sg.n - chunk_at(x) * kC);
+      TabEntry t[4];
+      if (!SHORT)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] = make_entry<REV>(g, g.past[e], 4 * lane + e < n, p.scale);
       if (x + 1 < chunks) load(x + 1);
       if (x > 0) {  // the groups are done with the last chunk's
-        wait_at(sbars + 8 * (kP), (x - 1) & 1, p.err);
-        wait_at(sbars + 8 * (kKp), (x - 1) & 1, p.err);
+        wait(kP, (x - 1) & 1);
+        wait(kKp, (x - 1) & 1);
       }
-      write_tab<REV>(tab, g, lane, min(kC, sg.n - chunk_at(x) * kC), p.scale);
+      if (SHORT) store_short<REV>(tab, g, lane, n, p.scale);
+      else store_tab(tab, t, g, lane);
       mbar_arrive(bars + kTab);
     }
   } else if (warp >= kStateWarp) {
@@ -451,7 +515,7 @@ __device__ __forceinline__ void run_job(const TcParams& p, const TcJob& job, con
     for (int x = 0;; ++x, next_chunk()) {
       const int ph = x & 1, t0 = chunk_at(x) * kC, n = min(kC, sg.n - t0);
       if (x > 0) {  // M <- decay M + what the chunk before added; near 1 the decay as M + expm1 M (la.cuh)
-        LL_GROUP_WAIT(warp == kStateWarp, kBarState, kStateThreads, wait_at(sbars + 8 * (kS4), (x - 1) & 1, p.err));
+        LL_GROUP_WAIT(warp == kStateWarp, kBarState, kStateThreads, wait(kS4, (x - 1) & 1));
         tc_fence_after();
         const f2 df = pair(d.x, d.x);
         const bool near = d.y != 0.f;
@@ -494,9 +558,9 @@ __device__ __forceinline__ void run_job(const TcParams& p, const TcJob& job, con
       // k' high in k's place, low in that of the state's low part
       unsigned char* kb = s + buf(K) * kTile;
       LL_GROUP_WAIT(warp == kStateWarp, kBarState, kStateThreads, {
-        wait_at(sbars + 8 * (kTab), ph, p.err);
-        wait_at(sbars + 8 * ((LO ? kS2 : kS1)), ph, p.err);
-        wait_at(sbars + 8 * (kFull + buf(K)), par(K), p.err);  // (long complete: the copy's writes, seen from here)
+        wait(kTab, ph);
+        wait((LO ? kS2 : kS1), ph);
+        wait(kFull + buf(K), par(K));  // (long complete: the copy's writes, seen from here)
       });
       const float weight = tab->weight[i];
       d = tab->decay;
@@ -551,8 +615,8 @@ __device__ __forceinline__ void run_job(const TcParams& p, const TcJob& job, con
     for (int x = 0; x < chunks; ++x, next_chunk()) {
       const int ph = x & 1, t0 = chunk_at(x) * kC, n = min(kC, sg.n - t0);
       LL_GROUP_WAIT(warp == 0, kBarRows, kRowThreads, {
-        wait_at(sbars + 8 * (kTab), ph, p.err);
-        wait_at(sbars + 8 * (kS1), ph, p.err);
+        wait(kTab, ph);
+        wait(kS1, ph);
       });
       tc_fence_after();
       const float2 own_log = tab->in_block[i];
@@ -640,9 +704,9 @@ __device__ __forceinline__ void run_job(const TcParams& p, const TcJob& job, con
       if (LO && n < kC) fence_proxy_async_shared();
       mbar_arrive(bars + kP);
       LL_GROUP_WAIT(warp == 0, kBarRows, kRowThreads, {
-        wait_at(sbars + 8 * (kS3), ph, p.err);
-        if (LO) wait_at(sbars + 8 * (kFull + buf(W)), par(W), p.err);
-        if (x > 0) wait_at(sbars + 8 * (kStored), (x - 1) & 1, p.err);  // (the stores never fall two chunks behind)
+        wait(kS3, ph);
+        if (LO) wait(kFull + buf(W), par(W));
+        if (x > 0) wait(kStored, (x - 1) & 1);  // (the stores never fall two chunks behind)
       });
       tc_fence_after();
       f2 dot = 0ull;
@@ -735,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_fwd_kernel(const __grid_con
   int slot, h;
   if (!enter(p, blockIdx.x, sg, slot, h, s)) return;
   if (sg.n == 0) return copy_state(p, p.job[0], sg, slot, h);
-  run_job<DK, DV, 3, false>(p, p.job[0], &m.q, &m.k, &m.v, nullptr, &m.o, true, true, false, false, false, sg, slot, h, s);
+  run_job<DK, DV, 3, false, false>(p, p.job[0], &m.q, &m.k, &m.v, nullptr, &m.o, true, true, false, false, false, sg, slot, h, s);
 }
 
 // dq, dv, dk of one segment and head side by side: they read the same tiles
@@ -750,9 +814,9 @@ __global__ void __launch_bounds__(kThreads, 1) la_tc_bwd_kernel(const __grid_con
     if (what == 1) copy_state(p, p.job[1], sg, slot, h);
     return;
   }
-  if (what == 0) run_job<DV, DK, 4, false>(p, p.job[0], &m.dout, &m.v, &m.k, &m.q, &m.dq, false, false, true, true, true, sg, slot, h, s);
-  else if (what == 1) run_job<DK, DV, 4, true>(p, p.job[1], &m.k, &m.q, &m.dout, &m.v, &m.dv, true, true, false, false, false, sg, slot, h, s);
-  else run_job<DV, DK, 3, true>(p, p.job[2], &m.v, &m.dout, &m.q, nullptr, &m.dk, false, false, true, false, true, sg, slot, h, s);
+  if (what == 0) run_job<DV, DK, 4, false, true>(p, p.job[0], &m.dout, &m.v, &m.k, &m.q, &m.dq, false, false, true, true, true, sg, slot, h, s);
+  else if (what == 1) run_job<DK, DV, 4, true, true>(p, p.job[1], &m.k, &m.q, &m.dout, &m.v, &m.dv, true, true, false, false, false, sg, slot, h, s);
+  else run_job<DV, DK, 3, true, true>(p, p.job[2], &m.v, &m.dout, &m.q, nullptr, &m.dk, false, false, true, false, true, sg, slot, h, s);
 }
 
 // ---------------------------------------------------------------- sums of the segments
@@ -847,9 +911,9 @@ __global__ void __launch_bounds__(kSumThreads, 1) la_tc_sum_kernel(const __grid_
         wait_bar(bars + bv, n & 1, p.err);
         wait_bar(bars + kReady, x & 1, p.err);
         tc_fence_after();
-        mma_mm(acc, sbuf + bv * kTile, sbuf + bk * kTile, idesc_bf16(128, DK, true, true), false);
-        mma_mm(acc, sbuf + bv * kTile, sbuf + kSumRing * kTile, idesc_bf16(128, DK, true, true), true);
-        if (PARTS == 3) mma_mm(acc, sbuf + bv * kTile, sbuf + (kSumRing + 1) * kTile, idesc_bf16(128, DK, true, true), true);
+        mma_mm<false>(acc, sbuf + bv * kTile, sbuf + bk * kTile, idesc_bf16(128, DK, true, true), false);
+        mma_mm<false>(acc, sbuf + bv * kTile, sbuf + kSumRing * kTile, idesc_bf16(128, DK, true, true), true);
+        if (PARTS == 3) mma_mm<false>(acc, sbuf + bv * kTile, sbuf + (kSumRing + 1) * kTile, idesc_bf16(128, DK, true, true), true);
         umma_commit(bars + kSumRing + bk);
         umma_commit(bars + kSumRing + bv);
         umma_commit(bars + kDone);
@@ -860,7 +924,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) la_tc_sum_kernel(const __grid_
     auto load = [&](int x) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int t = chunk_at(x) * kC + 32 * e + lane;
+        const int t = chunk_at(x) * kC + 4 * lane + e;
         next[e] = t < sg.n ? la_log(la[p.per_head ? 0 : t]) : 0.f;
       }
     };
@@ -872,18 +936,15 @@ __global__ void __launch_bounds__(kSumThreads, 1) la_tc_sum_kernel(const __grid_
       const ChunkLog g = chunk_log(next, lane);
       const int n = min(kC, sg.n - chunk_at(x) * kC);
       if (x + 1 < chunks) load(x + 1);
-      if (g.nan) bad = __int_as_float(0x7fffffff);
+      bad += g.bad;
       float w[4];
-      long long past = run + (dir ? 0 : g.total);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        w[e] = expf(log_float(dir ? past + g.block[e] : past - g.block[e]) + bad) * (dir ? p.scale : 1.f);
-        if (32 * e + lane >= n) w[e] = 0.f;
-        past += dir ? g.sum[e] : -g.sum[e];
+        w[e] = expf(log_float(run + (dir ? g.past[e] : g.total - g.past[e])) + bad) * (dir ? p.scale : 1.f);
+        if (4 * lane + e >= n) w[e] = 0.f;
       }
       if (x > 0) wait_bar(bars + kReady, (x - 1) & 1, p.err);  // the rows have read the last chunk's
-#pragma unroll
-      for (int e = 0; e < 4; ++e) weights[32 * e + lane] = w[e];
+      *reinterpret_cast<float4*>(weights + 4 * lane) = make_float4(w[0], w[1], w[2], w[3]);
       run = min(max(run + g.total, -((long long)1 << 60)), (long long)1 << 60);
       mbar_arrive(bars + kWeights);
     }
