@@ -4,8 +4,10 @@
 // Every named state is read and written once, 4 dk dv bytes each way, and that
 // bounds it.  A warp takes kRows x (32 / lanes of a row) rows of one state and has
 // all of their loads in flight at once, 16 bytes a lane and 512 bytes in a row;
-// gates, keys and sines are made while they travel.  The rows' sums over the lanes
-// are taken together: each step of the butterfly halves the rows a lane carries.
+// meanwhile the CTA's threads make the turned key and query, an element each.  The rows'
+// sums over the lanes are taken together: each step of the butterfly halves the rows a lane carries.
+// Four warps to a CTA and six CTAs to an SM: B 64, 32 heads of 128 x 128, 47 us, 84 % of the measured HBM rate;
+// with 85 registers (five CTAs) 61, eight CTAs 50, a CTA to a whole state 52.
 #include "la.cuh"
 #include "rope.cuh"
 
@@ -13,7 +15,7 @@ namespace llattn {
 namespace {
 
 constexpr int kRows = 8;    // 16-byte loads of a lane
-constexpr int kWarps = 4;
+constexpr int kWarps = 4;   // at most, of a CTA
 
 struct StepParams {
   int B, H, Hk, dv, parts, n_slots, per_head, rot, interleaved;
@@ -25,55 +27,41 @@ struct StepParams {
   unsigned* err;
 };
 
-template <typename IO> __device__ __forceinline__ void load4(const IO* p, float* x);
-template <> __device__ __forceinline__ void load4<float>(const float* p, float* x) {
+__device__ __forceinline__ void load4(const float* p, float* x) {
   const float4 v = *reinterpret_cast<const float4*>(p);
   x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
 }
-template <> __device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16* p, float* x) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xffff0000u);
-  x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xffff0000u);
-}
 
-// elements i0 .. i0 + 3 of a head, turned
+// element i of a head, turned to position `pos`
 template <typename IO>
-__device__ __forceinline__ void turned(const IO* row, int i0, const StepParams& p, const float* s, const float* c, float* x) {
-  load4(row + i0, x);
+__device__ __forceinline__ float turned(const IO* row, int i, long long pos, const StepParams& p) {
+  const float x = to_f(row[i]);
+  if (i >= p.rot) return x;
   const int half = p.rot / 2;
-  if (p.interleaved) {
-#pragma unroll
-    for (int e = 0; e < 4; e += 2)
-      if (i0 + e < p.rot) {
-        const float a = x[e], b = x[e + 1];
-        x[e] = a * c[e] - b * s[e];
-        x[e + 1] = fmaf(a, s[e], b * c[e]);
-      }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = i0 + e;
-      if (i < half) x[e] = x[e] * c[e] - to_f(row[i + half]) * s[e];
-      else if (i < p.rot) x[e] = fmaf(to_f(row[i - half]), s[e], x[e] * c[e]);
-    }
-  }
+  const bool second = p.interleaved ? i & 1 : i >= half;
+  const int pair = p.interleaved ? i >> 1 : second ? i - half : i;
+  const float y = to_f(row[p.interleaved ? i ^ 1 : second ? i - half : i + half]);
+  float s, c;
+  rope_sincos(pos, rope_turns(p.inv_freq[pair]), s, c);
+  s *= p.amp;
+  c *= p.amp;
+  return second ? fmaf(y, s, x * c) : x * c - y * s;
 }
 
 template <typename IO, int DK>
-__global__ void __launch_bounds__(32 * kWarps) la_step_kernel(StepParams p, const IO* q, const IO* k, const IO* v, IO* o) {
+__global__ void __launch_bounds__(32 * kWarps, 6) la_step_kernel(StepParams p, const IO* q, const IO* k, const IO* v, IO* o) {
   constexpr int LPR = DK / 4, RPI = 32 / LPR;  // lanes of a row, rows of a load
-  const int lane = threadIdx.x & 31, l = lane % LPR, i0 = 4 * l;
-  const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (unit >= (long long)p.B * p.H * p.parts) return;
-  const int part = (int)(unit % p.parts);
-  const long long bh = unit / p.parts;
+  __shared__ __align__(16) float qk[2 * DK];
+  const int lane = threadIdx.x & 31, l = lane % LPR, i0 = 4 * l, warps = blockDim.x >> 5;
+  const int part = (int)(blockIdx.x % (unsigned)p.parts);
+  const long long bh = blockIdx.x / (unsigned)p.parts;
   const int h = (int)(bh % p.H), b = (int)(bh / p.H);
   const long long slot = p.slots ? p.slots[b] : b;
   if (slot < 0 || slot >= p.n_slots) {  // -1 is a row of padding; anything else out of range an error
-    if (slot != -1 && lane == 0) raise_error(p.err, kErrDeviceArg);
+    if (slot != -1 && threadIdx.x == 0) raise_error(p.err, kErrDeviceArg);
     return;
   }
-  const int r0 = part * kRows * RPI + lane / LPR;
+  const int r0 = (part * warps + (threadIdx.x >> 5)) * kRows * RPI + lane / LPR;
   float* st = p.states + ((size_t)slot * p.H + h) * p.dv * DK;
   float4 s[kRows];
 #pragma unroll
@@ -84,32 +72,15 @@ __global__ void __launch_bounds__(32 * kWarps) la_step_kernel(StepParams p, cons
   for (int x = 0; x < kRows; ++x) vv[x] = r0 + x * RPI < p.dv ? to_f(v[bh * p.dv + r0 + x * RPI]) : 0.f;
   const float la = p.log_alpha[p.per_head ? h : bh];
   const size_t kh = ((size_t)b * p.Hk + h / (p.H / p.Hk)) * DK;
-  float kx[4], qx[4], sn[4], cs[4];
-  if (p.rot) {
-    const long long pos = p.positions[b];
-    const int half = p.rot / 2;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = i0 + e;
-      if (i < p.rot && !(p.interleaved && (e & 1))) {
-        rope_sincos(pos, rope_turns(p.inv_freq[p.interleaved ? i / 2 : i < half ? i : i - half]), sn[e], cs[e]);
-        sn[e] *= p.amp;
-        cs[e] *= p.amp;
-      } else {
-        sn[e] = cs[e] = 0.f;
-      }
-    }
-  }
-  if (p.rot) {
-    turned(k + kh, i0, p, sn, cs, kx);
-    turned(q + kh, i0, p, sn, cs, qx);
-  } else {
-    load4(k + kh + i0, kx);
-    load4(q + kh + i0, qx);
-  }
-  // two rows of the batch with one slot would race: one warp of the row looks
+  const long long pos = p.rot ? p.positions[b] : 0;
+  for (int e = threadIdx.x; e < 2 * DK; e += blockDim.x) qk[e] = turned((e < DK ? q : k) + kh, e & (DK - 1), pos, p);
+  __syncthreads();
+  float kx[4], qx[4];
+  load4(qk + i0, qx);
+  load4(qk + DK + i0, kx);
+  // two rows of the batch with one slot would race: one CTA of the row looks
   if (p.slots && part == 0 && h == 0)
-    for (int x = lane; x < b; x += 32)
+    for (int x = threadIdx.x; x < b; x += blockDim.x)
       if (p.slots[x] == slot) raise_error(p.err, kErrDeviceArg);
   const LaDecay d = la_decay(la);
   const bool forget = d.f == 0.f && !d.near;  // whatever the state holds: slots are handed on
@@ -155,10 +126,11 @@ __global__ void __launch_bounds__(32 * kWarps) la_step_kernel(StepParams p, cons
 
 template <typename IO, int DK> ll_status run(const LaStepArgs& a) {
   constexpr int rows = kRows * 32 / (DK / 4);
-  StepParams p{a.B, a.H, a.Hk, a.dv, (a.dv + rows - 1) / rows, a.n_slots, a.per_head, a.rope.rot, a.rope.interleaved,
+  const int warps = (a.dv + rows - 1) / rows;
+  const int parts = warps > kWarps ? warps / kWarps : 1;
+  StepParams p{a.B, a.H, a.Hk, a.dv, parts, a.n_slots, a.per_head, a.rope.rot, a.rope.interleaved,
                a.scale, a.rope.amp, a.slots, a.positions, a.rope.inv_freq, a.log_alpha, a.states, a.err};
-  const long long units = (long long)a.B * a.H * p.parts;
-  la_step_kernel<IO, DK><<<(unsigned)((units + kWarps - 1) / kWarps), 32 * kWarps, 0, a.stream>>>(
+  la_step_kernel<IO, DK><<<(unsigned)((long long)a.B * a.H * parts), 32 * (warps / parts), 0, a.stream>>>(
       p, static_cast<const IO*>(a.q), static_cast<const IO*>(a.k), static_cast<const IO*>(a.v), static_cast<IO*>(a.o));
   LL_CUDA_OK(cudaGetLastError());
   return LL_OK;
