@@ -8,9 +8,12 @@
 // halves of a pair at a time.
 #include "la.cuh"
 #include "rope.cuh"
+#include "sm100.cuh"
 
 namespace llattn {
 namespace {
+
+using sm100::pack_bf16x2;
 
 constexpr int kThreads = 256;
 // heads that share a thread's sines
@@ -24,27 +27,27 @@ struct RopeParams {
   const int64_t* positions;
 };
 
-template <typename IO, int N> struct Piece;  // N consecutive elements as float
+template <typename IO, int N> struct Piece;  // N consecutive elements, as they lie and as float
 template <> struct Piece<float, 1> {
-  static __device__ __forceinline__ void load(const float* p, float* x) { x[0] = *p; }
-  static __device__ __forceinline__ void store(float* p, const float* x) { *p = x[0]; }
+  using Raw = float;
+  static __device__ __forceinline__ void unpack(Raw v, float* x) { x[0] = v; }
+  static __device__ __forceinline__ Raw pack(const float* x) { return x[0]; }
 };
 template <> struct Piece<__nv_bfloat16, 1> {
-  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* x) { x[0] = __bfloat162float(*p); }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* x) { *p = __float2bfloat16_rn(x[0]); }
+  using Raw = __nv_bfloat16;
+  static __device__ __forceinline__ void unpack(Raw v, float* x) { x[0] = __bfloat162float(v); }
+  static __device__ __forceinline__ Raw pack(const float* x) { return __float2bfloat16_rn(x[0]); }
 };
 template <> struct Piece<float, 4> {
-  static __device__ __forceinline__ void load(const float* p, float* x) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
+  using Raw = float4;
+  static __device__ __forceinline__ void unpack(const Raw& v, float* x) {
     x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
   }
-  static __device__ __forceinline__ void store(float* p, const float* x) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-  }
+  static __device__ __forceinline__ Raw pack(const float* x) { return make_float4(x[0], x[1], x[2], x[3]); }
 };
 template <> struct Piece<__nv_bfloat16, 8> {
-  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* x) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
+  using Raw = uint4;
+  static __device__ __forceinline__ void unpack(const Raw& v, float* x) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -52,18 +55,14 @@ template <> struct Piece<__nv_bfloat16, 8> {
       x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* x) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  static __device__ __forceinline__ Raw pack(const float* x) {
+    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
   }
 };
 
-// VEC elements of each half of VEC pairs to a thread; VEC = 1: of any rot.
+// VEC elements of each half of VEC pairs to a thread; VEC = 1: of any rot.  The next kBatch heads are on
+// their way while these are turned, the first ones while the sines are made.
+constexpr int kBatch = 4;
 template <typename IO, int VEC>
 __global__ void __launch_bounds__(kThreads) rope_kernel(RopeParams p, const IO* q, const IO* k, IO* qo, IO* ko) {
   const long long at = (long long)(blockIdx.x / p.groups) * kThreads + threadIdx.x;
@@ -76,50 +75,64 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeParams p, const IO* 
   const bool turn = u < pairs;
   // where the first and the second elements of the pairs stand in a row
   const int i0 = turn ? (p.interleaved ? 2 * u * VEC : u * VEC) : p.rot + (u - pairs) * VEC;
-  const int i1 = p.interleaved ? i0 + VEC : i0 + p.half;
+  const int i1 = !turn ? i0 : p.interleaved ? i0 + VEC : i0 + p.half;
+  const int h0 = group * kHeads, h1 = min(h0 + kHeads, p.H + p.Hk);
+  auto row_of = [&](int h) {
+    return h >= p.H ? (((size_t)b * p.Hk + (h - p.H)) * p.T + t) * p.d : (((size_t)b * p.H + h) * p.T + t) * p.d;
+  };
+  using Raw = typename Piece<IO, VEC>::Raw;
+  Raw x[kBatch], y[kBatch];
+  auto load = [&](int h, Raw& a, Raw& c) {
+    const IO* src = (h >= p.H ? k : q) + row_of(h);
+    a = *reinterpret_cast<const Raw*>(src + i0);
+    c = *reinterpret_cast<const Raw*>(src + i1);
+  };
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j)
+    if (h0 + j < h1) load(h0 + j, x[j], y[j]);
   float s[VEC], c[VEC];
   if (turn) {
     const long long pos = p.positions ? p.positions[bt] : t;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-      rope_sincos(pos, rope_turns(p.inv_freq[u * VEC + i]), s[i], c[i]);
+      const uint64_t f = rope_turns(p.inv_freq[u * VEC + i]);
+      if (sizeof(IO) == 2) rope_sincos_fast(pos, f, s[i], c[i]);
+      else rope_sincos(pos, f, s[i], c[i]);
       s[i] *= p.amp * p.sign;
       c[i] *= p.amp;
     }
   }
-  const int h0 = group * kHeads, h1 = min(h0 + kHeads, p.H + p.Hk);
-#pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
-    const bool key = h >= p.H;
-    const size_t row = key ? ((size_t)b * p.Hk + (h - p.H)) * p.T + t : ((size_t)b * p.H + h) * p.T + t;
-    const IO* src = (key ? k : q) + row * p.d;
-    IO* dst = (key ? ko : qo) + row * p.d;
-    float x[VEC], y[VEC];
-    Piece<IO, VEC>::load(src + i0, x);
-    if (!turn) {
-      Piece<IO, VEC>::store(dst + i0, x);
-      continue;
-    }
-    Piece<IO, VEC>::load(src + i1, y);
-    if (VEC > 1 && p.interleaved) {  // pairs lie side by side: (x0 x1) (x2 x3) .. (y0 y1) ..
+#pragma unroll 1
+  for (int hb = h0; hb < h1; hb += kBatch) {
 #pragma unroll
-      for (int i = 0; i < VEC; i += 2) {
-        const float a = x[i], bb = x[i + 1], e = y[i], f = y[i + 1];
-        x[i] = a * c[i / 2] - bb * s[i / 2];
-        x[i + 1] = fmaf(a, s[i / 2], bb * c[i / 2]);
-        y[i] = e * c[(VEC + i) / 2] - f * s[(VEC + i) / 2];
-        y[i + 1] = fmaf(e, s[(VEC + i) / 2], f * c[(VEC + i) / 2]);
-      }
-    } else {
+    for (int j = 0; j < kBatch; ++j) {
+      const int h = hb + j;
+      if (h >= h1) break;
+      float a[VEC], e[VEC];
+      Piece<IO, VEC>::unpack(x[j], a);
+      Piece<IO, VEC>::unpack(y[j], e);
+      if (h + kBatch < h1) load(h + kBatch, x[j], y[j]);
+      IO* dst = (h >= p.H ? ko : qo) + row_of(h);
+      if (turn && VEC > 1 && p.interleaved) {  // pairs lie side by side: (a0 a1) (a2 a3) .. (e0 e1) ..
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float a = x[i], bb = y[i];
-        x[i] = a * c[i] - bb * s[i];
-        y[i] = fmaf(a, s[i], bb * c[i]);
+        for (int i = 0; i < VEC; i += 2) {
+          const float a0 = a[i], a1 = a[i + 1], e0 = e[i], e1 = e[i + 1];
+          a[i] = a0 * c[i / 2] - a1 * s[i / 2];
+          a[i + 1] = fmaf(a0, s[i / 2], a1 * c[i / 2]);
+          e[i] = e0 * c[(VEC + i) / 2] - e1 * s[(VEC + i) / 2];
+          e[i + 1] = fmaf(e0, s[(VEC + i) / 2], e1 * c[(VEC + i) / 2]);
+        }
+      } else if (turn) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float a0 = a[i], e0 = e[i];
+          a[i] = a0 * c[i] - e0 * s[i];
+          e[i] = fmaf(a0, s[i], e0 * c[i]);
+        }
       }
+      *reinterpret_cast<Raw*>(dst + i0) = Piece<IO, VEC>::pack(a);
+      if (turn) *reinterpret_cast<Raw*>(dst + i1) = Piece<IO, VEC>::pack(e);
     }
-    Piece<IO, VEC>::store(dst + i0, x);
-    Piece<IO, VEC>::store(dst + i1, y);
   }
 }
 
