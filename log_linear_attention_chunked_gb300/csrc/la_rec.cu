@@ -22,8 +22,8 @@
 // touched yet, and cancel.)  Sums over the lanes are taken for kLpr
 // tokens at once: each step of a butterfly halves the values that a lane carries.
 //
-// alpha_t is rounded to float32 once a token; what the roundings so far are off by
-// is taken out of the next one near 1, so that those of a constant decay do not add up.
+// alpha_t is rounded to float32 once a token; what the roundings of a staged tile are off by, those near 1,
+// is taken out of the next tile's first, so that those of a constant decay do not add up.
 #include <algorithm>
 
 #include "la.cuh"
@@ -215,19 +215,17 @@ __global__ void __launch_bounds__(kMaxThreads) la_rec_kernel(const __grid_consta
       const float ga = g_next;
       if (lane < kTile) g_next = log_alpha((tile + 1) * kTile + lane);
       g_all += lane < kTile ? (double)ga : 0.;
-      const bool near = ga > -0.5f;
-      const float f = near ? expm1f(ga) : expf(ga);
-      const uint32_t nears = __ballot_sync(0xffffffffu, near);
-      float a = f;
-#pragma unroll
-      for (int u = 0; u < kTile; ++u) {
-        const float c = __shfl_sync(0xffffffffu, f, u);
-        if (nears >> u & 1) {
-          const float d = c - off, r = 1.f + d;
-          off = (r - 1.f) - d;
-          if (lane == u) a = r;
-        }
+      const bool near = ga > -0.5f && lane < kTile;
+      float a = near ? expm1f(ga) : expf(ga), left = 0.f;
+      if (near) {
+        const float d = lane == 0 ? a - off : a;
+        a = 1.f + d;
+        left = (a - 1.f) - d;
       }
+      off = __shfl_sync(0xffffffffu, near ? 0.f : off, 0);  // (a first token that is not near leaves it to the next tile)
+#pragma unroll
+      for (int o = kTile / 2; o > 0; o >>= 1) left += __shfl_xor_sync(0xffffffffu, left, o);
+      off += __shfl_sync(0xffffffffu, left, 0);
       if (lane < kTile) sm.alpha[b][lane] = a;
     }
     __syncthreads();
@@ -432,13 +430,20 @@ struct FinishParams {
   const float *dq, *dkey;                    // [B,H,T,dk] float32, shared heads
   void *dq_out, *dk_out;
 };
-constexpr int kFinishThreads = 256;
+constexpr int kFinishThreads = 512;
 __device__ __forceinline__ double warp_sum(double x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
-// the decay's gradient of one (segment, head): a thread sums a run of tokens, then goes over it again
+__device__ __forceinline__ float2 pair_sum(float2 x) {  // over a warp
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    x = pair_add(x, make_float2(__shfl_xor_sync(0xffffffffu, x.x, o), __shfl_xor_sync(0xffffffffu, x.y, o)));
+  return x;
+}
+// The decay's gradient of one (segment, head): a thread sums a run of tokens, then goes over it again.  Sums are
+// pairs of floats (in float64, two operations a cycle and SM, they took 40 of 52 us for 320 segments).
 __global__ void __launch_bounds__(kFinishThreads) la_finish_kernel(FinishParams p) {
   la_chain();
   constexpr int W = kFinishThreads / 32;
@@ -451,7 +456,7 @@ __global__ void __launch_bounds__(kFinishThreads) la_finish_kernel(FinishParams 
     return;
   }
   const size_t row = ((size_t)s.row_b * p.seqs.H + h) * p.seqs.T + s.start;
-  __shared__ double red[3][W];
+  __shared__ float2 red[3][W];
   const int elems = p.dk * p.dv;
   const float* B = s.num > 0 ? p.behind + ((size_t)(slot - 1) * p.seqs.H + h) * elems
                    : p.first ? p.first + ((size_t)s.seq * p.seqs.H + h) * elems : nullptr;
@@ -460,72 +465,82 @@ __global__ void __launch_bounds__(kFinishThreads) la_finish_kernel(FinishParams 
       reinterpret_cast<float4*>(p.copy_first + ((size_t)s.seq * p.seqs.H + h) * elems)[e] = reinterpret_cast<const float4*>(B)[e];
   // <S, B> at the segment's start; `close`: and at its end, where it is known
   const bool last = (long long)s.num * p.seg + s.n == s.seq_len, close = p.close && (!last || !p.followed);
-  auto product = [&](const float* a, const float* b) {
-    const float4 *S = reinterpret_cast<const float4*>(a), *G = reinterpret_cast<const float4*>(b);
-    float t[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-    for (int e = tid; e < elems / 4; e += kFinishThreads) {
-      const float4 x = S[e], y = G[e];
-      t[0] = fmaf(x.x, y.x, t[0]);
-      t[1] = fmaf(x.y, y.y, t[1]);
-      t[2] = fmaf(x.z, y.z, t[2]);
-      t[3] = fmaf(x.w, y.w, t[3]);
-    }
-    return ((double)t[0] + t[1]) + ((double)t[2] + t[3]);
-  };
-  double border = 0., end = 0.;
-  if (p.entry && B) border = product(p.entry + ((size_t)(p.by_slot ? slot : s.seq) * p.seqs.H + h) * elems, B);
-  if (close && !last) end = product(p.entry + ((size_t)(slot + 1) * p.seqs.H + h) * elems, p.behind + ((size_t)slot * p.seqs.H + h) * elems);
+  auto at = [&](const float* x, int i) { return reinterpret_cast<const float4*>(x + ((size_t)i * p.seqs.H + h) * elems); };
+  const float4* S = p.entry && B ? at(p.entry, p.by_slot ? slot : s.seq) : nullptr;
+  const float4* S1 = close && !last ? at(p.entry, slot + 1) : nullptr;
+  const float4* B1 = close && !last ? at(p.behind, slot) : nullptr;
+  float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int e = tid; e < elems / 4; e += kFinishThreads) {
+    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 x = S ? S[e] : z, y = S ? reinterpret_cast<const float4*>(B)[e] : z, x1 = S1 ? S1[e] : z, y1 = S1 ? B1[e] : z;
+    d0[0] = fmaf(x.x, y.x, d0[0]);
+    d0[1] = fmaf(x.y, y.y, d0[1]);
+    d0[2] = fmaf(x.z, y.z, d0[2]);
+    d0[3] = fmaf(x.w, y.w, d0[3]);
+    d1[0] = fmaf(x1.x, y1.x, d1[0]);
+    d1[1] = fmaf(x1.y, y1.y, d1[1]);
+    d1[2] = fmaf(x1.z, y1.z, d1[2]);
+    d1[3] = fmaf(x1.w, y1.w, d1[3]);
+  }
+  const float2 border = pair_sum(pair_add(pair_add(make_float2(d0[0], 0.f), make_float2(d0[1], 0.f)),
+                                          pair_add(make_float2(d0[2], 0.f), make_float2(d0[3], 0.f))));
+  const float2 end = pair_sum(pair_add(pair_add(make_float2(d1[0], 0.f), make_float2(d1[1], 0.f)),
+                                       pair_add(make_float2(d1[2], 0.f), make_float2(d1[3], 0.f))));
   const int run = (s.n + kFinishThreads - 1) / kFinishThreads, t0 = min(tid * run, s.n), t1 = min(t0 + run, s.n);
   auto token = [&](int t) {
-    double x = 0.;
-    for (int i = 0; i < p.parts; ++i) x += (double)p.part_k[i * p.part_stride + row + t] - (double)p.part_q[i * p.part_stride + row + t];
+    float2 x = make_float2(0.f, 0.f);
+    for (int i = 0; i < p.parts; ++i) {
+      x = pair_add(x, make_float2(p.part_k[i * p.part_stride + row + t], 0.f));
+      x = pair_add(x, make_float2(-p.part_q[i * p.part_stride + row + t], 0.f));
+    }
     return x;
   };
-  double own = 0.;
+  float2 own = make_float2(0.f, 0.f);
 #pragma unroll 4
-  for (int t = t0; t < t1; ++t) own += token(t);
-  double x = own;
+  for (int t = t0; t < t1; ++t) own = pair_add(own, token(t));
+  float2 x = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const double y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const float2 y = make_float2(__shfl_up_sync(0xffffffffu, x.x, o), __shfl_up_sync(0xffffffffu, x.y, o));
+    if (lane >= o) x = pair_add(x, y);
   }
-  border = warp_sum(border);
-  end = warp_sum(end);
   if (lane == 31) {
     red[0][warp] = x;
     red[1][warp] = border;
     red[2][warp] = end;
   }
+  float2 v = make_float2(__shfl_up_sync(0xffffffffu, x.x, 1), __shfl_up_sync(0xffffffffu, x.y, 1));
+  if (lane == 0) v = make_float2(0.f, 0.f);
   __syncthreads();
-  double v = x - own, off = 0.;
-#pragma unroll
-  for (int w = 0; w < W; ++w) {
-    v += red[1][w];
-    if (w < warp) v += red[0][w];
-    off += red[0][w] + red[1][w] - red[2][w];
-  }
+  // one warp's lanes hold the warps' sums: those before mine, all of them, and the borders'
+  const float2 z = make_float2(0.f, 0.f);
+  const float2 before = pair_sum(lane < warp ? red[0][lane % W] : z);
+  const float2 start = pair_sum(lane < W ? red[1][lane % W] : z);
+  v = pair_add(v, pair_add(before, start));
   // what the sum over the whole segment is off by is taken out in proportion to the tokens
-  off = close ? off / s.n : 0.;
-  double all = 0.;
+  float off = 0.f;
+  if (close) {
+    const float2 whole = pair_add(start, pair_sum(lane < W ? red[0][lane % W] : z)), last_one = pair_sum(lane < W ? red[2][lane % W] : z);
+    const float2 d = pair_add(whole, make_float2(-last_one.x, -last_one.y));
+    off = (d.x + d.y) / (float)s.n;
+  }
+  float2 all = z;
 #pragma unroll 4
   for (int t = t0; t < t1; ++t) {
-    const double y = gdr_forgets(p.log_alpha[p.per_head ? (size_t)h : row + t]) ? 0. : v - off * t;
-    if (p.per_head) all += y;
-    else p.dlog_alpha[row + t] = (float)y;
-    v += token(t);
+    const float2 y = pair_add(v, make_float2(-off * (float)t, 0.f));
+    const float g = gdr_forgets(p.log_alpha[p.per_head ? (size_t)h : row + t]) ? 0.f : y.x + y.y;
+    if (p.per_head) all = pair_add(all, make_float2(g, 0.f));
+    else p.dlog_alpha[row + t] = g;
+    v = pair_add(v, token(t));
   }
   if (p.per_head) {
+    all = pair_sum(all);
     __syncthreads();
-    all = warp_sum(all);
     if (lane == 0) red[0][warp] = all;
     __syncthreads();
-    if (tid == 0) {
-      double sum = 0.;
-      for (int w = 0; w < W; ++w) sum += red[0][w];
-      p.head_sums[(size_t)slot * p.seqs.H + h] = sum;
-    }
+    all = pair_sum(lane < W ? red[0][lane % W] : z);
+    if (tid == 0) p.head_sums[(size_t)slot * p.seqs.H + h] = (double)all.x + (double)all.y;
   }
 }
 // dq and dk of a key head: its value heads' in their order, four elements to a thread
@@ -645,29 +660,54 @@ ll_status carry_launch(const LaCarry& c, int sequences, cudaStream_t stream) {
 }
 
 // ---- in chunks: tokens of a segment, a multiple of a chunk.  More segments fill more
-// SMs, and each costs the states' way between them and the filling of its pipeline.
-constexpr int kChunk = 128;
+// SMs, and each costs the states' way between them and the filling of its pipeline.  The
+// times are those measured at d = 128, in us: a chunk 3.1, of the gradient's jobs 7, of the sums 1.4 (1.9),
+// a segment's beginning and end 9, 12, 6.  Of packed sequences only the device knows the lengths: their
+// work is taken as spread evenly, with half a segment at the end of it.  (Gradient, B 2, H 16, T 4096, segments of
+// 6, 8, 11, 16 chunks: 226, 225, 202, 245 us; 7 packed sequences of 5003 tokens, 3, 6, 8, 11: 281, 226, 220, 362.)
+// The decay's gradient is summed over a segment, and its rounding with it: at most 12 chunks there.
+constexpr int kChunk = 128, kMostGradChunks = 12;
 int tc_segment(const LaArgs& a, bool bwd) {
-  const double chunk_us = bwd ? 5. : 2.8, fill_us = 7., sum_us = 1.4;
+  const double chunk_us = bwd ? 7. : 3.1, fill_us = bwd ? 12. : 9., sum_us = bwd ? 1.9 : 1.4, sum_fill_us = 6.;
   const long long chunks = ((long long)a.T + kChunk - 1) / kChunk;
   const int jobs = bwd ? 3 : 1, dirs = bwd ? 2 : 1, sms = 152;
   double best = 1e30;
   long long seg = chunks;
   for (long long n = 1; n <= chunks && n <= 2 * sms; ++n) {
-    const long long per = (chunks + n - 1) / n;
-    if (bwd && per > 12 && n < chunks) continue;  // (the decay's gradient is summed over a segment)
-    const double slots = (a.n_seqs ? (double)chunks / per + a.n_seqs : (double)a.B * ((chunks + per - 1) / per)) * a.H;
-    const double waves = std::ceil(slots * jobs / sms), sum_waves = std::ceil(slots * dirs / sms);
-    double t = waves * (per * chunk_us + fill_us);
-    if (n > 1) t += sum_waves * (per * sum_us + fill_us) + 3. + 0.1 * n;
+    const long long per = n == 2 * sms ? std::min<long long>((chunks + n - 1) / n, kMostGradChunks) : (chunks + n - 1) / n;
+    if (bwd && per > kMostGradChunks) continue;
+    double t;
+    if (a.n_seqs) {
+      const double slots = ((double)chunks / per + a.n_seqs) * a.H, work = (chunks + 0.5 * a.n_seqs) * a.H;
+      t = jobs * (slots * fill_us + work * chunk_us) / sms + std::max(0.5 * per * chunk_us, 1. * fill_us);
+      if (n > 1) t += dirs * (slots * sum_fill_us + work * sum_us) / sms + 0.5 * per * sum_us + 6.;
+    } else {
+      const double slots = (double)a.B * ((chunks + per - 1) / per) * a.H;
+      t = std::ceil(slots * jobs / sms) * (per * chunk_us + fill_us);
+      if (n > 1) t += std::ceil(slots * dirs / sms) * (per * sum_us + sum_fill_us) + 5. + 0.1 * n;
+    }
     if (t < best) {
       best = t;
       seg = per;
     }
   }
-  return (int)std::min<long long>(seg * kChunk, (1ll << 30));
+  if (bwd) seg = std::min<long long>(seg, kMostGradChunks);
+  return (int)std::min<long long>(seg * kChunk, 1ll << 30);
 }
-bool tc_use(const LaArgs& a, bool bwd) { return la_tc_formats(a); }
+// Which of the two ways is the faster (token by token / in chunks, us; mean lengths of 16, 32, 64 tokens):
+//   128 x 128, 4 heads      forward 12/21, 16/21, 25/21        gradient 19/31, 24/31, 32/31
+//              256 heads    forward 29/36, 42/36, 69/37        gradient 75/89, 112/89, 189/90
+//              2048 heads   forward 169/211, 259/213, 453/219  gradient 529/591, 804/582, 1395/584
+//   64 x 64,   32 heads     forward 14/13, 18/13, 29/13        gradient 20/23, 24/23, 34/23
+//              256 heads    forward 16/23, 21/23, 33/23        gradient 32/69, 46/68, 75/68
+//              2048 heads   forward 55/124, 84/125, 143/125    gradient 165/429, 251/429, 425/433
+bool tc_use(const LaArgs& a, bool bwd) {
+  if (!la_tc_formats(a)) return false;
+  const int mean = a.n_seqs ? (a.T + a.n_seqs - 1) / a.n_seqs : a.T;
+  const bool few = (long long)la_sequences(a) * a.H <= 152;
+  if (a.dk * a.dv > 64 * 64) return mean >= (few ? 48 : 24);
+  return mean >= (few ? 16 : 48) + (bwd ? 16 : 0);
+}
 
 struct Plan {
   bool tc, split;  // in chunks; more than one segment

@@ -186,6 +186,7 @@ def test_backward(B, shape, per_head):
 PACKED = [  # starts, T: empty sequences, single tokens, rows before, between and behind the sequences
     ([0, 5, 5, 6, 70], 70), ([3, 3, 40, 168, 296, 297, 560], 600), ([0, 1], 1), ([0, 0, 0], 4), ([7, 135, 300, 300], 301),
     (list(range(0, 41)), 41), ([0, 1300, 1301, 1301, 1500], 1503),
+    ([0, 1, 2, 3, 5, 5, 8, 700, 829], 829), ([2, 130, 258, 259, 515, 515, 643], 700),
 ]
 
 
