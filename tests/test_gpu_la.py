@@ -338,6 +338,106 @@ def test_captured_and_on_another_stream(B, kind):
     assert all(torch.equal(p, r) for p, r in zip(out, want_y))
 
 
+@pytest.mark.parametrize("kind", [(1, 1, 9001, 64, 64, "bf16"), (1, 1, 30001, 16, 16, "f32"), (2, 1, 5003, 128, 64, "bf16")], ids=str)
+def test_many_segments(B, kind):
+    """Long sequences of few heads, slow decays: states pass from segment to segment many times."""
+    x = draw(1, *kind, seed=61, rate=1e-3)
+    check_fwd(B, x)
+    check_bwd(B, x)
+
+
+@pytest.mark.parametrize("T", [15, 16, 17, 23, 24, 31, 32, 47, 48, 49, 63, 64])
+@pytest.mark.parametrize("heads", [2, 154])
+def test_short_sequences(B, heads, T):
+    """Both sides of the lengths from which chunks are taken, with few states and with many."""
+    for d in (64, 128):
+        x = draw(1, heads, heads // 2, T, d, d, "bf16", seed=T, per_head=T % 2 == 0)
+        check_fwd(B, x)
+        if heads == 2:
+            check_bwd(B, x)
+
+
+@pytest.mark.parametrize("kind", [(2, 1, 300, 64, 128, "bf16"), (2, 1, 90, 32, 32, "f32")], ids=str)
+def test_growth_is_computed_as_given(B, kind):
+    x = draw(1, *kind, seed=62, init=False)
+    x["log_alpha"] = x["log_alpha"].abs() * 0.02
+    check_fwd(B, x)
+
+
+@pytest.mark.parametrize("kind", [(2, 2, 700, 128, 128, "bf16"), (2, 2, 700, 32, 32, "f32")], ids=str)
+def test_bad_decays_stay_within_their_head_and_sequence(B, kind):
+    starts, H, T = [0, 200, 650, 700], kind[0], kind[2]
+    x = draw(1, *kind, n=3, seed=63)
+    o0, s0 = gpu_fwd(B, x, starts)
+    d0 = gpu_bwd(B, x, starts)
+    x["log_alpha"][0, 1, 460] = float("nan")
+    o, s = gpu_fwd(B, x, starts)
+    d = gpu_bwd(B, x, starts)
+    ok = np.ones((H, T), bool)
+    ok[1, 200:650] = False
+    assert np.array_equal(o[0][ok], o0[0][ok]) and np.array_equal(s[[0, 2]], s0[[0, 2]]) and np.array_equal(s[1, 0], s0[1, 0])
+    for a, c in zip(d[:4], d0[:4]):
+        assert np.array_equal(a[0][ok], c[0][ok])
+    assert np.isnan(o[0, 1, 460:650]).all() and np.isnan(s[1, 1]).all() and np.array_equal(o[0, 1, 200:328], o0[0, 1, 200:328])
+    assert np.isnan(d[3][0, 1, 200:461]).all() and np.isnan(d[4][1, 1]).all()
+
+
+def test_two_graphs_at_once(B):
+    """Two captured calls with workspaces of their own, replayed side by side on two streams."""
+    kind = (4, 2, 2000, 128, 128, "bf16")
+    xs = [setup(B, draw(1, *kind, seed=64 + i), None, 0.5)[0] for i in range(2)]
+
+    def call(g):
+        return [B.ll_la_fwd(g["q"], g["k"], g["v"], g["log_alpha"], state_in=g["state_in"]),
+                *B.ll_la_bwd(g["q"], g["k"], g["v"], g["log_alpha"], g["dout"], dstate_out=g["dstate_out"])]
+
+    want = [[t.clone() for t in call(g)] for g in xs]
+    graphs, outs, streams = [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for g in xs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(call(g))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for gr, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                gr.replay()
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(a, b) for a, b in zip(w, o))
+
+
+TAIL, SHOWN = 900, 300  # of a sequence whose decays leave e^-300 of what lies before the tail
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_offsets_past_31_bits(B, io):
+    """More elements than 31 bits count: the last tokens of the last head against the recurrence."""
+    H, Hk, T, dk, dv = 8, 1, 2_200_000, 64, 128
+    assert H * T * dv > 1 << 31
+    dt = torch.bfloat16 if io == "bf16" else torch.float32
+    gen = torch.Generator(DEV).manual_seed(65)
+    q, k, v, do = [torch.empty(1, h, T, d, dtype=dt, device=DEV).normal_(generator=gen)
+                   for h, d in ((Hk, dk), (Hk, dk), (H, dv), (H, dv))]
+    ga = torch.empty(1, H, T, device=DEV).uniform_(-0.6, -0.4, generator=gen)
+    f = lambda x: x.double().cpu().numpy()
+    tails = [[f(x[0, h if x.shape[1] == H else 0, -TAIL:]) for x in (q, k, v, ga, do)] for h in range(H)]
+    tol = TOL_F32 if io == "f32" else TOL_BF16
+    st = torch.empty(1, H, dv, dk, device=DEV)
+    o = B.ll_la_fwd(q, k, v, ga, scale=0.5, state_out=st)
+    ro, rs = la.forward(*tails[-1][:4], scale=0.5)
+    assert rel_err(f(o[0, -1, -SHOWN:]), ro[-SHOWN:], 0) <= tol and rel_err(f(st[0, -1]), rs, 0) <= TOL_F32
+    del o
+    dq, dkey, dval, dla = B.ll_la_bwd(q, k, v, ga, do, scale=0.5)
+    r = [la.backward(*t, scale=0.5) for t in tails]
+    for got, name in ((dq, "dq"), (dkey, "dk")):
+        assert rel_err(f(got[0, 0, -SHOWN:]), sum(x[name][-SHOWN:] for x in r), 0) <= tol, name
+    assert rel_err(f(dval[0, -1, -SHOWN:]), r[-1]["dv"][-SHOWN:], 0) <= tol
+    term = max(np.abs((tails[-1][0] * r[-1]["dq"]).sum(-1)).max(), r[-1]["terms"].max())
+    assert np.abs(f(dla[0, -1, -SHOWN:]) - r[-1]["dlog_alpha"][-SHOWN:]).max() <= TOL_F32 * term
+    assert B.ll_last_device_error() == 0
+
+
 def test_gradient_against_differences(B):
     """float32, token by token: a directional derivative of sum(o . dout) + sum(S . dS) computed in 64 bits."""
     x = draw(1, 2, 1, 90, 32, 16, "f32", seed=31)
@@ -425,6 +525,24 @@ def test_step_bad_slots(B):
     assert B.ll_last_device_error() == 0
 
 
+def test_step_states_past_31_bits(B):
+    """A pool of more elements than 31 bits count, its last slots."""
+    H, d, n = 32, 128, 4200
+    assert n * H * d * d > 1 << 31
+    x = draw(3, H, H, 1, d, d, "f32", seed=66, init=False)
+    g = {m: t.to(DEV)[:, :, 0].contiguous() for m, t in x.items()}
+    pool = torch.empty(n, H, d, d, device=DEV)
+    slots = [n - 1, 1, n - 2]
+    start = torch.randn(3, H, d, d, generator=torch.Generator().manual_seed(1))
+    pool[-4:] = 7.0
+    pool[torch.tensor(slots, device=DEV)] = start.to(DEV)
+    o = B.ll_la_decode_step(g["q"], g["k"], g["v"], g["log_alpha"], pool, slots=torch.tensor(slots, device=DEV)).cpu().numpy()
+    for (i, b, h, *_), a, _, _, _ in slices(x, None):
+        ro, rs = la.forward(*a, state=start[b, h].double().numpy())
+        assert rel_err(o[b, h], ro[0], 0) <= TOL_F32 and rel_err(pool[slots[b], h].cpu().numpy(), rs, 0) <= TOL_F32
+    assert (pool[-4:-2] == 7).all() and B.ll_last_device_error() == 0
+
+
 # ---------------------------------------------------------------- rotary positions
 @pytest.mark.parametrize("inter", [False, True])
 @pytest.mark.parametrize("kind", [(1, 1, 1, 1, 16, 2, "f32"), (2, 4, 2, 5, 64, 64, "bf16"), (1, 16, 3, 33, 128, 96, "bf16"),
@@ -472,6 +590,19 @@ def test_rope_angles_at_far_positions(B):
     want = la.rope(x.numpy(), pos.numpy()[:, None], f.numpy())
     assert np.abs(got - want)[:, :, :5].max() <= 2e-9 + 3 * 2.0 ** -24
     assert np.abs(got - want).max() <= 2e-9 + 3 * 2.0 ** -24 + 2 * np.pi * 2.0 ** -22  # (2^40 positions, 2^-64 + 2^-63 of a turn each)
+
+
+def test_rope_offsets_past_31_bits(B):
+    H, Hk, T, d = 9, 8, 2_000_000, 128
+    assert H * T * d > 1 << 31
+    gen = torch.Generator(DEV).manual_seed(67)
+    q, k = [torch.empty(1, h, T, d, dtype=torch.bfloat16, device=DEV).normal_(generator=gen) for h in (H, Hk)]
+    tail = [t[0, -1, -50:].double().cpu().numpy() for t in (q, k)]
+    f = B.ll_rope_freqs(d)
+    B.ll_rope_fwd(q, k, f.to(DEV), q_out=q, k_out=k)
+    for t, w in zip((q, k), tail):
+        want = la.rope(w, np.arange(T - 50, T), f.numpy())
+        assert rel_err(t[0, -1, -50:].double().cpu().numpy(), want) <= 2.0 ** -8 + TOL_F32
 
 
 def test_rope_of_single_tokens(B):
