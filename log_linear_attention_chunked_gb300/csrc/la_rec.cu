@@ -429,6 +429,7 @@ struct FinishParams {
   double* head_sums;                         // [slot, H] when log_alpha is one to a head
   const float *dq, *dkey;                    // [B,H,T,dk] float32, shared heads
   void *dq_out, *dk_out;
+  unsigned segments, key_rows;               // CTAs of the decays; B Hk T of shared heads
 };
 constexpr int kFinishThreads = 512;
 __device__ __forceinline__ double warp_sum(double x) {
@@ -442,13 +443,37 @@ __device__ __forceinline__ float2 pair_sum(float2 x) {  // over a warp
     x = pair_add(x, make_float2(__shfl_xor_sync(0xffffffffu, x.x, o), __shfl_xor_sync(0xffffffffu, x.y, o)));
   return x;
 }
+// dq and dk of a key head: its value heads' in their order, four elements to a thread (key_rows below 2^30)
+template <typename IO> __device__ __forceinline__ void store4(IO* d, float4 x);
+template <> __device__ __forceinline__ void store4<float>(float* d, float4 x) { *reinterpret_cast<float4*>(d) = x; }
+template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* d, float4 x) {
+  *reinterpret_cast<uint2*>(d) = make_uint2(sm100::pack_bf16x2(x.x, x.y), sm100::pack_bf16x2(x.z, x.w));
+}
+template <typename IO> __device__ __forceinline__ void sum_heads(const FinishParams& p, unsigned block) {
+  const unsigned n4 = p.dk / 4, per = kFinishThreads / n4, G = p.seqs.H / p.seqs.Hk, T = p.seqs.T;  // rows of a CTA
+  const unsigned krow = (block >> 1) * per + threadIdx.x / n4, c = threadIdx.x % n4;
+  if (krow >= p.key_rows) return;
+  const unsigned bk = krow / T, t = krow - bk * T;
+  if (p.seqs.starts && ((int)t < p.seqs.starts[0] || (int)t >= p.seqs.starts[p.seqs.n])) return;  // of no sequence
+  const float4* a = reinterpret_cast<const float4*>((block & 1 ? p.dkey : p.dq) + ((size_t)bk * G * T + t) * p.dk) + c;
+  const size_t head = (size_t)T * n4;
+  float4 x = *a;
+#pragma unroll 4
+  for (unsigned i = 1; i < G; ++i) {
+    const float4 y = a[i * head];
+    x.x += y.x;
+    x.y += y.y;
+    x.z += y.z;
+    x.w += y.w;
+  }
+  store4(static_cast<IO*>(block & 1 ? p.dk_out : p.dq_out) + (size_t)krow * p.dk + 4 * c, x);
+}
 // The decay's gradient of one (segment, head): a thread sums a run of tokens, then goes over it again.  Sums are
 // pairs of floats (in float64, two operations a cycle and SM, they took 40 of 52 us for 320 segments).
-__global__ void __launch_bounds__(kFinishThreads) la_finish_kernel(FinishParams p) {
-  la_chain();
+__device__ __forceinline__ void finish_decay(const FinishParams& p, unsigned block) {
   constexpr int W = kFinishThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.x % p.seqs.H, slot = blockIdx.x / p.seqs.H;
+  const int h = block % p.seqs.H, slot = block / p.seqs.H;
   LaSegment s;
   const bool found = la_find(p.seqs, slot, p.seg, s, nullptr) && s.n > 0;
   if (!found) {
@@ -543,32 +568,10 @@ __global__ void __launch_bounds__(kFinishThreads) la_finish_kernel(FinishParams 
     if (tid == 0) p.head_sums[(size_t)slot * p.seqs.H + h] = (double)all.x + (double)all.y;
   }
 }
-// dq and dk of a key head: its value heads' in their order, four elements to a thread
-template <typename IO> __device__ __forceinline__ void store4(IO* d, float4 x);
-template <> __device__ __forceinline__ void store4<float>(float* d, float4 x) { *reinterpret_cast<float4*>(d) = x; }
-template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* d, float4 x) {
-  *reinterpret_cast<uint2*>(d) = make_uint2(sm100::pack_bf16x2(x.x, x.y), sm100::pack_bf16x2(x.z, x.w));
-}
-template <typename IO>
-__global__ void __launch_bounds__(kFinishThreads) la_heads_kernel(FinishParams p, int B) {
+template <typename IO> __global__ void __launch_bounds__(kFinishThreads) la_finish_kernel(FinishParams p) {
   la_chain();
-  const long long e = (long long)blockIdx.x * kFinishThreads + threadIdx.x;
-  const int n4 = p.dk / 4, G = p.seqs.H / p.seqs.Hk;
-  const long long krow = e / n4;
-  if (krow >= (long long)B * p.seqs.Hk * p.seqs.T) return;
-  const long long bk = krow / p.seqs.T;
-  const int t = (int)(krow - bk * p.seqs.T);
-  if (p.seqs.starts && (t < p.seqs.starts[0] || t >= p.seqs.starts[p.seqs.n])) return;  // of no sequence
-  const float4* a = reinterpret_cast<const float4*>((blockIdx.y ? p.dkey : p.dq) + ((size_t)bk * G * p.seqs.T + t) * p.dk) + e % n4;
-  float4 x = *a;
-  for (int i = 1; i < G; ++i) {
-    const float4 y = a[(size_t)i * p.seqs.T * n4];
-    x.x += y.x;
-    x.y += y.y;
-    x.z += y.z;
-    x.w += y.w;
-  }
-  store4(static_cast<IO*>(blockIdx.y ? p.dk_out : p.dq_out) + krow * p.dk + 4 * (e % n4), x);
+  if (blockIdx.x < p.segments) finish_decay(p, blockIdx.x);
+  else sum_heads<IO>(p, blockIdx.x - p.segments);
 }
 __global__ void __launch_bounds__(128) la_head_sum_kernel(const double* sums, int slots, int H, float* out) {
   la_chain();
@@ -787,7 +790,7 @@ ll_status la_fwd_launch(const LaArgs& a) {
 size_t la_bwd_workspace(const LaArgs& a) { return plan_of(a, true).total; }
 int la_bwd_launches(const LaArgs& a) {
   const Plan pl = plan_of(a, true);
-  return (pl.split ? 2 : 0) + (pl.tc || a.dk == a.dv ? 1 : 2) + 1 + (a.H != a.Hk ? 1 : 0) + (a.per_head ? 1 : 0);
+  return (pl.split ? 2 : 0) + (pl.tc || a.dk == a.dv ? 1 : 2) + 1 + (a.per_head ? 1 : 0);
 }
 
 ll_status la_bwd_launch(const LaArgs& a) {
@@ -895,16 +898,13 @@ ll_status la_bwd_launch(const LaArgs& a) {
   f.dkey = dk32;
   f.dq_out = a.dq;
   f.dk_out = a.dkey;
-  const size_t grid = pl.slots * a.H;
+  const size_t segments = pl.slots * a.H, rows = kFinishThreads / (a.dk / 4);
+  f.key_rows = own ? 0u : (unsigned)((size_t)a.B * a.Hk * a.T);
+  const size_t grid = segments + (f.key_rows + rows - 1) / rows * 2;
   if (grid > 0x7fffffffull) return LL_ERR_UNSUPPORTED;
-  st = la_launch(true, la_finish_kernel, dim3((unsigned)grid), kFinishThreads, 0, a.stream, f);
-  if (st == LL_OK && !own) {
-    const long long blocks = ((long long)a.B * a.Hk * a.T * (a.dk / 4) + kFinishThreads - 1) / kFinishThreads;
-    if (blocks > 0x7fffffffll) return LL_ERR_UNSUPPORTED;
-    const dim3 g((unsigned)blocks, 2);
-    st = a.io == LL_F32 ? la_launch(true, la_heads_kernel<float>, g, kFinishThreads, 0, a.stream, f, a.B)
-                        : la_launch(true, la_heads_kernel<__nv_bfloat16>, g, kFinishThreads, 0, a.stream, f, a.B);
-  }
+  f.segments = (unsigned)segments;
+  st = a.io == LL_F32 ? la_launch(true, la_finish_kernel<float>, dim3((unsigned)grid), kFinishThreads, 0, a.stream, f)
+                      : la_launch(true, la_finish_kernel<__nv_bfloat16>, dim3((unsigned)grid), kFinishThreads, 0, a.stream, f);
   if (st != LL_OK || !a.per_head) return st;
   const double* sums = f.head_sums;
   return la_launch(true, la_head_sum_kernel, dim3((unsigned)a.H), 128, 0, a.stream, sums, (int)pl.slots, a.H, a.dlog_alpha);
