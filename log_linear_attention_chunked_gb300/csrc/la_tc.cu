@@ -20,6 +20,11 @@
 // the chunk is summed in float32 from two tiles of scores: sum_j P_ij (w v^T)_ij with w = Q (V).
 // bf16 has float32's range, so no operand is scaled.
 //
+// Bound: the chain of a chunk, 2.7 us of which the products take half (the scores' masking and k' stand between
+// them; tensor memory has no room for a second chunk's scores).  More segments are more chunks at a time: a pass
+// that sums up what each adds to the state, one along them, then all of them at once.  B 2, H 16, T 4096, d 128:
+// 65 us a call (sums 24, carry 6, outputs 38; 20 at the copy rate), its gradient 202 (sums 32, carry 7, dq dk dv 157).
+//
 // Decays between two tokens of a chunk are products of factors of at most 1: from the
 // row to its block of 32, over the blocks between, from the column's block to the column;
 // only the 32 x 32 blocks on the diagonal take an exponential per element.

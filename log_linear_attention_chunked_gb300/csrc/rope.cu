@@ -5,7 +5,8 @@
 // One launch turns queries and keys.  It moves every element once each way and
 // bounds on HBM if the angles cost nothing: a thread makes the sines of its pairs
 // once and applies them to a group of heads (up to kHeads), 16 bytes of both
-// halves of a pair at a time.
+// halves of a pair at a time.  Queries and keys of 2 x 4096 tokens, 32 heads of 128 in all, bf16, L2 flushed: 28.8 us
+// (20 at the copy rate); four heads to a thread 30.9, sixteen 29.9 (and single tokens 13 where 9), CTAs of 256 31.8.
 #include "la.cuh"
 #include "rope.cuh"
 #include "sm100.cuh"
@@ -15,7 +16,7 @@ namespace {
 
 using sm100::pack_bf16x2;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 // heads that share a thread's sines
 constexpr int kHeads = 8;
 
