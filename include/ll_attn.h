@@ -534,7 +534,8 @@ LL_API ll_status ll_gdr_decode_step(int B, int H, int Hk, int dk, int dv, ll_dty
  * Pairs (a, b) of the first `rot` elements of a head become
  *   (a', b') = amp (a cos x - b sin x, a sin x + b cos x),   x = position inv_freq[i],
  * i the pair's number; the other elements stay as they are.  x is taken modulo a turn
- * in integers, exact to 2^-31 of a turn at any position of up to 2^40. */
+ * in integers, exact to 2^-31 of a turn at any position of up to 2^40, and then rounded to
+ * float32; of bf16 tensors the sine and cosine are the hardware's, off by 2^-20 at most. */
 
 /*   rot          rotated elements of a head, even, 2 .. the head dim
  *   interleaved  0: pair i is elements i and i + rot/2;  1: elements 2i and 2i + 1
@@ -582,10 +583,14 @@ LL_API ll_status ll_rope_bwd(int B, int H, int Hk, int T, int d, ll_dtype io, co
  * packed end to end, and several value heads can share a query/key head; states have the
  * layout of ll_gdr_*'s.
  *
- * States, their gradients and dlog_alpha keep float32 accuracy relative to the terms
- * that they are sums of; o, dq, dk and dv that of their type.
+ * Computed in float32, each output rounded once; long bf16 sequences with head dims of 64
+ * and 128 in chunks of 128 tokens on the tensor cores, where a term of a state (state_out,
+ * dstate_in) is off by 2^-17 of itself at most, sums and decays are float32, and scores and
+ * states are rounded to bf16 on the way to o, dq, dk and dv.
+ * dlog_alpha keeps float32 accuracy relative to the terms that it is a sum of.
  *
- * Infinities and NaN stay within their sequence and head (and its key head's dq and dk).
+ * Infinities and NaN stay within their sequence and head (and its key head's dq and dk); in
+ * chunks those of a token can reach the outputs of earlier tokens of its chunk.
  * log_alpha <= 0 is expected; -inf forgets the state, if that is finite.  Larger values
  * are computed as given and may overflow.
  *
