@@ -794,7 +794,9 @@ __device__ __forceinline__ bool enter(const TcParams& p, int item, LaSegment& sg
     }
   h = item % p.seqs.H;
   slot = item / p.seqs.H;
-  return la_find(p.seqs, slot, p.seg, sg, p.err);
+  if (la_find(p.seqs, slot, p.seg, sg, p.err)) return true;
+  wait_for_previous();  // (what follows this launch takes those before it as ended)
+  return false;
 }
 
 template <int DK, int DV>

@@ -364,6 +364,20 @@ def test_growth_is_computed_as_given(B, kind):
     check_fwd(B, x)
 
 
+@pytest.mark.parametrize("kind", [(2, 1, 500, 128, 64, "bf16"), (2, 2, 70, 32, 32, "f32")], ids=str)
+def test_powers_of_two_pass_through(B, kind):
+    """Products and sums of inputs times powers of two are those of the inputs, times powers of two: every bit."""
+    x = draw(1, *kind, seed=68, init=False)
+    e = dict(q=-30, k=45, v=25, dout=-28)
+    y = dict(x, **{n: x[n] * 2.0 ** e[n] for n in e})
+    (o, st), d = gpu_fwd(B, x), gpu_bwd(B, x)
+    (oy, sty), dy = gpu_fwd(B, y), gpu_bwd(B, y)
+    whole = sum(e.values())
+    for a, b, by in [(o, oy, whole - e["dout"]), (st, sty, e["k"] + e["v"]), (d[0], dy[0], whole - e["q"]), (d[1], dy[1], whole - e["k"]),
+                     (d[2], dy[2], whole - e["v"]), (d[3], dy[3], whole), (d[4], dy[4], e["q"] + e["dout"])]:
+        assert np.array_equal(a * 2.0 ** by, b) and np.isfinite(b).all()
+
+
 @pytest.mark.parametrize("kind", [(2, 2, 700, 128, 128, "bf16"), (2, 2, 700, 32, 32, "f32")], ids=str)
 def test_bad_decays_stay_within_their_head_and_sequence(B, kind):
     starts, H, T = [0, 200, 650, 700], kind[0], kind[2]
