@@ -13,7 +13,8 @@
 // in the way of the gated delta rule's chunks (gdr.cuh), a segment in the place
 // of a chunk.
 //
-// A segment's log decay is summed in float64 (token by token) or as an integer (in chunks).
+// A segment's log decay is summed in float64 (token by token) or as an integer (in chunks; where only the way
+// back wants it in float32, over at most 1536 tokens).
 #pragma once
 
 #include "gdr.cuh"
