@@ -587,7 +587,11 @@ LL_API ll_status ll_rope_bwd(int B, int H, int Hk, int T, int d, ll_dtype io, co
  * and 128 in chunks of 128 tokens on the tensor cores, where a term of a state (state_out,
  * dstate_in) is off by 2^-17 of itself at most, sums and decays are float32, and scores and
  * states are rounded to bf16 on the way to o, dq, dk and dv.
- * dlog_alpha keeps float32 accuracy relative to the terms that it is a sum of.
+ * dlog_alpha is summed up from k.dk (in chunks v.dv) and q.dq of the tokens, from both ends of
+ * a piece, where its value is known: pieces lie between tokens that forget and the ends of
+ * segments (in chunks of at most 1536 tokens; by sizes alone).  A value is off by the float32
+ * roundings of these terms, not smaller where log_alpha is, on that side of the
+ * token within its piece whose terms have the smaller sum of squares.
  *
  * Infinities and NaN stay within their sequence and head (and its key head's dq and dk); in
  * chunks those of a token can reach the outputs of earlier tokens of its chunk.

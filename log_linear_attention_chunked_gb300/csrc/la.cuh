@@ -155,7 +155,7 @@ ll_status la_tc_sum_launch(const LaArgs& a, int seg, size_t slots, int dirs, flo
                            float* log_decay);
 ll_status la_tc_fwd_main(const LaArgs& a, int seg, size_t slots, const float* states, bool by_slot, bool after);
 ll_status la_tc_bwd_main(const LaArgs& a, int seg, size_t slots, const float* states, const float* adjoints,
-                         bool by_slot, float* before, float* dq32, float* dk32, float* part_q, float* part_v, bool after);
+                         bool by_slot, float* before, float* ends, float* dq32, float* dk32, float* part_q, float* part_v, bool after);
 
 struct LaRope {
   int rot, interleaved;

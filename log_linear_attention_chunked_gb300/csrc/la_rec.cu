@@ -17,9 +17,10 @@
 // that is what the decay's gradient is made of,
 //   dlog_alpha_t = <S, B> + sum_{j < t} (k_j.dk'_j - q_j.dq'_j),
 // over the tokens of the segment, the primes leaving out a token's own pair, S and B the
-// state and its gradient at the segment's start.  (Every partial sum is a dlog_alpha
-// itself: from the segment's end they would be taken from a state that no decay has
-// touched yet, and cancel.)  Sums over the lanes are taken for kLpr
+// state and its gradient at the segment's start, and likewise from the end backwards
+// (finish_decay).  (Every partial sum from the start is a dlog_alpha itself; the first ones from a
+// sequence's end are taken from a state that no decay has touched yet, and may cancel, which the
+// squares of their terms show.)  Sums over the lanes are taken for kLpr
 // tokens at once: each step of a butterfly halves the values that a lane carries.
 //
 // alpha_t is rounded to float32 once a token; what the roundings of a staged tile are off by, those near 1,
@@ -424,7 +425,7 @@ struct FinishParams {
   const float* behind;                       // gradients at the segments' ends by slot,
   const float* first;                        // before the sequences
   float* copy_first;                         // where `first` goes, or null
-  bool close, followed;                      // sums are closed at the segments' ends; the sequences' gradients go on behind them
+  const float *after, *dstate_out;           // behind the sequences: states and their gradients, or null
   float* dlog_alpha;
   double* head_sums;                         // [slot, H] when log_alpha is one to a head
   const float *dq, *dkey;                    // [B,H,T,dk] float32, shared heads
@@ -432,6 +433,7 @@ struct FinishParams {
   unsigned segments, key_rows;               // CTAs of the decays; B Hk T of shared heads
 };
 constexpr int kFinishThreads = 512;
+constexpr int kFinishKept = 3;  // every segment in chunks (at most 12 of 128 tokens)
 __device__ __forceinline__ double warp_sum(double x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -468,37 +470,82 @@ template <typename IO> __device__ __forceinline__ void sum_heads(const FinishPar
   }
   store4(static_cast<IO*>(block & 1 ? p.dk_out : p.dq_out) + (size_t)krow * p.dk + 4 * c, x);
 }
-// The decay's gradient of one (segment, head): a thread sums a run of tokens, then goes over it again.  Sums are
-// pairs of floats (in float64, two operations a cycle and SM, they took 40 of 52 us for 320 segments).
-__device__ __forceinline__ void finish_decay(const FinishParams& p, unsigned block) {
-  constexpr int W = kFinishThreads / 32;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = block % p.seqs.H, slot = block / p.seqs.H;
-  LaSegment s;
-  const bool found = la_find(p.seqs, slot, p.seg, s, nullptr) && s.n > 0;
-  if (!found) {
-    if (p.per_head && tid == 0) p.head_sums[(size_t)slot * p.seqs.H + h] = 0.;
-    return;
+// The decay's gradient of one (segment, head).  It is a running sum whose values at both ends of the segment, and at
+// tokens that forget (zero), are known, so that each token has two values, one summed up from the left and one from
+// the right, and each is off by the roundings of the terms that it went over.  Taken alone, the left one hands those of
+// large early terms to every later token, however short the memory has become (1e-2 of a token's own terms
+// behind values 256 times as large).  The two are joined by the squares of the terms on either side, as independent
+// errors ask for: what the sums differ by goes to where the large terms are.  Sums are pairs of
+// floats (in float64, two operations a cycle and SM, they took 40 of 52 us for 320 segments).
+struct Side {  // a sum towards one side, and of squares; `cut`: it begins at a known value
+  float2 s;
+  float w;
+  bool cut;
+};
+__device__ __forceinline__ Side join(const Side& near, const Side& far) {  // of what is nearer and what lies behind it
+  return near.cut ? near : Side{pair_add(far.s, near.s), far.w + near.w, far.cut};
+}
+__device__ __forceinline__ Side side_of(const Side& x, int lane) {
+  return Side{make_float2(__shfl_sync(0xffffffffu, x.s.x, lane), __shfl_sync(0xffffffffu, x.s.y, lane)),
+              __shfl_sync(0xffffffffu, x.w, lane), __shfl_sync(0xffffffffu, (int)x.cut, lane) != 0};
+}
+// everything up to this lane, from the left (dir = -1) or the right (1)
+__device__ __forceinline__ Side scan_side(Side x, int lane, int dir) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int from = lane + dir * o;
+    const Side y = side_of(x, from & 31);
+    if (from >= 0 && from < 32) x = join(x, y);
   }
+  return x;
+}
+// k.dk (v.dv) and q.dq of a token, and what the sum changes by behind it
+struct Term {
+  float2 x;
+  float k, q;
+};
+constexpr int kMostParts = 4;  // row blocks of 128 rows (row_blocks), halves of the columns in chunks
+__device__ __forceinline__ Term finish_term(const FinishParams& p, size_t at) {
+  float k[kMostParts], q[kMostParts];
+#pragma unroll
+  for (int i = 0; i < kMostParts; ++i)
+    if (i < p.parts) {
+      k[i] = p.part_k[i * p.part_stride + at];
+      q[i] = p.part_q[i * p.part_stride + at];
+    }
+  Term y{make_float2(0.f, 0.f), 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kMostParts; ++i)
+    if (i < p.parts) {
+      y.x = pair_add(y.x, make_float2(k[i], 0.f));
+      y.x = pair_add(y.x, make_float2(-q[i], 0.f));
+      y.k += k[i];
+      y.q += q[i];
+    }
+  return y;
+}
+// KEPT: tokens of a thread that stay in registers (in segments of up to KEPT x kFinishThreads), 0: read again for each pass
+template <int KEPT> __device__ __forceinline__ void finish_decay(const FinishParams& p, const LaSegment& s, int slot, int h) {
+  constexpr int W = kFinishThreads / 32;
+  static_assert(W <= 32, "a lane to each warp's sum");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const size_t row = ((size_t)s.row_b * p.seqs.H + h) * p.seqs.T + s.start;
-  __shared__ float2 red[3][W];
+  __shared__ float2 red[2][W];
+  __shared__ float most[W];
+  __shared__ Side warps[2][W];
   const int elems = p.dk * p.dv;
-  const float* B = s.num > 0 ? p.behind + ((size_t)(slot - 1) * p.seqs.H + h) * elems
-                   : p.first ? p.first + ((size_t)s.seq * p.seqs.H + h) * elems : nullptr;
-  if (p.copy_first && s.num == 0)
-    for (int e = tid; e < elems / 4; e += kFinishThreads)
-      reinterpret_cast<float4*>(p.copy_first + ((size_t)s.seq * p.seqs.H + h) * elems)[e] = reinterpret_cast<const float4*>(B)[e];
-  // <S, B> at the segment's start; `close`: and at its end, where it is known
-  const bool last = (long long)s.num * p.seg + s.n == s.seq_len, close = p.close && (!last || !p.followed);
-  auto at = [&](const float* x, int i) { return reinterpret_cast<const float4*>(x + ((size_t)i * p.seqs.H + h) * elems); };
-  const float4* S = p.entry && B ? at(p.entry, p.by_slot ? slot : s.seq) : nullptr;
-  const float4* S1 = close && !last ? at(p.entry, slot + 1) : nullptr;
-  const float4* B1 = close && !last ? at(p.behind, slot) : nullptr;
+  // <S, B> at the segment's start and at its end
+  const bool last = (long long)s.num * p.seg + s.n == s.seq_len;
+  auto at = [&](const float* x, int i) { return x ? reinterpret_cast<const float4*>(x + ((size_t)i * p.seqs.H + h) * elems) : nullptr; };
+  const float4* B = s.num > 0 ? at(p.behind, slot - 1) : at(p.first, s.seq);
+  const float4* S = B ? at(p.entry, p.by_slot ? slot : s.seq) : nullptr;
+  const float4* S1 = last ? at(p.after, s.seq) : at(p.entry, slot + 1);
+  const float4* B1 = p.by_slot ? at(p.behind, slot) : at(p.dstate_out, s.seq);
   float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
   for (int e = tid; e < elems / 4; e += kFinishThreads) {
     const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4 x = S ? S[e] : z, y = S ? reinterpret_cast<const float4*>(B)[e] : z, x1 = S1 ? S1[e] : z, y1 = S1 ? B1[e] : z;
+    const float4 x = S ? S[e] : z, y = S ? B[e] : z, x1 = S1 ? S1[e] : z, y1 = S1 ? B1[e] : z;
     d0[0] = fmaf(x.x, y.x, d0[0]);
     d0[1] = fmaf(x.y, y.y, d0[1]);
     d0[2] = fmaf(x.z, y.z, d0[2]);
@@ -513,56 +560,119 @@ __device__ __forceinline__ void finish_decay(const FinishParams& p, unsigned blo
   const float2 end = pair_sum(pair_add(pair_add(make_float2(d1[0], 0.f), make_float2(d1[1], 0.f)),
                                        pair_add(make_float2(d1[2], 0.f), make_float2(d1[3], 0.f))));
   const int run = (s.n + kFinishThreads - 1) / kFinishThreads, t0 = min(tid * run, s.n), t1 = min(t0 + run, s.n);
-  auto token = [&](int t) {
-    float2 x = make_float2(0.f, 0.f);
-    for (int i = 0; i < p.parts; ++i) {
-      x = pair_add(x, make_float2(p.part_k[i * p.part_stride + row + t], 0.f));
-      x = pair_add(x, make_float2(-p.part_q[i * p.part_stride + row + t], 0.f));
-    }
-    return x;
-  };
-  float2 own = make_float2(0.f, 0.f);
-#pragma unroll 4
-  for (int t = t0; t < t1; ++t) own = pair_add(own, token(t));
-  float2 x = own;
+  auto forgets = [&](int t) { return gdr_forgets(p.log_alpha[p.per_head ? (size_t)h : row + t]); };
+  Term kept[KEPT > 0 ? KEPT : 1];
+  bool cuts[KEPT > 0 ? KEPT : 1];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const float2 y = make_float2(__shfl_up_sync(0xffffffffu, x.x, o), __shfl_up_sync(0xffffffffu, x.y, o));
-    if (lane >= o) x = pair_add(x, y);
+  for (int j = 0; j < KEPT; ++j)
+    if (t0 + j < t1) {
+      kept[j] = finish_term(p, row + t0 + j);
+      cuts[j] = forgets(t0 + j);
+    }
+  auto term = [&](int j) { return KEPT > 0 ? kept[j] : finish_term(p, row + t0 + j); };
+  auto cut_at = [&](int j) { return KEPT > 0 ? cuts[j] : forgets(t0 + j); };
+  const int most_run = KEPT > 0 ? KEPT : run, own = t1 - t0;
+  // the largest term, which the squares are of a part of
+  float most_mine = 0.f;
+#pragma unroll
+  for (int j = 0; j < most_run; ++j)
+    if (j < own) {
+      const Term y = term(j);
+      most_mine = fmaxf(most_mine, fmaxf(fabsf(y.k), fabsf(y.q)));
+    }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) most_mine = fmaxf(most_mine, __shfl_xor_sync(0xffffffffu, most_mine, o));
+  if (lane == 0) {
+    red[0][warp] = border;
+    red[1][warp] = end;
+    most[warp] = most_mine;
   }
-  if (lane == 31) {
-    red[0][warp] = x;
-    red[1][warp] = border;
-    red[2][warp] = end;
-  }
-  float2 v = make_float2(__shfl_up_sync(0xffffffffu, x.x, 1), __shfl_up_sync(0xffffffffu, x.y, 1));
-  if (lane == 0) v = make_float2(0.f, 0.f);
   __syncthreads();
-  // one warp's lanes hold the warps' sums: those before mine, all of them, and the borders'
+  if (p.copy_first && s.num == 0)  // (this CTA alone reads what stands there, and has)
+    for (int e = tid; e < elems / 4; e += kFinishThreads)
+      reinterpret_cast<float4*>(p.copy_first + ((size_t)s.seq * p.seqs.H + h) * elems)[e] = B[e];
   const float2 z = make_float2(0.f, 0.f);
-  const float2 before = pair_sum(lane < warp ? red[0][lane % W] : z);
-  const float2 start = pair_sum(lane < W ? red[1][lane % W] : z);
-  v = pair_add(v, pair_add(before, start));
-  // what the sum over the whole segment is off by is taken out in proportion to the tokens
-  float off = 0.f;
-  if (close) {
-    const float2 whole = pair_add(start, pair_sum(lane < W ? red[0][lane % W] : z)), last_one = pair_sum(lane < W ? red[2][lane % W] : z);
-    const float2 d = pair_add(whole, make_float2(-last_one.x, -last_one.y));
-    off = (d.x + d.y) / (float)s.n;
-  }
+  const float2 start_at = pair_sum(lane < W ? red[0][lane % W] : z), end_at = pair_sum(lane < W ? red[1][lane % W] : z);
+  float top = lane < W ? most[lane % W] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float unit = top >= 1e-37f ? 1.f / top : 0.f;
+
+  auto square = [&](const Term& y) {
+    const float k = y.k * unit, q = y.q * unit;
+    return fmaf(k, k, q * q);
+  };
+  auto minus = [](float2 x) { return make_float2(-x.x, -x.y); };
+  const Side none{z, 0.f, false};
+  Side l = none, r = none;  // over this thread's tokens
+#pragma unroll
+  for (int j = 0; j < most_run; ++j)
+    if (j < own) {
+      const Term y = term(j);
+      const float w = square(y);
+      if (cut_at(j)) {
+        l = Side{z, 0.f, true};
+        r.cut = true;
+      }
+      l.s = pair_add(l.s, y.x);
+      l.w += w;
+      if (!r.cut) {
+        r.s = pair_add(r.s, minus(y.x));
+        r.w += w;
+      }
+    }
+  l = scan_side(l, lane, -1);
+  r = scan_side(r, lane, 1);
+  if (lane == 31) warps[0][warp] = l;
+  if (lane == 0) warps[1][warp] = r;
+  l = side_of(l, (lane - 1) & 31);
+  r = side_of(r, (lane + 1) & 31);
+  if (lane == 0) l = none;
+  if (lane == 31) r = none;
+  __syncthreads();
+  Side lw = scan_side(lane < W ? warps[0][lane % W] : none, lane, -1), rw = scan_side(lane < W ? warps[1][lane % W] : none, lane, 1);
+  lw = side_of(lw, (warp - 1) & 31);
+  rw = side_of(rw, (warp + 1) & 31);
+  if (warp == 0) lw = none;
+  if (warp == W - 1) rw = none;
+  l = join(l, join(lw, Side{start_at, 0.f, true}));
+  r = join(r, join(rw, Side{end_at, 0.f, true}));
   float2 all = z;
-#pragma unroll 4
-  for (int t = t0; t < t1; ++t) {
-    const float2 y = pair_add(v, make_float2(-off * (float)t, 0.f));
-    const float g = gdr_forgets(p.log_alpha[p.per_head ? (size_t)h : row + t]) ? 0.f : y.x + y.y;
-    if (p.per_head) all = pair_add(all, make_float2(g, 0.f));
-    else p.dlog_alpha[row + t] = g;
-    v = pair_add(v, token(t));
-  }
+  float apart = 0.f, squares = 0.f;  // of this piece: what its two sums differ by; all its squares
+#pragma unroll
+  for (int j = 0; j < most_run; ++j)
+    if (j < own) {
+      const bool cut = cut_at(j);
+      if (cut) l = Side{z, 0.f, true};
+      if (cut || j == 0) {  // as far as the next token that forgets, or on to what comes from the right
+        Side y = none;
+#pragma unroll
+        for (int u = j; u < most_run && (KEPT > 0 || !y.cut); ++u)
+          if (u < own && !y.cut) {
+            const Term x = term(u);
+            if (u > j && cut_at(u)) {
+              y.cut = true;
+            } else {
+              y.s = pair_add(y.s, minus(x.x));
+              y.w += square(x);
+            }
+          }
+        y = join(y, r);
+        const float2 d = pair_add(y.s, minus(l.s));
+        apart = d.x + d.y;
+        squares = l.w + y.w;
+      }
+      const Term x = term(j);
+      const float2 y = pair_add(l.s, make_float2(squares == 0.f ? 0.f : apart * (l.w / squares), 0.f));
+      const float g = cut ? 0.f : y.x + y.y;
+      if (p.per_head) all = pair_add(all, make_float2(g, 0.f));
+      else p.dlog_alpha[row + t0 + j] = g;
+      l.s = pair_add(l.s, x.x);
+      l.w += square(x);
+    }
   if (p.per_head) {
     all = pair_sum(all);
-    __syncthreads();
-    if (lane == 0) red[0][warp] = all;
+    if (lane == 0) red[0][warp] = all;  // (every warp has read it before the barrier above)
     __syncthreads();
     all = pair_sum(lane < W ? red[0][lane % W] : z);
     if (tid == 0) p.head_sums[(size_t)slot * p.seqs.H + h] = (double)all.x + (double)all.y;
@@ -570,8 +680,16 @@ __device__ __forceinline__ void finish_decay(const FinishParams& p, unsigned blo
 }
 template <typename IO> __global__ void __launch_bounds__(kFinishThreads) la_finish_kernel(FinishParams p) {
   la_chain();
-  if (blockIdx.x < p.segments) finish_decay(p, blockIdx.x);
-  else sum_heads<IO>(p, blockIdx.x - p.segments);
+  if (blockIdx.x >= p.segments) return sum_heads<IO>(p, blockIdx.x - p.segments);
+  const int h = blockIdx.x % p.seqs.H, slot = blockIdx.x / p.seqs.H;
+  LaSegment s;
+  if (!la_find(p.seqs, slot, p.seg, s, nullptr) || s.n == 0) {
+    if (p.per_head && threadIdx.x == 0) p.head_sums[(size_t)slot * p.seqs.H + h] = 0.;
+  } else if (s.n <= kFinishKept * kFinishThreads) {
+    finish_decay<kFinishKept>(p, s, slot, h);
+  } else {
+    finish_decay<0>(p, s, slot, h);
+  }
 }
 __global__ void __launch_bounds__(128) la_head_sum_kernel(const double* sums, int slots, int H, float* out) {
   la_chain();
@@ -715,7 +833,7 @@ bool tc_use(const LaArgs& a, bool bwd) {
 struct Plan {
   bool tc, split;  // in chunks; more than one segment
   int seg, parts;
-  size_t slots, sum_s, sum_a, first, dec, part_q, part_k, dq, dk, heads, total;
+  size_t slots, sum_s, sum_a, first, after, dec, part_q, part_k, dq, dk, heads, total;
 };
 // (the workspace cannot depend on which optional tensors a call brings)
 Plan plan_of(const LaArgs& a, bool bwd) {
@@ -739,6 +857,7 @@ Plan plan_of(const LaArgs& a, bool bwd) {
     pl.parts = pl.tc ? 2 : row_blocks(a.dk, a.dv);
     if (pl.split) pl.sum_a = take(states);
     pl.first = take((size_t)la_sequences(a) * a.H * elems_of(a) * 4);
+    pl.after = take((size_t)la_sequences(a) * a.H * elems_of(a) * 4);
     pl.part_q = take(tokens * pl.parts * 4);
     pl.part_k = take(tokens * pl.parts * 4);
     if (a.H != a.Hk) {
@@ -825,12 +944,14 @@ ll_status la_bwd_launch(const LaArgs& a) {
   // state there, and dstate_in.  In dstate_out's place it has to wait until all have read that.
   const bool aside = !pl.split && a.dstate_in == a.dstate_out;
   float* first = a.dstate_in && !aside ? a.dstate_in : a.dstate_in || a.state_in ? reinterpret_cast<float*>(ws + pl.first) : nullptr;
+  // the states behind the sequences, which the last decays' gradients end with where those states have gradients
+  float* after = a.dstate_out ? reinterpret_cast<float*>(ws + pl.after) : nullptr;
   float* part_q = reinterpret_cast<float*>(ws + pl.part_q);
   float* part_k = reinterpret_cast<float*>(ws + pl.part_k);
   float* dq32 = own ? nullptr : reinterpret_cast<float*>(ws + pl.dq);
   float* dk32 = own ? nullptr : reinterpret_cast<float*>(ws + pl.dk);
   if (pl.tc) {
-    st = la_tc_bwd_main(a, pl.seg, pl.slots, states, adjoints, pl.split, first, dq32, dk32, part_q, part_k, chained);
+    st = la_tc_bwd_main(a, pl.seg, pl.slots, states, adjoints, pl.split, first, after, dq32, dk32, part_q, part_k, chained);
     if (st != LL_OK) return st;
   } else {
     RecJob v = job_dv(a), q{}, k{};
@@ -853,6 +974,7 @@ ll_status la_bwd_launch(const LaArgs& a) {
     q.out_f32 = !own;
     q.part = part_q;
     k = q;
+    q.last = after;
     k.y = a.q;
     k.z = a.dout;
     k.x = a.v;
@@ -890,8 +1012,8 @@ ll_status la_bwd_launch(const LaArgs& a) {
   f.behind = sum_a;
   f.first = first;
   f.copy_first = aside ? a.dstate_in : nullptr;
-  f.close = pl.tc;
-  f.followed = a.dstate_out != nullptr;
+  f.after = after;
+  f.dstate_out = a.dstate_out;
   f.dlog_alpha = a.dlog_alpha;
   f.head_sums = reinterpret_cast<double*>(ws + pl.heads);
   f.dq = dq32;

@@ -602,13 +602,23 @@ __device__ __forceinline__ void run_job(const TcParams& p, const TcJob& job, con
       mbar_arrive(bars + kKp);
     }
     if (job.last && (REV ? sg.num == 0 : (long long)sg.num * p.seg + sg.n == sg.seq_len)) {
-      float* dst = job.last + ((size_t)sg.seq * p.seqs.H + h) * elems + (size_t)i * DX + part * N;
-      if (i < DY)
+      float* dst = job.last + ((size_t)sg.seq * p.seqs.H + h) * elems;
+      if (i < DY) {
+        if (trans) {  // lies [DX][DY]
 #pragma unroll
-        for (int e = 0; e < N / 2; e += 2) {
-          const float2 a = unpair(M[e]), b = unpair(M[e + 1]);
-          *reinterpret_cast<float4*>(dst + 2 * e) = make_float4(a.x, a.y, b.x, b.y);
+          for (int e = 0; e < N / 2; ++e) {
+            const float2 a = unpair(M[e]);
+            dst[(size_t)(part * N + 2 * e) * DY + i] = a.x;
+            dst[(size_t)(part * N + 2 * e + 1) * DY + i] = a.y;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < N / 2; e += 2) {
+            const float2 a = unpair(M[e]), b = unpair(M[e + 1]);
+            *reinterpret_cast<float4*>(dst + (size_t)i * DX + part * N + 2 * e) = make_float4(a.x, a.y, b.x, b.y);
+          }
         }
+      }
     }
     tc_fence_before();
   } else {
@@ -1113,8 +1123,8 @@ ll_status la_tc_fwd_main(const LaArgs& a, int seg, size_t slots, const float* st
   return la_launch(after, kernel, dim3((unsigned)grid), kThreads, Sm::kBytes, a.stream, m, p);
 }
 
-ll_status la_tc_bwd_main(const LaArgs& a, int seg, size_t slots, const float* states, const float* adjoints, bool by_slot, float* before, float* dq32,
-                         float* dk32, float* part_q, float* part_v, bool after) {
+ll_status la_tc_bwd_main(const LaArgs& a, int seg, size_t slots, const float* states, const float* adjoints, bool by_slot, float* before,
+                         float* ends, float* dq32, float* dk32, float* part_q, float* part_v, bool after) {
   const uint64_t rows = (uint64_t)a.B * a.H * a.T, krows = (uint64_t)a.B * a.Hk * a.T;
   BwdMaps m;
   if (!make_map(&m.q, a.q, krows, a.dk) || !make_map(&m.k, a.k, krows, a.dk) || !make_map(&m.v, a.v, rows, a.dv) ||
@@ -1122,7 +1132,7 @@ ll_status la_tc_bwd_main(const LaArgs& a, int seg, size_t slots, const float* st
       !make_map(&m.dv, a.dval, rows, a.dv))
     return LL_ERR_CUDA;
   TcParams p = tc_params(a, seg);
-  p.job[0] = TcJob{states, nullptr, by_slot, dq32, part_q, a.dq};
+  p.job[0] = TcJob{states, ends, by_slot, dq32, part_q, a.dq};
   p.job[1] = TcJob{adjoints, before, by_slot, nullptr, part_v, a.dval};
   p.job[2] = TcJob{adjoints, nullptr, by_slot, dk32, nullptr, a.dkey};
   auto kernel = a.dk == 128 ? (a.dv == 128 ? la_tc_bwd_kernel<128, 128> : la_tc_bwd_kernel<128, 64>)

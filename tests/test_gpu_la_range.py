@@ -1,0 +1,104 @@
+"""GPU parity of linear attention with a decay per head (ll_la_bwd) against the recurrence in 64 bits (oracle.la)
+where memory changes within a segment.
+
+Tolerances of dlog_alpha.  A token's value is a sum of terms along the sequence, of products of v and dv (k and dk)
+and of q and dq, from the nearer of the two ends of its piece: segments and tokens that forget.  With D the standard deviation of a
+term's error relative to its size, the sum over n tokens is off by D sqrt(sum of squares) (2-norm), and over some ten
+thousand tokens of a test no value by more than five times that; on top TOL_F32 of the largest term for the border's
+own product, as in tests/test_gpu_la.py.  In chunks D is 1.6e-6 (states in two bf16 parts), token by token it is
+2^-22: a float32 product of 128 elements and the two sums that it is made of, each rounded by half of 2^-23, with a few of
+the recurrence's own roundings."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import la
+from tests._parity import TOL_F32
+from tests.test_gpu_la import B, draw, gpu_bwd  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+D_CHUNKS, D_TOKENS = 1.6e-6, 2.0 ** -22
+
+
+def in_chunks(x, starts, bwd):
+    """Does a call of these tensors go in chunks?  (bf16, 64 and 128, from some mean length on.)"""
+    Bn, _, T, dk = x["q"].shape
+    H, dv = x["v"].shape[1], x["v"].shape[3]
+    if x["q"].dtype != torch.bfloat16 or min(dk, dv) < 64:
+        return False
+    n = Bn if starts is None else len(starts) - 1
+    mean = T if starts is None else -(-T // n)
+    few = n * H <= 152
+    return mean >= ((48 if few else 24) if dk * dv > 64 * 64 else (16 if few else 48) + (16 if bwd else 0))
+
+
+def head(x, starts, i, h):
+    """What the oracle takes of sequence i and value head h, and where it stands."""
+    b, lo, hi = (i, 0, x["q"].shape[2]) if starts is None else (0, starts[i], starts[i + 1])
+    hk = h // (x["v"].shape[1] // x["q"].shape[1])
+    f = {n: x[n][b, hk if n in "qk" else h, lo:hi].double().numpy() for n in ("q", "k", "v", "dout")}
+    ga = x["log_alpha"]
+    ga = np.full(hi - lo, float(ga[h])) if ga.dim() == 1 else ga[b, h, lo:hi].double().numpy()
+    st, ds = [x[n][i, h].double().numpy() if n in x else None for n in ("state_in", "dstate_out")]
+    return (b, hk, lo, hi), [f["q"], f["k"], f["v"], ga], f["dout"], st, ds
+
+
+def squares(a, r):
+    """The squares of a token's terms."""
+    return (a[0] * r["dq"]).sum(-1) ** 2 + np.maximum((a[1] * r["dk"]).sum(-1) ** 2, (a[2] * r["dv"]).sum(-1) ** 2)
+
+
+# ---------------------------------------------------------------- memory that changes within a segment
+@pytest.mark.parametrize("kind", [(2, 16, 16, 128, 128, "bf16"), (2, 16, 8, 64, 64, "bf16"), (4, 16, 16, 128, 128, "f32"),
+                                  (1, 2, 1, 32, 16, "f32"), (1, 2, 2, 64, 128, "bf16")], ids=str)
+@pytest.mark.parametrize("how", ["forgets", "shortens", "forgets and grows"])
+def test_decay_gradients_after_large_values(B, how, kind):  # noqa: F811
+    """A long memory of values 256 times as large comes before (behind) a short one.  The gradients of the short one's
+    decays are held to its own terms."""
+    Bn, H, Hk, dk, dv, io = kind
+    T, at = 3000, 1700
+    x = draw(Bn, H, Hk, T, dk, dv, io, seed=81, init=how == "shortens", rate=1e-3)
+    big, small = (slice(at, T), slice(0, at)) if how == "forgets and grows" else (slice(0, at), slice(at, T))
+    x["v"][:, :, big] *= 256
+    x["log_alpha"][:, :, small] = -torch.empty(Bn, H, T)[:, :, small].uniform_(0.7, 1.3, generator=torch.Generator().manual_seed(3))
+    if how != "shortens":
+        x["log_alpha"][:, :, at] = -float("inf")
+    dla = gpu_bwd(B, x)[3]
+    D = D_CHUNKS if in_chunks(x, None, True) else D_TOKENS
+    for b, h in ((0, 0), (Bn - 1, H - 1)):
+        _, a, do, s0, ds = head(x, None, b, h)
+        r = la.backward(*a, do, scale=0.5, state=s0, dstate=ds)
+        # (30 tokens at e^-1 leave e^-30 of the large values)
+        part = slice(at + 30, T) if how == "shortens" else small
+        s2 = squares(a, r)[part]
+        bound = 5 * D * np.sqrt(s2.sum()) + TOL_F32 * max(np.sqrt(s2.max()), r["terms"][part].max())
+        err = np.abs(dla[b, h] - r["dlog_alpha"])
+        assert err[part].max() <= bound, (b, h, err[part].max() / bound)
+        s2 = squares(a, r)
+        assert err.max() <= 5 * D * np.sqrt(s2.sum()) + TOL_F32 * max(np.sqrt(s2.max()), r["terms"].max())
+
+
+@pytest.mark.parametrize("kind", [(2, 16, 16, 128, 128, "bf16"), (1, 2, 1, 64, 64, "bf16"), (4, 16, 16, 128, 128, "f32"),
+                                  (1, 3, 3, 16, 32, "f32")], ids=str)
+def test_tokens_that_forget_keep_pieces_apart(B, kind):  # noqa: F811
+    """Pieces between tokens that forget, some of one token, with values from 2^-12 to 2^12: each held to its own terms."""
+    Bn, H, Hk, dk, dv, io = kind
+    T = 2500
+    x = draw(Bn, H, Hk, T, dk, dv, io, seed=82, rate=0.02)
+    cuts = [1, 2, 3, 40, 127, 128, 129, 300, 301, 600, 640, 1023, 1024, 1400, 1402, 1900, 2300, 2499]
+    for n, (lo, hi) in enumerate(zip([0] + cuts, cuts + [T])):
+        x["v"][:, :, lo:hi] *= 2.0 ** ((n * 7) % 25 - 12)
+    x["state_in"] *= 1000
+    x["dstate_out"] *= 1000
+    x["log_alpha"][:, :, cuts] = -float("inf")
+    dla = gpu_bwd(B, x)[3]
+    D = D_CHUNKS if in_chunks(x, None, True) else D_TOKENS
+    for b, h in ((0, 0), (Bn - 1, H - 1)):
+        _, a, do, s0, ds = head(x, None, b, h)
+        r = la.backward(*a, do, scale=0.5, state=s0, dstate=ds)
+        s2 = squares(a, r)
+        assert (dla[b, h, cuts] == 0).all()
+        for lo, hi in zip([0] + cuts, cuts + [T]):
+            bound = 5 * D * np.sqrt(s2[lo:hi].sum()) + TOL_F32 * max(np.sqrt(s2[lo:hi].max()), r["terms"][lo:hi].max())
+            assert np.abs(dla[b, h, lo:hi] - r["dlog_alpha"][lo:hi]).max() <= bound, (b, h, lo)
