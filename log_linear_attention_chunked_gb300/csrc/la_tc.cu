@@ -10,13 +10,13 @@
 //   dq   q = dO,  k = V,   v = K,   M = S^T     forwards
 //   dk   q = V,   k = dO,  v = Q,   M = A^T     backwards
 //   dv   q = K,   k = Q,   v = dO,  M = A       backwards
-// Five products of 128 x 128 x 128 a chunk: q k^T, q M^T, P v and twice v^T k'.
+// Five products of 128 x 128 x 128 a chunk: q k^T, q M^T, P v and v^T k' of two parts; six of three.
 //
-// Precision.  States (and their gradients) are float32 results: k' = weight k goes
-// into their products in two bf16 parts, 16 bits, off by 2^-17 of a term at most (2.5e-6 of a
-// state's norm).  P and the state in q M^T are rounded to bf16 once, as the
-// output is.  Where the decay's gradient is made of the states (dq, dv and their
-// segments' sums), k' has three parts, 24 bits, and the state in q M^T two, and what lies within
+// Precision.  States (and their gradients) that leave the call are float32 results: k' = weight k goes
+// into their products in three bf16 parts, all of float32's 24 bits (1.5e-7 of a state's norm; with two it was
+// 2.5e-6).  A state that goes no further than o, which is rounded to bf16, has two.  P and the state
+// in q M^T are rounded to bf16 once, as the output is.  Where the decay's gradient is made of the states (dq, dv and
+// their segments' sums), k' has three parts too and the state in q M^T two, and what lies within
 // the chunk is summed in float32 from two tiles of scores: sum_j P_ij (w v^T)_ij with w = Q (V).
 // bf16 has float32's range, so no operand is scaled.
 //
@@ -320,7 +320,9 @@ static __device__ __noinline__ void zero_rows(unsigned char* tile, uint32_t full
 // One segment of one head.  DX: columns of q and k, DY of v (and w) and of the output.
 //   NT = 4: w is loaded too, the state has two parts, row products are written.
 // Tiles go through a ring of buffers in the order of use.  Of the buffers that are left one
-// holds the state and another its low part, and once q M^T is done that of k' (k' high takes k's place).
+// holds the state and another its low part, and once q M^T is done that of k' (k' high takes k's place).  The third
+// part of k' takes the state's place (NT = 4) or, where q M^T waits for the outputs' way out and k' would wait
+// for it, one of the ring's (`third`: a state that is returned; 16384 tokens, 16 heads: 65 us where 58 with two parts).
 // The output is staged in v's place, with NT = 4 in w's.  The roles' code is kept short, in loops: unrolled
 // (90 KB) it left the instruction cache and every phase waited for its instructions.  With NT = 4 it has to be
 // shorter still, products and waits as calls (SHORT: 155 us where 190, 63 % of requests hit instead of 52; without
@@ -336,7 +338,8 @@ __device__ __forceinline__ void run_job(const TcParams& p, const TcJob& job, con
                                         bool k_key, bool v_key, bool w_key, bool trans, const LaSegment& sg, int slot, int h,
                                         unsigned char* s) {
   constexpr bool LO = NT == 4;
-  constexpr int kRing = kBufs - 2;
+  const bool third = !LO && job.last;
+  const int ring = third ? kBufs - 3 : kBufs - 2;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hk = h / (p.seqs.H / p.seqs.Hk);
   const size_t row = ((size_t)sg.row_b * p.seqs.H + h) * p.seqs.T + sg.start;
@@ -347,20 +350,20 @@ __device__ __forceinline__ void run_job(const TcParams& p, const TcJob& job, con
   const uint32_t sbars = smem_u32(bars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s + Sm::kSlot);
   Tab* tab = reinterpret_cast<Tab*>(s + Sm::kLog);
-  unsigned char* mb = s + kRing * kTile;
+  unsigned char* mb = s + (kBufs - 2) * kTile;
   unsigned char* mlo = mb + kTile;
   auto chunk_at = [&](int x) { return REV ? chunks - 1 - x : x; };
   // where in the ring a chunk's tiles begin, and on which time round; tile j's buffer, the parity of its arrival
   int rb = 0, rn = 0;
   auto next_chunk = [&]() {
     rb += NT;
-    if (rb >= kRing) {
-      rb -= kRing;
+    if (rb >= ring) {
+      rb -= ring;
       ++rn;
     }
   };
-  auto buf = [&](int j) { return rb + j >= kRing ? rb + j - kRing : rb + j; };
-  auto par = [&](int j) { return (rb + j >= kRing ? rn + 1 : rn) & 1; };
+  auto buf = [&](int j) { return rb + j >= ring ? rb + j - ring : rb + j; };
+  auto par = [&](int j) { return (rb + j >= ring ? rn + 1 : rn) & 1; };
   auto wait = [&](int b, uint32_t parity) {
     if (SHORT || !try_wait_at(sbars + 8 * b, parity)) wait_at(sbars + 8 * b, parity, p.err);
   };
@@ -388,7 +391,7 @@ __device__ __forceinline__ void run_job(const TcParams& p, const TcJob& job, con
         const int t0 = chunk_at(x) * kC;
 #pragma unroll 1
         for (int j = 0; j < NT; ++j) {
-          const int b = buf(j), n = rb + j >= kRing ? rn + 1 : rn;
+          const int b = buf(j), n = rb + j >= ring ? rn + 1 : rn;
           if (n > 0) wait(kEmpty + b, (n - 1) & 1);
           const CUtensorMap* m = j == W ? mw : j == Q ? mq : j == K ? mk : mv;
           const bool key = j == W ? w_key : j == Q ? q_key : j == K ? k_key : v_key;
@@ -402,7 +405,7 @@ __device__ __forceinline__ void run_job(const TcParams& p, const TcJob& job, con
     }
   } else if (warp == kIssueWarp) {
     if (lane == 0) {
-      const uint32_t smb = sbuf + kRing * kTile, low = smb + kTile;
+      const uint32_t smb = sbuf + (kBufs - 2) * kTile, low = smb + kTile, rest = LO ? smb : smb - kTile;
 #pragma unroll 1
       for (int x = 0; x < chunks; ++x, next_chunk()) {
         const int ph = x & 1;
@@ -436,9 +439,10 @@ __device__ __forceinline__ void run_job(const TcParams& p, const TcJob& job, con
         wait(kKp, ph);
         if (!LO) wait(kFull + buf(V), par(V));
         tc_fence_after();
-        mma_mm<SHORT>(tmem + kTmM, v, k, idesc_bf16(128, DX, true, true), false);
-        mma_mm<SHORT>(tmem + kTmM, v, low, idesc_bf16(128, DX, true, true), true);
-        if (LO) mma_mm<SHORT>(tmem + kTmM, v, smb, idesc_bf16(128, DX, true, true), true);
+        // the least first: a sum is cut off as often as it is added to, and only large ones by much
+        mma_mm<SHORT>(tmem + kTmM, v, low, idesc_bf16(128, DX, true, true), false);
+        if (LO || third) mma_mm<SHORT>(tmem + kTmM, v, rest, idesc_bf16(128, DX, true, true), true);
+        mma_mm<SHORT>(tmem + kTmM, v, k, idesc_bf16(128, DX, true, true), true);
         umma_commit(bars + kS4);
         umma_commit(bars + kEmpty + buf(K));
         if (LO) umma_commit(bars + kEmpty + buf(V));
@@ -571,6 +575,7 @@ __device__ __forceinline__ void run_job(const TcParams& p, const TcJob& job, con
       d = tab->decay;
       const f2 ww = pair(weight, weight);
       const ptrdiff_t to_low = mlo - kb;
+      const int low_to_rest = LO ? kTile : 2 * kTile;  // downwards
 #pragma unroll 1
       for (int e8 = 0; e8 < N / 8; e8 += 2) {  // two pieces at a time: their chains run side by side
         uint4 v[2];
@@ -584,18 +589,18 @@ __device__ __forceinline__ void run_job(const TcParams& p, const TcJob& job, con
           for (int e = 0; e < 4; ++e) {
             f2 a = mul2(unpack2(hi[e]), ww);
             hi[e] = take2(a);
-            lo[e] = LO ? take2(a) : pack2(a);
-            if (LO) rest[e] = pack2(a);
+            lo[e] = take2(a);
+            rest[e] = pack2(a);
           }
           *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           *reinterpret_cast<uint4*>(at + to_low) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          if (LO) *reinterpret_cast<uint4*>(at + to_low - kTile) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+          if (LO || third) *reinterpret_cast<uint4*>(at + to_low - low_to_rest) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
         }
       }
       if (n < kC) {  // rows of other sequences: zeros, whatever they hold
         zero_rows(kb, sbars + 8 * (kFull + buf(K)), par(K), i, n, part * (N / 8), N / 8, p.err);
         zero_rows(mlo, sbars + 8 * (kFull + buf(K)), par(K), i, n, part * (N / 8), N / 8, p.err);
-        if (LO) zero_rows(mb, sbars + 8 * (kFull + buf(K)), par(K), i, n, part * (N / 8), N / 8, p.err);
+        if (LO || third) zero_rows(mlo - low_to_rest, sbars + 8 * (kFull + buf(K)), par(K), i, n, part * (N / 8), N / 8, p.err);
       }
       if (!LO && n < kC) zero_rows(s + buf(V) * kTile, sbars + 8 * (kFull + buf(V)), par(V), i, n, part * kVN, kVN, p.err);
       fence_proxy_async_shared();
@@ -928,9 +933,9 @@ __global__ void __launch_bounds__(kSumThreads, 1) la_tc_sum_kernel(const __grid_
         wait_bar(bars + bv, n & 1, p.err);
         wait_bar(bars + kReady, x & 1, p.err);
         tc_fence_after();
-        mma_mm<false>(acc, sbuf + bv * kTile, sbuf + bk * kTile, idesc_bf16(128, DK, true, true), false);
-        mma_mm<false>(acc, sbuf + bv * kTile, sbuf + kSumRing * kTile, idesc_bf16(128, DK, true, true), true);
+        mma_mm<false>(acc, sbuf + bv * kTile, sbuf + kSumRing * kTile, idesc_bf16(128, DK, true, true), false);
         if (PARTS == 3) mma_mm<false>(acc, sbuf + bv * kTile, sbuf + (kSumRing + 1) * kTile, idesc_bf16(128, DK, true, true), true);
+        mma_mm<false>(acc, sbuf + bv * kTile, sbuf + bk * kTile, idesc_bf16(128, DK, true, true), true);
         umma_commit(bars + kSumRing + bk);
         umma_commit(bars + kSumRing + bv);
         umma_commit(bars + kDone);
@@ -1096,10 +1101,11 @@ ll_status la_tc_sum_launch(const LaArgs& a, int seg, size_t slots, int dirs, flo
       !make_map(&m.dout, a.dout ? a.dout : a.v, rows, a.dv))
     return LL_ERR_CUDA;
   SumParams p{la_seqs(a), seg, a.per_head, a.dk, a.dv, dirs, a.scale, a.log_alpha, {sum_s, sum_a}, log_decay, a.err};
-  auto kernel = dirs == 1 ? (a.dk == 128 ? (a.dv == 128 ? la_tc_sum_kernel<128, 128, 2> : la_tc_sum_kernel<128, 64, 2>)
-                                         : (a.dv == 128 ? la_tc_sum_kernel<64, 128, 2> : la_tc_sum_kernel<64, 64, 2>))
-                          : (a.dk == 128 ? (a.dv == 128 ? la_tc_sum_kernel<128, 128, 3> : la_tc_sum_kernel<128, 64, 3>)
-                                         : (a.dv == 128 ? la_tc_sum_kernel<64, 128, 3> : la_tc_sum_kernel<64, 64, 3>));
+  const bool two = dirs == 1 && !a.state_out;  // (states that go no further than the outputs)
+  auto kernel = two ? (a.dk == 128 ? (a.dv == 128 ? la_tc_sum_kernel<128, 128, 2> : la_tc_sum_kernel<128, 64, 2>)
+                                   : (a.dv == 128 ? la_tc_sum_kernel<64, 128, 2> : la_tc_sum_kernel<64, 64, 2>))
+                    : (a.dk == 128 ? (a.dv == 128 ? la_tc_sum_kernel<128, 128, 3> : la_tc_sum_kernel<128, 64, 3>)
+                                   : (a.dv == 128 ? la_tc_sum_kernel<64, 128, 3> : la_tc_sum_kernel<64, 64, 3>));
   const size_t grid = slots * a.H * dirs;
   if (grid > 0x7fffffffull) return LL_ERR_UNSUPPORTED;
   return la_launch(false, kernel, dim3((unsigned)grid), kSumThreads, Sm::kBytes, a.stream, m, p);

@@ -1,5 +1,5 @@
 """GPU parity of linear attention with a decay per head (ll_la_bwd) against the recurrence in 64 bits (oracle.la)
-where memory changes within a segment.
+where memory changes within a segment, and the accuracy of states.
 
 Tolerances of dlog_alpha.  A token's value is a sum of terms along the sequence, of products of v and dv (k and dk)
 and of q and dq, from the nearer of the two ends of its piece: segments and tokens that forget.  With D the standard deviation of a
@@ -15,7 +15,7 @@ import torch
 
 from oracle import la
 from tests._parity import TOL_F32
-from tests.test_gpu_la import B, draw, gpu_bwd  # noqa: F401
+from tests.test_gpu_la import B, draw, gpu_bwd, gpu_fwd  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 D_CHUNKS, D_TOKENS = 1.6e-6, 2.0 ** -22
@@ -102,3 +102,22 @@ def test_tokens_that_forget_keep_pieces_apart(B, kind):  # noqa: F811
         for lo, hi in zip([0] + cuts, cuts + [T]):
             bound = 5 * D * np.sqrt(s2[lo:hi].sum()) + TOL_F32 * max(np.sqrt(s2[lo:hi].max()), r["terms"][lo:hi].max())
             assert np.abs(dla[b, h, lo:hi] - r["dlog_alpha"][lo:hi]).max() <= bound, (b, h, lo)
+
+
+@pytest.mark.parametrize("kind", [(1, 2, 2, 77, 128, 128, None), (1, 2, 1, 1000, 128, 64, None), (1, 2, 2, 2100, 64, 64, None),
+                                  (2, 2, 1, 500, 64, 128, None), (1, 2, 1, 1300, 128, 128, [0, 5, 700, 700, 1297])], ids=str)
+def test_states_keep_float32(B, kind):  # noqa: F811
+    """What leaves a call as float32 is a sum of float32: products of three bf16 parts are exact to 2^-24, the tensor
+    cores' eight steps of a chunk are cut off by 2^-24 of the sum so far on average (3.3e-7 as that grows like the root of
+    the steps), and weights and additions round by 2^-24.  Twice that, 2-norm, is allowed: 1e-6.  (Two parts: 2.4e-6.)"""
+    Bn, H, Hk, T, dk, dv, starts = kind
+    x = draw(Bn, H, Hk, T, dk, dv, "bf16", n=Bn if starts is None else len(starts) - 1, seed=86, rate=0.01)
+    assert in_chunks(x, starts, True)
+    st, dst = gpu_fwd(B, x, starts)[1], gpu_bwd(B, x, starts)[4]
+    for i in range(len(st)):
+        for h in range(H):
+            _, a, do, s0, ds = head(x, starts, i, h)
+            want = la.forward(*a, scale=0.5, state=s0)[1]
+            assert np.linalg.norm(st[i, h] - want) <= 1e-6 * np.linalg.norm(want), (i, h, "state_out")
+            want = la.backward(*a, do, scale=0.5, state=s0, dstate=ds)["dstate_in"]
+            assert np.linalg.norm(dst[i, h] - want) <= 1e-6 * np.linalg.norm(want), (i, h, "dstate_in")
