@@ -586,7 +586,7 @@ LL_API ll_status ll_rope_bwd(int B, int H, int Hk, int T, int d, ll_dtype io, co
  * Computed in float32, each output rounded once; long bf16 sequences with head dims of 64
  * and 128 in chunks of 128 tokens on the tensor cores, where what is summed up to a state
  * (state_out, dstate_in) keeps float32's 24 bits, sums and decays are float32, and scores and
- * states are rounded to bf16 on the way to o, dq, dk and dv.
+ * states are rounded to bf16 on the way to o, dq, dk and dv (not on that to dlog_alpha).
  * dlog_alpha is summed up from k.dk (in chunks v.dv) and q.dq of the tokens, from both ends of
  * a piece, where its value is known: pieces lie between tokens that forget and the ends of
  * segments (in chunks of at most 1536 tokens; by sizes alone).  A value is off by the float32

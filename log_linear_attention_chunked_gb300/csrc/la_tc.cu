@@ -16,8 +16,10 @@
 // into their products in three bf16 parts, all of float32's 24 bits (1.5e-7 of a state's norm; with two it was
 // 2.5e-6).  A state that goes no further than o, which is rounded to bf16, has two.  P and the state
 // in q M^T are rounded to bf16 once, as the output is.  Where the decay's gradient is made of the states (dq, dv and
-// their segments' sums), k' has three parts too and the state in q M^T two, and what lies within
-// the chunk is summed in float32 from two tiles of scores: sum_j P_ij (w v^T)_ij with w = Q (V).
+// their segments' sums), k' and the state in q M^T have three parts, and what lies within
+// the chunk is summed in float32 from two tiles of scores: sum_j P_ij (w v^T)_ij with w = Q (V).  (Two parts of the
+// state: 2.2e-6 of d log alpha at B 2, H 16, T 4096, three 3.3e-7; 9 us of 216, since the high part waits for
+// the least one's product in its place.)
 // bf16 has float32's range, so no operand is scaled.
 //
 // Bound: the chain of a chunk, 2.7 us of which the products take half (the scores' masking and k' stand between
@@ -120,12 +122,12 @@ constexpr int kBarRows = 1, kBarState = 2;  // named barriers of the groups
 struct Sm {
   static constexpr uint32_t kLog = kBufs * kTile;            // behind the tiles, the chunk's decays: Tab
   static constexpr uint32_t kBars = kLog + 2624;
-  static constexpr uint32_t kSlot = kBars + (2 * kBufs + 11) * 8;
+  static constexpr uint32_t kSlot = kBars + (2 * kBufs + 13) * 8;
   static constexpr uint32_t kBytes = kSlot + 16;
 };
 static_assert(Sm::kBytes <= 232448, "shared memory budget of one CTA");
-enum Bar : int { kFull = 0, kEmpty = kBufs, kS1 = 2 * kBufs, kS2, kS3, kS4, kMb, kP, kKp, kTab, kRead, kStaged, kStored, kNumBars };
-static_assert(kNumBars <= 2 * kBufs + 11, "room for the barriers");
+enum Bar : int { kFull = 0, kEmpty = kBufs, kS1 = 2 * kBufs, kS2, kS3, kS4, kMb, kP, kKp, kTab, kRead, kStaged, kStored, kLeast, kMhi, kNumBars };
+static_assert(kNumBars <= 2 * kBufs + 13, "room for the barriers");
 
 // The log decays of a chunk are summed as integers of 2^-36, exactly, so that a
 // sum over the rest of a block is a difference, and one of far smaller ones behind a large
@@ -318,10 +320,10 @@ static __device__ __noinline__ void zero_rows(unsigned char* tile, uint32_t full
 }
 
 // One segment of one head.  DX: columns of q and k, DY of v (and w) and of the output.
-//   NT = 4: w is loaded too, the state has two parts, row products are written.
+//   NT = 4: w is loaded too, the state has three parts, row products are written.
 // Tiles go through a ring of buffers in the order of use.  Of the buffers that are left one
-// holds the state and another its low part, and once q M^T is done that of k' (k' high takes k's place).  The third
-// part of k' takes the state's place (NT = 4) or, where q M^T waits for the outputs' way out and k' would wait
+// holds the state and another its low part (the least part goes first, in the high one's place), and once
+// q M^T is done that of k' (k' high takes k's place).  The third part of k' takes the state's place (NT = 4) or, where q M^T waits for the outputs' way out and k' would wait
 // for it, one of the ring's (`third`: a state that is returned; 16384 tokens, 16 heads: 65 us where 58 with two parts).
 // The output is staged in v's place, with NT = 4 in w's.  The roles' code is kept short, in loops: unrolled
 // (90 KB) it left the instruction cache and every phase waited for its instructions.  With NT = 4 it has to be
@@ -371,7 +373,7 @@ __device__ __forceinline__ void run_job(const TcParams& p, const TcJob& job, con
 
   if (tid == 0) {
     for (int b = 0; b < kNumBars; ++b)
-      mbar_init(bars + b, b == kMb || b == kKp ? kStateThreads : b == kP || b == kRead || b == kStaged ? kRowThreads : b == kTab ? 32 : 1);
+      mbar_init(bars + b, b == kMb || b == kMhi || b == kKp ? kStateThreads : b == kP || b == kRead || b == kStaged ? kRowThreads : b == kTab ? 32 : 1);
     fence_mbar_init();
   }
   if (warp == kIssueWarp) {
@@ -426,7 +428,13 @@ __device__ __forceinline__ void run_job(const TcParams& p, const TcJob& job, con
         if (!LO && x > 0) wait(kRead, (x - 1) & 1);
         tc_fence_after();
         mma_kk<SHORT, DX>(tmem + kTmO1, q, smb, idesc_bf16(128, DY, false, false), false);
-        if (LO) mma_kk<SHORT, DX>(tmem + kTmO1, q, low, idesc_bf16(128, DY, false, false), true);
+        if (LO) {  // the least part was in the high one's place
+          umma_commit(bars + kLeast);
+          mma_kk<SHORT, DX>(tmem + kTmO1, q, low, idesc_bf16(128, DY, false, false), true);
+          wait(kMhi, ph);
+          tc_fence_after();
+          mma_kk<SHORT, DX>(tmem + kTmO1, q, smb, idesc_bf16(128, DY, false, false), true);
+        }
         umma_commit(bars + kS2);
         umma_commit(bars + kEmpty + buf(Q));
         auto output = [&]() {
@@ -542,28 +550,35 @@ __device__ __forceinline__ void run_job(const TcParams& p, const TcJob& job, con
         }
       }
       if (x == chunks) break;
-      if (DY == 128 || w4 < 2) {
+      auto put_state = [&](bool least) {  // (NT = 4) the two lower parts, then the high one in the least one's place
+        if (DY == 128 || w4 < 2) {
 #pragma unroll
-        for (int c = 0; c < N; c += 8) {
-          uint32_t hi[4], lo[4];
+          for (int c = 0; c < N; c += 8) {
+            uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            f2 a = M[(c >> 1) + v];
-            if (LO) {
-              hi[v] = take2(a);
-              lo[v] = pack2(a);
-            } else {
-              hi[v] = pack2(a);
+            for (int v = 0; v < 4; ++v) {
+              f2 a = M[(c >> 1) + v];
+              hi[v] = LO && least ? take2(a) : pack2(a);
+              if (LO && least) {
+                lo[v] = take2(a);
+                hi[v] = pack2(a);
+              }
             }
+            const uint32_t at = swz16(i, (part * N + c) >> 3);
+            *reinterpret_cast<uint4*>(mb + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (LO && least) *reinterpret_cast<uint4*>(mlo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
-          const uint32_t at = swz16(i, (part * N + c) >> 3);
-          *reinterpret_cast<uint4*>(mb + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          if (LO) *reinterpret_cast<uint4*>(mlo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
-      }
+        fence_proxy_async_shared();
+      };
+      put_state(true);
       tc_fence_before();
-      fence_proxy_async_shared();
       mbar_arrive(bars + kMb);
+      if (LO) {
+        LL_GROUP_WAIT(warp == kStateWarp, kBarState, kStateThreads, wait(kLeast, ph));
+        put_state(false);
+        mbar_arrive(bars + kMhi);
+      }
       // k' high in k's place, low in that of the state's low part
       unsigned char* kb = s + buf(K) * kTile;
       LL_GROUP_WAIT(warp == kStateWarp, kBarState, kStateThreads, {

@@ -121,3 +121,31 @@ def test_states_keep_float32(B, kind):  # noqa: F811
             assert np.linalg.norm(st[i, h] - want) <= 1e-6 * np.linalg.norm(want), (i, h, "state_out")
             want = la.backward(*a, do, scale=0.5, state=s0, dstate=ds)["dstate_in"]
             assert np.linalg.norm(dst[i, h] - want) <= 1e-6 * np.linalg.norm(want), (i, h, "dstate_in")
+
+
+@pytest.mark.parametrize("kind", [(2, 4, 4, 105, 128, 128, None, False, True), (1, 4, 2, 340, 128, 128, [0, 100, 220, 340], True, False),
+                                  (3, 8, 4, 128, 64, 128, None, True, True), (2, 4, 4, 121, 64, 64, None, False, True),
+                                  (1, 2, 2, 90, 128, 64, None, True, False)], ids=str)
+def test_decay_gradients_keep_float32(B, kind):  # noqa: F811
+    """Sequences of one chunk, whose two ends are known.  A term is a product of float32 values, the tensor cores' sum cut
+    off as in test_states_keep_float32, and rounded a few times by 2^-24: 5e-7.  With independent errors, L of them squared on a
+    token's left and R on its right, the joined sum is off by the root of L R / (L + R); a border's product of a state and
+    a gradient, each within 1.7e-7, by 2.5e-7 of its terms, which every token shares.  All 2-norms over the tokens.
+    (Terms from states in two bf16 parts, 1.6e-6, do not pass.)"""
+    Bn, H, Hk, T, dk, dv, starts, init, final = kind
+    x = draw(Bn, H, Hk, T, dk, dv, "bf16", n=Bn if starts is None else len(starts) - 1, seed=87, rate=0.05)
+    assert in_chunks(x, starts, True)
+    for n, there in (("state_in", init), ("dstate_out", final)):
+        if not there:
+            del x[n]
+    dla = gpu_bwd(B, x, starts)[3]
+    for i in range(Bn if starts is None else len(starts) - 1):
+        for h in range(H):
+            (b, _, lo, hi), a, do, s0, ds = head(x, starts, i, h)
+            r = la.backward(*a, do, scale=0.5, state=s0, dstate=ds)
+            left = np.concatenate([[0.0], np.cumsum(squares(a, r))])[:-1]
+            right = squares(a, r).sum() - left
+            ends = max(r["terms"][0], np.linalg.norm(la.forward(*a, scale=0.5, state=s0)[1] * (0.0 if ds is None else ds)))
+            err = np.linalg.norm(dla[b, h, lo:hi] - r["dlog_alpha"])
+            bound = 5e-7 * np.sqrt((left * right / (left + right)).sum()) + 2.5e-7 * ends * np.sqrt(hi - lo)
+            assert err <= bound, (i, h)
