@@ -594,7 +594,8 @@ LL_API ll_status ll_rope_bwd(int B, int H, int Hk, int T, int d, ll_dtype io, co
  * token within its piece whose terms have the smaller sum of squares.
  *
  * Infinities and NaN stay within their sequence and head (and its key head's dq and dk); in
- * chunks those of a token can reach the outputs of earlier tokens of its chunk.
+ * chunks those of a token can reach the outputs of earlier tokens of its chunk, and an infinite
+ * state becomes NaN (token by token and in ll_la_decode_step it stays infinite).
  * log_alpha <= 0 is expected; -inf forgets the state, if that is finite.  Larger values
  * are computed as given and may overflow.
  *

@@ -103,7 +103,11 @@ __device__ __forceinline__ LaDecay la_decay(float g) {
   const bool near = g > -0.5f;
   return LaDecay{near ? expm1f(g) : expf(g), near};
 }
-__device__ __forceinline__ float la_apply(const LaDecay& d, float x) { return d.near ? fmaf(d.f, x, x) : d.f * x; }
+// (the product is of a finite value, since infinity takes nothing off infinity)
+__device__ __forceinline__ float la_apply(const LaDecay& d, float x) {
+  constexpr float kMost = 3.402823466e38f;
+  return d.near ? fmaf(d.f, fminf(fmaxf(x, -kMost), kMost), x) : d.f * x;
+}
 
 // The kernels of a call follow one another closely: each lets the next one be set up
 // once all of its CTAs run, and the next waits, first of all and in every CTA, until

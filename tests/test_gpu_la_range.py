@@ -1,5 +1,5 @@
-"""GPU parity of linear attention with a decay per head (ll_la_bwd) against the recurrence in 64 bits (oracle.la)
-where memory changes within a segment, and the accuracy of states.
+"""GPU parity of linear attention with a decay per head (ll_la_fwd, ll_la_bwd, ll_la_decode_step) against the
+recurrence in 64 bits (oracle.la): memory that changes within a segment, the accuracy of states, infinities.
 
 Tolerances of dlog_alpha.  A token's value is a sum of terms along the sequence, of products of v and dv (k and dk)
 and of q and dq, from the nearer of the two ends of its piece: segments and tokens that forget.  With D the standard deviation of a
@@ -15,7 +15,7 @@ import torch
 
 from oracle import la
 from tests._parity import TOL_F32
-from tests.test_gpu_la import B, draw, gpu_bwd, gpu_fwd  # noqa: F401
+from tests.test_gpu_la import B, DEV, draw, gpu_bwd, gpu_fwd  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 D_CHUNKS, D_TOKENS = 1.6e-6, 2.0 ** -22
@@ -149,3 +149,30 @@ def test_decay_gradients_keep_float32(B, kind):  # noqa: F811
             err = np.linalg.norm(dla[b, h, lo:hi] - r["dlog_alpha"])
             bound = 5e-7 * np.sqrt((left * right / (left + right)).sum()) + 2.5e-7 * ends * np.sqrt(hi - lo)
             assert err <= bound, (i, h)
+
+
+# ---------------------------------------------------------------- infinities
+def test_infinite_states_stay_infinite(B):  # noqa: F811
+    """Token by token a decay above zero times infinity is infinity, near one as elsewhere."""
+    d = 32
+    for rate in (0.0, 1e-6, 0.1, 0.49, 0.51, 3.0):
+        g = {n: t.to(DEV) for n, t in draw(1, 2, 1, 1, d, d, "f32", seed=92, rate=rate, per_head=True).items()}
+        st = torch.randn(1, 2, d, d, device=DEV)
+        st[0, 0, 3, 4], st[0, 1, 5, 6] = float("inf"), -float("inf")
+        a = [g[n][:, :, 0].contiguous() for n in ("q", "k", "v")]
+        pool = st.clone()
+        B.ll_la_decode_step(*a, g["log_alpha"], pool)
+        out = torch.empty_like(st)
+        B.ll_la_fwd(g["q"], g["k"], g["v"], g["log_alpha"], state_in=st, state_out=out)
+        for x in (pool, out):
+            assert x[0, 0, 3, 4] == float("inf") and x[0, 1, 5, 6] == -float("inf"), rate
+            assert torch.isfinite(x).sum() == x.numel() - 2
+    # over segments: the state on entry to the second
+    T = 300
+    g = {n: t.to(DEV) for n, t in draw(1, 1, 1, T, d, d, "f32", seed=93, rate=1e-3, per_head=True).items()}
+    g["state_in"][0, 0, 3, 4] = float("inf")
+    g["dstate_out"][0, 0, 5, 6] = -float("inf")
+    out, back = torch.empty_like(g["state_in"]), torch.empty_like(g["state_in"])
+    B.ll_la_fwd(g["q"], g["k"], g["v"], g["log_alpha"], state_in=g["state_in"], state_out=out)
+    B.ll_la_bwd(g["q"], g["k"], g["v"], g["log_alpha"], g["dout"], dstate_out=g["dstate_out"], dstate_in=back)
+    assert out[0, 0, 3, 4] == float("inf") and back[0, 0, 5, 6] == -float("inf")
