@@ -534,7 +534,8 @@ LL_API ll_status ll_gdr_decode_step(int B, int H, int Hk, int dk, int dv, ll_dty
  * Pairs (a, b) of the first `rot` elements of a head become
  *   (a', b') = amp (a cos x - b sin x, a sin x + b cos x),   x = position inv_freq[i],
  * i the pair's number; the other elements stay as they are.  x is taken modulo a turn
- * in integers, exact to 2^-31 of a turn at any position of up to 2^40, and then rounded to
+ * in integers, off by 2^-32 + |position| 2^-65 of a turn at most (2^-31 up to position 2^33,
+ * 2^-25 at 2^40; inv_freq below 10^7), and then rounded to
  * float32; of bf16 tensors the sine and cosine are the hardware's, off by 2^-20 at most. */
 
 /*   rot          rotated elements of a head, even, 2 .. the head dim

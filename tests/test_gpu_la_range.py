@@ -1,5 +1,5 @@
 """GPU parity of linear attention with a decay per head (ll_la_fwd, ll_la_bwd, ll_la_decode_step) against the
-recurrence in 64 bits (oracle.la): memory that changes within a segment, the accuracy of states, infinities.
+recurrence in 64 bits (oracle.la): memory that changes within a segment, the accuracy of states, infinities, and far rotary positions.
 
 Tolerances of dlog_alpha.  A token's value is a sum of terms along the sequence, of products of v and dv (k and dk)
 and of q and dq, from the nearer of the two ends of its piece: segments and tokens that forget.  With D the standard deviation of a
@@ -8,6 +8,8 @@ thousand tokens of a test no value by more than five times that; on top TOL_F32 
 own product, as in tests/test_gpu_la.py.  In chunks D is 1.6e-6 (states in two bf16 parts), token by token it is
 2^-22: a float32 product of 128 elements and the two sums that it is made of, each rounded by half of 2^-23, with a few of
 the recurrence's own roundings."""
+
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -176,3 +178,22 @@ def test_infinite_states_stay_infinite(B):  # noqa: F811
     B.ll_la_fwd(g["q"], g["k"], g["v"], g["log_alpha"], state_in=g["state_in"], state_out=out)
     B.ll_la_bwd(g["q"], g["k"], g["v"], g["log_alpha"], g["dout"], dstate_out=g["dstate_out"], dstate_in=back)
     assert out[0, 0, 3, 4] == float("inf") and back[0, 0, 5, 6] == -float("inf")
+
+
+# ---------------------------------------------------------------- far rotary positions
+PI = Fraction(31415926535897932384626433832795028841971693993751, 10 ** 49)
+
+
+def test_rope_angles_at_the_farthest_positions(B):  # noqa: F811
+    """The angle is off by 2^-32 of a turn from its last bits and by |position| 2^-65 from the frequency's rounding to 2^-64
+    of a turn; sine and cosine by 3 x 2^-24 on top."""
+    f = torch.cat([B.ll_rope_freqs(56), torch.tensor([1.9, 2.5, 0.77, 6.2831855])])
+    places = [1 << 32, (1 << 33) - 7, 1 << 36, -(1 << 40) + 3, 1 << 40, 1 << 44, 5 << 41]
+    x = torch.zeros(1, 1, len(places), 64)
+    x[..., :32] = 1.0
+    got = B.ll_rope_fwd(x.to(DEV), None, f.to(DEV), positions=torch.tensor([places], device=DEV)).double().cpu().numpy()[0, 0]
+    for n, pos in enumerate(places):
+        turns = [Fraction(float(w)) * pos / (2 * PI) for w in f]
+        angle = np.array([float((t - round(t)) * 2 * PI) for t in turns])
+        err = max(np.abs(got[n, :32] - np.cos(angle)).max(), np.abs(got[n, 32:] - np.sin(angle)).max())
+        assert err <= 2 * np.pi * (2.0 ** -32 + 1.001 * abs(pos) * 2.0 ** -65) + 3 * 2.0 ** -24, (pos, err)
