@@ -1,11 +1,15 @@
 """GPU parity of linear attention with a decay per head (ll_la_fwd, ll_la_bwd, ll_la_decode_step) against the
-recurrence in 64 bits (oracle.la): memory that changes within a segment, the accuracy of states, infinities, and far rotary positions.
+recurrence in 64 bits (oracle.la) where tests/test_gpu_la.py does not go: segments of many chunks, many heads, many
+packed sequences, memory that changes within a segment, the accuracy of states and of the decays' gradients, starts out of order
+over several launches, infinities, and far rotary positions.
+
+Tolerances of outputs and states as there, but by the way that a call takes (chunks or token by token).
 
 Tolerances of dlog_alpha.  A token's value is a sum of terms along the sequence, of products of v and dv (k and dk)
 and of q and dq, from the nearer of the two ends of its piece: segments and tokens that forget.  With D the standard deviation of a
 term's error relative to its size, the sum over n tokens is off by D sqrt(sum of squares) (2-norm), and over some ten
 thousand tokens of a test no value by more than five times that; on top TOL_F32 of the largest term for the border's
-own product, as in tests/test_gpu_la.py.  In chunks D is 1.6e-6 (states in two bf16 parts), token by token it is
+own product, as in tests/test_gpu_la.py.  In chunks D is 5e-7 (test_decay_gradients_keep_float32), token by token it is
 2^-22: a float32 product of 128 elements and the two sums that it is made of, each rounded by half of 2^-23, with a few of
 the recurrence's own roundings."""
 
@@ -16,11 +20,11 @@ import pytest
 import torch
 
 from oracle import la
-from tests._parity import TOL_F32
-from tests.test_gpu_la import B, DEV, draw, gpu_bwd, gpu_fwd  # noqa: F401
+from tests._parity import TOL_BF16, TOL_F32, rel_err
+from tests.test_gpu_la import B, DEV, check_bwd, check_fwd, draw, gpu_bwd, gpu_fwd, setup  # noqa: F401
 
 pytestmark = pytest.mark.gpu
-D_CHUNKS, D_TOKENS = 1.6e-6, 2.0 ** -22
+D_CHUNKS, D_TOKENS = 5e-7, 2.0 ** -22
 
 
 def in_chunks(x, starts, bwd):
@@ -33,6 +37,10 @@ def in_chunks(x, starts, bwd):
     mean = T if starts is None else -(-T // n)
     few = n * H <= 152
     return mean >= ((48 if few else 24) if dk * dv > 64 * 64 else (16 if few else 48) + (16 if bwd else 0))
+
+
+def tol_out(x, starts, bwd):
+    return TOL_F32 if x["q"].dtype == torch.float32 else TOL_BF16 if in_chunks(x, starts, bwd) else 2.0 ** -8 + TOL_F32
 
 
 def head(x, starts, i, h):
@@ -51,9 +59,97 @@ def squares(a, r):
     return (a[0] * r["dq"]).sum(-1) ** 2 + np.maximum((a[1] * r["dk"]).sum(-1) ** 2, (a[2] * r["dv"]).sum(-1) ** 2)
 
 
+def check_heads(B, x, starts, which, scale=0.5):
+    """Forward and gradient; the oracle on every value head of the key heads (sequence, key head) of `which`."""
+    o, st = gpu_fwd(B, x, starts, scale)
+    d = gpu_bwd(B, x, starts, scale)
+    again = gpu_fwd(B, x, starts, scale), gpu_bwd(B, x, starts, scale)
+    assert np.array_equal(o, again[0][0]) and np.array_equal(st, again[0][1])
+    assert all(np.array_equal(p, q) for p, q in zip(d, again[1])), "two calls differ"
+    dq, dk, dv, dla, dst = d
+    G = x["v"].shape[1] // x["q"].shape[1]
+    tf, tb = tol_out(x, starts, False), tol_out(x, starts, True)
+    D = D_CHUNKS if in_chunks(x, starts, True) else D_TOKENS
+    for i, key in which:
+        rq = rk = 0.0
+        for h in range(key * G, key * G + G):
+            (b, hk, lo, hi), a, do, s0, ds = head(x, starts, i, h)
+            ro, rs = la.forward(*a, scale=scale, state=s0)
+            assert rel_err(st[i, h], rs, 0) <= TOL_F32, (i, h, "state")
+            r = la.backward(*a, do, scale=scale, state=s0, dstate=ds)
+            assert rel_err(dst[i, h], r["dstate_in"], 0) <= TOL_F32, (i, h, "dstate_in")
+            if hi == lo:
+                continue
+            assert rel_err(o[b, h, lo:hi], ro, 0) <= tf, (i, h, "o")
+            assert rel_err(dv[b, h, lo:hi], r["dv"], 0) <= tb, (i, h, "dv")
+            rq, rk = rq + r["dq"], rk + r["dk"]
+            if dla.ndim == 3:
+                s2 = squares(a, r)
+                bound = 5 * D * np.sqrt(s2.sum()) + TOL_F32 * max(np.sqrt(s2.max()), r["terms"].max())
+                assert np.abs(dla[b, h, lo:hi] - r["dlog_alpha"]).max() <= bound, (i, h, "dlog_alpha")
+        if hi > lo:
+            assert rel_err(dq[b, hk, lo:hi], rq, 0) <= tb and rel_err(dk[b, hk, lo:hi], rk, 0) <= tb, (i, key, "dq, dk")
+
+
+# ---------------------------------------------------------------- segments of many chunks, many heads, many sequences
+def most_segments(B, x, starts, bwd):
+    """No more segments than this, in all sequences: by the states that the workspace holds."""
+    _, (n, H, dv, dk), shape, _ = setup(B, {m: t for m, t in x.items() if m in ("q", "k", "v", "log_alpha")}, starts, 0.5)
+    Bn, Hk, T = x["q"].shape[0], x["q"].shape[1], x["q"].shape[2]
+    if not bwd:
+        return B.ll_la_fwd_workspace_size(shape) // (H * dv * dk * 4)
+    rest = Bn * H * T * 4 * (4 + (2 * dk if H != Hk else 0)) + n * H * dv * dk * 4
+    return (B.ll_la_bwd_workspace_size(shape) - rest) // (2 * H * dv * dk * 4)
+
+
+LONG = [  # B, H, Hk, T, dk, dv, starts, chunks of a segment (forward, gradient; at least), (sequence, key head) looked at
+    (2, 16, 16, 4096, 128, 128, None, 4, 6, [(0, 0), (1, 15)]),
+    (2, 16, 8, 4096, 128, 128, None, 4, 6, [(1, 3)]),
+    (2, 32, 32, 3071, 64, 64, None, 4, 6, [(0, 1), (1, 31)]),
+    (2, 16, 16, 3500, 64, 128, None, 4, 4, [(1, 2)]),
+    (1, 16, 8, 7001, 128, 128, [3, 2600, 2601, 2601, 6200, 6999], 3, 4, [(0, 0), (3, 7), (4, 5)]),
+    (1, 16, 16, 9000, 128, 64, [0, 4500, 9000], 4, 4, [(1, 9)]),
+]
+
+
+@pytest.mark.parametrize("case", LONG, ids=str)
+def test_segments_of_many_chunks(B, case):  # noqa: F811
+    """Slow decays: what a segment's later chunks hold and hand on is made of all of its chunks."""
+    Bn, H, Hk, T, dk, dv, starts, fwd, bwd, which = case
+    x = draw(Bn, H, Hk, T, dk, dv, "bf16", n=Bn if starts is None else len(starts) - 1, seed=T, rate=1e-3)
+    chunks = Bn * -(-T // 128)
+    assert chunks // most_segments(B, x, starts, False) >= fwd, "the case no longer has long segments"
+    assert chunks // most_segments(B, x, starts, True) >= bwd, "the case no longer has long segments"
+    check_heads(B, x, starts, which)
+
+
+@pytest.mark.parametrize("T", [15, 16, 23, 24, 31, 47, 48, 63, 64])
+@pytest.mark.parametrize("kind", [(154, 64, 64), (154, 128, 128), (76, 64, 128), (2, 64, 128), (2, 64, 64), (2, 128, 128)], ids=str)
+def test_short_sequences_of_many_heads(B, kind, T):  # noqa: F811
+    """Both sides of the lengths from which chunks are taken, gradients too."""
+    H, dk, dv = kind
+    x = draw(2 if H == 76 else 1, H, H // 2, T, dk, dv, "bf16", seed=100 + T)
+    check_heads(B, x, None, [(0, 0), (0, H // 2 - 1)])
+
+
+@pytest.mark.parametrize("kind", [(4, 2, 128, 128, "bf16"), (2, 2, 128, 128, "f32"), (4, 4, 64, 64, "bf16")], ids=str)
+def test_many_packed_sequences_token_by_token(B, kind):  # noqa: F811
+    """Sequences of 0 to 15 tokens, more of them than a segment holds."""
+    H, Hk, dk, dv, io = kind
+    lens = [(7 * i) % 16 for i in range(260)]
+    starts = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    T = starts[-1] + 3
+    for per_head in (False, True):
+        x = draw(1, H, Hk, T, dk, dv, io, n=len(lens), seed=71, per_head=per_head)
+        assert not in_chunks(x, starts, True) and B.ll_la_fwd_launches(setup(B, x, starts, 0.5)[2]) == 3
+        check_heads(B, x, starts, [(i, i % Hk) for i in (0, 1, 7, 16, 30, 128, 255, 258, 259)])
+    check_fwd(B, x, starts)
+    check_bwd(B, x, starts)
+
+
 # ---------------------------------------------------------------- memory that changes within a segment
 @pytest.mark.parametrize("kind", [(2, 16, 16, 128, 128, "bf16"), (2, 16, 8, 64, 64, "bf16"), (4, 16, 16, 128, 128, "f32"),
-                                  (1, 2, 1, 32, 16, "f32"), (1, 2, 2, 64, 128, "bf16")], ids=str)
+                                  (1, 2, 1, 32, 16, "f32"), (1, 2, 2, 64, 128, "bf16"), (8, 80, 80, 16, 16, "f32")], ids=str)
 @pytest.mark.parametrize("how", ["forgets", "shortens", "forgets and grows"])
 def test_decay_gradients_after_large_values(B, how, kind):  # noqa: F811
     """A long memory of values 256 times as large comes before (behind) a short one.  The gradients of the short one's
@@ -82,7 +178,7 @@ def test_decay_gradients_after_large_values(B, how, kind):  # noqa: F811
 
 
 @pytest.mark.parametrize("kind", [(2, 16, 16, 128, 128, "bf16"), (1, 2, 1, 64, 64, "bf16"), (4, 16, 16, 128, 128, "f32"),
-                                  (1, 3, 3, 16, 32, "f32")], ids=str)
+                                  (1, 3, 3, 16, 32, "f32"), (8, 80, 40, 16, 16, "bf16")], ids=str)
 def test_tokens_that_forget_keep_pieces_apart(B, kind):  # noqa: F811
     """Pieces between tokens that forget, some of one token, with values from 2^-12 to 2^12: each held to its own terms."""
     Bn, H, Hk, dk, dv, io = kind
@@ -151,6 +247,49 @@ def test_decay_gradients_keep_float32(B, kind):  # noqa: F811
             err = np.linalg.norm(dla[b, h, lo:hi] - r["dlog_alpha"])
             bound = 5e-7 * np.sqrt((left * right / (left + right)).sum()) + 2.5e-7 * ends * np.sqrt(hi - lo)
             assert err <= bound, (i, h)
+
+
+@pytest.mark.parametrize("rate", [0.02, 2.0])
+@pytest.mark.parametrize("kind", [(4, 2, 300, 128, 128, "bf16"), (4, 4, 256, 64, 64, "bf16"), (4, 2, 200, 32, 32, "f32")], ids=str)
+def test_gradients_of_constant_decays(B, kind, rate):  # noqa: F811
+    """The sum of a head's tokens.  A term's error goes to every token behind it, less the part that the joining of
+    both sums takes back: to as many tokens as lie behind, minus the sum over all of them of the share of squares on their left."""
+    H, Hk, T, dk, dv, io = kind
+    x = draw(1, *kind, seed=88, per_head=True, rate=rate)
+    seg, D = (128, D_CHUNKS) if in_chunks(x, None, True) else (64, D_TOKENS)
+    dla = gpu_bwd(B, x)[3]
+    for h in range(H):
+        _, a, do, s0, ds = head(x, None, 0, h)
+        r = la.backward(*a, do, scale=0.5, state=s0, dstate=ds)
+        s2, var = squares(a, r), 0.0
+        for lo in range(0, T, seg):
+            w = s2[lo:lo + seg]
+            before = np.concatenate([[0.0], np.cumsum(w)])[:-1]
+            share = (before / w.sum()).sum()
+            var += (w * (len(w) - 1 - np.arange(len(w)) - share) ** 2).sum()
+        ends = max(r["terms"].max(), np.linalg.norm(la.forward(*a, scale=0.5, state=s0)[1] * ds))
+        bound = 5 * D * np.sqrt(var) + 2.5e-7 * ends * T + 2.0 ** -23 * abs(r["dlog_alpha"].sum())
+        assert abs(dla[h] - r["dlog_alpha"].sum()) <= bound, h
+
+
+# ---------------------------------------------------------------- bad starts
+def test_starts_out_of_order_in_chunks(B):  # noqa: F811
+    """Every launch of a call in chunks, over several segments: the error word, nothing outside of the buffers, and the next
+    call is right."""
+    T, H, Hk, d = 5000, 4, 2, 128
+    x = draw(1, H, Hk, T, d, d, "bf16", n=3, seed=91)
+    g, st_shape, shape, _ = setup(B, x, [0, 100, 200, T], 0.5)
+    assert B.ll_la_fwd_launches(shape) == 3 and in_chunks(x, [0, 100, 200, T], True)
+    for starts in ([0, 4000, 1000, T], [0, 1000, T + 1, T], [-5, 1000, 2000, T], [T, 3000, 2000, 0], [0, T, 0, T]):
+        ss = torch.tensor(starts, dtype=torch.int32, device=DEV)
+        for per_head in (False, True):
+            ga = g["log_alpha"][0, :, 0].contiguous() if per_head else g["log_alpha"]
+            st = torch.empty(st_shape, device=DEV)
+            B.ll_la_fwd(g["q"], g["k"], g["v"], ga, state_in=g["state_in"], state_out=st, seq_starts=ss)
+            assert B.ll_last_device_error() == 6, starts
+            B.ll_la_bwd(g["q"], g["k"], g["v"], ga, g["dout"], state_in=g["state_in"], dstate_out=g["dstate_out"], dstate_in=st, seq_starts=ss)
+            assert B.ll_last_device_error() == 6, starts
+    check_heads(B, x, [0, 1700, 1700, 4990], [(0, 0), (1, 1), (2, 1)])
 
 
 # ---------------------------------------------------------------- infinities
