@@ -11,7 +11,8 @@
 // and a row needs no other row.  A group of kLpr lanes holds kRt rows (kEpl elements
 // of each a lane), a CTA a block of rows of one (segment, head).  An element takes
 // three operations a token (decay, dot product with the decayed row, update), on
-// pairs of floats, and these bound it; M_t x_t is a M_{t-1} x_t + y_t (z_t . x_t) with the
+// pairs of floats; what bounds it is reading z and x from shared memory for them (float32, 128 x 128,
+// B 2, H 16, T 4096: its pipe 62 to 74 % busy, the operations' 30 to 38; forward 777 us, gradient 1717).  M_t x_t is a M_{t-1} x_t + y_t (z_t . x_t) with the
 // scalar products z . x made once per staged tile, which keeps the update out of the
 // sum's chain, and gives the part of the sum that lies before token t by itself:
 // that is what the decay's gradient is made of,
@@ -783,9 +784,11 @@ ll_status carry_launch(const LaCarry& c, int sequences, cudaStream_t stream) {
 // ---- in chunks: tokens of a segment, a multiple of a chunk.  More segments fill more
 // SMs, and each costs the states' way between them and the filling of its pipeline.  The
 // times are those measured at d = 128, in us: a chunk 3.1, of the gradient's jobs 7, of the sums 1.4 (1.9),
-// a segment's beginning and end 9, 12, 6.  Of packed sequences only the device knows the lengths: their
+// a segment's beginning and end 9, 12, 6.  With smaller heads all of them shrink alike: at 64 and mixed sizes what
+// is chosen took at most 7 % more than the best of one to 32 chunks (1 x 8 heads of 8192 tokens, d 64, gradient: 114 us
+// where 107), at 128 2 %.  Of packed sequences only the device knows the lengths: their
 // work is taken as spread evenly, with half a segment at the end of it.  (Gradient, B 2, H 16, T 4096, segments of
-// 6, 8, 11, 16 chunks: 226, 225, 202, 245 us; 7 packed sequences of 5003 tokens, 3, 6, 8, 11: 281, 226, 220, 362.)
+// 6, 8, 11, 12 chunks: 241, 241, 218, 231 us; 7 packed sequences of 5003 tokens, 3, 6, 8, 11: 281, 226, 220, 362.)
 // The decay's gradient is summed over a segment, and its rounding with it: at most 12 chunks there.
 constexpr int kChunk = 128, kMostGradChunks = 12;
 int tc_segment(const LaArgs& a, bool bwd) {
@@ -815,18 +818,24 @@ int tc_segment(const LaArgs& a, bool bwd) {
   if (bwd) seg = std::min<long long>(seg, kMostGradChunks);
   return (int)std::min<long long>(seg * kChunk, 1ll << 30);
 }
-// Which of the two ways is the faster (token by token / in chunks, us; mean lengths of 16, 32, 64 tokens):
-//   128 x 128, 4 heads      forward 12/21, 16/21, 25/21        gradient 19/31, 24/31, 32/31
-//              256 heads    forward 29/36, 42/36, 69/37        gradient 75/89, 112/89, 189/90
-//              2048 heads   forward 169/211, 259/213, 453/219  gradient 529/591, 804/582, 1395/584
-//   64 x 64,   32 heads     forward 14/13, 18/13, 29/13        gradient 20/23, 24/23, 34/23
-//              256 heads    forward 16/23, 21/23, 33/23        gradient 32/69, 46/68, 75/68
-//              2048 heads   forward 55/124, 84/125, 143/125    gradient 165/429, 251/429, 425/433
+// Which of the two ways is the faster (token by token / in chunks, us of a captured call with states behind a flushed L2; mean
+// lengths of 16, 32, 64 tokens):
+//   128 x 128, 4 heads      forward 13/22, 18/22, 26/22       gradient 24/36, 28/34, 36/34
+//              256 heads    forward 30/38, 44/39, 71/40       gradient 83/99, 120/97, 198/99
+//              2048 heads   forward 170/221, 259/224, 452/231 gradient 596/659, 861/649, 1443/651
+//   64 x 64,   32 heads     forward 14/15, 21/14, 29/15       gradient 23/31, 27/31, 37/31
+//              256 heads    forward 16/25, 23/25, 35/26       gradient 37/76, 51/76, 80/76
+//              2048 heads   forward 55/132, 85/133, 143/133   gradient 199/480, 284/478, 454/479
+//   64 x 128,  4 heads      forward 15/17, 20/17, 30/17       gradient 40/28, 47/30, 71/30
+//              256 heads    forward 22/29, 31/29, 47/29       gradient 56/84, 80/83, 125/83
+//              2048 heads   forward 100/160, 154/160, 263/162 gradient 340/549, 490/541, 795/542
+// (128 x 64 as 64 x 128: 2048 heads forward 90/167, 137/169, 234/171.  Token by token their gradient takes a launch more.)
 bool tc_use(const LaArgs& a, bool bwd) {
   if (!la_tc_formats(a)) return false;
   const int mean = a.n_seqs ? (a.T + a.n_seqs - 1) / a.n_seqs : a.T;
   const bool few = (long long)la_sequences(a) * a.H <= 152;
-  if (a.dk * a.dv > 64 * 64) return mean >= (few ? 48 : 24);
+  if (a.dk != a.dv) return mean >= (few ? (bwd ? 8 : 24) : 40);
+  if (a.dk == 128) return mean >= (few ? 48 : 24);
   return mean >= (few ? 16 : 48) + (bwd ? 16 : 0);
 }
 

@@ -36,7 +36,9 @@ def in_chunks(x, starts, bwd):
     n = Bn if starts is None else len(starts) - 1
     mean = T if starts is None else -(-T // n)
     few = n * H <= 152
-    return mean >= ((48 if few else 24) if dk * dv > 64 * 64 else (16 if few else 48) + (16 if bwd else 0))
+    if dk != dv:
+        return mean >= ((8 if bwd else 24) if few else 40)
+    return mean >= ((48 if few else 24) if dk == 128 else (16 if few else 48) + (16 if bwd else 0))
 
 
 def tol_out(x, starts, bwd):
@@ -123,8 +125,8 @@ def test_segments_of_many_chunks(B, case):  # noqa: F811
     check_heads(B, x, starts, which)
 
 
-@pytest.mark.parametrize("T", [15, 16, 23, 24, 31, 47, 48, 63, 64])
-@pytest.mark.parametrize("kind", [(154, 64, 64), (154, 128, 128), (76, 64, 128), (2, 64, 128), (2, 64, 64), (2, 128, 128)], ids=str)
+@pytest.mark.parametrize("T", [7, 8, 15, 16, 23, 24, 31, 39, 40, 47, 48, 63, 64])
+@pytest.mark.parametrize("kind", [(154, 64, 64), (154, 128, 128), (76, 64, 128), (154, 128, 64), (2, 64, 128), (2, 64, 64), (2, 128, 128)], ids=str)
 def test_short_sequences_of_many_heads(B, kind, T):  # noqa: F811
     """Both sides of the lengths from which chunks are taken, gradients too."""
     H, dk, dv = kind
