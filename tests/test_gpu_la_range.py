@@ -274,6 +274,27 @@ def test_gradients_of_constant_decays(B, kind, rate):  # noqa: F811
         assert abs(dla[h] - r["dlog_alpha"].sum()) <= bound, h
 
 
+@pytest.mark.parametrize("kind", [(1, 2, 1, 100, 128, 128, "bf16", None), (3, 2, 2, 40, 32, 32, "f32", None), (2, 4, 2, 7, 64, 64, "bf16", None),
+                                  (1, 2, 1, 100, 64, 128, "bf16", [0, 0, 40, 97, 97]), (1, 2, 1, 60, 16, 32, "f32", [5, 30, 30, 60]),
+                                  (1, 2, 1, 900, 128, 128, "bf16", [0, 0, 400, 900])], ids=str)
+def test_state_gradients_in_place(B, kind):  # noqa: F811
+    """dstate_in in dstate_out's place, of one segment (the gradient there is read once more, for the decays') and of several."""
+    Bn, H, Hk, T, dk, dv, io, starts = kind
+    x = draw(Bn, H, Hk, T, dk, dv, io, n=Bn if starts is None else len(starts) - 1, seed=89)
+    g, st_shape, _, ss = setup(B, x, starts, 0.5)
+    a = (g["q"], g["k"], g["v"], g["log_alpha"], g["dout"])
+    for state in (g["state_in"], None):
+        apart, place = torch.empty(st_shape, device=DEV), g["dstate_out"].clone()
+        grads = [torch.zeros_like(t) for t in a[:4]], [torch.zeros_like(t) for t in a[:4]]
+        B.ll_la_bwd(*a, state_in=state, dstate_out=g["dstate_out"], dstate_in=apart, seq_starts=ss, grads=grads[0])
+        B.ll_la_bwd(*a, state_in=state, dstate_out=place, dstate_in=place, seq_starts=ss, grads=grads[1])
+        assert torch.equal(apart, place) and all(torch.equal(p, q) for p, q in zip(*grads))
+        if starts is not None:
+            for i in range(len(starts) - 1):
+                assert starts[i] < starts[i + 1] or torch.equal(place[i], g["dstate_out"][i])
+    check_bwd(B, x, starts)
+
+
 # ---------------------------------------------------------------- bad starts
 def test_starts_out_of_order_in_chunks(B):  # noqa: F811
     """Every launch of a call in chunks, over several segments: the error word, nothing outside of the buffers, and the next
