@@ -6,7 +6,7 @@
 // all of their loads in flight at once, 16 bytes a lane and 512 bytes in a row;
 // meanwhile the CTA's threads make the turned key and query, an element each.  The rows'
 // sums over the lanes are taken together: each step of the butterfly halves the rows a lane carries.
-// Four warps to a CTA and six CTAs to an SM: B 64, 32 heads of 128 x 128, 47 us, 84 % of the measured HBM rate;
+// Four warps to a CTA and six CTAs to an SM: B 64, 32 heads of 128 x 128, 48 us, 84 % of the measured HBM rate;
 // with 85 registers (five CTAs) 61, eight CTAs 50, a CTA to a whole state 52.
 #include "la.cuh"
 #include "rope.cuh"

@@ -23,9 +23,9 @@
 // bf16 has float32's range, so no operand is scaled.
 //
 // Bound: the chain of a chunk, 2.7 us of which the products take half (the scores' masking and k' stand between
-// them; tensor memory has no room for a second chunk's scores).  More segments are more chunks at a time: a pass
+// them).  More segments are more chunks at a time: a pass
 // that sums up what each adds to the state, one along them, then all of them at once.  B 2, H 16, T 4096, d 128:
-// 65 us a call (sums 24, carry 6, outputs 38; 20 at the copy rate), its gradient 202 (sums 32, carry 7, dq dk dv 157).
+// 65 us a call (sums 24, carry 7, outputs 39; 20 at the copy rate), its gradient 216 (sums 34, carry 9, dq dk dv 167, decays 14).
 //
 // Decays between two tokens of a chunk are products of factors of at most 1: from the
 // row to its block of 32, over the blocks between, from the column's block to the column;
@@ -327,7 +327,7 @@ static __device__ __noinline__ void zero_rows(unsigned char* tile, uint32_t full
 // for it, one of the ring's (`third`: a state that is returned; 16384 tokens, 16 heads: 65 us where 58 with two parts).
 // The output is staged in v's place, with NT = 4 in w's.  The roles' code is kept short, in loops: unrolled
 // (90 KB) it left the instruction cache and every phase waited for its instructions.  With NT = 4 it has to be
-// shorter still, products and waits as calls (SHORT: 155 us where 190, 63 % of requests hit instead of 52; without
+// shorter still, products and waits as calls (SHORT: 155 us where 190 with two parts, 63 % of requests hit instead of 52; without
 // them the forward takes 57 us where 69).  What a chunk adds
 // to the state is summed by itself in tensor memory and added to the state in registers: the tensor
 // cores' sums round towards zero, which over the chunks of a long memory adds up (6e-6 of a state

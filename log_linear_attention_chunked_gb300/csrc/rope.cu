@@ -5,8 +5,9 @@
 // One launch turns queries and keys.  It moves every element once each way and
 // bounds on HBM if the angles cost nothing: a thread makes the sines of its pairs
 // once and applies them to a group of heads (up to kHeads), 16 bytes of both
-// halves of a pair at a time.  Queries and keys of 2 x 4096 tokens, 32 heads of 128 in all, bf16, L2 flushed: 28.8 us
-// (20 at the copy rate); four heads to a thread 30.9, sixteen 29.9 (and single tokens 13 where 9), CTAs of 256 31.8.
+// halves of a pair at a time.  Queries and keys of 2 x 4096 tokens, 32 heads of 128 in all, bf16: 25.2 us a call among
+// others (20 at the copy rate); four heads to a thread 28.7, sixteen 26.9 (and single tokens 13.4 where 11.4), CTAs of 256 threads 28.7.
+// Captured, behind a flushed L2: 29.8; float32 48; a rotated part of 100, element by element, 77 (float32 82).
 #include "la.cuh"
 #include "rope.cuh"
 #include "sm100.cuh"
