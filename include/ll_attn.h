@@ -637,7 +637,9 @@ LL_API int ll_la_fwd_launches(const ll_la_shape* shape);
  *   log_alpha  [B,H,T] or [H] float32
  *   state_in   [N,H,dv,dk]  float32 or NULL (zero states), N = n_seqs or B
  *   state_out  [N,H,dv,dk]  float32 or NULL: the states after the last token
- *              (state_in's for an empty sequence).  May be state_in itself.
+ *              (state_in's for an empty sequence).  May be state_in itself.  In chunks a call
+ *              that returns them holds them to more bits on the way (see above), so that o
+ *              may differ in its last place from that of a call that does not.
  *   workspace  >= ll_la_fwd_workspace_size(shape) bytes, 256-byte aligned
  *              (NULL when that is 0)
  * o and state_out may not overlap the inputs (but state_out = state_in) or
