@@ -506,6 +506,7 @@ struct Term {
   float k, q;
 };
 constexpr int kMostParts = 4;  // row blocks of 128 rows (row_blocks), halves of the columns in chunks
+static_assert(std::min({Cfg<16>::kMaxRows, Cfg<32>::kMaxRows, Cfg<64>::kMaxRows, Cfg<128>::kMaxRows}) * kMostParts >= 128, "");
 __device__ __forceinline__ Term finish_term(const FinishParams& p, size_t at) {
   float k[kMostParts], q[kMostParts];
 #pragma unroll
